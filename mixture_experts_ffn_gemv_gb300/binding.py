@@ -16,7 +16,9 @@ import torch
 from .build import LIB, build_library, up_to_date
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_DEVICE = range(6)
-MOE_WEIGHTS_BF16, MOE_WEIGHTS_FP8_E4M3_B128, MOE_WEIGHTS_NVFP4 = 0, 1, 2
+MOE_WEIGHTS_BF16, MOE_WEIGHTS_FP8_E4M3_B128, MOE_WEIGHTS_NVFP4, MOE_WEIGHTS_MXFP4 = 0, 1, 2, 3
+MOE_ACT_SILU, MOE_ACT_GELU_TANH = 0, 1
+ACTIVATIONS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU_TANH}
 MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
 MOE_ARM_AUTO, MOE_ARM_GEMV, MOE_ARM_GEMM = 0, 1, 2
 ARMS = {"auto": MOE_ARM_AUTO, "gemv": MOE_ARM_GEMV, "gemm": MOE_ARM_GEMM}
@@ -30,6 +32,9 @@ EXPORTED = (
     "moe_layer_stall_test",
     "moe_last_launch_count", "moe_kernel_timing_enable", "moe_kernel_timing_read", "moe_kernel_count",
     "moe_kernel_name", "moe_status_string",
+    "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+    "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
+    "moe_mxfp4_dequant", "moe_mxfp4_gemm_workspace_size", "moe_mxfp4_gemm",
 )
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -44,6 +49,14 @@ class MoeConfig(ctypes.Structure):
 class MoeExpertWeights(ctypes.Structure):
     _fields_ = [("w1", _vp), ("w3", _vp), ("w2", _vp), ("s1", _vp), ("s3", _vp), ("s2", _vp), ("gate", _vp),
                 ("sb1", _vp), ("sb3", _vp), ("sb2", _vp)]
+
+
+class MoeFfnConfig(ctypes.Structure):
+    _fields_ = [("hidden", _i32), ("inter", _i32), ("activation", _i32), ("weights", _i32)]
+
+
+class MoeFfnWeights(ctypes.Structure):
+    _fields_ = [("w1", _vp), ("w3", _vp), ("w2", _vp), ("s1", _vp), ("s3", _vp), ("s2", _vp)]
 
 
 class MoeError(RuntimeError):
@@ -98,6 +111,20 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_kernel_name.restype = ctypes.c_char_p
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
+        sz = ctypes.c_size_t
+        lib.moe_ffn_create.argtypes = [ctypes.POINTER(MoeFfnConfig), ctypes.POINTER(MoeFfnWeights),
+                                       ctypes.POINTER(_vp)]
+        lib.moe_ffn_destroy.argtypes = [_vp]
+        lib.moe_ffn_workspace_size.argtypes = [_vp, _i64, ctypes.c_int, ctypes.POINTER(sz)]
+        lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_last_launch_count.argtypes = [_vp]
+        lib.moe_mxfp4_scales_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
+        lib.moe_mxfp4_quant.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
+        lib.moe_mxfp4_quant_f32.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
+        lib.moe_mxfp4_dequant.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp]
+        lib.moe_mxfp4_gemm_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
+        lib.moe_mxfp4_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, sz, _vp]
         _lib = lib
         return lib
 
@@ -341,3 +368,207 @@ class MoeLayer:
                                                      _p(w), ARMS[arm], _p(ws), ws.numel(), _stream(stream)),
                "moe_forward_residual_rmsnorm")
         return (norm_out, ids, w) if return_routing else norm_out
+
+
+# ---------------------------------------------------------------- the gated feed-forward block and MXFP4
+# (include/moe_ffn_block.h)
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, dtypes, n: int | None, what: str):
+    """A [rows, n] device matrix whose rows are dense and 16-byte aligned; returns its row stride."""
+    _need(t.dim() == 2 and t.dtype in dtypes and t.is_cuda, f"{what}: a 2-d device tensor of {dtypes}")
+    _need(n is None or t.shape[1] == n, f"{what}: [rows, {n}], got {tuple(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    _need(t.numel() == 0 or (t.stride(1) == 1 and ld >= t.shape[1] and ld * t.element_size() % 16 == 0
+                             and t.data_ptr() % 16 == 0), f"{what}: rows must be dense and 16-byte aligned")
+    return ld
+
+
+def _dense(t, dtype, shape, what: str):
+    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
+
+
+def mxfp4_scales_shape(rows: int, n: int):
+    """Shape of the packed scales of a [rows, n] matrix: [row tile, K tile, row % 32, row / 32, block]."""
+    return (-(-rows // 128), -(-n // 128), 32, 4, 4)
+
+
+def mxfp4_pack_scales(scales):
+    """e8m0 scale bytes in rows (uint8 [rows, n/32], as checkpoints hold them) to the packed order."""
+    rows, nb = scales.shape
+    rt, kt = -(-rows // 128), -(-nb // 4)
+    s = torch.zeros(rt * 128, kt * 4, dtype=torch.uint8, device=scales.device)
+    s[:rows, :nb] = scales
+    return s.reshape(rt, 4, 32, kt, 4).permute(0, 3, 2, 1, 4).contiguous()
+
+
+def mxfp4_unpack_scales(scales, rows: int, n: int):
+    """The packed scales of a [rows, n] matrix back in rows, uint8 [rows, n/32]."""
+    rt, kt = scales.shape[:2]
+    return scales.permute(0, 3, 2, 1, 4).reshape(rt * 128, kt * 4)[:rows, : n // 32].contiguous()
+
+
+def moe_mxfp4_quant(x, stream=None):
+    """x bf16 or fp32 [rows, n] (device; n a multiple of 32) -> (codes uint8 [rows, n/2], packed scales uint8)."""
+    lib = load_library()
+    ld = _rows(x, (torch.bfloat16, torch.float32), None, "x")
+    rows, n = x.shape
+    codes = torch.empty(rows, n // 2, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(mxfp4_scales_shape(rows, n), dtype=torch.uint8, device=x.device)
+    f32 = x.dtype == torch.float32
+    _check((lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
+        _p(x), ld, rows, n, _p(codes), _p(scales), _stream(stream)),
+        "moe_mxfp4_quant_f32" if f32 else "moe_mxfp4_quant")
+    return codes, scales
+
+
+def _mx_matrix(codes, scales, what: str):
+    """(rows, n) of a matrix held as codes and packed scales."""
+    _need(codes.dim() == 2, f"{what}: codes are [rows, n/2]")
+    rows, n = codes.shape[0], codes.shape[1] * 2
+    _dense(codes, torch.uint8, (rows, n // 2), f"{what} codes")
+    _dense(scales, torch.uint8, mxfp4_scales_shape(rows, n), f"{what} scales")
+    return rows, n
+
+
+def moe_mxfp4_dequant(codes, scales, stream=None):
+    """The values (bf16 [rows, n]) that codes and packed scales stand for."""
+    lib = load_library()
+    rows, n = _mx_matrix(codes, scales, "x")
+    out = torch.empty(rows, n, dtype=torch.bfloat16, device=codes.device)
+    _check(lib.moe_mxfp4_dequant(_p(codes), _p(scales), rows, n, _p(out), _stream(stream)), "moe_mxfp4_dequant")
+    return out
+
+
+_headers = {}  # device -> the zeroed workspace of moe_mxfp4_gemm calls
+
+
+def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
+    """A [m, k] times B [n, k] transposed, both MXFP4 (codes, packed scales) -> bf16 [m, n]."""
+    lib = load_library()
+    m, k = _mx_matrix(a_codes, a_scales, "a")
+    n, kb = _mx_matrix(b_codes, b_scales, "b")
+    _need(k == kb, f"k differs: {k} and {kb}")
+    if out is None:
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=a_codes.device)
+    else:
+        _dense(out, torch.bfloat16, (m, n), "out")
+    ws = _headers.get(a_codes.device)
+    if ws is None:
+        # ready before any later call on any stream uses it
+        ws = torch.zeros(256, dtype=torch.uint8, device=a_codes.device)
+        torch.cuda.synchronize(a_codes.device)
+        _headers[a_codes.device] = ws
+    _check(lib.moe_mxfp4_gemm(_p(a_codes), _p(a_scales), m, _p(b_codes), _p(b_scales), n, k, _p(out), _p(ws),
+                              ws.numel(), _stream(stream)), "moe_mxfp4_gemm")
+    return out
+
+
+def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
+    """x (bf16 or fp32 [m, k]) quantised per call, times a weight matrix [n, k] held in MXFP4 -> bf16 [m, n]."""
+    return moe_mxfp4_gemm(*moe_mxfp4_quant(x, stream), codes, scales, out=out, stream=stream)
+
+
+class GatedFfn:
+    """A dense gated feed-forward block over caller-owned device weights:
+    out = (act(x w1^T) * (x w3^T)) w2^T, w1, w3 [I, H], w2 [H, I].
+
+    Weights are bf16 tensors, or (codes, packed scales) pairs as
+    moe_mxfp4_quant returns them; act is "silu" or "gelu" (tanh form)."""
+
+    def __init__(self, w1, w3, w2, act="silu"):
+        self.lib = load_library()
+        _need(act in ACTIVATIONS, f"act: one of {sorted(ACTIVATIONS)}")
+        self.mxfp4 = isinstance(w1, (tuple, list))
+        if self.mxfp4:
+            (I, H), shapes = _mx_matrix(*w1, "w1"), [_mx_matrix(*w, n) for w, n in ((w3, "w3"), (w2, "w2"))]
+            _need(shapes == [(I, H), (H, I)], "w1, w3 [I, H], w2 [H, I]")
+            ptrs = [_p(w[0]) for w in (w1, w3, w2)] + [_p(w[1]) for w in (w1, w3, w2)]
+        else:
+            _need(w1.dim() == 2, "w1: [I, H]")
+            I, H = w1.shape
+            for w, shape, name in ((w1, (I, H), "w1"), (w3, (I, H), "w3"), (w2, (H, I), "w2")):
+                _dense(w, torch.bfloat16, shape, name)
+            ptrs = [_p(w) for w in (w1, w3, w2)] + [None] * 3
+        self._keep = (w1, w3, w2)
+        self.hidden, self.inter, self.act = H, I, act
+        cfg = MoeFfnConfig(H, I, ACTIVATIONS[act], MOE_WEIGHTS_MXFP4 if self.mxfp4 else MOE_WEIGHTS_BF16)
+        w = MoeFfnWeights(*ptrs)
+        handle = _vp()
+        _check(self.lib.moe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(handle)), "moe_ffn_create")
+        self.handle = handle
+        self._ws = None
+
+    def close(self):
+        if getattr(self, "handle", None):
+            self.lib.moe_ffn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def workspace_size(self, m: int, backward: bool = False) -> int:
+        n = ctypes.c_size_t()
+        _check(self.lib.moe_ffn_workspace_size(self.handle, int(m), int(backward), ctypes.byref(n)),
+               "moe_ffn_workspace_size")
+        return n.value
+
+    def workspace(self, m: int, backward: bool, device) -> torch.Tensor:
+        """The handle's own workspace; calls on one handle are ordered on one stream."""
+        need = self.workspace_size(m, backward)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        return self._ws
+
+    def last_launch_count(self) -> int:
+        return self.lib.moe_ffn_last_launch_count(self.handle)
+
+    def device_status(self, stream=None) -> int:
+        if self._ws is None:
+            return 0
+        code = _i32()
+        rc = self.lib.moe_device_status(_p(self._ws), _stream(stream), ctypes.byref(code))
+        if rc not in (MOE_OK, MOE_ERR_DEVICE):
+            raise MoeError(rc, "moe_device_status")
+        return code.value
+
+    def forward(self, x, save=False, out=None, stream=None):
+        """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
+        (out, saved) for backward: saved bf16 [2, m, I] holds x w1^T and x w3^T."""
+        ld = _rows(x, (torch.bfloat16,), self.hidden, "x")
+        m = x.shape[0]
+        if out is None:
+            out = torch.empty(m, self.hidden, dtype=torch.bfloat16, device=x.device)
+        else:
+            _dense(out, torch.bfloat16, (m, self.hidden), "out")
+        saved = torch.empty(2, m, self.inter, dtype=torch.bfloat16, device=x.device) if save else None
+        ws = self.workspace(m, False, x.device)
+        _check(self.lib.moe_ffn_forward(self.handle, _p(x), ld, m, _p(out), _p(saved), _p(ws), ws.numel(),
+                                        _stream(stream)), "moe_ffn_forward")
+        return (out, saved) if save else out
+
+    def backward(self, dout, x, saved, need_dx=True, need_dw=True, stream=None):
+        """Gradients (dx, dw1, dw3, dw2), bf16, of the forward pass that saved `saved`; None
+        for those not needed.  No tokens: the weight gradients are zero."""
+        ldd = _rows(dout, (torch.bfloat16,), self.hidden, "dout")
+        ldx = _rows(x, (torch.bfloat16,), self.hidden, "x")
+        m = x.shape[0]
+        _need(dout.shape[0] == m, "dout and x differ in rows")
+        _dense(saved, torch.bfloat16, (2, m, self.inter), "saved")
+        new = (lambda *s: torch.empty(s, dtype=torch.bfloat16, device=x.device)) if m else \
+              (lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=x.device))
+        dx = new(m, self.hidden) if need_dx else None
+        dw1, dw3, dw2 = (new(self.inter, self.hidden), new(self.inter, self.hidden),
+                         new(self.hidden, self.inter)) if need_dw else (None,) * 3
+        ws = self.workspace(m, True, x.device)
+        _check(self.lib.moe_ffn_backward(self.handle, _p(dout), ldd, _p(x), ldx, _p(saved), m, _p(dx), _p(dw1),
+                                         _p(dw3), _p(dw2), _p(ws), ws.numel(), _stream(stream)), "moe_ffn_backward")
+        return dx, dw1, dw3, dw2

@@ -149,6 +149,18 @@ __device__ __forceinline__ uint32_t e4m3x4_quotient(const float* f, float s, con
            (f32x2_to_e4m3x2(__fdiv_rn(f[2], s), __fdiv_rn(f[3], s)) << 16);
 }
 
+// 16 columns of an output row: two words of 16 bytes, or one store of 32 where
+// the row's address allows it; columns from n on are left out (n and col are
+// multiples of 8).
+__device__ __forceinline__ void store_row16(uint16_t* row, int col, int n, bool wide, const uint32_t (&o)[8]) {
+    if (wide && col + 16 <= n) {
+        st_global_v8(row + col, o);
+        return;
+    }
+    if (col + 8 <= n) *reinterpret_cast<uint4*>(row + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (col + 16 <= n) *reinterpret_cast<uint4*>(row + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 // ---- warp-private staged row stores (GEMM epilogues)
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");

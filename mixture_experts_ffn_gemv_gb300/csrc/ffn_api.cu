@@ -1,0 +1,370 @@
+// C-ABI of the dense gated feed-forward block and the MXFP4 operators:
+// argument checks, workspace layout and launch sequences.  Declarations and
+// contracts: include/moe_ffn_block.h.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <new>
+
+#include "common.cuh"
+#include "ffn_block.h"
+
+using namespace moe;
+
+struct moe_ffn {
+    moe_ffn_config cfg;
+    moe_ffn_weights w;
+    int device;
+    mutable int last_launches;
+    mutable const void* last_ws;  // its header is known to be clean
+    // maps of the weights: along K (128-row boxes), along M or N (64 x 64), MXFP4 codes and scales
+    CUtensorMap k1, k3, k2, mn1, mn3, mn2;
+    CUtensorMap s1, s3, s2;
+};
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: limit of every bounded mbarrier wait
+constexpr int kMaxDim = 1 << 20;
+
+inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t scale_bytes(int64_t rows, int64_t n) { return (size_t)((rows + 127) / 128) * ((n + 127) / 128) * 512; }
+template <typename T>
+inline T* at(void* ws, size_t off) {
+    return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+struct Layout {
+    size_t hdr, h, dg, du, xq, xs, hq, hs, total;
+};
+Layout layout(const moe_ffn* f, int64_t m, bool backward) {
+    Layout o{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t p = off;
+        off = align_up(off + bytes);
+        return p;
+    };
+    const size_t H = f->cfg.hidden, I = f->cfg.inter;
+    o.hdr = take(sizeof(WsHeader));
+    if (f->cfg.weights == MOE_WEIGHTS_MXFP4) {
+        o.xq = take((size_t)m * H / 2);
+        o.xs = take(scale_bytes(m, H));
+        o.hq = take((size_t)m * I / 2);
+        o.hs = take(scale_bytes(m, I));
+    } else {
+        o.h = take((size_t)m * I * 2);
+        if (backward) {
+            o.dg = take((size_t)m * I * 2);
+            o.du = take((size_t)m * I * 2);
+        }
+    }
+    o.total = off;
+    return o;
+}
+
+// The checks every call on a handle makes; *lo is the layout.
+int check_call(const moe_ffn* f, int64_t m, bool backward, void* ws, size_t ws_bytes, Layout* lo) {
+    if (!f || m < 0) return MOE_ERR_INVALID_ARG;
+    if (m > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dev != f->device) return MOE_ERR_INVALID_ARG;
+    if (m == 0) return MOE_OK;
+    *lo = layout(f, m, backward);
+    if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < lo->total) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+bool bad_rows(const void* p, int64_t ld, int64_t n) { return !p || !aligned(p, 16) || ld < n || ld % 8 || ld > (int64_t)1 << 38; }
+
+int prepare_header(const moe_ffn* f, void* ws, cudaStream_t st) {
+    if (f->last_ws == ws) return MOE_OK;
+    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return MOE_ERR_CUDA;
+    f->last_ws = ws;
+    return MOE_OK;
+}
+
+FfnProducts products(const moe_ffn* f, void* ws) {
+    FfnProducts p{};
+    p.act = f->cfg.activation;
+    p.hdr = at<WsHeader>(ws, 0);
+    p.wait_ns = kWaitNs;
+    return p;
+}
+
+// A product of one source, D [M, N] over K.
+FfnProduct& add(FfnProducts& p, int M, int N, int K, void* out) {
+    FfnProduct& q = p.p[p.count++];
+    q.sources = 1;
+    q.M = M;
+    q.N = N;
+    q.kblocks = ceil_div(K, 64);
+    q.out = static_cast<uint16_t*>(out);
+    return q;
+}
+
+int forward_bf16(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, void* saved,
+                 void* ws, cudaStream_t st) {
+    const int H = f->cfg.hidden, I = f->cfg.inter;
+    FfnProducts p = products(f, ws);
+    FfnProduct& gu = add(p, m, I, H, at<void>(ws, lo.h));
+    if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
+    gu.b[0] = f->k1;
+    gu.b[1] = f->k3;
+    p.o1 = static_cast<uint16_t*>(saved);
+    p.o2 = saved ? p.o1 + (size_t)m * I : nullptr;
+    if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
+    FfnProducts d = products(f, ws);
+    FfnProduct& y = add(d, m, H, I, out);
+    if (!ffn_map(&y.a[0], at<void>(ws, lo.h), m, I, I, 128)) return MOE_ERR_CUDA;
+    y.b[0] = f->k2;
+    if (launch_ffn_products(d, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
+    f->last_launches = 2;
+    return MOE_OK;
+}
+
+MxProduct mx_product(int M, int N, int K, void* ws) {
+    MxProduct p{};
+    p.M = M;
+    p.N = N;
+    p.kblocks = ceil_div(K, 256);
+    p.hdr = at<WsHeader>(ws, 0);
+    p.wait_ns = kWaitNs;
+    return p;
+}
+
+int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, void* ws,
+                  cudaStream_t st) {
+    const int H = f->cfg.hidden, I = f->cfg.inter;
+    uint8_t *xq = at<uint8_t>(ws, lo.xq), *xs = at<uint8_t>(ws, lo.xs), *hq = at<uint8_t>(ws, lo.hq),
+            *hs = at<uint8_t>(ws, lo.hs);
+    MxProduct g = mx_product(m, I, H, ws), d = mx_product(m, H, I, ws);
+    if (!mx_code_map(&g.a, xq, m, H, 128) || !mx_scale_map(&g.as, xs, m, H) || !mx_code_map(&d.a, hq, m, I, 128) ||
+        !mx_scale_map(&d.as, hs, m, I))
+        return MOE_ERR_CUDA;
+    g.b[0] = f->k1;
+    g.b[1] = f->k3;
+    g.bs[0] = f->s1;
+    g.bs[1] = f->s3;
+    g.act = f->cfg.activation;
+    g.codes = hq;
+    g.scales = hs;
+    g.nkt = ceil_div(I, 128);
+    d.b[0] = f->k2;
+    d.bs[0] = f->s2;
+    d.out = static_cast<uint16_t*>(out);
+    if (launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) != cudaSuccess ||
+        launch_mx_product(g, true, st) != cudaSuccess || launch_mx_product(d, false, st) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    f->last_launches = 3;
+    return MOE_OK;
+}
+
+int quant(const void* x, bool f32, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+          void* stream) {
+    if (rows < 0 || n <= 0 || n % 32) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (rows > INT32_MAX / 64 || n > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    if (!x || !aligned(x, 16) || ldx < n || ldx % (f32 ? 4 : 8) || !codes || !scales || !aligned(codes, 16) ||
+        !aligned(scales, 16))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx_quant(x, f32, (size_t)ldx, (int)rows, (int)n, codes, scales, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_ffn_create(const moe_ffn_config* cfg, const moe_ffn_weights* w, moe_ffn** out) {
+    if (!out) return MOE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!cfg || !w) return MOE_ERR_INVALID_ARG;
+    const moe_ffn_config& c = *cfg;
+    if (c.weights != MOE_WEIGHTS_BF16 && c.weights != MOE_WEIGHTS_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (c.activation != MOE_ACT_SILU && c.activation != MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    const bool mx = c.weights == MOE_WEIGHTS_MXFP4;
+    const int mult = mx ? 32 : 8;
+    if (c.hidden <= 0 || c.inter <= 0) return MOE_ERR_INVALID_ARG;
+    if (c.hidden % mult || c.inter % mult || c.hidden > kMaxDim || c.inter > kMaxDim) return MOE_ERR_UNSUPPORTED;
+    const void* ptrs[6] = {w->w1, w->w3, w->w2, w->s1, w->s3, w->s2};
+    for (int i = 0; i < 6; ++i) {
+        if (i >= 3 && !mx) {
+            if (ptrs[i]) return MOE_ERR_INVALID_ARG;
+        } else if (!ptrs[i] || !aligned(ptrs[i], 16)) {
+            return MOE_ERR_INVALID_ARG;
+        }
+    }
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    moe_ffn* f = new (std::nothrow) moe_ffn();
+    if (!f) return MOE_ERR_CUDA;
+    f->cfg = c;
+    f->w = *w;
+    f->device = dev;
+    const uint64_t H = c.hidden, I = c.inter;
+    const bool ok = mx ? mx_code_map(&f->k1, w->w1, I, H, 128) && mx_code_map(&f->k3, w->w3, I, H, 128) &&
+                             mx_code_map(&f->k2, w->w2, H, I, 128) && mx_scale_map(&f->s1, w->s1, I, H) &&
+                             mx_scale_map(&f->s3, w->s3, I, H) && mx_scale_map(&f->s2, w->s2, H, I)
+                       : ffn_map(&f->k1, w->w1, I, H, H, 128) && ffn_map(&f->k3, w->w3, I, H, H, 128) &&
+                             ffn_map(&f->k2, w->w2, H, I, I, 128) && ffn_map(&f->mn1, w->w1, I, H, H, 64) &&
+                             ffn_map(&f->mn3, w->w3, I, H, H, 64) && ffn_map(&f->mn2, w->w2, H, I, I, 64);
+    if (!ok) {
+        delete f;
+        return MOE_ERR_CUDA;
+    }
+    *out = f;
+    return MOE_OK;
+}
+
+int moe_ffn_destroy(moe_ffn* f) {
+    delete f;
+    return MOE_OK;
+}
+
+int moe_ffn_workspace_size(const moe_ffn* f, int64_t m, int backward, size_t* bytes) {
+    if (!f || m < 0 || !bytes || (backward != 0 && backward != 1)) return MOE_ERR_INVALID_ARG;
+    if (m > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    *bytes = layout(f, m, backward != 0).total;
+    return MOE_OK;
+}
+
+int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, void* out, void* saved, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    Layout lo;
+    const int rc = check_call(f, m, false, workspace, workspace_bytes, &lo);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 16)))
+        return MOE_ERR_INVALID_ARG;
+    const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
+    if (mx && saved) return MOE_ERR_UNSUPPORTED;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
+    return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
+              : forward_bf16(f, lo, x, ldx, (int)m, out, saved, workspace, st);
+}
+
+int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void* x, int64_t ldx, const void* saved,
+                     int64_t m, void* dx, void* dw1, void* dw3, void* dw2, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    Layout lo;
+    if (f && f->cfg.weights != MOE_WEIGHTS_BF16) return MOE_ERR_UNSUPPORTED;
+    const int rc = check_call(f, m, true, workspace, workspace_bytes, &lo);
+    if (rc != MOE_OK || m == 0) return rc;
+    const int H = f->cfg.hidden, I = f->cfg.inter, n = (int)m;
+    const bool dw = dw1 || dw3 || dw2;
+    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !aligned(saved, 16) || (dx && !aligned(dx, 16)) ||
+        (dw && (!dw1 || !dw3 || !dw2 || !aligned(dw1, 16) || !aligned(dw3, 16) || !aligned(dw2, 16))))
+        return MOE_ERR_INVALID_ARG;
+    if (!dx && !dw) return MOE_OK;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
+    void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du), *h = at<void>(workspace, lo.h);
+    // dh = dout W2 and, in its epilogue, dg, du and h
+    FfnProducts p = products(f, workspace);
+    FfnProduct& q = add(p, n, I, H, dg);
+    if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
+    q.b[0] = f->mn2;
+    q.b_mn = 1;
+    p.g = static_cast<const uint16_t*>(saved);
+    p.u = p.g + (size_t)m * I;
+    p.o1 = static_cast<uint16_t*>(du);
+    p.o2 = static_cast<uint16_t*>(h);
+    if (launch_ffn_products(p, EPI_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
+    // the four products that need them, in one launch
+    FfnProducts r = products(f, workspace);
+    if (dx) {
+        FfnProduct& d = add(r, n, H, I, dx);
+        d.sources = 2;
+        if (!ffn_map(&d.a[0], dg, m, I, I, 128) || !ffn_map(&d.a[1], du, m, I, I, 128)) return MOE_ERR_CUDA;
+        d.b[0] = f->mn1;
+        d.b[1] = f->mn3;
+        d.b_mn = 1;
+    }
+    if (dw) {
+        CUtensorMap mx, md, mdg, mdu, mh;
+        if (!ffn_map(&mx, x, m, H, ldx, 64) || !ffn_map(&md, dout, m, H, ldd, 64) || !ffn_map(&mdg, dg, m, I, I, 64) ||
+            !ffn_map(&mdu, du, m, I, I, 64) || !ffn_map(&mh, h, m, I, I, 64))
+            return MOE_ERR_CUDA;
+        FfnProduct& g1 = add(r, I, H, n, dw1);
+        g1.a[0] = mdg;
+        g1.b[0] = mx;
+        FfnProduct& g3 = add(r, I, H, n, dw3);
+        g3.a[0] = mdu;
+        g3.b[0] = mx;
+        FfnProduct& g2 = add(r, H, I, n, dw2);
+        g2.a[0] = md;
+        g2.b[0] = mh;
+        for (FfnProduct* g : {&g1, &g3, &g2}) g->a_mn = g->b_mn = 1;
+    }
+    if (launch_ffn_products(r, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
+    f->last_launches = 2;
+    return MOE_OK;
+}
+
+int moe_ffn_last_launch_count(const moe_ffn* f) { return f ? f->last_launches : -1; }
+
+int moe_mxfp4_scales_size(int64_t rows, int64_t n, size_t* bytes) {
+    if (rows < 0 || n <= 0 || n % 32 || !bytes) return MOE_ERR_INVALID_ARG;
+    if (rows > INT32_MAX / 64 || n > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    *bytes = scale_bytes(rows, n);
+    return MOE_OK;
+}
+
+int moe_mxfp4_quant(const void* x, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+                    void* stream) {
+    return quant(x, false, ldx, rows, n, codes, scales, stream);
+}
+
+int moe_mxfp4_quant_f32(const float* x, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
+                        void* stream) {
+    return quant(x, true, ldx, rows, n, codes, scales, stream);
+}
+
+int moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t n, void* out, void* stream) {
+    if (rows < 0 || n <= 0 || n % 32) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    if (rows > INT32_MAX / 64 || n > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    if (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16))
+        return MOE_ERR_INVALID_ARG;
+    return launch_mx_dequant(codes, scales, (int)rows, (int)n, static_cast<uint16_t*>(out),
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+int moe_mxfp4_gemm_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+    if (m < 0 || n <= 0 || n % 8 || k <= 0 || k % 32 || !bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = align_up(sizeof(WsHeader));
+    return MOE_OK;
+}
+
+int moe_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, const uint8_t* b_codes,
+                   const uint8_t* b_scales, int64_t n, int64_t k, void* out, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+    size_t need = 0;
+    const int rc = moe_mxfp4_gemm_workspace_size(m, n, k, &need);
+    if (rc != MOE_OK) return rc;
+    if (m > INT32_MAX / 64 || n > kMaxDim || k > kMaxDim) return MOE_ERR_UNSUPPORTED;
+    if (m == 0) return MOE_OK;
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    for (const void* p : {(const void*)a_codes, (const void*)a_scales, (const void*)b_codes, (const void*)b_scales,
+                          (const void*)out})
+        if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+    MxProduct g = mx_product((int)m, (int)n, (int)k, workspace);
+    if (!mx_code_map(&g.a, a_codes, m, k, 128) || !mx_scale_map(&g.as, a_scales, m, k) ||
+        !mx_code_map(&g.b[0], b_codes, n, k, 128) || !mx_scale_map(&g.bs[0], b_scales, n, k))
+        return MOE_ERR_CUDA;
+    g.out = static_cast<uint16_t*>(out);
+    return launch_mx_product(g, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,75 @@
+// Dense gated feed-forward block and MXFP4 operators: host interface of their
+// kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_ffn_block.h"
+
+namespace moe {
+
+struct WsHeader;
+
+// What a product's epilogue makes of its fp32 sums.
+enum FfnEpilogue : int {
+    EPI_STORE = 0,    // out = D
+    EPI_GATEUP,       // D = (g, u) side by side: out = act(g) u
+    EPI_GATEUP_SAVE,  // ... and g, u themselves
+    EPI_DACT,         // D = dh: dg = dh u act'(g), du = dh act(g), h = act(g) u
+};
+
+// One product D[M, N] = sum over one or two sources of A B^T, as a work list
+// of 256 x 256 tiles (gate/up: 256 rows x 128 columns of g and of u).
+struct FfnProduct {
+    CUtensorMap a[2], b[2];  // per source (gate/up: b = W1, W3, one source)
+    int a_mn, b_mn;          // operand stored along M (N) instead of along K
+    int kblocks;             // 64-wide K blocks per source
+    int sources;
+    int m_tiles, n_tiles;
+    int M, N;
+    uint16_t* out;           // [M, N], row stride N
+};
+constexpr int kMaxProducts = 4;
+struct FfnProducts {
+    FfnProduct p[kMaxProducts];
+    int count;
+    int first[kMaxProducts + 1];  // first work item of each product
+    int act;
+    const uint16_t *g, *u;  // EPI_DACT: saved pre-activations
+    uint16_t *o1, *o2;      // EPI_GATEUP_SAVE: g, u; EPI_DACT: du, h (out: dg)
+    WsHeader* hdr;
+    uint64_t wait_ns;
+};
+
+// Maps of a bf16 operand [rows, cols] (row stride ld elements).  K-major: 64 of
+// K x box_rows rows; MN-major: 64 of M x 64 rows of K.
+bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
+
+cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st);
+
+// One MXFP4 product (codes and packed scales of both sides).
+struct MxProduct {
+    CUtensorMap a, as;        // codes [M, K/2], scale tiles
+    CUtensorMap b[2], bs[2];  // one matrix, or W1 and W3 (gate/up)
+    int kblocks;              // ceil(K / 256)
+    int m_tiles, n_tiles;
+    int M, N;
+    int act;
+    uint16_t* out;            // EPI_STORE: bf16 [M, N]
+    uint8_t *codes, *scales;  // EPI_GATEUP: h as MXFP4, [M, N/2] and packed scales
+    int nkt;                  // ... scale tiles per row of it
+    WsHeader* hdr;
+    uint64_t wait_ns;
+};
+bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, uint32_t box_rows);
+bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k);
+cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st);
+
+cudaError_t launch_mx_quant(const void* x, bool f32, size_t ldx, int rows, int n, uint8_t* codes, uint8_t* scales,
+                            cudaStream_t st);
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int n, uint16_t* out,
+                              cudaStream_t st);
+
+}  // namespace moe

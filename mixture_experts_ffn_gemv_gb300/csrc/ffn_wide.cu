@@ -1,0 +1,381 @@
+// bf16 products of the gated feed-forward block and of its backward pass on
+// the tensor cores, for many tokens.
+//
+// One persistent kernel on CTA pairs (a cluster of two, cta_group::2) works
+// through the 256 x 256 tiles of up to four products D = A B^T; a product's
+// reduction runs over one or two sources (dx = dg W1 + du W3 is one sum of
+// length 2 I), and either operand may be stored along K or along M (N): the
+// backward products read W, x, dg and h as they lie, through MN-major
+// descriptors, so nothing is transposed in memory.
+//   warp 0      TMA producer: this CTA's 128 rows of A and half of the tile's
+//               256 rows of B, 64 of K per stage, 7 stages of 32 KB;
+//   warp 1      (leader) MMA issuer: M = 256, N = 256, fp32 accumulators in
+//               TMEM, two buffers of 256 columns;
+//   warps 2..9  epilogue, two per TMEM lane quarter, each half of the columns.
+// Gate/up: the leader's half of B is 128 rows of W1, the peer's the same rows
+// of W3, so a thread finds g and u of one element in its own lane.
+// Every wait is bounded; on expiry the CTA records DEV_ERR_TIMEOUT, stops
+// issuing, waits (2 s at most) for its copies and MMAs in flight, frees TMEM
+// and returns.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ffn_act.cuh"
+#include "ffn_block.h"
+#include "launch.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int STAGES = 7;
+constexpr int A_BYTES = BM * BK * 2, B_BYTES = 128 * BK * 2;  // per CTA
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int TMEM_COLS = 2 * BN;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
+
+__device__ __forceinline__ void load8bf(const uint16_t* p, float* v) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16lo(w[i]);
+        v[2 * i + 1] = bf16hi(w[i]);
+    }
+}
+
+struct Item {
+    int op, mt, nt;
+};
+__device__ __forceinline__ Item item_of(const FfnProducts& p, int t) {
+    Item it;
+    it.op = 0;
+#pragma unroll
+    for (int i = 1; i < kMaxProducts; ++i)
+        if (i < p.count && t >= p.first[i]) it.op = i;
+    const int r = t - p.first[it.op];
+    it.mt = r / p.p[it.op].n_tiles;
+    it.nt = r % p.p[it.op].n_tiles;
+    return it;
+}
+
+template <int EPI>
+__global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
+    constexpr bool GATEUP = EPI == EPI_GATEUP || EPI == EPI_GATEUP_SAVE;
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+    const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = smem_u32(bars + 2 * STAGES + 2);
+    const uint32_t drain = smem_u32(bars + 2 * STAGES + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(tfull0 + 8 * a, 1);
+            mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either signals the other
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = p.first[p.count];
+    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t lead_full0 = mapa(full0, 0), lead_tempty0 = mapa(tempty0, 0);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = cl; t < total && ok; t += ncl) {
+                if (*abort_flag) break;
+                const Item w = item_of(p, t);
+                const FfnProduct& q = p.p[w.op];
+                const int m0 = w.mt * 256 + (int)rank * BM;
+                const int n0 = GATEUP ? w.nt * 128 : w.nt * 256 + (int)rank * 128;
+                for (int src = 0; src < q.sources && ok; ++src) {
+                    const CUtensorMap* ma = &q.a[src];
+                    const CUtensorMap* mb = &q.b[GATEUP ? rank : src];
+                    for (int kb = 0; kb < q.kblocks; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                        if (!mbar_wait_cluster(empty0 + 8 * s, ph ^ 1u, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES, bar = lead_full0 + 8 * s;
+                        if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * STAGE_BYTES);
+                        if (q.a_mn) {
+                            tma_load_2d_pair(sa, ma, m0, kb * BK, bar);
+                            tma_load_2d_pair(sa + A_BYTES / 2, ma, m0 + 64, kb * BK, bar);
+                        } else {
+                            tma_load_2d_pair(sa, ma, kb * BK, m0, bar);
+                        }
+                        if (q.b_mn) {
+                            tma_load_2d_pair(sb, mb, n0, kb * BK, bar);
+                            tma_load_2d_pair(sb + B_BYTES / 2, mb, n0 + 64, kb * BK, bar);
+                        } else {
+                            tma_load_2d_pair(sb, mb, kb * BK, n0, bar);
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 21);
+                *abort_flag = 1;
+            }
+            if (leader) {
+                // every issued copy of both CTAs has landed before either can exit
+                for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
+                    mbar_wait_cluster(full0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
+            } else if (!ok || *abort_flag) {
+                // the peer's copies complete on the leader's barriers: after an
+                // abort, give any still in flight time to land
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t it = 0, tc = 0;
+            bool ok = true;
+            for (int t = cl; t < total && ok; t += ncl, ++tc) {
+                if (*abort_flag) break;
+                const FfnProduct& q = p.p[item_of(p, t).op];
+                const uint32_t idesc = idesc_bf16(2 * BM, BN) | (q.a_mn ? kIdescAMn : 0u) | (q.b_mn ? kIdescBMn : 0u);
+                // 16 of K further: 32 bytes along a swizzled row, or 16 rows of 128
+                const uint32_t sta = q.a_mn ? 128 : 2, stb = q.b_mn ? 128 : 2;
+                const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
+                if (!mbar_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + acc * BN;
+                const int kbs = q.kblocks * q.sources;
+                for (int kb = 0; kb < kbs; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES;
+                    const uint64_t ad = q.a_mn ? desc_sw128_mn(sa) : desc_sw128(sa);
+                    const uint64_t bd = q.b_mn ? desc_sw128_mn(sb) : desc_sw128(sb);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        mma_bf16_pair(d, ad + sta * kk, bd + stb * kk, idesc, (kb | kk) != 0);
+                    mma_commit_pair(empty0 + 8 * s);
+                }
+                if (!ok) break;
+                mma_commit_pair(tfull0 + 8 * acc);
+            }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 22);
+                *abort_flag = 1;
+            }
+            mma_commit_pair(drain);
+            mbar_wait_cluster(drain, 0, DRAIN_NS);
+        }
+        __syncwarp();
+    } else {
+        const int q4 = warp & 3;           // the TMEM lane quarter this warp may read
+        const int half = (warp - 2) >> 2;  // which half of the tile's columns
+        uint32_t tc = 0;
+        for (int t = cl; t < total; t += ncl, ++tc) {
+            if (*abort_flag) break;
+            const Item w = item_of(p, t);
+            const FfnProduct& q = p.p[w.op];
+            const int r = w.mt * 256 + (int)rank * BM + q4 * 32 + lane;  // this thread's row of D
+            const bool ok = r < q.M;
+            const bool any = r - lane < q.M;  // of its warp
+            const int N = q.N;
+            const bool wide = (N & 15) == 0;
+            const size_t at = (size_t)r * N;
+            const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
+            if (!mbar_wait_cluster(tfull0 + 8 * acc, aph, p.wait_ns)) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 23);
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16) + acc * BN;
+            if (!any) {
+                // a lane quarter past the last row
+            } else if (GATEUP) {
+#pragma unroll 1
+                for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                    const int col = w.nt * 128 + c * 32;
+                    if (col >= N) break;
+                    uint32_t gv[32], uv[32];
+                    tmem_ld32(taddr + c * 32, gv);
+                    tmem_ld32(taddr + 128 + c * 32, uv);
+                    tmem_wait_ld();
+                    if (ok) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            uint32_t o[8], og[8], ou[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float g0 = __uint_as_float(gv[16 * v + 2 * i]), g1 = __uint_as_float(gv[16 * v + 2 * i + 1]);
+                                const float u0 = __uint_as_float(uv[16 * v + 2 * i]), u1 = __uint_as_float(uv[16 * v + 2 * i + 1]);
+                                o[i] = pack_bf16x2(glu(g0, u0, p.act), glu(g1, u1, p.act));
+                                og[i] = pack_bf16x2(g0, g1);
+                                ou[i] = pack_bf16x2(u0, u1);
+                            }
+                            store_row16(q.out + at, col + 16 * v, N, wide, o);
+                            if (EPI == EPI_GATEUP_SAVE) {
+                                store_row16(p.o1 + at, col + 16 * v, N, wide, og);
+                                store_row16(p.o2 + at, col + 16 * v, N, wide, ou);
+                            }
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 4 * half; c < 4 * half + 4; ++c) {
+                    const int col = w.nt * 256 + c * 32;
+                    if (col >= N) break;
+                    uint32_t dv[32];
+                    tmem_ld32(taddr + c * 32, dv);
+                    tmem_wait_ld();
+                    if (ok) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const int cv = col + 16 * v;
+                            if (EPI == EPI_DACT) {
+                                uint32_t og[8], ou[8], oh[8];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    if (cv + 8 * e >= N) break;
+                                    float g[8], u[8], dg[8], du[8], h[8];
+                                    load8bf(p.g + at + cv + 8 * e, g);
+                                    load8bf(p.u + at + cv + 8 * e, u);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const float dh = __uint_as_float(dv[16 * v + 8 * e + i]);
+                                        float a, slope;
+                                        act_slope(g[i], p.act, a, slope);
+                                        dg[i] = dh * u[i] * slope;
+                                        du[i] = dh * a;
+                                        h[i] = a * u[i];
+                                    }
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        og[4 * e + i] = pack_bf16x2(dg[2 * i], dg[2 * i + 1]);
+                                        ou[4 * e + i] = pack_bf16x2(du[2 * i], du[2 * i + 1]);
+                                        oh[4 * e + i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
+                                    }
+                                }
+                                store_row16(q.out + at, cv, N, wide, og);
+                                store_row16(p.o1 + at, cv, N, wide, ou);
+                                store_row16(p.o2 + at, cv, N, wide, oh);
+                            } else {
+                                uint32_t o[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    o[i] = pack_bf16x2(__uint_as_float(dv[16 * v + 2 * i]), __uint_as_float(dv[16 * v + 2 * i + 1]));
+                                store_row16(q.out + at, cv, N, wide, o);
+                            }
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other may still signal it or read its TMEM
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+int sms() {
+    static int n = device_sm_count();
+    return n;
+}
+
+template <int EPI>
+cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
+    static cudaError_t attr =
+        cudaFuncSetAttribute(ffn_products<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (attr != cudaSuccess) return attr;
+    const int pairs = std::max(1, std::min(sms() / 2, p.first[p.count]));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, ffn_products<EPI>, p);
+}
+
+}  // namespace
+
+bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    const uint64_t dims[2] = {cols, rows};
+    return tmap_encode(m, p, 2, dims, 2, BK, box_rows, true, ld);
+}
+
+cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
+    const int bn = epilogue == EPI_GATEUP || epilogue == EPI_GATEUP_SAVE ? 128 : 256;
+    p.first[0] = 0;
+    for (int i = 0; i < p.count; ++i) {
+        FfnProduct& q = p.p[i];
+        q.m_tiles = ceil_div(q.M, 256);
+        q.n_tiles = ceil_div(q.N, bn);
+        p.first[i + 1] = p.first[i] + q.m_tiles * q.n_tiles;
+    }
+    switch (epilogue) {
+        case EPI_GATEUP: return launch<EPI_GATEUP>(p, st);
+        case EPI_GATEUP_SAVE: return launch<EPI_GATEUP_SAVE>(p, st);
+        case EPI_DACT: return launch<EPI_DACT>(p, st);
+        default: return launch<EPI_STORE>(p, st);
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,311 @@
+// MXFP4 products for many tokens on the block-scaled fp4 MMA
+// (tcgen05.mma kind::mxf4, K = 64, one e8m0 scale per 32).
+//
+// A persistent kernel on CTA pairs; tiles are 256 rows x 256 columns (gate/up:
+// 128 columns of g and the same of u).  A stage is 256 of K: this CTA's 128
+// rows of A codes (16 KB, 128-byte swizzle), its half of the 256 rows of B
+// (16 KB), and the packed scales of its A rows (1 KB) and of all 256 B rows
+// (2 KB), which each CTA needs whole.  The scales are packed in the order that
+// tcgen05.cp moves them to tensor memory, so the MMA issuer itself copies a
+// stage's scales and issues its MMAs, with no other warp in between.
+// TMEM: one accumulator of 256 columns and 24 scale columns per stage.  One
+// accumulator, not two: 256 x 256 tiles halve the operand bytes per product
+// of the 128 x 128 tiles that would leave room for two, and the epilogue holds
+// up the next tile only while it reads the accumulator.
+// Gate/up quantises h in its epilogue: a thread's 32 columns of a row are one
+// MXFP4 block, so h never exists in wider form.
+//   warp 0 producer, warp 1 (leader) issuer, warps 2..9 epilogue.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ffn_act.cuh"
+#include "ffn_block.h"
+#include "launch.cuh"
+#include "mxfp4.cuh"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 256;
+constexpr int BKB = 128;  // bytes of K per stage and row: 256 codes
+constexpr int STAGES = 6;
+constexpr int A_BYTES = BM * BKB, B_BYTES = 128 * BKB;
+constexpr int SA_BYTES = 2 * 512, SB_BYTES = 2 * 2 * 512;  // two K tiles x one / two row tiles
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+constexpr int B_OFF = A_BYTES, SA_OFF = B_OFF + B_BYTES, SB_OFF = SA_OFF + SA_BYTES;
+constexpr int STAGE_STRIDE = 35 * 1024;
+static_assert(STAGE_BYTES == STAGE_STRIDE, "stages keep the swizzle's 1024-byte alignment");
+constexpr int TMEM_COLS = 512;
+constexpr int SF_COL0 = BN, SF_COLS = 24;  // per stage: 2 K tiles x (4 of A + 8 of B)
+static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "accumulator and scale columns fit tensor memory");
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_STRIDE + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
+
+template <bool GATEUP>
+__global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__ MxProduct p) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_STRIDE);
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+    const uint32_t tfull = smem_u32(bars + 2 * STAGES), tempty = smem_u32(bars + 2 * STAGES + 1);
+    const uint32_t drain = smem_u32(bars + 2 * STAGES + 2);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 3);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 2 * EPI_WARPS);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = p.m_tiles * p.n_tiles;
+    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const uint32_t lead_full0 = mapa(full0, 0), lead_tempty = mapa(tempty, 0);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = cl; t < total && ok; t += ncl) {
+                if (*abort_flag) break;
+                const int mt = t / p.n_tiles, nt = t % p.n_tiles;
+                const int m0 = mt * 256 + (int)rank * BM;
+                const int n0 = GATEUP ? nt * 128 : nt * 256 + (int)rank * 128;
+                const CUtensorMap* mb = &p.b[GATEUP ? rank : 0];
+                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait_cluster(empty0 + 8 * s, ph ^ 1u, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = sbase + s * STAGE_STRIDE, bar = lead_full0 + 8 * s;
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * STAGE_BYTES);
+                    tma_load_2d_pair(sa, &p.a, kb * BKB, m0, bar);
+                    tma_load_2d_pair(sa + B_OFF, mb, kb * BKB, n0, bar);
+                    tma_load_3d_pair(sa + SA_OFF, &p.as, 0, 2 * kb, m0 >> 7, bar);
+                    tma_load_3d_pair(sa + SB_OFF, &p.bs[0], 0, 2 * kb, GATEUP ? nt : 2 * nt, bar);
+                    tma_load_3d_pair(sa + SB_OFF + 1024, &p.bs[GATEUP ? 1 : 0], 0, 2 * kb, GATEUP ? nt : 2 * nt + 1, bar);
+                }
+            }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 31);
+                *abort_flag = 1;
+            }
+            if (leader) {
+                for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
+                    mbar_wait_cluster(full0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
+            } else if (!ok || *abort_flag) {
+                const uint64_t t0 = globaltimer();
+                while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t it = 0, tc = 0;
+            bool ok = true;
+            for (int t = cl; t < total && ok; t += ncl, ++tc) {
+                if (*abort_flag) break;
+                if (!mbar_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = sbase + s * STAGE_STRIDE;
+                    const uint32_t sf = tmem_base + SF_COL0 + s * SF_COLS;
+                    // columns: A tiles of K 0..127, 128..255; then per K tile the two B row tiles
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt) {
+                        tmem_cp_scales_pair(sf + 4 * kt, desc_scales(sa + SA_OFF + kt * 512));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tmem_cp_scales_pair(sf + 8 + 8 * kt + 4 * h, desc_scales(sa + SB_OFF + h * 1024 + kt * 512));
+                    }
+                    const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + B_OFF);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mxf4_pair(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc_mxf4(2 * BM, BN, 2 * (kk & 1)),
+                                      sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb | kk) != 0);
+                    mma_commit_pair(empty0 + 8 * s);
+                }
+                if (!ok) break;
+                mma_commit_pair(tfull);
+            }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 32);
+                *abort_flag = 1;
+            }
+            mma_commit_pair(drain);
+            mbar_wait_cluster(drain, 0, DRAIN_NS);
+        }
+        __syncwarp();
+    } else {
+        const int q4 = warp & 3, half = (warp - 2) >> 2;
+        uint32_t tc = 0;
+        for (int t = cl; t < total; t += ncl, ++tc) {
+            if (*abort_flag) break;
+            const int mt = t / p.n_tiles, nt = t % p.n_tiles;
+            const int r = mt * 256 + (int)rank * BM + q4 * 32 + lane;
+            const bool ok = r < p.M, any = r - lane < p.M;
+            if (!mbar_wait_cluster(tfull, tc & 1u, p.wait_ns)) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 33);
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16);
+            if (!any) {
+                // a lane quarter past the last row
+            } else if (GATEUP) {
+                uint32_t word = 0;  // this thread's two scale bytes
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 2 * half + j, col = nt * 128 + c * 32;
+                    if (col >= p.N) break;
+                    uint32_t gv[32], uv[32];
+                    tmem_ld32(taddr + c * 32, gv);
+                    tmem_ld32(taddr + 128 + c * 32, uv);
+                    tmem_wait_ld();
+                    float h[32];
+                    uint32_t a = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        h[i] = glu(__uint_as_float(gv[i]), __uint_as_float(uv[i]), p.act);
+                        a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
+                    }
+                    const uint32_t s = mx_scale(a);
+                    const float inv = mx_inverse(s);
+                    if (ok) {
+                        uint4 w;
+                        w.x = mx_codes8(h, inv);
+                        w.y = mx_codes8(h + 8, inv);
+                        w.z = mx_codes8(h + 16, inv);
+                        w.w = mx_codes8(h + 24, inv);
+                        if (s == 255u) w = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(p.codes + ((size_t)r * p.N + col) / 2) = w;
+                    }
+                    word |= s << (8 * j);
+                }
+                // two blocks of the row's scale tile; blocks past the last column are 0
+                if (ok) *reinterpret_cast<uint16_t*>(p.scales + mx_scale_at(r, (size_t)nt * 4 + 2 * half, p.nkt)) = (uint16_t)word;
+            } else {
+                const bool wide = (p.N & 15) == 0;
+                uint16_t* row = p.out + (size_t)r * p.N;
+#pragma unroll 1
+                for (int c = 4 * half; c < 4 * half + 4; ++c) {
+                    const int col = nt * 256 + c * 32;
+                    if (col >= p.N) break;
+                    uint32_t dv[32];
+                    tmem_ld32(taddr + c * 32, dv);
+                    tmem_wait_ld();
+                    if (ok) {
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                o[i] = pack_bf16x2(__uint_as_float(dv[16 * v + 2 * i]), __uint_as_float(dv[16 * v + 2 * i + 1]));
+                            store_row16(row, col + 16 * v, p.N, wide, o);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_tempty);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+int sms() {
+    static int n = device_sm_count();
+    return n;
+}
+
+template <bool GATEUP>
+cudaError_t launch(const MxProduct& p, cudaStream_t st) {
+    static cudaError_t attr =
+        cudaFuncSetAttribute(mx_product<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (attr != cudaSuccess) return attr;
+    const int pairs = std::max(1, std::min(sms() / 2, p.m_tiles * p.n_tiles));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mx_product<GATEUP>, p);
+}
+
+}  // namespace
+
+// Codes [rows, k/2]: boxes of 128 bytes x box_rows rows, 128-byte swizzle.
+bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, uint32_t box_rows) {
+    const uint64_t dims[2] = {k / 2, rows};
+    return tmap_encode(m, codes, 2, dims, 1, BKB, box_rows);
+}
+// Packed scales as [row tiles][K tiles][256 x 16 bits]: boxes of two K tiles of
+// one row tile (tiles past the end read as zero: scale 2^-127 on zero codes).
+bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k) {
+    const uint64_t dims[3] = {256, (k + 127) / 128, (rows + 127) / 128};
+    return tmap_encode(m, scales, 3, dims, 2, 256, 2, false);
+}
+
+cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st) {
+    p.m_tiles = ceil_div(p.M, 256);
+    p.n_tiles = ceil_div(p.N, gateup ? 128 : 256);
+    return gateup ? launch<true>(p, st) : launch<false>(p, st);
+}
+
+}  // namespace moe

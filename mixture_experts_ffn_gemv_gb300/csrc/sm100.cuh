@@ -250,5 +250,60 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
         : "memory");
 }
 
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte
+// swizzled layout: TMA boxes of 64 M (or N) elements x 64 of K, each 8 KB --
+// K rows of 128 bytes, 8 of them per 1024-byte atom -- one after another along
+// M.  The next 8 rows of K are 1024 bytes on (stride byte offset), the next 64
+// elements of M 8192 bytes on (leading byte offset).
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Unswizzled 32 rows x 16 bytes (a tile of packed MXFP4 scales): 8-row groups
+// of 128 bytes follow one another.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+// Instruction-descriptor bits that mark A or B as MN-major.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
+// ---- block-scaled fp4 (kind::mxf4: e2m1 operands, one e8m0 scale per 32)
+// Instruction descriptor: A and B e2m1 (format 1), e8m0 scales (bit 23), fp32
+// D, both K-major.  sf picks the byte pair of the scale words that an MMA
+// (K = 64, two scales per row) reads: 0 or 2, for A and for B.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+           ((uint32_t)sf << 4) | ((uint32_t)sf << 29);
+}
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// One tile of packed scales (32 rows x 16 bytes of shared memory) to four TMEM
+// columns, repeated in every lane quarter; a later tcgen05.mma of the same
+// thread sees it.  _pair: in both CTAs, each from its own shared memory.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 }  // namespace sm100
 }  // namespace moe

@@ -1,0 +1,142 @@
+"""The gated feed-forward block and MXFP4 entry points without a GPU: refusals, sizes, the scale
+order, and the formulas the GPU tests compare against."""
+import ctypes
+
+import pytest
+import torch
+
+import _ffn_plain as P
+
+FAKE = 0x10000  # never dereferenced: the calls fail before any device access
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_ffn_gemv_gb300 import binding
+    binding.load_library()
+    return binding
+
+
+def _create(B, ptrs=None, **kw):
+    c = dict(hidden=256, inter=128, activation=0, weights=0)
+    c.update(kw)
+    cfg = B.MoeFfnConfig(*(c[k] for k in ("hidden", "inter", "activation", "weights")))
+    if ptrs is None:
+        ptrs = [FAKE] * (6 if c["weights"] == 3 else 3)
+    w = B.MoeFfnWeights(*ptrs)
+    out = ctypes.c_void_p()
+    rc = B.load_library().moe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(out))
+    assert not out.value
+    return rc
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(hidden=0), 1), (dict(inter=-8), 1),
+    (dict(hidden=100), 2), (dict(inter=12), 2),                      # bf16: multiples of 8
+    (dict(weights=3, hidden=40), 2), (dict(weights=3, inter=48), 2),  # MXFP4: multiples of 32
+    (dict(hidden=(1 << 20) + 8), 2),
+    (dict(activation=2), 1), (dict(activation=-1), 1),
+    (dict(weights=1), 1), (dict(weights=2), 1), (dict(weights=4), 1),
+    (dict(ptrs=[FAKE, None, FAKE]), 1), (dict(ptrs=[FAKE, FAKE + 8, FAKE]), 1),
+    (dict(ptrs=[FAKE] * 6), 1),                                      # scales with bf16 weights
+    (dict(weights=3, ptrs=[FAKE] * 5), 1), (dict(weights=3, ptrs=[FAKE] * 5 + [FAKE + 4]), 1),
+])
+def test_create_refuses(B, kw, want):
+    assert _create(B, **kw) == want
+
+
+def test_null_arguments(B):
+    lib = B.load_library()
+    assert lib.moe_ffn_create(None, None, None) == 1
+    n = ctypes.c_size_t()
+    assert lib.moe_ffn_workspace_size(None, 1, 0, ctypes.byref(n)) == 1
+    assert lib.moe_ffn_forward(None, FAKE, 8, 1, FAKE, None, FAKE, 1 << 20, None) == 1
+    assert lib.moe_ffn_backward(None, FAKE, 8, FAKE, 8, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == 1
+    assert lib.moe_ffn_last_launch_count(None) == -1
+    assert lib.moe_ffn_destroy(None) == 0
+
+
+def test_mxfp4_refusals(B):
+    lib = B.load_library()
+    n = ctypes.c_size_t()
+    for rows, cols, rc in ((4, 33, 1), (-1, 32, 1), (4, 0, 1), (1 << 30, 32, 2), (4, 1 << 30, 2)):
+        assert lib.moe_mxfp4_scales_size(rows, cols, ctypes.byref(n)) == rc
+    for rows, cols, want in ((1, 32, 512), (128, 128, 512), (129, 128, 1024), (128, 160, 1024), (300, 416, 3 * 4 * 512)):
+        assert lib.moe_mxfp4_scales_size(rows, cols, ctypes.byref(n)) == 0 and n.value == want
+    for fn in (lib.moe_mxfp4_quant, lib.moe_mxfp4_quant_f32):
+        assert fn(FAKE, 64, 4, 40, FAKE, FAKE, None) == 1       # n % 32
+        assert fn(FAKE, 32, 4, 64, FAKE, FAKE, None) == 1       # ldx < n
+        assert fn(FAKE, 66, 4, 64, FAKE, FAKE, None) == 1       # rows not 16-byte aligned
+        assert fn(FAKE + 2, 64, 4, 64, FAKE, FAKE, None) == 1
+        assert fn(FAKE, 64, 4, 64, FAKE, None, None) == 1
+        assert fn(FAKE, 64, 1 << 40, 64, FAKE, FAKE, None) == 2
+        assert fn(None, 64, 0, 64, None, None, None) == 0       # nothing to do
+    assert lib.moe_mxfp4_dequant(FAKE, FAKE, 4, 48, FAKE, None) == 1
+    assert lib.moe_mxfp4_dequant(FAKE, FAKE, 4, 64, None, None) == 1
+    assert lib.moe_mxfp4_dequant(None, None, 0, 64, None, None) == 0
+    assert lib.moe_mxfp4_gemm_workspace_size(4, 12, 64, ctypes.byref(n)) == 1
+    assert lib.moe_mxfp4_gemm_workspace_size(4, 16, 64, ctypes.byref(n)) == 0
+    need = n.value
+
+    def gemm(m=4, n=16, k=64, a=FAKE, ws=FAKE, size=need, out=FAKE):
+        return lib.moe_mxfp4_gemm(a, FAKE, m, FAKE, FAKE, n, k, out, ws, size, None)
+    assert gemm(n=12) == 1 and gemm(k=48) == 1 and gemm(m=-1) == 1 and gemm(m=0) == 0
+    assert gemm(ws=None) == 1 and gemm(ws=FAKE + 16) == 1 and gemm(size=128) == 3
+    assert gemm(a=None) == 1 and gemm(a=FAKE + 8) == 1 and gemm(out=None) == 1 and gemm(m=1 << 30) == 2
+
+
+def test_binding_refuses_host_tensors(B):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_quant(x)
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_dequant(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1, 1, 32, 4, 4, dtype=torch.uint8))
+    w = torch.zeros(64, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        B.GatedFfn(w, w, w)
+    with pytest.raises(ValueError):
+        B.GatedFfn(w, w, w, act="relu")
+
+
+@pytest.mark.parametrize("rows,n", [(1, 32), (128, 128), (130, 160), (300, 1056)])
+def test_packed_scale_order(B, rows, n):
+    s = torch.randint(0, 256, (rows, n // 32), dtype=torch.uint8)
+    p = B.mxfp4_pack_scales(s)
+    assert tuple(p.shape) == B.mxfp4_scales_shape(rows, n)
+    flat, nkt = p.reshape(-1), p.shape[1]
+    for r in range(0, rows, 7):
+        for b in range(n // 32):
+            at = (r // 128 * nkt + b // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + b % 4
+            assert flat[at] == s[r, b]
+    assert torch.equal(B.mxfp4_unpack_scales(p, rows, n), s)
+    pad = p.permute(0, 3, 2, 1, 4).reshape(-1, nkt * 4)[:, n // 32:]
+    assert not pad.any()
+
+
+def test_grid_is_its_own_rounding():
+    v = torch.tensor(P.GRID + tuple(-x for x in P.GRID) + (4.0,) * 16).reshape(1, 32)
+    assert torch.equal(P.mx_round(v), v.double())
+    # ties: 0.25 -> 0, 0.75 -> 1, 1.25 -> 1, 1.75 -> 2, 2.5 -> 2, 3.5 -> 4, 5 -> 4; above 6 -> 6
+    t = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.75] * 4).reshape(1, 32)
+    assert P.mx_round(t)[0, :8].tolist() == [0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, 6.0]
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_backward_formula_against_differences(kind):
+    """The formulas against central differences of the forward pass, in 64 bits."""
+    gen = torch.Generator().manual_seed(3)
+    x, w1, w3, w2, dout = (torch.randn(s, generator=gen, dtype=torch.float64)
+                           for s in ((5, 8), (16, 8), (16, 8), (8, 16), (5, 8)))
+    grads = P.backward(dout, x, w1, w3, w2, kind)
+    leaves = [x, w1, w3, w2]
+    for i, grad in enumerate(grads):
+        v = torch.randn(leaves[i].shape, generator=gen, dtype=torch.float64)
+        e = 1e-5
+        hi, lo = ([t + s * e * v if j == i else t for j, t in enumerate(leaves)] for s in (1, -1))
+        diff = ((P.forward(*hi, kind) - P.forward(*lo, kind)) * dout).sum() / (2 * e)
+        # a central difference is off by e^2 f''' / 6 and by rounding 1e-16 / e
+        assert abs(diff - (grad * v).sum()) <= 1e-7 * (1 + grad.abs().sum())
+    # and the bounds on slope and curvature that the tolerances use
+    g = torch.linspace(-12, 12, 200001, dtype=torch.float64)
+    _, s = P.act_slope(g, kind)
+    assert s.abs().max() < P.SLOPE and (s.diff() / g.diff()).abs().max() < P.CURVE

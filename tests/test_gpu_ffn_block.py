@@ -1,0 +1,360 @@
+"""The gated feed-forward block, its backward pass, and the MXFP4 operators on the GPU, against
+64-bit formulas with bounds derived from the roundings (tests/_ffn_plain.py)."""
+import pytest
+import torch
+
+import _ffn_plain as P
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_ffn_gemv_gb300 import binding
+    binding.load_library()
+    return binding
+
+
+def _n(seed, *shape, std=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _within(got, ref, bound):
+    got = got.double()
+    assert torch.isfinite(got).all()
+    over = (got - ref).abs() - bound
+    i = int(over.argmax())
+    assert over.max() <= 0, (f"off by {(got - ref).abs().flatten()[i]:.3e}, bound {bound.flatten()[i]:.3e} at {i} of "
+                             f"{tuple(got.shape)}: {got.flatten()[i]:.6e} for {ref.flatten()[i]:.6e}")
+
+
+def _weights(seed, H, I):
+    return _n(seed, I, H, std=H ** -0.5), _n(seed + 1, I, H, std=H ** -0.5), _n(seed + 2, H, I, std=I ** -0.5)
+
+
+def _quantised(B, w):
+    """Weights as MXFP4 pairs, and their values in 64 bits (read by the plain code)."""
+    pairs = [B.moe_mxfp4_quant(t) for t in w]
+    vals = [P.mx_values(P.mx_unpack(c), B.mxfp4_unpack_scales(s, c.shape[0], c.shape[1] * 2)) for c, s in pairs]
+    return pairs, vals
+
+
+# ---------------------------------------------------------------- MXFP4 quantisation
+
+def _check_quant(B, x):
+    rows, n = x.shape
+    codes, scales = B.moe_mxfp4_quant(x)
+    want_s = P.mx_scales(x)
+    want_c = P.mx_codes(x, want_s)
+    assert torch.equal(B.mxfp4_unpack_scales(scales, rows, n), want_s)
+    assert torch.equal(P.mx_unpack(codes), want_c)
+    pad = scales.permute(0, 3, 2, 1, 4).reshape(-1, scales.shape[1] * 4)[:rows, n // 32:]
+    assert not pad.any()
+    want = P.mx_values(want_c, want_s)
+    got = B.moe_mxfp4_dequant(codes, scales).double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))  # -0 equals 0 here
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,n", [(1, 32), (3, 96), (37, 4128), (129, 256), (1000, 544), (2, 7168)])
+def test_quant(B, rows, n, dtype):
+    x = _n(rows + n, rows, n, dtype=torch.float32)
+    x *= torch.exp2(torch.randint(-40, 40, (rows, 1), device="cuda").float())
+    _check_quant(B, x.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant_borders(B, dtype):
+    """Every rounding border and a step to either side, at small, middle and large scales; zeros,
+    subnormals, infinities, NaN; the type's largest and lowest values."""
+    mids = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.96875]
+    rows = []
+    for e in (-126, -60, -3, 0, 5, 100, 125):
+        b = torch.tensor(mids, dtype=torch.float64) * 2.0 ** e
+        b = b.to(dtype)
+        up = torch.nextafter(b, torch.full_like(b, float("inf")))
+        dn = torch.nextafter(b, torch.zeros_like(b))
+        rows.append(torch.cat([b, -up, dn, torch.tensor([4.0 * 2.0 ** e, 0.0], dtype=dtype)]))
+    z = torch.zeros(32, dtype=dtype)
+    lim = torch.finfo(dtype)
+    for v in (0.0, -0.0, lim.tiny, lim.tiny / 4, -lim.max, lim.max, float("inf"), float("-inf"), float("nan")):
+        r = z.clone()
+        r[5] = v
+        r[9] = 1.0 if v not in (0.0, lim.tiny, lim.tiny / 4) else 0.0
+        rows.append(r)
+    x = torch.stack(rows).cuda()
+    _check_quant(B, x)
+    _check_quant(B, torch.cat([x, x.flip(0), x], 1))  # such blocks beside ordinary ones
+
+
+def test_quant_strided_and_empty(B):
+    base = _n(1, 40, 320)
+    x = base[:, 64:160]  # rows 320 apart, 128-byte offset
+    c, s = B.moe_mxfp4_quant(x)
+    c2, s2 = B.moe_mxfp4_quant(x.contiguous())
+    assert torch.equal(c, c2) and torch.equal(B.mxfp4_unpack_scales(s, 40, 96), B.mxfp4_unpack_scales(s2, 40, 96))
+    c, s = B.moe_mxfp4_quant(base[:0])
+    assert c.shape == (0, 160) and B.moe_mxfp4_dequant(c, s).shape == (0, 320)
+    for bad in (base[:, 4:36], base.T, base[:, ::2], base.half()):
+        with pytest.raises(ValueError):
+            B.moe_mxfp4_quant(bad)
+    with pytest.raises(B.MoeError):
+        B.moe_mxfp4_quant(base[:, :40])
+
+
+# ---------------------------------------------------------------- MXFP4 product
+
+GEMM_SIZES = [(1, 8, 32), (1, 2048, 7168), (2, 136, 96), (5, 1000, 544), (16, 256, 256), (17, 128, 2080), (64, 520, 1024),
+              (100, 384, 4128), (128, 256, 512), (129, 264, 288), (256, 256, 256), (300, 1032, 1568), (1000, 776, 928)]
+
+
+@pytest.mark.parametrize("m,n,k", GEMM_SIZES)
+def test_mx_linear(B, m, n, k):
+    x = _n(m, m, k, dtype=torch.float32) * torch.exp2(torch.randint(-8, 8, (m, 1), device="cuda").float())
+    (w,), (wv,) = _quantised(B, [_n(n + k, n, k, std=k ** -0.5)])
+    xb = x.to(torch.bfloat16)
+    xv = P.mx_round(xb)
+    ref = xv @ wv.T
+    bound = P.HALF * ref.abs() + (1 + P.HALF) * k * P.F32 * (xv.abs() @ wv.abs().T)
+    _within(B.moe_mxfp4_linear(xb, *w), ref, bound)
+
+
+def test_mx_gemm_scales_by_position(B):
+    """Every block its own scale and every row its own sign pattern: a scale read for another row
+    or block shows at once."""
+    m, n, k = 200, 328, 640
+    g = torch.Generator(device="cuda").manual_seed(5)
+    def mat(rows):
+        codes = torch.randint(0, 16, (rows, k), generator=g, device="cuda").to(torch.uint8)
+        scales = torch.randint(117, 138, (rows, k // 32), generator=g, device="cuda").to(torch.uint8)
+        return codes, scales
+    (ac, as_), (bc, bs) = mat(m), mat(n)
+    got = B.moe_mxfp4_gemm(P.mx_pack(ac), B.mxfp4_pack_scales(as_), P.mx_pack(bc), B.mxfp4_pack_scales(bs))
+    a, b = P.mx_values(ac, as_), P.mx_values(bc, bs)
+    ref = a @ b.T
+    _within(got, ref, P.HALF * ref.abs() + (1 + P.HALF) * k * P.F32 * (a.abs() @ b.abs().T))
+
+
+def test_mx_gemm_nan_scale_stays_in_its_row(B):
+    x = _n(3, 40, 256)
+    x[7, 33] = float("inf")
+    x[21, 200] = float("nan")
+    (w,), (wv,) = _quantised(B, [_n(4, 64, 256)])
+    out = B.moe_mxfp4_linear(x, *w)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[[7, 21]] = True
+    assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
+
+
+# ---------------------------------------------------------------- the block
+
+FFN_SIZES = [(1, 2048, 768), (1, 8, 8), (3, 24, 40), (16, 256, 128), (17, 136, 264), (48, 1024, 512), (65, 520, 1032),
+             (128, 256, 256), (200, 512, 384), (333, 1032, 2056), (777, 1016, 680)]
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("m,H,I", FFN_SIZES)
+def test_forward(B, m, H, I, kind):
+    w = _weights(H + I, H, I)
+    x = _n(m, m, H)
+    blk = B.GatedFfn(*w, act=kind)
+    out = blk.forward(x)
+    _within(out, P.forward(x, *w, kind), P.forward_bound(x, *w, kind))
+    out2, saved = blk.forward(x, save=True)
+    assert torch.equal(out, out2)
+    for s, t in zip(saved, w[:2]):
+        ref = x.double() @ t.double().T
+        e = H * P.F32 * (x.double().abs() @ t.double().abs().T)
+        _within(s, ref, e + P.HALF * (ref.abs() + e))
+    assert blk.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("m,H,I", FFN_SIZES)
+def test_backward(B, m, H, I, kind):
+    w = _weights(H + I + 1, H, I)
+    x, dout = _n(m, m, H), _n(m + 1, m, H)
+    blk = B.GatedFfn(*w, act=kind)
+    _, saved = blk.forward(x, save=True)
+    got = blk.backward(dout, x, saved)
+    ref = P.backward(dout, x, *w, kind)
+    for g, r, b in zip(got, ref, P.backward_bounds(dout, x, *w, kind)):
+        _within(g, r, b)
+    assert blk.device_status() == 0
+    # only the gradients asked for
+    dx, *none = blk.backward(dout, x, saved, need_dw=False)
+    assert torch.equal(dx, got[0]) and none == [None] * 3
+    none, *dw = blk.backward(dout, x, saved, need_dx=False)
+    assert none is None and all(torch.equal(a, b) for a, b in zip(dw, got[1:]))
+
+
+def test_backward_against_differences(B):
+    """The kernels' gradients along a direction against central differences of the 64-bit forward
+    pass: off by no more than their bounds summed over the direction, and the difference's own error."""
+    m, H, I = 24, 64, 96
+    w = _weights(9, H, I)
+    x, dout = _n(1, m, H), _n(2, m, H)
+    blk = B.GatedFfn(*w, act="gelu")
+    _, saved = blk.forward(x, save=True)
+    got = blk.backward(dout, x, saved)
+    leaves = [t.double() for t in (x, *w)]
+    for i, (g, b) in enumerate(zip(got, P.backward_bounds(dout, x, *w, "gelu"))):
+        v = torch.randn(leaves[i].shape, device="cuda", dtype=torch.float64)
+        e = 1e-5
+        hi, lo = ([t + s * e * v if j == i else t for j, t in enumerate(leaves)] for s in (1, -1))
+        diff = ((P.forward(*hi, "gelu") - P.forward(*lo, "gelu")) * dout.double()).sum() / (2 * e)
+        assert abs(diff - (g.double() * v).sum()) <= (b * v.abs()).sum() + 1e-6 * (1 + g.double().abs().sum())
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("m,H,I", [(1, 7168, 2048), (1, 32, 32), (3, 96, 160), (16, 256, 128), (48, 1024, 512), (65, 544, 1056),
+                                   (128, 256, 256), (200, 512, 416), (333, 1056, 2080)])
+def test_mx_forward(B, m, H, I, kind):
+    pairs, vals = _quantised(B, _weights(H + I, H, I))
+    x = _n(m, m, H)
+    blk = B.GatedFfn(*pairs, act=kind)
+    ref, bound = P.mx_forward(x, *vals, kind)
+    _within(blk.forward(x), ref, bound)
+    assert blk.device_status() == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_forward_strided_rows_and_no_rows(B, mx):
+    H, I = 256, 160
+    w = _weights(5, H, I)
+    blk = B.GatedFfn(*(_quantised(B, w)[0] if mx else w))
+    base = _n(8, 70, 3 * H)
+    x = base[:, H:2 * H]
+    assert torch.equal(blk.forward(x), blk.forward(x.contiguous()))
+    assert blk.forward(x[:0]).shape == (0, H)
+    if not mx:
+        dbase = _n(9, 70, 2 * H)
+        dout = dbase[:, H:]
+        _, saved = blk.forward(x, save=True)
+        a, b = blk.backward(dout, x, saved), blk.backward(dout.contiguous(), x.contiguous(), saved)
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+        _, s0 = blk.forward(x[:0], save=True)
+        dx, *dw = blk.backward(dout[:0], x[:0], s0)
+        assert dx.shape == (0, H) and not any(t.any() for t in dw)
+
+
+def test_a_bad_row_spoils_no_other(B):
+    H, I = 264, 272
+    w = _weights(11, H, I)
+    blk = B.GatedFfn(*w)
+    x = _n(12, 300, H)
+    good = blk.forward(x)
+    x2 = x.clone()
+    x2[17, 3] = float("nan")
+    x2[290, 5] = float("inf")
+    out = blk.forward(x2)
+    bad = torch.zeros(300, dtype=torch.bool, device="cuda")
+    bad[[17, 290]] = True
+    assert torch.equal(out[~bad], good[~bad]) and torch.isnan(out[17]).all()
+
+
+def test_extreme_pre_activations(B):
+    """act and its slope where the exponential overflows and underflows: g of +-2^k up to 2^30."""
+    H = I = 8
+    eye = torch.eye(8, dtype=torch.bfloat16, device="cuda")
+    e = torch.tensor([-30, -3, 0, 2, 4, 6.5, 8, 30.0], device="cuda")
+    x = torch.cat([torch.exp2(e), -torch.exp2(e)]).reshape(-1, 1).expand(-1, 8).to(torch.bfloat16).contiguous()
+    dout = _n(3, 16, 8)
+    for kind in ("silu", "gelu"):
+        blk = B.GatedFfn(eye, eye, eye, act=kind)
+        out, saved = blk.forward(x, save=True)
+        w = (eye, eye, eye)
+        xs = x.double()
+        # h = act(g) g, rounded twice; below 2^-120 (exp(-t) past 2^126) the kernel may give 0
+        ref = P.forward(x, *w, kind)
+        assert torch.isfinite(out).all()
+        assert ((out.double() - ref).abs() <= 3 * P.HALF * ref.abs() + 1e-30).all()
+        got = blk.backward(dout, x, saved)
+        want = P.backward(dout, x, *w, kind)
+        assert all(torch.isfinite(t).all() for t in got)
+        a, s = P.act_slope(xs, kind)
+        # dx = dh (g s(g) + act(g)): each part rounded once, their sum once
+        part = (dout.double() * xs * s).abs() + (dout.double() * a).abs()
+        assert ((got[0].double() - want[0]).abs() <= 3 * P.HALF * part + 1e-30 + 2.0 ** -20 * (dout.double() * xs).abs()).all()
+
+
+def test_graph_capture_and_other_streams(B):
+    """Forward and backward captured in a graph, replayed on new inputs, and run on a side stream:
+    the same bits as eager calls."""
+    H, I, m = 512, 384, 150
+    w = _weights(21, H, I)
+    blk = B.GatedFfn(*w)
+    x, dout = _n(22, m, H), _n(23, m, H)
+    blk.forward(x, save=True)
+    blk.backward(dout, x, torch.zeros(2, m, I, dtype=torch.bfloat16, device="cuda"))  # the workspace exists
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, saved = blk.forward(x, save=True)
+        grads = blk.backward(dout, x, saved)
+    for seed in (31, 32):
+        x.copy_(_n(seed, m, H))
+        dout.copy_(_n(seed + 10, m, H))
+        g.replay()
+        torch.cuda.synchronize()
+        e_out, e_saved = blk.forward(x, save=True)
+        e_grads = blk.backward(dout, x, e_saved)
+        assert torch.equal(out, e_out) and all(torch.equal(a, b) for a, b in zip(grads, e_grads))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    s_out = blk.forward(x, stream=st)
+    st.synchronize()
+    assert torch.equal(s_out, e_out)
+
+
+def test_repeatable(B):
+    H, I, m = 1032, 776, 555
+    w = _weights(41, H, I)
+    blk = B.GatedFfn(*w)
+    x, dout = _n(42, m, H), _n(43, m, H)
+    out, saved = blk.forward(x, save=True)
+    first = (out, saved, *blk.backward(dout, x, saved))
+    for _ in range(3):
+        o, s = blk.forward(x, save=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, (o, s, *blk.backward(dout, x, s))))
+
+
+def test_refusals(B):
+    H, I = 64, 96
+    w1, w3, w2 = _weights(1, H, I)
+    blk = B.GatedFfn(w1, w3, w2)
+    x = _n(2, 10, H)
+    _, saved = blk.forward(x, save=True)
+    for bad in (x.float(), x[:, :56], x.T, x.cpu(), x[0], x[:, 1:].contiguous()):
+        with pytest.raises(ValueError):
+            blk.forward(bad)
+    with pytest.raises(ValueError):
+        blk.forward(x, out=torch.empty(9, H, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        blk.backward(x[:5], x, saved)
+    with pytest.raises(ValueError):
+        blk.backward(x, x, saved[:, :5])
+    with pytest.raises(ValueError):
+        B.GatedFfn(w1, w3, w2.T)
+    with pytest.raises(ValueError):
+        B.GatedFfn(w1, w2, w2)
+    pairs = _quantised(B, (w1, w3, w2))[0]
+    mx = B.GatedFfn(*pairs)
+    with pytest.raises(B.MoeError) as e:
+        mx.forward(x, save=True)
+    assert e.value.status == B.MOE_ERR_UNSUPPORTED
+    with pytest.raises(B.MoeError):
+        mx.backward(x, x, saved)
+    with pytest.raises(ValueError):
+        B.moe_mxfp4_gemm(*pairs[0], *pairs[2])
+    lib, p = B.load_library(), B._p
+    ws = blk.workspace(10, True, x.device)
+    out = torch.empty_like(x)
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), None, p(ws), 256, None) == B.MOE_ERR_WORKSPACE
+    assert lib.moe_ffn_forward(blk.handle, p(x), H - 8, 10, p(out), None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, -1, p(out), None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 1 << 30, p(out), None, p(ws), ws.numel(), None) == 2
+    assert lib.moe_ffn_backward(blk.handle, p(x), H, p(x), H, p(saved), 10, p(out), p(w1), None, None, p(ws),
+                                ws.numel(), None) == 1
