@@ -128,6 +128,54 @@ int forward_bf16(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx,
     return MOE_OK;
 }
 
+NarrowProduct narrow(int T, int R, int K, void* ws) {
+    NarrowProduct p{};
+    p.T = T;
+    p.R = R;
+    p.K = K;
+    p.hdr = at<WsHeader>(ws, 0);
+    p.wait_ns = kWaitNs;
+    return p;
+}
+
+// The block for few tokens: each kernel after the first streams its weights
+// while the one before drains.
+int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, void* saved,
+                   void* ws, cudaStream_t st) {
+    const int H = f->cfg.hidden, I = f->cfg.inter;
+    const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
+    NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
+    uint8_t *xq = at<uint8_t>(ws, lo.xq), *xs = at<uint8_t>(ws, lo.xs), *hq = at<uint8_t>(ws, lo.hq),
+            *hs = at<uint8_t>(ws, lo.hs);
+    void* h = at<void>(ws, lo.h);
+    const uint32_t nt = (uint32_t)narrow_tokens(m);
+    const bool ok = mx ? mx_code_map(&g.b, xq, m, H, nt) && mx_scale_map(&g.bs, xs, m, H) &&
+                             mx_code_map(&d.b, hq, m, I, nt) && mx_scale_map(&d.bs, hs, m, I)
+                       : ffn_map(&g.b, x, m, H, ldx, nt) && ffn_map(&d.b, h, m, I, I, nt);
+    if (!ok) return MOE_ERR_CUDA;
+    g.a[0] = f->k1;
+    g.a[1] = f->k3;
+    g.as[0] = f->s1;
+    g.as[1] = f->s3;
+    g.act = f->cfg.activation;
+    g.early = mx;  // behind the quantiser
+    g.out = static_cast<uint16_t*>(h);
+    g.g = static_cast<uint16_t*>(saved);
+    g.u = saved ? g.g + (size_t)m * I : nullptr;
+    g.codes = hq;
+    g.scales = hs;
+    g.nkt = ceil_div(I, 128);
+    d.a[0] = f->k2;
+    d.as[0] = f->s2;
+    d.early = 1;
+    d.out = static_cast<uint16_t*>(out);
+    if (mx && launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) != cudaSuccess) return MOE_ERR_CUDA;
+    if (launch_ffn_narrow(g, mx, true, st) != cudaSuccess || launch_ffn_narrow(d, mx, false, st) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    f->last_launches = mx ? 3 : 2;
+    return MOE_OK;
+}
+
 MxProduct mx_product(int M, int N, int K, void* ws) {
     MxProduct p{};
     p.M = M;
@@ -247,6 +295,7 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, voi
     if (mx && saved) return MOE_ERR_UNSUPPORTED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
+    if (m <= kNarrowTokens) return forward_narrow(f, lo, x, ldx, (int)m, out, saved, workspace, st);
     return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
               : forward_bf16(f, lo, x, ldx, (int)m, out, saved, workspace, st);
 }
@@ -359,12 +408,21 @@ int moe_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, c
     for (const void* p : {(const void*)a_codes, (const void*)a_scales, (const void*)b_codes, (const void*)b_scales,
                           (const void*)out})
         if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (m <= kNarrowTokens) {
+        NarrowProduct q = narrow((int)m, (int)n, (int)k, workspace);
+        if (!mx_code_map(&q.a[0], b_codes, n, k, 128) || !mx_scale_map(&q.as[0], b_scales, n, k) ||
+            !mx_code_map(&q.b, a_codes, m, k, (uint32_t)narrow_tokens((int)m)) || !mx_scale_map(&q.bs, a_scales, m, k))
+            return MOE_ERR_CUDA;
+        q.out = static_cast<uint16_t*>(out);
+        return launch_ffn_narrow(q, true, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     MxProduct g = mx_product((int)m, (int)n, (int)k, workspace);
     if (!mx_code_map(&g.a, a_codes, m, k, 128) || !mx_scale_map(&g.as, a_scales, m, k) ||
         !mx_code_map(&g.b[0], b_codes, n, k, 128) || !mx_scale_map(&g.bs[0], b_scales, n, k))
         return MOE_ERR_CUDA;
     g.out = static_cast<uint16_t*>(out);
-    return launch_mx_product(g, false, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_mx_product(g, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

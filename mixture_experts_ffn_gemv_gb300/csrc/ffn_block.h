@@ -67,6 +67,27 @@ bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, u
 bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k);
 cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st);
 
+// One product for few tokens, out[T, R] = tokens W^T, weights as the MMA's M
+// operand (gate/up: W1 and W3).
+struct NarrowProduct {
+    CUtensorMap a[2], as[2];  // weights (128-row boxes) and, MXFP4, their scales
+    CUtensorMap b, bs;        // tokens (narrow_tokens(T)-row boxes) and their scales
+    int T, R, K;
+    int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
+    int act;
+    uint16_t* out;            // bf16 [T, R]; gate/up of a bf16 block: h
+    uint16_t *g, *u;          // gate/up: saved pre-activations, or null
+    uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
+    int nkt;                  // ... scale tiles per row of it
+    WsHeader* hdr;
+    uint64_t wait_ns;
+    // set by launch_ffn_narrow
+    int nt, kstages, slices, stages, ring_bytes, tmem_cols;
+};
+constexpr int kNarrowTokens = 128;  // up to here
+int narrow_tokens(int m);           // rows of a token tile
+cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream_t st);
+
 cudaError_t launch_mx_quant(const void* x, bool f32, size_t ldx, int rows, int n, uint8_t* codes, uint8_t* scales,
                             cudaStream_t st);
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int n, uint16_t* out,

@@ -34,6 +34,17 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* v, float r) {
     return w;
 }
 
+// The e2m1 code of one value, rounded as above.
+__device__ __forceinline__ uint32_t mx_code(float v) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %1, %1;\n\t"
+        "mov.b32 %0, {b0, b0, b0, b0};\n\t}"
+        : "=r"(w)
+        : "f"(v));
+    return w & 15u;
+}
+
 // Byte of the scale of row r, block b; nkt = ceil(blocks / 4) tiles per row.
 __host__ __device__ __forceinline__ size_t mx_scale_at(size_t r, size_t b, size_t nkt) {
     return ((r >> 7) * nkt + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
