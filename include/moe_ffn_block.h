@@ -75,8 +75,9 @@ MOE_API int moe_ffn_workspace_size(const moe_ffn* ffn, int64_t m, int backward, 
 
 /* out[t, :] = the block applied to x[t, :].
  *   x bf16 [m, H] with row stride ldx >= H (a multiple of 8); out bf16 [m, H].
- *   saved (bf16 weights only, else NULL): NULL, or bf16 [2, m, I] that receives
- *   g = x W1^T and u = x W3^T for moe_ffn_backward.
+ *   saved (bf16 weights only, else NULL): NULL, or fp32 [2, m, I], 32-byte aligned, that receives
+ *   g = x W1^T and u = x W3^T for moe_ffn_backward (fp32: rounded to bf16 they
+ *   would be the largest error of the gradients).
  * The intermediate h is rounded to bf16 (MXFP4: to MXFP4, straight from the
  * fp32 products), x to MXFP4 for MXFP4 weights; sums are fp32. */
 MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, void* saved,
@@ -120,6 +121,16 @@ MOE_API int moe_mxfp4_gemm_workspace_size(int64_t m, int64_t n, int64_t k, size_
 MOE_API int moe_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, const uint8_t* b_codes,
                            const uint8_t* b_scales, int64_t n, int64_t k, void* out, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/* moe_mxfp4_quant of x [m, k] (bf16, or fp32 for _f32; row stride ldx), kept in
+ * the workspace, then moe_mxfp4_gemm of it with W [n, k]: out bf16 [m, n].
+ * Workspace as for moe_mxfp4_gemm, moe_mxfp4_linear_workspace_size bytes. */
+MOE_API int moe_mxfp4_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+MOE_API int moe_mxfp4_linear(const void* x, int64_t ldx, int64_t m, const uint8_t* w_codes, const uint8_t* w_scales,
+                             int64_t n, int64_t k, void* out, void* workspace, size_t workspace_bytes, void* stream);
+MOE_API int moe_mxfp4_linear_f32(const float* x, int64_t ldx, int64_t m, const uint8_t* w_codes,
+                                 const uint8_t* w_scales, int64_t n, int64_t k, void* out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

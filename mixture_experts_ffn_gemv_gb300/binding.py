@@ -35,6 +35,7 @@ EXPORTED = (
     "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
     "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
     "moe_mxfp4_dequant", "moe_mxfp4_gemm_workspace_size", "moe_mxfp4_gemm",
+    "moe_mxfp4_linear_workspace_size", "moe_mxfp4_linear", "moe_mxfp4_linear_f32",
 )
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -125,6 +126,9 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_mxfp4_dequant.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp]
         lib.moe_mxfp4_gemm_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
         lib.moe_mxfp4_gemm.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, sz, _vp]
+        lib.moe_mxfp4_linear_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
+        for fn in (lib.moe_mxfp4_linear, lib.moe_mxfp4_linear_f32):
+            fn.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, sz, _vp]
         _lib = lib
         return lib
 
@@ -371,31 +375,45 @@ class MoeLayer:
 
 
 # ---------------------------------------------------------------- the gated feed-forward block and MXFP4
-# (include/moe_ffn_block.h)
+# (include/moe_ffn_block.h).  A decode step calls these once per layer, so the
+# checks test the common case (dense rows) first and word the refusal after.
+
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+
 
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _rows(t, dtypes, n: int | None, what: str):
-    """A [rows, n] device matrix whose rows are dense and 16-byte aligned; returns its row stride."""
-    _need(t.dim() == 2 and t.dtype in dtypes and t.is_cuda, f"{what}: a 2-d device tensor of {dtypes}")
-    _need(n is None or t.shape[1] == n, f"{what}: [rows, {n}], got {tuple(t.shape)}")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    _need(t.numel() == 0 or (t.stride(1) == 1 and ld >= t.shape[1] and ld * t.element_size() % 16 == 0
+def _rows(t, n: int, what: str, f32: bool = False) -> int:
+    """Checks a [rows, n] device matrix of bf16 (or fp32 where f32) whose rows are dense and
+    16-byte aligned; returns its row stride."""
+    if t.dtype is _BF16 and t.is_cuda and t.is_contiguous() and t.dim() == 2 and t.shape[1] == n \
+            and t.data_ptr() % 16 == 0:
+        return n
+    _need(t.is_cuda and t.dim() == 2 and (t.dtype is _BF16 or (f32 and t.dtype is _F32)),
+          f"{what}: a 2-d device tensor of bfloat16{' or float32' if f32 else ''}")
+    _need(t.shape[1] == n, f"{what}: [rows, {n}], got {tuple(t.shape)}")
+    ld = t.stride(0) if t.shape[0] > 1 else n
+    _need(t.numel() == 0 or (t.stride(1) == 1 and ld >= n and ld * t.element_size() % 16 == 0
                              and t.data_ptr() % 16 == 0), f"{what}: rows must be dense and 16-byte aligned")
     return ld
 
 
 def _dense(t, dtype, shape, what: str):
-    _need(t.is_cuda and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
+    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.shape == shape):
+        raise ValueError(f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
+
+
+def _on(t, stream) -> int:
+    """The CUDA stream to launch on: `stream`, or the current one of t's device."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def mxfp4_scales_shape(rows: int, n: int):
     """Shape of the packed scales of a [rows, n] matrix: [row tile, K tile, row % 32, row / 32, block]."""
-    return (-(-rows // 128), -(-n // 128), 32, 4, 4)
+    return (rows + 127) // 128, (n + 127) // 128, 32, 4, 4
 
 
 def mxfp4_pack_scales(scales):
@@ -413,65 +431,111 @@ def mxfp4_unpack_scales(scales, rows: int, n: int):
     return scales.permute(0, 3, 2, 1, 4).reshape(rt * 128, kt * 4)[:rows, : n // 32].contiguous()
 
 
-def moe_mxfp4_quant(x, stream=None):
-    """x bf16 or fp32 [rows, n] (device; n a multiple of 32) -> (codes uint8 [rows, n/2], packed scales uint8)."""
-    lib = load_library()
-    ld = _rows(x, (torch.bfloat16, torch.float32), None, "x")
-    rows, n = x.shape
-    codes = torch.empty(rows, n // 2, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(mxfp4_scales_shape(rows, n), dtype=torch.uint8, device=x.device)
-    f32 = x.dtype == torch.float32
-    _check((lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
-        _p(x), ld, rows, n, _p(codes), _p(scales), _stream(stream)),
-        "moe_mxfp4_quant_f32" if f32 else "moe_mxfp4_quant")
-    return codes, scales
-
-
 def _mx_matrix(codes, scales, what: str):
     """(rows, n) of a matrix held as codes and packed scales."""
     _need(codes.dim() == 2, f"{what}: codes are [rows, n/2]")
-    rows, n = codes.shape[0], codes.shape[1] * 2
-    _dense(codes, torch.uint8, (rows, n // 2), f"{what} codes")
-    _dense(scales, torch.uint8, mxfp4_scales_shape(rows, n), f"{what} scales")
-    return rows, n
+    rows, half = codes.shape
+    if not (codes.dtype is _U8 and codes.is_cuda and codes.is_contiguous()):
+        raise ValueError(f"{what} codes: a contiguous device tensor of uint8")
+    _dense(scales, _U8, mxfp4_scales_shape(rows, 2 * half), f"{what} scales")
+    return rows, 2 * half
+
+
+def moe_mxfp4_quant(x, stream=None):
+    """x bf16 or fp32 [rows, n] (device; n a multiple of 32) -> (codes uint8 [rows, n/2], packed scales uint8)."""
+    lib = _lib or load_library()
+    _need(x.dim() == 2, "x: [rows, n]")
+    rows, n = x.shape
+    ld = _rows(x, n, "x", f32=True)
+    codes = x.new_empty((rows, n // 2), dtype=_U8)
+    scales = x.new_empty(mxfp4_scales_shape(rows, n), dtype=_U8)
+    f32 = x.dtype is _F32
+    rc = (lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
+        x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), _on(x, stream))
+    if rc:
+        raise MoeError(rc, "moe_mxfp4_quant_f32" if f32 else "moe_mxfp4_quant")
+    return codes, scales
 
 
 def moe_mxfp4_dequant(codes, scales, stream=None):
     """The values (bf16 [rows, n]) that codes and packed scales stand for."""
-    lib = load_library()
+    lib = _lib or load_library()
     rows, n = _mx_matrix(codes, scales, "x")
-    out = torch.empty(rows, n, dtype=torch.bfloat16, device=codes.device)
-    _check(lib.moe_mxfp4_dequant(_p(codes), _p(scales), rows, n, _p(out), _stream(stream)), "moe_mxfp4_dequant")
+    out = codes.new_empty((rows, n), dtype=_BF16)
+    rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), _on(codes, stream))
+    if rc:
+        raise MoeError(rc, "moe_mxfp4_dequant")
     return out
 
 
-_headers = {}  # device -> the zeroed workspace of moe_mxfp4_gemm calls
+_spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on that stream
+
+
+def _space(like, stream: int, need: int) -> torch.Tensor:
+    """A workspace of at least `need` bytes for calls on `stream`, its header zeroed before first use."""
+    key = (like.get_device(), stream)
+    ws = _spaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = like.new_empty((max(need, 1 << 16),), dtype=_U8)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if stream else
+                               torch.cuda.default_stream(like.device)):
+            ws[:256].zero_()
+        _spaces[key] = ws
+    return ws
+
+
+def mxfp4_device_status(stream=None) -> int:
+    """The first device error (0: none) of the MXFP4 products on `stream` since it was last read."""
+    s = stream if stream is not None else torch.cuda.current_stream()
+    ws = _spaces.get((s.device.index, s.cuda_stream))
+    if ws is None:
+        return 0
+    code = _i32()
+    rc = load_library().moe_device_status(_p(ws), ctypes.c_void_p(s.cuda_stream), ctypes.byref(code))
+    if rc not in (MOE_OK, MOE_ERR_DEVICE):
+        raise MoeError(rc, "moe_device_status")
+    return code.value
 
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     """A [m, k] times B [n, k] transposed, both MXFP4 (codes, packed scales) -> bf16 [m, n]."""
-    lib = load_library()
+    lib = _lib or load_library()
     m, k = _mx_matrix(a_codes, a_scales, "a")
     n, kb = _mx_matrix(b_codes, b_scales, "b")
     _need(k == kb, f"k differs: {k} and {kb}")
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=a_codes.device)
+        out = a_codes.new_empty((m, n), dtype=_BF16)
     else:
-        _dense(out, torch.bfloat16, (m, n), "out")
-    ws = _headers.get(a_codes.device)
-    if ws is None:
-        # ready before any later call on any stream uses it
-        ws = torch.zeros(256, dtype=torch.uint8, device=a_codes.device)
-        torch.cuda.synchronize(a_codes.device)
-        _headers[a_codes.device] = ws
-    _check(lib.moe_mxfp4_gemm(_p(a_codes), _p(a_scales), m, _p(b_codes), _p(b_scales), n, k, _p(out), _p(ws),
-                              ws.numel(), _stream(stream)), "moe_mxfp4_gemm")
+        _dense(out, _BF16, (m, n), "out")
+    st = _on(a_codes, stream)
+    ws = _space(a_codes, st, 256)
+    rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n, k,
+                            out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if rc:
+        raise MoeError(rc, "moe_mxfp4_gemm")
     return out
 
 
 def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
-    """x (bf16 or fp32 [m, k]) quantised per call, times a weight matrix [n, k] held in MXFP4 -> bf16 [m, n]."""
-    return moe_mxfp4_gemm(*moe_mxfp4_quant(x, stream), codes, scales, out=out, stream=stream)
+    """x (bf16 or fp32 [m, k]) quantised to MXFP4 per call, times a weight matrix [n, k] held in
+    MXFP4 -> bf16 [m, n]."""
+    lib = _lib or load_library()
+    n, k = _mx_matrix(codes, scales, "w")
+    ld = _rows(x, k, "x", f32=True)
+    m = x.shape[0]
+    if out is None:
+        out = x.new_empty((m, n), dtype=_BF16)
+    else:
+        _dense(out, _BF16, (m, n), "out")
+    st = _on(x, stream)
+    # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
+    ws = _space(x, st, 1024 + m * k // 2 + (m + 127) // 128 * ((k + 127) // 128) * 512)
+    f32 = x.dtype is _F32
+    rc = (lib.moe_mxfp4_linear_f32 if f32 else lib.moe_mxfp4_linear)(
+        x.data_ptr(), ld, m, codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if rc:
+        raise MoeError(rc, "moe_mxfp4_linear_f32" if f32 else "moe_mxfp4_linear")
+    return out
 
 
 class GatedFfn:
@@ -479,7 +543,8 @@ class GatedFfn:
     out = (act(x w1^T) * (x w3^T)) w2^T, w1, w3 [I, H], w2 [H, I].
 
     Weights are bf16 tensors, or (codes, packed scales) pairs as
-    moe_mxfp4_quant returns them; act is "silu" or "gelu" (tanh form)."""
+    moe_mxfp4_quant returns them; act is "silu" or "gelu" (tanh form).
+    A handle keeps one workspace: order its calls on one stream."""
 
     def __init__(self, w1, w3, w2, act="silu"):
         self.lib = load_library()
@@ -493,7 +558,7 @@ class GatedFfn:
             _need(w1.dim() == 2, "w1: [I, H]")
             I, H = w1.shape
             for w, shape, name in ((w1, (I, H), "w1"), (w3, (I, H), "w3"), (w2, (H, I), "w2")):
-                _dense(w, torch.bfloat16, shape, name)
+                _dense(w, _BF16, shape, name)
             ptrs = [_p(w) for w in (w1, w3, w2)] + [None] * 3
         self._keep = (w1, w3, w2)
         self.hidden, self.inter, self.act = H, I, act
@@ -503,6 +568,8 @@ class GatedFfn:
         _check(self.lib.moe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(handle)), "moe_ffn_create")
         self.handle = handle
         self._ws = None
+        self._ws_at = (None, 0)
+        self._fits = [-1, -1]  # tokens the workspace holds: forward, backward
 
     def close(self):
         if getattr(self, "handle", None):
@@ -522,10 +589,13 @@ class GatedFfn:
         return n.value
 
     def workspace(self, m: int, backward: bool, device) -> torch.Tensor:
-        """The handle's own workspace; calls on one handle are ordered on one stream."""
-        need = self.workspace_size(m, backward)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        """The handle's own workspace, grown to what a call on m tokens needs."""
+        if m > self._fits[backward]:
+            need = self.workspace_size(m, backward)
+            if self._ws is None or self._ws.numel() < need:
+                self._ws = torch.empty(max(need, 256), dtype=_U8, device=device)
+                self._ws_at = (self._ws.data_ptr(), self._ws.numel())
+            self._fits[backward] = m
         return self._ws
 
     def last_launch_count(self) -> int:
@@ -542,33 +612,38 @@ class GatedFfn:
 
     def forward(self, x, save=False, out=None, stream=None):
         """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
-        (out, saved) for backward: saved bf16 [2, m, I] holds x w1^T and x w3^T."""
-        ld = _rows(x, (torch.bfloat16,), self.hidden, "x")
+        (out, saved) for backward: saved fp32 [2, m, I] holds x w1^T and x w3^T."""
+        ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
         if out is None:
-            out = torch.empty(m, self.hidden, dtype=torch.bfloat16, device=x.device)
+            out = x.new_empty((m, self.hidden))
         else:
-            _dense(out, torch.bfloat16, (m, self.hidden), "out")
-        saved = torch.empty(2, m, self.inter, dtype=torch.bfloat16, device=x.device) if save else None
-        ws = self.workspace(m, False, x.device)
-        _check(self.lib.moe_ffn_forward(self.handle, _p(x), ld, m, _p(out), _p(saved), _p(ws), ws.numel(),
-                                        _stream(stream)), "moe_ffn_forward")
+            _dense(out, _BF16, (m, self.hidden), "out")
+        if m > self._fits[0]:
+            self.workspace(m, False, x.device)
+        saved = x.new_empty((2, m, self.inter), dtype=_F32) if save else None
+        rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
+                                      saved.data_ptr() if save else None, *self._ws_at, _on(x, stream))
+        if rc:
+            raise MoeError(rc, "moe_ffn_forward")
         return (out, saved) if save else out
 
     def backward(self, dout, x, saved, need_dx=True, need_dw=True, stream=None):
         """Gradients (dx, dw1, dw3, dw2), bf16, of the forward pass that saved `saved`; None
         for those not needed.  No tokens: the weight gradients are zero."""
-        ldd = _rows(dout, (torch.bfloat16,), self.hidden, "dout")
-        ldx = _rows(x, (torch.bfloat16,), self.hidden, "x")
+        H, I = self.hidden, self.inter
+        ldd, ldx = _rows(dout, H, "dout"), _rows(x, H, "x")
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
-        _dense(saved, torch.bfloat16, (2, m, self.inter), "saved")
-        new = (lambda *s: torch.empty(s, dtype=torch.bfloat16, device=x.device)) if m else \
-              (lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=x.device))
-        dx = new(m, self.hidden) if need_dx else None
-        dw1, dw3, dw2 = (new(self.inter, self.hidden), new(self.inter, self.hidden),
-                         new(self.hidden, self.inter)) if need_dw else (None,) * 3
-        ws = self.workspace(m, True, x.device)
-        _check(self.lib.moe_ffn_backward(self.handle, _p(dout), ldd, _p(x), ldx, _p(saved), m, _p(dx), _p(dw1),
-                                         _p(dw3), _p(dw2), _p(ws), ws.numel(), _stream(stream)), "moe_ffn_backward")
+        _dense(saved, _F32, (2, m, I), "saved")
+        new = x.new_empty if m else x.new_zeros
+        dx = new((m, H)) if need_dx else None
+        dw1, dw3, dw2 = (new((I, H)), new((I, H)), new((H, I))) if need_dw else (None,) * 3
+        if m > self._fits[1]:
+            self.workspace(m, True, x.device)
+        at = [None if t is None else t.data_ptr() for t in (dx, dw1, dw3, dw2)]
+        rc = self.lib.moe_ffn_backward(self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m, *at,
+                                       *self._ws_at, _on(x, stream))
+        if rc:
+            raise MoeError(rc, "moe_ffn_backward")
         return dx, dw1, dw3, dw2

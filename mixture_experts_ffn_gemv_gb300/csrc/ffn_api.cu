@@ -116,8 +116,8 @@ int forward_bf16(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx,
     if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
     gu.b[0] = f->k1;
     gu.b[1] = f->k3;
-    p.o1 = static_cast<uint16_t*>(saved);
-    p.o2 = saved ? p.o1 + (size_t)m * I : nullptr;
+    p.sg = static_cast<float*>(saved);
+    p.su = saved ? p.sg + (size_t)m * I : nullptr;
     if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
     FfnProducts d = products(f, ws);
     FfnProduct& y = add(d, m, H, I, out);
@@ -160,7 +160,7 @@ int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ld
     g.act = f->cfg.activation;
     g.early = mx;  // behind the quantiser
     g.out = static_cast<uint16_t*>(h);
-    g.g = static_cast<uint16_t*>(saved);
+    g.g = static_cast<float*>(saved);
     g.u = saved ? g.g + (size_t)m * I : nullptr;
     g.codes = hq;
     g.scales = hs;
@@ -227,6 +227,61 @@ int quant(const void* x, bool f32, int64_t ldx, int64_t rows, int64_t n, uint8_t
                : MOE_ERR_CUDA;
 }
 
+// What moe_mxfp4_gemm and moe_mxfp4_linear check alike.
+int check_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* w, const uint8_t* ws, const void* out,
+               const void* workspace, size_t bytes, size_t need) {
+    if (m > INT32_MAX / 64 || n > kMaxDim || k > kMaxDim) return MOE_ERR_UNSUPPORTED;
+    if (m == 0) return MOE_OK;
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    if (bytes < need) return MOE_ERR_WORKSPACE;
+    for (const void* p : {(const void*)w, (const void*)ws, out})
+        if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// early: the preceding kernel on the stream is the quantiser of A.
+int gemm(const uint8_t* a, const uint8_t* as, int m, const uint8_t* b, const uint8_t* bs, int n, int k, void* out,
+         void* ws, bool early, cudaStream_t st) {
+    if (m <= kNarrowTokens) {
+        NarrowProduct q = narrow(m, n, k, ws);
+        if (!mx_code_map(&q.a[0], b, n, k, 128) || !mx_scale_map(&q.as[0], bs, n, k) ||
+            !mx_code_map(&q.b, a, m, k, (uint32_t)narrow_tokens(m)) || !mx_scale_map(&q.bs, as, m, k))
+            return MOE_ERR_CUDA;
+        q.early = early;
+        q.out = static_cast<uint16_t*>(out);
+        return launch_ffn_narrow(q, true, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    MxProduct g = mx_product(m, n, k, ws);
+    if (!mx_code_map(&g.a, a, m, k, 128) || !mx_scale_map(&g.as, as, m, k) || !mx_code_map(&g.b[0], b, n, k, 128) ||
+        !mx_scale_map(&g.bs[0], bs, n, k))
+        return MOE_ERR_CUDA;
+    g.out = static_cast<uint16_t*>(out);
+    return launch_mx_product(g, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+struct LinearLayout {
+    size_t codes, scales, total;
+};
+LinearLayout linear_layout(int64_t m, int64_t k) {
+    LinearLayout o;
+    o.codes = align_up(sizeof(WsHeader));
+    o.scales = align_up(o.codes + (size_t)m * k / 2);
+    o.total = align_up(o.scales + scale_bytes(m, k));
+    return o;
+}
+
+int linear(const void* x, bool f32, int64_t ldx, int64_t m, const uint8_t* w, const uint8_t* ws, int64_t n, int64_t k,
+           void* out, void* workspace, size_t bytes, void* stream) {
+    if (m < 0 || n <= 0 || n % 8 || k <= 0 || k % 32) return MOE_ERR_INVALID_ARG;
+    const LinearLayout lo = linear_layout(m, k);
+    const int rc = check_gemm(m, n, k, w, ws, out, workspace, bytes, lo.total);
+    if (rc != MOE_OK || m == 0) return rc;
+    uint8_t *codes = at<uint8_t>(workspace, lo.codes), *scales = at<uint8_t>(workspace, lo.scales);
+    const int qc = quant(x, f32, ldx, m, k, codes, scales, stream);
+    if (qc != MOE_OK) return qc;
+    return gemm(codes, scales, (int)m, w, ws, (int)n, (int)k, out, workspace, true, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -289,7 +344,7 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, voi
     Layout lo;
     const int rc = check_call(f, m, false, workspace, workspace_bytes, &lo);
     if (rc != MOE_OK || m == 0) return rc;
-    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 16)))
+    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 32)))
         return MOE_ERR_INVALID_ARG;
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
     if (mx && saved) return MOE_ERR_UNSUPPORTED;
@@ -309,7 +364,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     if (rc != MOE_OK || m == 0) return rc;
     const int H = f->cfg.hidden, I = f->cfg.inter, n = (int)m;
     const bool dw = dw1 || dw3 || dw2;
-    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !aligned(saved, 16) || (dx && !aligned(dx, 16)) ||
+    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !aligned(saved, 32) || (dx && !aligned(dx, 16)) ||
         (dw && (!dw1 || !dw3 || !dw2 || !aligned(dw1, 16) || !aligned(dw3, 16) || !aligned(dw2, 16))))
         return MOE_ERR_INVALID_ARG;
     if (!dx && !dw) return MOE_OK;
@@ -322,7 +377,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
     q.b[0] = f->mn2;
     q.b_mn = 1;
-    p.g = static_cast<const uint16_t*>(saved);
+    p.g = static_cast<const float*>(saved);
     p.u = p.g + (size_t)m * I;
     p.o1 = static_cast<uint16_t*>(du);
     p.o2 = static_cast<uint16_t*>(h);
@@ -399,30 +454,29 @@ int moe_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int64_t m, c
                    const uint8_t* b_scales, int64_t n, int64_t k, void* out, void* workspace, size_t workspace_bytes,
                    void* stream) {
     size_t need = 0;
-    const int rc = moe_mxfp4_gemm_workspace_size(m, n, k, &need);
-    if (rc != MOE_OK) return rc;
+    int rc = moe_mxfp4_gemm_workspace_size(m, n, k, &need);
+    if (rc == MOE_OK) rc = check_gemm(m, n, k, b_codes, b_scales, out, workspace, workspace_bytes, need);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (!a_codes || !a_scales || !aligned(a_codes, 16) || !aligned(a_scales, 16)) return MOE_ERR_INVALID_ARG;
+    return gemm(a_codes, a_scales, (int)m, b_codes, b_scales, (int)n, (int)k, out, workspace, false,
+                static_cast<cudaStream_t>(stream));
+}
+
+int moe_mxfp4_linear_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+    if (m < 0 || n <= 0 || n % 8 || k <= 0 || k % 32 || !bytes) return MOE_ERR_INVALID_ARG;
     if (m > INT32_MAX / 64 || n > kMaxDim || k > kMaxDim) return MOE_ERR_UNSUPPORTED;
-    if (m == 0) return MOE_OK;
-    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-    for (const void* p : {(const void*)a_codes, (const void*)a_scales, (const void*)b_codes, (const void*)b_scales,
-                          (const void*)out})
-        if (!p || !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (m <= kNarrowTokens) {
-        NarrowProduct q = narrow((int)m, (int)n, (int)k, workspace);
-        if (!mx_code_map(&q.a[0], b_codes, n, k, 128) || !mx_scale_map(&q.as[0], b_scales, n, k) ||
-            !mx_code_map(&q.b, a_codes, m, k, (uint32_t)narrow_tokens((int)m)) || !mx_scale_map(&q.bs, a_scales, m, k))
-            return MOE_ERR_CUDA;
-        q.out = static_cast<uint16_t*>(out);
-        return launch_ffn_narrow(q, true, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-    }
-    MxProduct g = mx_product((int)m, (int)n, (int)k, workspace);
-    if (!mx_code_map(&g.a, a_codes, m, k, 128) || !mx_scale_map(&g.as, a_scales, m, k) ||
-        !mx_code_map(&g.b[0], b_codes, n, k, 128) || !mx_scale_map(&g.bs[0], b_scales, n, k))
-        return MOE_ERR_CUDA;
-    g.out = static_cast<uint16_t*>(out);
-    return launch_mx_product(g, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    *bytes = linear_layout(m, k).total;
+    return MOE_OK;
+}
+
+int moe_mxfp4_linear(const void* x, int64_t ldx, int64_t m, const uint8_t* w_codes, const uint8_t* w_scales, int64_t n,
+                     int64_t k, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    return linear(x, false, ldx, m, w_codes, w_scales, n, k, out, workspace, workspace_bytes, stream);
+}
+
+int moe_mxfp4_linear_f32(const float* x, int64_t ldx, int64_t m, const uint8_t* w_codes, const uint8_t* w_scales,
+                         int64_t n, int64_t k, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    return linear(x, true, ldx, m, w_codes, w_scales, n, k, out, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

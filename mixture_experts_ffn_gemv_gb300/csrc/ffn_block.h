@@ -37,8 +37,9 @@ struct FfnProducts {
     int count;
     int first[kMaxProducts + 1];  // first work item of each product
     int act;
-    const uint16_t *g, *u;  // EPI_DACT: saved pre-activations
-    uint16_t *o1, *o2;      // EPI_GATEUP_SAVE: g, u; EPI_DACT: du, h (out: dg)
+    float *sg, *su;         // EPI_GATEUP_SAVE: pre-activations g, u
+    const float *g, *u;     // EPI_DACT: the same
+    uint16_t *o1, *o2;      // EPI_DACT: du, h (out: dg)
     WsHeader* hdr;
     uint64_t wait_ns;
 };
@@ -76,7 +77,7 @@ struct NarrowProduct {
     int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
     int act;
     uint16_t* out;            // bf16 [T, R]; gate/up of a bf16 block: h
-    uint16_t *g, *u;          // gate/up: saved pre-activations, or null
+    float *g, *u;             // gate/up: saved pre-activations, or null
     uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;

@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
             if (GATEUP) {
                 p.out[at] = f32_to_bf16(glu(v0, v1, p.act));
                 if (p.g) {
-                    p.g[at] = f32_to_bf16(v0);
-                    p.u[at] = f32_to_bf16(v1);
+                    p.g[at] = v0;
+                    p.u[at] = v1;
                 }
             } else {
                 p.out[at] = f32_to_bf16(v0);

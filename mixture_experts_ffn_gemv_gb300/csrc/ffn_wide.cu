@@ -45,14 +45,10 @@ constexpr uint64_t DRAIN_NS = 2000000000ull;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 
-__device__ __forceinline__ void load8bf(const uint16_t* p, float* v) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(w[i]);
-        v[2 * i + 1] = bf16hi(w[i]);
-    }
+__device__ __forceinline__ void load8(const float* p, float* v) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 struct Item {
@@ -245,19 +241,28 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
                     if (ok) {
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
-                            uint32_t o[8], og[8], ou[8];
+                            uint32_t o[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const float g0 = __uint_as_float(gv[16 * v + 2 * i]), g1 = __uint_as_float(gv[16 * v + 2 * i + 1]);
                                 const float u0 = __uint_as_float(uv[16 * v + 2 * i]), u1 = __uint_as_float(uv[16 * v + 2 * i + 1]);
                                 o[i] = pack_bf16x2(glu(g0, u0, p.act), glu(g1, u1, p.act));
-                                og[i] = pack_bf16x2(g0, g1);
-                                ou[i] = pack_bf16x2(u0, u1);
                             }
                             store_row16(q.out + at, col + 16 * v, N, wide, o);
                             if (EPI == EPI_GATEUP_SAVE) {
-                                store_row16(p.o1 + at, col + 16 * v, N, wide, og);
-                                store_row16(p.o2 + at, col + 16 * v, N, wide, ou);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int ce = col + 16 * v + 8 * e, k = 16 * v + 8 * e;
+                                    if (ce >= N) break;
+                                    uint32_t a[8], b[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        a[i] = gv[k + i];
+                                        b[i] = uv[k + i];
+                                    }
+                                    st_global_v8(p.sg + at + ce, a);  // rows of a multiple of 8 floats
+                                    st_global_v8(p.su + at + ce, b);
+                                }
                             }
                         }
                     }
@@ -280,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
                                 for (int e = 0; e < 2; ++e) {
                                     if (cv + 8 * e >= N) break;
                                     float g[8], u[8], dg[8], du[8], h[8];
-                                    load8bf(p.g + at + cv + 8 * e, g);
-                                    load8bf(p.u + at + cv + 8 * e, u);
+                                    load8(p.g + at + cv + 8 * e, g);
+                                    load8(p.u + at + cv + 8 * e, u);
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) {
                                         const float dh = __uint_as_float(dv[16 * v + 8 * e + i]);

@@ -62,10 +62,9 @@ def forward_bound(x, w1, w3, w2, kind):
 
 
 def backward_bounds(dout, x, w1, w3, w2, kind):
-    """The same of (dx, dw1, dw3, dw2): g and u saved in bf16, dg, du and h rounded to bf16."""
+    """The same of (dx, dw1, dw3, dw2): g and u saved in fp32, dg, du and h rounded to bf16."""
     dout, x, w1, w3, w2 = (t.double() for t in (dout, x, w1, w3, w2))
     g, u, eg, eu = _h_parts(x, w1, w3, kind)
-    eg, eu = eg + HALF * (g.abs() + eg), eu + HALF * (u.abs() + eu)
     a, s = act_slope(g, kind)
     dh = dout @ w2
     ed = dout.shape[1] * F32 * (dout.abs() @ w2.abs())

@@ -82,6 +82,16 @@ def test_mxfp4_refusals(B):
         return lib.moe_mxfp4_gemm(a, FAKE, m, FAKE, FAKE, n, k, out, ws, size, None)
     assert gemm(n=12) == 1 and gemm(k=48) == 1 and gemm(m=-1) == 1 and gemm(m=0) == 0
     assert gemm(ws=None) == 1 and gemm(ws=FAKE + 16) == 1 and gemm(size=128) == 3
+    assert lib.moe_mxfp4_linear_workspace_size(4, 16, 48, ctypes.byref(n)) == 1
+    assert lib.moe_mxfp4_linear_workspace_size(1, 16, 1 << 21, ctypes.byref(n)) == 2
+    assert lib.moe_mxfp4_linear_workspace_size(130, 16, 160, ctypes.byref(n)) == 0
+    assert n.value == 256 + -(-130 * 80 // 256) * 256 + 4 * 512
+    for fn in (lib.moe_mxfp4_linear, lib.moe_mxfp4_linear_f32):
+        assert fn(FAKE, 64, 0, FAKE, FAKE, 16, 64, FAKE, None, 0, None) == 0
+        assert fn(FAKE, 64, 4, FAKE, FAKE, 12, 64, FAKE, FAKE, 1 << 20, None) == 1
+        assert fn(FAKE, 64, 4, FAKE, FAKE, 16, 64, FAKE, FAKE, 256, None) == 3
+        assert fn(FAKE, 32, 4, FAKE, FAKE, 16, 64, FAKE, FAKE, 1 << 20, None) == 1
+        assert fn(FAKE, 64, 4, None, FAKE, 16, 64, FAKE, FAKE, 1 << 20, None) == 1
     assert gemm(a=None) == 1 and gemm(a=FAKE + 8) == 1 and gemm(out=None) == 1 and gemm(m=1 << 30) == 2
 
 
