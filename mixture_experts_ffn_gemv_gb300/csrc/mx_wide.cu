@@ -5,16 +5,21 @@
 // 128 columns of g and the same of u).  A stage is 256 of K: this CTA's 128
 // rows of A codes (16 KB, 128-byte swizzle), its half of the 256 rows of B
 // (16 KB), and the packed scales of its A rows (1 KB) and of all 256 B rows
-// (2 KB), which each CTA needs whole.  The scales are packed in the order that
-// tcgen05.cp moves them to tensor memory, so the MMA issuer itself copies a
-// stage's scales and issues its MMAs, with no other warp in between.
+// (2 KB), which each CTA needs whole.
+// Scales: four warps, one per TMEM lane quarter, move a stage's scales to
+// tensor memory -- a lane's 16 bytes of each 512-byte tile are its four
+// columns as they lie -- with tcgen05.st, beside the running MMAs.  tcgen05.cp
+// would need no warps, but copies and MMAs run in issue order and the six
+// copies of a stage held the tensor core up for 175 ns of every 480 (4096 x
+// 7168 x 7168; issuing them a stage ahead changed nothing).
 // TMEM: one accumulator of 256 columns and 24 scale columns per stage.  One
 // accumulator, not two: 256 x 256 tiles halve the operand bytes per product
 // of the 128 x 128 tiles that would leave room for two, and the epilogue holds
-// up the next tile only while it reads the accumulator.
+// up the next tile only while it reads the accumulator into registers.
 // Gate/up quantises h in its epilogue: a thread's 32 columns of a row are one
 // MXFP4 block, so h never exists in wider form.
-//   warp 0 producer, warp 1 (leader) issuer, warps 2..9 epilogue.
+//   warp 0 producer, warp 1 (leader) issuer, warps 2..17 epilogue (four per lane
+//   quarter, 64 columns each), warps 18..21 scales.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -45,8 +50,10 @@ static_assert(STAGE_BYTES == STAGE_STRIDE, "stages keep the swizzle's 1024-byte 
 constexpr int TMEM_COLS = 512;
 constexpr int SF_COL0 = BN, SF_COLS = 24;  // per stage: 2 K tiles x (4 of A + 8 of B)
 static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "accumulator and scale columns fit tensor memory");
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int EPI_WARPS = 16, SCALE0 = 2 + EPI_WARPS;
+constexpr int SCALE_SETS = 1, SCALE_WARPS = 4 * SCALE_SETS;
+constexpr int EC = 32 / EPI_WARPS;  // 32-column chunks of the accumulator per epilogue warp
+constexpr int THREADS = 32 * (SCALE0 + SCALE_WARPS);
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_STRIDE + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
@@ -62,7 +69,9 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
     const uint32_t tfull = smem_u32(bars + 2 * STAGES), tempty = smem_u32(bars + 2 * STAGES + 1);
     const uint32_t drain = smem_u32(bars + 2 * STAGES + 2);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 3);
+    // scales of a stage: landed in this CTA's shared memory; in both CTAs' TMEM
+    const uint32_t sland0 = smem_u32(bars + 2 * STAGES + 3), sfull0 = smem_u32(bars + 3 * STAGES + 3);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -72,6 +81,8 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
+            mbar_init(sland0 + 8 * s, 1);
+            mbar_init(sfull0 + 8 * s, 2 * 4);
         }
         mbar_init(tfull, 1);
         mbar_init(tempty, 2 * EPI_WARPS);
@@ -109,18 +120,22 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
                         break;
                     }
                     const uint32_t sa = sbase + s * STAGE_STRIDE, bar = lead_full0 + 8 * s;
-                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (A_BYTES + B_BYTES));
                     tma_load_2d_pair(sa, &p.a, kb * BKB, m0, bar);
                     tma_load_2d_pair(sa + B_OFF, mb, kb * BKB, n0, bar);
-                    tma_load_3d_pair(sa + SA_OFF, &p.as, 0, 2 * kb, m0 >> 7, bar);
-                    tma_load_3d_pair(sa + SB_OFF, &p.bs[0], 0, 2 * kb, GATEUP ? nt : 2 * nt, bar);
-                    tma_load_3d_pair(sa + SB_OFF + 1024, &p.bs[GATEUP ? 1 : 0], 0, 2 * kb, GATEUP ? nt : 2 * nt + 1, bar);
+                    const uint32_t sl = sland0 + 8 * s;
+                    mbar_arrive_expect_tx(sl, SA_BYTES + SB_BYTES);
+                    tma_load_3d(sa + SA_OFF, &p.as, 0, 2 * kb, m0 >> 7, sl);
+                    tma_load_3d(sa + SB_OFF, &p.bs[0], 0, 2 * kb, GATEUP ? nt : 2 * nt, sl);
+                    tma_load_3d(sa + SB_OFF + 1024, &p.bs[GATEUP ? 1 : 0], 0, 2 * kb, GATEUP ? nt : 2 * nt + 1, sl);
                 }
             }
             if (!ok) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 31);
                 *abort_flag = 1;
             }
+            for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
+                mbar_wait(sland0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
             if (leader) {
                 for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
                     mbar_wait_cluster(full0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
@@ -135,28 +150,18 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             bool ok = true;
             for (int t = cl; t < total && ok; t += ncl, ++tc) {
                 if (*abort_flag) break;
-                if (!mbar_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
                 for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
+                    const uint32_t s = it % STAGES;
+                    const uint32_t ph = (it / STAGES) & 1u;
+                    if ((kb == 0 && !mbar_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) ||
+                        !mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns) ||
+                        !mbar_wait_cluster(sfull0 + 8 * s, ph, p.wait_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = sbase + s * STAGE_STRIDE;
                     const uint32_t sf = tmem_base + SF_COL0 + s * SF_COLS;
-                    // columns: A tiles of K 0..127, 128..255; then per K tile the two B row tiles
-#pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) {
-                        tmem_cp_scales_pair(sf + 4 * kt, desc_scales(sa + SA_OFF + kt * 512));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tmem_cp_scales_pair(sf + 8 + 8 * kt + 4 * h, desc_scales(sa + SB_OFF + h * 1024 + kt * 512));
-                    }
                     const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + B_OFF);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -175,8 +180,37 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             mbar_wait_cluster(drain, 0, DRAIN_NS);
         }
         __syncwarp();
+    } else if (warp >= SCALE0) {
+        // columns: A tiles of K 0..127, 128..255; then per K tile the two B row tiles
+        const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + SF_COL0;
+        const uint32_t lead_sfull0 = mapa(sfull0, 0);
+        const uint32_t n = total > cl ? (uint32_t)((total - cl + ncl - 1) / ncl) * p.kblocks : 0;
+        for (uint32_t it = (warp - SCALE0) >> 2; it < n; it += SCALE_SETS) {
+            const uint32_t s = it % STAGES;
+            if (*abort_flag || !mbar_wait(sland0 + 8 * s, (it / STAGES) & 1u, p.wait_ns)) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 34);
+                *abort_flag = 1;
+                break;
+            }
+            const uint32_t src = sbase + s * STAGE_STRIDE + SA_OFF + lane * 16;
+            uint4 w[6];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[i] = lds128(src + i * 512);
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w[2 + 2 * kt + h] = lds128(src + SB_OFF - SA_OFF + h * 1024 + kt * 512);
+            const uint32_t d = lane_base + s * SF_COLS;
+            tmem_st8(d, w[0], w[1]);
+            tmem_st8(d + 8, w[2], w[3]);
+            tmem_st8(d + 16, w[4], w[5]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead_sfull0 + 8 * s);
+        }
     } else {
-        const int q4 = warp & 3, half = (warp - 2) >> 2;
+        const int q4 = warp & 3, part = (warp - 2) >> 2;  // lane quarter, 64 of the tile's columns
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
             if (*abort_flag) break;
@@ -190,65 +224,53 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             }
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16);
-            if (!any) {
-                // a lane quarter past the last row
-            } else if (GATEUP) {
-                uint32_t word = 0;  // this thread's two scale bytes
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    const int c = 2 * half + j, col = nt * 128 + c * 32;
-                    if (col >= p.N) break;
-                    uint32_t gv[32], uv[32];
-                    tmem_ld32(taddr + c * 32, gv);
-                    tmem_ld32(taddr + 128 + c * 32, uv);
-                    tmem_wait_ld();
-                    float h[32];
-                    uint32_t a = 0;
+            // the accumulator is read whole and handed back before anything is
+            // computed from it or stored: the next tile's MMAs wait for no more
+            uint32_t v[EC][32];  // gate/up: EC / 2 blocks of g, then of u; else 32 EC columns of D
+            if (any) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        h[i] = glu(__uint_as_float(gv[i]), __uint_as_float(uv[i]), p.act);
-                        a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
-                    }
-                    const uint32_t s = mx_scale(a);
-                    const float inv = mx_inverse(s);
-                    if (ok) {
-                        uint4 w;
-                        w.x = mx_codes8(h, inv);
-                        w.y = mx_codes8(h + 8, inv);
-                        w.z = mx_codes8(h + 16, inv);
-                        w.w = mx_codes8(h + 24, inv);
-                        if (s == 255u) w = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(p.codes + ((size_t)r * p.N + col) / 2) = w;
-                    }
-                    word |= s << (8 * j);
-                }
-                // two blocks of the row's scale tile; blocks past the last column are 0
-                if (ok) *reinterpret_cast<uint16_t*>(p.scales + mx_scale_at(r, (size_t)nt * 4 + 2 * half, p.nkt)) = (uint16_t)word;
-            } else {
-                const bool wide = (p.N & 15) == 0;
-                uint16_t* row = p.out + (size_t)r * p.N;
-#pragma unroll 1
-                for (int c = 4 * half; c < 4 * half + 4; ++c) {
-                    const int col = nt * 256 + c * 32;
-                    if (col >= p.N) break;
-                    uint32_t dv[32];
-                    tmem_ld32(taddr + c * 32, dv);
-                    tmem_wait_ld();
-                    if (ok) {
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            uint32_t o[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                o[i] = pack_bf16x2(__uint_as_float(dv[16 * v + 2 * i]), __uint_as_float(dv[16 * v + 2 * i + 1]));
-                            store_row16(row, col + 16 * v, p.N, wide, o);
-                        }
-                    }
-                }
+                for (int c = 0; c < EC; ++c)
+                    tmem_ld32(taddr + (GATEUP ? 128 * (c / (EC / 2)) + 16 * EC * part + 32 * (c % (EC / 2)) : 32 * (EC * part + c)), v[c]);
+                tmem_wait_ld();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty);
+            if (lane == 0) mbar_arrive_remote(lead_tempty);
+            if (!ok) continue;
+            if (GATEUP) {
+#pragma unroll
+                for (int j = 0; j < EC / 2; ++j) {
+                    const int blk = part * (EC / 2) + j, col = nt * 128 + blk * 32;
+                    uint32_t s = 0;  // blocks past the last column: 0
+                    if (col < p.N) {
+                        float h[32];
+                        uint32_t a = 0;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            h[i] = glu(__uint_as_float(v[j][i]), __uint_as_float(v[EC / 2 + j][i]), p.act);
+                            a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
+                        }
+                        s = mx_scale(a);
+                        const float inv = mx_inverse(s);
+                        uint4 w = make_uint4(mx_codes8(h, inv), mx_codes8(h + 8, inv), mx_codes8(h + 16, inv), mx_codes8(h + 24, inv));
+                        if (s == 255u) w = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(p.codes + ((size_t)r * p.N + col) / 2) = w;
+                    }
+                    p.scales[mx_scale_at(r, (size_t)nt * 4 + blk, p.nkt)] = (uint8_t)s;
+                }
+            } else {
+                const bool wide = (p.N & 15) == 0;
+                uint16_t* row = p.out + (size_t)r * p.N;
+#pragma unroll
+                for (int c = 0; c < 2 * EC; ++c) {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = pack_bf16x2(__uint_as_float(v[c >> 1][16 * (c & 1) + 2 * i]),
+                                           __uint_as_float(v[c >> 1][16 * (c & 1) + 2 * i + 1]));
+                    store_row16(row, nt * 256 + part * 32 * EC + 16 * c, p.N, wide, o);
+                }
+            }
         }
     }
     tc_fence_before();
