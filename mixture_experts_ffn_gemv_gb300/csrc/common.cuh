@@ -180,6 +180,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // that the writes and the reads each take the minimum four wavefronts.  Rows
 // from `valid` on are not stored.  gdst: row 0's segment; ldb: the output's row
 // stride in bytes.
+// The staging of W = 128 alone is the 128-byte swizzle of a TMA box of 32 rows
+// (stg 1024-byte aligned): stage_row128 writes it for a TMA store.
+__device__ __forceinline__ void stage_row128(uint32_t stg, const uint32_t (&v)[32], int lane) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        sts128(stg + lane * 128 + ((c ^ (lane & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
 template <int W>
 __device__ __forceinline__ void warp_store_rows(uint32_t stg, const uint32_t (&v)[W / 4], int lane, uint8_t* gdst,
                                                 size_t ldb, int valid) {

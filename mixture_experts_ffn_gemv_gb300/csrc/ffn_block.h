@@ -58,8 +58,9 @@ struct MxProduct {
     int m_tiles, n_tiles;
     int M, N;
     int act;
-    uint16_t* out;            // EPI_STORE: bf16 [M, N]
-    uint8_t *codes, *scales;  // EPI_GATEUP: h as MXFP4, [M, N/2] and packed scales
+    uint16_t* out;            // plain: bf16 [M, N]
+    CUtensorMap o;            // ... its map (set by launch_mx_product)
+    uint8_t *codes, *scales;  // gate/up: h as MXFP4, [M, N/2] and packed scales
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;
     uint64_t wait_ns;

@@ -18,8 +18,8 @@
 // up the next tile only while it reads the accumulator into registers.
 // Gate/up quantises h in its epilogue: a thread's 32 columns of a row are one
 // MXFP4 block, so h never exists in wider form.
-//   warp 0 producer, warp 1 (leader) issuer, warps 2..17 epilogue (four per lane
-//   quarter, 64 columns each), warps 18..21 scales.
+//   warp 0 producer, warp 1 (leader) issuer, then the epilogue warps (an
+//   equal number per lane quarter) and four scale warps.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,7 +40,6 @@ using namespace sm100;
 
 constexpr int BM = 128, BN = 256;
 constexpr int BKB = 128;  // bytes of K per stage and row: 256 codes
-constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * BKB, B_BYTES = 128 * BKB;
 constexpr int SA_BYTES = 2 * 512, SB_BYTES = 2 * 2 * 512;  // two K tiles x one / two row tiles
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
@@ -49,23 +48,33 @@ constexpr int STAGE_STRIDE = 35 * 1024;
 static_assert(STAGE_BYTES == STAGE_STRIDE, "stages keep the swizzle's 1024-byte alignment");
 constexpr int TMEM_COLS = 512;
 constexpr int SF_COL0 = BN, SF_COLS = 24;  // per stage: 2 K tiles x (4 of A + 8 of B)
-static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "accumulator and scale columns fit tensor memory");
-constexpr int EPI_WARPS = 16, SCALE0 = 2 + EPI_WARPS;
-constexpr int SCALE_SETS = 1, SCALE_WARPS = 4 * SCALE_SETS;
-constexpr int EC = 32 / EPI_WARPS;  // 32-column chunks of the accumulator per epilogue warp
-constexpr int THREADS = 32 * (SCALE0 + SCALE_WARPS);
+// Epilogue warps: gate/up has the activation and the quantisation of h to
+// compute; a plain product only rounds, and more warps would only poll.
+template <bool GATEUP>
+struct Shape {
+    static constexpr int EPI_WARPS = GATEUP ? 16 : 8;
+    static constexpr int STAGES = GATEUP ? 6 : 5;  // a plain product also stages its output: 4 KB per epilogue warp
+    static constexpr int STG_OFF = STAGES * STAGE_STRIDE;
+    static constexpr int BAR_OFF = STG_OFF + (GATEUP ? 0 : EPI_WARPS * 4096);
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
+    static_assert(SF_COL0 + STAGES * SF_COLS <= TMEM_COLS, "accumulator and scale columns fit tensor memory");
+    static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
+    static constexpr int SCALE0 = 2 + EPI_WARPS;
+    static constexpr int THREADS = 32 * (SCALE0 + 4);
+};
+constexpr int SCALE_WARPS = 4;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_STRIDE + 256;
-static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 
 template <bool GATEUP>
-__global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__ MxProduct p) {
+__global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __grid_constant__ MxProduct p) {
+    constexpr int EPI_WARPS = Shape<GATEUP>::EPI_WARPS, SCALE0 = Shape<GATEUP>::SCALE0;
+    constexpr int STAGES = Shape<GATEUP>::STAGES, STG_OFF = Shape<GATEUP>::STG_OFF, BAR_OFF = Shape<GATEUP>::BAR_OFF;
     pdl_wait();
     pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_STRIDE);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
     const uint32_t tfull = smem_u32(bars + 2 * STAGES), tempty = smem_u32(bars + 2 * STAGES + 1);
     const uint32_t drain = smem_u32(bars + 2 * STAGES + 2);
@@ -82,7 +91,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(sland0 + 8 * s, 1);
-            mbar_init(sfull0 + 8 * s, 2 * 4);
+            mbar_init(sfull0 + 8 * s, 2 * SCALE_WARPS);
         }
         mbar_init(tfull, 1);
         mbar_init(tempty, 2 * EPI_WARPS);
@@ -145,14 +154,15 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            uint32_t it = 0, tc = 0;
+        // The whole warp walks the loop and one lane issues: the addresses are
+        // then warp-uniform values.  (One lane looping alone took 310 ns for a
+        // stage's four MMAs, more than the tensor core does.)
+        if (leader) {
+            uint32_t s = 0, ph = 0, tc = 0;
             bool ok = true;
             for (int t = cl; t < total && ok; t += ncl, ++tc) {
                 if (*abort_flag) break;
-                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    const uint32_t ph = (it / STAGES) & 1u;
+                for (int kb = 0; kb < p.kblocks; ++kb) {
                     if ((kb == 0 && !mbar_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) ||
                         !mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns) ||
                         !mbar_wait_cluster(sfull0 + 8 * s, ph, p.wait_ns)) {
@@ -163,20 +173,26 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
                     const uint32_t sa = sbase + s * STAGE_STRIDE;
                     const uint32_t sf = tmem_base + SF_COL0 + s * SF_COLS;
                     const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + B_OFF);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_mxf4_pair(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc_mxf4(2 * BM, BN, 2 * (kk & 1)),
-                                      sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb | kk) != 0);
-                    mma_commit_pair(empty0 + 8 * s);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_mxf4_pair(tmem_base, ad + 2 * kk, bd + 2 * kk, idesc_mxf4(2 * BM, BN, 2 * (kk & 1)),
+                                          sf + 4 * (kk >> 1), sf + 8 + 8 * (kk >> 1), (kb | kk) != 0);
+                        mma_commit_pair(empty0 + 8 * s);
+                        if (kb == p.kblocks - 1) mma_commit_pair(tfull);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                if (!ok) break;
-                mma_commit_pair(tfull);
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 32);
                 *abort_flag = 1;
             }
-            mma_commit_pair(drain);
+            if (elect_one()) mma_commit_pair(drain);
             mbar_wait_cluster(drain, 0, DRAIN_NS);
         }
         __syncwarp();
@@ -185,9 +201,9 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp & 3) * 32) << 16) + SF_COL0;
         const uint32_t lead_sfull0 = mapa(sfull0, 0);
         const uint32_t n = total > cl ? (uint32_t)((total - cl + ncl - 1) / ncl) * p.kblocks : 0;
-        for (uint32_t it = (warp - SCALE0) >> 2; it < n; it += SCALE_SETS) {
-            const uint32_t s = it % STAGES;
-            if (*abort_flag || !mbar_wait(sland0 + 8 * s, (it / STAGES) & 1u, p.wait_ns)) {
+        uint32_t s = 0, ph = 0;
+        for (uint32_t it = 0; it < n; ++it) {
+            if (*abort_flag || !mbar_wait(sland0 + 8 * s, ph, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 34);
                 *abort_flag = 1;
                 break;
@@ -208,9 +224,13 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(lead_sfull0 + 8 * s);
+            if (++s == STAGES) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
     } else {
-        const int q4 = warp & 3, part = (warp - 2) >> 2;  // lane quarter, 64 of the tile's columns
+        const int q4 = warp & 3, part = (warp - 2) >> 2;  // lane quarter, share of the columns
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
             if (*abort_flag) break;
@@ -226,52 +246,67 @@ __global__ void __launch_bounds__(THREADS, 1) mx_product(const __grid_constant__
             const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16);
             // the accumulator is read whole and handed back before anything is
             // computed from it or stored: the next tile's MMAs wait for no more
-            uint32_t v[EC][32];  // gate/up: EC / 2 blocks of g, then of u; else 32 EC columns of D
+            uint32_t v[2][32];            // gate/up: a block of g and of u; else two chunks of D on their way to o
+            uint32_t o[GATEUP ? 1 : 2][32];  // bf16 pairs of 64 columns each
             if (any) {
+                if (GATEUP) {
+                    tmem_ld32(taddr + 32 * part, v[0]);
+                    tmem_ld32(taddr + 128 + 32 * part, v[1]);
+                    tmem_wait_ld();
+                } else {
 #pragma unroll
-                for (int c = 0; c < EC; ++c)
-                    tmem_ld32(taddr + (GATEUP ? 128 * (c / (EC / 2)) + 16 * EC * part + 32 * (c % (EC / 2)) : 32 * (EC * part + c)), v[c]);
-                tmem_wait_ld();
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld32(taddr + 128 * part + 64 * c, v[0]);
+                        tmem_ld32(taddr + 128 * part + 64 * c + 32, v[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[GATEUP ? 0 : c][i] = pack_bf16x2(__uint_as_float(v[i >> 4][(2 * i) & 31]),
+                                                               __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
+                    }
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(lead_tempty);
-            if (!ok) continue;
+            if (!any) continue;
             if (GATEUP) {
+                if (!ok) continue;
+                const int col = nt * 128 + part * 32;
+                uint32_t s = 0;  // blocks past the last column: 0
+                if (col < p.N) {
+                    float h[32];
+                    uint32_t a = 0;
 #pragma unroll
-                for (int j = 0; j < EC / 2; ++j) {
-                    const int blk = part * (EC / 2) + j, col = nt * 128 + blk * 32;
-                    uint32_t s = 0;  // blocks past the last column: 0
-                    if (col < p.N) {
-                        float h[32];
-                        uint32_t a = 0;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            h[i] = glu(__uint_as_float(v[j][i]), __uint_as_float(v[EC / 2 + j][i]), p.act);
-                            a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
-                        }
-                        s = mx_scale(a);
-                        const float inv = mx_inverse(s);
-                        uint4 w = make_uint4(mx_codes8(h, inv), mx_codes8(h + 8, inv), mx_codes8(h + 16, inv), mx_codes8(h + 24, inv));
-                        if (s == 255u) w = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(p.codes + ((size_t)r * p.N + col) / 2) = w;
+                    for (int i = 0; i < 32; ++i) {
+                        h[i] = glu(__uint_as_float(v[0][i]), __uint_as_float(v[1][i]), p.act);
+                        a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
                     }
-                    p.scales[mx_scale_at(r, (size_t)nt * 4 + blk, p.nkt)] = (uint8_t)s;
+                    s = mx_scale(a);
+                    const float inv = mx_inverse(s);
+                    uint4 w = make_uint4(mx_codes8(h, inv), mx_codes8(h + 8, inv), mx_codes8(h + 16, inv), mx_codes8(h + 24, inv));
+                    if (s == 255u) w = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(p.codes + ((size_t)r * p.N + col) / 2) = w;
                 }
+                p.scales[mx_scale_at(r, (size_t)nt * 4 + part, p.nkt)] = (uint8_t)s;
             } else {
-                const bool wide = (p.N & 15) == 0;
-                uint16_t* row = p.out + (size_t)r * p.N;
+                // 32 rows x 64 columns at a time through this warp's staging
+                // and out by TMA: whole lines, clipped at M and N
+                const uint32_t stg = sbase + STG_OFF + (warp - 2) * 4096;
 #pragma unroll
-                for (int c = 0; c < 2 * EC; ++c) {
-                    uint32_t o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = pack_bf16x2(__uint_as_float(v[c >> 1][16 * (c & 1) + 2 * i]),
-                                           __uint_as_float(v[c >> 1][16 * (c & 1) + 2 * i + 1]));
-                    store_row16(row, nt * 256 + part * 32 * EC + 16 * c, p.N, wide, o);
+                for (int c = 0; c < 2; ++c) {
+                    const int col = nt * 256 + part * 128 + 64 * c;
+                    if (col >= p.N) break;
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
+                    stage_row128(stg, o[GATEUP ? 0 : c], lane);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&p.o, col, r, stg);
                 }
             }
         }
+        if (!GATEUP && lane == 0) tma_store_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -290,13 +325,13 @@ int sms() {
 template <bool GATEUP>
 cudaError_t launch(const MxProduct& p, cudaStream_t st) {
     static cudaError_t attr =
-        cudaFuncSetAttribute(mx_product<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        cudaFuncSetAttribute(mx_product<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<GATEUP>::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     const int pairs = std::max(1, std::min(sms() / 2, p.m_tiles * p.n_tiles));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.blockDim = dim3(Shape<GATEUP>::THREADS);
+    cfg.dynamicSmemBytes = Shape<GATEUP>::SMEM_BYTES;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -327,6 +362,10 @@ bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k)
 cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st) {
     p.m_tiles = ceil_div(p.M, 256);
     p.n_tiles = ceil_div(p.N, gateup ? 128 : 256);
+    if (!gateup) {
+        const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.M};
+        if (!tmap_encode(&p.o, p.out, 2, dims, 2, 64, 32)) return cudaErrorUnknown;
+    }
     return gateup ? launch<true>(p, st) : launch<false>(p, st);
 }
 
