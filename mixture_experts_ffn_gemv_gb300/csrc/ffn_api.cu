@@ -116,8 +116,7 @@ int forward_bf16(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx,
     if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
     gu.b[0] = f->k1;
     gu.b[1] = f->k3;
-    p.sg = static_cast<float*>(saved);
-    p.su = saved ? p.sg + (size_t)m * I : nullptr;
+    p.save = static_cast<float*>(saved);
     if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
     FfnProducts d = products(f, ws);
     FfnProduct& y = add(d, m, H, I, out);
@@ -379,8 +378,8 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     q.b_mn = 1;
     p.g = static_cast<const float*>(saved);
     p.u = p.g + (size_t)m * I;
-    p.o1 = static_cast<uint16_t*>(du);
-    p.o2 = static_cast<uint16_t*>(h);
+    p.out_du = static_cast<uint16_t*>(du);
+    p.out_h = static_cast<uint16_t*>(h);
     if (launch_ffn_products(p, EPI_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
     // the four products that need them, in one launch
     FfnProducts r = products(f, workspace);

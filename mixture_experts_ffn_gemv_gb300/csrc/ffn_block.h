@@ -30,6 +30,7 @@ struct FfnProduct {
     int m_tiles, n_tiles;
     int M, N;
     uint16_t* out;           // [M, N], row stride N
+    CUtensorMap o;           // ... in boxes of 64 columns x 32 rows (set by launch_ffn_products)
 };
 constexpr int kMaxProducts = 4;
 struct FfnProducts {
@@ -37,9 +38,10 @@ struct FfnProducts {
     int count;
     int first[kMaxProducts + 1];  // first work item of each product
     int act;
-    float *sg, *su;         // EPI_GATEUP_SAVE: pre-activations g, u
+    float* save;            // EPI_GATEUP_SAVE: g, then u, [M, N] each
     const float *g, *u;     // EPI_DACT: the same
-    uint16_t *o1, *o2;      // EPI_DACT: du, h (out: dg)
+    uint16_t *out_du, *out_h;  // EPI_DACT (out: dg)
+    CUtensorMap sg, su, du, h;  // maps of these (set by launch_ffn_products)
     WsHeader* hdr;
     uint64_t wait_ns;
 };

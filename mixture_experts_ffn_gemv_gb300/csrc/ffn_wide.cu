@@ -8,10 +8,13 @@
 // backward products read W, x, dg and h as they lie, through MN-major
 // descriptors, so nothing is transposed in memory.
 //   warp 0      TMA producer: this CTA's 128 rows of A and half of the tile's
-//               256 rows of B, 64 of K per stage, 7 stages of 32 KB;
+//               256 rows of B, 64 of K per stage, 6 stages of 32 KB;
 //   warp 1      (leader) MMA issuer: M = 256, N = 256, fp32 accumulators in
-//               TMEM, two buffers of 256 columns;
-//   warps 2..9  epilogue, two per TMEM lane quarter, each half of the columns.
+//               TMEM, two buffers of 256 columns; the whole warp walks the
+//               loop and one lane issues, so addresses are warp-uniform;
+//   warps 2..9  epilogue, two per TMEM lane quarter, each half of the columns;
+//               outputs leave through 4 KB of staging per warp and TMA stores,
+//               which write whole lines and clip at the matrix's edges.
 // Gate/up: the leader's half of B is 128 rows of W1, the peer's the same rows
 // of W3, so a thread finds g and u of one element in its own lane.
 // Every wait is bounded; on expiry the CTA records DEV_ERR_TIMEOUT, stops
@@ -35,20 +38,56 @@ namespace {
 using namespace sm100;
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int STAGES = 7;
+constexpr int STAGES = 6;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = 128 * BK * 2;  // per CTA
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint64_t DRAIN_NS = 2000000000ull;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
+constexpr int STG_OFF = STAGES * STAGE_BYTES;
+constexpr int BAR_OFF = STG_OFF + EPI_WARPS * 4096;
+constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 
-__device__ __forceinline__ void load8(const float* p, float* v) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 32 rows x 32 fp32 of a matrix, whole lines per instruction: register i of a
+// lane is its 16 bytes of rows 4 i .. 4 i + 3.  Rows from m and columns from n
+// on read as zero.
+__device__ __forceinline__ void load_block(const float* p, int row0, int m, int col0, int n, int lane, uint4 (&v)[8]) {
+    const int col = col0 + 4 * (lane & 7);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = row0 + 4 * i + (lane >> 3);
+        v[i] = row < m && col < n ? ld_stream_v4(p + (size_t)row * n + col) : make_uint4(0, 0, 0, 0);
+    }
+}
+// ... turned round through the warp's staging: lane r gets row r.
+__device__ __forceinline__ void turn_block(uint32_t stg, const uint4 (&v)[8], int lane, float (&f)[32]) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3);
+        sts128(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint4 q = lds128(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
+        f[4 * c] = __uint_as_float(q.x);
+        f[4 * c + 1] = __uint_as_float(q.y);
+        f[4 * c + 2] = __uint_as_float(q.z);
+        f[4 * c + 3] = __uint_as_float(q.w);
+    }
+}
+// One row segment of 128 bytes per lane out by TMA: a box at (col, row0).
+__device__ __forceinline__ void put_block(const CUtensorMap* m, uint32_t stg, const uint32_t (&v)[32], int lane, int col,
+                                          int row0) {
+    if (lane == 0) tma_store_wait_read();
+    __syncwarp();
+    stage_row128(stg, v, lane);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(m, col, row0, stg);
 }
 
 struct Item {
@@ -74,7 +113,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
     const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = smem_u32(bars + 2 * STAGES + 2);
     const uint32_t drain = smem_u32(bars + 2 * STAGES + 4);
@@ -162,8 +201,8 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            uint32_t it = 0, tc = 0;
+        if (leader) {
+            uint32_t s = 0, ph = 0, tc = 0;
             bool ok = true;
             for (int t = cl; t < total && ok; t += ncl, ++tc) {
                 if (*abort_flag) break;
@@ -179,46 +218,55 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
                 tc_fence_after();
                 const uint32_t d = tmem_base + acc * BN;
                 const int kbs = q.kblocks * q.sources;
-                for (int kb = 0; kb < kbs; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                const uint64_t ad0 = q.a_mn ? desc_sw128_mn(sbase) : desc_sw128(sbase);
+                const uint64_t bd0 = q.b_mn ? desc_sw128_mn(sbase + A_BYTES) : desc_sw128(sbase + A_BYTES);
+                for (int kb = 0; kb < kbs; ++kb) {
                     if (!mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES;
-                    const uint64_t ad = q.a_mn ? desc_sw128_mn(sa) : desc_sw128(sa);
-                    const uint64_t bd = q.b_mn ? desc_sw128_mn(sb) : desc_sw128(sb);
+                    const uint64_t ad = ad0 + s * (STAGE_BYTES >> 4), bd = bd0 + s * (STAGE_BYTES >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        mma_bf16_pair(d, ad + sta * kk, bd + stb * kk, idesc, (kb | kk) != 0);
-                    mma_commit_pair(empty0 + 8 * s);
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma_bf16_pair(d, ad + sta * kk, bd + stb * kk, idesc, (kb | kk) != 0);
+                        mma_commit_pair(empty0 + 8 * s);
+                        if (kb == kbs - 1) mma_commit_pair(tfull0 + 8 * acc);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
-                if (!ok) break;
-                mma_commit_pair(tfull0 + 8 * acc);
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 22);
                 *abort_flag = 1;
             }
-            mma_commit_pair(drain);
+            if (elect_one()) mma_commit_pair(drain);
             mbar_wait_cluster(drain, 0, DRAIN_NS);
         }
         __syncwarp();
     } else {
         const int q4 = warp & 3;           // the TMEM lane quarter this warp may read
         const int half = (warp - 2) >> 2;  // which half of the tile's columns
+        const uint32_t stg = sbase + STG_OFF + (warp - 2) * 4096;
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
             if (*abort_flag) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
-            const int r = w.mt * 256 + (int)rank * BM + q4 * 32 + lane;  // this thread's row of D
-            const bool ok = r < q.M;
-            const bool any = r - lane < q.M;  // of its warp
+            const int row0 = w.mt * 256 + (int)rank * BM + q4 * 32;  // first of this warp's rows of D
+            const bool any = row0 < q.M;
             const int N = q.N;
-            const bool wide = (N & 15) == 0;
-            const size_t at = (size_t)r * N;
+            const int col0 = GATEUP ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;  // ... columns of the output
+            uint4 gl[8], ul[8];  // EPI_DACT: the next 32 columns of g and u on their way
+            if (EPI == EPI_DACT && any && col0 < N) {
+                load_block(p.g, row0, q.M, col0, N, lane, gl);
+                load_block(p.u, row0, q.M, col0, N, lane, ul);
+            }
             const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
             if (!mbar_wait_cluster(tfull0 + 8 * acc, aph, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 23);
@@ -227,100 +275,85 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
             }
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16) + acc * BN;
-            if (!any) {
-                // a lane quarter past the last row
+            if (!any || col0 >= N) {
+                // nothing of the tile in the matrix
             } else if (GATEUP) {
-#pragma unroll 1
-                for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                    const int col = w.nt * 128 + c * 32;
-                    if (col >= N) break;
+                uint32_t o[32];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     uint32_t gv[32], uv[32];
-                    tmem_ld32(taddr + c * 32, gv);
-                    tmem_ld32(taddr + 128 + c * 32, uv);
+                    tmem_ld32(taddr + 64 * half + 32 * j, gv);
+                    tmem_ld32(taddr + 128 + 64 * half + 32 * j, uv);
                     tmem_wait_ld();
-                    if (ok) {
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            uint32_t o[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float g0 = __uint_as_float(gv[16 * v + 2 * i]), g1 = __uint_as_float(gv[16 * v + 2 * i + 1]);
-                                const float u0 = __uint_as_float(uv[16 * v + 2 * i]), u1 = __uint_as_float(uv[16 * v + 2 * i + 1]);
-                                o[i] = pack_bf16x2(glu(g0, u0, p.act), glu(g1, u1, p.act));
-                            }
-                            store_row16(q.out + at, col + 16 * v, N, wide, o);
-                            if (EPI == EPI_GATEUP_SAVE) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int ce = col + 16 * v + 8 * e, k = 16 * v + 8 * e;
-                                    if (ce >= N) break;
-                                    uint32_t a[8], b[8];
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        a[i] = gv[k + i];
-                                        b[i] = uv[k + i];
-                                    }
-                                    st_global_v8(p.sg + at + ce, a);  // rows of a multiple of 8 floats
-                                    st_global_v8(p.su + at + ce, b);
-                                }
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i)
+                        o[16 * j + i] = pack_bf16x2(glu(__uint_as_float(gv[2 * i]), __uint_as_float(uv[2 * i]), p.act),
+                                                    glu(__uint_as_float(gv[2 * i + 1]), __uint_as_float(uv[2 * i + 1]), p.act));
+                    if (EPI == EPI_GATEUP_SAVE && col0 + 32 * j < N) {
+                        put_block(&p.sg, stg, gv, lane, col0 + 32 * j, row0);
+                        put_block(&p.su, stg, uv, lane, col0 + 32 * j, row0);
                     }
                 }
-            } else {
+                put_block(&q.o, stg, o, lane, col0, row0);
+            } else if (EPI == EPI_DACT) {
 #pragma unroll 1
-                for (int c = 4 * half; c < 4 * half + 4; ++c) {
-                    const int col = w.nt * 256 + c * 32;
-                    if (col >= N) break;
-                    uint32_t dv[32];
-                    tmem_ld32(taddr + c * 32, dv);
-                    tmem_wait_ld();
-                    if (ok) {
+                for (int j = 0; j < 2; ++j) {
+                    if (col0 + 64 * j >= N) break;
+                    uint32_t og[32], ou[32], oh[32];
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const int cv = col + 16 * v;
-                            if (EPI == EPI_DACT) {
-                                uint32_t og[8], ou[8], oh[8];
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t dv[32];
+                        tmem_ld32(taddr + 128 * half + 64 * j + 32 * e, dv);
+                        float g[32], u[32];
+                        if (lane == 0) tma_store_wait_read();  // the staging may still be going out
+                        turn_block(stg, gl, lane, g);
+                        turn_block(stg, ul, lane, u);
+                        const int next = col0 + 64 * j + 32 * e + 32;
+                        if (next < col0 + 128 && next < N) {
+                            load_block(p.g, row0, q.M, next, N, lane, gl);
+                            load_block(p.u, row0, q.M, next, N, lane, ul);
+                        }
+                        tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    if (cv + 8 * e >= N) break;
-                                    float g[8], u[8], dg[8], du[8], h[8];
-                                    load8(p.g + at + cv + 8 * e, g);
-                                    load8(p.u + at + cv + 8 * e, u);
+                        for (int i = 0; i < 16; ++i) {
+                            float r[2][3];
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const float dh = __uint_as_float(dv[16 * v + 8 * e + i]);
-                                        float a, slope;
-                                        act_slope(g[i], p.act, a, slope);
-                                        dg[i] = dh * u[i] * slope;
-                                        du[i] = dh * a;
-                                        h[i] = a * u[i];
-                                    }
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        og[4 * e + i] = pack_bf16x2(dg[2 * i], dg[2 * i + 1]);
-                                        ou[4 * e + i] = pack_bf16x2(du[2 * i], du[2 * i + 1]);
-                                        oh[4 * e + i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
-                                    }
-                                }
-                                store_row16(q.out + at, cv, N, wide, og);
-                                store_row16(p.o1 + at, cv, N, wide, ou);
-                                store_row16(p.o2 + at, cv, N, wide, oh);
-                            } else {
-                                uint32_t o[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    o[i] = pack_bf16x2(__uint_as_float(dv[16 * v + 2 * i]), __uint_as_float(dv[16 * v + 2 * i + 1]));
-                                store_row16(q.out + at, cv, N, wide, o);
+                            for (int k = 0; k < 2; ++k) {
+                                const float dh = __uint_as_float(dv[2 * i + k]);
+                                float a, slope;
+                                act_slope(g[2 * i + k], p.act, a, slope);
+                                r[k][0] = dh * u[2 * i + k] * slope;
+                                r[k][1] = dh * a;
+                                r[k][2] = a * u[2 * i + k];
                             }
+                            og[16 * e + i] = pack_bf16x2(r[0][0], r[1][0]);
+                            ou[16 * e + i] = pack_bf16x2(r[0][1], r[1][1]);
+                            oh[16 * e + i] = pack_bf16x2(r[0][2], r[1][2]);
                         }
                     }
+                    put_block(&q.o, stg, og, lane, col0 + 64 * j, row0);
+                    put_block(&p.du, stg, ou, lane, col0 + 64 * j, row0);
+                    put_block(&p.h, stg, oh, lane, col0 + 64 * j, row0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (col0 + 64 * j >= N) break;
+                    uint32_t v[2][32], o[32];
+                    tmem_ld32(taddr + 128 * half + 64 * j, v[0]);
+                    tmem_ld32(taddr + 128 * half + 64 * j + 32, v[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = pack_bf16x2(__uint_as_float(v[i >> 4][(2 * i) & 31]), __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
+                    put_block(&q.o, stg, o, lane, col0 + 64 * j, row0);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+            if (lane == 0) mbar_arrive_remote(lead_tempty0 + 8 * acc);
         }
+        if (lane == 0) tma_store_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -374,7 +407,14 @@ cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
         q.m_tiles = ceil_div(q.M, 256);
         q.n_tiles = ceil_div(q.N, bn);
         p.first[i + 1] = p.first[i] + q.m_tiles * q.n_tiles;
+        if (!ffn_map(&q.o, q.out, q.M, q.N, q.N, 32)) return cudaErrorUnknown;
     }
+    const uint64_t M = p.p[0].M, N = p.p[0].N, dims[2] = {N, M};
+    if (epilogue == EPI_GATEUP_SAVE && (!tmap_encode(&p.sg, p.save, 2, dims, 4, 32, 32) ||
+                                        !tmap_encode(&p.su, p.save + M * N, 2, dims, 4, 32, 32)))
+        return cudaErrorUnknown;
+    if (epilogue == EPI_DACT && (!ffn_map(&p.du, p.out_du, M, N, N, 32) || !ffn_map(&p.h, p.out_h, M, N, N, 32)))
+        return cudaErrorUnknown;
     switch (epilogue) {
         case EPI_GATEUP: return launch<EPI_GATEUP>(p, st);
         case EPI_GATEUP_SAVE: return launch<EPI_GATEUP_SAVE>(p, st);
