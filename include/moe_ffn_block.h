@@ -75,16 +75,18 @@ MOE_API int moe_ffn_workspace_size(const moe_ffn* ffn, int64_t m, int backward, 
 
 /* out[t, :] = the block applied to x[t, :].
  *   x bf16 [m, H] with row stride ldx >= H (a multiple of 8); out bf16 [m, H].
- *   saved (bf16 weights only, else NULL): NULL, or fp32 [2, m, I], 32-byte aligned, that receives
- *   g = x W1^T and u = x W3^T for moe_ffn_backward (fp32: rounded to bf16 they
- *   would be the largest error of the gradients).
+ *   saved, saved_h (bf16 weights only, else NULL; both or neither, 32-byte
+ *   aligned): with g = x W1^T and u = x W3^T, fp32 [2, m, I] that receives
+ *   act(g) and u act'(g), and bf16 [m, I] that receives h = act(g) u, for
+ *   moe_ffn_backward.  (fp32: rounded to bf16 they would be the largest error
+ *   of the gradients.)
  * The intermediate h is rounded to bf16 (MXFP4: to MXFP4, straight from the
  * fp32 products), x to MXFP4 for MXFP4 weights; sums are fp32. */
-MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, void* saved,
-                            void* workspace, size_t workspace_bytes, void* stream);
+MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, float* saved,
+                            void* saved_h, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of the block, given dout = dL/dout and what forward saved:
- *   dh = dout W2, dg = dh u act'(g), du = dh act(g), h = act(g) u (bf16 each)
+ *   dh = dout W2 (fp32), dg = dh u act'(g), du = dh act(g) (bf16)
  *   dx = dg W1 + du W3   dw1 = dg^T x   dw3 = du^T x   dw2 = dout^T h
  *   dout bf16 [m, H] with row stride ldd, x as in forward; dx bf16 [m, H];
  *   dw1, dw3 bf16 [I, H]; dw2 bf16 [H, I], all overwritten.  dx may be NULL,
@@ -92,7 +94,7 @@ MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int6
  * bf16 weights only (MOE_ERR_UNSUPPORTED otherwise).  m == 0 writes nothing:
  * weight gradients are then left as they are. */
 MOE_API int moe_ffn_backward(const moe_ffn* ffn, const void* dout, int64_t ldd, const void* x, int64_t ldx,
-                             const void* saved, int64_t m, void* dx, void* dw1, void* dw3, void* dw2,
+                             const float* saved, const void* saved_h, int64_t m, void* dx, void* dw1, void* dw3, void* dw2,
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Kernels the last successful call on `ffn` launched. */

@@ -117,8 +117,8 @@ def load_library(path: str | None = None, build: bool = True):
                                        ctypes.POINTER(_vp)]
         lib.moe_ffn_destroy.argtypes = [_vp]
         lib.moe_ffn_workspace_size.argtypes = [_vp, _i64, ctypes.c_int, ctypes.POINTER(sz)]
-        lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, sz, _vp]
-        lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
         lib.moe_ffn_last_launch_count.argtypes = [_vp]
         lib.moe_mxfp4_scales_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
         lib.moe_mxfp4_quant.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
@@ -612,7 +612,8 @@ class GatedFfn:
 
     def forward(self, x, save=False, out=None, stream=None):
         """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
-        (out, saved) for backward: saved fp32 [2, m, I] holds x w1^T and x w3^T."""
+        (out, saved) for backward: saved is (fp32 [2, m, I]: act(g) and u act'(g), bf16 [m, I]: h) with
+        g = x w1^T, u = x w3^T, h = act(g) u."""
         ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
         if out is None:
@@ -621,9 +622,10 @@ class GatedFfn:
             _dense(out, _BF16, (m, self.hidden), "out")
         if m > self._fits[0]:
             self.workspace(m, False, x.device)
-        saved = x.new_empty((2, m, self.inter), dtype=_F32) if save else None
+        saved = (x.new_empty((2, m, self.inter), dtype=_F32), x.new_empty((m, self.inter))) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
-                                      saved.data_ptr() if save else None, *self._ws_at, _on(x, stream))
+                                      saved[0].data_ptr() if save else None,
+                                      saved[1].data_ptr() if save else None, *self._ws_at, _on(x, stream))
         if rc:
             raise MoeError(rc, "moe_ffn_forward")
         return (out, saved) if save else out
@@ -635,15 +637,16 @@ class GatedFfn:
         ldd, ldx = _rows(dout, H, "dout"), _rows(x, H, "x")
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
-        _dense(saved, _F32, (2, m, I), "saved")
+        _dense(saved[0], _F32, (2, m, I), "saved[0]")
+        _dense(saved[1], _BF16, (m, I), "saved[1]")
         new = x.new_empty if m else x.new_zeros
         dx = new((m, H)) if need_dx else None
         dw1, dw3, dw2 = (new((I, H)), new((I, H)), new((H, I))) if need_dw else (None,) * 3
         if m > self._fits[1]:
             self.workspace(m, True, x.device)
         at = [None if t is None else t.data_ptr() for t in (dx, dw1, dw3, dw2)]
-        rc = self.lib.moe_ffn_backward(self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m, *at,
-                                       *self._ws_at, _on(x, stream))
+        rc = self.lib.moe_ffn_backward(self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved[0].data_ptr(),
+                                       saved[1].data_ptr(), m, *at, *self._ws_at, _on(x, stream))
         if rc:
             raise MoeError(rc, "moe_ffn_backward")
         return dx, dw1, dw3, dw2

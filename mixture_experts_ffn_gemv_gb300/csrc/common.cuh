@@ -161,6 +161,23 @@ __device__ __forceinline__ void store_row16(uint16_t* row, int col, int n, bool 
     if (col + 16 <= n) *reinterpret_cast<uint4*>(row + col + 8) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// 32 columns of an output row, of which n are in it (a multiple of 8).
+__device__ __forceinline__ void store_row32(uint16_t* row, int n, bool wide, const uint32_t (&o)[16]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = o[8 * v + i];
+        store_row16(row, 16 * v, n, wide, w);
+    }
+}
+// One 32-byte load (p 32-byte aligned).
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
 // ---- warp-private staged row stores (GEMM epilogues)
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");

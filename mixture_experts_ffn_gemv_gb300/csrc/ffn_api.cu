@@ -56,10 +56,11 @@ Layout layout(const moe_ffn* f, int64_t m, bool backward) {
         o.hq = take((size_t)m * I / 2);
         o.hs = take(scale_bytes(m, I));
     } else {
-        o.h = take((size_t)m * I * 2);
         if (backward) {
             o.dg = take((size_t)m * I * 2);
             o.du = take((size_t)m * I * 2);
+        } else {
+            o.h = take((size_t)m * I * 2);
         }
     }
     o.total = off;
@@ -108,19 +109,20 @@ FfnProduct& add(FfnProducts& p, int M, int N, int K, void* out) {
     return q;
 }
 
-int forward_bf16(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, void* saved,
-                 void* ws, cudaStream_t st) {
+int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out, float* saved,
+                 void* h, void* ws, cudaStream_t st) {
     const int H = f->cfg.hidden, I = f->cfg.inter;
     FfnProducts p = products(f, ws);
-    FfnProduct& gu = add(p, m, I, H, at<void>(ws, lo.h));
+    FfnProduct& gu = add(p, m, I, H, h);
     if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
     gu.b[0] = f->k1;
     gu.b[1] = f->k3;
-    p.save = static_cast<float*>(saved);
+    p.a = saved;
+    p.d = saved ? saved + (size_t)m * I : nullptr;
     if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
     FfnProducts d = products(f, ws);
     FfnProduct& y = add(d, m, H, I, out);
-    if (!ffn_map(&y.a[0], at<void>(ws, lo.h), m, I, I, 128)) return MOE_ERR_CUDA;
+    if (!ffn_map(&y.a[0], h, m, I, I, 128)) return MOE_ERR_CUDA;
     y.b[0] = f->k2;
     if (launch_ffn_products(d, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
     f->last_launches = 2;
@@ -139,14 +141,13 @@ NarrowProduct narrow(int T, int R, int K, void* ws) {
 
 // The block for few tokens: each kernel after the first streams its weights
 // while the one before drains.
-int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, void* saved,
-                   void* ws, cudaStream_t st) {
+int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, float* saved,
+                   void* h, void* ws, cudaStream_t st) {
     const int H = f->cfg.hidden, I = f->cfg.inter;
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
     NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
     uint8_t *xq = at<uint8_t>(ws, lo.xq), *xs = at<uint8_t>(ws, lo.xs), *hq = at<uint8_t>(ws, lo.hq),
             *hs = at<uint8_t>(ws, lo.hs);
-    void* h = at<void>(ws, lo.h);
     const uint32_t nt = (uint32_t)narrow_tokens(m);
     const bool ok = mx ? mx_code_map(&g.b, xq, m, H, nt) && mx_scale_map(&g.bs, xs, m, H) &&
                              mx_code_map(&d.b, hq, m, I, nt) && mx_scale_map(&d.bs, hs, m, I)
@@ -159,8 +160,8 @@ int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ld
     g.act = f->cfg.activation;
     g.early = mx;  // behind the quantiser
     g.out = static_cast<uint16_t*>(h);
-    g.g = static_cast<float*>(saved);
-    g.u = saved ? g.g + (size_t)m * I : nullptr;
+    g.sa = saved;
+    g.sd = saved ? saved + (size_t)m * I : nullptr;
     g.codes = hq;
     g.scales = hs;
     g.nkt = ceil_div(I, 128);
@@ -338,48 +339,50 @@ int moe_ffn_workspace_size(const moe_ffn* f, int64_t m, int backward, size_t* by
     return MOE_OK;
 }
 
-int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, void* out, void* saved, void* workspace,
-                    size_t workspace_bytes, void* stream) {
+int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, void* out, float* saved, void* saved_h,
+                    void* workspace, size_t workspace_bytes, void* stream) {
     Layout lo;
     const int rc = check_call(f, m, false, workspace, workspace_bytes, &lo);
     if (rc != MOE_OK || m == 0) return rc;
-    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 32)))
+    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || !saved != !saved_h ||
+        (saved && (!aligned(saved, 32) || !aligned(saved_h, 32))))
         return MOE_ERR_INVALID_ARG;
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
     if (mx && saved) return MOE_ERR_UNSUPPORTED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
-    if (m <= kNarrowTokens) return forward_narrow(f, lo, x, ldx, (int)m, out, saved, workspace, st);
+    void* h = saved ? saved_h : at<void>(workspace, lo.h);
+    if (m <= kNarrowTokens) return forward_narrow(f, lo, x, ldx, (int)m, out, saved, h, workspace, st);
     return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
-              : forward_bf16(f, lo, x, ldx, (int)m, out, saved, workspace, st);
+              : forward_bf16(f, x, ldx, (int)m, out, saved, h, workspace, st);
 }
 
-int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void* x, int64_t ldx, const void* saved,
-                     int64_t m, void* dx, void* dw1, void* dw3, void* dw2, void* workspace, size_t workspace_bytes,
-                     void* stream) {
+int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void* x, int64_t ldx, const float* saved,
+                     const void* saved_h, int64_t m, void* dx, void* dw1, void* dw3, void* dw2, void* workspace,
+                     size_t workspace_bytes, void* stream) {
     Layout lo;
     if (f && f->cfg.weights != MOE_WEIGHTS_BF16) return MOE_ERR_UNSUPPORTED;
     const int rc = check_call(f, m, true, workspace, workspace_bytes, &lo);
     if (rc != MOE_OK || m == 0) return rc;
     const int H = f->cfg.hidden, I = f->cfg.inter, n = (int)m;
     const bool dw = dw1 || dw3 || dw2;
-    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !aligned(saved, 32) || (dx && !aligned(dx, 16)) ||
+    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !saved_h || !aligned(saved, 32) ||
+        !aligned(saved_h, 32) || (dx && !aligned(dx, 16)) ||
         (dw && (!dw1 || !dw3 || !dw2 || !aligned(dw1, 16) || !aligned(dw3, 16) || !aligned(dw2, 16))))
         return MOE_ERR_INVALID_ARG;
     if (!dx && !dw) return MOE_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
-    void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du), *h = at<void>(workspace, lo.h);
-    // dh = dout W2 and, in its epilogue, dg, du and h
+    void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du);
+    // dh = dout W2 and, in its epilogue, dg and du
     FfnProducts p = products(f, workspace);
     FfnProduct& q = add(p, n, I, H, dg);
     if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
     q.b[0] = f->mn2;
     q.b_mn = 1;
-    p.g = static_cast<const float*>(saved);
-    p.u = p.g + (size_t)m * I;
+    p.a = const_cast<float*>(saved);
+    p.d = p.a + (size_t)m * I;
     p.out_du = static_cast<uint16_t*>(du);
-    p.out_h = static_cast<uint16_t*>(h);
     if (launch_ffn_products(p, EPI_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
     // the four products that need them, in one launch
     FfnProducts r = products(f, workspace);
@@ -394,7 +397,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     if (dw) {
         CUtensorMap mx, md, mdg, mdu, mh;
         if (!ffn_map(&mx, x, m, H, ldx, 64) || !ffn_map(&md, dout, m, H, ldd, 64) || !ffn_map(&mdg, dg, m, I, I, 64) ||
-            !ffn_map(&mdu, du, m, I, I, 64) || !ffn_map(&mh, h, m, I, I, 64))
+            !ffn_map(&mdu, du, m, I, I, 64) || !ffn_map(&mh, saved_h, m, I, I, 64))
             return MOE_ERR_CUDA;
         FfnProduct& g1 = add(r, I, H, n, dw1);
         g1.a[0] = mdg;

@@ -16,8 +16,8 @@ struct WsHeader;
 enum FfnEpilogue : int {
     EPI_STORE = 0,    // out = D
     EPI_GATEUP,       // D = (g, u) side by side: out = act(g) u
-    EPI_GATEUP_SAVE,  // ... and g, u themselves
-    EPI_DACT,         // D = dh: dg = dh u act'(g), du = dh act(g), h = act(g) u
+    EPI_GATEUP_SAVE,  // ... and a = act(g), d = u act'(g) for the backward pass
+    EPI_DACT,         // D = dh: out = dg = dh d, du = dh a
 };
 
 // One product D[M, N] = sum over one or two sources of A B^T, as a work list
@@ -38,10 +38,10 @@ struct FfnProducts {
     int count;
     int first[kMaxProducts + 1];  // first work item of each product
     int act;
-    float* save;            // EPI_GATEUP_SAVE: g, then u, [M, N] each
-    const float *g, *u;     // EPI_DACT: the same
-    uint16_t *out_du, *out_h;  // EPI_DACT (out: dg)
-    CUtensorMap sg, su, du, h;  // maps of these (set by launch_ffn_products)
+    // a = act(g) and d = u act'(g), fp32 [M, N]: written by EPI_GATEUP_SAVE, read by EPI_DACT
+    float *a, *d;
+    uint16_t* out_du;       // EPI_DACT (out: dg)
+    CUtensorMap sa, sd, du;  // maps of these (set by launch_ffn_products)
     WsHeader* hdr;
     uint64_t wait_ns;
 };
@@ -80,7 +80,7 @@ struct NarrowProduct {
     int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
     int act;
     uint16_t* out;            // bf16 [T, R]; gate/up of a bf16 block: h
-    float *g, *u;             // gate/up: saved pre-activations, or null
+    float *sa, *sd;           // gate/up: act(g) and u act'(g) for the backward pass, or null
     uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;

@@ -245,10 +245,12 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
         } else if (r < p.R) {
             const size_t at = t * p.R + r;
             if (GATEUP) {
-                p.out[at] = f32_to_bf16(glu(v0, v1, p.act));
-                if (p.g) {
-                    p.g[at] = v0;
-                    p.u[at] = v1;
+                float a, slope;
+                act_slope(v0, p.act, a, slope);
+                p.out[at] = f32_to_bf16(a * v1);
+                if (p.sa) {
+                    p.sa[at] = a;
+                    p.sd[at] = v1 * slope;
                 }
             } else {
                 p.out[at] = f32_to_bf16(v0);

@@ -8,13 +8,19 @@
 // backward products read W, x, dg and h as they lie, through MN-major
 // descriptors, so nothing is transposed in memory.
 //   warp 0      TMA producer: this CTA's 128 rows of A and half of the tile's
-//               256 rows of B, 64 of K per stage, 6 stages of 32 KB;
+//               256 rows of B, 64 of K per stage, 5 stages of 32 KB;
 //   warp 1      (leader) MMA issuer: M = 256, N = 256, fp32 accumulators in
 //               TMEM, two buffers of 256 columns; the whole warp walks the
 //               loop and one lane issues, so addresses are warp-uniform;
-//   warps 2..9  epilogue, two per TMEM lane quarter, each half of the columns;
-//               outputs leave through 4 KB of staging per warp and TMA stores,
-//               which write whole lines and clip at the matrix's edges.
+//   warps 2..   epilogue, 8 (plain products) or 16 (where there is an
+//               activation or its gradient to compute), an equal share of each
+//               TMEM lane quarter's columns; outputs leave through staging in
+//               shared memory and TMA stores, which write whole lines and clip
+//               at the matrix's edges.
+// A forward pass that is to be differentiated saves a = act(g), d = u act'(g) in
+// fp32 and h = a u in bf16, so that the backward pass multiplies (du = dh a,
+// dg = dh d) where it would recompute: its epilogue, with the activation in it,
+// took 202 us for 4096 x 8192 x 2048, three times the MMAs' time.
 // Gate/up: the leader's half of B is 128 rows of W1, the peer's the same rows
 // of W3, so a thread finds g and u of one element in its own lane.
 // Every wait is bounded; on expiry the CTA records DEV_ERR_TIMEOUT, stops
@@ -38,45 +44,29 @@ namespace {
 using namespace sm100;
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = 128 * BK * 2;  // per CTA
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+template <int EPI>
+struct Shape {
+    static constexpr int EPI_WARPS = EPI == EPI_STORE ? 8 : 16;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int STG_BYTES = 65536 / EPI_WARPS;  // per epilogue warp
+};
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 constexpr int STG_OFF = STAGES * STAGE_BYTES;
-constexpr int BAR_OFF = STG_OFF + EPI_WARPS * 4096;
+constexpr int BAR_OFF = STG_OFF + 65536;
 constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 
-// 32 rows x 32 fp32 of a matrix, whole lines per instruction: register i of a
-// lane is its 16 bytes of rows 4 i .. 4 i + 3.  Rows from m and columns from n
-// on read as zero.
-__device__ __forceinline__ void load_block(const float* p, int row0, int m, int col0, int n, int lane, uint4 (&v)[8]) {
-    const int col = col0 + 4 * (lane & 7);
+__device__ __forceinline__ void load_row32(const float* p, int n, float (&f)[32]) {  // n of 32, a multiple of 8
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = row0 + 4 * i + (lane >> 3);
-        v[i] = row < m && col < n ? ld_stream_v4(p + (size_t)row * n + col) : make_uint4(0, 0, 0, 0);
-    }
-}
-// ... turned round through the warp's staging: lane r gets row r.
-__device__ __forceinline__ void turn_block(uint32_t stg, const uint4 (&v)[8], int lane, float (&f)[32]) {
-    __syncwarp();
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[8] = {};
+        if (8 * i < n) ld_global_v8(p + 8 * i, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = 4 * i + (lane >> 3);
-        sts128(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint4 q = lds128(stg + lane * 128 + ((c ^ (lane & 7)) << 4));
-        f[4 * c] = __uint_as_float(q.x);
-        f[4 * c + 1] = __uint_as_float(q.y);
-        f[4 * c + 2] = __uint_as_float(q.z);
-        f[4 * c + 3] = __uint_as_float(q.w);
+        for (int k = 0; k < 8; ++k) f[8 * i + k] = __uint_as_float(w[k]);
     }
 }
 // One row segment of 128 bytes per lane out by TMA: a box at (col, row0).
@@ -106,7 +96,8 @@ __device__ __forceinline__ Item item_of(const FfnProducts& p, int t) {
 }
 
 template <int EPI>
-__global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
+__global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
+    constexpr int EPI_WARPS = Shape<EPI>::EPI_WARPS;
     constexpr bool GATEUP = EPI == EPI_GATEUP || EPI == EPI_GATEUP_SAVE;
     pdl_wait();
     pdl_trigger();
@@ -251,22 +242,19 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
         __syncwarp();
     } else {
         const int q4 = warp & 3;           // the TMEM lane quarter this warp may read
-        const int half = (warp - 2) >> 2;  // which half of the tile's columns
-        const uint32_t stg = sbase + STG_OFF + (warp - 2) * 4096;
+        const int part = (warp - 2) >> 2;  // its share of the tile's columns
+        const uint32_t stg = sbase + STG_OFF + (warp - 2) * Shape<EPI>::STG_BYTES;
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
             if (*abort_flag) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
             const int row0 = w.mt * 256 + (int)rank * BM + q4 * 32;  // first of this warp's rows of D
-            const bool any = row0 < q.M;
             const int N = q.N;
-            const int col0 = GATEUP ? w.nt * 128 + half * 64 : w.nt * 256 + half * 128;  // ... columns of the output
-            uint4 gl[8], ul[8];  // EPI_DACT: the next 32 columns of g and u on their way
-            if (EPI == EPI_DACT && any && col0 < N) {
-                load_block(p.g, row0, q.M, col0, N, lane, gl);
-                load_block(p.u, row0, q.M, col0, N, lane, ul);
-            }
+            // first of its columns of the output
+            const int col0 = GATEUP ? w.nt * 128 + part * 32 : w.nt * 256 + part * (1024 / EPI_WARPS);
+            const bool ok = row0 + lane < q.M;
+            const size_t at = (size_t)(row0 + lane) * N + col0;
             const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
             if (!mbar_wait_cluster(tfull0 + 8 * acc, aph, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 23);
@@ -275,83 +263,85 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_products(const __grid_constant
             }
             tc_fence_after();
             const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16) + acc * BN;
-            if (!any || col0 >= N) {
-                // nothing of the tile in the matrix
+            const uint32_t tempty = lead_tempty0 + 8 * acc;
+            const auto release = [&] {  // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty);
+            };
+            if (row0 >= q.M || col0 >= N) {  // nothing of the tile in the matrix
+                release();
             } else if (GATEUP) {
-                uint32_t o[32];
+                uint32_t gv[32], uv[32], o[16];
+                tmem_ld32(taddr + 32 * part, gv);
+                tmem_ld32(taddr + 128 + 32 * part, uv);
+                tmem_wait_ld();
+                release();
+                if (EPI == EPI_GATEUP_SAVE) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t gv[32], uv[32];
-                    tmem_ld32(taddr + 64 * half + 32 * j, gv);
-                    tmem_ld32(taddr + 128 + 64 * half + 32 * j, uv);
-                    tmem_wait_ld();
+                    for (int i = 0; i < 32; ++i) {
+                        const float u = __uint_as_float(uv[i]);
+                        float a, slope;
+                        act_slope(__uint_as_float(gv[i]), p.act, a, slope);
+                        gv[i] = __float_as_uint(a);
+                        uv[i] = __float_as_uint(u * slope);
+                        const float h = a * u;
+                        if (i & 1) o[i >> 1] = pack_bf16x2(__uint_as_float(o[i >> 1]), h);
+                        else o[i >> 1] = __float_as_uint(h);
+                    }
+                    put_block(&p.sa, stg, gv, lane, col0, row0);
+                    put_block(&p.sd, stg, uv, lane, col0, row0);
+                } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        o[16 * j + i] = pack_bf16x2(glu(__uint_as_float(gv[2 * i]), __uint_as_float(uv[2 * i]), p.act),
-                                                    glu(__uint_as_float(gv[2 * i + 1]), __uint_as_float(uv[2 * i + 1]), p.act));
-                    if (EPI == EPI_GATEUP_SAVE && col0 + 32 * j < N) {
-                        put_block(&p.sg, stg, gv, lane, col0 + 32 * j, row0);
-                        put_block(&p.su, stg, uv, lane, col0 + 32 * j, row0);
-                    }
+                        o[i] = pack_bf16x2(glu(__uint_as_float(gv[2 * i]), __uint_as_float(uv[2 * i]), p.act),
+                                           glu(__uint_as_float(gv[2 * i + 1]), __uint_as_float(uv[2 * i + 1]), p.act));
                 }
-                put_block(&q.o, stg, o, lane, col0, row0);
+                if (ok) store_row32(q.out + at, N - col0, (N & 15) == 0, o);
             } else if (EPI == EPI_DACT) {
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    if (col0 + 64 * j >= N) break;
-                    uint32_t og[32], ou[32], oh[32];
+                uint32_t dv[2][32], o[32];
+                tmem_ld32(taddr + 64 * part, dv[0]);
+                tmem_ld32(taddr + 64 * part + 32, dv[1]);
+                tmem_wait_ld();
+                release();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float* src = (x ? p.d : p.a) + at;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        uint32_t dv[32];
-                        tmem_ld32(taddr + 128 * half + 64 * j + 32 * e, dv);
-                        float g[32], u[32];
-                        if (lane == 0) tma_store_wait_read();  // the staging may still be going out
-                        turn_block(stg, gl, lane, g);
-                        turn_block(stg, ul, lane, u);
-                        const int next = col0 + 64 * j + 32 * e + 32;
-                        if (next < col0 + 128 && next < N) {
-                            load_block(p.g, row0, q.M, next, N, lane, gl);
-                            load_block(p.u, row0, q.M, next, N, lane, ul);
-                        }
-                        tmem_wait_ld();
+                        float f[32];
+                        load_row32(src + 32 * e, ok ? N - col0 - 32 * e : 0, f);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float r[2][3];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float dh = __uint_as_float(dv[2 * i + k]);
-                                float a, slope;
-                                act_slope(g[2 * i + k], p.act, a, slope);
-                                r[k][0] = dh * u[2 * i + k] * slope;
-                                r[k][1] = dh * a;
-                                r[k][2] = a * u[2 * i + k];
-                            }
-                            og[16 * e + i] = pack_bf16x2(r[0][0], r[1][0]);
-                            ou[16 * e + i] = pack_bf16x2(r[0][1], r[1][1]);
-                            oh[16 * e + i] = pack_bf16x2(r[0][2], r[1][2]);
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            o[16 * e + i] = pack_bf16x2(__uint_as_float(dv[e][2 * i]) * f[2 * i],
+                                                        __uint_as_float(dv[e][2 * i + 1]) * f[2 * i + 1]);
                     }
-                    put_block(&q.o, stg, og, lane, col0 + 64 * j, row0);
-                    put_block(&p.du, stg, ou, lane, col0 + 64 * j, row0);
-                    put_block(&p.h, stg, oh, lane, col0 + 64 * j, row0);
+                    put_block(x ? &q.o : &p.du, stg, o, lane, col0, row0);
                 }
             } else {
+                uint32_t o[2][32];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    if (col0 + 64 * j >= N) break;
-                    uint32_t v[2][32], o[32];
-                    tmem_ld32(taddr + 128 * half + 64 * j, v[0]);
-                    tmem_ld32(taddr + 128 * half + 64 * j + 32, v[1]);
+                    uint32_t v[2][32];
+                    tmem_ld32(taddr + 128 * part + 64 * j, v[0]);
+                    tmem_ld32(taddr + 128 * part + 64 * j + 32, v[1]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        o[i] = pack_bf16x2(__uint_as_float(v[i >> 4][(2 * i) & 31]), __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
-                    put_block(&q.o, stg, o, lane, col0 + 64 * j, row0);
+                        o[j][i] = pack_bf16x2(__uint_as_float(v[i >> 4][(2 * i) & 31]), __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
+                }
+                release();
+                if (lane == 0) tma_store_wait_read();
+                __syncwarp();
+                stage_row128(stg, o[0], lane);
+                stage_row128(stg + 4096, o[1], lane);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&q.o, col0, row0, stg);
+                    if (col0 + 64 < N) tma_store_2d(&q.o, col0 + 64, row0, stg + 4096);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(lead_tempty0 + 8 * acc);
         }
         if (lane == 0) tma_store_wait();
     }
@@ -377,7 +367,7 @@ cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
     const int pairs = std::max(1, std::min(sms() / 2, p.first[p.count]));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Shape<EPI>::THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -410,11 +400,9 @@ cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
         if (!ffn_map(&q.o, q.out, q.M, q.N, q.N, 32)) return cudaErrorUnknown;
     }
     const uint64_t M = p.p[0].M, N = p.p[0].N, dims[2] = {N, M};
-    if (epilogue == EPI_GATEUP_SAVE && (!tmap_encode(&p.sg, p.save, 2, dims, 4, 32, 32) ||
-                                        !tmap_encode(&p.su, p.save + M * N, 2, dims, 4, 32, 32)))
+    if (epilogue == EPI_GATEUP_SAVE && (!tmap_encode(&p.sa, p.a, 2, dims, 4, 32, 32) || !tmap_encode(&p.sd, p.d, 2, dims, 4, 32, 32)))
         return cudaErrorUnknown;
-    if (epilogue == EPI_DACT && (!ffn_map(&p.du, p.out_du, M, N, N, 32) || !ffn_map(&p.h, p.out_h, M, N, N, 32)))
-        return cudaErrorUnknown;
+    if (epilogue == EPI_DACT && !ffn_map(&p.du, p.out_du, M, N, N, 32)) return cudaErrorUnknown;
     switch (epilogue) {
         case EPI_GATEUP: return launch<EPI_GATEUP>(p, st);
         case EPI_GATEUP_SAVE: return launch<EPI_GATEUP_SAVE>(p, st);

@@ -186,9 +186,14 @@ def test_forward(B, m, H, I, kind):
     _within(out, P.forward(x, *w, kind), P.forward_bound(x, *w, kind))
     out2, saved = blk.forward(x, save=True)
     assert torch.equal(out, out2)
-    for s, t in zip(saved, w[:2]):
-        ref = x.double() @ t.double().T
-        _within(s, ref, H * P.F32 * (x.double().abs() @ t.double().abs().T))
+    g, u = (x.double() @ v.double().T for v in w[:2])
+    eg, eu = (H * P.F32 * (x.double().abs() @ v.double().abs().T) for v in w[:2])
+    a, s = P.act_slope(g, kind)
+    ea, es = P.SLOPE * eg + 2.0 ** -20 * a.abs(), P.CURVE * eg + 2.0 ** -20
+    _within(saved[0][0], a, ea)
+    _within(saved[0][1], u * s, u.abs() * es + eu * s.abs() + eu * es + 2.0 ** -22 * (u * s).abs())
+    eh = a.abs() * eu + ea * u.abs() + ea * eu + 2.0 ** -22 * (a * u).abs()
+    _within(saved[1], a * u, eh + P.HALF * ((a * u).abs() + eh))
     assert blk.device_status() == 0
 
 
@@ -309,7 +314,7 @@ def test_graph_capture_and_other_streams(B):
     blk = B.GatedFfn(*w)
     x, dout = _n(22, m, H), _n(23, m, H)
     blk.forward(x, save=True)
-    blk.backward(dout, x, torch.zeros(2, m, I, device="cuda"))  # the workspace exists
+    blk.workspace(m, True, x.device)  # exists before the capture
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
@@ -322,7 +327,7 @@ def test_graph_capture_and_other_streams(B):
         torch.cuda.synchronize()
         e_out, e_saved = blk.forward(x, save=True)
         e_grads = blk.backward(dout, x, e_saved)
-        assert torch.equal(out, e_out) and all(torch.equal(a, b) for a, b in zip(grads, e_grads))
+        assert torch.equal(out, e_out) and torch.equal(saved[0], e_saved[0]) and all(torch.equal(a, b) for a, b in zip(grads, e_grads))
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
     s_out = blk.forward(x, stream=st)
@@ -336,10 +341,10 @@ def test_repeatable(B):
     blk = B.GatedFfn(*w)
     x, dout = _n(42, m, H), _n(43, m, H)
     out, saved = blk.forward(x, save=True)
-    first = (out, saved, *blk.backward(dout, x, saved))
+    first = (out, *saved, *blk.backward(dout, x, saved))
     for _ in range(3):
         o, s = blk.forward(x, save=True)
-        assert all(torch.equal(a, b) for a, b in zip(first, (o, s, *blk.backward(dout, x, s))))
+        assert all(torch.equal(a, b) for a, b in zip(first, (o, *s, *blk.backward(dout, x, s))))
 
 
 def test_refusals(B):
@@ -356,7 +361,7 @@ def test_refusals(B):
     with pytest.raises(ValueError):
         blk.backward(x[:5], x, saved)
     with pytest.raises(ValueError):
-        blk.backward(x, x, saved[:, :5])
+        blk.backward(x, x, (saved[0][:, :5], saved[1]))
     with pytest.raises(ValueError):
         B.GatedFfn(w1, w3, w2.T)
     with pytest.raises(ValueError):
@@ -373,9 +378,10 @@ def test_refusals(B):
     lib, p = B.load_library(), B._p
     ws = blk.workspace(10, True, x.device)
     out = torch.empty_like(x)
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), None, p(ws), 256, None) == B.MOE_ERR_WORKSPACE
-    assert lib.moe_ffn_forward(blk.handle, p(x), H - 8, 10, p(out), None, p(ws), ws.numel(), None) == 1
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, -1, p(out), None, p(ws), ws.numel(), None) == 1
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, 1 << 30, p(out), None, p(ws), ws.numel(), None) == 2
-    assert lib.moe_ffn_backward(blk.handle, p(x), H, p(x), H, p(saved), 10, p(out), p(w1), None, None, p(ws),
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), None, None, p(ws), 256, None) == B.MOE_ERR_WORKSPACE
+    assert lib.moe_ffn_forward(blk.handle, p(x), H - 8, 10, p(out), None, None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), p(saved[0]), None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, -1, p(out), None, None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 1 << 30, p(out), None, None, p(ws), ws.numel(), None) == 2
+    assert lib.moe_ffn_backward(blk.handle, p(x), H, p(x), H, p(saved[0]), p(saved[1]), 10, p(out), p(w1), None, None, p(ws),
                                 ws.numel(), None) == 1
