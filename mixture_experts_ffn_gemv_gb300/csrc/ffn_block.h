@@ -30,7 +30,7 @@ struct FfnProduct {
     int m_tiles, n_tiles;
     int M, N;
     uint16_t* out;           // [M, N], row stride N
-    CUtensorMap o;           // ... in boxes of 64 columns x 32 rows (set by launch_ffn_products)
+    CUtensorMap o;           // ... of a plain product, in boxes of 64 columns x 32 rows (set by launch_ffn_products)
 };
 constexpr int kMaxProducts = 4;
 struct FfnProducts {
@@ -41,13 +41,14 @@ struct FfnProducts {
     // a = act(g) and d = u act'(g), fp32 [M, N]: written by EPI_GATEUP_SAVE, read by EPI_DACT
     float *a, *d;
     uint16_t* out_du;       // EPI_DACT (out: dg)
-    CUtensorMap sa, sd, du;  // maps of these (set by launch_ffn_products)
     WsHeader* hdr;
     uint64_t wait_ns;
 };
 
-// Maps of a bf16 operand [rows, cols] (row stride ld elements).  K-major: 64 of
-// K x box_rows rows; MN-major: 64 of M x 64 rows of K.
+// Maps of a bf16 operand [rows, cols] (row stride ld elements), all even.
+// K-major: 64 of K x box_rows rows; MN-major: 64 of M x 64 rows of K.  The
+// maps count 32-bit words (coordinates along a row are halves): boxes of a
+// 16-bit type arrive more slowly (32 KB per SM in 712 cycles, as words 616).
 bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
 
 cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st);

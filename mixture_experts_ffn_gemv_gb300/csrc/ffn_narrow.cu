@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
             const auto weights = [&](int ks, uint32_t s) {
                 const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
                 mbar_arrive_expect_tx(bar, ss.bytes);
-                const int c = MX ? 128 : 64;  // elements of the map per 128 bytes of K
+                const int c = MX ? 128 : 32;  // elements of the map per 128 bytes of K
                 const int kc = (GATEUP ? ks : 2 * ks) * c;
                 tma_load_2d(st, &p.a[0], kc, row0, bar);
                 tma_load_2d(st + TILE, &p.a[GATEUP ? 1 : 0], GATEUP ? kc : kc + c, row0, bar);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
             };
             const auto tokens = [&](int ks, uint32_t s) {
                 const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
-                const int c = MX ? 128 : 64;
+                const int c = MX ? 128 : 32;
                 const int kc = (GATEUP ? ks : 2 * ks) * c;
                 tma_load_2d(st + ss.tok, &p.b, kc, tok0, bar);
                 if (!GATEUP) tma_load_2d(st + ss.tok + p.nt * 128, &p.b, kc + c, tok0, bar);

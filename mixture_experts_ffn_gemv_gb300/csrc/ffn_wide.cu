@@ -8,15 +8,16 @@
 // backward products read W, x, dg and h as they lie, through MN-major
 // descriptors, so nothing is transposed in memory.
 //   warp 0      TMA producer: this CTA's 128 rows of A and half of the tile's
-//               256 rows of B, 64 of K per stage, 5 stages of 32 KB;
+//               256 rows of B, 64 of K per stage of 32 KB, 6 or 7 stages;
 //   warp 1      (leader) MMA issuer: M = 256, N = 256, fp32 accumulators in
 //               TMEM, two buffers of 256 columns; the whole warp walks the
 //               loop and one lane issues, so addresses are warp-uniform;
 //   warps 2..   epilogue, 8 (plain products) or 16 (where there is an
 //               activation or its gradient to compute), an equal share of each
-//               TMEM lane quarter's columns; outputs leave through staging in
-//               shared memory and TMA stores, which write whole lines and clip
-//               at the matrix's edges.
+//               TMEM lane quarter's columns.  A plain product's output leaves
+//               through staging in shared memory and TMA stores, which write
+//               whole lines and clip at the matrix's edges; the others store
+//               32 bytes at a time from the lanes and keep the seventh stage.
 // A forward pass that is to be differentiated saves a = act(g), d = u act'(g) in
 // fp32 and h = a u in bf16, so that the backward pass multiplies (du = dh a,
 // dg = dh d) where it would recompute: its epilogue, with the activation in it,
@@ -44,23 +45,23 @@ namespace {
 using namespace sm100;
 
 constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BK * 2, B_BYTES = 128 * BK * 2;  // per CTA
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int TMEM_COLS = 2 * BN;
+constexpr uint64_t DRAIN_NS = 2000000000ull;
 template <int EPI>
 struct Shape {
     static constexpr int EPI_WARPS = EPI == EPI_STORE ? 8 : 16;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr int STG_BYTES = 65536 / EPI_WARPS;  // per epilogue warp
+    static constexpr int STAGES = EPI == EPI_STORE ? 6 : 7;
+    static constexpr int STG_OFF = STAGES * STAGE_BYTES;  // staging of a plain product: 4 KB per epilogue warp
+    static constexpr int BAR_OFF = STG_OFF + (EPI == EPI_STORE ? EPI_WARPS * 4096 : 0);
+    static constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
+    static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 };
-constexpr uint64_t DRAIN_NS = 2000000000ull;
-constexpr int STG_OFF = STAGES * STAGE_BYTES;
-constexpr int BAR_OFF = STG_OFF + 65536;
-constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
-static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 
-__device__ __forceinline__ void load_row32(const float* p, int n, float (&f)[32]) {  // n of 32, a multiple of 8
+// n of 32 fp32 of a row (n a multiple of 8; the rest zero), and the way back.
+__device__ __forceinline__ void load_row32(const float* p, int n, float (&f)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[8] = {};
@@ -69,15 +70,14 @@ __device__ __forceinline__ void load_row32(const float* p, int n, float (&f)[32]
         for (int k = 0; k < 8; ++k) f[8 * i + k] = __uint_as_float(w[k]);
     }
 }
-// One row segment of 128 bytes per lane out by TMA: a box at (col, row0).
-__device__ __forceinline__ void put_block(const CUtensorMap* m, uint32_t stg, const uint32_t (&v)[32], int lane, int col,
-                                          int row0) {
-    if (lane == 0) tma_store_wait_read();
-    __syncwarp();
-    stage_row128(stg, v, lane);
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) tma_store_2d(m, col, row0, stg);
+__device__ __forceinline__ void store_row32f(float* p, int n, const uint32_t (&f)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = f[8 * i + k];
+        if (8 * i < n) st_global_v8(p + 8 * i, w);
+    }
 }
 
 struct Item {
@@ -97,7 +97,7 @@ __device__ __forceinline__ Item item_of(const FfnProducts& p, int t) {
 
 template <int EPI>
 __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
-    constexpr int EPI_WARPS = Shape<EPI>::EPI_WARPS;
+    constexpr int EPI_WARPS = Shape<EPI>::EPI_WARPS, STAGES = Shape<EPI>::STAGES, BAR_OFF = Shape<EPI>::BAR_OFF;
     constexpr bool GATEUP = EPI == EPI_GATEUP || EPI == EPI_GATEUP_SAVE;
     pdl_wait();
     pdl_trigger();
@@ -162,16 +162,16 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                         const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES, bar = lead_full0 + 8 * s;
                         if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * STAGE_BYTES);
                         if (q.a_mn) {
-                            tma_load_2d_pair(sa, ma, m0, kb * BK, bar);
-                            tma_load_2d_pair(sa + A_BYTES / 2, ma, m0 + 64, kb * BK, bar);
+                            tma_load_2d_pair(sa, ma, m0 / 2, kb * BK, bar);
+                            tma_load_2d_pair(sa + A_BYTES / 2, ma, m0 / 2 + 32, kb * BK, bar);
                         } else {
-                            tma_load_2d_pair(sa, ma, kb * BK, m0, bar);
+                            tma_load_2d_pair(sa, ma, kb * BK / 2, m0, bar);
                         }
                         if (q.b_mn) {
-                            tma_load_2d_pair(sb, mb, n0, kb * BK, bar);
-                            tma_load_2d_pair(sb + B_BYTES / 2, mb, n0 + 64, kb * BK, bar);
+                            tma_load_2d_pair(sb, mb, n0 / 2, kb * BK, bar);
+                            tma_load_2d_pair(sb + B_BYTES / 2, mb, n0 / 2 + 32, kb * BK, bar);
                         } else {
-                            tma_load_2d_pair(sb, mb, kb * BK, n0, bar);
+                            tma_load_2d_pair(sb, mb, kb * BK / 2, n0, bar);
                         }
                     }
                 }
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
     } else {
         const int q4 = warp & 3;           // the TMEM lane quarter this warp may read
         const int part = (warp - 2) >> 2;  // its share of the tile's columns
-        const uint32_t stg = sbase + STG_OFF + (warp - 2) * Shape<EPI>::STG_BYTES;
+        const uint32_t stg = sbase + Shape<EPI>::STG_OFF + (warp - 2) * 4096;
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
             if (*abort_flag) break;
@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                         if (i & 1) o[i >> 1] = pack_bf16x2(__uint_as_float(o[i >> 1]), h);
                         else o[i >> 1] = __float_as_uint(h);
                     }
-                    put_block(&p.sa, stg, gv, lane, col0, row0);
-                    put_block(&p.sd, stg, uv, lane, col0, row0);
+                    if (ok) {
+                        store_row32f(p.a + at, N - col0, gv);
+                        store_row32f(p.d + at, N - col0, uv);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -299,25 +301,26 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                 }
                 if (ok) store_row32(q.out + at, N - col0, (N & 15) == 0, o);
             } else if (EPI == EPI_DACT) {
-                uint32_t dv[2][32], o[32];
+                uint32_t dv[2][32];
                 tmem_ld32(taddr + 64 * part, dv[0]);
                 tmem_ld32(taddr + 64 * part + 32, dv[1]);
                 tmem_wait_ld();
                 release();
+                if (!ok) continue;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float* src = (x ? p.d : p.a) + at;
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int x = 0; x < 2; ++x) {
+                        const int n = N - col0 - 32 * e;
                         float f[32];
-                        load_row32(src + 32 * e, ok ? N - col0 - 32 * e : 0, f);
+                        uint32_t o[16];
+                        load_row32((x ? p.d : p.a) + at + 32 * e, n, f);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            o[16 * e + i] = pack_bf16x2(__uint_as_float(dv[e][2 * i]) * f[2 * i],
-                                                        __uint_as_float(dv[e][2 * i + 1]) * f[2 * i + 1]);
+                            o[i] = pack_bf16x2(__uint_as_float(dv[e][2 * i]) * f[2 * i],
+                                               __uint_as_float(dv[e][2 * i + 1]) * f[2 * i + 1]);
+                        store_row32((x ? q.out : p.out_du) + at + 32 * e, n, (N & 15) == 0, o);
                     }
-                    put_block(x ? &q.o : &p.du, stg, o, lane, col0, row0);
-                }
             } else {
                 uint32_t o[2][32];
 #pragma unroll
@@ -331,15 +334,15 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                         o[j][i] = pack_bf16x2(__uint_as_float(v[i >> 4][(2 * i) & 31]), __uint_as_float(v[i >> 4][(2 * i + 1) & 31]));
                 }
                 release();
-                if (lane == 0) tma_store_wait_read();
-                __syncwarp();
-                stage_row128(stg, o[0], lane);
-                stage_row128(stg + 4096, o[1], lane);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tma_store_2d(&q.o, col0, row0, stg);
-                    if (col0 + 64 < N) tma_store_2d(&q.o, col0 + 64, row0, stg + 4096);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (col0 + 64 * j >= N) break;
+                    if (lane == 0) tma_store_wait_read();
+                    __syncwarp();
+                    stage_row128(stg, o[j], lane);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&q.o, col0 / 2 + 32 * j, row0, stg);
                 }
             }
         }
@@ -362,13 +365,13 @@ int sms() {
 template <int EPI>
 cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
     static cudaError_t attr =
-        cudaFuncSetAttribute(ffn_products<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        cudaFuncSetAttribute(ffn_products<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<EPI>::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     const int pairs = std::max(1, std::min(sms() / 2, p.first[p.count]));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(Shape<EPI>::THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.dynamicSmemBytes = Shape<EPI>::SMEM_BYTES;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -385,8 +388,8 @@ cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
 }  // namespace
 
 bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
-    const uint64_t dims[2] = {cols, rows};
-    return tmap_encode(m, p, 2, dims, 2, BK, box_rows, true, ld);
+    const uint64_t dims[2] = {cols / 2, rows};
+    return tmap_encode(m, p, 2, dims, 4, BK / 2, box_rows, true, ld / 2);
 }
 
 cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
@@ -397,12 +400,8 @@ cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
         q.m_tiles = ceil_div(q.M, 256);
         q.n_tiles = ceil_div(q.N, bn);
         p.first[i + 1] = p.first[i] + q.m_tiles * q.n_tiles;
-        if (!ffn_map(&q.o, q.out, q.M, q.N, q.N, 32)) return cudaErrorUnknown;
+        if (epilogue == EPI_STORE && !ffn_map(&q.o, q.out, q.M, q.N, q.N, 32)) return cudaErrorUnknown;
     }
-    const uint64_t M = p.p[0].M, N = p.p[0].N, dims[2] = {N, M};
-    if (epilogue == EPI_GATEUP_SAVE && (!tmap_encode(&p.sa, p.a, 2, dims, 4, 32, 32) || !tmap_encode(&p.sd, p.d, 2, dims, 4, 32, 32)))
-        return cudaErrorUnknown;
-    if (epilogue == EPI_DACT && !ffn_map(&p.du, p.out_du, M, N, N, 32)) return cudaErrorUnknown;
     switch (epilogue) {
         case EPI_GATEUP: return launch<EPI_GATEUP>(p, st);
         case EPI_GATEUP_SAVE: return launch<EPI_GATEUP_SAVE>(p, st);

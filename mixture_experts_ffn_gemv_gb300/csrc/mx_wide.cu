@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
                     stage_row128(stg, o[GATEUP ? 0 : c], lane);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) tma_store_2d(&p.o, col, r, stg);
+                    if (lane == 0) tma_store_2d(&p.o, col / 2, r, stg);
                 }
             }
         }
@@ -352,19 +352,18 @@ bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, u
     const uint64_t dims[2] = {k / 2, rows};
     return tmap_encode(m, codes, 2, dims, 1, BKB, box_rows);
 }
-// Packed scales as [row tiles][K tiles][256 x 16 bits]: boxes of two K tiles of
+// Packed scales as [row tiles][K tiles][128 words]: boxes of two K tiles of
 // one row tile (tiles past the end read as zero: scale 2^-127 on zero codes).
 bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k) {
-    const uint64_t dims[3] = {256, (k + 127) / 128, (rows + 127) / 128};
-    return tmap_encode(m, scales, 3, dims, 2, 256, 2, false);
+    const uint64_t dims[3] = {128, (k + 127) / 128, (rows + 127) / 128};
+    return tmap_encode(m, scales, 3, dims, 4, 128, 2, false);
 }
 
 cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st) {
     p.m_tiles = ceil_div(p.M, 256);
     p.n_tiles = ceil_div(p.N, gateup ? 128 : 256);
     if (!gateup) {
-        const uint64_t dims[2] = {(uint64_t)p.N, (uint64_t)p.M};
-        if (!tmap_encode(&p.o, p.out, 2, dims, 2, 64, 32)) return cudaErrorUnknown;
+        if (!ffn_map(&p.o, p.out, p.M, p.N, p.N, 32)) return cudaErrorUnknown;
     }
     return gateup ? launch<true>(p, st) : launch<false>(p, st);
 }

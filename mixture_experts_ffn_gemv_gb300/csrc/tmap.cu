@@ -37,7 +37,7 @@ bool tmap_encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
     for (int i = 0; i < rank; ++i) gdim[i] = dims[i];
     gstride[0] = (ld ? ld : dims[0]) * esize;
     if (rank == 3) gstride[1] = dims[0] * dims[1] * esize;
-    const CUtensorMapDataType type = esize == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+    const CUtensorMapDataType type = esize == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
                                      : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUresult r = fn(m, type,

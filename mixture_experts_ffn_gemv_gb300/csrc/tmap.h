@@ -8,7 +8,7 @@
 namespace moe {
 
 // Row-major tensor of `rank` (2 or 3) dims, dims[0] innermost, elements of
-// esize bytes (4 = fp32, 2 = bf16 / f16, 1 = byte codes); box of box_cols x box_rows
+// esize bytes (4 = words, 2 = bf16 / f16, 1 = byte codes); box of box_cols x box_rows
 // (x 1); 128-byte swizzle unless swizzle is false (the box then lands densely,
 // row after row); rank 2: rows ld elements apart (0: dense).  Out-of-range
 // elements read as zero.
