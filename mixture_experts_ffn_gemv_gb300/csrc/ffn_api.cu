@@ -18,8 +18,9 @@ struct moe_ffn {
     int device;
     mutable int last_launches;
     mutable const void* last_ws;  // its header is known to be clean
-    // maps of the weights: along K (128-row boxes), along M or N (64 x 64), MXFP4 codes and scales
+    // maps of the weights: along K (128-row boxes), along M or N, MXFP4 codes and scales
     CUtensorMap k1, k3, k2, mn1, mn3, mn2;
+    int mn13_order, mn2_order;
     CUtensorMap s1, s3, s2;
 };
 
@@ -317,8 +318,10 @@ int moe_ffn_create(const moe_ffn_config* cfg, const moe_ffn_weights* w, moe_ffn*
                              mx_code_map(&f->k2, w->w2, H, I, 128) && mx_scale_map(&f->s1, w->s1, I, H) &&
                              mx_scale_map(&f->s3, w->s3, I, H) && mx_scale_map(&f->s2, w->s2, H, I)
                        : ffn_map(&f->k1, w->w1, I, H, H, 128) && ffn_map(&f->k3, w->w3, I, H, H, 128) &&
-                             ffn_map(&f->k2, w->w2, H, I, I, 128) && ffn_map(&f->mn1, w->w1, I, H, H, 64) &&
-                             ffn_map(&f->mn3, w->w3, I, H, H, 64) && ffn_map(&f->mn2, w->w2, H, I, I, 64);
+                             ffn_map(&f->k2, w->w2, H, I, I, 128) &&
+                             (f->mn13_order = ffn_map_mn(&f->mn1, w->w1, I, H, H)) &&
+                             ffn_map_mn(&f->mn3, w->w3, I, H, H) == f->mn13_order &&
+                             (f->mn2_order = ffn_map_mn(&f->mn2, w->w2, H, I, I));
     if (!ok) {
         delete f;
         return MOE_ERR_CUDA;
@@ -379,7 +382,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     FfnProduct& q = add(p, n, I, H, dg);
     if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
     q.b[0] = f->mn2;
-    q.b_mn = 1;
+    q.b_mn = f->mn2_order;
     p.a = const_cast<float*>(saved);
     p.d = p.a + (size_t)m * I;
     p.out_du = static_cast<uint16_t*>(du);
@@ -392,23 +395,18 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
         if (!ffn_map(&d.a[0], dg, m, I, I, 128) || !ffn_map(&d.a[1], du, m, I, I, 128)) return MOE_ERR_CUDA;
         d.b[0] = f->mn1;
         d.b[1] = f->mn3;
-        d.b_mn = 1;
+        d.b_mn = f->mn13_order;
     }
     if (dw) {
-        CUtensorMap mx, md, mdg, mdu, mh;
-        if (!ffn_map(&mx, x, m, H, ldx, 64) || !ffn_map(&md, dout, m, H, ldd, 64) || !ffn_map(&mdg, dg, m, I, I, 64) ||
-            !ffn_map(&mdu, du, m, I, I, 64) || !ffn_map(&mh, saved_h, m, I, I, 64))
-            return MOE_ERR_CUDA;
-        FfnProduct& g1 = add(r, I, H, n, dw1);
-        g1.a[0] = mdg;
-        g1.b[0] = mx;
-        FfnProduct& g3 = add(r, I, H, n, dw3);
-        g3.a[0] = mdu;
-        g3.b[0] = mx;
-        FfnProduct& g2 = add(r, H, I, n, dw2);
-        g2.a[0] = md;
-        g2.b[0] = mh;
-        for (FfnProduct* g : {&g1, &g3, &g2}) g->a_mn = g->b_mn = 1;
+        // dw1 = dg^T x, dw3 = du^T x, dw2 = dout^T h
+        const void* lhs[3] = {dg, du, dout};
+        void* out[3] = {dw1, dw3, dw2};
+        for (int i = 0; i < 3; ++i) {
+            FfnProduct& g = i < 2 ? add(r, I, H, n, out[i]) : add(r, H, I, n, out[i]);
+            g.a_mn = i < 2 ? ffn_map_mn(&g.a[0], lhs[i], m, I, I) : ffn_map_mn(&g.a[0], dout, m, H, ldd);
+            g.b_mn = i < 2 ? ffn_map_mn(&g.b[0], x, m, H, ldx) : ffn_map_mn(&g.b[0], saved_h, m, I, I);
+            if (!g.a_mn || !g.b_mn) return MOE_ERR_CUDA;
+        }
     }
     if (launch_ffn_products(r, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
     f->last_launches = 2;

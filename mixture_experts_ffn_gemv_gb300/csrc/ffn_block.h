@@ -20,11 +20,15 @@ enum FfnEpilogue : int {
     EPI_DACT,         // D = dh: out = dg = dh d, du = dh a
 };
 
+// How an operand lies in memory: along K; along M (N), as boxes of 64 x 64, or
+// (multiples of 64) two of these at a time.
+enum FfnOrder : int { K_MAJOR = 0, MN_ROWS, MN_BLOCKS };
+
 // One product D[M, N] = sum over one or two sources of A B^T, as a work list
 // of 256 x 256 tiles (gate/up: 256 rows x 128 columns of g and of u).
 struct FfnProduct {
     CUtensorMap a[2], b[2];  // per source (gate/up: b = W1, W3, one source)
-    int a_mn, b_mn;          // operand stored along M (N) instead of along K
+    int a_mn, b_mn;          // FfnOrder of the operands
     int kblocks;             // 64-wide K blocks per source
     int sources;
     int m_tiles, n_tiles;
@@ -45,11 +49,12 @@ struct FfnProducts {
     uint64_t wait_ns;
 };
 
-// Maps of a bf16 operand [rows, cols] (row stride ld elements), all even.
-// K-major: 64 of K x box_rows rows; MN-major: 64 of M x 64 rows of K.  The
-// maps count 32-bit words (coordinates along a row are halves): boxes of a
-// 16-bit type arrive more slowly (32 KB per SM in 712 cycles, as words 616).
+// Maps of a bf16 operand [rows, cols] (row stride ld elements), all even, as
+// 32-bit words in three dimensions.  K-major: (word, row, 0), boxes of 64 of K
+// x box_rows rows.  ffn_map_mn: MN-major, 64 of M x 64 rows of K; returns the
+// order it chose (K_MAJOR: an error).
 bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
+int ffn_map_mn(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld);
 
 cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st);
 

@@ -105,10 +105,10 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
             const auto weights = [&](int ks, uint32_t s) {
                 const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
                 mbar_arrive_expect_tx(bar, ss.bytes);
-                const int c = MX ? 128 : 32;  // elements of the map per 128 bytes of K
+                const int c = 32;  // words per 128 bytes of K
                 const int kc = (GATEUP ? ks : 2 * ks) * c;
-                tma_load_2d(st, &p.a[0], kc, row0, bar);
-                tma_load_2d(st + TILE, &p.a[GATEUP ? 1 : 0], GATEUP ? kc : kc + c, row0, bar);
+                tma_load_3d(st, &p.a[0], kc, row0, 0, bar);
+                tma_load_3d(st + TILE, &p.a[GATEUP ? 1 : 0], GATEUP ? kc : kc + c, row0, 0, bar);
                 if (MX) {
                     const int kt = (GATEUP ? 2 : 4) * ks;
                     tma_load_3d(st + ss.sa, &p.as[0], 0, kt, tile, bar);
@@ -117,10 +117,10 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
             };
             const auto tokens = [&](int ks, uint32_t s) {
                 const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
-                const int c = MX ? 128 : 32;
+                const int c = 32;
                 const int kc = (GATEUP ? ks : 2 * ks) * c;
-                tma_load_2d(st + ss.tok, &p.b, kc, tok0, bar);
-                if (!GATEUP) tma_load_2d(st + ss.tok + p.nt * 128, &p.b, kc + c, tok0, bar);
+                tma_load_3d(st + ss.tok, &p.b, kc, tok0, 0, bar);
+                if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, &p.b, kc + c, tok0, 0, bar);
                 if (MX) {
                     const int kt = (GATEUP ? 2 : 4) * ks;
                     tma_load_3d(st + ss.sb, &p.bs, 0, kt, tok0 >> 7, bar);

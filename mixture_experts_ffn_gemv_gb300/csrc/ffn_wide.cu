@@ -80,6 +80,20 @@ __device__ __forceinline__ void store_row32f(float* p, int n, const uint32_t (&f
     }
 }
 
+// Coordinates of an operand's box of 128 rows of M (or N) from m0 on: the
+// first K block's, and the step per K block; two: the tile takes two boxes.
+struct BoxWalk {
+    int c0, c1, c2, d0, d1;
+    bool two;
+    __device__ __forceinline__ BoxWalk(int order, int m0)
+        : c0(order == MN_ROWS ? m0 / 2 : 0),
+          c1(order == K_MAJOR ? m0 : 0),
+          c2(order == MN_BLOCKS ? m0 / 64 : 0),
+          d0(order == K_MAJOR ? BK / 2 : 0),
+          d1(order == K_MAJOR ? 0 : BK),
+          two(order == MN_ROWS) {}
+};
+
 struct Item {
     int op, mt, nt;
 };
@@ -141,55 +155,57 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
     const uint32_t lead_full0 = mapa(full0, 0), lead_tempty0 = mapa(tempty0, 0);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = cl; t < total && ok; t += ncl) {
-                if (*abort_flag) break;
-                const Item w = item_of(p, t);
-                const FfnProduct& q = p.p[w.op];
-                const int m0 = w.mt * 256 + (int)rank * BM;
-                const int n0 = GATEUP ? w.nt * 128 : w.nt * 256 + (int)rank * 128;
-                for (int src = 0; src < q.sources && ok; ++src) {
-                    const CUtensorMap* ma = &q.a[src];
-                    const CUtensorMap* mb = &q.b[GATEUP ? rank : src];
-                    for (int kb = 0; kb < q.kblocks; ++kb, ++it) {
-                        const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                        if (!mbar_wait_cluster(empty0 + 8 * s, ph ^ 1u, p.wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES, bar = lead_full0 + 8 * s;
+        // Like the issuer's, this loop is the whole warp's, its body one lane's
+        // and free of choices: every map has three dimensions, and a box moves
+        // by (w, r) along the first two per K block.  (One lane alone, choosing
+        // by order, took 620 to 790 cycles a stage: more than the MMAs.)
+        uint32_t s = 0, ph = 1, n = 0;
+        bool ok = true;
+        for (int t = cl; t < total && ok; t += ncl) {
+            if (*abort_flag) break;
+            const Item w = item_of(p, t);
+            const FfnProduct& q = p.p[w.op];
+            const int m0 = w.mt * 256 + (int)rank * BM;
+            const int n0 = GATEUP ? w.nt * 128 : w.nt * 256 + (int)rank * 128;
+            const BoxWalk a(q.a_mn, m0), b(q.b_mn, n0);
+            for (int src = 0; src < q.sources && ok; ++src) {
+                const CUtensorMap* ma = &q.a[src];
+                const CUtensorMap* mb = &q.b[GATEUP ? rank : src];
+                for (int kb = 0; kb < q.kblocks; ++kb) {
+                    if (!mbar_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = sbase + s * STAGE_BYTES, sb = sa + A_BYTES, bar = lead_full0 + 8 * s;
+                    if (elect_one()) {
                         if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * STAGE_BYTES);
-                        if (q.a_mn) {
-                            tma_load_2d_pair(sa, ma, m0 / 2, kb * BK, bar);
-                            tma_load_2d_pair(sa + A_BYTES / 2, ma, m0 / 2 + 32, kb * BK, bar);
-                        } else {
-                            tma_load_2d_pair(sa, ma, kb * BK / 2, m0, bar);
-                        }
-                        if (q.b_mn) {
-                            tma_load_2d_pair(sb, mb, n0 / 2, kb * BK, bar);
-                            tma_load_2d_pair(sb + B_BYTES / 2, mb, n0 / 2 + 32, kb * BK, bar);
-                        } else {
-                            tma_load_2d_pair(sb, mb, kb * BK / 2, n0, bar);
-                        }
+                        tma_load_3d_pair(sa, ma, a.c0 + kb * a.d0, a.c1 + kb * a.d1, a.c2, bar);
+                        if (a.two) tma_load_3d_pair(sa + A_BYTES / 2, ma, a.c0 + 32, a.c1 + kb * a.d1, 0, bar);
+                        tma_load_3d_pair(sb, mb, b.c0 + kb * b.d0, b.c1 + kb * b.d1, b.c2, bar);
+                        if (b.two) tma_load_3d_pair(sb + B_BYTES / 2, mb, b.c0 + 32, b.c1 + kb * b.d1, 0, bar);
+                    }
+                    __syncwarp();
+                    ++n;
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
             }
-            if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 21);
-                *abort_flag = 1;
-            }
-            if (leader) {
-                // every issued copy of both CTAs has landed before either can exit
-                for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
-                    mbar_wait_cluster(full0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
-            } else if (!ok || *abort_flag) {
-                // the peer's copies complete on the leader's barriers: after an
-                // abort, give any still in flight time to land
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
-            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 21);
+            *abort_flag = 1;
+        }
+        if (leader) {
+            // every issued copy of both CTAs has landed before either can exit
+            for (uint32_t i = n > (uint32_t)STAGES ? n - STAGES : 0; i < n; ++i)
+                mbar_wait_cluster(full0 + 8 * (i % STAGES), (i / STAGES) & 1u, DRAIN_NS);
+        } else if (!ok || *abort_flag) {
+            // the peer's copies complete on the leader's barriers: after an
+            // abort, give any still in flight time to land
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
         }
     } else if (warp == 1) {
         if (leader) {
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                     stage_row128(stg, o[j], lane);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) tma_store_2d(&q.o, col0 / 2 + 32 * j, row0, stg);
+                    if (lane == 0) tma_store_3d(&q.o, col0 / 2 + 32 * j, row0, 0, stg);
                 }
             }
         }
@@ -388,8 +404,16 @@ cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
 }  // namespace
 
 bool ffn_map(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
-    const uint64_t dims[2] = {cols / 2, rows};
-    return tmap_encode(m, p, 2, dims, 4, BK / 2, box_rows, true, ld / 2);
+    const uint64_t dims[3] = {cols / 2, rows, 1}, strides[2] = {ld * 2, 128};
+    const uint32_t box[3] = {BK / 2, box_rows, 1};
+    return tmap_encode_words(m, p, 3, dims, strides, box);
+}
+
+int ffn_map_mn(CUtensorMap* m, const void* p, uint64_t rows, uint64_t cols, uint64_t ld) {
+    if (cols % 64) return ffn_map(m, p, rows, cols, ld, 64) ? MN_ROWS : K_MAJOR;
+    const uint64_t dims[3] = {32, rows, cols / 64}, strides[2] = {ld * 2, 128};
+    const uint32_t box[3] = {32, 64, 2};
+    return tmap_encode_words(m, p, 3, dims, strides, box) ? MN_BLOCKS : K_MAJOR;
 }
 
 cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {

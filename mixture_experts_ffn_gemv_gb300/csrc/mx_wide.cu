@@ -113,45 +113,51 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
     const uint32_t lead_full0 = mapa(full0, 0), lead_tempty = mapa(tempty, 0);
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = cl; t < total && ok; t += ncl) {
-                if (*abort_flag) break;
-                const int mt = t / p.n_tiles, nt = t % p.n_tiles;
-                const int m0 = mt * 256 + (int)rank * BM;
-                const int n0 = GATEUP ? nt * 128 : nt * 256 + (int)rank * 128;
-                const CUtensorMap* mb = &p.b[GATEUP ? rank : 0];
-                for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!mbar_wait_cluster(empty0 + 8 * s, ph ^ 1u, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = sbase + s * STAGE_STRIDE, bar = lead_full0 + 8 * s;
-                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (A_BYTES + B_BYTES));
-                    tma_load_2d_pair(sa, &p.a, kb * BKB, m0, bar);
-                    tma_load_2d_pair(sa + B_OFF, mb, kb * BKB, n0, bar);
-                    const uint32_t sl = sland0 + 8 * s;
+        // the whole warp's loop, one lane's body: as in ffn_wide.cu
+        uint32_t s = 0, ph = 1, n = 0;
+        bool ok = true;
+        for (int t = cl; t < total && ok; t += ncl) {
+            if (*abort_flag) break;
+            const int mt = t / p.n_tiles, nt = t % p.n_tiles;
+            const int m0 = mt * 256 + (int)rank * BM, mt0 = m0 >> 7;
+            const int n0 = GATEUP ? nt * 128 : nt * 256 + (int)rank * 128;
+            const int bt0 = GATEUP ? nt : 2 * nt, bt1 = GATEUP ? nt : 2 * nt + 1;
+            const CUtensorMap *mb = &p.b[GATEUP ? rank : 0], *ms1 = &p.bs[GATEUP ? 1 : 0];
+            for (int kb = 0; kb < p.kblocks; ++kb) {
+                if (!mbar_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = sbase + s * STAGE_STRIDE, bar = lead_full0 + 8 * s, sl = sland0 + 8 * s;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(sl, SA_BYTES + SB_BYTES);
-                    tma_load_3d(sa + SA_OFF, &p.as, 0, 2 * kb, m0 >> 7, sl);
-                    tma_load_3d(sa + SB_OFF, &p.bs[0], 0, 2 * kb, GATEUP ? nt : 2 * nt, sl);
-                    tma_load_3d(sa + SB_OFF + 1024, &p.bs[GATEUP ? 1 : 0], 0, 2 * kb, GATEUP ? nt : 2 * nt + 1, sl);
+                    tma_load_3d(sa + SA_OFF, &p.as, 0, 2 * kb, mt0, sl);
+                    tma_load_3d(sa + SB_OFF, &p.bs[0], 0, 2 * kb, bt0, sl);
+                    tma_load_3d(sa + SB_OFF + 1024, ms1, 0, 2 * kb, bt1, sl);
+                    if (leader) mbar_arrive_expect_tx(full0 + 8 * s, 2 * (A_BYTES + B_BYTES));
+                    tma_load_3d_pair(sa, &p.a, kb * (BKB / 4), m0, 0, bar);
+                    tma_load_3d_pair(sa + B_OFF, mb, kb * (BKB / 4), n0, 0, bar);
+                }
+                __syncwarp();
+                ++n;
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 31);
-                *abort_flag = 1;
-            }
-            for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
-                mbar_wait(sland0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
-            if (leader) {
-                for (uint32_t j = it > (uint32_t)STAGES ? it - STAGES : 0; j < it; ++j)
-                    mbar_wait_cluster(full0 + 8 * (j % STAGES), (j / STAGES) & 1u, DRAIN_NS);
-            } else if (!ok || *abort_flag) {
-                const uint64_t t0 = globaltimer();
-                while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
-            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 31);
+            *abort_flag = 1;
+        }
+        const uint32_t first = n > (uint32_t)STAGES ? n - STAGES : 0;
+        for (uint32_t i = first; i < n; ++i) mbar_wait(sland0 + 8 * (i % STAGES), (i / STAGES) & 1u, DRAIN_NS);
+        if (leader) {
+            for (uint32_t i = first; i < n; ++i)
+                mbar_wait_cluster(full0 + 8 * (i % STAGES), (i / STAGES) & 1u, DRAIN_NS);
+        } else if (!ok || *abort_flag) {
+            const uint64_t t0 = globaltimer();
+            while (globaltimer() - t0 < 50000ull) __nanosleep(1000);
         }
     } else if (warp == 1) {
         // The whole warp walks the loop and one lane issues: the addresses are
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
                     stage_row128(stg, o[GATEUP ? 0 : c], lane);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) tma_store_2d(&p.o, col / 2, r, stg);
+                    if (lane == 0) tma_store_3d(&p.o, col / 2, r, 0, stg);
                 }
             }
         }
@@ -347,10 +353,9 @@ cudaError_t launch(const MxProduct& p, cudaStream_t st) {
 
 }  // namespace
 
-// Codes [rows, k/2]: boxes of 128 bytes x box_rows rows, 128-byte swizzle.
+// Codes [rows, k/2 bytes]: boxes of 128 bytes x box_rows rows, as bf16 rows of k/4.
 bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, uint32_t box_rows) {
-    const uint64_t dims[2] = {k / 2, rows};
-    return tmap_encode(m, codes, 2, dims, 1, BKB, box_rows);
+    return ffn_map(m, codes, rows, k / 4, k / 4, box_rows);
 }
 // Packed scales as [row tiles][K tiles][128 words]: boxes of two K tiles of
 // one row tile (tiles past the end read as zero: scale 2^-127 on zero codes).

@@ -49,6 +49,22 @@ bool tmap_encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
     return r == CUDA_SUCCESS;
 }
 
+bool tmap_encode_words(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank < 2 || rank > 3) return false;
+    cuuint64_t gdim[3], gstride[2];
+    cuuint32_t b[3], estr[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        gdim[i] = dims[i];
+        b[i] = box[i];
+        if (i) gstride[i - 1] = strides[i - 1];
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, (cuuint32_t)rank, const_cast<void*>(base), gdim, gstride, b, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int device_sm_count() {
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;

@@ -15,6 +15,10 @@ namespace moe {
 bool tmap_encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, int esize, uint32_t box_cols,
                  uint32_t box_rows, bool swizzle = true, uint64_t ld = 0);
 
+// The same by hand: words, strides[i] bytes from one index of dims[i + 1] to the next.
+bool tmap_encode_words(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box);
+
 int device_sm_count();
 
 }  // namespace moe
