@@ -101,68 +101,75 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const auto weights = [&](int ks, uint32_t s) {
-                const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
-                mbar_arrive_expect_tx(bar, ss.bytes);
-                const int c = 32;  // words per 128 bytes of K
-                const int kc = (GATEUP ? ks : 2 * ks) * c;
-                tma_load_3d(st, &p.a[0], kc, row0, 0, bar);
-                tma_load_3d(st + TILE, &p.a[GATEUP ? 1 : 0], GATEUP ? kc : kc + c, row0, 0, bar);
-                if (MX) {
-                    const int kt = (GATEUP ? 2 : 4) * ks;
-                    tma_load_3d(st + ss.sa, &p.as[0], 0, kt, tile, bar);
-                    tma_load_3d(st + ss.sa + 1024, &p.as[GATEUP ? 1 : 0], 0, GATEUP ? kt : kt + 2, tile, bar);
-                }
-            };
-            const auto tokens = [&](int ks, uint32_t s) {
-                const uint32_t st = sbase + s * stride, bar = full0 + 8 * s;
-                const int c = 32;
-                const int kc = (GATEUP ? ks : 2 * ks) * c;
-                tma_load_3d(st + ss.tok, &p.b, kc, tok0, 0, bar);
-                if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, &p.b, kc + c, tok0, 0, bar);
-                if (MX) {
-                    const int kt = (GATEUP ? 2 : 4) * ks;
-                    tma_load_3d(st + ss.sb, &p.bs, 0, kt, tok0 >> 7, bar);
-                    if (!GATEUP) tma_load_3d(st + ss.sb + 1024, &p.bs, 0, kt + 2, tok0 >> 7, bar);
-                }
-            };
-            const int n = k1 - k0, pre = min(n, p.stages);
-            bool ok = true;
-            for (int i = 0; i < pre; ++i) weights(k0 + i, i);
-            if (p.early) pdl_wait();
-            for (int i = 0; i < pre; ++i) tokens(k0 + i, i);
-            int i = pre;
-            for (; i < n; ++i) {
-                const uint32_t s = i % p.stages, ph = (i / p.stages) & 1u;
-                if (*abort_flag || !mbar_wait(empty0 + 8 * s, ph ^ 1u, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                weights(k0 + i, s);
-                tokens(k0 + i, s);
+        // the whole warp's loop, one lane's body: as in ffn_wide.cu
+        const CUtensorMap *a0 = &p.a[0], *a1 = &p.a[GATEUP ? 1 : 0], *s0 = &p.as[0], *s1 = &p.as[GATEUP ? 1 : 0];
+        const auto weights = [&](int ks, uint32_t st, uint32_t bar) {
+            const int kc = (GATEUP ? ks : 2 * ks) * 32;  // words along K: 128 bytes are 32
+            mbar_arrive_expect_tx(bar, ss.bytes);
+            tma_load_3d(st, a0, kc, row0, 0, bar);
+            tma_load_3d(st + TILE, a1, GATEUP ? kc : kc + 32, row0, 0, bar);
+            if (MX) {
+                const int kt = (GATEUP ? 2 : 4) * ks;
+                tma_load_3d(st + ss.sa, s0, 0, kt, tile, bar);
+                tma_load_3d(st + ss.sa + 1024, s1, 0, GATEUP ? kt : kt + 2, tile, bar);
             }
-            if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 41);
-                *abort_flag = 1;
+        };
+        const auto tokens = [&](int ks, uint32_t st, uint32_t bar) {
+            const int kc = (GATEUP ? ks : 2 * ks) * 32;
+            tma_load_3d(st + ss.tok, &p.b, kc, tok0, 0, bar);
+            if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, &p.b, kc + 32, tok0, 0, bar);
+            if (MX) {
+                const int kt = (GATEUP ? 2 : 4) * ks;
+                tma_load_3d(st + ss.sb, &p.bs, 0, kt, tok0 >> 7, bar);
+                if (!GATEUP) tma_load_3d(st + ss.sb + 1024, &p.bs, 0, kt + 2, tok0 >> 7, bar);
             }
-            for (int j = max(0, i - p.stages); j < i; ++j)  // every issued copy has landed
-                mbar_wait(full0 + 8 * (j % p.stages), (j / p.stages) & 1u, DRAIN_NS);
-        }
+        };
+        const int n = k1 - k0, pre = min(n, p.stages);
+        bool ok = true;
+        if (elect_one())
+            for (int i = 0; i < pre; ++i) weights(k0 + i, sbase + i * stride, full0 + 8 * i);
         __syncwarp();
+        if (p.early) pdl_wait();
+        if (elect_one())
+            for (int i = 0; i < pre; ++i) tokens(k0 + i, sbase + i * stride, full0 + 8 * i);
+        __syncwarp();
+        int i = pre, s = 0;
+        uint32_t ph = 0;
+        for (; i < n; ++i) {
+            if (!mbar_wait(empty0 + 8 * s, ph, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            if (elect_one()) {
+                weights(k0 + i, sbase + s * stride, full0 + 8 * s);
+                tokens(k0 + i, sbase + s * stride, full0 + 8 * s);
+            }
+            __syncwarp();
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 41);
+            *abort_flag = 1;
+        }
+        for (int j = max(0, i - p.stages); j < i; ++j)  // every issued copy has landed
+            mbar_wait(full0 + 8 * (j % p.stages), (j / p.stages) & 1u, DRAIN_NS);
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            const uint32_t idesc = idesc_bf16(128, p.nt);
-            for (int i = 0; i < k1 - k0; ++i) {
-                const uint32_t s = i % p.stages, ph = (i / p.stages) & 1u;
-                if (*abort_flag || !mbar_wait(full0 + 8 * s, ph, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t st = sbase + s * stride;
-                const uint32_t sf = sf0 + s * 32;
+        bool ok = true;
+        const uint32_t idesc = idesc_bf16(128, p.nt);
+        int s = 0;
+        uint32_t ph = 0;
+        for (int i = 0; i < k1 - k0; ++i) {
+            if (*abort_flag || !mbar_wait(full0 + 8 * s, ph, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t st = sbase + s * stride;
+            const uint32_t sf = sf0 + s * 32;
+            if (elect_one()) {
                 if (MX) {
                     // 8 columns per weight tile (two K tiles of 128), then 8 per token tile
 #pragma unroll
@@ -191,12 +198,17 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
                 }
                 mma_commit(empty0 + 8 * s);
             }
-            if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 42);
-                *abort_flag = 1;
+            __syncwarp();
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
             }
-            mma_commit(done);
         }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 42);
+            *abort_flag = 1;
+        }
+        if (elect_one()) mma_commit(done);
         __syncwarp();
     }
     // the sums to shared memory, over the ring (its copies have landed and its
