@@ -104,7 +104,9 @@ MOE_API int moe_ffn_last_launch_count(const moe_ffn* ffn);
 MOE_API int moe_mxfp4_scales_size(int64_t rows, int64_t n, size_t* bytes);
 
 /* x [rows, n] (bf16, or fp32 for _f32; row stride ldx >= n elements, rows
- * 16-byte aligned) to MXFP4: codes uint8 [rows, n/2], scales packed. */
+ * 16-byte aligned) to MXFP4: codes uint8 [rows, n/2], scales packed.  At most
+ * 2^26 pieces of 512 elements of a row (2^35 elements in full pieces), here and
+ * in moe_mxfp4_dequant. */
 MOE_API int moe_mxfp4_quant(const void* x, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
                             void* stream);
 MOE_API int moe_mxfp4_quant_f32(const float* x, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes,

@@ -617,7 +617,7 @@ class GatedFfn:
         ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
         if out is None:
-            out = x.new_empty((m, self.hidden))
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
         if m > self._fits[0]:

@@ -214,11 +214,16 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
     return MOE_OK;
 }
 
+// Rows and columns whose pieces of 16 elements the quantisers count in 32 bits.
+bool too_large(int64_t rows, int64_t n) {
+    return rows > INT32_MAX / 64 || n > INT32_MAX / 64 || rows * ((n + 511) / 512) > (int64_t)1 << 26;
+}
+
 int quant(const void* x, bool f32, int64_t ldx, int64_t rows, int64_t n, uint8_t* codes, uint8_t* scales,
           void* stream) {
     if (rows < 0 || n <= 0 || n % 32) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (rows > INT32_MAX / 64 || n > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    if (too_large(rows, n)) return MOE_ERR_UNSUPPORTED;
     if (!x || !aligned(x, 16) || ldx < n || ldx % (f32 ? 4 : 8) || !codes || !scales || !aligned(codes, 16) ||
         !aligned(scales, 16))
         return MOE_ERR_INVALID_ARG;
@@ -435,7 +440,7 @@ int moe_mxfp4_quant_f32(const float* x, int64_t ldx, int64_t rows, int64_t n, ui
 int moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t n, void* out, void* stream) {
     if (rows < 0 || n <= 0 || n % 32) return MOE_ERR_INVALID_ARG;
     if (rows == 0) return MOE_OK;
-    if (rows > INT32_MAX / 64 || n > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    if (too_large(rows, n)) return MOE_ERR_UNSUPPORTED;
     if (!codes || !scales || !out || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 16))
         return MOE_ERR_INVALID_ARG;
     return launch_mx_dequant(codes, scales, (int)rows, (int)n, static_cast<uint16_t*>(out),
