@@ -13,13 +13,14 @@
 //              for the preceding kernel where that one wrote only the tokens,
 //              so that the stream of weights starts while that kernel drains;
 //   warp 1     MMA issuer (and, MXFP4, the scale copies to tensor memory);
-//   all warps  the sum over slices and the epilogue, a warp per (token, 32 rows):
-//              of an MXFP4 h exactly one block.
+//   all warps  the sum over slices and the epilogue, a warp per token, four rows
+//              per lane: eight lanes hold one block of an MXFP4 h.
 // A stage holds two weight tiles of 128 bytes of K: W1 and W3, or (one matrix)
 // two neighbours along K.  Bounded waits as in ffn_wide.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "ffn_act.cuh"
@@ -38,6 +39,7 @@ using namespace sm100;
 constexpr int TILE = 128 * 128;  // 128 rows x 128 bytes of K
 constexpr int WARPS = 10, THREADS = 32 * WARPS;
 constexpr int MAX_STAGES = 8;
+constexpr int MAX_SLICES = 8;  // the portable cluster size
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
 // Byte offsets inside a stage.
@@ -55,14 +57,22 @@ __host__ __device__ inline StageShape stage_shape(bool mx, bool gateup, int nt) 
 }
 __host__ __device__ inline int stage_stride(const StageShape& s) { return (s.bytes + 1023) & ~1023; }
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr));
     return v;
+}
+__device__ __forceinline__ void add4(float (&a)[4], const float4& v) {
+    a[0] += v.x;
+    a[1] += v.y;
+    a[2] += v.z;
+    a[3] += v.w;
 }
 
 template <bool MX, bool GATEUP>
-__global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__ NarrowProduct p) {
+__global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__ NarrowProduct p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -230,42 +240,71 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
         tc_fence_before();
     }
     cluster_sync();
-    // units of (token, 32 rows), dealt over the cluster's warps
-    const uint32_t pbase = smem_u32(part);
-    for (int u = (int)rank + S * warp; u < ntok * 4; u += S * WARPS) {
-        const int j = u >> 2, q = u & 3;
-        const int r = row0 + q * 32 + lane;  // output column of this lane
-        if (row0 + q * 32 >= p.R && !(MX && GATEUP)) continue;
-        const uint32_t off = pbase + (uint32_t)(j * 128 + q * 32 + lane) * 4;
-        float v0 = 0.f, v1 = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < S; ++s) {
-            const uint32_t a = mapa(off, s);
-            v0 += ld_cluster(a);
-            if (GATEUP) v1 += ld_cluster(a + p.nt * 512);
-        }
-        const size_t t = (size_t)(tok0 + j);
-        if (GATEUP && MX) {
-            const float h = r < p.R ? glu(v0, v1, p.act) : 0.f;
-            const uint32_t sc = mx_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu));
-            uint32_t w = sc == 255u ? 0u : mx_code(h * mx_inverse(sc)) << (4 * (lane & 7));
-            w |= __shfl_xor_sync(0xffffffffu, w, 1);
-            w |= __shfl_xor_sync(0xffffffffu, w, 2);
-            w |= __shfl_xor_sync(0xffffffffu, w, 4);
-            if ((lane & 7) == 0 && r < p.R) *reinterpret_cast<uint32_t*>(p.codes + (t * p.R + r) / 2) = w;
-            if (lane == 0) p.scales[mx_scale_at(t, (size_t)(tile * 4 + q), p.nkt)] = (uint8_t)sc;
-        } else if (r < p.R) {
-            const size_t at = t * p.R + r;
-            if (GATEUP) {
-                float a, slope;
-                act_slope(v0, p.act, a, slope);
-                p.out[at] = f32_to_bf16(a * v1);
-                if (p.sa) {
-                    p.sa[at] = a;
-                    p.sd[at] = v1 * slope;
+    // tokens, dealt over the cluster's warps, U at a time; the loads of all
+    // slices are on their way (one takes a microsecond) before the first is added
+    constexpr int U = GATEUP ? 1 : 2;
+    const uint32_t pbase = smem_u32(part) + lane * 16;
+    const int r = row0 + lane * 4;  // this lane's output columns r .. r + 3
+    for (int j0 = (int)rank + S * warp; j0 < ntok; j0 += U * S * WARPS) {
+        float v0[U][4] = {}, v1[U][4] = {};
+        float4 q0[U][MAX_SLICES], q1[U][MAX_SLICES];
+#pragma unroll
+        for (int s = 0; s < MAX_SLICES; ++s)
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int j = j0 + x * S * WARPS;
+                if (s < S && j < ntok) {
+                    const uint32_t a = mapa(pbase + j * 512, s);
+                    q0[x][s] = ld_cluster4(a);
+                    if (GATEUP) q1[x][s] = ld_cluster4(a + p.nt * 512);
                 }
-            } else {
-                p.out[at] = f32_to_bf16(v0);
+            }
+#pragma unroll
+        for (int s = 0; s < MAX_SLICES; ++s)
+#pragma unroll
+            for (int x = 0; x < U; ++x)
+                if (s < S) {
+                    add4(v0[x], q0[x][s]);
+                    if (GATEUP) add4(v1[x], q1[x][s]);
+                }
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+            const int j = j0 + x * S * WARPS;
+            if (j >= ntok) break;
+            const size_t t = (size_t)(tok0 + j);
+            if (GATEUP && MX) {
+                float h[4];
+                uint32_t a = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = r < p.R ? glu(v0[x][i], v1[x][i], p.act) : 0.f;
+                    a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
+                }
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const uint32_t sc = mx_scale(a);
+                const uint32_t w = sc == 255u ? 0u : mx_codes4(h, mx_inverse(sc));
+                if (r < p.R) *reinterpret_cast<uint16_t*>(p.codes + (t * p.R + r) / 2) = (uint16_t)w;
+                if ((lane & 7) == 0) p.scales[mx_scale_at(t, (size_t)(tile * 4 + (lane >> 3)), p.nkt)] = (uint8_t)sc;
+            } else if (r < p.R) {  // R is a multiple of 8: whole quads
+                const size_t at = t * p.R + r;
+                float o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[i] = v0[x][i];
+                    if (GATEUP) {
+                        float a, slope;
+                        act_slope(v0[x][i], p.act, a, slope);
+                        o[i] = a * v1[x][i];
+                        v0[x][i] = a;
+                        v1[x][i] *= slope;
+                    }
+                }
+                if (GATEUP && p.sa) {
+                    *reinterpret_cast<float4*>(p.sa + at) = make_float4(v0[x][0], v0[x][1], v0[x][2], v0[x][3]);
+                    *reinterpret_cast<float4*>(p.sd + at) = make_float4(v1[x][0], v1[x][1], v1[x][2], v1[x][3]);
+                }
+                *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             }
         }
     }
@@ -279,6 +318,32 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_narrow(const __grid_constant__
 int sms() {
     static int n = device_sm_count();
     return n;
+}
+
+// Clusters of `size` CTAs that the device holds at once with one CTA per SM (asked once).
+int clusters_resident(int size) {
+    static std::atomic<int> known[MAX_SLICES + 1];
+    std::atomic<int>& k = known[size];
+    if (k.load() == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = 222 * 1024;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = size;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(ffn_narrow<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, ffn_narrow<false, true>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = sms() / size * 3 / 4;
+        }
+        k.store(std::max(n, 1));
+    }
+    return k.load();
 }
 
 template <bool MX, bool GATEUP>
@@ -312,9 +377,12 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream
     p.kstages = ceil_div(p.K, (mx ? 256 : 64) * (gateup ? 1 : 2));
     const StageShape ss = stage_shape(mx, gateup, p.nt);
     const int stride = stage_stride(ss);
-    // two CTAs per SM while the token tiles are small: the second one's stream
-    // covers the first one's start and end
-    const int budget = p.nt <= 48 ? 110 * 1024 : 220 * 1024;
+    // Two CTAs per SM for up to 16 tokens: the next kernel's weights then arrive
+    // while this one drains (7168 x 2048, one token: 20.2 us, with one CTA of
+    // twice the stages 21.2).  Above, two would have two or three stages each
+    // (48 tokens: 27.4 us, with one of five 23.6).
+    const int resident = p.nt <= 16 ? 2 : 1;
+    const int budget = resident == 2 ? 110 * 1024 : 220 * 1024;
     p.stages = std::min(MAX_STAGES, budget / stride);
     if (mx) p.stages = std::min(p.stages, 4);  // 32 scale columns each
     const int acc = (gateup ? 2 : 1) * p.nt;
@@ -323,21 +391,18 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream
     int cols = 32;
     while (cols < acc + (mx ? 32 * p.stages : 0)) cols *= 2;
     p.tmem_cols = cols;
-    // slices of K: the count (at most 8, the portable cluster size, and a stage
-    // each) that spreads the row tiles most evenly over two CTAs per SM
+    // Slices of K: as many as the device takes at once, with two stages or more
+    // each.  At one CTA per SM that goes by the clusters that fit (eights do not
+    // fill the SMs: 16 row tiles in 8 slices took 31.5 us, in 6 slices 23.6); at
+    // two, where a few clusters may start late, by CTAs, an eighth of the slots
+    // left free (56 tiles: 224 CTAs 20.2 us, 280 20.9, 168 21.4).
     const int tiles = ceil_div(p.R, 128) * ceil_div(p.T, p.nt);
-    int best = 1;
-    double eff = 0.0;
-    for (int s = 1; s <= std::min(8, p.kstages); ++s) {
-        const int ctas = tiles * s;
-        if (s > 1 && ctas > 2 * sms()) break;
-        const double e = (double)ctas / ((double)sms() * ceil_div(ctas, sms()));
-        if (e > eff + 1e-9) {
-            eff = e;
-            best = s;
+    p.slices = 1;
+    for (int s = std::min(MAX_SLICES, p.kstages / 2); s > 1; --s)
+        if (resident == 2 ? 8 * tiles * s <= 7 * 2 * sms() : tiles <= clusters_resident(s)) {
+            p.slices = s;
+            break;
         }
-    }
-    p.slices = best;
     if (mx) return gateup ? launch<true, true>(p, smem, st) : launch<true, false>(p, smem, st);
     return gateup ? launch<false, true>(p, smem, st) : launch<false, false>(p, smem, st);
 }

@@ -34,15 +34,16 @@ __device__ __forceinline__ uint32_t mx_codes8(const float* v, float r) {
     return w;
 }
 
-// The e2m1 code of one value, rounded as above.
-__device__ __forceinline__ uint32_t mx_code(float v) {
+// Four of them, in 16 bits.
+__device__ __forceinline__ uint32_t mx_codes4(const float* v, float r) {
     uint32_t w;
-    asm("{\n\t.reg .b8 b0;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %1, %1;\n\t"
-        "mov.b32 %0, {b0, b0, b0, b0};\n\t}"
+    asm("{\n\t.reg .b8 b0, b1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "mov.b32 %0, {b0, b1, b0, b1};\n\t}"
         : "=r"(w)
-        : "f"(v));
-    return w & 15u;
+        : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r));
+    return w & 0xffffu;
 }
 
 // Byte of the scale of row r, block b; nkt = ceil(blocks / 4) tiles per row.
