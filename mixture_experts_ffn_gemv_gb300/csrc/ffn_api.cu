@@ -110,26 +110,6 @@ FfnProduct& add(FfnProducts& p, int M, int N, int K, void* out) {
     return q;
 }
 
-int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out, float* saved,
-                 void* h, void* ws, cudaStream_t st) {
-    const int H = f->cfg.hidden, I = f->cfg.inter;
-    FfnProducts p = products(f, ws);
-    FfnProduct& gu = add(p, m, I, H, h);
-    if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
-    gu.b[0] = f->k1;
-    gu.b[1] = f->k3;
-    p.a = saved;
-    p.d = saved ? saved + (size_t)m * I : nullptr;
-    if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
-    FfnProducts d = products(f, ws);
-    FfnProduct& y = add(d, m, H, I, out);
-    if (!ffn_map(&y.a[0], h, m, I, I, 128)) return MOE_ERR_CUDA;
-    y.b[0] = f->k2;
-    if (launch_ffn_products(d, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
-    f->last_launches = 2;
-    return MOE_OK;
-}
-
 NarrowProduct narrow(int T, int R, int K, void* ws) {
     NarrowProduct p{};
     p.T = T;
@@ -140,40 +120,47 @@ NarrowProduct narrow(int T, int R, int K, void* ws) {
     return p;
 }
 
-// The block for few tokens: each kernel after the first streams its weights
-// while the one before drains.
-int forward_narrow(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx, int m, void* out, float* saved,
-                   void* h, void* ws, cudaStream_t st) {
+// Each product of a bf16 block takes the kernel that suits its size.
+int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out, float* saved, void* h, void* ws,
+                 cudaStream_t st) {
     const int H = f->cfg.hidden, I = f->cfg.inter;
-    const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
-    NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
-    uint8_t *xq = at<uint8_t>(ws, lo.xq), *xs = at<uint8_t>(ws, lo.xs), *hq = at<uint8_t>(ws, lo.hq),
-            *hs = at<uint8_t>(ws, lo.hs);
     const uint32_t nt = (uint32_t)narrow_tokens(m);
-    const bool ok = mx ? mx_code_map(&g.b, xq, m, H, nt) && mx_scale_map(&g.bs, xs, m, H) &&
-                             mx_code_map(&d.b, hq, m, I, nt) && mx_scale_map(&d.bs, hs, m, I)
-                       : ffn_map(&g.b, x, m, H, ldx, nt) && ffn_map(&d.b, h, m, I, I, nt);
-    if (!ok) return MOE_ERR_CUDA;
-    g.a[0] = f->k1;
-    g.a[1] = f->k3;
-    g.as[0] = f->s1;
-    g.as[1] = f->s3;
-    g.act = f->cfg.activation;
-    g.early = mx;  // behind the quantiser
-    g.out = static_cast<uint16_t*>(h);
-    g.sa = saved;
-    g.sd = saved ? saved + (size_t)m * I : nullptr;
-    g.codes = hq;
-    g.scales = hs;
-    g.nkt = ceil_div(I, 128);
-    d.a[0] = f->k2;
-    d.as[0] = f->s2;
-    d.early = 1;
-    d.out = static_cast<uint16_t*>(out);
-    if (mx && launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) != cudaSuccess) return MOE_ERR_CUDA;
-    if (launch_ffn_narrow(g, mx, true, st) != cudaSuccess || launch_ffn_narrow(d, mx, false, st) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    f->last_launches = mx ? 3 : 2;
+    float* saved_d = saved ? saved + (size_t)m * I : nullptr;
+    if (narrow_is_faster(m, I, false)) {
+        NarrowProduct g = narrow(m, I, H, ws);
+        if (!ffn_map(&g.b[0], x, m, H, ldx, nt)) return MOE_ERR_CUDA;
+        g.a[0] = f->k1;
+        g.a[1] = f->k3;
+        g.act = f->cfg.activation;
+        g.out = static_cast<uint16_t*>(h);
+        g.sa = saved;
+        g.sd = saved_d;
+        if (launch_ffn_narrow(g, false, NARROW_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        FfnProducts p = products(f, ws);
+        FfnProduct& gu = add(p, m, I, H, h);
+        if (!ffn_map(&gu.a[0], x, m, H, ldx, 128)) return MOE_ERR_CUDA;
+        gu.b[0] = f->k1;
+        gu.b[1] = f->k3;
+        p.a = saved;
+        p.d = saved_d;
+        if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    if (narrow_is_faster(m, H, false)) {
+        NarrowProduct d = narrow(m, H, I, ws);
+        if (!ffn_map(&d.b[0], h, m, I, I, nt)) return MOE_ERR_CUDA;
+        d.a[0] = f->k2;
+        d.early = 1;  // behind the kernel that wrote h
+        d.out = static_cast<uint16_t*>(out);
+        if (launch_ffn_narrow(d, false, NARROW_PLAIN, st) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        FfnProducts d = products(f, ws);
+        FfnProduct& y = add(d, m, H, I, out);
+        if (!ffn_map(&y.a[0], h, m, I, I, 128)) return MOE_ERR_CUDA;
+        y.b[0] = f->k2;
+        if (launch_ffn_products(d, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    f->last_launches = 2;
     return MOE_OK;
 }
 
@@ -192,6 +179,32 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
     const int H = f->cfg.hidden, I = f->cfg.inter;
     uint8_t *xq = at<uint8_t>(ws, lo.xq), *xs = at<uint8_t>(ws, lo.xs), *hq = at<uint8_t>(ws, lo.hq),
             *hs = at<uint8_t>(ws, lo.hs);
+    f->last_launches = 3;
+    if (narrow_is_faster(m, I, true)) {
+        // each kernel after the quantiser streams its weights while the one before drains
+        NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
+        const uint32_t nt = (uint32_t)narrow_tokens(m);
+        if (!mx_code_map(&g.b[0], xq, m, H, nt) || !mx_scale_map(&g.bs, xs, m, H) ||
+            !mx_code_map(&d.b[0], hq, m, I, nt) || !mx_scale_map(&d.bs, hs, m, I))
+            return MOE_ERR_CUDA;
+        g.a[0] = f->k1;
+        g.a[1] = f->k3;
+        g.as[0] = f->s1;
+        g.as[1] = f->s3;
+        g.act = f->cfg.activation;
+        g.codes = hq;
+        g.scales = hs;
+        g.nkt = ceil_div(I, 128);
+        d.a[0] = f->k2;
+        d.as[0] = f->s2;
+        d.out = static_cast<uint16_t*>(out);
+        g.early = d.early = 1;
+        return launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) == cudaSuccess &&
+                       launch_ffn_narrow(g, true, NARROW_GATEUP, st) == cudaSuccess &&
+                       launch_ffn_narrow(d, true, NARROW_PLAIN, st) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
+    }
     MxProduct g = mx_product(m, I, H, ws), d = mx_product(m, H, I, ws);
     if (!mx_code_map(&g.a, xq, m, H, 128) || !mx_scale_map(&g.as, xs, m, H) || !mx_code_map(&d.a, hq, m, I, 128) ||
         !mx_scale_map(&d.as, hs, m, I))
@@ -207,11 +220,10 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
     d.b[0] = f->k2;
     d.bs[0] = f->s2;
     d.out = static_cast<uint16_t*>(out);
-    if (launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) != cudaSuccess ||
-        launch_mx_product(g, true, st) != cudaSuccess || launch_mx_product(d, false, st) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    f->last_launches = 3;
-    return MOE_OK;
+    return launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) == cudaSuccess &&
+                   launch_mx_product(g, true, st) == cudaSuccess && launch_mx_product(d, false, st) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 // Rows and columns whose pieces of 16 elements the quantisers count in 32 bits.
@@ -248,14 +260,14 @@ int check_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* w, const uint8_t*
 // early: the preceding kernel on the stream is the quantiser of A.
 int gemm(const uint8_t* a, const uint8_t* as, int m, const uint8_t* b, const uint8_t* bs, int n, int k, void* out,
          void* ws, bool early, cudaStream_t st) {
-    if (m <= kNarrowTokens) {
+    if (narrow_is_faster(m, n, true)) {
         NarrowProduct q = narrow(m, n, k, ws);
         if (!mx_code_map(&q.a[0], b, n, k, 128) || !mx_scale_map(&q.as[0], bs, n, k) ||
-            !mx_code_map(&q.b, a, m, k, (uint32_t)narrow_tokens(m)) || !mx_scale_map(&q.bs, as, m, k))
+            !mx_code_map(&q.b[0], a, m, k, (uint32_t)narrow_tokens(m)) || !mx_scale_map(&q.bs, as, m, k))
             return MOE_ERR_CUDA;
         q.early = early;
         q.out = static_cast<uint16_t*>(out);
-        return launch_ffn_narrow(q, true, false, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        return launch_ffn_narrow(q, true, NARROW_PLAIN, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     MxProduct g = mx_product(m, n, k, ws);
     if (!mx_code_map(&g.a, a, m, k, 128) || !mx_scale_map(&g.as, as, m, k) || !mx_code_map(&g.b[0], b, n, k, 128) ||
@@ -360,7 +372,6 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, voi
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
     void* h = saved ? saved_h : at<void>(workspace, lo.h);
-    if (m <= kNarrowTokens) return forward_narrow(f, lo, x, ldx, (int)m, out, saved, h, workspace, st);
     return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
               : forward_bf16(f, x, ldx, (int)m, out, saved, h, workspace, st);
 }
@@ -382,19 +393,44 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
     void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du);
+    float *sa = const_cast<float*>(saved), *sd = sa + (size_t)m * I;  // only read
+    const uint32_t nt = (uint32_t)narrow_tokens(n);
     // dh = dout W2 and, in its epilogue, dg and du
-    FfnProducts p = products(f, workspace);
-    FfnProduct& q = add(p, n, I, H, dg);
-    if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
-    q.b[0] = f->mn2;
-    q.b_mn = f->mn2_order;
-    p.a = const_cast<float*>(saved);
-    p.d = p.a + (size_t)m * I;
-    p.out_du = static_cast<uint16_t*>(du);
-    if (launch_ffn_products(p, EPI_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
-    // the four products that need them, in one launch
+    if (narrow_is_faster(n, I, false)) {
+        NarrowProduct q = narrow(n, I, H, workspace);
+        if (!ffn_map(&q.b[0], dout, m, H, ldd, nt)) return MOE_ERR_CUDA;
+        q.a[0] = f->mn2;
+        q.a_mn = f->mn2_order;
+        q.sa = sa;
+        q.sd = sd;
+        q.out = static_cast<uint16_t*>(dg);
+        q.du = static_cast<uint16_t*>(du);
+        if (launch_ffn_narrow(q, false, NARROW_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
+        FfnProducts p = products(f, workspace);
+        FfnProduct& q = add(p, n, I, H, dg);
+        if (!ffn_map(&q.a[0], dout, m, H, ldd, 128)) return MOE_ERR_CUDA;
+        q.b[0] = f->mn2;
+        q.b_mn = f->mn2_order;
+        p.a = sa;
+        p.d = sd;
+        p.out_du = static_cast<uint16_t*>(du);
+        if (launch_ffn_products(p, EPI_DACT, st) != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    f->last_launches = 1;
+    // dx, by itself or with the weight gradients in one launch
     FfnProducts r = products(f, workspace);
-    if (dx) {
+    if (dx && narrow_is_faster(n, H, false)) {
+        NarrowProduct d = narrow(n, H, I, workspace);
+        if (!ffn_map(&d.b[0], dg, m, I, I, nt) || !ffn_map(&d.b[1], du, m, I, I, nt)) return MOE_ERR_CUDA;
+        d.a[0] = f->mn1;
+        d.a[1] = f->mn3;
+        d.a_mn = f->mn13_order;
+        d.early = 1;  // behind the kernel that wrote dg and du
+        d.out = static_cast<uint16_t*>(dx);
+        if (launch_ffn_narrow(d, false, NARROW_DX, st) != cudaSuccess) return MOE_ERR_CUDA;
+        ++f->last_launches;
+    } else if (dx) {
         FfnProduct& d = add(r, n, H, I, dx);
         d.sources = 2;
         if (!ffn_map(&d.a[0], dg, m, I, I, 128) || !ffn_map(&d.a[1], du, m, I, I, 128)) return MOE_ERR_CUDA;
@@ -413,8 +449,10 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
             if (!g.a_mn || !g.b_mn) return MOE_ERR_CUDA;
         }
     }
-    if (launch_ffn_products(r, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
-    f->last_launches = 2;
+    if (r.count) {
+        if (launch_ffn_products(r, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
+        ++f->last_launches;
+    }
     return MOE_OK;
 }
 

@@ -78,15 +78,22 @@ bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k)
 cudaError_t launch_mx_product(MxProduct& p, bool gateup, cudaStream_t st);
 
 // One product for few tokens, out[T, R] = tokens W^T, weights as the MMA's M
-// operand (gate/up: W1 and W3).
+// operand.
+enum NarrowKind : int {
+    NARROW_PLAIN = 0,
+    NARROW_GATEUP,  // W1 and W3: h
+    NARROW_DACT,    // dout W2, W2 along M: dg and du
+    NARROW_DX,      // dg W1 + du W3, both along M
+};
 struct NarrowProduct {
     CUtensorMap a[2], as[2];  // weights (128-row boxes) and, MXFP4, their scales
-    CUtensorMap b, bs;        // tokens (narrow_tokens(T)-row boxes) and their scales
+    CUtensorMap b[2], bs;     // tokens (narrow_tokens(T)-row boxes; NARROW_DX: dg, du) and their scales
+    int a_mn;                 // FfnOrder of weights along M
     int T, R, K;
     int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
     int act;
-    uint16_t* out;            // bf16 [T, R]; gate/up of a bf16 block: h
-    float *sa, *sd;           // gate/up: act(g) and u act'(g) for the backward pass, or null
+    uint16_t *out, *du;       // bf16 [T, R]; gate/up of a bf16 block: h; NARROW_DACT: dg, du
+    float *sa, *sd;           // act(g) and u act'(g): NARROW_GATEUP writes them unless null, NARROW_DACT reads
     uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;
@@ -94,9 +101,9 @@ struct NarrowProduct {
     // set by launch_ffn_narrow
     int nt, kstages, slices, stages, ring_bytes, tmem_cols;
 };
-constexpr int kNarrowTokens = 128;  // up to here
+bool narrow_is_faster(int m, int R, bool mx);  // than the 256 x 256 tiles, for out [m, R]
 int narrow_tokens(int m);           // rows of a token tile
-cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream_t st);
+cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t st);
 
 cudaError_t launch_mx_quant(const void* x, bool f32, size_t ldx, int rows, int n, uint8_t* codes, uint8_t* scales,
                             cudaStream_t st);

@@ -15,8 +15,10 @@
 //   warp 1     MMA issuer (and, MXFP4, the scale copies to tensor memory);
 //   all warps  the sum over slices and the epilogue, a warp per token, four rows
 //              per lane: eight lanes hold one block of an MXFP4 h.
-// A stage holds two weight tiles of 128 bytes of K: W1 and W3, or (one matrix)
-// two neighbours along K.  Bounded waits as in ffn_wide.cu.
+// A stage holds two weight tiles of 128 bytes of K: W1 and W3 (which share the
+// tokens); two neighbours along K; or a tile of each source, with its tokens,
+// of dx = dg W1 + du W3.  The backward products read the weights as they lie,
+// 64 of K x 128 of M.  Bounded waits as in ffn_wide.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,6 +27,7 @@
 #include "common.cuh"
 #include "ffn_act.cuh"
 #include "ffn_block.h"
+#include "ffn_box.cuh"
 #include "launch.cuh"
 #include "mxfp4.cuh"
 #include "sm100.cuh"
@@ -47,7 +50,8 @@ struct StageShape {
     int tok, sa, sb, bytes;
 };
 // tok: the token tile(s); sa, sb: scales of the weights and of the tokens.
-__host__ __device__ inline StageShape stage_shape(bool mx, bool gateup, int nt) {
+__host__ __device__ inline StageShape stage_shape(bool mx, int kind, int nt) {
+    const bool gateup = kind == NARROW_GATEUP;
     StageShape s;
     s.tok = 2 * TILE;
     s.sa = s.tok + (gateup ? 1 : 2) * nt * 128;
@@ -71,12 +75,15 @@ __device__ __forceinline__ void add4(float (&a)[4], const float4& v) {
     a[3] += v.w;
 }
 
-template <bool MX, bool GATEUP>
+template <bool MX, int KIND>
 __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__ NarrowProduct p) {
+    constexpr bool GATEUP = KIND == NARROW_GATEUP;      // two accumulators, one token tile
+    constexpr bool SOURCES = KIND == NARROW_DX;         // a stage's tiles: two sources, not two K blocks
+    constexpr bool MN = KIND == NARROW_DACT || KIND == NARROW_DX;  // weights along M
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const StageShape ss = stage_shape(MX, GATEUP, p.nt);
+    const StageShape ss = stage_shape(MX, KIND, p.nt);
     const int stride = stage_stride(ss);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
@@ -112,12 +119,20 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
 
     if (warp == 0) {
         // the whole warp's loop, one lane's body: as in ffn_wide.cu
-        const CUtensorMap *a0 = &p.a[0], *a1 = &p.a[GATEUP ? 1 : 0], *s0 = &p.as[0], *s1 = &p.as[GATEUP ? 1 : 0];
+        const CUtensorMap *a0 = &p.a[0], *a1 = &p.a[GATEUP || SOURCES ? 1 : 0];
+        const CUtensorMap *b0 = &p.b[0], *b1 = &p.b[SOURCES ? 1 : 0];
+        const CUtensorMap *s0 = &p.as[0], *s1 = &p.as[GATEUP ? 1 : 0];
+        const BoxWalk w(MN ? p.a_mn : K_MAJOR, row0);
         const auto weights = [&](int ks, uint32_t st, uint32_t bar) {
-            const int kc = (GATEUP ? ks : 2 * ks) * 32;  // words along K: 128 bytes are 32
+            // K blocks (128 bytes) of the stage's two tiles
+            const int ka = GATEUP || SOURCES ? ks : 2 * ks, kb = GATEUP || SOURCES ? ks : 2 * ks + 1;
             mbar_arrive_expect_tx(bar, ss.bytes);
-            tma_load_3d(st, a0, kc, row0, 0, bar);
-            tma_load_3d(st + TILE, a1, GATEUP ? kc : kc + 32, row0, 0, bar);
+            tma_load_3d(st, a0, w.c0 + ka * w.d0, w.c1 + ka * w.d1, w.c2, bar);
+            tma_load_3d(st + TILE, a1, w.c0 + kb * w.d0, w.c1 + kb * w.d1, w.c2, bar);
+            if (MN && w.two) {
+                tma_load_3d(st + TILE / 2, a0, w.c0 + 32, w.c1 + ka * w.d1, 0, bar);
+                tma_load_3d(st + TILE + TILE / 2, a1, w.c0 + 32, w.c1 + kb * w.d1, 0, bar);
+            }
             if (MX) {
                 const int kt = (GATEUP ? 2 : 4) * ks;
                 tma_load_3d(st + ss.sa, s0, 0, kt, tile, bar);
@@ -125,9 +140,9 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             }
         };
         const auto tokens = [&](int ks, uint32_t st, uint32_t bar) {
-            const int kc = (GATEUP ? ks : 2 * ks) * 32;
-            tma_load_3d(st + ss.tok, &p.b, kc, tok0, 0, bar);
-            if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, &p.b, kc + 32, tok0, 0, bar);
+            const int kc = (GATEUP || SOURCES ? ks : 2 * ks) * 32;  // words along K: 128 bytes are 32
+            tma_load_3d(st + ss.tok, b0, kc, tok0, 0, bar);
+            if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, b1, SOURCES ? kc : kc + 32, tok0, 0, bar);
             if (MX) {
                 const int kt = (GATEUP ? 2 : 4) * ks;
                 tma_load_3d(st + ss.sb, &p.bs, 0, kt, tok0 >> 7, bar);
@@ -168,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             mbar_wait(full0 + 8 * (j % p.stages), (j / p.stages) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         bool ok = true;
-        const uint32_t idesc = idesc_bf16(128, p.nt);
+        const uint32_t idesc = idesc_bf16(128, p.nt) | (MN ? kIdescAMn : 0u);
         int s = 0;
         uint32_t ph = 0;
         for (int i = 0; i < k1 - k0; ++i) {
@@ -193,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint64_t ad = desc_sw128(st + h * TILE);
+                    const uint64_t ad = MN ? desc_sw128_mn(st + h * TILE) : desc_sw128(st + h * TILE);
                     const uint64_t bd = desc_sw128(st + ss.tok + (GATEUP ? 0 : h * p.nt * 128));
                     const uint32_t d = tmem_base + (GATEUP ? h * p.nt : 0);
 #pragma unroll
@@ -203,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                             mma_mxf4(d, ad + 2 * kk, bd + 2 * kk, idesc_mxf4(128, p.nt, 2 * (kk & 1)),
                                      sf + 8 * h + 4 * (kk >> 1), sf + 16 + (GATEUP ? 0 : 8 * h) + 4 * (kk >> 1), acc);
                         else
-                            mma_bf16(d, ad + 2 * kk, bd + 2 * kk, idesc, acc);
+                            mma_bf16(d, ad + (MN ? 128 : 2) * kk, bd + 2 * kk, idesc, acc);
                     }
                 }
                 mma_commit(empty0 + 8 * s);
@@ -289,6 +304,13 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             } else if (r < p.R) {  // R is a multiple of 8: whole quads
                 const size_t at = t * p.R + r;
                 float o[4];
+                if (KIND == NARROW_DACT) {  // dg = dh d; du = dh a
+                    const float4 a = *reinterpret_cast<const float4*>(p.sa + at), d = *reinterpret_cast<const float4*>(p.sd + at);
+                    const float* h = v0[x];
+                    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(h[0] * d.x, h[1] * d.y), pack_bf16x2(h[2] * d.z, h[3] * d.w));
+                    *reinterpret_cast<uint2*>(p.du + at) = make_uint2(pack_bf16x2(h[0] * a.x, h[1] * a.y), pack_bf16x2(h[2] * a.z, h[3] * a.w));
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     o[i] = v0[x][i];
@@ -336,8 +358,8 @@ int clusters_resident(int size) {
         cfg.attrs = &at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaFuncSetAttribute(ffn_narrow<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, ffn_narrow<false, true>, &cfg) != cudaSuccess) {
+        if (cudaFuncSetAttribute(ffn_narrow<false, NARROW_GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, ffn_narrow<false, NARROW_GATEUP>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = sms() / size * 3 / 4;
         }
@@ -346,10 +368,10 @@ int clusters_resident(int size) {
     return k.load();
 }
 
-template <bool MX, bool GATEUP>
+template <bool MX, int KIND>
 cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
     static cudaError_t attr =
-        cudaFuncSetAttribute(ffn_narrow<MX, GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaFuncSetAttribute(ffn_narrow<MX, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ceil_div(p.R, 128) * p.slices, ceil_div(p.T, p.nt));
@@ -365,17 +387,27 @@ cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ffn_narrow<MX, GATEUP>, p);
+    return cudaLaunchKernelEx(&cfg, ffn_narrow<MX, KIND>, p);
 }
 
 }  // namespace
 
+// Measured as whole blocks, narrow / wide in us: bf16 7168 x 2048 at 256 tokens
+// 35.6 / 48.8, at 384 54.2 / 50.1; 2048 x 8192 at 256 38.8 / 55.2, at 384 65.2 /
+// 64.8; 2048 x 768 (few tiles) at 512 18.5 / 21.2, at 1024 22.6 / 21.5.  MXFP4
+// 7168 x 2048 at 128 20.7 / 25.3, 2048 x 8192 at 256 27.4 / 24.5.
+bool narrow_is_faster(int m, int R, bool mx) {
+    if (mx) return m <= 128;
+    return m <= 256 || (m <= 512 && ceil_div(m, 256) * ceil_div(R, 256) * 4 <= sms() / 2);
+}
+
 int narrow_tokens(int m) { return std::min(128, (m + 15) / 16 * 16); }
 
-cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream_t st) {
+cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t st) {
+    const bool gateup = kind == NARROW_GATEUP;
     p.nt = narrow_tokens(p.T);
-    p.kstages = ceil_div(p.K, (mx ? 256 : 64) * (gateup ? 1 : 2));
-    const StageShape ss = stage_shape(mx, gateup, p.nt);
+    p.kstages = ceil_div(p.K, (mx ? 256 : 64) * (gateup || kind == NARROW_DX ? 1 : 2));
+    const StageShape ss = stage_shape(mx, kind, p.nt);
     const int stride = stage_stride(ss);
     // Two CTAs per SM for up to 16 tokens: the next kernel's weights then arrive
     // while this one drains (7168 x 2048, one token: 20.2 us, with one CTA of
@@ -403,8 +435,13 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, bool gateup, cudaStream
             p.slices = s;
             break;
         }
-    if (mx) return gateup ? launch<true, true>(p, smem, st) : launch<true, false>(p, smem, st);
-    return gateup ? launch<false, true>(p, smem, st) : launch<false, false>(p, smem, st);
+    if (mx) return gateup ? launch<true, NARROW_GATEUP>(p, smem, st) : launch<true, NARROW_PLAIN>(p, smem, st);
+    switch (kind) {
+        case NARROW_GATEUP: return launch<false, NARROW_GATEUP>(p, smem, st);
+        case NARROW_DACT: return launch<false, NARROW_DACT>(p, smem, st);
+        case NARROW_DX: return launch<false, NARROW_DX>(p, smem, st);
+        default: return launch<false, NARROW_PLAIN>(p, smem, st);
+    }
 }
 
 }  // namespace moe

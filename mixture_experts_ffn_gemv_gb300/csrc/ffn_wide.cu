@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "ffn_act.cuh"
 #include "ffn_block.h"
+#include "ffn_box.cuh"
 #include "launch.cuh"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -79,20 +80,6 @@ __device__ __forceinline__ void store_row32f(float* p, int n, const uint32_t (&f
         if (8 * i < n) st_global_v8(p + 8 * i, w);
     }
 }
-
-// Coordinates of an operand's box of 128 rows of M (or N) from m0 on: the
-// first K block's, and the step per K block; two: the tile takes two boxes.
-struct BoxWalk {
-    int c0, c1, c2, d0, d1;
-    bool two;
-    __device__ __forceinline__ BoxWalk(int order, int m0)
-        : c0(order == MN_ROWS ? m0 / 2 : 0),
-          c1(order == K_MAJOR ? m0 : 0),
-          c2(order == MN_BLOCKS ? m0 / 64 : 0),
-          d0(order == K_MAJOR ? BK / 2 : 0),
-          d1(order == K_MAJOR ? 0 : BK),
-          two(order == MN_ROWS) {}
-};
 
 struct Item {
     int op, mt, nt;

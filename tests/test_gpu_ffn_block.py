@@ -173,7 +173,8 @@ def test_mx_linear_fp32_strided_and_streams(B):
 # ---------------------------------------------------------------- the block
 
 FFN_SIZES = [(1, 2048, 768), (1, 8, 8), (3, 24, 40), (16, 256, 128), (17, 136, 264), (48, 1024, 512), (65, 520, 1032),
-             (128, 256, 256), (200, 512, 384), (333, 1032, 2056), (777, 1016, 680)]
+             (128, 256, 256), (200, 512, 384), (333, 1032, 2056), (777, 1016, 680), (130, 1032, 72), (256, 328, 200),
+             (257, 4104, 64), (500, 200, 136)]
 
 
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
