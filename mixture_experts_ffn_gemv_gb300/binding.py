@@ -379,6 +379,7 @@ class MoeLayer:
 # checks test the common case (dense rows) first and word the refusal after.
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_empty = torch.empty
 
 
 def _need(ok, what: str):
@@ -447,8 +448,9 @@ def moe_mxfp4_quant(x, stream=None):
     _need(x.dim() == 2, "x: [rows, n]")
     rows, n = x.shape
     ld = _rows(x, n, "x", f32=True)
-    codes = x.new_empty((rows, n // 2), dtype=_U8)
-    scales = x.new_empty(mxfp4_scales_shape(rows, n), dtype=_U8)
+    dev = x.device
+    codes = _empty((rows, n // 2), dtype=_U8, device=dev)
+    scales = _empty(mxfp4_scales_shape(rows, n), dtype=_U8, device=dev)
     f32 = x.dtype is _F32
     rc = (lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
         x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), _on(x, stream))
@@ -461,7 +463,7 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
     """The values (bf16 [rows, n]) that codes and packed scales stand for."""
     lib = _lib or load_library()
     rows, n = _mx_matrix(codes, scales, "x")
-    out = codes.new_empty((rows, n), dtype=_BF16)
+    out = _empty((rows, n), dtype=_BF16, device=codes.device)
     rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), _on(codes, stream))
     if rc:
         raise MoeError(rc, "moe_mxfp4_dequant")
@@ -504,7 +506,7 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     n, kb = _mx_matrix(b_codes, b_scales, "b")
     _need(k == kb, f"k differs: {k} and {kb}")
     if out is None:
-        out = a_codes.new_empty((m, n), dtype=_BF16)
+        out = _empty((m, n), dtype=_BF16, device=a_codes.device)
     else:
         _dense(out, _BF16, (m, n), "out")
     st = _on(a_codes, stream)
@@ -524,7 +526,7 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
     ld = _rows(x, k, "x", f32=True)
     m = x.shape[0]
     if out is None:
-        out = x.new_empty((m, n), dtype=_BF16)
+        out = _empty((m, n), dtype=_BF16, device=x.device)
     else:
         _dense(out, _BF16, (m, n), "out")
     st = _on(x, stream)
@@ -622,7 +624,10 @@ class GatedFfn:
             _dense(out, _BF16, (m, self.hidden), "out")
         if m > self._fits[0]:
             self.workspace(m, False, x.device)
-        saved = (x.new_empty((2, m, self.inter), dtype=_F32), x.new_empty((m, self.inter))) if save else None
+        saved = None
+        if save:
+            saved = (_empty((2, m, self.inter), dtype=_F32, device=x.device),
+                     _empty((m, self.inter), dtype=_BF16, device=x.device))
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
                                       saved[0].data_ptr() if save else None,
                                       saved[1].data_ptr() if save else None, *self._ws_at, _on(x, stream))
@@ -639,14 +644,19 @@ class GatedFfn:
         _need(dout.shape[0] == m, "dout and x differ in rows")
         _dense(saved[0], _F32, (2, m, I), "saved[0]")
         _dense(saved[1], _BF16, (m, I), "saved[1]")
-        new = x.new_empty if m else x.new_zeros
-        dx = new((m, H)) if need_dx else None
-        dw1, dw3, dw2 = (new((I, H)), new((I, H)), new((H, I))) if need_dw else (None,) * 3
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+        dw1 = dw3 = dw2 = None
+        if need_dw:
+            new, dev = _empty if m else torch.zeros, x.device
+            dw1 = new((I, H), dtype=_BF16, device=dev)
+            dw3 = new((I, H), dtype=_BF16, device=dev)
+            dw2 = new((H, I), dtype=_BF16, device=dev)
         if m > self._fits[1]:
             self.workspace(m, True, x.device)
-        at = [None if t is None else t.data_ptr() for t in (dx, dw1, dw3, dw2)]
-        rc = self.lib.moe_ffn_backward(self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved[0].data_ptr(),
-                                       saved[1].data_ptr(), m, *at, *self._ws_at, _on(x, stream))
+        rc = self.lib.moe_ffn_backward(
+            self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved[0].data_ptr(), saved[1].data_ptr(), m,
+            dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else
+                                                  (None, None, None)), *self._ws_at, _on(x, stream))
         if rc:
             raise MoeError(rc, "moe_ffn_backward")
         return dx, dw1, dw3, dw2
