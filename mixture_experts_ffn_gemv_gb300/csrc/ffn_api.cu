@@ -430,14 +430,17 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
         d.out = static_cast<uint16_t*>(dx);
         if (launch_ffn_narrow(d, false, NARROW_DX, st) != cudaSuccess) return MOE_ERR_CUDA;
         ++f->last_launches;
-    } else if (dx) {
+    }
+    const auto add_dx = [&] {
         FfnProduct& d = add(r, n, H, I, dx);
         d.sources = 2;
-        if (!ffn_map(&d.a[0], dg, m, I, I, 128) || !ffn_map(&d.a[1], du, m, I, I, 128)) return MOE_ERR_CUDA;
         d.b[0] = f->mn1;
         d.b[1] = f->mn3;
         d.b_mn = f->mn13_order;
-    }
+        return ffn_map(&d.a[0], dg, m, I, I, 128) && ffn_map(&d.a[1], du, m, I, I, 128);
+    };
+    const bool wide_dx = dx && !narrow_is_faster(n, H, false), dx_first = 2 * ceil_div(I, 64) >= ceil_div(n, 64);
+    if (wide_dx && dx_first && !add_dx()) return MOE_ERR_CUDA;
     if (dw) {
         // dw1 = dg^T x, dw3 = du^T x, dw2 = dout^T h
         const void* lhs[3] = {dg, du, dout};
@@ -449,6 +452,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
             if (!g.a_mn || !g.b_mn) return MOE_ERR_CUDA;
         }
     }
+    if (wide_dx && !dx_first && !add_dx()) return MOE_ERR_CUDA;
     if (r.count) {
         if (launch_ffn_products(r, EPI_STORE, st) != cudaSuccess) return MOE_ERR_CUDA;
         ++f->last_launches;

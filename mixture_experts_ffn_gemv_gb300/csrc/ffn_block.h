@@ -38,9 +38,10 @@ struct FfnProduct {
 };
 constexpr int kMaxProducts = 4;
 struct FfnProducts {
-    FfnProduct p[kMaxProducts];
+    FfnProduct p[kMaxProducts];  // longest reductions (sources * kblocks) first
     int count;
-    int first[kMaxProducts + 1];  // first work item of each product
+    int first[kMaxProducts + 1];  // first work item of each product; set by launch_ffn_products, as are
+    int dear, fill;               // ... the order of the items (ffn_wide.cu, Turns)
     int act;
     // a = act(g) and d = u act'(g), fp32 [M, N]: written by EPI_GATEUP_SAVE, read by EPI_DACT
     float *a, *d;

@@ -96,6 +96,29 @@ __device__ __forceinline__ Item item_of(const FfnProducts& p, int t) {
     return it;
 }
 
+// The work items of CTA pair c of n, in order.  The first `dear` items (the
+// products with the longest reductions come first) go round; the pairs that
+// then have one fewer take `fill` of the others each instead, and the rest go
+// round again, from those pairs on.  (dx and three weight gradients of 4096 x 2048 x 8192: 1152 K
+// blocks on the fullest pair by plain turns, 1088 so, 1078 on the average.)
+struct Turns {
+    int a, b, c0, n, pairs, total, dear, rest;
+    __device__ __forceinline__ Turns(const FfnProducts& p, int pair, int pairs_)
+        : c0(pair), pairs(pairs_), total(p.first[p.count]), dear(p.dear) {
+        const int r = dear % pairs;
+        a = pair < dear ? (dear - pair + pairs - 1) / pairs : 0;
+        b = r && pair >= r ? p.fill : 0;
+        n = pairs - r;
+        rest = dear + (r ? n * p.fill : 0);
+    }
+    __device__ __forceinline__ int item(int i) const {  // -1: no more
+        if (i < a) return c0 + i * pairs;
+        if (i < a + b) return dear + (i - a) * n + c0 - (pairs - n);
+        const int t = rest + (c0 + n) % pairs + (i - a - b) * pairs;
+        return t < total ? t : -1;
+    }
+};
+
 template <int EPI>
 __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
     constexpr int EPI_WARPS = Shape<EPI>::EPI_WARPS, STAGES = Shape<EPI>::STAGES, BAR_OFF = Shape<EPI>::BAR_OFF;
@@ -137,8 +160,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
     cluster_sync();  // both CTAs' barriers exist before either signals the other
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = p.first[p.count];
-    const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+    const Turns turns(p, blockIdx.x >> 1, gridDim.x >> 1);
     const uint32_t lead_full0 = mapa(full0, 0), lead_tempty0 = mapa(tempty0, 0);
 
     if (warp == 0) {
@@ -148,7 +170,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         // by order, took 620 to 790 cycles a stage: more than the MMAs.)
         uint32_t s = 0, ph = 1, n = 0;
         bool ok = true;
-        for (int t = cl; t < total && ok; t += ncl) {
+        for (int i = 0, t; ok && (t = turns.item(i)) >= 0; ++i) {
             if (*abort_flag) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
@@ -198,7 +220,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         if (leader) {
             uint32_t s = 0, ph = 0, tc = 0;
             bool ok = true;
-            for (int t = cl; t < total && ok; t += ncl, ++tc) {
+            for (int t; ok && (t = turns.item((int)tc)) >= 0; ++tc) {
                 if (*abort_flag) break;
                 const FfnProduct& q = p.p[item_of(p, t).op];
                 const uint32_t idesc = idesc_bf16(2 * BM, BN) | (q.a_mn ? kIdescAMn : 0u) | (q.b_mn ? kIdescBMn : 0u);
@@ -248,7 +270,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         const int part = (warp - 2) >> 2;  // its share of the tile's columns
         const uint32_t stg = sbase + Shape<EPI>::STG_OFF + (warp - 2) * 4096;
         uint32_t tc = 0;
-        for (int t = cl; t < total; t += ncl, ++tc) {
+        for (int t; (t = turns.item((int)tc)) >= 0; ++tc) {
             if (*abort_flag) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
@@ -413,6 +435,15 @@ cudaError_t launch_ffn_products(FfnProducts& p, int epilogue, cudaStream_t st) {
         p.first[i + 1] = p.first[i] + q.m_tiles * q.n_tiles;
         if (epilogue == EPI_STORE && !ffn_map(&q.o, q.out, q.M, q.N, q.N, 32)) return cudaErrorUnknown;
     }
+    // items of the longest reduction, and how many of the others weigh as much
+    // (an epilogue counted as 6 K blocks)
+    const int total = p.first[p.count], pairs = std::min(sms() / 2, total);
+    const auto cost = [&](int i) { return p.p[i].sources * p.p[i].kblocks + 6; };
+    int k = 1;
+    while (k < p.count && cost(k) == cost(0)) ++k;
+    p.dear = p.first[k];
+    p.fill = 0;
+    if (k < p.count) p.fill = std::min(cost(0) / cost(p.count - 1), (total - p.dear) / (pairs - p.dear % pairs));
     switch (epilogue) {
         case EPI_GATEUP: return launch<EPI_GATEUP>(p, st);
         case EPI_GATEUP_SAVE: return launch<EPI_GATEUP_SAVE>(p, st);
