@@ -76,9 +76,10 @@ MOE_API int moe_ffn_workspace_size(const moe_ffn* ffn, int64_t m, int backward, 
 /* out[t, :] = the block applied to x[t, :].
  *   x bf16 [m, H] with row stride ldx >= H (a multiple of 8); out bf16 [m, H].
  *   saved, saved_h (bf16 weights only, else NULL; both or neither, 32-byte
- *   aligned): with g = x W1^T and u = x W3^T, fp32 [2, m, I] that receives
- *   act(g) and u act'(g), and bf16 [m, I] that receives h = act(g) u, for
- *   moe_ffn_backward.  (fp32: rounded to bf16 they would be the largest error
+ *   aligned): with g = x W1^T and u = x W3^T, fp32 [2, ceil(m / 32),
+ *   ceil(I / 32), 4, 32, 8] that receives act(g) and u act'(g) (row r, column c
+ *   at [r / 32, c / 32, c % 32 / 8, r % 32, c % 8]; what pads m and I is left as
+ *   it is), and bf16 [m, I] that receives h = act(g) u, for moe_ffn_backward.  (fp32: rounded to bf16 they would be the largest error
  *   of the gradients.)
  * The intermediate h is rounded to bf16 (MXFP4: to MXFP4, straight from the
  * fp32 products), x to MXFP4 for MXFP4 weights; sums are fp32. */

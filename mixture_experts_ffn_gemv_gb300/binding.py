@@ -612,10 +612,13 @@ class GatedFfn:
             raise MoeError(rc, "moe_device_status")
         return code.value
 
+    def _saved_shape(self, m: int):
+        return 2, (m + 31) // 32, (self.inter + 31) // 32, 4, 32, 8
+
     def forward(self, x, save=False, out=None, stream=None):
         """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
-        (out, saved) for backward: saved is (fp32 [2, m, I]: act(g) and u act'(g), bf16 [m, I]: h) with
-        g = x w1^T, u = x w3^T, h = act(g) u."""
+        (out, saved) for backward: with g = x w1^T, u = x w3^T, saved is (fp32: act(g) and u act'(g) in
+        blocks of 32 x 32, see moe_ffn_block.h; bf16 [m, I]: h = act(g) u)."""
         ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
         if out is None:
@@ -626,7 +629,7 @@ class GatedFfn:
             self.workspace(m, False, x.device)
         saved = None
         if save:
-            saved = (_empty((2, m, self.inter), dtype=_F32, device=x.device),
+            saved = (_empty(self._saved_shape(m), dtype=_F32, device=x.device),
                      _empty((m, self.inter), dtype=_BF16, device=x.device))
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
                                       saved[0].data_ptr() if save else None,
@@ -642,7 +645,7 @@ class GatedFfn:
         ldd, ldx = _rows(dout, H, "dout"), _rows(x, H, "x")
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
-        _dense(saved[0], _F32, (2, m, I), "saved[0]")
+        _dense(saved[0], _F32, self._saved_shape(m), "saved[0]")
         _dense(saved[1], _BF16, (m, I), "saved[1]")
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
         dw1 = dw3 = dw2 = None

@@ -9,6 +9,7 @@
 
 #include "common.cuh"
 #include "ffn_block.h"
+#include "ffn_box.cuh"
 
 using namespace moe;
 
@@ -125,7 +126,7 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
                  cudaStream_t st) {
     const int H = f->cfg.hidden, I = f->cfg.inter;
     const uint32_t nt = (uint32_t)narrow_tokens(m);
-    float* saved_d = saved ? saved + (size_t)m * I : nullptr;
+    float* saved_d = saved ? saved + saved_floats(m, I) : nullptr;
     if (narrow_is_faster(m, I, false)) {
         NarrowProduct g = narrow(m, I, H, ws);
         if (!ffn_map(&g.b[0], x, m, H, ldx, nt)) return MOE_ERR_CUDA;
@@ -393,7 +394,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
     void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du);
-    float *sa = const_cast<float*>(saved), *sd = sa + (size_t)m * I;  // only read
+    float *sa = const_cast<float*>(saved), *sd = sa + saved_floats(m, I);  // only read
     const uint32_t nt = (uint32_t)narrow_tokens(n);
     // dh = dout W2 and, in its epilogue, dg and du
     if (narrow_is_faster(n, I, false)) {

@@ -43,7 +43,7 @@ struct FfnProducts {
     int first[kMaxProducts + 1];  // first work item of each product; set by launch_ffn_products, as are
     int dear, fill;               // ... the order of the items (ffn_wide.cu, Turns)
     int act;
-    // a = act(g) and d = u act'(g), fp32 [M, N]: written by EPI_GATEUP_SAVE, read by EPI_DACT
+    // a = act(g) and d = u act'(g), fp32, in the order of saved_at: written by EPI_GATEUP_SAVE, read by EPI_DACT
     float *a, *d;
     uint16_t* out_du;       // EPI_DACT (out: dg)
     WsHeader* hdr;
@@ -94,7 +94,7 @@ struct NarrowProduct {
     int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
     int act;
     uint16_t *out, *du;       // bf16 [T, R]; gate/up of a bf16 block: h; NARROW_DACT: dg, du
-    float *sa, *sd;           // act(g) and u act'(g): NARROW_GATEUP writes them unless null, NARROW_DACT reads
+    float *sa, *sd;           // act(g) and u act'(g) (saved_at): NARROW_GATEUP writes them unless null, NARROW_DACT reads
     uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;

@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                 const size_t at = t * p.R + r;
                 float o[4];
                 if (KIND == NARROW_DACT) {  // dg = dh d; du = dh a
-                    const float4 a = *reinterpret_cast<const float4*>(p.sa + at), d = *reinterpret_cast<const float4*>(p.sd + at);
+                    const size_t sat = saved_at(t, r, p.R);
+                    const float4 a = *reinterpret_cast<const float4*>(p.sa + sat), d = *reinterpret_cast<const float4*>(p.sd + sat);
                     const float* h = v0[x];
                     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(h[0] * d.x, h[1] * d.y), pack_bf16x2(h[2] * d.z, h[3] * d.w));
                     *reinterpret_cast<uint2*>(p.du + at) = make_uint2(pack_bf16x2(h[0] * a.x, h[1] * a.y), pack_bf16x2(h[2] * a.z, h[3] * a.w));
@@ -323,8 +324,9 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                     }
                 }
                 if (GATEUP && p.sa) {
-                    *reinterpret_cast<float4*>(p.sa + at) = make_float4(v0[x][0], v0[x][1], v0[x][2], v0[x][3]);
-                    *reinterpret_cast<float4*>(p.sd + at) = make_float4(v1[x][0], v1[x][1], v1[x][2], v1[x][3]);
+                    const size_t sat = saved_at(t, r, p.R);
+                    *reinterpret_cast<float4*>(p.sa + sat) = make_float4(v0[x][0], v0[x][1], v0[x][2], v0[x][3]);
+                    *reinterpret_cast<float4*>(p.sd + sat) = make_float4(v1[x][0], v1[x][1], v1[x][2], v1[x][3]);
                 }
                 *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             }

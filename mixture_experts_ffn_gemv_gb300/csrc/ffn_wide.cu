@@ -61,23 +61,24 @@ struct Shape {
     static_assert(SMEM_BYTES <= 227 * 1024, "fits one SM's shared memory");
 };
 
-// n of 32 fp32 of a row (n a multiple of 8; the rest zero), and the way back.
-__device__ __forceinline__ void load_row32(const float* p, int n, float (&f)[32]) {
+// A lane's row of a saved block (ffn_box.cuh, saved_at): 32 values, n of them in
+// the matrix (n a multiple of 8; the rest zero); a warp moves 1 KB at a time.
+__device__ __forceinline__ void load_saved(const float* p, int n, float (&f)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[8] = {};
-        if (8 * i < n) ld_global_v8(p + 8 * i, w);
+        if (8 * i < n) ld_global_v8(p + 256 * i, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[8 * i + k] = __uint_as_float(w[k]);
     }
 }
-__device__ __forceinline__ void store_row32f(float* p, int n, const uint32_t (&f)[32]) {
+__device__ __forceinline__ void store_saved(float* p, int n, const uint32_t (&f)[32]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = f[8 * i + k];
-        if (8 * i < n) st_global_v8(p + 8 * i, w);
+        if (8 * i < n) st_global_v8(p + 256 * i, w);
     }
 }
 
@@ -315,8 +316,9 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                         else o[i >> 1] = __float_as_uint(h);
                     }
                     if (ok) {
-                        store_row32f(p.a + at, N - col0, gv);
-                        store_row32f(p.d + at, N - col0, uv);
+                        const size_t sat = saved_at(row0 + lane, col0, N);
+                        store_saved(p.a + sat, N - col0, gv);
+                        store_saved(p.d + sat, N - col0, uv);
                     }
                 } else {
 #pragma unroll
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                         const int n = N - col0 - 32 * e;
                         float f[32];
                         uint32_t o[16];
-                        load_row32((x ? p.d : p.a) + at + 32 * e, n, f);
+                        load_saved((x ? p.d : p.a) + saved_at(row0 + lane, col0, N) + 1024 * e, n, f);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             o[i] = pack_bf16x2(__uint_as_float(dv[e][2 * i]) * f[2 * i],
