@@ -304,27 +304,16 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                 tmem_wait_ld();
                 release();
                 if (EPI == EPI_GATEUP_SAVE) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float u = __uint_as_float(uv[i]);
-                        float a, slope;
-                        act_slope(__uint_as_float(gv[i]), p.act, a, slope);
-                        gv[i] = __float_as_uint(a);
-                        uv[i] = __float_as_uint(u * slope);
-                        const float h = a * u;
-                        if (i & 1) o[i >> 1] = pack_bf16x2(__uint_as_float(o[i >> 1]), h);
-                        else o[i >> 1] = __float_as_uint(h);
-                    }
+                    glu32_save(gv, uv, o, p.act);
                     if (ok) {
                         const size_t sat = saved_at(row0 + lane, col0, N);
                         store_saved(p.a + sat, N - col0, gv);
                         store_saved(p.d + sat, N - col0, uv);
                     }
                 } else {
+                    glu32(gv, uv, p.act);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = pack_bf16x2(glu(__uint_as_float(gv[2 * i]), __uint_as_float(uv[2 * i]), p.act),
-                                           glu(__uint_as_float(gv[2 * i + 1]), __uint_as_float(uv[2 * i + 1]), p.act));
+                    for (int i = 0; i < 16; ++i) o[i] = pack_bf16x2(__uint_as_float(gv[2 * i]), __uint_as_float(gv[2 * i + 1]));
                 }
                 if (ok) store_row32(q.out + at, N - col0, (N & 15) == 0, o);
             } else if (EPI == EPI_DACT) {

@@ -281,14 +281,12 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
                 const int col = nt * 128 + part * 32;
                 uint32_t s = 0;  // blocks past the last column: 0
                 if (col < p.N) {
-                    float h[32];
-                    uint32_t a = 0;
+                    glu32(v[0], v[1], p.act);
+                    const float* h = reinterpret_cast<const float*>(v[0]);
+                    float a = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        h[i] = glu(__uint_as_float(v[0][i]), __uint_as_float(v[1][i]), p.act);
-                        a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
-                    }
-                    s = mx_scale(a);
+                    for (int i = 0; i < 32; ++i) a = max_nan(a, fabsf(h[i]));
+                    s = mx_scale(__float_as_uint(a));
                     const float inv = mx_inverse(s);
                     uint4 w = make_uint4(mx_codes8(h, inv), mx_codes8(h + 8, inv), mx_codes8(h + 16, inv), mx_codes8(h + 24, inv));
                     if (s == 255u) w = make_uint4(0, 0, 0, 0);

@@ -13,6 +13,12 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t amax_bits) {
     const uint32_t f = amax_bits >> 23;
     return f == 255u ? 255u : (f < 2u ? 0u : f - 2u);
 }
+// The larger of two magnitudes; a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // 2^(127 - s): v times it is v / 2^(s - 127), exact for every value that does
 // not underflow far below e2m1's smallest midpoint.  0 for a NaN scale, so
 // that finite elements of such a block give zero codes.
