@@ -1,6 +1,7 @@
 """GB300-native MoE FFN layer forward (router, softmax top-k, permute, grouped
 SwiGLU experts, weighted unpermute-reduce, shared-expert add) behind a C-ABI
-CUDA library.
+CUDA library, with the dense gated feed-forward block (forward, backward, and
+served from MXFP4 weights) and the MXFP4 operators beside it.
 
 The compute lives in ``libmoe_ffn_gb300.so`` (hand-written sm_103a kernels);
 ``binding`` marshals torch tensors into its entry points.  The library is
@@ -13,7 +14,7 @@ __all__ = ["LayerShape", "Workload", "WORKLOADS", "TINY", "QWEN3_30B_A3B", "DEEP
 
 def __getattr__(name):
     # the binding (and with it the CUDA library) loads only when asked for
-    if name in ("binding", "MoeLayer", "build_library"):
+    if name in ("binding", "MoeLayer", "GatedFfn", "build_library"):
         import importlib
         binding = importlib.import_module(__name__ + ".binding")
         if name == "binding":

@@ -407,9 +407,10 @@ def _dense(t, dtype, shape, what: str):
         raise ValueError(f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
 
 
-def _on(t, stream) -> int:
-    """The CUDA stream to launch on: `stream`, or the current one of t's device."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+def _on(t) -> int:
+    """The current CUDA stream of t's device.  A call that is given a stream makes it the current
+    one first, so that what it allocates belongs to the stream that writes it."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def mxfp4_scales_shape(rows: int, n: int):
@@ -444,6 +445,9 @@ def _mx_matrix(codes, scales, what: str):
 
 def moe_mxfp4_quant(x, stream=None):
     """x bf16 or fp32 [rows, n] (device; n a multiple of 32) -> (codes uint8 [rows, n/2], packed scales uint8)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mxfp4_quant(x)
     lib = _lib or load_library()
     _need(x.dim() == 2, "x: [rows, n]")
     rows, n = x.shape
@@ -453,7 +457,7 @@ def moe_mxfp4_quant(x, stream=None):
     scales = _empty(mxfp4_scales_shape(rows, n), dtype=_U8, device=dev)
     f32 = x.dtype is _F32
     rc = (lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
-        x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), _on(x, stream))
+        x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), _on(x))
     if rc:
         raise MoeError(rc, "moe_mxfp4_quant_f32" if f32 else "moe_mxfp4_quant")
     return codes, scales
@@ -461,10 +465,13 @@ def moe_mxfp4_quant(x, stream=None):
 
 def moe_mxfp4_dequant(codes, scales, stream=None):
     """The values (bf16 [rows, n]) that codes and packed scales stand for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mxfp4_dequant(codes, scales)
     lib = _lib or load_library()
     rows, n = _mx_matrix(codes, scales, "x")
     out = _empty((rows, n), dtype=_BF16, device=codes.device)
-    rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), _on(codes, stream))
+    rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), _on(codes))
     if rc:
         raise MoeError(rc, "moe_mxfp4_dequant")
     return out
@@ -474,15 +481,15 @@ _spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on 
 
 
 def _space(like, stream: int, need: int) -> torch.Tensor:
-    """A workspace of at least `need` bytes for calls on `stream`, its header zeroed before first use."""
+    """A workspace of at least `need` bytes for calls on `stream`, the current one, its header
+    zeroed before first use.  One made while a graph is captured belongs to that graph alone."""
     key = (like.get_device(), stream)
     ws = _spaces.get(key)
     if ws is None or ws.numel() < need:
-        ws = like.new_empty((max(need, 1 << 16),), dtype=_U8)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if stream else
-                               torch.cuda.default_stream(like.device)):
-            ws[:256].zero_()
-        _spaces[key] = ws
+        ws = _empty((max(need, 1 << 16),), dtype=_U8, device=like.device)
+        ws[:256].zero_()
+        if not torch.cuda.is_current_stream_capturing():
+            _spaces[key] = ws
     return ws
 
 
@@ -501,6 +508,9 @@ def mxfp4_device_status(stream=None) -> int:
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     """A [m, k] times B [n, k] transposed, both MXFP4 (codes, packed scales) -> bf16 [m, n]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out)
     lib = _lib or load_library()
     m, k = _mx_matrix(a_codes, a_scales, "a")
     n, kb = _mx_matrix(b_codes, b_scales, "b")
@@ -509,7 +519,7 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
         out = _empty((m, n), dtype=_BF16, device=a_codes.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(a_codes, stream)
+    st = _on(a_codes)
     ws = _space(a_codes, st, 256)
     rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n, k,
                             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
@@ -521,6 +531,9 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
 def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
     """x (bf16 or fp32 [m, k]) quantised to MXFP4 per call, times a weight matrix [n, k] held in
     MXFP4 -> bf16 [m, n]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_mxfp4_linear(x, codes, scales, out)
     lib = _lib or load_library()
     n, k = _mx_matrix(codes, scales, "w")
     ld = _rows(x, k, "x", f32=True)
@@ -529,7 +542,7 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
         out = _empty((m, n), dtype=_BF16, device=x.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(x, stream)
+    st = _on(x)
     # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
     ws = _space(x, st, 1024 + m * k // 2 + (m + 127) // 128 * ((k + 127) // 128) * 512)
     f32 = x.dtype is _F32
@@ -619,6 +632,9 @@ class GatedFfn:
         """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
         (out, saved) for backward: with g = x w1^T, u = x w3^T, saved is (fp32: act(g) and u act'(g) in
         blocks of 32 x 32, see moe_ffn_block.h; bf16 [m, I]: h = act(g) u)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, save, out)
         ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
         if out is None:
@@ -633,7 +649,7 @@ class GatedFfn:
                      _empty((m, self.inter), dtype=_BF16, device=x.device))
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
                                       saved[0].data_ptr() if save else None,
-                                      saved[1].data_ptr() if save else None, *self._ws_at, _on(x, stream))
+                                      saved[1].data_ptr() if save else None, *self._ws_at, _on(x))
         if rc:
             raise MoeError(rc, "moe_ffn_forward")
         return (out, saved) if save else out
@@ -641,6 +657,9 @@ class GatedFfn:
     def backward(self, dout, x, saved, need_dx=True, need_dw=True, stream=None):
         """Gradients (dx, dw1, dw3, dw2), bf16, of the forward pass that saved `saved`; None
         for those not needed.  No tokens: the weight gradients are zero."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(dout, x, saved, need_dx, need_dw)
         H, I = self.hidden, self.inter
         ldd, ldx = _rows(dout, H, "dout"), _rows(x, H, "x")
         m = x.shape[0]
@@ -659,7 +678,7 @@ class GatedFfn:
         rc = self.lib.moe_ffn_backward(
             self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved[0].data_ptr(), saved[1].data_ptr(), m,
             dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else
-                                                  (None, None, None)), *self._ws_at, _on(x, stream))
+                                                  (None, None, None)), *self._ws_at, _on(x))
         if rc:
             raise MoeError(rc, "moe_ffn_backward")
         return dx, dw1, dw3, dw2
