@@ -109,6 +109,12 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
         tmem_relinquish();
     }
+    if (warp == 2 && lane < 2) {
+        prefetch_tmap(&p.a[GATEUP || SOURCES ? lane : 0]);
+        prefetch_tmap(&p.b[SOURCES ? lane : 0]);
+        if (MX) prefetch_tmap(&p.as[GATEUP ? lane : 0]);
+        if (MX) prefetch_tmap(&p.bs);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -124,8 +124,6 @@ template <int EPI>
 __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __grid_constant__ FfnProducts p) {
     constexpr int EPI_WARPS = Shape<EPI>::EPI_WARPS, STAGES = Shape<EPI>::STAGES, BAR_OFF = Shape<EPI>::BAR_OFF;
     constexpr bool GATEUP = EPI == EPI_GATEUP || EPI == EPI_GATEUP_SAVE;
-    pdl_wait();
-    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -156,11 +154,18 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    if (warp == 2 && lane < 2 * p.count) {
+        const FfnProduct& q = p.p[lane >> 1];
+        prefetch_tmap(&q.a[lane & 1 & (q.sources - 1)]);
+        prefetch_tmap(&q.b[GATEUP ? rank : lane & 1 & (q.sources - 1)]);
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before either signals the other
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();  // all of the above ran beside the preceding kernel's end
+    pdl_trigger();
     const Turns turns(p, blockIdx.x >> 1, gridDim.x >> 1);
     const uint32_t lead_full0 = mapa(full0, 0), lead_tempty0 = mapa(tempty0, 0);
 

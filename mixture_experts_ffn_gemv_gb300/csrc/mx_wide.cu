@@ -69,8 +69,6 @@ template <bool GATEUP>
 __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __grid_constant__ MxProduct p) {
     constexpr int EPI_WARPS = Shape<GATEUP>::EPI_WARPS, SCALE0 = Shape<GATEUP>::SCALE0;
     constexpr int STAGES = Shape<GATEUP>::STAGES, STG_OFF = Shape<GATEUP>::STG_OFF, BAR_OFF = Shape<GATEUP>::BAR_OFF;
-    pdl_wait();
-    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -103,11 +101,20 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish_pair();
     }
+    if (warp == 2 && lane == 0) {
+        prefetch_tmap(&p.a);
+        prefetch_tmap(&p.as);
+        prefetch_tmap(&p.b[GATEUP ? rank : 0]);
+        prefetch_tmap(&p.bs[0]);
+        if (GATEUP) prefetch_tmap(&p.bs[1]);
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();  // all of the above ran beside the preceding kernel's end
+    pdl_trigger();
     const int total = p.m_tiles * p.n_tiles;
     const int cl = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     const uint32_t lead_full0 = mapa(full0, 0), lead_tempty = mapa(tempty, 0);
