@@ -185,9 +185,14 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
         // each kernel after the quantiser streams its weights while the one before drains
         NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
         const uint32_t nt = (uint32_t)narrow_tokens(m);
-        if (!mx_code_map(&g.b[0], xq, m, H, nt) || !mx_scale_map(&g.bs, xs, m, H) ||
-            !mx_code_map(&d.b[0], hq, m, I, nt) || !mx_scale_map(&d.bs, hs, m, I))
+        const bool fused = m <= kNarrowQuant;  // x is quantised by the gate/up kernel itself
+        if (fused) {
+            g.x = static_cast<const uint16_t*>(x);
+            g.ldx = (size_t)ldx;
+        } else if (!mx_code_map(&g.b[0], xq, m, H, nt) || !mx_scale_map(&g.bs, xs, m, H)) {
             return MOE_ERR_CUDA;
+        }
+        if (!mx_code_map(&d.b[0], hq, m, I, nt) || !mx_scale_map(&d.bs, hs, m, I)) return MOE_ERR_CUDA;
         g.a[0] = f->k1;
         g.a[1] = f->k3;
         g.as[0] = f->s1;
@@ -199,8 +204,10 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
         d.a[0] = f->k2;
         d.as[0] = f->s2;
         d.out = static_cast<uint16_t*>(out);
-        g.early = d.early = 1;
-        return launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) == cudaSuccess &&
+        g.early = !fused;
+        d.early = 1;
+        f->last_launches = fused ? 2 : 3;
+        return (fused || launch_mx_quant(x, false, (size_t)ldx, m, H, xq, xs, st) == cudaSuccess) &&
                        launch_ffn_narrow(g, true, NARROW_GATEUP, st) == cudaSuccess &&
                        launch_ffn_narrow(d, true, NARROW_PLAIN, st) == cudaSuccess
                    ? MOE_OK
@@ -295,6 +302,15 @@ int linear(const void* x, bool f32, int64_t ldx, int64_t m, const uint8_t* w, co
     const LinearLayout lo = linear_layout(m, k);
     const int rc = check_gemm(m, n, k, w, ws, out, workspace, bytes, lo.total);
     if (rc != MOE_OK || m == 0) return rc;
+    if (m <= kNarrowQuant && !f32) {  // quantised by the product's kernel itself
+        if (!x || !aligned(x, 16) || ldx < k || ldx % 8) return MOE_ERR_INVALID_ARG;
+        NarrowProduct q = narrow((int)m, (int)n, (int)k, workspace);
+        if (!mx_code_map(&q.a[0], w, n, k, 128) || !mx_scale_map(&q.as[0], ws, n, k)) return MOE_ERR_CUDA;
+        q.x = static_cast<const uint16_t*>(x);
+        q.ldx = (size_t)ldx;
+        q.out = static_cast<uint16_t*>(out);
+        return launch_ffn_narrow(q, true, NARROW_PLAIN, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     uint8_t *codes = at<uint8_t>(workspace, lo.codes), *scales = at<uint8_t>(workspace, lo.scales);
     const int qc = quant(x, f32, ldx, m, k, codes, scales, stream);
     if (qc != MOE_OK) return qc;

@@ -89,6 +89,8 @@ enum NarrowKind : int {
 struct NarrowProduct {
     CUtensorMap a[2], as[2];  // weights (128-row boxes) and, MXFP4, their scales
     CUtensorMap b[2], bs;     // tokens (narrow_tokens(T)-row boxes; NARROW_DX: dg, du) and their scales
+    const uint16_t* x;        // MXFP4 weights, at most kNarrowQuant tokens: bf16 tokens in place of b and bs,
+    size_t ldx;               // ... quantised by the kernel itself; else null
     int a_mn;                 // FfnOrder of weights along M
     int T, R, K;
     int early;                // the preceding kernel wrote only the tokens: weights may be read before it ends
@@ -103,6 +105,7 @@ struct NarrowProduct {
     int nt, kstages, slices, stages, ring_bytes, tmem_cols;
 };
 bool narrow_is_faster(int m, int R, bool mx);  // than the 256 x 256 tiles, for out [m, R]
+constexpr int kNarrowQuant = 16;
 int narrow_tokens(int m);           // rows of a token tile
 cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t st);
 

@@ -13,6 +13,9 @@
 //              for the preceding kernel where that one wrote only the tokens,
 //              so that the stream of weights starts while that kernel drains;
 //   warp 1     MMA issuer (and, MXFP4, the scale copies to tensor memory);
+//   warps 2..  where bf16 tokens meet MXFP4 weights (up to 16 tokens): quantise
+//              each stage's piece of them straight into the ring, which saves
+//              the quantiser's launch;
 //   all warps  the sum over slices and the epilogue, a warp per token, four rows
 //              per lane: eight lanes hold one block of an MXFP4 h.
 // A stage holds two weight tiles of 128 bytes of K: W1 and W3 (which share the
@@ -45,6 +48,10 @@ constexpr int MAX_STAGES = 8;
 constexpr int MAX_SLICES = 8;  // the portable cluster size
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 
+// bf16; MXFP4 on both sides; the same from bf16 tokens, quantised on the way.
+enum : int { FMT_BF16 = 0, FMT_MXFP4, FMT_MXFP4_QUANT };
+constexpr int QUANT_WARPS = WARPS - 2;
+
 // Byte offsets inside a stage.
 struct StageShape {
     int tok, sa, sb, bytes;
@@ -61,6 +68,9 @@ __host__ __device__ inline StageShape stage_shape(bool mx, int kind, int nt) {
 }
 __host__ __device__ inline int stage_stride(const StageShape& s) { return (s.bytes + 1023) & ~1023; }
 
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -75,8 +85,9 @@ __device__ __forceinline__ void add4(float (&a)[4], const float4& v) {
     a[3] += v.w;
 }
 
-template <bool MX, int KIND>
+template <int FMT, int KIND>
 __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__ NarrowProduct p) {
+    constexpr bool MX = FMT != FMT_BF16, QUANT = FMT == FMT_MXFP4_QUANT;
     constexpr bool GATEUP = KIND == NARROW_GATEUP;      // two accumulators, one token tile
     constexpr bool SOURCES = KIND == NARROW_DX;         // a stage's tiles: two sources, not two K blocks
     constexpr bool MN = KIND == NARROW_DACT || KIND == NARROW_DX;  // weights along M
@@ -98,7 +109,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
     const int k0 = (int)((int64_t)p.kstages * rank / S), k1 = (int)((int64_t)p.kstages * (rank + 1) / S);
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(full0 + 8 * s, 1);
+            mbar_init(full0 + 8 * s, QUANT ? 1 + QUANT_WARPS : 1);
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(done, 1);
@@ -111,9 +122,9 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
     }
     if (warp == 2 && lane < 2) {
         prefetch_tmap(&p.a[GATEUP || SOURCES ? lane : 0]);
-        prefetch_tmap(&p.b[SOURCES ? lane : 0]);
+        if (!QUANT) prefetch_tmap(&p.b[SOURCES ? lane : 0]);
         if (MX) prefetch_tmap(&p.as[GATEUP ? lane : 0]);
-        if (MX) prefetch_tmap(&p.bs);
+        if (MX && !QUANT) prefetch_tmap(&p.bs);
     }
     tc_fence_before();
     __syncthreads();
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         const auto weights = [&](int ks, uint32_t st, uint32_t bar) {
             // K blocks (128 bytes) of the stage's two tiles
             const int ka = GATEUP || SOURCES ? ks : 2 * ks, kb = GATEUP || SOURCES ? ks : 2 * ks + 1;
-            mbar_arrive_expect_tx(bar, ss.bytes);
+            mbar_arrive_expect_tx(bar, QUANT ? 2 * TILE + 2048 : ss.bytes);
             tma_load_3d(st, a0, w.c0 + ka * w.d0, w.c1 + ka * w.d1, w.c2, bar);
             tma_load_3d(st + TILE, a1, w.c0 + kb * w.d0, w.c1 + kb * w.d1, w.c2, bar);
             if (MN && w.two) {
@@ -146,6 +157,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             }
         };
         const auto tokens = [&](int ks, uint32_t st, uint32_t bar) {
+            if (QUANT) return;
             const int kc = (GATEUP || SOURCES ? ks : 2 * ks) * 32;  // words along K: 128 bytes are 32
             tma_load_3d(st + ss.tok, b0, kc, tok0, 0, bar);
             if (!GATEUP) tma_load_3d(st + ss.tok + p.nt * 128, b1, SOURCES ? kc : kc + 32, tok0, 0, bar);
@@ -241,6 +253,72 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         }
         if (elect_one()) mma_commit(done);
         __syncwarp();
+    } else if (QUANT) {
+        // Tokens warp - 2 and warp - 2 + 8, 256 of K per tile: eight elements a
+        // lane, four lanes a block.  Two stages' loads are under way ahead of
+        // the one being written.
+        constexpr int TT = GATEUP ? 1 : 2;  // token tiles of a stage
+        const int n = k1 - k0, ntok = min(p.nt, p.T - tok0);
+        struct Piece {
+            uint4 v[2][TT];
+        };
+        const auto load = [&](int i) {
+            Piece q{};
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int h = 0; h < TT; ++h) {
+                    const int j = warp - 2 + x * QUANT_WARPS, k = (TT * (k0 + i) + h) * 256 + lane * 8;
+                    if (i < n && j < ntok && k < p.K)
+                        q.v[x][h] = *reinterpret_cast<const uint4*>(p.x + (size_t)(tok0 + j) * p.ldx + k);
+                }
+            return q;
+        };
+        Piece cur = load(0), next = load(1);
+        int s = 0;
+        uint32_t ph = 1;
+        for (int i = 0; i < n; ++i) {
+            const Piece after = load(i + 2);
+            if (*abort_flag || !mbar_wait(empty0 + 8 * s, ph, p.wait_ns)) {
+                if (lane == 0) {
+                    set_error(p.hdr, DEV_ERR_TIMEOUT, 44);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            const uint32_t st = sbase + s * stride;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int h = 0; h < TT; ++h) {
+                    const int j = warp - 2 + x * QUANT_WARPS;
+                    if (j >= ntok) continue;  // a column of D that is never read
+                    const uint4 q = cur.v[x][h];
+                    const float v[8] = {bf16lo(q.x), bf16hi(q.x), bf16lo(q.y), bf16hi(q.y),
+                                        bf16lo(q.z), bf16hi(q.z), bf16lo(q.w), bf16hi(q.w)};
+                    uint32_t a = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a = max(a, __float_as_uint(v[e]) & 0x7fffffffu);
+                    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                    const uint32_t sc = mx_scale(a);
+                    const uint32_t w = sc == 255u ? 0u : mx_codes8(v, mx_inverse(sc));
+                    sts32(st + ss.tok + h * p.nt * 128 + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4, w);
+                    uint32_t sw = sc << (((lane >> 2) & 3) * 8);
+                    sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+                    sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+                    if ((lane & 15) == 0) sts32(st + ss.sb + h * 1024 + (lane >> 4) * 512 + j * 16, sw);
+                }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full0 + 8 * s);
+            cur = next;
+            next = after;
+            if (++s == p.stages) {
+                s = 0;
+                ph ^= 1u;
+            }
+        }
     }
     // the sums to shared memory, over the ring (its copies have landed and its
     // MMAs have read them): part[h][token][row], fp32
@@ -366,8 +444,8 @@ int clusters_resident(int size) {
         cfg.attrs = &at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaFuncSetAttribute(ffn_narrow<false, NARROW_GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, ffn_narrow<false, NARROW_GATEUP>, &cfg) != cudaSuccess) {
+        if (cudaFuncSetAttribute(ffn_narrow<FMT_BF16, NARROW_GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, ffn_narrow<FMT_BF16, NARROW_GATEUP>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = sms() / size * 3 / 4;
         }
@@ -376,10 +454,10 @@ int clusters_resident(int size) {
     return k.load();
 }
 
-template <bool MX, int KIND>
+template <int FMT, int KIND>
 cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
     static cudaError_t attr =
-        cudaFuncSetAttribute(ffn_narrow<MX, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        cudaFuncSetAttribute(ffn_narrow<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ceil_div(p.R, 128) * p.slices, ceil_div(p.T, p.nt));
@@ -395,7 +473,7 @@ cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ffn_narrow<MX, KIND>, p);
+    return cudaLaunchKernelEx(&cfg, ffn_narrow<FMT, KIND>, p);
 }
 
 }  // namespace
@@ -443,12 +521,13 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t 
             p.slices = s;
             break;
         }
-    if (mx) return gateup ? launch<true, NARROW_GATEUP>(p, smem, st) : launch<true, NARROW_PLAIN>(p, smem, st);
+    if (p.x) return gateup ? launch<FMT_MXFP4_QUANT, NARROW_GATEUP>(p, smem, st) : launch<FMT_MXFP4_QUANT, NARROW_PLAIN>(p, smem, st);
+    if (mx) return gateup ? launch<FMT_MXFP4, NARROW_GATEUP>(p, smem, st) : launch<FMT_MXFP4, NARROW_PLAIN>(p, smem, st);
     switch (kind) {
-        case NARROW_GATEUP: return launch<false, NARROW_GATEUP>(p, smem, st);
-        case NARROW_DACT: return launch<false, NARROW_DACT>(p, smem, st);
-        case NARROW_DX: return launch<false, NARROW_DX>(p, smem, st);
-        default: return launch<false, NARROW_PLAIN>(p, smem, st);
+        case NARROW_GATEUP: return launch<FMT_BF16, NARROW_GATEUP>(p, smem, st);
+        case NARROW_DACT: return launch<FMT_BF16, NARROW_DACT>(p, smem, st);
+        case NARROW_DX: return launch<FMT_BF16, NARROW_DX>(p, smem, st);
+        default: return launch<FMT_BF16, NARROW_PLAIN>(p, smem, st);
     }
 }
 

@@ -396,6 +396,24 @@ def test_refusals(B):
                                 ws.numel(), None) == 1
 
 
+@pytest.mark.parametrize("m,k", [(1, 32), (1, 7168), (7, 544), (9, 4128), (16, 1056)])
+def test_few_tokens_are_quantised_alike(B, m, k):
+    """Up to 16 bf16 tokens are quantised inside the product's kernel: the same bits as by
+    moe_mxfp4_quant, with zero, infinite and strided rows among them."""
+    (w,), _ = _quantised(B, [_n(4, 520, k, std=k ** -0.5)])
+    base = _n(6, m, k + 72, dtype=torch.float32) * torch.exp2(torch.randint(-30, 30, (m, 1), device="cuda").float())
+    x = base.bfloat16()[:, 8:k + 8]
+    if m > 5:
+        x[1] = 0
+        x[3, 5] = float("inf")
+        x[4, k - 1] = float("nan")
+    got = B.moe_mxfp4_linear(x, *w)
+    want = B.moe_mxfp4_gemm(*B.moe_mxfp4_quant(x), *w)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+    if m > 5:
+        assert torch.isnan(got[3:5]).all() and not got[1].any() and torch.isfinite(got[5:]).all()
+
+
 def test_capture_of_the_linear(B):
     """A product whose stream has no workspace yet, first called while a graph is captured."""
     (w,), _ = _quantised(B, [_n(4, 264, 320)])
