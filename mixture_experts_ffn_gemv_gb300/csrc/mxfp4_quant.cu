@@ -60,11 +60,12 @@ __device__ __forceinline__ void widen(const Raw<float>& r, float (&v)[16]) {
 
 // Two lanes share a block of 32, a warp takes 512 elements of a row: four scale
 // tiles' words, padding blocks (zeros) included.  Bound by HBM; a warp has U
-// such pieces in flight (one kept 32 KB per SM under way, and 3.9 TB/s).
+// such pieces in flight (14336 x 7168 bf16 with 1, 2, 3, 4: 50.0, 44.0, 42.3,
+// 44.9 us, 6.1 TB/s at best).
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) mx_quant(const T* x, size_t ldx, uint32_t total, uint32_t pieces, int n,
                                                 int nkt, uint8_t* codes, uint8_t* scales) {
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    constexpr int U = sizeof(T) == 2 ? 3 : 2;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(256) mx_quant(const T* x, size_t ldx, uint32_t
     }
 }
 
-// Sixteen codes a thread (8 bytes in, 32 out), U in flight.
+// Sixteen codes a thread (8 bytes in, 32 out), U in flight.  Bound by HBM:
+// 14336 x 7168 in 40.0 us, 6.5 TB/s.
 __global__ void __launch_bounds__(256) mx_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t total,
                                                   uint32_t per, int nkt, uint16_t* out) {
     constexpr int U = 4;
@@ -154,16 +156,18 @@ __global__ void __launch_bounds__(256) mx_dequant(const uint8_t* codes, const ui
     }
 }
 
-// Blocks for `work` block-sized pieces, at most eight per SM (all resident).
-int grid_for(size_t work) {
+// Blocks for `work` block-sized pieces, at most per_sm an SM.  The quantiser
+// takes 8 (16 and 64: 46 and 55 us where 8 took 45); the way back, which
+// mostly writes, 64 (8 and 16: 49 and 44 us where 64 took 40).
+int grid_for(size_t work, int per_sm) {
     static const int sms = device_sm_count();
-    return (int)std::min<size_t>(std::max<size_t>(work, 1), (size_t)sms * 8);
+    return (int)std::min<size_t>(std::max<size_t>(work, 1), (size_t)sms * per_sm);
 }
 
 template <typename T>
 cudaError_t quant(const T* x, size_t ldx, int rows, int n, uint8_t* codes, uint8_t* scales, cudaStream_t st) {
     const uint32_t pieces = (uint32_t)ceil_div(n, 512), total = (uint32_t)rows * pieces;
-    const dim3 grid(grid_for((total + 7) / 8)), block(256);
+    const dim3 grid(grid_for((total + 7) / 8, 8)), block(256);
     const bool wide = (reinterpret_cast<uintptr_t>(x) % 32) == 0 && ldx * sizeof(T) % 32 == 0;
     return launch_pdl(wide ? mx_quant<T, true> : mx_quant<T, false>, grid, block, 0, st, x, ldx, total, pieces, n,
                       ceil_div(n, 128), codes, scales);
@@ -180,7 +184,7 @@ cudaError_t launch_mx_quant(const void* x, bool f32, size_t ldx, int rows, int n
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int n, uint16_t* out,
                               cudaStream_t st) {
     const uint32_t per = (uint32_t)(n / 16), total = (uint32_t)rows * per;
-    return launch_pdl(mx_dequant, dim3(grid_for(((size_t)total + 255) / 256)), dim3(256), 0, st, codes, scales, total,
+    return launch_pdl(mx_dequant, dim3(grid_for(((size_t)total + 255) / 256, 64)), dim3(256), 0, st, codes, scales, total,
                       per, ceil_div(n, 128), out);
 }
 
