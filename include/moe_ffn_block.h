@@ -73,18 +73,21 @@ MOE_API int moe_ffn_destroy(moe_ffn* ffn);
  * passes a workspace other than its previous call's. */
 MOE_API int moe_ffn_workspace_size(const moe_ffn* ffn, int64_t m, int backward, size_t* bytes);
 
+/* Bytes that a forward pass on m tokens saves for the backward pass. */
+MOE_API int moe_ffn_saved_size(const moe_ffn* ffn, int64_t m, size_t* bytes);
+
 /* out[t, :] = the block applied to x[t, :].
  *   x bf16 [m, H] with row stride ldx >= H (a multiple of 8); out bf16 [m, H].
- *   saved, saved_h (bf16 weights only, else NULL; both or neither, 32-byte
- *   aligned): with g = x W1^T and u = x W3^T, fp32 [2, ceil(m / 32),
- *   ceil(I / 32), 4, 32, 8] that receives act(g) and u act'(g) (row r, column c
- *   at [r / 32, c / 32, c % 32 / 8, r % 32, c % 8]; what pads m and I is left as
- *   it is), and bf16 [m, I] that receives h = act(g) u, for moe_ffn_backward.  (fp32: rounded to bf16 they would be the largest error
- *   of the gradients.)
+ *   saved (bf16 weights only, else NULL): NULL, or moe_ffn_saved_size bytes,
+ *   32-byte aligned, that receive what moe_ffn_backward needs: with g = x W1^T
+ *   and u = x W3^T, act(g) and u act'(g) in fp32 (rounded to bf16 they would be
+ *   the largest error of the gradients), each [ceil(m / 32), ceil(I / 32), 4, 32, 8]
+ *   with row r, column c at [r / 32, c / 32, c % 32 / 8, r % 32, c % 8] (what pads
+ *   m and I is left as it is), then h = act(g) u, bf16 [m, I].
  * The intermediate h is rounded to bf16 (MXFP4: to MXFP4, straight from the
  * fp32 products), x to MXFP4 for MXFP4 weights; sums are fp32. */
-MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, float* saved,
-                            void* saved_h, void* workspace, size_t workspace_bytes, void* stream);
+MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, void* saved,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients of the block, given dout = dL/dout and what forward saved:
  *   dh = dout W2 (fp32), dg = dh u act'(g), du = dh act(g) (bf16)
@@ -95,7 +98,7 @@ MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int6
  * bf16 weights only (MOE_ERR_UNSUPPORTED otherwise).  m == 0 writes nothing:
  * weight gradients are then left as they are. */
 MOE_API int moe_ffn_backward(const moe_ffn* ffn, const void* dout, int64_t ldd, const void* x, int64_t ldx,
-                             const float* saved, const void* saved_h, int64_t m, void* dx, void* dw1, void* dw3, void* dw2,
+                             const void* saved, int64_t m, void* dx, void* dw1, void* dw3, void* dw2,
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Kernels the last successful call on `ffn` launched. */

@@ -32,7 +32,7 @@ EXPORTED = (
     "moe_layer_stall_test",
     "moe_last_launch_count", "moe_kernel_timing_enable", "moe_kernel_timing_read", "moe_kernel_count",
     "moe_kernel_name", "moe_status_string",
-    "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+    "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_workspace_size", "moe_ffn_saved_size", "moe_ffn_forward", "moe_ffn_backward",
     "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
     "moe_mxfp4_dequant", "moe_mxfp4_gemm_workspace_size", "moe_mxfp4_gemm",
     "moe_mxfp4_linear_workspace_size", "moe_mxfp4_linear", "moe_mxfp4_linear_f32",
@@ -117,8 +117,9 @@ def load_library(path: str | None = None, build: bool = True):
                                        ctypes.POINTER(_vp)]
         lib.moe_ffn_destroy.argtypes = [_vp]
         lib.moe_ffn_workspace_size.argtypes = [_vp, _i64, ctypes.c_int, ctypes.POINTER(sz)]
-        lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, sz, _vp]
-        lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_saved_size.argtypes = [_vp, _i64, ctypes.POINTER(sz)]
+        lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
         lib.moe_ffn_last_launch_count.argtypes = [_vp]
         lib.moe_mxfp4_scales_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
         lib.moe_mxfp4_quant.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
@@ -585,6 +586,7 @@ class GatedFfn:
         self._ws = None
         self._ws_at = (None, 0)
         self._fits = [-1, -1]  # tokens the workspace holds: forward, backward
+        self._saved = {}       # words saved, by tokens
 
     def close(self):
         if getattr(self, "handle", None):
@@ -625,13 +627,18 @@ class GatedFfn:
             raise MoeError(rc, "moe_device_status")
         return code.value
 
-    def _saved_shape(self, m: int):
-        return 2, (m + 31) // 32, (self.inter + 31) // 32, 4, 32, 8
+    def saved_size(self, m: int) -> int:
+        """Words of what a forward pass on m tokens saves (moe_ffn_saved_size, in 4-byte words)."""
+        n = self._saved.get(m)
+        if n is None:
+            c = ctypes.c_size_t()
+            _check(self.lib.moe_ffn_saved_size(self.handle, int(m), ctypes.byref(c)), "moe_ffn_saved_size")
+            n = self._saved[m] = (c.value + 3) // 4
+        return n
 
     def forward(self, x, save=False, out=None, stream=None):
         """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
-        (out, saved) for backward: with g = x w1^T, u = x w3^T, saved is (fp32: act(g) and u act'(g) in
-        blocks of 32 x 32, see moe_ffn_block.h; bf16 [m, I]: h = act(g) u)."""
+        (out, saved) for backward: saved is fp32 [saved_size(m)], in moe_ffn_forward's own order."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.forward(x, save, out)
@@ -643,13 +650,9 @@ class GatedFfn:
             _dense(out, _BF16, (m, self.hidden), "out")
         if m > self._fits[0]:
             self.workspace(m, False, x.device)
-        saved = None
-        if save:
-            saved = (_empty(self._saved_shape(m), dtype=_F32, device=x.device),
-                     _empty((m, self.inter), dtype=_BF16, device=x.device))
+        saved = _empty(self.saved_size(m), dtype=_F32, device=x.device) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
-                                      saved[0].data_ptr() if save else None,
-                                      saved[1].data_ptr() if save else None, *self._ws_at, _on(x))
+                                      saved.data_ptr() if save else None, *self._ws_at, _on(x))
         if rc:
             raise MoeError(rc, "moe_ffn_forward")
         return (out, saved) if save else out
@@ -664,8 +667,7 @@ class GatedFfn:
         ldd, ldx = _rows(dout, H, "dout"), _rows(x, H, "x")
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
-        _dense(saved[0], _F32, self._saved_shape(m), "saved[0]")
-        _dense(saved[1], _BF16, (m, I), "saved[1]")
+        _dense(saved, _F32, (self.saved_size(m),), "saved")
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
         dw1 = dw3 = dw2 = None
         if need_dw:
@@ -676,7 +678,7 @@ class GatedFfn:
         if m > self._fits[1]:
             self.workspace(m, True, x.device)
         rc = self.lib.moe_ffn_backward(
-            self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved[0].data_ptr(), saved[1].data_ptr(), m,
+            self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m,
             dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else
                                                   (None, None, None)), *self._ws_at, _on(x))
         if rc:

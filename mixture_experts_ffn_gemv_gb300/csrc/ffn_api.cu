@@ -376,41 +376,48 @@ int moe_ffn_workspace_size(const moe_ffn* f, int64_t m, int backward, size_t* by
     return MOE_OK;
 }
 
-int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, void* out, float* saved, void* saved_h,
-                    void* workspace, size_t workspace_bytes, void* stream) {
+int moe_ffn_saved_size(const moe_ffn* f, int64_t m, size_t* bytes) {
+    if (!f || m < 0 || !bytes) return MOE_ERR_INVALID_ARG;
+    if (f->cfg.weights != MOE_WEIGHTS_BF16 || m > INT32_MAX / 64) return MOE_ERR_UNSUPPORTED;
+    *bytes = saved_floats(m, f->cfg.inter) * 8 + (size_t)m * f->cfg.inter * 2;
+    return MOE_OK;
+}
+
+int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, void* out, void* saved, void* workspace,
+                    size_t workspace_bytes, void* stream) {
     Layout lo;
     const int rc = check_call(f, m, false, workspace, workspace_bytes, &lo);
     if (rc != MOE_OK || m == 0) return rc;
-    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || !saved != !saved_h ||
-        (saved && (!aligned(saved, 32) || !aligned(saved_h, 32))))
+    if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 32)))
         return MOE_ERR_INVALID_ARG;
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
     if (mx && saved) return MOE_ERR_UNSUPPORTED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
-    void* h = saved ? saved_h : at<void>(workspace, lo.h);
+    float* sa = static_cast<float*>(saved);
+    void* h = saved ? sa + 2 * saved_floats(m, f->cfg.inter) : at<void>(workspace, lo.h);
     return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
-              : forward_bf16(f, x, ldx, (int)m, out, saved, h, workspace, st);
+              : forward_bf16(f, x, ldx, (int)m, out, sa, h, workspace, st);
 }
 
-int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void* x, int64_t ldx, const float* saved,
-                     const void* saved_h, int64_t m, void* dx, void* dw1, void* dw3, void* dw2, void* workspace,
-                     size_t workspace_bytes, void* stream) {
+int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void* x, int64_t ldx, const void* saved,
+                     int64_t m, void* dx, void* dw1, void* dw3, void* dw2, void* workspace, size_t workspace_bytes,
+                     void* stream) {
     Layout lo;
     if (f && f->cfg.weights != MOE_WEIGHTS_BF16) return MOE_ERR_UNSUPPORTED;
     const int rc = check_call(f, m, true, workspace, workspace_bytes, &lo);
     if (rc != MOE_OK || m == 0) return rc;
     const int H = f->cfg.hidden, I = f->cfg.inter, n = (int)m;
     const bool dw = dw1 || dw3 || dw2;
-    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !saved_h || !aligned(saved, 32) ||
-        !aligned(saved_h, 32) || (dx && !aligned(dx, 16)) ||
+    if (bad_rows(dout, ldd, H) || bad_rows(x, ldx, H) || !saved || !aligned(saved, 32) || (dx && !aligned(dx, 16)) ||
         (dw && (!dw1 || !dw3 || !dw2 || !aligned(dw1, 16) || !aligned(dw3, 16) || !aligned(dw2, 16))))
         return MOE_ERR_INVALID_ARG;
     if (!dx && !dw) return MOE_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
     void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du);
-    float *sa = const_cast<float*>(saved), *sd = sa + saved_floats(m, I);  // only read
+    float* sa = static_cast<float*>(const_cast<void*>(saved));  // only read
+    float *sd = sa + saved_floats(m, I), *h = sd + saved_floats(m, I);
     const uint32_t nt = (uint32_t)narrow_tokens(n);
     // dh = dout W2 and, in its epilogue, dg and du
     if (narrow_is_faster(n, I, false)) {
@@ -465,7 +472,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
         for (int i = 0; i < 3; ++i) {
             FfnProduct& g = i < 2 ? add(r, I, H, n, out[i]) : add(r, H, I, n, out[i]);
             g.a_mn = i < 2 ? ffn_map_mn(&g.a[0], lhs[i], m, I, I) : ffn_map_mn(&g.a[0], dout, m, H, ldd);
-            g.b_mn = i < 2 ? ffn_map_mn(&g.b[0], x, m, H, ldx) : ffn_map_mn(&g.b[0], saved_h, m, I, I);
+            g.b_mn = i < 2 ? ffn_map_mn(&g.b[0], x, m, H, ldx) : ffn_map_mn(&g.b[0], h, m, I, I);
             if (!g.a_mn || !g.b_mn) return MOE_ERR_CUDA;
         }
     }

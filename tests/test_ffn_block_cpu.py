@@ -50,8 +50,9 @@ def test_null_arguments(B):
     assert lib.moe_ffn_create(None, None, None) == 1
     n = ctypes.c_size_t()
     assert lib.moe_ffn_workspace_size(None, 1, 0, ctypes.byref(n)) == 1
-    assert lib.moe_ffn_forward(None, FAKE, 8, 1, FAKE, None, None, FAKE, 1 << 20, None) == 1
-    assert lib.moe_ffn_backward(None, FAKE, 8, FAKE, 8, FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == 1
+    assert lib.moe_ffn_saved_size(None, 1, ctypes.byref(n)) == 1
+    assert lib.moe_ffn_forward(None, FAKE, 8, 1, FAKE, None, FAKE, 1 << 20, None) == 1
+    assert lib.moe_ffn_backward(None, FAKE, 8, FAKE, 8, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == 1
     assert lib.moe_ffn_last_launch_count(None) == -1
     assert lib.moe_ffn_destroy(None) == 0
 

@@ -172,9 +172,12 @@ def test_mx_linear_fp32_strided_and_streams(B):
 
 # ---------------------------------------------------------------- the block
 
-def _rows_of_saved(s, m, I):
-    """[row block, column block, column group, row, column] to [m, I]."""
-    return s.permute(0, 3, 1, 2, 4).reshape(s.shape[0] * 32, -1)[:m, :I]
+def _saved_parts(saved, m, I):
+    """act(g), u act'(g) and h [m, I] of what a forward pass saved."""
+    n = (m + 31) // 32 * ((I + 31) // 32) * 1024
+    blocks = [s.reshape((m + 31) // 32, (I + 31) // 32, 4, 32, 8) for s in (saved[:n], saved[n:2 * n])]
+    a, d = (s.permute(0, 3, 1, 2, 4).reshape(s.shape[0] * 32, -1)[:m, :I] for s in blocks)
+    return a, d, saved[2 * n:].view(torch.bfloat16)[:m * I].reshape(m, I)
 
 
 FFN_SIZES = [(1, 2048, 768), (1, 8, 8), (3, 24, 40), (16, 256, 128), (17, 136, 264), (48, 1024, 512), (65, 520, 1032),
@@ -196,11 +199,11 @@ def test_forward(B, m, H, I, kind):
     eg, eu = (H * P.F32 * (x.double().abs() @ v.double().abs().T) for v in w[:2])
     a, s = P.act_slope(g, kind)
     ea, es = P.SLOPE * eg + 2.0 ** -20 * a.abs(), P.CURVE * eg + 2.0 ** -20
-    sa, sd = (_rows_of_saved(s, m, I) for s in saved[0])
+    sa, sd, sh = _saved_parts(saved, m, I)
     _within(sa, a, ea)
     _within(sd, u * s, u.abs() * es + eu * s.abs() + eu * es + 2.0 ** -22 * (u * s).abs())
     eh = a.abs() * eu + ea * u.abs() + ea * eu + 2.0 ** -22 * (a * u).abs()
-    _within(saved[1], a * u, eh + P.HALF * ((a * u).abs() + eh))
+    _within(sh, a * u, eh + P.HALF * ((a * u).abs() + eh))
     assert blk.device_status() == 0
 
 
@@ -334,7 +337,7 @@ def test_graph_capture_and_other_streams(B):
         torch.cuda.synchronize()
         e_out, e_saved = blk.forward(x, save=True)
         e_grads = blk.backward(dout, x, e_saved)
-        assert torch.equal(out, e_out) and torch.equal(saved[1], e_saved[1]) and all(torch.equal(a, b) for a, b in zip(grads, e_grads))
+        assert torch.equal(out, e_out) and torch.equal(_saved_parts(saved, m, I)[2], _saved_parts(e_saved, m, I)[2]) and all(torch.equal(a, b) for a, b in zip(grads, e_grads))
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
     s_out = blk.forward(x, stream=st)
@@ -348,10 +351,10 @@ def test_repeatable(B):
     blk = B.GatedFfn(*w)
     x, dout = _n(42, m, H), _n(43, m, H)
     out, saved = blk.forward(x, save=True)
-    first = (out, saved[1], *blk.backward(dout, x, saved))
+    first = (out, _saved_parts(saved, m, I)[2], *blk.backward(dout, x, saved))
     for _ in range(3):
         o, s = blk.forward(x, save=True)
-        assert all(torch.equal(a, b) for a, b in zip(first, (o, s[1], *blk.backward(dout, x, s))))
+        assert all(torch.equal(a, b) for a, b in zip(first, (o, _saved_parts(s, m, I)[2], *blk.backward(dout, x, s))))
 
 
 def test_refusals(B):
@@ -368,9 +371,9 @@ def test_refusals(B):
     with pytest.raises(ValueError):
         blk.backward(x[:5], x, saved)
     with pytest.raises(ValueError):
-        blk.backward(x, x, (saved[0], saved[1][:5]))
+        blk.backward(x, x, saved[:-4])
     with pytest.raises(ValueError):
-        blk.backward(x, x, (saved[0].bfloat16(), saved[1]))
+        blk.backward(x, x, saved.bfloat16())
     with pytest.raises(ValueError):
         B.GatedFfn(w1, w3, w2.T)
     with pytest.raises(ValueError):
@@ -387,12 +390,12 @@ def test_refusals(B):
     lib, p = B.load_library(), B._p
     ws = blk.workspace(10, True, x.device)
     out = torch.empty_like(x)
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), None, None, p(ws), 256, None) == B.MOE_ERR_WORKSPACE
-    assert lib.moe_ffn_forward(blk.handle, p(x), H - 8, 10, p(out), None, None, p(ws), ws.numel(), None) == 1
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), p(saved[0]), None, p(ws), ws.numel(), None) == 1
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, -1, p(out), None, None, p(ws), ws.numel(), None) == 1
-    assert lib.moe_ffn_forward(blk.handle, p(x), H, 1 << 30, p(out), None, None, p(ws), ws.numel(), None) == 2
-    assert lib.moe_ffn_backward(blk.handle, p(x), H, p(x), H, p(saved[0]), p(saved[1]), 10, p(out), p(w1), None, None, p(ws),
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), None, p(ws), 256, None) == B.MOE_ERR_WORKSPACE
+    assert lib.moe_ffn_forward(blk.handle, p(x), H - 8, 10, p(out), None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 10, p(out), saved.data_ptr() + 16, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, -1, p(out), None, p(ws), ws.numel(), None) == 1
+    assert lib.moe_ffn_forward(blk.handle, p(x), H, 1 << 30, p(out), None, p(ws), ws.numel(), None) == 2
+    assert lib.moe_ffn_backward(blk.handle, p(x), H, p(x), H, p(saved), 10, p(out), p(w1), None, None, p(ws),
                                 ws.numel(), None) == 1
 
 
