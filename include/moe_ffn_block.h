@@ -84,7 +84,8 @@ MOE_API int moe_ffn_saved_size(const moe_ffn* ffn, int64_t m, size_t* bytes);
  *   the largest error of the gradients), each [ceil(m / 32), ceil(I / 32), 4, 32, 8]
  *   with row r, column c at [r / 32, c / 32, c % 32 / 8, r % 32, c % 8] (what pads
  *   m and I is left as it is), then h = act(g) u, bf16 [m, I].
- * The intermediate h is rounded to bf16 (MXFP4: to MXFP4, straight from the
+ * The intermediate h is rounded to bf16 (up to 8 tokens whose h is not saved: to
+ * two bf16 parts, 16 bits; MXFP4: to MXFP4, straight from the
  * fp32 products), x to MXFP4 for MXFP4 weights; sums are fp32. */
 MOE_API int moe_ffn_forward(const moe_ffn* ffn, const void* x, int64_t ldx, int64_t m, void* out, void* saved,
                             void* workspace, size_t workspace_bytes, void* stream);

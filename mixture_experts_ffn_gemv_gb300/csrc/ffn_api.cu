@@ -62,7 +62,7 @@ Layout layout(const moe_ffn* f, int64_t m, bool backward) {
             o.dg = take((size_t)m * I * 2);
             o.du = take((size_t)m * I * 2);
         } else {
-            o.h = take((size_t)m * I * 2);
+            o.h = take((size_t)(m <= kNarrowParts ? 2 * kNarrowParts : m) * I * 2);
         }
     }
     o.total = off;
@@ -126,6 +126,7 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
                  cudaStream_t st) {
     const int H = f->cfg.hidden, I = f->cfg.inter;
     const uint32_t nt = (uint32_t)narrow_tokens(m);
+    const bool parts = m <= kNarrowParts && !saved;  // h is not kept: two parts (ffn_narrow.cu)
     float* saved_d = saved ? saved + saved_floats(m, I) : nullptr;
     if (narrow_is_faster(m, I, false)) {
         NarrowProduct g = narrow(m, I, H, ws);
@@ -136,7 +137,7 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
         g.out = static_cast<uint16_t*>(h);
         g.sa = saved;
         g.sd = saved_d;
-        if (launch_ffn_narrow(g, false, NARROW_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_ffn_narrow(g, false, parts ? NARROW_GATEUP_PARTS : NARROW_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
     } else {
         FfnProducts p = products(f, ws);
         FfnProduct& gu = add(p, m, I, H, h);
@@ -149,11 +150,11 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
     }
     if (narrow_is_faster(m, H, false)) {
         NarrowProduct d = narrow(m, H, I, ws);
-        if (!ffn_map(&d.b[0], h, m, I, I, nt)) return MOE_ERR_CUDA;
+        if (!ffn_map(&d.b[0], h, parts ? 2 * kNarrowParts : m, I, I, nt)) return MOE_ERR_CUDA;
         d.a[0] = f->k2;
         d.early = 1;  // behind the kernel that wrote h
         d.out = static_cast<uint16_t*>(out);
-        if (launch_ffn_narrow(d, false, NARROW_PLAIN, st) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_ffn_narrow(d, false, parts ? NARROW_PLAIN_PARTS : NARROW_PLAIN, st) != cudaSuccess) return MOE_ERR_CUDA;
     } else {
         FfnProducts d = products(f, ws);
         FfnProduct& y = add(d, m, H, I, out);

@@ -85,6 +85,9 @@ enum NarrowKind : int {
     NARROW_GATEUP,  // W1 and W3: h
     NARROW_DACT,    // dout W2, W2 along M: dg and du
     NARROW_DX,      // dg W1 + du W3, both along M
+    // at most kNarrowParts tokens: h written, and read, in two bf16 parts, rows t and 8 + t
+    NARROW_GATEUP_PARTS,
+    NARROW_PLAIN_PARTS,
 };
 struct NarrowProduct {
     CUtensorMap a[2], as[2];  // weights (128-row boxes) and, MXFP4, their scales
@@ -105,7 +108,7 @@ struct NarrowProduct {
     int nt, kstages, slices, stages, ring_bytes, tmem_cols;
 };
 bool narrow_is_faster(int m, int R, bool mx);  // than the 256 x 256 tiles, for out [m, R]
-constexpr int kNarrowQuant = 16;
+constexpr int kNarrowQuant = 16, kNarrowParts = 8;
 int narrow_tokens(int m);           // rows of a token tile
 cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t st);
 

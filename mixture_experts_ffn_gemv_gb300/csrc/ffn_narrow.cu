@@ -18,6 +18,9 @@
 //              the quantiser's launch;
 //   all warps  the sum over slices and the epilogue, a warp per token, four rows
 //              per lane: eight lanes hold one block of an MXFP4 h.
+// Up to 8 tokens' h goes from gate/up to down in two bf16 parts (h and what its
+// rounding left, 16 bits together): 8 + 8 rows of the smallest token tile, so
+// the second part costs four MMAs of 16 columns per K block and no bandwidth.
 // A stage holds two weight tiles of 128 bytes of K: W1 and W3 (which share the
 // tokens); two neighbours along K; or a tile of each source, with its tokens,
 // of dx = dg W1 + du W3.  The backward products read the weights as they lie,
@@ -58,7 +61,7 @@ struct StageShape {
 };
 // tok: the token tile(s); sa, sb: scales of the weights and of the tokens.
 __host__ __device__ inline StageShape stage_shape(bool mx, int kind, int nt) {
-    const bool gateup = kind == NARROW_GATEUP;
+    const bool gateup = kind == NARROW_GATEUP || kind == NARROW_GATEUP_PARTS;
     StageShape s;
     s.tok = 2 * TILE;
     s.sa = s.tok + (gateup ? 1 : 2) * nt * 128;
@@ -88,7 +91,8 @@ __device__ __forceinline__ void add4(float (&a)[4], const float4& v) {
 template <int FMT, int KIND>
 __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__ NarrowProduct p) {
     constexpr bool MX = FMT != FMT_BF16, QUANT = FMT == FMT_MXFP4_QUANT;
-    constexpr bool GATEUP = KIND == NARROW_GATEUP;      // two accumulators, one token tile
+    constexpr bool GATEUP = KIND == NARROW_GATEUP || KIND == NARROW_GATEUP_PARTS;  // two accumulators, one token tile
+    constexpr bool PARTS = KIND == NARROW_GATEUP_PARTS || KIND == NARROW_PLAIN_PARTS;
     constexpr bool SOURCES = KIND == NARROW_DX;         // a stage's tiles: two sources, not two K blocks
     constexpr bool MN = KIND == NARROW_DACT || KIND == NARROW_DX;  // weights along M
     extern __shared__ uint8_t smem_raw[];
@@ -237,6 +241,9 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                                      sf + 8 * h + 4 * (kk >> 1), sf + 16 + (GATEUP ? 0 : 8 * h) + 4 * (kk >> 1), acc);
                         else
                             mma_bf16(d, ad + (MN ? 128 : 2) * kk, bd + 2 * kk, idesc, acc);
+                        // tokens in two parts: the second one's rows, 8 further on, onto the same columns
+                        if (PARTS && !GATEUP)
+                            mma_bf16(d, ad + 2 * kk, bd + 64 + 2 * kk, idesc, 1u);
                     }
                 }
                 mma_commit(empty0 + 8 * s);
@@ -412,7 +419,12 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                     *reinterpret_cast<float4*>(p.sa + sat) = make_float4(v0[x][0], v0[x][1], v0[x][2], v0[x][3]);
                     *reinterpret_cast<float4*>(p.sd + sat) = make_float4(v1[x][0], v1[x][1], v1[x][2], v1[x][3]);
                 }
-                *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                const uint2 hi = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                *reinterpret_cast<uint2*>(p.out + at) = hi;
+                if (GATEUP && PARTS)  // what rounding left of h, 8 rows further on
+                    *reinterpret_cast<uint2*>(p.out + at + 8 * (size_t)p.R) =
+                        make_uint2(pack_bf16x2(o[0] - bf16lo(hi.x), o[1] - bf16hi(hi.x)),
+                                   pack_bf16x2(o[2] - bf16lo(hi.y), o[3] - bf16hi(hi.y)));
             }
         }
     }
@@ -490,7 +502,7 @@ bool narrow_is_faster(int m, int R, bool mx) {
 int narrow_tokens(int m) { return std::min(128, (m + 15) / 16 * 16); }
 
 cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t st) {
-    const bool gateup = kind == NARROW_GATEUP;
+    const bool gateup = kind == NARROW_GATEUP || kind == NARROW_GATEUP_PARTS;
     p.nt = narrow_tokens(p.T);
     p.kstages = ceil_div(p.K, (mx ? 256 : 64) * (gateup || kind == NARROW_DX ? 1 : 2));
     const StageShape ss = stage_shape(mx, kind, p.nt);
@@ -525,6 +537,8 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t 
     if (mx) return gateup ? launch<FMT_MXFP4, NARROW_GATEUP>(p, smem, st) : launch<FMT_MXFP4, NARROW_PLAIN>(p, smem, st);
     switch (kind) {
         case NARROW_GATEUP: return launch<FMT_BF16, NARROW_GATEUP>(p, smem, st);
+        case NARROW_GATEUP_PARTS: return launch<FMT_BF16, NARROW_GATEUP_PARTS>(p, smem, st);
+        case NARROW_PLAIN_PARTS: return launch<FMT_BF16, NARROW_PLAIN_PARTS>(p, smem, st);
         case NARROW_DACT: return launch<FMT_BF16, NARROW_DACT>(p, smem, st);
         case NARROW_DX: return launch<FMT_BF16, NARROW_DX>(p, smem, st);
         default: return launch<FMT_BF16, NARROW_PLAIN>(p, smem, st);

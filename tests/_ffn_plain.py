@@ -48,15 +48,15 @@ def _h_parts(x, w1, w3, kind):
     return g, u, n * F32 * (x.abs() @ w1.abs().T), n * F32 * (x.abs() @ w3.abs().T)
 
 
-def forward_bound(x, w1, w3, w2, kind):
-    """|kernel - forward|, element by element, for h and out rounded to bf16 and fp32 sums;
-    the activation is within 2^-20 of itself."""
+def forward_bound(x, w1, w3, w2, kind, h_half=HALF):
+    """|kernel - forward|, element by element, for h rounded by h_half of itself at most, out rounded
+    to bf16 and fp32 sums; the activation is within 2^-20 of itself."""
     x, w1, w3, w2 = (t.double() for t in (x, w1, w3, w2))
     g, u, eg, eu = _h_parts(x, w1, w3, kind)
     a = act(g, kind)
     h = (a * u).abs()
     eh = SLOPE * eg * (u.abs() + eu) + (a.abs() + SLOPE * eg) * eu + 2.0 ** -20 * h
-    eh = eh + HALF * (h + eh)
+    eh = eh + h_half * (h + eh)
     eo = eh @ w2.abs().T + w2.shape[1] * F32 * ((h + eh) @ w2.abs().T)
     return eo + HALF * (((a * u) @ w2.T).abs() + eo)
 

@@ -180,7 +180,7 @@ def _saved_parts(saved, m, I):
     return a, d, saved[2 * n:].view(torch.bfloat16)[:m * I].reshape(m, I)
 
 
-FFN_SIZES = [(1, 2048, 768), (1, 8, 8), (3, 24, 40), (16, 256, 128), (17, 136, 264), (48, 1024, 512), (65, 520, 1032),
+FFN_SIZES = [(1, 2048, 768), (1, 8, 8), (3, 24, 40), (8, 264, 520), (9, 264, 520), (16, 256, 128), (17, 136, 264), (48, 1024, 512), (65, 520, 1032),
              (128, 256, 256), (200, 512, 384), (333, 1032, 2056), (777, 1016, 680), (130, 1032, 72), (256, 328, 200),
              (257, 4104, 64), (500, 200, 136)]
 
@@ -192,9 +192,13 @@ def test_forward(B, m, H, I, kind):
     x = _n(m, m, H)
     blk = B.GatedFfn(*w, act=kind)
     out = blk.forward(x)
-    _within(out, P.forward(x, *w, kind), P.forward_bound(x, *w, kind))
+    ref = P.forward(x, *w, kind)
     out2, saved = blk.forward(x, save=True)
-    assert torch.equal(out, out2)
+    _within(out2, ref, P.forward_bound(x, *w, kind))
+    if m > 8:
+        assert torch.equal(out, out2)
+    else:  # h in two parts: half a step of the second one
+        _within(out, ref, P.forward_bound(x, *w, kind, P.HALF ** 2))
     g, u = (x.double() @ v.double().T for v in w[:2])
     eg, eu = (H * P.F32 * (x.double().abs() @ v.double().abs().T) for v in w[:2])
     a, s = P.act_slope(g, kind)
