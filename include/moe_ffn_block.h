@@ -102,6 +102,14 @@ MOE_API int moe_ffn_backward(const moe_ffn* ffn, const void* dout, int64_t ldd, 
                              const void* saved, int64_t m, void* dx, void* dw1, void* dw3, void* dw2,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* As moe_layer_set_wait_limit and moe_layer_stall_test: the limit (ns; 0: 2 s)
+ * of every bounded wait in the handle's kernels, and the test of the failure
+ * path, in which their tensor-core issuers first wait on a barrier that nothing
+ * completes.  A wait that runs out leaves DEV_ERR_TIMEOUT (2) in the workspace's
+ * error word, and that call's outputs unspecified. */
+MOE_API int moe_ffn_set_wait_limit(moe_ffn* ffn, uint64_t ns);
+MOE_API int moe_ffn_stall_test(moe_ffn* ffn, int enable);
+
 /* Kernels the last successful call on `ffn` launched. */
 MOE_API int moe_ffn_last_launch_count(const moe_ffn* ffn);
 

@@ -33,7 +33,7 @@ EXPORTED = (
     "moe_last_launch_count", "moe_kernel_timing_enable", "moe_kernel_timing_read", "moe_kernel_count",
     "moe_kernel_name", "moe_status_string",
     "moe_ffn_create", "moe_ffn_destroy", "moe_ffn_workspace_size", "moe_ffn_saved_size", "moe_ffn_forward", "moe_ffn_backward",
-    "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
+    "moe_ffn_set_wait_limit", "moe_ffn_stall_test", "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
     "moe_mxfp4_dequant", "moe_mxfp4_gemm_workspace_size", "moe_mxfp4_gemm",
     "moe_mxfp4_linear_workspace_size", "moe_mxfp4_linear", "moe_mxfp4_linear_f32",
 )
@@ -120,6 +120,8 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_ffn_saved_size.argtypes = [_vp, _i64, ctypes.POINTER(sz)]
         lib.moe_ffn_forward.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _vp, sz, _vp]
         lib.moe_ffn_backward.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_ffn_set_wait_limit.argtypes = [_vp, ctypes.c_uint64]
+        lib.moe_ffn_stall_test.argtypes = [_vp, ctypes.c_int]
         lib.moe_ffn_last_launch_count.argtypes = [_vp]
         lib.moe_mxfp4_scales_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
         lib.moe_mxfp4_quant.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
@@ -614,6 +616,14 @@ class GatedFfn:
                 self._ws_at = (self._ws.data_ptr(), self._ws.numel())
             self._fits[backward] = m
         return self._ws
+
+    def set_wait_limit(self, ns: int):
+        """Limit (ns) of the kernels' bounded waits; 0 restores 2 s."""
+        _check(self.lib.moe_ffn_set_wait_limit(self.handle, int(ns)), "moe_ffn_set_wait_limit")
+
+    def stall_test(self, enable: bool):
+        """Make the kernels wait on a barrier nothing completes."""
+        _check(self.lib.moe_ffn_stall_test(self.handle, int(bool(enable))), "moe_ffn_stall_test")
 
     def last_launch_count(self) -> int:
         return self.lib.moe_ffn_last_launch_count(self.handle)

@@ -19,6 +19,8 @@ struct moe_ffn {
     int device;
     mutable int last_launches;
     mutable const void* last_ws;  // its header is known to be clean
+    uint64_t wait_ns;
+    int stall;
     // maps of the weights: along K (128-row boxes), along M or N, MXFP4 codes and scales
     CUtensorMap k1, k3, k2, mn1, mn3, mn2;
     int mn13_order, mn2_order;
@@ -96,7 +98,8 @@ FfnProducts products(const moe_ffn* f, void* ws) {
     FfnProducts p{};
     p.act = f->cfg.activation;
     p.hdr = at<WsHeader>(ws, 0);
-    p.wait_ns = kWaitNs;
+    p.wait_ns = f->wait_ns;
+    p.stall = f->stall;
     return p;
 }
 
@@ -111,13 +114,15 @@ FfnProduct& add(FfnProducts& p, int M, int N, int K, void* out) {
     return q;
 }
 
-NarrowProduct narrow(int T, int R, int K, void* ws) {
+// f: the block, or null for a product of its own.
+NarrowProduct narrow(const moe_ffn* f, int T, int R, int K, void* ws) {
     NarrowProduct p{};
     p.T = T;
     p.R = R;
     p.K = K;
     p.hdr = at<WsHeader>(ws, 0);
-    p.wait_ns = kWaitNs;
+    p.wait_ns = f ? f->wait_ns : kWaitNs;
+    p.stall = f ? f->stall : 0;
     return p;
 }
 
@@ -129,7 +134,7 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
     const bool parts = m <= kNarrowParts && !saved;  // h is not kept: two parts (ffn_narrow.cu)
     float* saved_d = saved ? saved + saved_floats(m, I) : nullptr;
     if (narrow_is_faster(m, I, false)) {
-        NarrowProduct g = narrow(m, I, H, ws);
+        NarrowProduct g = narrow(f, m, I, H, ws);
         if (!ffn_map(&g.b[0], x, m, H, ldx, nt)) return MOE_ERR_CUDA;
         g.a[0] = f->k1;
         g.a[1] = f->k3;
@@ -149,7 +154,7 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
         if (launch_ffn_products(p, saved ? EPI_GATEUP_SAVE : EPI_GATEUP, st) != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (narrow_is_faster(m, H, false)) {
-        NarrowProduct d = narrow(m, H, I, ws);
+        NarrowProduct d = narrow(f, m, H, I, ws);
         if (!ffn_map(&d.b[0], h, parts ? 2 * kNarrowParts : m, I, I, nt)) return MOE_ERR_CUDA;
         d.a[0] = f->k2;
         d.early = 1;  // behind the kernel that wrote h
@@ -166,13 +171,14 @@ int forward_bf16(const moe_ffn* f, const void* x, int64_t ldx, int m, void* out,
     return MOE_OK;
 }
 
-MxProduct mx_product(int M, int N, int K, void* ws) {
+MxProduct mx_product(const moe_ffn* f, int M, int N, int K, void* ws) {
     MxProduct p{};
     p.M = M;
     p.N = N;
     p.kblocks = ceil_div(K, 256);
     p.hdr = at<WsHeader>(ws, 0);
-    p.wait_ns = kWaitNs;
+    p.wait_ns = f ? f->wait_ns : kWaitNs;
+    p.stall = f ? f->stall : 0;
     return p;
 }
 
@@ -184,7 +190,7 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
     f->last_launches = 3;
     if (narrow_is_faster(m, I, true)) {
         // each kernel after the quantiser streams its weights while the one before drains
-        NarrowProduct g = narrow(m, I, H, ws), d = narrow(m, H, I, ws);
+        NarrowProduct g = narrow(f, m, I, H, ws), d = narrow(f, m, H, I, ws);
         const uint32_t nt = (uint32_t)narrow_tokens(m);
         const bool fused = m <= kNarrowQuant;  // x is quantised by the gate/up kernel itself
         if (fused) {
@@ -214,7 +220,7 @@ int forward_mxfp4(const moe_ffn* f, const Layout& lo, const void* x, int64_t ldx
                    ? MOE_OK
                    : MOE_ERR_CUDA;
     }
-    MxProduct g = mx_product(m, I, H, ws), d = mx_product(m, H, I, ws);
+    MxProduct g = mx_product(f, m, I, H, ws), d = mx_product(f, m, H, I, ws);
     if (!mx_code_map(&g.a, xq, m, H, 128) || !mx_scale_map(&g.as, xs, m, H) || !mx_code_map(&d.a, hq, m, I, 128) ||
         !mx_scale_map(&d.as, hs, m, I))
         return MOE_ERR_CUDA;
@@ -270,7 +276,7 @@ int check_gemm(int64_t m, int64_t n, int64_t k, const uint8_t* w, const uint8_t*
 int gemm(const uint8_t* a, const uint8_t* as, int m, const uint8_t* b, const uint8_t* bs, int n, int k, void* out,
          void* ws, bool early, cudaStream_t st) {
     if (narrow_is_faster(m, n, true)) {
-        NarrowProduct q = narrow(m, n, k, ws);
+        NarrowProduct q = narrow(nullptr, m, n, k, ws);
         if (!mx_code_map(&q.a[0], b, n, k, 128) || !mx_scale_map(&q.as[0], bs, n, k) ||
             !mx_code_map(&q.b[0], a, m, k, (uint32_t)narrow_tokens(m)) || !mx_scale_map(&q.bs, as, m, k))
             return MOE_ERR_CUDA;
@@ -278,7 +284,7 @@ int gemm(const uint8_t* a, const uint8_t* as, int m, const uint8_t* b, const uin
         q.out = static_cast<uint16_t*>(out);
         return launch_ffn_narrow(q, true, NARROW_PLAIN, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
-    MxProduct g = mx_product(m, n, k, ws);
+    MxProduct g = mx_product(nullptr, m, n, k, ws);
     if (!mx_code_map(&g.a, a, m, k, 128) || !mx_scale_map(&g.as, as, m, k) || !mx_code_map(&g.b[0], b, n, k, 128) ||
         !mx_scale_map(&g.bs[0], bs, n, k))
         return MOE_ERR_CUDA;
@@ -305,7 +311,7 @@ int linear(const void* x, bool f32, int64_t ldx, int64_t m, const uint8_t* w, co
     if (rc != MOE_OK || m == 0) return rc;
     if (m <= kNarrowQuant && !f32) {  // quantised by the product's kernel itself
         if (!x || !aligned(x, 16) || ldx < k || ldx % 8) return MOE_ERR_INVALID_ARG;
-        NarrowProduct q = narrow((int)m, (int)n, (int)k, workspace);
+        NarrowProduct q = narrow(nullptr, (int)m, (int)n, (int)k, workspace);
         if (!mx_code_map(&q.a[0], w, n, k, 128) || !mx_scale_map(&q.as[0], ws, n, k)) return MOE_ERR_CUDA;
         q.x = static_cast<const uint16_t*>(x);
         q.ldx = (size_t)ldx;
@@ -348,6 +354,7 @@ int moe_ffn_create(const moe_ffn_config* cfg, const moe_ffn_weights* w, moe_ffn*
     f->cfg = c;
     f->w = *w;
     f->device = dev;
+    f->wait_ns = kWaitNs;
     const uint64_t H = c.hidden, I = c.inter;
     const bool ok = mx ? mx_code_map(&f->k1, w->w1, I, H, 128) && mx_code_map(&f->k3, w->w3, I, H, 128) &&
                              mx_code_map(&f->k2, w->w2, H, I, 128) && mx_scale_map(&f->s1, w->s1, I, H) &&
@@ -367,6 +374,18 @@ int moe_ffn_create(const moe_ffn_config* cfg, const moe_ffn_weights* w, moe_ffn*
 
 int moe_ffn_destroy(moe_ffn* f) {
     delete f;
+    return MOE_OK;
+}
+
+int moe_ffn_set_wait_limit(moe_ffn* f, uint64_t ns) {
+    if (!f) return MOE_ERR_INVALID_ARG;
+    f->wait_ns = ns ? ns : kWaitNs;
+    return MOE_OK;
+}
+
+int moe_ffn_stall_test(moe_ffn* f, int enable) {
+    if (!f || (enable != 0 && enable != 1)) return MOE_ERR_INVALID_ARG;
+    f->stall = enable;
     return MOE_OK;
 }
 
@@ -392,7 +411,7 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, voi
     if (bad_rows(x, ldx, f->cfg.hidden) || !out || !aligned(out, 16) || (saved && !aligned(saved, 32)))
         return MOE_ERR_INVALID_ARG;
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
-    if (mx && saved) return MOE_ERR_UNSUPPORTED;
+    if (mx && (saved || too_large(m, f->cfg.hidden))) return MOE_ERR_UNSUPPORTED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
     float* sa = static_cast<float*>(saved);
@@ -422,7 +441,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     const uint32_t nt = (uint32_t)narrow_tokens(n);
     // dh = dout W2 and, in its epilogue, dg and du
     if (narrow_is_faster(n, I, false)) {
-        NarrowProduct q = narrow(n, I, H, workspace);
+        NarrowProduct q = narrow(f, n, I, H, workspace);
         if (!ffn_map(&q.b[0], dout, m, H, ldd, nt)) return MOE_ERR_CUDA;
         q.a[0] = f->mn2;
         q.a_mn = f->mn2_order;
@@ -446,7 +465,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
     // dx, by itself or with the weight gradients in one launch
     FfnProducts r = products(f, workspace);
     if (dx && narrow_is_faster(n, H, false)) {
-        NarrowProduct d = narrow(n, H, I, workspace);
+        NarrowProduct d = narrow(f, n, H, I, workspace);
         if (!ffn_map(&d.b[0], dg, m, I, I, nt) || !ffn_map(&d.b[1], du, m, I, I, nt)) return MOE_ERR_CUDA;
         d.a[0] = f->mn1;
         d.a[1] = f->mn3;

@@ -47,7 +47,8 @@ struct FfnProducts {
     float *a, *d;
     uint16_t* out_du;       // EPI_DACT (out: dg)
     WsHeader* hdr;
-    uint64_t wait_ns;
+    uint64_t wait_ns;  // limit of every protocol wait
+    int stall;         // 1: the issuer first waits on a barrier nothing completes
 };
 
 // Maps of a bf16 operand [rows, cols] (row stride ld elements), all even, as
@@ -72,7 +73,8 @@ struct MxProduct {
     uint8_t *codes, *scales;  // gate/up: h as MXFP4, [M, N/2] and packed scales
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;
-    uint64_t wait_ns;
+    uint64_t wait_ns;  // limit of every protocol wait
+    int stall;         // 1: the issuer first waits on a barrier nothing completes
 };
 bool mx_code_map(CUtensorMap* m, const void* codes, uint64_t rows, uint64_t k, uint32_t box_rows);
 bool mx_scale_map(CUtensorMap* m, const void* scales, uint64_t rows, uint64_t k);
@@ -103,7 +105,8 @@ struct NarrowProduct {
     uint8_t *codes, *scales;  // gate/up of an MXFP4 block: h
     int nkt;                  // ... scale tiles per row of it
     WsHeader* hdr;
-    uint64_t wait_ns;
+    uint64_t wait_ns;  // limit of every protocol wait
+    int stall;         // 1: the issuer first waits on a barrier nothing completes
     // set by launch_ffn_narrow
     int nt, kstages, slices, stages, ring_bytes, tmem_cols;
 };

@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
     const int stride = stage_stride(ss);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 1);
+    const uint32_t never = smem_u32(bars + 2 * MAX_STAGES + 1);  // stall test: no thread ever arrives here
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             mbar_init(empty0 + 8 * s, 1);
         }
         mbar_init(done, 1);
+        mbar_init(never, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         int i = pre, s = 0;
         uint32_t ph = 0;
         for (; i < n; ++i) {
-            if (!mbar_wait(empty0 + 8 * s, ph, p.wait_ns)) {
+            if (!warp_wait(empty0 + 8 * s, ph, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -204,12 +206,12 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         for (int j = max(0, i - p.stages); j < i; ++j)  // every issued copy has landed
             mbar_wait(full0 + 8 * (j % p.stages), (j / p.stages) & 1u, DRAIN_NS);
     } else if (warp == 1) {
-        bool ok = true;
+        bool ok = !p.stall || warp_wait(never, 0, p.wait_ns);
         const uint32_t idesc = idesc_bf16(128, p.nt) | (MN ? kIdescAMn : 0u);
         int s = 0;
         uint32_t ph = 0;
-        for (int i = 0; i < k1 - k0; ++i) {
-            if (*abort_flag || !mbar_wait(full0 + 8 * s, ph, p.wait_ns)) {
+        for (int i = 0; ok && i < k1 - k0; ++i) {
+            if (warp_sees(abort_flag) || !warp_wait(full0 + 8 * s, ph, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         uint32_t ph = 1;
         for (int i = 0; i < n; ++i) {
             const Piece after = load(i + 2);
-            if (*abort_flag || !mbar_wait(empty0 + 8 * s, ph, p.wait_ns)) {
+            if (warp_sees(abort_flag) || !warp_wait(empty0 + 8 * s, ph, p.wait_ns)) {
                 if (lane == 0) {
                     set_error(p.hdr, DEV_ERR_TIMEOUT, 44);
                     *abort_flag = 1;

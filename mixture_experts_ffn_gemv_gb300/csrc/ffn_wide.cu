@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
     const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = smem_u32(bars + 2 * STAGES + 2);
     const uint32_t drain = smem_u32(bars + 2 * STAGES + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+    const uint32_t never = smem_u32(bars + 2 * STAGES + 5);  // stall test: no thread ever arrives here
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 6);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
             mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);
         }
         mbar_init(drain, 1);
+        mbar_init(never, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         uint32_t s = 0, ph = 1, n = 0;
         bool ok = true;
         for (int i = 0, t; ok && (t = turns.item(i)) >= 0; ++i) {
-            if (*abort_flag) break;
+            if (warp_sees(abort_flag)) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
             const int m0 = w.mt * 256 + (int)rank * BM;
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                 const CUtensorMap* ma = &q.a[src];
                 const CUtensorMap* mb = &q.b[GATEUP ? rank : src];
                 for (int kb = 0; kb < q.kblocks; ++kb) {
-                    if (!mbar_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
+                    if (!warp_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -225,15 +227,15 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
     } else if (warp == 1) {
         if (leader) {
             uint32_t s = 0, ph = 0, tc = 0;
-            bool ok = true;
+            bool ok = !p.stall || warp_wait(never, 0, p.wait_ns);
             for (int t; ok && (t = turns.item((int)tc)) >= 0; ++tc) {
-                if (*abort_flag) break;
+                if (warp_sees(abort_flag)) break;
                 const FfnProduct& q = p.p[item_of(p, t).op];
                 const uint32_t idesc = idesc_bf16(2 * BM, BN) | (q.a_mn ? kIdescAMn : 0u) | (q.b_mn ? kIdescBMn : 0u);
                 // 16 of K further: 32 bytes along a swizzled row, or 16 rows of 128
                 const uint32_t sta = q.a_mn ? 128 : 2, stb = q.b_mn ? 128 : 2;
                 const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
-                if (!mbar_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, p.wait_ns)) {
+                if (!warp_wait_cluster(tempty0 + 8 * acc, aph ^ 1u, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
                 const uint64_t ad0 = q.a_mn ? desc_sw128_mn(sbase) : desc_sw128(sbase);
                 const uint64_t bd0 = q.b_mn ? desc_sw128_mn(sbase + A_BYTES) : desc_sw128(sbase + A_BYTES);
                 for (int kb = 0; kb < kbs; ++kb) {
-                    if (!mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
+                    if (!warp_wait_cluster(full0 + 8 * s, ph, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
         const uint32_t stg = sbase + Shape<EPI>::STG_OFF + (warp - 2) * 4096;
         uint32_t tc = 0;
         for (int t; (t = turns.item((int)tc)) >= 0; ++tc) {
-            if (*abort_flag) break;
+            if (warp_sees(abort_flag)) break;
             const Item w = item_of(p, t);
             const FfnProduct& q = p.p[w.op];
             const int row0 = w.mt * 256 + (int)rank * BM + q4 * 32;  // first of this warp's rows of D
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(Shape<EPI>::THREADS, 1) ffn_products(const __g
             const bool ok = row0 + lane < q.M;
             const size_t at = (size_t)(row0 + lane) * N + col0;
             const uint32_t acc = tc & 1u, aph = (tc >> 1) & 1u;
-            if (!mbar_wait_cluster(tfull0 + 8 * acc, aph, p.wait_ns)) {
+            if (!warp_wait_cluster(tfull0 + 8 * acc, aph, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 23);
                 *abort_flag = 1;
                 break;

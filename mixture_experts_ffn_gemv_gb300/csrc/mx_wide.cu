@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
     const uint32_t drain = smem_u32(bars + 2 * STAGES + 2);
     // scales of a stage: landed in this CTA's shared memory; in both CTAs' TMEM
     const uint32_t sland0 = smem_u32(bars + 2 * STAGES + 3), sfull0 = smem_u32(bars + 3 * STAGES + 3);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 3);
+    const uint32_t never = smem_u32(bars + 4 * STAGES + 3);  // stall test: no thread ever arrives here
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 4 * STAGES + 4);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         mbar_init(tfull, 1);
         mbar_init(tempty, 2 * EPI_WARPS);
         mbar_init(drain, 1);
+        mbar_init(never, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -124,14 +126,14 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         uint32_t s = 0, ph = 1, n = 0;
         bool ok = true;
         for (int t = cl; t < total && ok; t += ncl) {
-            if (*abort_flag) break;
+            if (warp_sees(abort_flag)) break;
             const int mt = t / p.n_tiles, nt = t % p.n_tiles;
             const int m0 = mt * 256 + (int)rank * BM, mt0 = m0 >> 7;
             const int n0 = GATEUP ? nt * 128 : nt * 256 + (int)rank * 128;
             const int bt0 = GATEUP ? nt : 2 * nt, bt1 = GATEUP ? nt : 2 * nt + 1;
             const CUtensorMap *mb = &p.b[GATEUP ? rank : 0], *ms1 = &p.bs[GATEUP ? 1 : 0];
             for (int kb = 0; kb < p.kblocks; ++kb) {
-                if (!mbar_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
+                if (!warp_wait_cluster(empty0 + 8 * s, ph, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -172,13 +174,13 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         // stage's four MMAs, more than the tensor core does.)
         if (leader) {
             uint32_t s = 0, ph = 0, tc = 0;
-            bool ok = true;
+            bool ok = !p.stall || warp_wait(never, 0, p.wait_ns);
             for (int t = cl; t < total && ok; t += ncl, ++tc) {
-                if (*abort_flag) break;
+                if (warp_sees(abort_flag)) break;
                 for (int kb = 0; kb < p.kblocks; ++kb) {
-                    if ((kb == 0 && !mbar_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) ||
-                        !mbar_wait_cluster(full0 + 8 * s, ph, p.wait_ns) ||
-                        !mbar_wait_cluster(sfull0 + 8 * s, ph, p.wait_ns)) {
+                    if ((kb == 0 && !warp_wait_cluster(tempty, (tc & 1u) ^ 1u, p.wait_ns)) ||
+                        !warp_wait_cluster(full0 + 8 * s, ph, p.wait_ns) ||
+                        !warp_wait_cluster(sfull0 + 8 * s, ph, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         const uint32_t n = total > cl ? (uint32_t)((total - cl + ncl - 1) / ncl) * p.kblocks : 0;
         uint32_t s = 0, ph = 0;
         for (uint32_t it = 0; it < n; ++it) {
-            if (*abort_flag || !mbar_wait(sland0 + 8 * s, ph, p.wait_ns)) {
+            if (warp_sees(abort_flag) || !warp_wait(sland0 + 8 * s, ph, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 34);
                 *abort_flag = 1;
                 break;
@@ -246,11 +248,11 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         const int q4 = warp & 3, part = (warp - 2) >> 2;  // lane quarter, share of the columns
         uint32_t tc = 0;
         for (int t = cl; t < total; t += ncl, ++tc) {
-            if (*abort_flag) break;
+            if (warp_sees(abort_flag)) break;
             const int mt = t / p.n_tiles, nt = t % p.n_tiles;
             const int r = mt * 256 + (int)rank * BM + q4 * 32 + lane;
             const bool ok = r < p.M, any = r - lane < p.M;
-            if (!mbar_wait_cluster(tfull, tc & 1u, p.wait_ns)) {
+            if (!warp_wait_cluster(tfull, tc & 1u, p.wait_ns)) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 33);
                 *abort_flag = 1;
                 break;

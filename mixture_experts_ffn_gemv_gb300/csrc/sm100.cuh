@@ -341,5 +341,16 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// Waits of a whole warp, for loops that it walks together: every lane gets the
+// same answer, so that they part neither when a wait runs out nor when another
+// warp has given up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, limit_ns));
+}
+__device__ __forceinline__ bool warp_sees(volatile int* flag) { return __any_sync(0xffffffffu, *flag); }
+
 }  // namespace sm100
 }  // namespace moe

@@ -54,6 +54,7 @@ def test_null_arguments(B):
     assert lib.moe_ffn_forward(None, FAKE, 8, 1, FAKE, None, FAKE, 1 << 20, None) == 1
     assert lib.moe_ffn_backward(None, FAKE, 8, FAKE, 8, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, 1 << 20, None) == 1
     assert lib.moe_ffn_last_launch_count(None) == -1
+    assert lib.moe_ffn_set_wait_limit(None, 0) == 1 and lib.moe_ffn_stall_test(None, 1) == 1
     assert lib.moe_ffn_destroy(None) == 0
 
 

@@ -361,6 +361,35 @@ def test_repeatable(B):
         assert all(torch.equal(a, b) for a, b in zip(first, (o, _saved_parts(s, m, I)[2], *blk.backward(dout, x, s))))
 
 
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("m", [3, 300])
+def test_a_wait_that_runs_out(B, mx, m):
+    """A stalled issuer ends its kernel by the wait limit with the error word set; the call after it
+    is whole."""
+    H, I = 256, 512
+    w = _weights(2, H, I)
+    blk = B.GatedFfn(*(_quantised(B, w)[0] if mx else w))
+    x = _n(3, m, H)
+    want = blk.forward(x)
+    if not mx:
+        _, saved = blk.forward(x, save=True)
+        grads = blk.backward(x, x, saved)
+    assert blk.device_status() == 0
+    blk.set_wait_limit(20_000_000)
+    blk.stall_test(True)
+    blk.forward(x)
+    assert blk.device_status() == 2  # read, and cleared
+    if not mx:
+        blk.backward(x, x, saved)
+        assert blk.device_status() == 2
+    blk.stall_test(False)
+    blk.set_wait_limit(0)
+    assert torch.equal(blk.forward(x), want)
+    if not mx:
+        assert all(torch.equal(a, b) for a, b in zip(blk.backward(x, x, saved), grads))
+    assert blk.device_status() == 0
+
+
 def test_refusals(B):
     H, I = 64, 96
     w1, w3, w2 = _weights(1, H, I)
