@@ -320,6 +320,37 @@ def test_extreme_pre_activations(B):
         assert ((got[0].double() - want[0]).abs() <= 3 * P.HALF * part + 1e-30 + 2.0 ** -20 * (dout.double() * xs).abs()).all()
 
 
+@pytest.mark.parametrize("mx", [False, True])
+def test_offsets_past_32_bits(B, mx):
+    """h has 2.4e9 elements (MXFP4: as many bytes of codes): the last rows against the formula, and
+    alone; the last rows of dx likewise."""
+    H, I, m, last = 64, 8192, 600_000 if mx else 300_000, 300
+    w = _weights(7, H, I)
+    x = _n(8, m, H)
+    if mx:
+        pairs, vals = _quantised(B, w)
+        blk = B.GatedFfn(*pairs)
+        ref, bound = P.mx_forward(x[-last:], *vals, "silu")
+        _within(blk.forward(x)[-last:], ref, bound)
+        return
+    blk = B.GatedFfn(*w)
+    tail = x[-last:].contiguous()
+    out, saved = blk.forward(x, save=True)
+    _within(out[-last:], P.forward(tail, *w, "silu"), P.forward_bound(tail, *w, "silu"))
+    dx, *_ = blk.backward(x, x, saved, need_dw=False)
+    _within(dx[-last:], P.backward(tail, tail, *w, "silu")[0], P.backward_bounds(tail, tail, *w, "silu")[0])
+    assert blk.device_status() == 0
+
+
+def test_quant_past_32_bits(B):
+    rows, n = 300_000, 8192
+    x = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    x[-200:] = _n(5, 200, n)
+    codes, scales = B.moe_mxfp4_quant(x)
+    back = B.moe_mxfp4_dequant(codes, scales)[-200:].double()
+    assert torch.equal(back, P.mx_round(x[-200:]))
+
+
 def test_graph_capture_and_other_streams(B):
     """Forward and backward captured in a graph, replayed on new inputs, and run on a side stream:
     the same bits as eager calls."""
