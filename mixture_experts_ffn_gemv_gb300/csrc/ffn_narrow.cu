@@ -348,86 +348,76 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
         tc_fence_before();
     }
     cluster_sync();
-    // tokens, dealt over the cluster's warps, U at a time; the loads of all
-    // slices are on their way (one takes a microsecond) before the first is added
-    constexpr int U = GATEUP ? 1 : 2;
+    // Tokens, dealt over the cluster's warps; the loads of all slices of a token
+    // are on their way before the first is added.  One token at a time: this code
+    // runs once or a few times per CTA, and its size costs more (instructions
+    // fetched cold) than more loads under way would save.
     const uint32_t pbase = smem_u32(part) + lane * 16;
     const int r = row0 + lane * 4;  // this lane's output columns r .. r + 3
-    for (int j0 = (int)rank + S * warp; j0 < ntok; j0 += U * S * WARPS) {
-        float v0[U][4] = {}, v1[U][4] = {};
-        float4 q0[U][MAX_SLICES], q1[U][MAX_SLICES];
+    for (int j = (int)rank + S * warp; j < ntok; j += S * WARPS) {
+        float v0[4] = {}, v1[4] = {};
+        float4 q0[MAX_SLICES], q1[MAX_SLICES];
 #pragma unroll
         for (int s = 0; s < MAX_SLICES; ++s)
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-                const int j = j0 + x * S * WARPS;
-                if (s < S && j < ntok) {
-                    const uint32_t a = mapa(pbase + j * 512, s);
-                    q0[x][s] = ld_cluster4(a);
-                    if (GATEUP) q1[x][s] = ld_cluster4(a + p.nt * 512);
-                }
+            if (s < S) {
+                const uint32_t a = mapa(pbase + j * 512, s);
+                q0[s] = ld_cluster4(a);
+                if (GATEUP) q1[s] = ld_cluster4(a + p.nt * 512);
             }
 #pragma unroll
         for (int s = 0; s < MAX_SLICES; ++s)
-#pragma unroll
-            for (int x = 0; x < U; ++x)
-                if (s < S) {
-                    add4(v0[x], q0[x][s]);
-                    if (GATEUP) add4(v1[x], q1[x][s]);
-                }
-#pragma unroll
-        for (int x = 0; x < U; ++x) {
-            const int j = j0 + x * S * WARPS;
-            if (j >= ntok) break;
-            const size_t t = (size_t)(tok0 + j);
-            if (GATEUP && MX) {
-                float h[4];
-                uint32_t a = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = r < p.R ? glu(v0[x][i], v1[x][i], p.act) : 0.f;
-                    a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
-                }
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-                const uint32_t sc = mx_scale(a);
-                const uint32_t w = sc == 255u ? 0u : mx_codes4(h, mx_inverse(sc));
-                if (r < p.R) *reinterpret_cast<uint16_t*>(p.codes + (t * p.R + r) / 2) = (uint16_t)w;
-                if ((lane & 7) == 0) p.scales[mx_scale_at(t, (size_t)(tile * 4 + (lane >> 3)), p.nkt)] = (uint8_t)sc;
-            } else if (r < p.R) {  // R is a multiple of 8: whole quads
-                const size_t at = t * p.R + r;
-                float o[4];
-                if (KIND == NARROW_DACT) {  // dg = dh d; du = dh a
-                    const size_t sat = saved_at(t, r, p.R);
-                    const float4 a = *reinterpret_cast<const float4*>(p.sa + sat), d = *reinterpret_cast<const float4*>(p.sd + sat);
-                    const float* h = v0[x];
-                    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(h[0] * d.x, h[1] * d.y), pack_bf16x2(h[2] * d.z, h[3] * d.w));
-                    *reinterpret_cast<uint2*>(p.du + at) = make_uint2(pack_bf16x2(h[0] * a.x, h[1] * a.y), pack_bf16x2(h[2] * a.z, h[3] * a.w));
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[i] = v0[x][i];
-                    if (GATEUP) {
-                        float a, slope;
-                        act_slope(v0[x][i], p.act, a, slope);
-                        o[i] = a * v1[x][i];
-                        v0[x][i] = a;
-                        v1[x][i] *= slope;
-                    }
-                }
-                if (GATEUP && p.sa) {
-                    const size_t sat = saved_at(t, r, p.R);
-                    *reinterpret_cast<float4*>(p.sa + sat) = make_float4(v0[x][0], v0[x][1], v0[x][2], v0[x][3]);
-                    *reinterpret_cast<float4*>(p.sd + sat) = make_float4(v1[x][0], v1[x][1], v1[x][2], v1[x][3]);
-                }
-                const uint2 hi = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-                *reinterpret_cast<uint2*>(p.out + at) = hi;
-                if (GATEUP && PARTS)  // what rounding left of h, 8 rows further on
-                    *reinterpret_cast<uint2*>(p.out + at + 8 * (size_t)p.R) =
-                        make_uint2(pack_bf16x2(o[0] - bf16lo(hi.x), o[1] - bf16hi(hi.x)),
-                                   pack_bf16x2(o[2] - bf16lo(hi.y), o[3] - bf16hi(hi.y)));
+            if (s < S) {
+                add4(v0, q0[s]);
+                if (GATEUP) add4(v1, q1[s]);
             }
+        const size_t t = (size_t)(tok0 + j);
+        if (GATEUP && MX) {
+            float h[4];
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[i] = r < p.R ? glu(v0[i], v1[i], p.act) : 0.f;
+                a = max(a, __float_as_uint(h[i]) & 0x7fffffffu);
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const uint32_t sc = mx_scale(a);
+            const uint32_t w = sc == 255u ? 0u : mx_codes4(h, mx_inverse(sc));
+            if (r < p.R) *reinterpret_cast<uint16_t*>(p.codes + (t * p.R + r) / 2) = (uint16_t)w;
+            if ((lane & 7) == 0) p.scales[mx_scale_at(t, (size_t)(tile * 4 + (lane >> 3)), p.nkt)] = (uint8_t)sc;
+        } else if (r < p.R) {  // R is a multiple of 8: whole quads
+            const size_t at = t * p.R + r;
+            float o[4];
+            if (KIND == NARROW_DACT) {  // dg = dh d; du = dh a
+                const size_t sat = saved_at(t, r, p.R);
+                const float4 a = *reinterpret_cast<const float4*>(p.sa + sat), d = *reinterpret_cast<const float4*>(p.sd + sat);
+                const float* h = v0;
+                *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16x2(h[0] * d.x, h[1] * d.y), pack_bf16x2(h[2] * d.z, h[3] * d.w));
+                *reinterpret_cast<uint2*>(p.du + at) = make_uint2(pack_bf16x2(h[0] * a.x, h[1] * a.y), pack_bf16x2(h[2] * a.z, h[3] * a.w));
+                continue;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = v0[i];
+                if (GATEUP) {
+                    float a, slope;
+                    act_slope(v0[i], p.act, a, slope);
+                    o[i] = a * v1[i];
+                    v0[i] = a;
+                    v1[i] *= slope;
+                }
+            }
+            if (GATEUP && p.sa) {
+                const size_t sat = saved_at(t, r, p.R);
+                *reinterpret_cast<float4*>(p.sa + sat) = make_float4(v0[0], v0[1], v0[2], v0[3]);
+                *reinterpret_cast<float4*>(p.sd + sat) = make_float4(v1[0], v1[1], v1[2], v1[3]);
+            }
+            const uint2 hi = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+            *reinterpret_cast<uint2*>(p.out + at) = hi;
+            if (GATEUP && PARTS)  // what rounding left of h, 8 rows further on
+                *reinterpret_cast<uint2*>(p.out + at + 8 * (size_t)p.R) =
+                    make_uint2(pack_bf16x2(o[0] - bf16lo(hi.x), o[1] - bf16hi(hi.x)),
+                               pack_bf16x2(o[2] - bf16lo(hi.y), o[3] - bf16hi(hi.y)));
         }
     }
     cluster_sync();  // no CTA leaves while another reads its sums
