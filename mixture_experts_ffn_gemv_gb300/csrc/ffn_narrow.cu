@@ -1,6 +1,10 @@
 // Products of the gated feed-forward block for few tokens: every weight is read
 // once, so the time is that of streaming the weights.
 //
+// Both products of a block of 7168 x 2048, weights from HBM: bf16 (88 MB) 24 us
+// for 48 tokens (3.7 TB/s over all), 21 for one; MXFP4 (23 MB) 16 and 12 to 14.
+// What is not streaming is the two kernels' start and end.
+//
 // The operands change places: 128 weight rows are the MMA's M, the tokens
 // (16 .. 128, a multiple of 16) its N, so no tensor-core row is wasted and a
 // CTA's shared memory holds almost nothing but weights in flight.  One CTA
