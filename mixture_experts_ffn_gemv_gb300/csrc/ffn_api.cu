@@ -14,7 +14,7 @@
 using namespace moe;
 
 struct moe_ffn {
-    moe_ffn_config cfg;
+    moe_ffn_config cfg;  // first: the sizes below need nothing else of a handle
     moe_ffn_weights w;
     int device;
     mutable int last_launches;
@@ -64,7 +64,9 @@ Layout layout(const moe_ffn* f, int64_t m, bool backward) {
             o.dg = take((size_t)m * I * 2);
             o.du = take((size_t)m * I * 2);
         } else {
-            o.h = take((size_t)(m <= kNarrowParts ? 2 * kNarrowParts : m) * I * 2);
+            // up to kNarrowParts tokens take 2 kNarrowParts rows; at least as many for more
+            // tokens, so that what holds m tokens holds fewer
+            o.h = take((size_t)std::max<int64_t>(m, 2 * kNarrowParts) * I * 2);
         }
     }
     o.total = off;

@@ -58,6 +58,22 @@ def test_null_arguments(B):
     assert lib.moe_ffn_destroy(None) == 0
 
 
+@pytest.mark.parametrize("weights", [0, 3])
+def test_workspace_sizes_never_fall(B, weights):
+    """What holds m tokens holds fewer.  The sizes are computed from the config alone, with which a
+    handle begins; there is no handle without a device."""
+    lib, n = B.load_library(), ctypes.c_size_t()
+    handle = ctypes.create_string_buffer(1 << 14)
+    cfg = B.MoeFfnConfig(2048, 768, 0, weights)
+    ctypes.memmove(handle, ctypes.byref(cfg), ctypes.sizeof(cfg))
+    for backward in (0, 1) if weights == 0 else (0,):
+        last = 0
+        for m in range(600):
+            assert lib.moe_ffn_workspace_size(handle, m, backward, ctypes.byref(n)) == 0
+            assert n.value >= last, (m, n.value, last)
+            last = n.value
+
+
 def test_mxfp4_refusals(B):
     lib = B.load_library()
     n = ctypes.c_size_t()

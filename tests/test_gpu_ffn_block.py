@@ -528,3 +528,16 @@ def test_example_trains_and_serves():
     assert last < 0.7 * first
     # two quantised operands per product: e2m1 steps of 1/4 to 1/2 of a value give about 0.1 each, in three products
     assert prompt < 0.35 and token < 0.5
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_fewer_tokens_on_one_handle(B, mx):
+    """A handle whose largest call had 9 to 15 tokens takes a call of 1 to 8 after it."""
+    H, I = 256, 768
+    w = _weights(13, H, I)
+    w = _quantised(B, w)[0] if mx else w
+    x = _n(14, 15, H)
+    for first in (9, 12, 15):
+        blk = B.GatedFfn(*w)
+        for m in (first, 8, 1):
+            assert torch.equal(blk.forward(x[:m]), B.GatedFfn(*w).forward(x[:m]))
