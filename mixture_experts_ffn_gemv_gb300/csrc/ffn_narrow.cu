@@ -92,6 +92,12 @@ __device__ __forceinline__ void add4(float (&a)[4], const float4& v) {
     a[3] += v.w;
 }
 
+// h's second part where hi is the first: 0 where that is infinite (or a NaN),
+// since an infinity less itself would make the sum of both a NaN.
+__device__ __forceinline__ float second_part(float h, float hi) {
+    return fabsf(hi) < __int_as_float(0x7f800000) ? h - hi : 0.f;
+}
+
 template <int FMT, int KIND>
 __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__ NarrowProduct p) {
     constexpr bool MX = FMT != FMT_BF16, QUANT = FMT == FMT_MXFP4_QUANT;
@@ -420,8 +426,8 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             *reinterpret_cast<uint2*>(p.out + at) = hi;
             if (GATEUP && PARTS)  // what rounding left of h, 8 rows further on
                 *reinterpret_cast<uint2*>(p.out + at + 8 * (size_t)p.R) =
-                    make_uint2(pack_bf16x2(o[0] - bf16lo(hi.x), o[1] - bf16hi(hi.x)),
-                               pack_bf16x2(o[2] - bf16lo(hi.y), o[3] - bf16hi(hi.y)));
+                    make_uint2(pack_bf16x2(second_part(o[0], bf16lo(hi.x)), second_part(o[1], bf16hi(hi.x))),
+                               pack_bf16x2(second_part(o[2], bf16lo(hi.y)), second_part(o[3], bf16hi(hi.y))));
         }
     }
     cluster_sync();  // no CTA leaves while another reads its sums

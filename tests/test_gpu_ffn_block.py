@@ -541,3 +541,21 @@ def test_fewer_tokens_on_one_handle(B, mx):
         blk = B.GatedFfn(*w)
         for m in (first, 8, 1):
             assert torch.equal(blk.forward(x[:m]), B.GatedFfn(*w).forward(x[:m]))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_h_past_bf16_is_infinite_at_every_number_of_tokens(B, kind):
+    """h that overflows fp32, and h that fp32 holds but bf16 does not, give infinities of W2's sign
+    where h goes on in two bf16 parts (4 and 8 tokens) as where it does in one (9 and 12)."""
+    eye = torch.eye(8, device="cuda")
+    sign = torch.tensor([1.0, -1.0] * 4, device="cuda")
+    blk = B.GatedFfn(eye.bfloat16(), 2 * eye.bfloat16(), sign[:, None].expand(8, 8).bfloat16().contiguous(), act=kind)
+    x = torch.ones(12, 8, device="cuda")
+    x[1, 3] = 2.0 ** 64                # h = 2^129
+    x[2, 5] = 181 / 128 * 2.0 ** 63    # h = 1.9996 2^127: a step below 2^128 in fp32, 2^128 in bf16
+    x = x.bfloat16()
+    for m in (4, 8, 9, 12):
+        out = blk.forward(x[:m]).float()
+        assert torch.equal(out[1], sign * float("inf")) and torch.equal(out[2], sign * float("inf"))
+        assert torch.isfinite(out[0]).all() and torch.isfinite(out[3:]).all()
+    assert blk.device_status() == 0
