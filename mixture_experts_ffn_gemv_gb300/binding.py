@@ -184,6 +184,15 @@ def moe_act_quant_nvfp4(x, stream=None):
     return codes, sb, g
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
+def _hold(held: list, ws):
+    """While a CUDA graph is captured: keeps ws, into which the graph will replay, alive in `held`."""
+    if _capturing() and not any(t is ws for t in held):
+        held.append(ws)
+
+
 class MoeLayer:
     """A layer handle over caller-owned device weights (see include/moe_ffn.h).
 
@@ -222,7 +231,11 @@ class MoeLayer:
                                          ctypes.byref(shared) if shared is not None else None,
                                          ctypes.byref(handle)), "moe_layer_create")
         self.handle = handle
+        self._new_workspaces()
+
+    def _new_workspaces(self):
         self._ws = None
+        self._held = []  # the workspaces that captured graphs use
 
     def close(self):
         if getattr(self, "handle", None):
@@ -242,10 +255,13 @@ class MoeLayer:
         return n.value
 
     def workspace(self, m: int, device=None) -> torch.Tensor:
+        """The handle's own workspace, grown to what a call on m tokens needs.  Those that captured
+        graphs use live as long as the handle."""
         need = self.workspace_size(m)
         if self._ws is None or self._ws.numel() < need:
             dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
             self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _hold(self._held, self._ws)
         return self._ws
 
     def select_arm(self, m: int) -> int:
@@ -485,19 +501,22 @@ _spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on 
 
 def _space(like, stream: int, need: int) -> torch.Tensor:
     """A workspace of at least `need` bytes for calls on `stream`, the current one, its header
-    zeroed before first use.  One made while a graph is captured belongs to that graph alone."""
+    zeroed before first use.  A call that is captured into a graph gets one from the graph's own
+    pool: the graph may be replayed beside eager calls, and after they have needed a larger one."""
+    capturing = _capturing()
     key = (like.get_device(), stream)
-    ws = _spaces.get(key)
+    ws = None if capturing else _spaces.get(key)
     if ws is None or ws.numel() < need:
         ws = _empty((max(need, 1 << 16),), dtype=_U8, device=like.device)
         ws[:256].zero_()
-        if not torch.cuda.is_current_stream_capturing():
+        if not capturing:
             _spaces[key] = ws
     return ws
 
 
 def mxfp4_device_status(stream=None) -> int:
-    """The first device error (0: none) of the MXFP4 products on `stream` since it was last read."""
+    """The first device error (0: none) of the MXFP4 products on `stream` since it was last read
+    (of eager calls: a captured one keeps its error word inside its graph)."""
     s = stream if stream is not None else torch.cuda.current_stream()
     ws = _spaces.get((s.device.index, s.cuda_stream))
     if ws is None:
@@ -562,7 +581,9 @@ class GatedFfn:
 
     Weights are bf16 tensors, or (codes, packed scales) pairs as
     moe_mxfp4_quant returns them; act is "silu" or "gelu" (tanh form).
-    A handle keeps one workspace: order its calls on one stream."""
+    A handle keeps one workspace: order its calls, replays of graphs that
+    captured them among these, as on one stream.  Such graphs need the handle
+    alive."""
 
     def __init__(self, w1, w3, w2, act="silu"):
         self.lib = load_library()
@@ -585,10 +606,14 @@ class GatedFfn:
         handle = _vp()
         _check(self.lib.moe_ffn_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(handle)), "moe_ffn_create")
         self.handle = handle
+        self._saved = {}  # words saved, by tokens
+        self._new_workspaces()
+
+    def _new_workspaces(self):
         self._ws = None
         self._ws_at = (None, 0)
         self._fits = [-1, -1]  # tokens the workspace holds: forward, backward
-        self._saved = {}       # words saved, by tokens
+        self._held = []        # the workspaces that captured graphs use
 
     def close(self):
         if getattr(self, "handle", None):
@@ -608,13 +633,15 @@ class GatedFfn:
         return n.value
 
     def workspace(self, m: int, backward: bool, device) -> torch.Tensor:
-        """The handle's own workspace, grown to what a call on m tokens needs."""
+        """The handle's own workspace, grown to what a call on m tokens needs.  Those that captured
+        graphs use live as long as the handle."""
         if m > self._fits[backward]:
             need = self.workspace_size(m, backward)
             if self._ws is None or self._ws.numel() < need:
                 self._ws = torch.empty(max(need, 256), dtype=_U8, device=device)
                 self._ws_at = (self._ws.data_ptr(), self._ws.numel())
             self._fits[backward] = m
+        _hold(self._held, self._ws)
         return self._ws
 
     def set_wait_limit(self, ns: int):
@@ -658,7 +685,7 @@ class GatedFfn:
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
-        if m > self._fits[0]:
+        if m > self._fits[0] or _capturing():
             self.workspace(m, False, x.device)
         saved = _empty(self.saved_size(m), dtype=_F32, device=x.device) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
@@ -685,7 +712,7 @@ class GatedFfn:
             dw1 = new((I, H), dtype=_BF16, device=dev)
             dw3 = new((I, H), dtype=_BF16, device=dev)
             dw2 = new((H, I), dtype=_BF16, device=dev)
-        if m > self._fits[1]:
+        if m > self._fits[1] or _capturing():
             self.workspace(m, True, x.device)
         rc = self.lib.moe_ffn_backward(
             self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m,

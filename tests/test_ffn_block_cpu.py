@@ -1,6 +1,8 @@
 """The gated feed-forward block and MXFP4 entry points without a GPU: refusals, sizes, the scale
 order, and the formulas the GPU tests compare against."""
 import ctypes
+import types
+import weakref
 
 import pytest
 import torch
@@ -168,3 +170,57 @@ def test_backward_formula_against_differences(kind):
     g = torch.linspace(-12, 12, 200001, dtype=torch.float64)
     _, s = P.act_slope(g, kind)
     assert s.abs().max() < P.SLOPE and (s.diff() / g.diff()).abs().max() < P.CURVE
+
+
+# ---------------------------------------------------------------- workspaces (host memory stands in for the device's)
+
+def _handle(B, cls):
+    """A handle of cls without a device: 256 bytes of workspace a token."""
+    h = object.__new__(cls)
+    h.handle = None
+    h.workspace_size = lambda m, backward=False: 256 * m
+    h._new_workspaces()
+    if cls is B.MoeLayer:
+        return h, lambda m: h.workspace(m, device="cpu")
+    return h, lambda m: h.workspace(m, False, "cpu")
+
+
+@pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
+def test_a_captured_workspace_outlives_its_successor(B, monkeypatch, cls):
+    """A CUDA graph replays into the workspace that its capture saw, also after a larger call."""
+    capturing = False
+    monkeypatch.setattr(B, "_capturing", lambda: capturing)
+    h, space = _handle(B, getattr(B, cls))
+    first = weakref.ref(space(4))
+    space(8)
+    assert first() is None  # no graph knows it
+    capturing = True
+    used = weakref.ref(space(6))
+    assert used() is space(8)
+    capturing = False
+    assert space(100).numel() >= 25600 and used() is not None
+    at = used().data_ptr()
+    assert space(200).data_ptr() != at and used() is not None
+    if cls == "GatedFfn":
+        assert h._ws_at == (space(200).data_ptr(), space(200).numel())
+    capturing = True  # one that grows during a capture is kept too
+    used = weakref.ref(space(400))
+    capturing = False
+    space(800)
+    assert used() is not None
+
+
+def test_captured_products_share_no_workspace(B, monkeypatch):
+    """The products' hidden workspaces: a capture neither takes the one that eager calls on its
+    stream share nor leaves its own to them."""
+    capturing = False
+    monkeypatch.setattr(B, "_capturing", lambda: capturing)
+    monkeypatch.setattr(B, "_spaces", {})
+    like = types.SimpleNamespace(get_device=lambda: 0, device="cpu")
+    eager = B._space(like, 7, 1000)
+    assert B._space(like, 7, 1000) is eager
+    capturing = True
+    a, b = B._space(like, 7, 1000), B._space(like, 7, 1000)
+    assert len({t.data_ptr() for t in (eager, a, b)}) == 3 and not a[:256].any() and not b[:256].any()
+    capturing = False
+    assert B._space(like, 7, 1000) is eager

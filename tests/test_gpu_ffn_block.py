@@ -559,3 +559,71 @@ def test_h_past_bf16_is_infinite_at_every_number_of_tokens(B, kind):
         assert torch.equal(out[1], sign * float("inf")) and torch.equal(out[2], sign * float("inf"))
         assert torch.isfinite(out[0]).all() and torch.isfinite(out[3:]).all()
     assert blk.device_status() == 0
+
+
+def _others(like, count=8):
+    """Tensors that take up memory freed just now, filled with a pattern."""
+    return [torch.full_like(like, 0x5A) for _ in range(count)]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_a_graph_survives_a_larger_call(B, mx):
+    """Warm-up and capture of a small call, a large eager call, then replays: right outputs, and
+    nothing written into memory that others have got since."""
+    H, I, m = 512, 768, 40
+    w = _weights(51, H, I)
+    blk = B.GatedFfn(*(_quantised(B, w)[0] if mx else w))
+    x, dout = _n(52, m, H), _n(53, m, H)
+
+    def call():
+        if mx:
+            return (blk.forward(x),)
+        out, saved = blk.forward(x, save=True)
+        return (out, *blk.backward(dout, x, saved), blk.forward(x[:5]))
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = call()
+    small = blk.workspace(m, not mx, x.device)
+    blk.forward(_n(54, 3000, H))
+    if not mx:
+        blk.backward(_n(54, 3000, H), _n(55, 3000, H), blk.forward(_n(55, 3000, H), save=True)[1])
+    assert blk.workspace(m, not mx, x.device).numel() > small.numel()
+    shape = torch.empty_like(small)
+    del small
+    others = [shape, *_others(shape)]
+    shape.fill_(0x5A)
+    for seed in (61, 62):
+        x.copy_(_n(seed, m, H))
+        dout.copy_(_n(seed + 10, m, H))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, call()))
+        assert all((t == 0x5A).all() for t in others)
+    assert blk.device_status() == 0
+
+
+def test_a_graph_of_products_survives_a_larger_call(B):
+    """The same of moe_mxfp4_linear, warmed up on the stream that is then captured."""
+    (w,), _ = _quantised(B, [_n(4, 264, 2048)])
+    x = _n(6, 200, 2048)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        B.moe_mxfp4_linear(x, *w)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        got = B.moe_mxfp4_linear(x, *w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        B.moe_mxfp4_linear(_n(8, 5000, 2048), *w)
+        others = _others(torch.empty(1024 + 200 * 1024 + 2 * 16 * 512, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    x.copy_(_n(7, 200, 2048))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, B.moe_mxfp4_linear(x, *w))
+    assert all((t == 0x5A).all() for t in others)
+    assert B.mxfp4_device_status() == 0 and B.mxfp4_device_status(st) == 0

@@ -705,3 +705,24 @@ def test_deterministic_and_graph_capturable(cuda, wl_name, m):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, a)
+
+
+def test_a_graph_survives_a_larger_call(cuda):
+    """A captured small call replays into the workspace that it was captured with, after an eager
+    call that needed a larger one."""
+    wl = I.WORKLOADS["tiny"]
+    tensors, layer = layer_for(wl, cuda)
+    x = I.make_x(wl.shape, 16, device=cuda)
+    want = layer.moe_forward(x, tensors["router_w"], tensors["router_bias"])
+    small = layer.workspace(16).numel()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer.moe_forward(x, tensors["router_w"], tensors["router_bias"])
+    layer.moe_forward(I.make_x(wl.shape, 2000, device=cuda), tensors["router_w"], tensors["router_bias"])
+    assert layer.workspace(16).numel() > small
+    others = [torch.full((small,), 0x5A, dtype=torch.uint8, device=cuda) for _ in range(8)]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and all((t == 0x5A).all() for t in others)
+    assert layer.device_status() == 0
