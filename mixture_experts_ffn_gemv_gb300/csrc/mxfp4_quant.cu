@@ -106,8 +106,10 @@ __global__ void __launch_bounds__(256) mx_quant(const T* x, size_t ldx, uint32_t
     }
 }
 
-// Sixteen codes a thread (8 bytes in, 32 out), U in flight.  Bound by HBM:
-// 14336 x 7168 in 40.0 us, 6.5 TB/s.
+// Sixteen codes a thread (8 bytes in, 32 out), U in flight, the 32 as one store
+// where out is so aligned (WIDE), else as two.  Bound by HBM: 14336 x 7168 in
+// 40.0 us, 6.5 TB/s.
+template <bool WIDE>
 __global__ void __launch_bounds__(256) mx_dequant(const uint8_t* codes, const uint8_t* scales, uint32_t total,
                                                   uint32_t per, int nkt, uint16_t* out) {
     constexpr int U = 4;
@@ -151,7 +153,13 @@ __global__ void __launch_bounds__(256) mx_dequant(const uint8_t* codes, const ui
                     o[4 * h + j] = pack_bf16x2(lo * f, hi * f);
                 }
             }
-            st_global_v8(out + (size_t)i * 16, o);
+            if (WIDE) {
+                st_global_v8(out + (size_t)i * 16, o);
+            } else {
+                uint4* q = reinterpret_cast<uint4*>(out + (size_t)i * 16);
+                q[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                q[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
         }
     }
 }
@@ -184,7 +192,8 @@ cudaError_t launch_mx_quant(const void* x, bool f32, size_t ldx, int rows, int n
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int rows, int n, uint16_t* out,
                               cudaStream_t st) {
     const uint32_t per = (uint32_t)(n / 16), total = (uint32_t)rows * per;
-    return launch_pdl(mx_dequant, dim3(grid_for(((size_t)total + 255) / 256, 64)), dim3(256), 0, st, codes, scales, total,
+    const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+    return launch_pdl(wide ? mx_dequant<true> : mx_dequant<false>, dim3(grid_for(((size_t)total + 255) / 256, 64)), dim3(256), 0, st, codes, scales, total,
                       per, ceil_div(n, 128), out);
 }
 

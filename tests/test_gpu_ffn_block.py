@@ -627,3 +627,32 @@ def test_a_graph_of_products_survives_a_larger_call(B):
     assert torch.equal(got, B.moe_mxfp4_linear(x, *w))
     assert all((t == 0x5A).all() for t in others)
     assert B.mxfp4_device_status() == 0 and B.mxfp4_device_status(st) == 0
+
+
+@pytest.mark.parametrize("rows,n", [(1, 32), (5, 96), (300, 544)])
+def test_buffers_aligned_to_16_bytes_alone(B, rows, n):
+    """What the C entry points ask of their buffers is enough: all of them 16 bytes past a multiple
+    of 32, with nothing written around the outputs."""
+    def at16(nbytes):
+        t = torch.full((nbytes + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+        assert t.data_ptr() % 32 == 0
+        return t, t[16:16 + nbytes], t.data_ptr() + 16
+    lib = B.load_library()
+    for dtype, fn in ((torch.bfloat16, lib.moe_mxfp4_quant), (torch.float32, lib.moe_mxfp4_quant_f32)):
+        x = _n(rows, rows, n, dtype=dtype)
+        size = rows * n * x.element_size()
+        _, xm, xp = at16(size)
+        xm.copy_(x.reshape(-1).view(torch.uint8))
+        want_c, want_s = B.moe_mxfp4_quant(x)
+        codes, cm, cp = at16(want_c.numel())
+        scales, sm, sp = at16(want_s.numel())
+        out, om, op = at16(rows * n * 2)
+        assert fn(xp, n, rows, n, cp, sp, None) == 0
+        assert lib.moe_mxfp4_dequant(cp, sp, rows, n, op, None) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(cm, want_c.reshape(-1))
+        sm = sm.reshape(want_s.shape)
+        assert torch.equal(B.mxfp4_unpack_scales(sm, rows, n), B.mxfp4_unpack_scales(want_s, rows, n))
+        assert torch.equal(om.view(torch.bfloat16).reshape(rows, n), B.moe_mxfp4_dequant(want_c, want_s))
+        for t, k in ((codes, cm.numel()), (scales, sm.numel()), (out, om.numel())):
+            assert (t[:16] == 0x5A).all() and (t[16 + k:] == 0x5A).all()
