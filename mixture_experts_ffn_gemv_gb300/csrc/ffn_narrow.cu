@@ -24,7 +24,8 @@
 //              per lane: eight lanes hold one block of an MXFP4 h.
 // Up to 8 tokens' h goes from gate/up to down in two bf16 parts (h and what its
 // rounding left, 16 bits together): 8 + 8 rows of the smallest token tile, so
-// the second part costs four MMAs of 16 columns per K block and no bandwidth.
+// the second part costs four MMAs of 16 columns per K block and no bandwidth
+// (they read past the tile: ring_margin).
 // A stage holds two weight tiles of 128 bytes of K: W1 and W3 (which share the
 // tokens); two neighbours along K; or a tile of each source, with its tokens,
 // of dx = dg W1 + du W3.  The backward products read the weights as they lie,
@@ -75,6 +76,17 @@ __host__ __device__ inline StageShape stage_shape(bool mx, int kind, int nt) {
 }
 __host__ __device__ inline int stage_stride(const StageShape& s) { return (s.bytes + 1023) & ~1023; }
 
+// The MMA of a second part starts kNarrowParts rows into a token tile and takes
+// the smallest N, 16 columns: its last kNarrowParts rows lie past the tile.
+// What they hold does not matter (they make columns of D that are never read),
+// but they are read, so that this much shared memory has to follow the ring.
+constexpr int PARTS_N = 16, ROW_BYTES = 128;
+constexpr int PARTS_MARGIN = kNarrowParts * ROW_BYTES;
+__host__ __device__ constexpr int ring_margin(int kind) { return kind == NARROW_PLAIN_PARTS ? PARTS_MARGIN : 0; }
+static_assert((kNarrowParts + PARTS_N) * ROW_BYTES == PARTS_N * ROW_BYTES + PARTS_MARGIN,
+              "a second part's MMA ends within the token tile and the margin behind it");
+static_assert(2 * kNarrowParts <= PARTS_N, "both parts' rows fit a token tile");
+
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -110,7 +122,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
     const uint32_t sbase = smem_u32(smem);
     const StageShape ss = stage_shape(MX, KIND, p.nt);
     const int stride = stage_stride(ss);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.ring_bytes + ring_margin(KIND));
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
     const uint32_t never = smem_u32(bars + 2 * MAX_STAGES + 1);  // stall test: no thread ever arrives here
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MAX_STAGES + 2);
@@ -253,9 +265,9 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
                                      sf + 8 * h + 4 * (kk >> 1), sf + 16 + (GATEUP ? 0 : 8 * h) + 4 * (kk >> 1), acc);
                         else
                             mma_bf16(d, ad + (MN ? 128 : 2) * kk, bd + 2 * kk, idesc, acc);
-                        // tokens in two parts: the second one's rows, 8 further on, onto the same columns
+                        // tokens in two parts: the second one's rows, further on, onto the same columns
                         if (PARTS && !GATEUP)
-                            mma_bf16(d, ad + 2 * kk, bd + 64 + 2 * kk, idesc, 1u);
+                            mma_bf16(d, ad + 2 * kk, bd + kNarrowParts * ROW_BYTES / 16 + 2 * kk, idesc, 1u);
                     }
                 }
                 mma_commit(empty0 + 8 * s);
@@ -424,8 +436,8 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             }
             const uint2 hi = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
             *reinterpret_cast<uint2*>(p.out + at) = hi;
-            if (GATEUP && PARTS)  // what rounding left of h, 8 rows further on
-                *reinterpret_cast<uint2*>(p.out + at + 8 * (size_t)p.R) =
+            if (GATEUP && PARTS)  // what rounding left of h, kNarrowParts rows further on
+                *reinterpret_cast<uint2*>(p.out + at + kNarrowParts * (size_t)p.R) =
                     make_uint2(pack_bf16x2(second_part(o[0], bf16lo(hi.x)), second_part(o[1], bf16hi(hi.x))),
                                pack_bf16x2(second_part(o[2], bf16lo(hi.y)), second_part(o[3], bf16hi(hi.y))));
         }
@@ -519,7 +531,7 @@ cudaError_t launch_ffn_narrow(NarrowProduct& p, bool mx, int kind, cudaStream_t 
     if (mx) p.stages = std::min(p.stages, 4);  // 32 scale columns each
     const int acc = (gateup ? 2 : 1) * p.nt;
     p.ring_bytes = (std::max(p.stages * stride, acc * 512) + 1023) & ~1023;
-    const int smem = 1024 + p.ring_bytes + 256;
+    const int smem = 1024 + p.ring_bytes + ring_margin(kind) + 256;
     int cols = 32;
     while (cols < acc + (mx ? 32 * p.stages : 0)) cols *= 2;
     p.tmem_cols = cols;
