@@ -29,7 +29,8 @@
  *     calls: counters that every call leaves at zero, and the device error
  *     word read (and cleared) by moe_device_status.  A layer zeroes the
  *     header itself when a call passes a workspace other than the one its
- *     previous call used; a caller that writes into those 256 bytes between
+ *     previous call used (a captured call counts only as part of its graph);
+ *     a caller that writes into those 256 bytes between
  *     two calls of one layer on the same workspace must zero them itself
  *     (cudaMemsetAsync on the call's stream).  Calls that share a workspace
  *     must be ordered on one stream.

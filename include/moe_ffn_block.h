@@ -70,7 +70,7 @@ MOE_API int moe_ffn_destroy(moe_ffn* ffn);
 /* Workspace bytes a forward (backward = 0) or backward (1) call on m tokens
  * needs, never fewer for more tokens; 256-byte aligned.  Its first 256 bytes are the header of moe_ffn.h,
  * read and cleared by moe_device_status; a handle zeroes it when a call
- * passes a workspace other than its previous call's. */
+ * passes a workspace other than its previous call's, as in moe_ffn.h. */
 MOE_API int moe_ffn_workspace_size(const moe_ffn* ffn, int64_t m, int backward, size_t* bytes);
 
 /* Bytes that a forward pass on m tokens saves for the backward pass. */

@@ -287,10 +287,7 @@ PermuteOut permute_out(const Layout& lo, void* ws, int32_t* sorted_pair, int32_t
 // call used therefore needs no zeroing; any other gets its header zeroed
 // first (one memset, which would otherwise open every call's launch chain).
 int prepare_header(const moe_layer* L, void* ws, cudaStream_t st) {
-    if (L->last_ws == ws) return MOE_OK;
-    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return MOE_ERR_CUDA;
-    L->last_ws = ws;
-    return MOE_OK;
+    return clear_header(L->last_ws, ws, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 GemvArgs gemv_args(const moe_layer* L, const Layout& lo, void* ws) {

@@ -19,6 +19,18 @@ struct WsHeader {
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
+// Zeroes the header of `ws` on `st` unless `last`, the workspace of the handle's
+// last call, is this one: its header is then known to be clean.  A memset that is
+// being captured runs when the graph does, so that nothing is known after it.
+inline cudaError_t clear_header(const void*& last, void* ws, cudaStream_t st) {
+    if (last == ws) return cudaSuccess;
+    cudaStreamCaptureStatus capture;
+    cudaError_t e = cudaStreamIsCapturing(st, &capture);
+    if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, sizeof(WsHeader), st);
+    if (e == cudaSuccess && capture == cudaStreamCaptureStatusNone) last = ws;
+    return e;
+}
+
 // device error codes (the header's err word)
 enum : int {
     DEV_ERR_NONE = 0,

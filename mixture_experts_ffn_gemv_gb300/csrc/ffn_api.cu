@@ -89,13 +89,6 @@ int check_call(const moe_ffn* f, int64_t m, bool backward, void* ws, size_t ws_b
 
 bool bad_rows(const void* p, int64_t ld, int64_t n) { return !p || !aligned(p, 16) || ld < n || ld % 8 || ld > (int64_t)1 << 38; }
 
-int prepare_header(const moe_ffn* f, void* ws, cudaStream_t st) {
-    if (f->last_ws == ws) return MOE_OK;
-    if (cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) != cudaSuccess) return MOE_ERR_CUDA;
-    f->last_ws = ws;
-    return MOE_OK;
-}
-
 FfnProducts products(const moe_ffn* f, void* ws) {
     FfnProducts p{};
     p.act = f->cfg.activation;
@@ -415,7 +408,7 @@ int moe_ffn_forward(const moe_ffn* f, const void* x, int64_t ldx, int64_t m, voi
     const bool mx = f->cfg.weights == MOE_WEIGHTS_MXFP4;
     if (mx && (saved || too_large(m, f->cfg.hidden))) return MOE_ERR_UNSUPPORTED;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
+    if (clear_header(f->last_ws, workspace, st) != cudaSuccess) return MOE_ERR_CUDA;
     float* sa = static_cast<float*>(saved);
     void* h = saved ? sa + 2 * saved_floats(m, f->cfg.inter) : at<void>(workspace, lo.h);
     return mx ? forward_mxfp4(f, lo, x, ldx, (int)m, out, workspace, st)
@@ -436,7 +429,7 @@ int moe_ffn_backward(const moe_ffn* f, const void* dout, int64_t ldd, const void
         return MOE_ERR_INVALID_ARG;
     if (!dx && !dw) return MOE_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (prepare_header(f, workspace, st) != MOE_OK) return MOE_ERR_CUDA;
+    if (clear_header(f->last_ws, workspace, st) != cudaSuccess) return MOE_ERR_CUDA;
     void *dg = at<void>(workspace, lo.dg), *du = at<void>(workspace, lo.du);
     float* sa = static_cast<float*>(const_cast<void*>(saved));  // only read
     float *sd = sa + saved_floats(m, I), *h = sd + saved_floats(m, I);

@@ -1,5 +1,7 @@
 """The gated feed-forward block, its backward pass, and the MXFP4 operators on the GPU, against
 64-bit formulas with bounds derived from the roundings (tests/_ffn_plain.py)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -656,3 +658,30 @@ def test_buffers_aligned_to_16_bytes_alone(B, rows, n):
         assert torch.equal(om.view(torch.bfloat16).reshape(rows, n), B.moe_mxfp4_dequant(want_c, want_s))
         for t, k in ((codes, cm.numel()), (scales, sm.numel()), (out, om.numel())):
             assert (t[:16] == 0x5A).all() and (t[16 + k:] == 0x5A).all()
+
+
+def test_a_captured_header_is_not_taken_for_clean(B):
+    """A workspace first seen by a captured call: its header is zeroed in the graph, and again for an
+    eager call that comes before any replay."""
+    H, I, m = 64, 96, 20
+    blk = B.GatedFfn(*_weights(1, H, I))
+    x = _n(2, m, H)
+    want = blk.forward(x)
+    lib, p = B.load_library(), B._p
+    ws = torch.full((blk.workspace_size(m),), 0x5A, dtype=torch.uint8, device="cuda")
+    out, code = torch.zeros_like(x), ctypes.c_int32()
+
+    def call(stream):
+        assert lib.moe_ffn_forward(blk.handle, p(x), H, m, p(out), None, p(ws), ws.numel(), B._stream(stream)) == 0
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(None)
+    assert (ws == 0x5A).all()
+    call(None)
+    assert lib.moe_device_status(p(ws), B._stream(), ctypes.byref(code)) == 0 and code.value == 0
+    assert torch.equal(out, want)
+    ws.fill_(0x5A)
+    out.zero_()
+    g.replay()
+    assert lib.moe_device_status(p(ws), B._stream(), ctypes.byref(code)) == 0 and torch.equal(out, want)

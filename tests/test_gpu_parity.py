@@ -726,3 +726,23 @@ def test_a_graph_survives_a_larger_call(cuda):
     torch.cuda.synchronize()
     assert torch.equal(out, want) and all((t == 0x5A).all() for t in others)
     assert layer.device_status() == 0
+
+
+def test_a_captured_header_is_not_taken_for_clean(cuda):
+    """A layer whose workspace is made during a capture: its counters are zeroed in the graph, and
+    again for the eager call that comes before any replay."""
+    wl = I.WORKLOADS["tiny"]
+    tensors, layer = layer_for(wl, cuda)
+    x = I.make_x(wl.shape, 16, device=cuda)
+    want = layer.moe_forward(x, tensors["router_w"], tensors["router_bias"])
+    layer._ws = None
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        out = layer.moe_forward(x, tensors["router_w"], tensors["router_bias"])
+    layer._ws.fill_(0x5A)
+    assert torch.equal(layer.moe_forward(x, tensors["router_w"], tensors["router_bias"]), want)
+    assert layer.device_status() == 0
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and layer.device_status() == 0
