@@ -187,10 +187,41 @@ def moe_act_quant_nvfp4(x, stream=None):
 _capturing = torch.cuda.is_current_stream_capturing
 
 
-def _hold(held: list, ws):
-    """While a CUDA graph is captured: keeps ws, into which the graph will replay, alive in `held`."""
-    if _capturing() and not any(t is ws for t in held):
-        held.append(ws)
+class _Workspaces:
+    """What a handle keeps of its workspaces besides the current one: those that captured graphs
+    replay into, and the error words of those it has outgrown."""
+
+    def __init__(self):
+        self.held = []     # used by captured graphs
+        self.headers = []  # of outgrown ones that no graph uses
+
+    def grown(self, old, need: int, device):
+        """A workspace of `need` bytes in place of `old`, its header zeroed."""
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+        if old is not None and not any(t is old for t in self.held):
+            # a copy made during a capture would not be made until the graph runs
+            self.headers.append(old if _capturing() else old[:256].clone())
+        return ws
+
+    def use(self, ws):
+        """A call on ws follows.  One that is captured makes its graph replay into ws."""
+        if _capturing() and not any(t is ws for t in self.held):
+            self.held.append(ws)
+
+    def status(self, ws, stream) -> int:
+        """The first device error (0: none) in the words of ws and of those before it; a word that
+        is set is cleared."""
+        code, first = _i32(), 0
+        for t in (*self.headers, *(t for t in self.held if t is not ws), ws):
+            if t is None:
+                continue
+            rc = load_library().moe_device_status(_p(t), _stream(stream), ctypes.byref(code))
+            if rc not in (MOE_OK, MOE_ERR_DEVICE):
+                raise MoeError(rc, "moe_device_status")
+            first = first or code.value
+        self.headers.clear()
+        return first
 
 
 class MoeLayer:
@@ -235,7 +266,7 @@ class MoeLayer:
 
     def _new_workspaces(self):
         self._ws = None
-        self._held = []  # the workspaces that captured graphs use
+        self._past = _Workspaces()
 
     def close(self):
         if getattr(self, "handle", None):
@@ -260,8 +291,8 @@ class MoeLayer:
         need = self.workspace_size(m)
         if self._ws is None or self._ws.numel() < need:
             dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        _hold(self._held, self._ws)
+            self._ws = self._past.grown(self._ws, need, dev)
+        self._past.use(self._ws)
         return self._ws
 
     def select_arm(self, m: int) -> int:
@@ -308,14 +339,9 @@ class MoeLayer:
         return out
 
     def device_status(self, stream=None) -> int:
-        code = _i32()
-        ws = self._ws
-        if ws is None:
-            return 0
-        rc = self.lib.moe_device_status(_p(ws), _stream(stream), ctypes.byref(code))
-        if rc not in (MOE_OK, MOE_ERR_DEVICE):
-            raise MoeError(rc, "moe_device_status")
-        return code.value
+        """The first device error (0: none) of the handle's calls since it was last read; of a workspace
+        that was made during a capture, from the graph's first run on."""
+        return self._past.status(self._ws, stream)
 
     # ---- entry points
     def moe_route(self, x, router_w, router_bias=None, logits=False, stream=None):
@@ -496,36 +522,28 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
     return out
 
 
-_spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on that stream
+_spaces = {}  # (device, stream) -> [workspace of the MXFP4 products launched on that stream, those before it]
 
 
 def _space(like, stream: int, need: int) -> torch.Tensor:
     """A workspace of at least `need` bytes for calls on `stream`, the current one, its header
     zeroed before first use.  A call that is captured into a graph gets one from the graph's own
     pool: the graph may be replayed beside eager calls, and after they have needed a larger one."""
-    capturing = _capturing()
-    key = (like.get_device(), stream)
-    ws = None if capturing else _spaces.get(key)
-    if ws is None or ws.numel() < need:
-        ws = _empty((max(need, 1 << 16),), dtype=_U8, device=like.device)
-        ws[:256].zero_()
-        if not capturing:
-            _spaces[key] = ws
-    return ws
+    need = max(need, 1 << 16)
+    if _capturing():
+        return _Workspaces().grown(None, need, like.device)
+    entry = _spaces.setdefault((like.get_device(), stream), [None, _Workspaces()])
+    if entry[0] is None or entry[0].numel() < need:
+        entry[0] = entry[1].grown(entry[0], need, like.device)
+    return entry[0]
 
 
 def mxfp4_device_status(stream=None) -> int:
     """The first device error (0: none) of the MXFP4 products on `stream` since it was last read
     (of eager calls: a captured one keeps its error word inside its graph)."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    ws = _spaces.get((s.device.index, s.cuda_stream))
-    if ws is None:
-        return 0
-    code = _i32()
-    rc = load_library().moe_device_status(_p(ws), ctypes.c_void_p(s.cuda_stream), ctypes.byref(code))
-    if rc not in (MOE_OK, MOE_ERR_DEVICE):
-        raise MoeError(rc, "moe_device_status")
-    return code.value
+    ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
+    return 0 if ws is None else past.status(ws, s)
 
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
@@ -613,7 +631,7 @@ class GatedFfn:
         self._ws = None
         self._ws_at = (None, 0)
         self._fits = [-1, -1]  # tokens the workspace holds: forward, backward
-        self._held = []        # the workspaces that captured graphs use
+        self._past = _Workspaces()
 
     def close(self):
         if getattr(self, "handle", None):
@@ -638,10 +656,10 @@ class GatedFfn:
         if m > self._fits[backward]:
             need = self.workspace_size(m, backward)
             if self._ws is None or self._ws.numel() < need:
-                self._ws = torch.empty(max(need, 256), dtype=_U8, device=device)
+                self._ws = self._past.grown(self._ws, need, device)
                 self._ws_at = (self._ws.data_ptr(), self._ws.numel())
             self._fits[backward] = m
-        _hold(self._held, self._ws)
+        self._past.use(self._ws)
         return self._ws
 
     def set_wait_limit(self, ns: int):
@@ -656,13 +674,9 @@ class GatedFfn:
         return self.lib.moe_ffn_last_launch_count(self.handle)
 
     def device_status(self, stream=None) -> int:
-        if self._ws is None:
-            return 0
-        code = _i32()
-        rc = self.lib.moe_device_status(_p(self._ws), _stream(stream), ctypes.byref(code))
-        if rc not in (MOE_OK, MOE_ERR_DEVICE):
-            raise MoeError(rc, "moe_device_status")
-        return code.value
+        """The first device error (0: none) of the handle's calls since it was last read; of a workspace
+        that was made during a capture, from the graph's first run on."""
+        return self._past.status(self._ws, stream)
 
     def saved_size(self, m: int) -> int:
         """Words of what a forward pass on m tokens saves (moe_ffn_saved_size, in 4-byte words)."""

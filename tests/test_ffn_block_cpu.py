@@ -224,3 +224,52 @@ def test_captured_products_share_no_workspace(B, monkeypatch):
     assert len({t.data_ptr() for t in (eager, a, b)}) == 3 and not a[:256].any() and not b[:256].any()
     capturing = False
     assert B._space(like, 7, 1000) is eager
+
+
+def _host_status(ws, stream, code):
+    """moe_device_status of a workspace in host memory."""
+    word = ctypes.c_int32.from_address(ws.value)
+    code._obj.value, word.value = word.value, 0
+    return 5 if code._obj.value else 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
+def test_error_words_outlive_their_workspace(B, monkeypatch, cls, captured):
+    """A new workspace reads as clean before its first call, and an error that nobody has read is
+    still there after the workspace has grown."""
+    capturing = False
+    monkeypatch.setattr(B, "_capturing", lambda: capturing)
+    monkeypatch.setattr(B, "load_library", lambda: types.SimpleNamespace(moe_device_status=_host_status))
+    monkeypatch.setattr(B, "_stream", lambda stream=None: None)
+    h, space = _handle(B, getattr(B, cls))
+    assert h.device_status() == 0
+    first = space(4)
+    assert not first[:256].any() and h.device_status() == 0
+    capturing = captured
+    assert space(4) is first
+    capturing = False
+    first[0] = 2
+    space(100)
+    assert h.device_status() == 2 and h.device_status() == 0
+    first[0] = 3  # a graph may set its own again
+    space(200)
+    assert h.device_status() == (3 if captured else 0) and h.device_status() == 0
+    space(300)[0] = 1
+    capturing = captured  # grown during a capture
+    assert space(400)[0] == 0
+    capturing = False
+    assert h.device_status() == 1 and h.device_status() == 0
+
+
+def test_error_words_of_products_outlive_their_workspace(B, monkeypatch):
+    monkeypatch.setattr(B, "_capturing", lambda: False)
+    monkeypatch.setattr(B, "_spaces", {})
+    monkeypatch.setattr(B, "load_library", lambda: types.SimpleNamespace(moe_device_status=_host_status))
+    monkeypatch.setattr(B, "_stream", lambda stream=None: None)
+    like = types.SimpleNamespace(get_device=lambda: 0, device="cpu")
+    stream = types.SimpleNamespace(device=types.SimpleNamespace(index=0), cuda_stream=7)
+    assert B.mxfp4_device_status(stream) == 0
+    B._space(like, 7, 1000)[0] = 2
+    B._space(like, 7, 1 << 20)
+    assert B.mxfp4_device_status(stream) == 2 and B.mxfp4_device_status(stream) == 0

@@ -685,3 +685,18 @@ def test_a_captured_header_is_not_taken_for_clean(B):
     out.zero_()
     g.replay()
     assert lib.moe_device_status(p(ws), B._stream(), ctypes.byref(code)) == 0 and torch.equal(out, want)
+
+
+def test_an_error_is_read_after_the_workspace_has_grown(B):
+    H, I = 256, 512
+    blk = B.GatedFfn(*_weights(2, H, I))
+    x = _n(3, 3, H)
+    blk.workspace(3, False, x.device)
+    assert blk.device_status() == 0  # before any call
+    blk.set_wait_limit(20_000_000)
+    blk.stall_test(True)
+    blk.forward(x)
+    blk.stall_test(False)
+    blk.set_wait_limit(0)
+    blk.forward(_n(4, 2000, H))
+    assert blk.device_status() == 2 and blk.device_status() == 0
