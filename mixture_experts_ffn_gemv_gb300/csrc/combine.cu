@@ -132,8 +132,7 @@ __global__ __launch_bounds__(256) void combine_tail(const YT* __restrict__ y, co
 template <typename YT>
 static cudaError_t launch_tail(const YT* y, const int32_t* slot_of_pair, const float* w, int m, int k, int H, int P,
                                int has_shared, const float* shared_g, const TailArgs& tail, cudaStream_t st) {
-    static cudaError_t attr = cudaFuncSetAttribute(combine_tail<YT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kTailMaxH * 4);
+    const cudaError_t attr = allow_smem<combine_tail<YT>>(kTailMaxH * 4);
     if (attr != cudaSuccess) return attr;
     const int early = one_wave((const void*)combine_tail<YT>, m, 256, (size_t)H * 4);
     launch_pdl(combine_tail<YT>, dim3(m), dim3(256), (size_t)H * 4, st, y, slot_of_pair, w, k, H, P, has_shared,

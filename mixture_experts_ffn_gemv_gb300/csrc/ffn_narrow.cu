@@ -470,7 +470,7 @@ int clusters_resident(int size) {
         cfg.attrs = &at;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaFuncSetAttribute(ffn_narrow<FMT_BF16, NARROW_GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        if (allow_smem<ffn_narrow<FMT_BF16, NARROW_GATEUP>>(227 * 1024) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, ffn_narrow<FMT_BF16, NARROW_GATEUP>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = sms() / size * 3 / 4;
@@ -482,8 +482,7 @@ int clusters_resident(int size) {
 
 template <int FMT, int KIND>
 cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
-    static cudaError_t attr =
-        cudaFuncSetAttribute(ffn_narrow<FMT, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    const cudaError_t attr = allow_smem<ffn_narrow<FMT, KIND>>(227 * 1024);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ceil_div(p.R, 128) * p.slices, ceil_div(p.T, p.nt));

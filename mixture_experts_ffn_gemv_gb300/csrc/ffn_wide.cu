@@ -393,8 +393,7 @@ int sms() {
 
 template <int EPI>
 cudaError_t launch(const FfnProducts& p, cudaStream_t st) {
-    static cudaError_t attr =
-        cudaFuncSetAttribute(ffn_products<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<EPI>::SMEM_BYTES);
+    const cudaError_t attr = allow_smem<ffn_products<EPI>>(Shape<EPI>::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     const int pairs = std::max(1, std::min(sms() / 2, p.first[p.count]));
     cudaLaunchConfig_t cfg = {};

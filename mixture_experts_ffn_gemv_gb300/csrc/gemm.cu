@@ -559,9 +559,7 @@ int num_sms() {
 
 template <bool GATEUP>
 cudaError_t set_smem_attr() {
-    static cudaError_t e = cudaFuncSetAttribute(grouped_gemm_bf16<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                SMEM_BYTES);
-    return e;
+    return allow_smem<grouped_gemm_bf16<GATEUP>>(SMEM_BYTES);
 }
 
 }  // namespace
@@ -661,10 +659,8 @@ bool use_pairs(const GemmCall& g) {
 // down: A = h, B = W2 in 128-row boxes, out = y
 template <bool GATEUP>
 cudaError_t launch_pair(const GemmLaunch& L, cudaStream_t st) {
-    static cudaError_t attr6 = cudaFuncSetAttribute(grouped_gemm_bf16_pair<6, GATEUP>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_MAX);
-    static cudaError_t attr7 = cudaFuncSetAttribute(grouped_gemm_bf16_pair<7, GATEUP>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, P_SMEM_MAX);
+    const cudaError_t attr6 = allow_smem<grouped_gemm_bf16_pair<6, GATEUP>>(P_SMEM_MAX);
+    const cudaError_t attr7 = allow_smem<grouped_gemm_bf16_pair<7, GATEUP>>(P_SMEM_MAX);
     if (attr6 != cudaSuccess) return attr6;
     if (attr7 != cudaSuccess) return attr7;
     const GemmCall& g = L.call;

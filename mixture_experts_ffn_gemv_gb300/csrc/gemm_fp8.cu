@@ -330,9 +330,7 @@ int num_sms() {
 
 template <bool GATEUP>
 cudaError_t set_smem_attr() {
-    static cudaError_t e =
-        cudaFuncSetAttribute(grouped_gemm_fp8<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    return e;
+    return allow_smem<grouped_gemm_fp8<GATEUP>>(SMEM_BYTES);
 }
 
 }  // namespace

@@ -395,9 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 template <bool GATEUP>
 cudaError_t set_smem_attr() {
-    static cudaError_t e = cudaFuncSetAttribute(grouped_gemm_nvfp4<GATEUP>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    return e;
+    return allow_smem<grouped_gemm_nvfp4<GATEUP>>(SMEM_BYTES);
 }
 
 int sms() {

@@ -340,8 +340,7 @@ int sms() {
 
 template <bool GATEUP>
 cudaError_t launch(const MxProduct& p, cudaStream_t st) {
-    static cudaError_t attr =
-        cudaFuncSetAttribute(mx_product<GATEUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<GATEUP>::SMEM_BYTES);
+    const cudaError_t attr = allow_smem<mx_product<GATEUP>>(Shape<GATEUP>::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     const int pairs = std::max(1, std::min(sms() / 2, p.m_tiles * p.n_tiles));
     cudaLaunchConfig_t cfg = {};

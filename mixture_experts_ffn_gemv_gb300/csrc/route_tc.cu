@@ -247,8 +247,7 @@ cudaError_t launch_router_tc(const uint16_t* x, int m, int H, const uint16_t* pl
     uint32_t cols = 32;
     while ((int)cols < N) cols <<= 1;
     const int smem = 1024 + p.stages * p.stage_bytes + 256;
-    static cudaError_t attr = cudaFuncSetAttribute(router_logits_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   R_SMEM_MAX);
+    const cudaError_t attr = allow_smem<router_logits_tc>(R_SMEM_MAX);
     if (attr != cudaSuccess) return attr;
     const dim3 grid(ceil_div(m, RBM), S, ceil_div(Epad, N));
     launch_pdl(router_logits_tc, dim3(grid), dim3(R_THREADS), smem, st, tx, tw, p, cols);
