@@ -452,10 +452,18 @@ def _dense(t, dtype, shape, what: str):
         raise ValueError(f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
 
 
-def _on(t) -> int:
-    """The current CUDA stream of t's device.  A call that is given a stream makes it the current
-    one first, so that what it allocates belongs to the stream that writes it."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+_current_device = torch._C._cuda_getDevice
+
+
+def _on(*tensors) -> int:
+    """The current CUDA stream of the device that every one of `tensors` lies on: the current
+    device, on which the library launches.  A call that is given a stream makes it the current one
+    first, so that what it allocates belongs to the stream that writes it."""
+    dev = _current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"a tensor on {t.device} in a call on cuda:{dev}, the current device")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def mxfp4_scales_shape(rows: int, n: int):
@@ -497,12 +505,13 @@ def moe_mxfp4_quant(x, stream=None):
     _need(x.dim() == 2, "x: [rows, n]")
     rows, n = x.shape
     ld = _rows(x, n, "x", f32=True)
+    st = _on(x)
     dev = x.device
     codes = _empty((rows, n // 2), dtype=_U8, device=dev)
     scales = _empty(mxfp4_scales_shape(rows, n), dtype=_U8, device=dev)
     f32 = x.dtype is _F32
     rc = (lib.moe_mxfp4_quant_f32 if f32 else lib.moe_mxfp4_quant)(
-        x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), _on(x))
+        x.data_ptr(), ld, rows, n, codes.data_ptr(), scales.data_ptr(), st)
     if rc:
         raise MoeError(rc, "moe_mxfp4_quant_f32" if f32 else "moe_mxfp4_quant")
     return codes, scales
@@ -515,8 +524,9 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
             return moe_mxfp4_dequant(codes, scales)
     lib = _lib or load_library()
     rows, n = _mx_matrix(codes, scales, "x")
+    st = _on(codes, scales)
     out = _empty((rows, n), dtype=_BF16, device=codes.device)
-    rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), _on(codes))
+    rc = lib.moe_mxfp4_dequant(codes.data_ptr(), scales.data_ptr(), rows, n, out.data_ptr(), st)
     if rc:
         raise MoeError(rc, "moe_mxfp4_dequant")
     return out
@@ -559,7 +569,7 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
         out = _empty((m, n), dtype=_BF16, device=a_codes.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(a_codes)
+    st = _on(a_codes, a_scales, b_codes, b_scales, out)
     ws = _space(a_codes, st, 256)
     rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n, k,
                             out.data_ptr(), ws.data_ptr(), ws.numel(), st)
@@ -582,7 +592,7 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
         out = _empty((m, n), dtype=_BF16, device=x.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(x)
+    st = _on(x, codes, scales, out)
     # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
     ws = _space(x, st, 1024 + m * k // 2 + (m + 127) // 128 * ((k + 127) // 128) * 512)
     f32 = x.dtype is _F32
@@ -618,6 +628,7 @@ class GatedFfn:
                 _dense(w, _BF16, shape, name)
             ptrs = [_p(w) for w in (w1, w3, w2)] + [None] * 3
         self._keep = (w1, w3, w2)
+        _on(*(t for w in self._keep for t in (w if self.mxfp4 else (w,))))
         self.hidden, self.inter, self.act = H, I, act
         cfg = MoeFfnConfig(H, I, ACTIVATIONS[act], MOE_WEIGHTS_MXFP4 if self.mxfp4 else MOE_WEIGHTS_BF16)
         w = MoeFfnWeights(*ptrs)
@@ -699,11 +710,12 @@ class GatedFfn:
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
+        st = _on(x, out)
         if m > self._fits[0] or _capturing():
             self.workspace(m, False, x.device)
         saved = _empty(self.saved_size(m), dtype=_F32, device=x.device) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
-                                      saved.data_ptr() if save else None, *self._ws_at, _on(x))
+                                      saved.data_ptr() if save else None, *self._ws_at, st)
         if rc:
             raise MoeError(rc, "moe_ffn_forward")
         return (out, saved) if save else out
@@ -719,6 +731,7 @@ class GatedFfn:
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
         _dense(saved, _F32, (self.saved_size(m),), "saved")
+        st = _on(dout, x, saved)
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
         dw1 = dw3 = dw2 = None
         if need_dw:
@@ -731,7 +744,7 @@ class GatedFfn:
         rc = self.lib.moe_ffn_backward(
             self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m,
             dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else
-                                                  (None, None, None)), *self._ws_at, _on(x))
+                                                  (None, None, None)), *self._ws_at, st)
         if rc:
             raise MoeError(rc, "moe_ffn_backward")
         return dx, dw1, dw3, dw2

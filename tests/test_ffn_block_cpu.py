@@ -273,3 +273,14 @@ def test_error_words_of_products_outlive_their_workspace(B, monkeypatch):
     B._space(like, 7, 1000)[0] = 2
     B._space(like, 7, 1 << 20)
     assert B.mxfp4_device_status(stream) == 2 and B.mxfp4_device_status(stream) == 0
+
+
+def test_operands_lie_on_the_current_device(B, monkeypatch):
+    """The library launches on the current device: operands elsewhere are refused before a launch."""
+    monkeypatch.setattr(B, "_current_device", lambda: 1)
+    monkeypatch.setattr(B.torch._C, "_cuda_getCurrentRawStream", lambda dev: 40 + dev)
+    there, here = (types.SimpleNamespace(get_device=lambda d=d: d, device=f"cuda:{d}") for d in (0, 1))
+    assert B._on(here) == 41 and B._on(here, here, here) == 41
+    for bad in ((there,), (here, there), (there, here), (here, here, here, there)):
+        with pytest.raises(ValueError, match="cuda:0 in a call on cuda:1"):
+            B._on(*bad)
