@@ -533,6 +533,9 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
 
 
 _spaces = {}  # (device, stream) -> [workspace of the MXFP4 products launched on that stream, those before it]
+# Held from the choice of such a workspace to the last launch that uses it: a product may be two
+# launches, and other threads run during the library's calls.
+_spaces_lock = threading.RLock()
 
 
 def _space(like, stream: int, need: int) -> torch.Tensor:
@@ -552,8 +555,9 @@ def mxfp4_device_status(stream=None) -> int:
     """The first device error (0: none) of the MXFP4 products on `stream` since it was last read
     (of eager calls: a captured one keeps its error word inside its graph)."""
     s = stream if stream is not None else torch.cuda.current_stream()
-    ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
-    return 0 if ws is None else past.status(ws, s)
+    with _spaces_lock:
+        ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
+        return 0 if ws is None else past.status(ws, s)
 
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
@@ -570,9 +574,10 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     else:
         _dense(out, _BF16, (m, n), "out")
     st = _on(a_codes, a_scales, b_codes, b_scales, out)
-    ws = _space(a_codes, st, 256)
-    rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n, k,
-                            out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    with _spaces_lock:
+        ws = _space(a_codes, st, 256)
+        rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n,
+                                k, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
     if rc:
         raise MoeError(rc, "moe_mxfp4_gemm")
     return out
@@ -593,11 +598,13 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
     else:
         _dense(out, _BF16, (m, n), "out")
     st = _on(x, codes, scales, out)
-    # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
-    ws = _space(x, st, 1024 + m * k // 2 + (m + 127) // 128 * ((k + 127) // 128) * 512)
     f32 = x.dtype is _F32
-    rc = (lib.moe_mxfp4_linear_f32 if f32 else lib.moe_mxfp4_linear)(
-        x.data_ptr(), ld, m, codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    with _spaces_lock:
+        # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
+        ws = _space(x, st, 1024 + m * k // 2 + (m + 127) // 128 * ((k + 127) // 128) * 512)
+        rc = (lib.moe_mxfp4_linear_f32 if f32 else lib.moe_mxfp4_linear)(
+            x.data_ptr(), ld, m, codes.data_ptr(), scales.data_ptr(), n, k, out.data_ptr(), ws.data_ptr(), ws.numel(),
+            st)
     if rc:
         raise MoeError(rc, "moe_mxfp4_linear_f32" if f32 else "moe_mxfp4_linear")
     return out
@@ -610,8 +617,8 @@ class GatedFfn:
     Weights are bf16 tensors, or (codes, packed scales) pairs as
     moe_mxfp4_quant returns them; act is "silu" or "gelu" (tanh form).
     A handle keeps one workspace: order its calls, replays of graphs that
-    captured them among these, as on one stream.  Such graphs need the handle
-    alive."""
+    captured them among these, as on one stream, and make them from one thread
+    at a time.  Such graphs need the handle alive."""
 
     def __init__(self, w1, w3, w2, act="silu"):
         self.lib = load_library()

@@ -1,6 +1,8 @@
 """The gated feed-forward block and MXFP4 entry points without a GPU: refusals, sizes, the scale
 order, and the formulas the GPU tests compare against."""
 import ctypes
+import threading
+import time
 import types
 import weakref
 
@@ -284,3 +286,31 @@ def test_operands_lie_on_the_current_device(B, monkeypatch):
     for bad in ((there,), (here, there), (there, here), (here, here, here, there)):
         with pytest.raises(ValueError, match="cuda:0 in a call on cuda:1"):
             B._on(*bad)
+
+
+def test_products_of_two_threads_do_not_interleave(B, monkeypatch):
+    """A product of many tokens is two launches with the stream's shared workspace between them, and
+    the interpreter runs other threads while the library launches."""
+    inside, together, seen = 0, [], set()
+
+    def linear(x, ld, m, codes, scales, n, k, out, ws, size, stream):
+        nonlocal inside
+        inside += 1
+        time.sleep(0.002)
+        together.append(inside)
+        seen.add(ws)
+        inside -= 1
+        return 0
+    monkeypatch.setattr(B, "_capturing", lambda: False)
+    monkeypatch.setattr(B, "_spaces", {})
+    monkeypatch.setattr(B, "_lib", types.SimpleNamespace(moe_mxfp4_linear=linear, moe_mxfp4_linear_f32=linear))
+    monkeypatch.setattr(B, "_mx_matrix", lambda *a: (64, 64))
+    monkeypatch.setattr(B, "_rows", lambda *a, **k: 64)
+    monkeypatch.setattr(B, "_on", lambda *t: 7)
+    x = torch.zeros(20, 64, dtype=torch.bfloat16)
+    threads = [threading.Thread(target=lambda: [B.moe_mxfp4_linear(x, x, x) for _ in range(10)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(together) == 40 and max(together) == 1 and len(seen) == 1

@@ -700,3 +700,23 @@ def test_an_error_is_read_after_the_workspace_has_grown(B):
     blk.set_wait_limit(0)
     blk.forward(_n(4, 2000, H))
     assert blk.device_status() == 2 and blk.device_status() == 0
+
+
+def test_products_of_two_threads_on_one_stream(B):
+    import threading
+    (w,), _ = _quantised(B, [_n(4, 256, 512)])
+    xs = [_n(60 + i, 300, 512) for i in range(4)]
+    want = [B.moe_mxfp4_linear(x, *w) for x in xs]
+    torch.cuda.synchronize()
+    got = [[] for _ in xs]
+
+    def work(i):
+        for _ in range(200):
+            got[i].append(B.moe_mxfp4_linear(xs[i], *w))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert all(len(g) == 200 and all(torch.equal(o, v) for o in g) for g, v in zip(got, want))
