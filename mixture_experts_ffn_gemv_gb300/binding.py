@@ -189,11 +189,12 @@ _capturing = torch.cuda.is_current_stream_capturing
 
 class _Workspaces:
     """What a handle keeps of its workspaces besides the current one: those that captured graphs
-    replay into, and the error words of those it has outgrown."""
+    replay into, the error words of those it has outgrown, and which streams use the current one."""
 
     def __init__(self):
         self.held = []     # used by captured graphs
         self.headers = []  # of outgrown ones that no graph uses
+        self.streams = (None, set())  # a workspace and the streams it is recorded on
 
     def grown(self, old, need: int, device):
         """A workspace of `need` bytes in place of `old`, its header zeroed."""
@@ -208,6 +209,16 @@ class _Workspaces:
         """A call on ws follows.  One that is captured makes its graph replay into ws."""
         if _capturing() and not any(t is ws for t in self.held):
             self.held.append(ws)
+
+    def record(self, ws, stream):
+        """The same of a call on `stream` (None: the current one): when ws is let go, torch gives its
+        memory to others only after what that stream has been given."""
+        raw = torch._C._cuda_getCurrentRawStream(ws.get_device()) if stream is None else stream.cuda_stream
+        if self.streams[0] is not ws:
+            self.streams = (ws, set())
+        if raw not in self.streams[1] and not _capturing():  # a captured one is held
+            ws.record_stream(stream if stream is not None else torch.cuda.current_stream(ws.device))
+            self.streams[1].add(raw)
 
     def status(self, ws, stream) -> int:
         """The first device error (0: none) in the words of ws and of those before it; a word that
@@ -295,6 +306,11 @@ class MoeLayer:
         self._past.use(self._ws)
         return self._ws
 
+    def _call_space(self, m: int, stream) -> torch.Tensor:
+        ws = self.workspace(m)
+        self._past.record(ws, stream)
+        return ws
+
     def select_arm(self, m: int) -> int:
         return self.lib.moe_select_arm(self.handle, int(m))
 
@@ -350,7 +366,7 @@ class MoeLayer:
         ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
         w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
         lg = torch.empty(m, self.shape.num_experts, dtype=torch.float32, device=dev) if logits else None
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_route(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(lg), _p(ids), _p(w),
                                   _p(ws), ws.numel(), _stream(stream)), "moe_route")
         return (ids, w, lg) if logits else (ids, w)
@@ -363,7 +379,7 @@ class MoeLayer:
         off = torch.empty(n_local + 1, dtype=torch.int32, device=dev)
         sp = torch.empty(P, dtype=torch.int32, device=dev)
         sl = torch.empty(P, dtype=torch.int32, device=dev)
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_permute(self.handle, _p(topk_ids), m, _p(off), _p(sp), _p(sl), _p(ws), ws.numel(),
                                     _stream(stream)), "moe_permute")
         return off, sp, sl
@@ -372,7 +388,7 @@ class MoeLayer:
         m = x.shape[0]
         if out is None:
             out = torch.empty(m, self.shape.hidden, dtype=torch.bfloat16, device=x.device)
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_experts(self.handle, _p(x), m, _p(topk_ids), _p(topk_w), _p(out), ARMS[arm], _p(ws),
                                     ws.numel(), _stream(stream)), "moe_experts")
         return out
@@ -380,7 +396,7 @@ class MoeLayer:
     def moe_shared_expert_add(self, x, out, arm="auto", stream=None):
         """out (bf16 [m, H], in place) += the shared expert of x."""
         m = x.shape[0]
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_shared_expert_add(self.handle, _p(x), m, _p(out), ARMS[arm], _p(ws), ws.numel(),
                                               _stream(stream)), "moe_shared_expert_add")
         return out
@@ -394,7 +410,7 @@ class MoeLayer:
         if return_routing:
             ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
             w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_forward(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(out), _p(ids), _p(w),
                                     ARMS[arm], _p(ws), ws.numel(), _stream(stream)), "moe_forward")
         return (out, ids, w) if return_routing else out
@@ -411,7 +427,7 @@ class MoeLayer:
         if return_routing:
             ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
             w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
-        ws = self.workspace(m)
+        ws = self._call_space(m, stream)
         _check(self.lib.moe_forward_residual_rmsnorm(self.handle, _p(x), m, _p(router_w), _p(router_bias),
                                                      _p(residual), _p(norm_w), float(eps), _p(norm_out), _p(ids),
                                                      _p(w), ARMS[arm], _p(ws), ws.numel(), _stream(stream)),
@@ -676,6 +692,7 @@ class GatedFfn:
             if self._ws is None or self._ws.numel() < need:
                 self._ws = self._past.grown(self._ws, need, device)
                 self._ws_at = (self._ws.data_ptr(), self._ws.numel())
+                self._past.streams = (self._ws, set())
             self._fits[backward] = m
         self._past.use(self._ws)
         return self._ws
@@ -720,6 +737,8 @@ class GatedFfn:
         st = _on(x, out)
         if m > self._fits[0] or _capturing():
             self.workspace(m, False, x.device)
+        if st not in self._past.streams[1]:
+            self._past.record(self._ws, None)
         saved = _empty(self.saved_size(m), dtype=_F32, device=x.device) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
                                       saved.data_ptr() if save else None, *self._ws_at, st)
@@ -748,6 +767,8 @@ class GatedFfn:
             dw2 = new((H, I), dtype=_BF16, device=dev)
         if m > self._fits[1] or _capturing():
             self.workspace(m, True, x.device)
+        if st not in self._past.streams[1]:
+            self._past.record(self._ws, None)
         rc = self.lib.moe_ffn_backward(
             self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m,
             dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else

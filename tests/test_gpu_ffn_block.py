@@ -720,3 +720,31 @@ def test_products_of_two_threads_on_one_stream(B):
         t.join()
     torch.cuda.synchronize()
     assert all(len(g) == 200 and all(torch.equal(o, v) for o in g) for g, v in zip(got, want))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("grow", [False, True])
+def test_a_workspace_let_go_while_another_stream_uses_it(B, mx, grow):
+    """A handle's workspace belongs to the stream of its first call.  Outgrown, or gone with the
+    handle, while a call on another stream is still to run, it is not given to others before that."""
+    H, I, m = 512, 2048, 300
+    w = _weights(71, H, I)
+    w = _quantised(B, w)[0] if mx else w
+    x, big = _n(72, m, H), _n(73, 2000, H)
+    blk = B.GatedFfn(*w)
+    want = blk.forward(x)
+    size = blk.workspace(m, False, x.device).numel()
+    st, load = torch.cuda.Stream(), torch.zeros(1 << 28, device="cuda")
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            load.add_(1)  # some 6 ms before the call's turn comes
+        blk.forward(x, out=out)
+    if grow:
+        blk.workspace(2000, False, x.device)
+    else:
+        del blk
+    others = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all((t == 0x5A).all() for t in others) and torch.equal(out, want)

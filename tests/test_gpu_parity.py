@@ -746,3 +746,23 @@ def test_a_captured_header_is_not_taken_for_clean(cuda):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and layer.device_status() == 0
+
+
+def test_a_workspace_let_go_while_another_stream_uses_it(cuda):
+    """A layer's workspace, outgrown while a call on another stream is still to run, is not given to
+    others before that."""
+    wl = I.WORKLOADS["tiny"]
+    tensors, layer = layer_for(wl, cuda)
+    x = I.make_x(wl.shape, 300, device=cuda)
+    want = layer.moe_forward(x, tensors["router_w"], tensors["router_bias"])
+    size = layer.workspace(300).numel()
+    st, load, out = torch.cuda.Stream(), torch.zeros(1 << 28, device=cuda), torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            load.add_(1)
+    layer.moe_forward(x, tensors["router_w"], tensors["router_bias"], out=out, stream=st)
+    layer.workspace(4000)
+    others = [torch.full((size,), 0x5A, dtype=torch.uint8, device=cuda) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all((t == 0x5A).all() for t in others) and torch.equal(out, want)
