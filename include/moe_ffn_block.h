@@ -9,7 +9,8 @@
  * Conventions as in moe_ffn.h: device pointers, caller-owned buffers, no
  * allocation, no synchronisation (every call can be captured in a CUDA
  * graph), MOE_OK or an error status, m == 0 launches nothing, results
- * deterministic.  Pointers are 16-byte aligned.
+ * deterministic.  Pointers are 16-byte aligned.  Outputs share no memory with
+ * inputs, but out may be x (or lie in it) in moe_ffn_forward and moe_mxfp4_linear.
  *
  * MXFP4 (OCP Microscaling Formats v1.0): e2m1 codes (magnitudes 0, 0.5, 1,
  * 1.5, 2, 3, 4, 6), two per byte, element 2j in the low nibble of byte j; one

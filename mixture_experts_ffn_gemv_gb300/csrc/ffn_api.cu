@@ -298,13 +298,21 @@ LinearLayout linear_layout(int64_t m, int64_t k) {
     return o;
 }
 
+// Whether rows of k bf16 elements, ldx apart, and a dense [m, n] share memory.
+bool overlap(const void* x, int64_t ldx, int64_t k, const void* out, int64_t n, int64_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+    return a < b + (size_t)m * n * 2 && b < a + ((size_t)(m - 1) * ldx + k) * 2;
+}
+
 int linear(const void* x, bool f32, int64_t ldx, int64_t m, const uint8_t* w, const uint8_t* ws, int64_t n, int64_t k,
            void* out, void* workspace, size_t bytes, void* stream) {
     if (m < 0 || n <= 0 || n % 8 || k <= 0 || k % 32) return MOE_ERR_INVALID_ARG;
     const LinearLayout lo = linear_layout(m, k);
     const int rc = check_gemm(m, n, k, w, ws, out, workspace, bytes, lo.total);
     if (rc != MOE_OK || m == 0) return rc;
-    if (m <= kNarrowQuant && !f32) {  // quantised by the product's kernel itself
+    // quantised by the product's kernel itself, whose CTAs read x to the end while
+    // others write: only where out is not (part of) x
+    if (m <= kNarrowQuant && !f32 && !overlap(x, ldx, k, out, n, m)) {
         if (!x || !aligned(x, 16) || ldx < k || ldx % 8) return MOE_ERR_INVALID_ARG;
         NarrowProduct q = narrow(nullptr, (int)m, (int)n, (int)k, workspace);
         if (!mx_code_map(&q.a[0], w, n, k, 128) || !mx_scale_map(&q.as[0], ws, n, k)) return MOE_ERR_CUDA;

@@ -748,3 +748,30 @@ def test_a_workspace_let_go_while_another_stream_uses_it(B, mx, grow):
     others = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert all((t == 0x5A).all() for t in others) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m", [1, 3, 16, 40, 300])
+def test_out_may_be_x(B, m):
+    """In place: the linear (up to 16 tokens of bf16 are quantised by the kernel that writes out) and
+    both forms of the block."""
+    n = 2048
+    (w,), _ = _quantised(B, [_n(4, n, n, std=n ** -0.5)])
+    x = _n(5, m, n)
+    want = B.moe_mxfp4_linear(x, *w)
+    for _ in range(5):
+        y = x.clone()
+        assert B.moe_mxfp4_linear(y, *w, out=y) is y and torch.equal(y, want)
+    if m > 1:  # rows of x are twice as long as the output's: out within x
+        base = torch.cat([x, x], 1)
+        y = base.reshape(-1)[:m * n].reshape(m, n)
+        assert torch.equal(B.moe_mxfp4_linear(base[:, n:], *w, out=y), want)
+    # x at the start of out's rows, in more row tiles than the device holds at once
+    k, n2 = 512, 1 << 16
+    (v,), _ = _quantised(B, [_n(4, n2, k, std=k ** -0.5)])
+    want, y = B.moe_mxfp4_linear(x[:, :k], *v), torch.zeros(m, n2, dtype=torch.bfloat16, device="cuda")
+    y[:, :k] = x[:, :k]
+    assert torch.equal(B.moe_mxfp4_linear(y[:, :k], *v, out=y), want)
+    ws = _weights(6, n, 512)
+    for blk in (B.GatedFfn(*ws), B.GatedFfn(*_quantised(B, ws)[0])):
+        want, y = blk.forward(x), x.clone()
+        assert blk.forward(y, out=y) is y and torch.equal(y, want)
