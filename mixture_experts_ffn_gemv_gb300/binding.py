@@ -184,7 +184,9 @@ def moe_act_quant_nvfp4(x, stream=None):
     return codes, sb, g
 
 
-_capturing = torch.cuda.is_current_stream_capturing
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index
+_current_device = torch._C._cuda_getDevice
 
 
 class _Workspaces:
@@ -213,7 +215,7 @@ class _Workspaces:
     def record(self, ws, stream):
         """The same of a call on `stream` (None: the current one): when ws is let go, torch gives its
         memory to others only after what that stream has been given."""
-        raw = torch._C._cuda_getCurrentRawStream(ws.get_device()) if stream is None else stream.cuda_stream
+        raw = _raw_stream(ws.get_device()) if stream is None else stream.cuda_stream
         if self.streams[0] is not ws:
             self.streams = (ws, set())
         if raw not in self.streams[1] and not _capturing():  # a captured one is held
@@ -468,9 +470,6 @@ def _dense(t, dtype, shape, what: str):
         raise ValueError(f"{what}: a contiguous device tensor of {dtype}, {tuple(shape)}")
 
 
-_current_device = torch._C._cuda_getDevice
-
-
 def _on(*tensors) -> int:
     """The current CUDA stream of the device that every one of `tensors` lies on: the current
     device, on which the library launches.  A call that is given a stream makes it the current one
@@ -479,7 +478,7 @@ def _on(*tensors) -> int:
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"a tensor on {t.device} in a call on cuda:{dev}, the current device")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _raw_stream(dev)
 
 
 def mxfp4_scales_shape(rows: int, n: int):
@@ -548,7 +547,7 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
     return out
 
 
-_spaces = {}  # (device, stream) -> [workspace of the MXFP4 products launched on that stream, those before it]
+_spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on that stream, _Workspaces
 # Held from the choice of such a workspace to the last launch that uses it: a product may be two
 # launches, and other threads run during the library's calls.
 _spaces_lock = threading.RLock()
@@ -561,10 +560,12 @@ def _space(like, stream: int, need: int) -> torch.Tensor:
     need = max(need, 1 << 16)
     if _capturing():
         return _Workspaces().grown(None, need, like.device)
-    entry = _spaces.setdefault((like.get_device(), stream), [None, _Workspaces()])
-    if entry[0] is None or entry[0].numel() < need:
-        entry[0] = entry[1].grown(entry[0], need, like.device)
-    return entry[0]
+    key = (like.get_device(), stream)
+    ws, past = _spaces.get(key) or (None, _Workspaces())
+    if ws is None or ws.numel() < need:
+        ws = past.grown(ws, need, like.device)
+        _spaces[key] = ws, past
+    return ws
 
 
 def mxfp4_device_status(stream=None) -> int:
@@ -652,6 +653,7 @@ class GatedFfn:
             ptrs = [_p(w) for w in (w1, w3, w2)] + [None] * 3
         self._keep = (w1, w3, w2)
         _on(*(t for w in self._keep for t in (w if self.mxfp4 else (w,))))
+        self._dev = (w1[0] if self.mxfp4 else w1).get_device()
         self.hidden, self.inter, self.act = H, I, act
         cfg = MoeFfnConfig(H, I, ACTIVATIONS[act], MOE_WEIGHTS_MXFP4 if self.mxfp4 else MOE_WEIGHTS_BF16)
         w = MoeFfnWeights(*ptrs)
@@ -713,6 +715,14 @@ class GatedFfn:
         that was made during a capture, from the graph's first run on."""
         return self._past.status(self._ws, stream)
 
+    def _stream_for(self, *tensors) -> int:
+        """As _on, for tensors on the weights' device; that it is the current one the library checks."""
+        dev = self._dev
+        for t in tensors:
+            if t.get_device() != dev:
+                raise ValueError(f"a tensor on {t.device} in a call of a block on cuda:{dev}")
+        return _raw_stream(dev)
+
     def saved_size(self, m: int) -> int:
         """Words of what a forward pass on m tokens saves (moe_ffn_saved_size, in 4-byte words)."""
         n = self._saved.get(m)
@@ -734,7 +744,7 @@ class GatedFfn:
             out = torch.empty_like(x, memory_format=torch.contiguous_format)
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
-        st = _on(x, out)
+        st = self._stream_for(x, out)
         if m > self._fits[0] or _capturing():
             self.workspace(m, False, x.device)
         if st not in self._past.streams[1]:
@@ -757,7 +767,7 @@ class GatedFfn:
         m = x.shape[0]
         _need(dout.shape[0] == m, "dout and x differ in rows")
         _dense(saved, _F32, (self.saved_size(m),), "saved")
-        st = _on(dout, x, saved)
+        st = self._stream_for(dout, x, saved)
         dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
         dw1 = dw3 = dw2 = None
         if need_dw:

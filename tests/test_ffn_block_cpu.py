@@ -280,12 +280,17 @@ def test_error_words_of_products_outlive_their_workspace(B, monkeypatch):
 def test_operands_lie_on_the_current_device(B, monkeypatch):
     """The library launches on the current device: operands elsewhere are refused before a launch."""
     monkeypatch.setattr(B, "_current_device", lambda: 1)
-    monkeypatch.setattr(B.torch._C, "_cuda_getCurrentRawStream", lambda dev: 40 + dev)
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 40 + dev)
     there, here = (types.SimpleNamespace(get_device=lambda d=d: d, device=f"cuda:{d}") for d in (0, 1))
     assert B._on(here) == 41 and B._on(here, here, here) == 41
+    block = object.__new__(B.GatedFfn)
+    block._dev = 1
+    assert block._stream_for(here, here) == 41
     for bad in ((there,), (here, there), (there, here), (here, here, here, there)):
         with pytest.raises(ValueError, match="cuda:0 in a call on cuda:1"):
             B._on(*bad)
+        with pytest.raises(ValueError, match="cuda:0 in a call of a block on cuda:1"):
+            block._stream_for(*bad)
 
 
 def test_products_of_two_threads_do_not_interleave(B, monkeypatch):
