@@ -442,7 +442,7 @@ class MoeLayer:
 # checks test the common case (dense rows) first and word the refusal after.
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
-_empty = torch.empty
+_empty, _empty_like, _dense_rows = torch.empty, torch.empty_like, torch.contiguous_format
 
 
 def _need(ok, what: str):
@@ -503,11 +503,12 @@ def mxfp4_unpack_scales(scales, rows: int, n: int):
 
 def _mx_matrix(codes, scales, what: str):
     """(rows, n) of a matrix held as codes and packed scales."""
-    _need(codes.dim() == 2, f"{what}: codes are [rows, n/2]")
+    if codes.dim() != 2:
+        raise ValueError(f"{what}: codes are [rows, n/2]")
     rows, half = codes.shape
     if not (codes.dtype is _U8 and codes.is_cuda and codes.is_contiguous()):
         raise ValueError(f"{what} codes: a contiguous device tensor of uint8")
-    _dense(scales, _U8, mxfp4_scales_shape(rows, 2 * half), f"{what} scales")
+    _dense(scales, _U8, ((rows + 127) // 128, (half + 63) // 64, 32, 4, 4), what)
     return rows, 2 * half
 
 
@@ -557,13 +558,14 @@ def _space(like, stream: int, need: int) -> torch.Tensor:
     """A workspace of at least `need` bytes for calls on `stream`, the current one, its header
     zeroed before first use.  A call that is captured into a graph gets one from the graph's own
     pool: the graph may be replayed beside eager calls, and after they have needed a larger one."""
-    need = max(need, 1 << 16)
-    if _capturing():
-        return _Workspaces().grown(None, need, like.device)
     key = (like.get_device(), stream)
-    ws, past = _spaces.get(key) or (None, _Workspaces())
-    if ws is None or ws.numel() < need:
-        ws = past.grown(ws, need, like.device)
+    entry = _spaces.get(key)
+    capturing = _capturing()
+    if entry is not None and entry[0].numel() >= need and not capturing:
+        return entry[0]
+    old, past = entry if entry is not None and not capturing else (None, _Workspaces())
+    ws = past.grown(old, max(need, 1 << 16), like.device)
+    if not capturing:
         _spaces[key] = ws, past
     return ws
 
@@ -586,11 +588,12 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     m, k = _mx_matrix(a_codes, a_scales, "a")
     n, kb = _mx_matrix(b_codes, b_scales, "b")
     _need(k == kb, f"k differs: {k} and {kb}")
+    st = _on(a_codes, a_scales, b_codes, b_scales)
     if out is None:
         out = _empty((m, n), dtype=_BF16, device=a_codes.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(a_codes, a_scales, b_codes, b_scales, out)
+        _on(out)
     with _spaces_lock:
         ws = _space(a_codes, st, 256)
         rc = lib.moe_mxfp4_gemm(a_codes.data_ptr(), a_scales.data_ptr(), m, b_codes.data_ptr(), b_scales.data_ptr(), n,
@@ -610,11 +613,12 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
     n, k = _mx_matrix(codes, scales, "w")
     ld = _rows(x, k, "x", f32=True)
     m = x.shape[0]
+    st = _on(x, codes, scales)
     if out is None:
         out = _empty((m, n), dtype=_BF16, device=x.device)
     else:
         _dense(out, _BF16, (m, n), "out")
-    st = _on(x, codes, scales, out)
+        _on(out)
     f32 = x.dtype is _F32
     with _spaces_lock:
         # what moe_mxfp4_linear_workspace_size returns for a k that is a multiple of 32
@@ -740,11 +744,12 @@ class GatedFfn:
                 return self.forward(x, save, out)
         ld = _rows(x, self.hidden, "x")
         m = x.shape[0]
+        st = self._stream_for(x)
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            out = _empty_like(x, memory_format=_dense_rows)
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
-        st = self._stream_for(x, out)
+            self._stream_for(out)
         if m > self._fits[0] or _capturing():
             self.workspace(m, False, x.device)
         if st not in self._past.streams[1]:
@@ -768,7 +773,7 @@ class GatedFfn:
         _need(dout.shape[0] == m, "dout and x differ in rows")
         _dense(saved, _F32, (self.saved_size(m),), "saved")
         st = self._stream_for(dout, x, saved)
-        dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+        dx = _empty_like(x, memory_format=_dense_rows) if need_dx else None
         dw1 = dw3 = dw2 = None
         if need_dw:
             new, dev = _empty if m else torch.zeros, x.device
