@@ -15,7 +15,6 @@ using namespace moe;
 
 struct moe_ffn {
     moe_ffn_config cfg;  // first: the sizes below need nothing else of a handle
-    moe_ffn_weights w;
     int device;
     mutable int last_launches;
     mutable const void* last_ws;  // its header is known to be clean
@@ -355,7 +354,6 @@ int moe_ffn_create(const moe_ffn_config* cfg, const moe_ffn_weights* w, moe_ffn*
     moe_ffn* f = new (std::nothrow) moe_ffn();
     if (!f) return MOE_ERR_CUDA;
     f->cfg = c;
-    f->w = *w;
     f->device = dev;
     f->wait_ns = kWaitNs;
     const uint64_t H = c.hidden, I = c.inter;

@@ -29,13 +29,13 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool tmap_encode(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, int esize, uint32_t box_cols,
-                 uint32_t box_rows, bool swizzle, uint64_t ld) {
+                 uint32_t box_rows, bool swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (!fn || rank < 2 || rank > 3) return false;
     cuuint64_t gdim[3], gstride[2];
     cuuint32_t box[3] = {box_cols, box_rows, 1}, estr[3] = {1, 1, 1};
     for (int i = 0; i < rank; ++i) gdim[i] = dims[i];
-    gstride[0] = (ld ? ld : dims[0]) * esize;
+    gstride[0] = dims[0] * esize;
     if (rank == 3) gstride[1] = dims[0] * dims[1] * esize;
     const CUtensorMapDataType type = esize == 4   ? CU_TENSOR_MAP_DATA_TYPE_UINT32
                                      : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
