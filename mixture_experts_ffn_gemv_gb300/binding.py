@@ -534,7 +534,7 @@ def moe_mxfp4_quant(x, stream=None):
 
 
 def moe_mxfp4_dequant(codes, scales, stream=None):
-    """The values (bf16 [rows, n]) that codes and packed scales stand for."""
+    """The values (bf16 [rows, n]) that codes and packed scales stand for; infinite past bf16's range."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_mxfp4_dequant(codes, scales)
@@ -737,8 +737,10 @@ class GatedFfn:
         return n
 
     def forward(self, x, save=False, out=None, stream=None):
-        """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H]; with save (bf16 weights),
-        (out, saved) for backward: saved is fp32 [saved_size(m)], in moe_ffn_forward's own order."""
+        """x bf16 [m, H] (rows may be strided) -> out bf16 [m, H] (out may be x); with save (bf16
+        weights), (out, saved) for backward: saved is fp32 [saved_size(m)], in moe_ffn_forward's own
+        order.  Up to 8 tokens keep h in 16 bits unless it is saved, and differ from a saving call by
+        h's rounding to bf16.  Given a stream, the call's inputs have to stay until that has run it."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.forward(x, save, out)

@@ -15,8 +15,9 @@ __device__ __forceinline__ float logistic(float t) { return __fdividef(1.0f, 1.0
 constexpr float kGelu0 = 1.5957691216057308f;              // 2 sqrt(2 / pi)
 constexpr float kGelu1 = 1.5957691216057308f * 0.044715f;
 
-// t(g).  Its square stops at 10^4: s(t) is 0 or 1 long before, and t and t'
-// stay finite for every finite g.
+// t(g).  Its square stops at 10^4: s(t) is 0 or 1 long before.  t' stays finite
+// for every finite g; t for |g| up to 4.7e35, past which it is an infinity of
+// g's sign, with s(t) 1 or 0 as before.
 __device__ __forceinline__ float act_square(float g) { return fminf(g * g, 1.0e4f); }
 
 // t(g) and t'(g) of an activation known at compile time.

@@ -454,7 +454,9 @@ int sms() {
     return n;
 }
 
-// Clusters of `size` CTAs that the device holds at once with one CTA per SM (asked once).
+// Clusters of `size` CTAs that the device holds at once with one CTA per SM
+// (asked once, of one kernel: with 222 KB each, no kernel here has two CTAs on an
+// SM, and what is left to decide is where SMs stand, not which kernel it is).
 int clusters_resident(int size) {
     static std::atomic<int> known[MAX_SLICES + 1];
     std::atomic<int>& k = known[size];
@@ -505,8 +507,13 @@ cudaError_t launch(const NarrowProduct& p, int smem, cudaStream_t st) {
 
 // Measured as whole blocks, narrow / wide in us: bf16 7168 x 2048 at 256 tokens
 // 35.6 / 48.8, at 384 54.2 / 50.1; 2048 x 8192 at 256 38.8 / 55.2, at 384 65.2 /
-// 64.8; 2048 x 768 (few tiles) at 512 18.5 / 21.2, at 1024 22.6 / 21.5.  MXFP4
-// 7168 x 2048 at 128 20.7 / 25.3, 2048 x 8192 at 256 27.4 / 24.5.
+// 64.8; 2048 x 768 (few tiles) at 512 18.5 / 21.2, at 1024 22.6 / 21.5.
+// MXFP4, weights from HBM, at 64, 128, 192 and 256 tokens: blocks of 7168 x 2048
+// 17.6 / 21.3, 21.4 / 22.5, 22.3 / 23.0, 24.1 / 23.2; 2048 x 8192 18.5 / 23.3,
+// 22.5 / 24.2, 26.5 / 24.4, 27.7 / 24.8; the product 7168 -> 7168 12.1 / 16.2,
+// 14.2 / 17.1, 17.7 / 17.4, 18.1 / 17.8.  One border for all does not suit small
+// blocks (2048 x 768: 12.8 / 12.9, 16.9 / 14.2) nor a long K with few rows (the
+// product 7168 -> 2048 at 256: 12.1 / 16.6).
 bool narrow_is_faster(int m, int R, bool mx) {
     if (mx) return m <= 128;
     return m <= 256 || (m <= 512 && ceil_div(m, 256) * ceil_div(R, 256) * 4 <= sms() / 2);

@@ -775,3 +775,13 @@ def test_out_may_be_x(B, m):
     for blk in (B.GatedFfn(*ws), B.GatedFfn(*_quantised(B, ws)[0])):
         want, y = blk.forward(x), x.clone()
         assert blk.forward(y, out=y) is y and torch.equal(y, want)
+
+
+def test_read_back_past_bf16(B):
+    """Scales 252 to 255 with every code: exact, infinite past bf16's range, or NaN."""
+    codes = torch.arange(16, dtype=torch.uint8, device="cuda").repeat(4, 2)
+    scales = torch.tensor([[252], [253], [254], [255]], dtype=torch.uint8, device="cuda")
+    got = B.moe_mxfp4_dequant(P.mx_pack(codes), B.mxfp4_pack_scales(scales))
+    want = P.mx_values(codes, scales).to(torch.bfloat16)
+    assert torch.isinf(want[1:3]).any(1).all() and torch.isfinite(want[0]).all()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[:3], want[:3])
