@@ -189,44 +189,55 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device index
 _current_device = torch._C._cuda_getDevice
 
 
+def _record(ws, stream):
+    """Tells torch that `stream` (None: the current one) uses ws: when ws is let go, its memory goes
+    to others only after what that stream has been given."""
+    ws.record_stream(stream if stream is not None else torch.cuda.current_stream(ws.device))
+
+
 class _Workspaces:
-    """What a handle keeps of its workspaces besides the current one: those that captured graphs
-    replay into, the error words of those it has outgrown, and which streams use the current one."""
+    """The workspaces of a handle as its calls use them, one after another as each is outgrown.  A
+    handle zeroes a workspace's header in the first call on it, on that call's stream; nothing here
+    writes into one."""
 
     def __init__(self):
-        self.held = []     # used by captured graphs
-        self.headers = []  # of outgrown ones that no graph uses
-        self.streams = (None, set())  # a workspace and the streams it is recorded on
+        self.used = None      # of the last call; kept until there is a call on another
+        self.streams = set()  # that `used` is recorded on
+        self.held = []        # those that captured graphs replay into
+        self.headers = []     # of those outgrown that no graph uses
 
-    def grown(self, old, need: int, device):
-        """A workspace of `need` bytes in place of `old`, its header zeroed."""
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        ws[:256].zero_()
-        if old is not None and not any(t is old for t in self.held):
-            # a copy made during a capture would not be made until the graph runs
-            self.headers.append(old if _capturing() else old[:256].clone())
-        return ws
-
-    def use(self, ws):
-        """A call on ws follows.  One that is captured makes its graph replay into ws."""
+    def hold(self, ws):
+        """Keeps ws for good if a CUDA graph is being captured, which will replay into it."""
         if _capturing() and not any(t is ws for t in self.held):
             self.held.append(ws)
 
-    def record(self, ws, stream):
-        """The same of a call on `stream` (None: the current one): when ws is let go, torch gives its
-        memory to others only after what that stream has been given."""
+    def called(self, ws, stream=None):
+        """A call on `stream` (None: the current one) that uses ws has been launched."""
         raw = _raw_stream(ws.get_device()) if stream is None else stream.cuda_stream
-        if self.streams[0] is not ws:
-            self.streams = (ws, set())
-        if raw not in self.streams[1] and not _capturing():  # a captured one is held
-            ws.record_stream(stream if stream is not None else torch.cuda.current_stream(ws.device))
-            self.streams[1].add(raw)
+        capturing = _capturing()
+        if ws is not self.used:
+            old, self.used, self.streams = self.used, ws, set()
+            if old is not None and not any(t is old for t in self.held):
+                if capturing:  # a copy would be made when the graph runs
+                    self.headers.append(old)
+                elif stream is None:
+                    self.headers.append(old[:256].clone())
+                    _record(old, None)
+                else:
+                    with torch.cuda.stream(stream):
+                        self.headers.append(old[:256].clone())
+                    _record(old, stream)
+        if capturing:
+            self.hold(ws)
+        elif raw not in self.streams:
+            _record(ws, stream)
+            self.streams.add(raw)
 
-    def status(self, ws, stream) -> int:
-        """The first device error (0: none) in the words of ws and of those before it; a word that
-        is set is cleared."""
+    def status(self, stream) -> int:
+        """The first device error (0: none) in the words of the workspaces that calls have used; a
+        word that is set is cleared."""
         code, first = _i32(), 0
-        for t in (*self.headers, *(t for t in self.held if t is not ws), ws):
+        for t in (*self.headers, *(t for t in self.held if t is not self.used), self.used):
             if t is None:
                 continue
             rc = load_library().moe_device_status(_p(t), _stream(stream), ctypes.byref(code))
@@ -303,15 +314,24 @@ class MoeLayer:
         graphs use live as long as the handle."""
         need = self.workspace_size(m)
         if self._ws is None or self._ws.numel() < need:
-            dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-            self._ws = self._past.grown(self._ws, need, dev)
-        self._past.use(self._ws)
+            self._grow(need, device)
+        self._past.hold(self._ws)
         return self._ws
 
+    def _grow(self, need: int, device=None):
+        dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+
     def _call_space(self, m: int, stream) -> torch.Tensor:
-        ws = self.workspace(m)
-        self._past.record(ws, stream)
-        return ws
+        """The workspace for a call on `stream`."""
+        need = self.workspace_size(m)
+        if self._ws is None or self._ws.numel() < need:
+            if stream is None:
+                self._grow(need)
+            else:
+                with torch.cuda.stream(stream):  # what it allocates belongs to the stream that writes it
+                    self._grow(need)
+        return self._ws
 
     def select_arm(self, m: int) -> int:
         return self.lib.moe_select_arm(self.handle, int(m))
@@ -359,7 +379,7 @@ class MoeLayer:
     def device_status(self, stream=None) -> int:
         """The first device error (0: none) of the handle's calls since it was last read; of a workspace
         that was made during a capture, from the graph's first run on."""
-        return self._past.status(self._ws, stream)
+        return self._past.status(stream)
 
     # ---- entry points
     def moe_route(self, x, router_w, router_bias=None, logits=False, stream=None):
@@ -371,6 +391,8 @@ class MoeLayer:
         ws = self._call_space(m, stream)
         _check(self.lib.moe_route(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(lg), _p(ids), _p(w),
                                   _p(ws), ws.numel(), _stream(stream)), "moe_route")
+        if m:
+            self._past.called(ws, stream)
         return (ids, w, lg) if logits else (ids, w)
 
     def moe_permute(self, topk_ids, stream=None):
@@ -384,6 +406,8 @@ class MoeLayer:
         ws = self._call_space(m, stream)
         _check(self.lib.moe_permute(self.handle, _p(topk_ids), m, _p(off), _p(sp), _p(sl), _p(ws), ws.numel(),
                                     _stream(stream)), "moe_permute")
+        if m:
+            self._past.called(ws, stream)
         return off, sp, sl
 
     def moe_experts(self, x, topk_ids, topk_w, arm="auto", out=None, stream=None):
@@ -393,6 +417,8 @@ class MoeLayer:
         ws = self._call_space(m, stream)
         _check(self.lib.moe_experts(self.handle, _p(x), m, _p(topk_ids), _p(topk_w), _p(out), ARMS[arm], _p(ws),
                                     ws.numel(), _stream(stream)), "moe_experts")
+        if m:
+            self._past.called(ws, stream)
         return out
 
     def moe_shared_expert_add(self, x, out, arm="auto", stream=None):
@@ -401,6 +427,8 @@ class MoeLayer:
         ws = self._call_space(m, stream)
         _check(self.lib.moe_shared_expert_add(self.handle, _p(x), m, _p(out), ARMS[arm], _p(ws), ws.numel(),
                                               _stream(stream)), "moe_shared_expert_add")
+        if m:
+            self._past.called(ws, stream)
         return out
 
     def moe_forward(self, x, router_w, router_bias=None, arm="auto", out=None, return_routing=False, stream=None):
@@ -415,6 +443,8 @@ class MoeLayer:
         ws = self._call_space(m, stream)
         _check(self.lib.moe_forward(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(out), _p(ids), _p(w),
                                     ARMS[arm], _p(ws), ws.numel(), _stream(stream)), "moe_forward")
+        if m:
+            self._past.called(ws, stream)
         return (out, ids, w) if return_routing else out
 
     def moe_forward_residual_rmsnorm(self, x, router_w, residual, norm_w, eps=1e-6, router_bias=None, arm="auto",
@@ -434,6 +464,8 @@ class MoeLayer:
                                                      _p(residual), _p(norm_w), float(eps), _p(norm_out), _p(ids),
                                                      _p(w), ARMS[arm], _p(ws), ws.numel(), _stream(stream)),
                "moe_forward_residual_rmsnorm")
+        if m:
+            self._past.called(ws, stream)
         return (norm_out, ids, w) if return_routing else norm_out
 
 
@@ -508,7 +540,7 @@ def _mx_matrix(codes, scales, what: str):
     rows, half = codes.shape
     if not (codes.dtype is _U8 and codes.is_cuda and codes.is_contiguous()):
         raise ValueError(f"{what} codes: a contiguous device tensor of uint8")
-    _dense(scales, _U8, ((rows + 127) // 128, (half + 63) // 64, 32, 4, 4), what)
+    _dense(scales, _U8, ((rows + 127) // 128, (half + 63) // 64, 32, 4, 4), what + " scales")
     return rows, 2 * half
 
 
@@ -563,9 +595,11 @@ def _space(like, stream: int, need: int) -> torch.Tensor:
     capturing = _capturing()
     if entry is not None and entry[0].numel() >= need and not capturing:
         return entry[0]
-    old, past = entry if entry is not None and not capturing else (None, _Workspaces())
-    ws = past.grown(old, max(need, 1 << 16), like.device)
+    ws = _empty((max(need, 1 << 16),), dtype=_U8, device=like.device)
+    ws[:256].zero_()
     if not capturing:
+        past = entry[1] if entry is not None else _Workspaces()
+        past.called(ws)
         _spaces[key] = ws, past
     return ws
 
@@ -576,7 +610,7 @@ def mxfp4_device_status(stream=None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     with _spaces_lock:
         ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
-        return 0 if ws is None else past.status(ws, s)
+        return 0 if ws is None else past.status(s)
 
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
@@ -696,11 +730,10 @@ class GatedFfn:
         if m > self._fits[backward]:
             need = self.workspace_size(m, backward)
             if self._ws is None or self._ws.numel() < need:
-                self._ws = self._past.grown(self._ws, need, device)
+                self._ws = torch.empty(max(need, 256), dtype=_U8, device=device)
                 self._ws_at = (self._ws.data_ptr(), self._ws.numel())
-                self._past.streams = (self._ws, set())
             self._fits[backward] = m
-        self._past.use(self._ws)
+        self._past.hold(self._ws)
         return self._ws
 
     def set_wait_limit(self, ns: int):
@@ -717,7 +750,7 @@ class GatedFfn:
     def device_status(self, stream=None) -> int:
         """The first device error (0: none) of the handle's calls since it was last read; of a workspace
         that was made during a capture, from the graph's first run on."""
-        return self._past.status(self._ws, stream)
+        return self._past.status(stream)
 
     def _stream_for(self, *tensors) -> int:
         """As _on, for tensors on the weights' device; that it is the current one the library checks."""
@@ -752,15 +785,16 @@ class GatedFfn:
         else:
             _dense(out, _BF16, (m, self.hidden), "out")
             self._stream_for(out)
-        if m > self._fits[0] or _capturing():
+        if m > self._fits[0]:
             self.workspace(m, False, x.device)
-        if st not in self._past.streams[1]:
-            self._past.record(self._ws, None)
         saved = _empty(self.saved_size(m), dtype=_F32, device=x.device) if save else None
         rc = self.lib.moe_ffn_forward(self.handle, x.data_ptr(), ld, m, out.data_ptr(),
                                       saved.data_ptr() if save else None, *self._ws_at, st)
         if rc:
             raise MoeError(rc, "moe_ffn_forward")
+        past = self._past
+        if m and (past.used is not self._ws or st not in past.streams or _capturing()):
+            past.called(self._ws)
         return (out, saved) if save else out
 
     def backward(self, dout, x, saved, need_dx=True, need_dw=True, stream=None):
@@ -782,14 +816,15 @@ class GatedFfn:
             dw1 = new((I, H), dtype=_BF16, device=dev)
             dw3 = new((I, H), dtype=_BF16, device=dev)
             dw2 = new((H, I), dtype=_BF16, device=dev)
-        if m > self._fits[1] or _capturing():
+        if m > self._fits[1]:
             self.workspace(m, True, x.device)
-        if st not in self._past.streams[1]:
-            self._past.record(self._ws, None)
         rc = self.lib.moe_ffn_backward(
             self.handle, dout.data_ptr(), ldd, x.data_ptr(), ldx, saved.data_ptr(), m,
             dx.data_ptr() if need_dx else None, *((dw1.data_ptr(), dw3.data_ptr(), dw2.data_ptr()) if need_dw else
                                                   (None, None, None)), *self._ws_at, st)
         if rc:
             raise MoeError(rc, "moe_ffn_backward")
+        past = self._past
+        if m and (past.used is not self._ws or st not in past.streams or _capturing()):
+            past.called(self._ws)
         return dx, dw1, dw3, dw2

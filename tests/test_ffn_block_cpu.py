@@ -176,15 +176,23 @@ def test_backward_formula_against_differences(kind):
 
 # ---------------------------------------------------------------- workspaces (host memory stands in for the device's)
 
-def _handle(B, cls):
-    """A handle of cls without a device: 256 bytes of workspace a token."""
+def _handle(B, monkeypatch, cls):
+    """A handle of cls without a device: 256 bytes of workspace a token; and a call on m tokens, from
+    which the workspace comes back."""
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(B, "_record", lambda ws, stream: None)
     h = object.__new__(cls)
     h.handle = None
     h.workspace_size = lambda m, backward=False: 256 * m
     h._new_workspaces()
-    if cls is B.MoeLayer:
-        return h, lambda m: h.workspace(m, device="cpu")
-    return h, lambda m: h.workspace(m, False, "cpu")
+
+    def call(m):
+        ws = h.workspace(m, device="cpu") if cls is B.MoeLayer else h.workspace(m, False, "cpu")
+        if ws is not h._past.used:
+            ws[:256] = 0  # as the library does in the first call on it
+        h._past.called(ws)
+        return ws
+    return h, call
 
 
 @pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
@@ -192,7 +200,7 @@ def test_a_captured_workspace_outlives_its_successor(B, monkeypatch, cls):
     """A CUDA graph replays into the workspace that its capture saw, also after a larger call."""
     capturing = False
     monkeypatch.setattr(B, "_capturing", lambda: capturing)
-    h, space = _handle(B, getattr(B, cls))
+    h, space = _handle(B, monkeypatch, getattr(B, cls))
     first = weakref.ref(space(4))
     space(8)
     assert first() is None  # no graph knows it
@@ -218,6 +226,8 @@ def test_captured_products_share_no_workspace(B, monkeypatch):
     capturing = False
     monkeypatch.setattr(B, "_capturing", lambda: capturing)
     monkeypatch.setattr(B, "_spaces", {})
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(B, "_record", lambda ws, stream: None)
     like = types.SimpleNamespace(get_device=lambda: 0, device="cpu")
     eager = B._space(like, 7, 1000)
     assert B._space(like, 7, 1000) is eager
@@ -238,16 +248,19 @@ def _host_status(ws, stream, code):
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
 def test_error_words_outlive_their_workspace(B, monkeypatch, cls, captured):
-    """A new workspace reads as clean before its first call, and an error that nobody has read is
-    still there after the workspace has grown."""
+    """A workspace is not read before a call has used it, and an error that nobody has read is still
+    there after the workspace has grown."""
     capturing = False
     monkeypatch.setattr(B, "_capturing", lambda: capturing)
     monkeypatch.setattr(B, "load_library", lambda: types.SimpleNamespace(moe_device_status=_host_status))
     monkeypatch.setattr(B, "_stream", lambda stream=None: None)
-    h, space = _handle(B, getattr(B, cls))
+    h, space = _handle(B, monkeypatch, getattr(B, cls))
+    assert h.device_status() == 0
+    unused = h.workspace(2, False, "cpu") if cls == "GatedFfn" else h.workspace(2, "cpu")
+    unused.fill_(0x5A)
     assert h.device_status() == 0
     first = space(4)
-    assert not first[:256].any() and h.device_status() == 0
+    assert h.device_status() == 0
     capturing = captured
     assert space(4) is first
     capturing = False
@@ -269,6 +282,8 @@ def test_error_words_of_products_outlive_their_workspace(B, monkeypatch):
     monkeypatch.setattr(B, "_spaces", {})
     monkeypatch.setattr(B, "load_library", lambda: types.SimpleNamespace(moe_device_status=_host_status))
     monkeypatch.setattr(B, "_stream", lambda stream=None: None)
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(B, "_record", lambda ws, stream: None)
     like = types.SimpleNamespace(get_device=lambda: 0, device="cpu")
     stream = types.SimpleNamespace(device=types.SimpleNamespace(index=0), cuda_stream=7)
     assert B.mxfp4_device_status(stream) == 0
@@ -312,6 +327,8 @@ def test_products_of_two_threads_do_not_interleave(B, monkeypatch):
     monkeypatch.setattr(B, "_mx_matrix", lambda *a: (64, 64))
     monkeypatch.setattr(B, "_rows", lambda *a, **k: 64)
     monkeypatch.setattr(B, "_on", lambda *t: 7)
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(B, "_record", lambda ws, stream: None)
     x = torch.zeros(20, 64, dtype=torch.bfloat16)
     threads = [threading.Thread(target=lambda: [B.moe_mxfp4_linear(x, x, x) for _ in range(10)]) for _ in range(4)]
     for t in threads:
@@ -319,3 +336,44 @@ def test_products_of_two_threads_do_not_interleave(B, monkeypatch):
     for t in threads:
         t.join()
     assert len(together) == 40 and max(together) == 1 and len(seen) == 1
+
+
+@pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
+def test_a_workspace_is_kept_until_its_successor_is_used(B, monkeypatch, cls):
+    """The library takes a header for clean by its workspace's address, that of the last call: no
+    other workspace may get that address before the next call."""
+    monkeypatch.setattr(B, "_capturing", lambda: False)
+    h, call = _handle(B, monkeypatch, getattr(B, cls))
+    last = weakref.ref(call(4))
+    for m in (8, 16, 32):
+        h.workspace(m, False, "cpu") if cls == "GatedFfn" else h.workspace(m, "cpu")
+        assert last() is not None
+    call(32)
+    assert last() is None
+
+
+def test_streams_of_a_workspace_are_recorded_once_each(B, monkeypatch):
+    recorded = []
+    monkeypatch.setattr(B, "_capturing", lambda: False)
+    past = B._Workspaces()
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(B, "_record", lambda ws, stream: recorded.append((id(ws), stream and stream.cuda_stream)))
+    a, b = torch.zeros(256), torch.zeros(256)
+    side = types.SimpleNamespace(cuda_stream=9)
+    for stream in (None, None, side, side, None):
+        past.called(a, stream)
+    assert recorded == [(id(a), None), (id(a), 9)]
+    recorded.clear()
+    past.called(b)  # the copy of a's header is a use of a
+    past.called(b)
+    assert recorded == [(id(a), None), (id(b), None)]
+
+
+@pytest.mark.parametrize("cls", ["GatedFfn", "MoeLayer"])
+def test_making_a_workspace_writes_nothing(B, monkeypatch, cls):
+    """A write from the stream that made a workspace could come late, amid a call on another one."""
+    monkeypatch.setattr(B, "_capturing", lambda: False)
+    h, _ = _handle(B, monkeypatch, getattr(B, cls))
+    monkeypatch.setattr(B.torch, "empty", lambda n, **kw: torch.full((n,), 0x5A, dtype=torch.uint8))
+    ws = h.workspace(4, False, "cpu") if cls == "GatedFfn" else h.workspace(4, "cpu")
+    assert (ws == 0x5A).all()
