@@ -234,6 +234,15 @@ MOE_API int moe_experts(const moe_layer* layer, const void* x, int64_t m, const 
                 const float* topk_w, void* out, int arm, void* workspace,
                 size_t workspace_bytes, void* stream);
 
+/* moe_experts of an fp8 layer whose input is in 8 bits already, as moe_add_rmsnorm
+ * or moe_act_quant_fp8 leave it: the experts' own quantisation of x is skipped.
+ *   x_codes uint8 [m, H]; x_scales fp32 [m, H/128], both 16-byte aligned; x bf16
+ *   [m, H], read only for the shared expert's sigmoid gate (else it may be NULL).
+ * MOE_ERR_UNSUPPORTED for other weight formats.                              */
+MOE_API int moe_experts_fp8(const moe_layer* layer, const uint8_t* x_codes, const float* x_scales, const void* x,
+                            int64_t m, const int32_t* topk_ids, const float* topk_w, void* out, int arm,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* out[t, :] = bf16(out[t, :] + shared(x[t, :])): the shared expert alone
  * (weight 1, or its sigmoid gate), added to out in fp32 and rounded once --
  * forward_prefill.rs's "defer shared expert blend until after all-reduce",

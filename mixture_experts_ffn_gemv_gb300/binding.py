@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -25,7 +26,7 @@ ARMS = {"auto": MOE_ARM_AUTO, "gemv": MOE_ARM_GEMV, "gemm": MOE_ARM_GEMM}
 
 EXPORTED = (
     "moe_layer_create", "moe_layer_destroy", "moe_workspace_size", "moe_select_arm", "moe_route",
-    "moe_permute", "moe_permute_noalloc", "moe_experts", "moe_shared_expert_add", "moe_forward",
+    "moe_permute", "moe_permute_noalloc", "moe_experts", "moe_experts_fp8", "moe_shared_expert_add", "moe_forward",
     "moe_forward_residual_rmsnorm",
     "moe_act_quant_fp8", "moe_act_quant_nvfp4", "moe_act_quant_nvfp4_f32", "moe_device_status", "moe_router_planes_size",
     "moe_router_prepare", "moe_layer_set_wait_limit",
@@ -36,6 +37,9 @@ EXPORTED = (
     "moe_ffn_set_wait_limit", "moe_ffn_stall_test", "moe_ffn_last_launch_count", "moe_mxfp4_scales_size", "moe_mxfp4_quant", "moe_mxfp4_quant_f32",
     "moe_mxfp4_dequant", "moe_mxfp4_gemm_workspace_size", "moe_mxfp4_gemm",
     "moe_mxfp4_linear_workspace_size", "moe_mxfp4_linear", "moe_mxfp4_linear_f32",
+    "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_size", "moe_add_rmsnorm_backward",
+    "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
+    "moe_lora_add_workspace_size", "moe_lora_add",
 )
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -91,6 +95,7 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_permute.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         lib.moe_permute_noalloc.argtypes = [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp]
         lib.moe_experts.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+        lib.moe_experts_fp8.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
         lib.moe_shared_expert_add.argtypes = [_vp, _vp, _i64, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
         lib.moe_forward.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]
         lib.moe_forward_residual_rmsnorm.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp,
@@ -132,6 +137,18 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_mxfp4_linear_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
         for fn in (lib.moe_mxfp4_linear, lib.moe_mxfp4_linear_f32):
             fn.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, sz, _vp]
+        f32 = ctypes.c_float
+        lib.moe_add_rmsnorm.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, f32, _vp, _i64, _vp, _vp, _vp, _vp]
+        lib.moe_add_rmsnorm_backward_workspace_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
+        lib.moe_add_rmsnorm_backward.argtypes = [_vp, _i64, _vp, _i64, _i64, _i64, _vp, f32, _vp, _i64, _vp, _vp, _vp, sz,
+                                                 _vp]
+        lib.moe_balance_loss_workspace_size.argtypes = [_i64, _i64, ctypes.POINTER(sz)]
+        lib.moe_balance_loss.argtypes = [_vp, _vp, _i64, _i32, _i32, _vp, _i64, ctypes.c_int, _vp, _vp, _vp, _vp, sz, _vp]
+        lib.moe_route_backward.argtypes = [_vp, _vp, _i64, _i32, _i32, ctypes.c_int, ctypes.c_int, f32, _vp, _vp, _i64, _vp,
+                                           _vp, _vp, _vp, _vp]
+        lib.moe_lora_add_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
+        lib.moe_lora_add.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
+                                     sz, _vp]
         _lib = lib
         return lib
 
@@ -421,6 +438,44 @@ class MoeLayer:
             self._past.called(ws, stream)
         return out
 
+    def moe_experts_fp8(self, codes, scales, topk_ids, topk_w, x=None, arm="auto", out=None, stream=None):
+        """moe_experts of an fp8 layer from x in 8 bits (codes uint8 [m, H], scales fp32 [m, H/128], as
+        moe_add_rmsnorm and moe_act_quant_fp8 give them); x (bf16) only for a shared expert with a gate."""
+        H, k = self.shape.hidden, self.shape.top_k
+        _need(codes.dim() == 2, "codes: [m, H]")
+        m = codes.shape[0]
+        _dense(codes, _U8, (m, H), "codes")
+        _dense(scales, _F32, (m, H // 128), "scales")
+        _dense(topk_ids, torch.int32, (m, k), "topk_ids")
+        _dense(topk_w, _F32, (m, k), "topk_w")
+        _on(codes, scales, topk_ids, topk_w)
+        if x is not None:
+            _dense(x, _BF16, (m, H), "x")
+            _on(x)
+        if out is None:
+            out = torch.empty(m, H, dtype=torch.bfloat16, device=codes.device)
+        else:
+            _dense(out, _BF16, (m, H), "out")
+            _on(out)
+        ws = self._call_space(m, stream)
+        _check(self.lib.moe_experts_fp8(self.handle, _p(codes), _p(scales), _p(x), m, _p(topk_ids), _p(topk_w), _p(out),
+                                        ARMS[arm], _p(ws), ws.numel(), _stream(stream)), "moe_experts_fp8")
+        if m:
+            self._past.called(ws, stream)
+        return out
+
+    def moe_balance_loss(self, logits, topk_ids, seq_offsets=None, stream=None):
+        """moe_balance_loss of this layer's scoring."""
+        return moe_balance_loss(logits, topk_ids, seq_offsets, getattr(self.shape, "scoring", "softmax"), stream)
+
+    def moe_route_backward(self, logits, topk_ids, dtopk_w=None, dbalance=None, dz=None, counts=None, seq_offsets=None,
+                           stream=None):
+        """moe_route_backward of this layer's scoring and weights."""
+        sh = self.shape
+        return moe_route_backward(logits, topk_ids, dtopk_w, dbalance, dz, counts, seq_offsets,
+                                  getattr(sh, "scoring", "softmax"), getattr(sh, "norm_topk_prob", True),
+                                  float(getattr(sh, "routed_scaling", 1.0)), stream)
+
     def moe_shared_expert_add(self, x, out, arm="auto", stream=None):
         """out (bf16 [m, H], in place) += the shared expert of x."""
         m = x.shape[0]
@@ -605,8 +660,8 @@ def _space(like, stream: int, need: int) -> torch.Tensor:
 
 
 def mxfp4_device_status(stream=None) -> int:
-    """The first device error (0: none) of the MXFP4 products on `stream` since it was last read
-    (of eager calls: a captured one keeps its error word inside its graph)."""
+    """The first device error (0: none) of the MXFP4 products and adapters on `stream` since it was
+    last read (of eager calls: a captured one keeps its error word inside its graph)."""
     s = stream if stream is not None else torch.cuda.current_stream()
     with _spaces_lock:
         ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
@@ -637,12 +692,23 @@ def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):
     return out
 
 
-def moe_mxfp4_linear(x, codes, scales, out=None, stream=None):
+def moe_mxfp4_linear(x, codes, scales, out=None, stream=None, adapters=None, adapter_ids=None):
     """x (bf16 or fp32 [m, k]) quantised to MXFP4 per call, times a weight matrix [n, k] held in
-    MXFP4 -> bf16 [m, n]."""
+    MXFP4 -> bf16 [m, n].  With adapters (a, b, scale), each token's low-rank adapter of x (bf16)
+    is then added, moe_lora_add of adapter_ids; out may not be x there."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return moe_mxfp4_linear(x, codes, scales, out)
+            return moe_mxfp4_linear(x, codes, scales, out, None, adapters, adapter_ids)
+    if adapters is not None:
+        _need(adapter_ids is not None, "adapters without adapter_ids")
+        a, b, scale = adapters
+        _need(codes.dim() == 2, "w: codes are [rows, n/2]")
+        y = _empty((x.shape[0], codes.shape[0]), dtype=_BF16, device=x.device) if out is None else out
+        _dense(y, _BF16, (x.shape[0], codes.shape[0]), "out")
+        add = _lora_call(y, x, a, b, adapter_ids, scale, None)  # all is checked before anything is launched
+        moe_mxfp4_linear(x, codes, scales, y)
+        return add()
+    _need(adapter_ids is None, "adapter_ids without adapters")
     lib = _lib or load_library()
     n, k = _mx_matrix(codes, scales, "w")
     ld = _rows(x, k, "x", f32=True)
@@ -828,3 +894,253 @@ class GatedFfn:
         if m and (past.used is not self._ws or st not in past.streams or _capturing()):
             past.called(self._ws)
         return dx, dw1, dw3, dw2
+
+
+# ---------------------------------------------------------------- operators around the layer and the block
+# (include/moe_ffn_ops.h)
+
+class NormOut(NamedTuple):
+    """What moe_add_rmsnorm gives; None for what was not asked for."""
+    out: torch.Tensor | None       # bf16 [m, h]
+    residual: torch.Tensor | None  # bf16 [m, h]: x + residual, what the norm was taken of
+    codes: torch.Tensor | None     # uint8 [m, h], e4m3
+    scales: torch.Tensor | None    # fp32 [m, ceil(h / 128)]
+
+
+def _share(a, b) -> bool:
+    """Whether two matrices of dense rows share memory: their spans meet and, where their rows are as
+    far apart, so do their columns."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    es, (m, n), (p, q) = a.element_size(), a.shape, b.shape
+    at, to = a.data_ptr(), b.data_ptr()
+    if at >= to + ((p - 1) * b.stride(0) + q) * es or to >= at + ((m - 1) * a.stride(0) + n) * es:
+        return False
+    pitch = a.stride(0) * es
+    if m == 1 or p == 1 or pitch != b.stride(0) * es:
+        return True
+    ahead = (to - at) % pitch  # of a's rows, b's columns begin
+    return ahead < n * es or ahead + q * es > pitch
+
+
+def _same(a, b) -> bool:
+    return a.data_ptr() == b.data_ptr() and a.shape == b.shape and (a.shape[0] <= 1 or a.stride() == b.stride())
+
+
+def _vector(t, n: int, what: str):
+    _dense(t, _F32, (n,), what)
+    _need(t.data_ptr() % 16 == 0, f"{what}: 16-byte aligned")
+
+
+def moe_add_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, out=None, bf16=True, fp8=False,
+                    stream=None) -> NormOut:
+    """RMSNorm of x (bf16 [m, h], rows may be strided), or of r = x + residual, times weight (fp32
+    [h]): to bf16 (out; it may be x) and, with fp8, to e4m3 codes and scales per 128 columns, of the
+    values before they are rounded to bf16.  r goes to residual_out (a new tensor unless given; it may
+    be residual)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_add_rmsnorm(x, weight, eps, residual, residual_out, out, bf16, fp8)
+    lib = _lib or load_library()
+    _need(x.dim() == 2, "x: [m, h]")
+    m, h = x.shape
+    ldx = _rows(x, h, "x")
+    _vector(weight, h, "weight")
+    _need(bf16 or fp8, "neither bf16 nor fp8 is asked for")
+    _need(out is None or bf16, "out: given, and bf16 not asked for")
+    st = _on(x, weight)
+    dev = x.device
+    ldr = ldo = 0
+    if residual is not None:
+        ldr = _rows(residual, h, "residual")
+        _need(residual.shape[0] == m, "x and residual differ in rows")
+        if residual_out is None:
+            residual_out = _empty((m, h), dtype=_BF16, device=dev)
+            ldo = h
+        else:
+            ldo = _rows(residual_out, h, "residual_out")
+            _need(residual_out.shape[0] == m, "x and residual_out differ in rows")
+            _need(not _share(residual_out, x) and (_same(residual_out, residual) or not _share(residual_out, residual)),
+                  "residual_out: residual itself, or memory of its own")
+        _on(residual, residual_out)
+    else:
+        _need(residual_out is None, "residual_out without a residual")
+    if out is not None:
+        _dense(out, _BF16, (m, h), "out")
+        _need(out.data_ptr() % 16 == 0, "out: 16-byte aligned")
+        _need((_same(out, x) or not _share(out, x))
+              and not any(t is not None and _share(out, t) for t in (residual, residual_out)),
+              "out: x itself, or memory of its own")
+        _on(out)
+    elif bf16:
+        out = _empty((m, h), dtype=_BF16, device=dev)
+    codes = scales = None
+    if fp8:
+        codes = _empty((m, h), dtype=_U8, device=dev)
+        scales = _empty((m, (h + 127) // 128), dtype=_F32, device=dev)
+    rc = lib.moe_add_rmsnorm(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, m, h,
+                             weight.data_ptr(), eps, None if residual is None else residual_out.data_ptr(), ldo,
+                             out.data_ptr() if bf16 else None, codes.data_ptr() if fp8 else None,
+                             scales.data_ptr() if fp8 else None, st)
+    if rc:
+        raise MoeError(rc, "moe_add_rmsnorm")
+    return NormOut(out, residual_out, codes, scales)
+
+
+def moe_add_rmsnorm_backward(dout, r, weight, eps=1e-6, dresidual=None, need_dw=True, stream=None):
+    """Gradients (dx bf16 [m, h], dweight fp32 [h]) of moe_add_rmsnorm's out, given the r that it
+    normalised (its residual, or x where there was none); dx is the gradient of x and of the residual
+    alike, dresidual (bf16) what else flows into r.  dweight is None where not needed, zero of no rows."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_add_rmsnorm_backward(dout, r, weight, eps, dresidual, need_dw)
+    lib = _lib or load_library()
+    _need(r.dim() == 2, "r: [m, h]")
+    m, h = r.shape
+    ldd, ldr, ldq = _rows(dout, h, "dout"), _rows(r, h, "r"), 0
+    _need(dout.shape[0] == m, "dout and r differ in rows")
+    _vector(weight, h, "weight")
+    st = _on(dout, r, weight)
+    if dresidual is not None:
+        ldq = _rows(dresidual, h, "dresidual")
+        _need(dresidual.shape[0] == m, "dresidual and r differ in rows")
+        _on(dresidual)
+    dx = _empty((m, h), dtype=_BF16, device=r.device)
+    dw = ws = None
+    need = 0
+    if need_dw:
+        size = ctypes.c_size_t()
+        _check(lib.moe_add_rmsnorm_backward_workspace_size(m, h, ctypes.byref(size)),
+               "moe_add_rmsnorm_backward_workspace_size")
+        need = size.value
+        dw = (_empty if m else torch.zeros)((h,), dtype=_F32, device=r.device)
+        ws = _empty((need,), dtype=_U8, device=r.device)
+    rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps,
+                                      None if dresidual is None else dresidual.data_ptr(), ldq, dx.data_ptr(),
+                                      dw.data_ptr() if need_dw else None, ws.data_ptr() if need_dw else None, need, st)
+    if rc:
+        raise MoeError(rc, "moe_add_rmsnorm_backward")
+    return dx, dw
+
+
+SCORINGS = {"softmax": MOE_SCORING_SOFTMAX, "sigmoid": MOE_SCORING_SIGMOID}
+
+
+def _router_args(logits, topk_ids, seq_offsets, scoring):
+    """Checks what the router's operators share; returns (m, E, k, sequences, scoring, stream)."""
+    _need(logits.dim() == 2 and topk_ids.dim() == 2, "logits: [m, E], topk_ids: [m, k]")
+    (m, E), k = logits.shape, topk_ids.shape[1]
+    _dense(logits, _F32, (m, E), "logits")
+    _dense(topk_ids, torch.int32, (m, k), "topk_ids")
+    _need(scoring in SCORINGS, f"scoring: one of {sorted(SCORINGS)}")
+    seqs = 1
+    st = _on(logits, topk_ids)
+    if seq_offsets is not None:
+        _need(seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2, "seq_offsets: [sequences + 1], at least one sequence")
+        seqs = seq_offsets.shape[0] - 1
+        _dense(seq_offsets, torch.int32, (seqs + 1,), "seq_offsets")
+        _on(seq_offsets)
+    return m, E, k, seqs, SCORINGS[scoring], st
+
+
+def moe_balance_loss(logits, topk_ids, seq_offsets=None, scoring="softmax", stream=None):
+    """(balance, z, counts) of a router's logits (fp32 [m, E]) and picks (int32 [m, k]), for each
+    sequence of tokens seq_offsets[s] .. seq_offsets[s + 1] (int32 on the device, not falling; None:
+    one sequence of all): balance and z fp32 [S], counts int32 [S, E].  Tokens in no sequence and ids
+    outside [0, E) count nowhere."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_balance_loss(logits, topk_ids, seq_offsets, scoring)
+    lib = _lib or load_library()
+    m, E, k, S, mode, st = _router_args(logits, topk_ids, seq_offsets, scoring)
+    dev = logits.device
+    new = _empty if m else torch.zeros
+    losses = new((2, S), dtype=_F32, device=dev)
+    counts = new((S, E), dtype=torch.int32, device=dev)
+    # what moe_balance_loss_workspace_size returns
+    ws = _empty(((4 * S + 255) // 256 * 256 + (((m + 7) // 8 + S) * 8 + 255) // 256 * 256,), dtype=_U8, device=dev)
+    balance = losses.data_ptr()
+    rc = lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), m, E, k,
+                              None if seq_offsets is None else seq_offsets.data_ptr(), S, mode, balance, balance + 4 * S,
+                              counts.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    if rc:
+        raise MoeError(rc, "moe_balance_loss")
+    return losses[0], losses[1], counts
+
+
+def moe_route_backward(logits, topk_ids, dtopk_w=None, dbalance=None, dz=None, counts=None, seq_offsets=None,
+                       scoring="softmax", norm_topk_prob=True, routed_scaling=1.0, stream=None):
+    """The gradient of a router's logits, fp32 [m, E]: through the routing weights (dtopk_w fp32
+    [m, k]) and through moe_balance_loss's balance and z (dbalance, dz fp32 [S], with the counts
+    that it gave and the same seq_offsets)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_route_backward(logits, topk_ids, dtopk_w, dbalance, dz, counts, seq_offsets, scoring,
+                                      norm_topk_prob, routed_scaling)
+    lib = _lib or load_library()
+    m, E, k, S, mode, st = _router_args(logits, topk_ids, seq_offsets, scoring)
+    for t, shape, dtype, what in ((dtopk_w, (m, k), _F32, "dtopk_w"), (dbalance, (S,), _F32, "dbalance"),
+                                  (dz, (S,), _F32, "dz"), (counts, (S, E), torch.int32, "counts")):
+        if t is not None:
+            _dense(t, dtype, shape, what)
+            _on(t)
+    _need(dbalance is None or counts is not None, "dbalance without counts")
+    d = _empty((m, E), dtype=_F32, device=logits.device)
+    ptr = [None if t is None else t.data_ptr() for t in (dtopk_w, seq_offsets, counts, dbalance, dz)]
+    rc = lib.moe_route_backward(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, mode, int(bool(norm_topk_prob)),
+                                routed_scaling, ptr[0], ptr[1], S, *ptr[2:], d.data_ptr(), st)
+    if rc:
+        raise MoeError(rc, "moe_route_backward")
+    return d
+
+
+def _lora_call(y, x, a, b, ids, scale, out):
+    """Checks a call of moe_lora_add; returns what makes it."""
+    lib = _lib or load_library()
+    _need(a.dim() == 3 and b.dim() == 3, "a: [n, r, k], b: [n, d, r]")
+    n, r, k = a.shape
+    d = b.shape[1]
+    _dense(a, _BF16, (n, r, k), "a")
+    _dense(b, _BF16, (n, d, r), "b")
+    ldx, ldy = _rows(x, k, "x"), _rows(y, d, "y")
+    m = x.shape[0]
+    _need(y.shape[0] == m, "x and y differ in rows")
+    _dense(ids, torch.int32, (m,), "ids")
+    st = _on(y, x, a, b, ids)
+    if scale is not None:
+        _dense(scale, _F32, (n,), "scale")
+        _on(scale)
+    if out is None:
+        out, ldo = y, ldy
+    else:
+        ldo = _rows(out, d, "out")
+        _need(out.shape[0] == m, "out and y differ in rows")
+        _need(_same(out, y) or not _share(out, y), "out: y itself, or memory of its own")
+        _on(out)
+    _need(not _share(out, x), "out shares memory with x")
+    size = ctypes.c_size_t()
+    rc = lib.moe_lora_add_workspace_size(m, k, r, ctypes.byref(size))
+    if rc:
+        raise MoeError(rc, "moe_lora_add")
+
+    def call():
+        with _spaces_lock:
+            ws = _space(x, st, size.value)
+            rc = lib.moe_lora_add(x.data_ptr(), ldx, m, k, y.data_ptr(), ldy, d, a.data_ptr(), b.data_ptr(), n, r,
+                                  ids.data_ptr(), None if scale is None else scale.data_ptr(), out.data_ptr(), ldo,
+                                  ws.data_ptr(), ws.numel(), st)
+        if rc:
+            raise MoeError(rc, "moe_lora_add")
+        return out
+    return call
+
+
+def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
+    """y (bf16 [m, d], a projection's output for x, bf16 [m, k]; rows may be strided) plus each token's
+    low-rank adapter: scale[i] b[i] (a[i] x[t]), i = ids[t] (int32 [m]; -1: none), a bf16 [n, r, k],
+    b bf16 [n, d, r], scale fp32 [n] (None: 1).  Into y unless out is given.  Ids outside [-1, n) count
+    as -1 and set the error word that mxfp4_device_status reads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_lora_add(y, x, a, b, ids, scale, out)
+    return _lora_call(y, x, a, b, ids, scale, out)()

@@ -315,11 +315,18 @@ GemvArgs gemv_args(const moe_layer* L, const Layout& lo, void* ws) {
     return a;
 }
 
+// fp8 codes and scales of x that a caller has
+struct CodedRows {
+    const uint8_t* codes;
+    const float* scales;
+};
+
 // permuted: the permute tables are already in the workspace; x_quantized: so
-// are the fp8 codes and scales of x (both written by the fused decode routing)
+// are the fp8 codes and scales of x (both written by the fused decode routing);
+// coded: the caller's take their place (x is then read for the shared gate alone)
 int run_experts(const moe_layer* L, const Layout& lo, const void* x, int m, const int32_t* ids, const float* w,
                 void* out, int arm, void* ws, Launcher& ln, bool permuted = false, bool x_quantized = false,
-                const TailArgs* tail = nullptr) {
+                const TailArgs* tail = nullptr, const CodedRows* coded = nullptr) {
     const moe_config& c = L->cfg;
     const cudaStream_t st = ln.st;
     const int E = L->E_local, k = lo.k, H = c.hidden, I = c.inter;
@@ -360,12 +367,13 @@ int run_experts(const moe_layer* L, const Layout& lo, const void* x, int m, cons
             MOE_LAUNCH(K_H_QUANT_NVFP4, launch_act_quant_nvfp4_f32(hf, lo.rows, I, hq, hsb, hg, st));
             MOE_LAUNCH(K_GEMV_DOWN, launch_gemv_down_nvfp4(a, hq, hsb, hg, y, st));
         } else if (L->fp8) {
-            uint8_t* xq = at<uint8_t>(ws, lo.xq);
-            float* xsc = at<float>(ws, lo.xsc);
+            const uint8_t* xq = coded ? coded->codes : at<uint8_t>(ws, lo.xq);
+            const float* xsc = coded ? coded->scales : at<float>(ws, lo.xsc);
             uint8_t* hq = at<uint8_t>(ws, lo.h);
             float* hsc = at<float>(ws, lo.hsc);
-            if (!x_quantized)
-            MOE_LAUNCH(K_ACT_QUANT, launch_act_quant_fp8(static_cast<const uint16_t*>(x), m, H, xq, xsc, st));
+            if (!x_quantized && !coded)
+                MOE_LAUNCH(K_ACT_QUANT, launch_act_quant_fp8(static_cast<const uint16_t*>(x), m, H, at<uint8_t>(ws, lo.xq),
+                                                             at<float>(ws, lo.xsc), st));
             float* hf = at<float>(ws, lo.hf);
             MOE_LAUNCH(K_GEMV_GATEUP, launch_gemv_gateup_fp8(a, xq, xsc, hf, st));
             MOE_LAUNCH(K_H_QUANT, launch_quant_rows_fp8(hf, lo.rows, I, hq, hsc, st));
@@ -420,10 +428,11 @@ int run_experts(const moe_layer* L, const Layout& lo, const void* x, int m, cons
         g.h_g = at<float>(ws, lo.hg);
         g.hf = at<float>(ws, lo.hf);
     } else if (L->fp8) {
-        uint8_t* xq = at<uint8_t>(ws, lo.xq);
-        float* xsc = at<float>(ws, lo.xsc);
-        if (!x_quantized)
-            MOE_LAUNCH(K_ACT_QUANT, launch_act_quant_fp8(static_cast<const uint16_t*>(x), m, H, xq, xsc, st));
+        const uint8_t* xq = coded ? coded->codes : at<uint8_t>(ws, lo.xq);
+        const float* xsc = coded ? coded->scales : at<float>(ws, lo.xsc);
+        if (!x_quantized && !coded)
+            MOE_LAUNCH(K_ACT_QUANT, launch_act_quant_fp8(static_cast<const uint16_t*>(x), m, H, at<uint8_t>(ws, lo.xq),
+                                                         at<float>(ws, lo.xsc), st));
         if (place_in_gather)
             MOE_LAUNCH(K_GATHER, launch_gather_pairs_fp8(xq, xsc, ids, L->e_lo, E, c.num_experts, k, lo.P, lo.rows, H,
                                                          po, at<uint8_t>(ws, lo.xs), at<float>(ws, lo.xs_sc), st));
@@ -660,6 +669,24 @@ int moe_experts(const moe_layer* layer, const void* x, int64_t m, const int32_t*
     return rc;
 }
 
+int moe_experts_fp8(const moe_layer* layer, const uint8_t* x_codes, const float* x_scales, const void* x, int64_t m,
+                    const int32_t* topk_ids, const float* topk_w, void* out, int arm, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    Layout lo;
+    if (layer && !layer->fp8) return MOE_ERR_UNSUPPORTED;
+    int rc = check_call(layer, m, workspace, workspace_bytes, &lo);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (!x_codes || !x_scales || !topk_ids || !topk_w || !out || !aligned(x_codes, 16) || !aligned(x_scales, 16) ||
+        !aligned(out, 16) || (lo.shared && layer->shared.gate ? !x || !aligned(x, 16) : false))
+        return MOE_ERR_INVALID_ARG;
+    if (arm < MOE_ARM_AUTO || arm > MOE_ARM_GEMM) return MOE_ERR_INVALID_ARG;
+    Launcher ln{layer, static_cast<cudaStream_t>(stream)};
+    if (prepare_header(layer, workspace, ln.st) != MOE_OK) return MOE_ERR_CUDA;
+    const CodedRows coded{x_codes, x_scales};
+    rc = run_experts(layer, lo, x, (int)m, topk_ids, topk_w, out, arm, workspace, ln, false, false, nullptr, &coded);
+    layer->last_launches = ln.n;
+    return rc;
+}
 
 int moe_shared_expert_add(const moe_layer* layer, const void* x, int64_t m, void* out, int arm, void* workspace,
                           size_t workspace_bytes, void* stream) {

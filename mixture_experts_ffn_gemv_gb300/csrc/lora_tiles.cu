@@ -1,0 +1,549 @@
+// Low-rank adapters for many tokens: out[t] = y[t] + scale B (A x[t]) as two
+// kernels over tiles of 128 tokens as they lie, whatever adapters they use.
+//
+// A tile's tokens are not sorted.  It lists the adapters that occur in it, in the
+// order of their first tokens, and multiplies the whole tile by each; a row then
+// takes the result of its own.  That spends products, which the tensor core has to
+// spare (r is small and everything here is bound by x, y and out), and saves
+// sorting, gathering and scattering: x, y and out move as TMA boxes.  Requests that
+// lie together make one or two adapters a tile.
+//
+// lora_shrink: part[z, t, :] = A x[t] over slice z of K.  Up to 256 / r adapters
+// share a pass over x: their rows of A are the MMA's N.
+// lora_expand: T = scale * sum of the slices, as two bf16 parts (the second what
+// the first's rounding left, so that T counts with 16 bits), in shared memory for
+// all of a block's tiles of 128 outputs; D = T B^T per adapter and tile, the row's
+// own added to y in shared memory, rounded once, and out by TMA.  y and the first
+// B are loaded before the shrink kernel ends.
+// Each: warp 0 TMA producer, warp 1 MMA issuer, then the epilogue warps.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "ffn_block.h"
+#include "launch.cuh"
+#include "ops.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BK = 64;
+constexpr int X_BYTES = BM * BK * 2;  // a box of 128 rows x 64 columns, 128-byte swizzle
+constexpr uint64_t DRAIN_NS = 2000000000ull;
+constexpr int TMEM_COLS = 256;
+
+// The adapters of a tile's tokens.
+struct Tile {
+    int id[BM];    // of each token, -1: none
+    int list[BM];  // those that occur
+    int slot[BM];  // a token's place in the list, -1: none
+    uint32_t firsts[4];
+    int count;
+};
+// By all threads of the block (at least 128).
+__device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& tl) {
+    const int i = threadIdx.x;
+    int id = -1;
+    if (i < BM) {
+        if (m0 + i < p.m) {
+            id = p.ids[m0 + i];
+            if (id < -1 || id >= p.n) {
+                set_error(p.hdr, DEV_ERR_BAD_ID, m0 + i);
+                id = -1;
+            }
+        }
+        tl.id[i] = id;
+    }
+    __syncthreads();
+    int first = i;
+    if (i < BM) {
+        for (int j = BM - 4; j >= 0; j -= 4) {
+            const int4 q = *reinterpret_cast<const int4*>(tl.id + j);
+            if (q.w == id) first = min(first, j + 3);
+            if (q.z == id) first = min(first, j + 2);
+            if (q.y == id) first = min(first, j + 1);
+            if (q.x == id) first = min(first, j);
+        }
+        const uint32_t b = __ballot_sync(0xffffffffu, id >= 0 && first == i);
+        if ((i & 31) == 0) tl.firsts[i >> 5] = b;
+    }
+    __syncthreads();
+    if (i < BM) {
+        int place = __popc(tl.firsts[first >> 5] & ((1u << (first & 31)) - 1u));
+        for (int w = 0; w < first >> 5; ++w) place += __popc(tl.firsts[w]);
+        tl.slot[i] = id >= 0 ? place : -1;
+        if (id >= 0 && first == i) tl.list[place] = id;
+        if (i == 0) {
+            int n = 0;
+            for (int w = 0; w < 4; ++w) n += __popc(tl.firsts[w]);
+            tl.count = n;
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- A x
+
+constexpr int SHRINK_THREADS = 192;
+
+__global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_constant__ LoraArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ alignas(16) Tile tl;
+    __shared__ uint64_t bars[2 * 8 + 3];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem), stride = X_BYTES + p.a_bytes;
+    const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + 8), tfull = smem_u32(bars + 16),
+                   tempty = smem_u32(bars + 17), drain = smem_u32(bars + 18);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int z = blockIdx.y, m0 = blockIdx.x * BM;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(full0 + 8 * s, 1);
+            mbar_init(empty0 + 8 * s, 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 4);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    list_adapters(p, m0, tl);
+    if (tl.count == 0) return;  // the whole block: nothing is allocated yet
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int k0 = z * p.split_blocks, k1 = min(p.kblocks, k0 + p.split_blocks);
+    const int passes = (tl.count + p.group - 1) / p.group;
+
+    if (warp == 0) {
+        uint32_t s = 0, ph = 1, n = 0;
+        bool ok = true;
+        for (int g = 0; g < passes && ok; ++g) {
+            const int u0 = g * p.group, u1 = min(tl.count, u0 + p.group);
+            for (int kb = k0; kb < k1; ++kb) {
+                if (warp_sees(&abort_flag) || !warp_wait(empty0 + 8 * s, ph, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t sa = sbase + s * stride, bar = full0 + 8 * s;
+                    mbar_arrive_expect_tx(bar, X_BYTES + (u1 - u0) * p.r * BK * 2);
+                    tma_load_3d(sa, &p.mx, kb * (BK / 2), m0, 0, bar);
+                    for (int u = u0; u < u1; ++u)
+                        tma_load_3d(sa + X_BYTES + (u - u0) * p.r * BK * 2, &p.ma, kb * (BK / 2), tl.list[u] * p.r, 0, bar);
+                }
+                __syncwarp();
+                ++n;
+                if (++s == (uint32_t)p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 61);
+            abort_flag = 1;
+        }
+        const uint32_t S = p.stages;
+        for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(full0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
+    } else if (warp == 1) {
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        for (int g = 0; g < passes && ok; ++g) {
+            const int u0 = g * p.group, u1 = min(tl.count, u0 + p.group);
+            const uint32_t idesc = idesc_bf16(BM, ((u1 - u0) * p.r + 15) / 16 * 16);
+            if (!warp_wait(tempty, (g & 1u) ^ 1u, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            for (int kb = k0; kb < k1; ++kb) {
+                if (warp_sees(&abort_flag) || !warp_wait(full0 + 8 * s, ph, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = sbase + s * stride;
+                const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + X_BYTES);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, kb != k0 || kk != 0);
+                    mma_commit(empty0 + 8 * s);
+                    if (kb == k1 - 1) mma_commit(tfull);
+                }
+                __syncwarp();
+                if (++s == (uint32_t)p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 62);
+            abort_flag = 1;
+        }
+        if (elect_one()) mma_commit(drain);
+        mbar_wait(drain, 0, DRAIN_NS);
+        __syncwarp();
+    } else {
+        const int row = (warp & 3) * 32 + lane, slot = tl.slot[row];
+        float* dst = p.part + ((size_t)z * p.m + m0 + row) * p.r;
+        const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        for (int g = 0; g < passes; ++g) {
+            if (!warp_wait(tfull, g & 1u, p.wait_ns) || warp_sees(&abort_flag)) {
+                if (lane == 0) {
+                    set_error(p.hdr, DEV_ERR_TIMEOUT, 63);
+                    abort_flag = 1;
+                }
+                break;
+            }
+            tc_fence_after();
+            const int u0 = g * p.group, u1 = min(tl.count, u0 + p.group);
+            for (int u = u0; u < u1; ++u) {
+                const bool own = slot == u;
+                if (!__any_sync(0xffffffffu, own)) continue;
+                for (int j = 0; j < p.r; j += 8) {
+                    uint32_t v[8];
+                    tmem_ld8(taddr + (u - u0) * p.r + j, v);
+                    tmem_wait_ld();
+                    if (own) {
+                        *reinterpret_cast<uint4*>(dst + j) = make_uint4(v[0], v[1], v[2], v[3]);
+                        *reinterpret_cast<uint4*>(dst + j + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- y + T B^T
+
+constexpr int BN = 128;
+constexpr int EPI_WARPS = 8;
+constexpr int EXPAND_THREADS = 32 * (2 + EPI_WARPS);
+constexpr int Y_STAGES = 3, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
+constexpr int MAX_B = 4;
+
+__global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ alignas(16) Tile tl;
+    __shared__ uint64_t bars[2 * Y_STAGES + 2 * MAX_B + 6];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int nb = (p.r + BK - 1) / BK;  // boxes along r
+    // T's first parts, its second parts, y, B
+    const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + Y_STAGES * Y_BYTES;
+    const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * Y_STAGES, bfull0 = yempty0 + 8 * Y_STAGES,
+                   bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 16,
+                   tready = dempty0 + 16, drain = tready + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m0 = blockIdx.x * BM;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Y_STAGES; ++s) {
+            mbar_init(yfull0 + 8 * s, 1);
+            mbar_init(yempty0 + 8 * s, EPI_WARPS);
+        }
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(bfull0 + 8 * s, 1);
+            mbar_init(bempty0 + 8 * s, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(dfull0 + 8 * s, 1);
+            mbar_init(dempty0 + 8 * s, EPI_WARPS);
+        }
+        mbar_init(tready, EPI_WARPS);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    list_adapters(p, m0, tl);  // ids, like y, are older than the shrink kernel, whose sums alone are waited for
+    if (tl.count == 0 && p.out == p.y && p.ldo == p.ldy) {
+        pdl_wait();
+        return;
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
+        bool ok = true;
+        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
+            if (warp_sees(&abort_flag) || !warp_wait(yempty0 + 8 * ys, yph, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            const bool two = nt * BN + 64 < p.N;
+            if (elect_one()) {
+                const uint32_t dst = y_at + ys * Y_BYTES, bar = yfull0 + 8 * ys;
+                mbar_arrive_expect_tx(bar, two ? Y_BYTES : X_BYTES);
+                tma_load_3d(dst, &p.my, nt * (BN / 2), m0, 0, bar);
+                if (two) tma_load_3d(dst + X_BYTES, &p.my, nt * (BN / 2) + 32, m0, 0, bar);
+            }
+            __syncwarp();
+            ++yn;
+            if (++ys == Y_STAGES) {
+                ys = 0;
+                yph ^= 1u;
+            }
+            for (int u = 0; u < tl.count && ok; ++u)
+                for (int kb = 0; kb < nb; ++kb) {
+                    if (warp_sees(&abort_flag) || !warp_wait(bempty0 + 8 * bs, bph, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        const uint32_t bar = bfull0 + 8 * bs;
+                        mbar_arrive_expect_tx(bar, X_BYTES);
+                        tma_load_3d(b_at + bs * X_BYTES, &p.mb, kb * (BK / 2), nt * BN, tl.list[u], bar);
+                    }
+                    __syncwarp();
+                    ++bn;
+                    if (++bs == (uint32_t)p.stages) {
+                        bs = 0;
+                        bph ^= 1u;
+                    }
+                }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 64);
+            abort_flag = 1;
+        }
+        const uint32_t S = p.stages;
+        for (uint32_t i = yn > Y_STAGES ? yn - Y_STAGES : 0; i < yn; ++i)
+            mbar_wait(yfull0 + 8 * (i % Y_STAGES), (i / Y_STAGES) & 1u, DRAIN_NS);
+        for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
+    } else if (warp == 1) {
+        uint32_t bs = 0, bph = 0, d = 0;
+        bool ok = tl.count == 0 || warp_wait(tready, 0, p.wait_ns);
+        tc_fence_after();
+        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas)
+            for (int u = 0; u < tl.count && ok; ++u, ++d) {
+                if (warp_sees(&abort_flag) || !warp_wait(dempty0 + 8 * (d & 1), ((d >> 1) & 1u) ^ 1u, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                for (int kb = 0; kb < nb; ++kb) {
+                    if (!warp_wait(bfull0 + 8 * bs, bph, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t hi = desc_sw128(t_at + kb * X_BYTES), lo = desc_sw128(t_at + (nb + kb) * X_BYTES),
+                                   bd = desc_sw128(b_at + bs * X_BYTES);
+                    const int steps = min(4, (p.r - kb * BK + 15) / 16);
+                    if (elect_one()) {
+                        for (int kk = 0; kk < steps; ++kk) {
+                            mma_bf16(tmem + (d & 1) * BN, hi + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), (kb | kk) != 0);
+                            mma_bf16(tmem + (d & 1) * BN, lo + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), 1);
+                        }
+                        mma_commit(bempty0 + 8 * bs);
+                        if (kb == nb - 1) mma_commit(dfull0 + 8 * (d & 1));
+                    }
+                    __syncwarp();
+                    if (++bs == (uint32_t)p.stages) {
+                        bs = 0;
+                        bph ^= 1u;
+                    }
+                }
+            }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 65);
+            abort_flag = 1;
+        }
+        if (elect_one()) mma_commit(drain);
+        mbar_wait(drain, 0, DRAIN_NS);
+        __syncwarp();
+    } else {
+        const int q4 = warp & 3, half = (warp - 2) >> 2;  // lane quarter, which 64 columns
+        const int row = q4 * 32 + lane, slot = tl.slot[row];
+        pdl_wait();
+        pdl_trigger();
+        if (tl.count) {
+            // this row's T (its pieces of 8, every second one), then zeros up to a multiple of 16
+            const int pieces = (p.r + 15) / 16 * 2;
+            const float* src = p.part + (size_t)(m0 + row) * p.r;
+            const float scale = slot >= 0 && p.scale ? p.scale[tl.id[row]] : 1.f;
+            for (int c = half; c < pieces; c += 2) {
+                float v[8] = {};
+                if (slot >= 0 && 8 * c < p.r) {
+                    for (int z = 0; z < p.splits; ++z) {
+                        const float4* q = reinterpret_cast<const float4*>(src + (size_t)z * p.m * p.r + 8 * c);
+                        const float4 f = q[0], g = q[1];
+                        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+                        v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
+                    }
+                }
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = v[2 * i] * scale, b = v[2 * i + 1] * scale;
+                    hi[i] = pack_bf16x2(a, b);
+                    const float ah = bf16lo(hi[i]), bh = bf16hi(hi[i]);
+                    // an infinite first part is all there is of it
+                    lo[i] = pack_bf16x2(isinf(ah) ? 0.f : a - ah, isinf(bh) ? 0.f : b - bh);
+                }
+                const uint32_t at = t_at + (c >> 3) * X_BYTES + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                sts128(at + nb * X_BYTES, lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tready);
+        }
+        uint32_t ys = 0, yph = 0, d = 0;
+        int before = -1;  // the stage whose stores are still being read
+        bool ok = true;
+        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
+            if (warp_sees(&abort_flag) || !warp_wait(yfull0 + 8 * ys, yph, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            const int col = nt * BN + 64 * half;
+            const uint32_t box = y_at + ys * Y_BYTES + half * X_BYTES, line = box + row * 128;
+            for (int u = 0; u < tl.count; ++u, ++d) {
+                if (!warp_wait(dfull0 + 8 * (d & 1), (d >> 1) & 1u, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const bool own = slot == u, any = __any_sync(0xffffffffu, own);
+                uint32_t v[2][32];
+                if (any) {
+                    const uint32_t taddr = tmem + ((uint32_t)(q4 * 32) << 16) + (d & 1) * BN + 64 * half;
+                    tmem_ld32(taddr, v[0]);
+                    tmem_ld32(taddr + 32, v[1]);
+                    tmem_wait_ld();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dempty0 + 8 * (d & 1));
+                if (own && col < p.N) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t at = line + ((c ^ (row & 7)) << 4);
+                        const uint4 q = lds128(at);
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = pack_bf16x2(bf16lo(w[i]) + __uint_as_float(v[c >> 2][(8 * c + 2 * i) & 31]),
+                                               bf16hi(w[i]) + __uint_as_float(v[c >> 2][(8 * c + 2 * i + 1) & 31]));
+                        sts128(at, o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            if (!ok) break;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (col < p.N && m0 + q4 * 32 < p.m) {
+                    tma_store_3d(&p.mo, col / 2, m0 + q4 * 32, 0, box + q4 * 4096);
+                    tma_store_wait_read_but1();
+                } else {
+                    tma_store_wait_read();
+                }
+                // this thread's store of the stage before, if there was one, has been read
+                if (before >= 0) mbar_arrive(yempty0 + 8 * before);
+            }
+            before = (int)ys;
+            if (++ys == Y_STAGES) {
+                ys = 0;
+                yph ^= 1u;
+            }
+        }
+        if (!ok && lane == 0) {
+            set_error(p.hdr, DEV_ERR_TIMEOUT, 66);
+            abort_flag = 1;
+        }
+        if (lane == 0) tma_store_wait();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+int sms() {
+    static int n = device_sm_count();
+    return n;
+}
+
+constexpr int kSmem = 225 * 1024;  // beside the static part (tile lists, barriers)
+
+// Slices of K: as many as fill the device, of at least 4 blocks of 64.
+int split_blocks(int64_t m, int64_t K) {
+    const int tiles = (int)std::min<int64_t>((m + BM - 1) / BM, 1 << 20), kblocks = (int)((K + BK - 1) / BK);
+    const int splits = std::max(1, std::min(sms() / tiles, kblocks / 4));
+    return ceil_div(kblocks, splits);
+}
+
+}  // namespace
+
+// Slices times tokens: tiles * splits is at most the SMs while there are splits.
+int64_t lora_part_floats(int64_t m, int64_t r) {
+    if (m <= kLoraByToken) return 0;
+    return std::max<int64_t>(m, (int64_t)sms() * BM) * r;
+}
+
+cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
+    const int tiles = ceil_div(p.m, BM);
+    p.kblocks = ceil_div(p.K, BK);
+    p.split_blocks = split_blocks(p.m, p.K);
+    p.splits = ceil_div(p.kblocks, p.split_blocks);
+    p.group = std::min(std::min(256 / p.r, p.n), BM);
+    p.a_bytes = ceil_div(p.group * p.r, 16) * 16 * BK * 2;  // the MMA's N is a multiple of 16
+    const uint64_t bdims[3] = {(uint64_t)p.r / 2, (uint64_t)p.N, (uint64_t)p.n};
+    const uint64_t bstrides[2] = {(uint64_t)p.r * 2, (uint64_t)p.N * p.r * 2};
+    const uint32_t bbox[3] = {BK / 2, BN, 1};
+    if (!ffn_map(&p.mx, p.x, p.m, p.K, p.ldx, BM) || !ffn_map(&p.ma, p.a, (uint64_t)p.n * p.r, p.K, p.K, p.r) ||
+        !tmap_encode_words(&p.mb, p.b, 3, bdims, bstrides, bbox) || !ffn_map(&p.my, p.y, p.m, p.N, p.ldy, BM) ||
+        !ffn_map(&p.mo, p.out, p.m, p.N, p.ldo, 32))
+        return cudaErrorUnknown;
+    cudaError_t e = allow_smem<lora_shrink>(kSmem);
+    if (e == cudaSuccess) e = allow_smem<lora_expand>(kSmem);
+    if (e != cudaSuccess) return e;
+    p.stages = std::min(8, (kSmem - 1024) / (X_BYTES + p.a_bytes));
+    e = launch_pdl(lora_shrink, dim3(tiles, p.splits), dim3(SHRINK_THREADS), 1024 + p.stages * (X_BYTES + p.a_bytes), st, p);
+    if (e != cudaSuccess) return e;
+    const int nb = ceil_div(p.r, BK);
+    p.n_tiles = ceil_div(p.N, BN);
+    p.n_ctas = std::max(1, std::min(p.n_tiles, sms() / tiles));
+    p.stages = std::min(MAX_B, (kSmem - 1024 - 2 * nb * X_BYTES - Y_STAGES * Y_BYTES) / X_BYTES);
+    return launch_pdl(lora_expand, dim3(tiles, p.n_ctas), dim3(EXPAND_THREADS),
+                      1024 + 2 * nb * X_BYTES + Y_STAGES * Y_BYTES + p.stages * X_BYTES, st, p);
+}
+
+}  // namespace moe

@@ -1,0 +1,223 @@
+// C-ABI of the operators around the layer and the block: argument checks and
+// launches.  Declarations and contracts: include/moe_ffn_ops.h.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "moe_ffn_ops.h"
+#include "ops.h"
+
+using namespace moe;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: limit of every bounded mbarrier wait
+constexpr int64_t kMaxRows = INT32_MAX / 64;
+
+inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// bf16 rows of n elements, ld apart
+bool bad_rows(const void* p, int64_t ld, int64_t n) {
+    return !p || !aligned(p, 16) || ld < n || ld % 8 || ld > (int64_t)1 << 38;
+}
+bool bad_words(const void* p) { return !p || !aligned(p, 4); }
+int check_norm(int64_t m, int64_t h) {
+    if (m < 0 || h <= 0 || h % 8) return MOE_ERR_INVALID_ARG;
+    return m > kMaxRows || h > kNormMaxH ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+int check_router(int64_t m, int32_t e, int32_t k, const int32_t* off, int64_t seqs, int scoring) {
+    if (m < 0 || e <= 0 || k <= 0 || k > e || seqs <= 0 || (!off && seqs != 1)) return MOE_ERR_INVALID_ARG;
+    if (scoring != MOE_SCORING_SOFTMAX && scoring != MOE_SCORING_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (off && !aligned(off, 4)) return MOE_ERR_INVALID_ARG;
+    return e > kMaxExperts || k > kMaxTopK || m > kMaxRows || seqs > 1 << 24 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+int status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+int moe_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t m, int64_t h,
+                    const float* weight, float eps, void* residual_out, int64_t ldo, void* out, uint8_t* codes,
+                    float* scales, void* stream) {
+    const int rc = check_norm(m, h);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (bad_rows(x, ldx, h) || !weight || !aligned(weight, 16) || !(eps >= 0.f) || !std::isfinite(eps))
+        return MOE_ERR_INVALID_ARG;
+    if (residual ? bad_rows(residual, ldr, h) || bad_rows(residual_out, ldo, h) || (residual_out == residual && ldo != ldr)
+                 : residual_out != nullptr)
+        return MOE_ERR_INVALID_ARG;
+    if ((!out && !codes) || (codes != nullptr) != (scales != nullptr)) return MOE_ERR_INVALID_ARG;
+    if ((out && (!aligned(out, 16) || (out == x && ldx != h))) || (codes && (!aligned(codes, 16) || !aligned(scales, 4))))
+        return MOE_ERR_INVALID_ARG;
+    NormArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.res = static_cast<const uint16_t*>(residual);
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldo = ldo;
+    a.w = weight;
+    a.eps = eps;
+    a.res_out = static_cast<uint16_t*>(residual_out);
+    a.out = static_cast<uint16_t*>(out);
+    a.codes = codes;
+    a.scales = scales;
+    a.m = (int)m;
+    a.H = (int)h;
+    return status(launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_add_rmsnorm_backward_workspace_size(int64_t m, int64_t h, size_t* bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const int rc = check_norm(m, h);
+    if (rc == MOE_OK) *bytes = align_up((size_t)norm_grad_blocks((int)m, (int)h) * h * 4);
+    return rc;
+}
+
+int moe_add_rmsnorm_backward(const void* dout, int64_t ldd, const void* r, int64_t ldr, int64_t m, int64_t h,
+                             const float* weight, float eps, const void* dresidual, int64_t ldq, void* dx,
+                             float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+    size_t need = 0;
+    const int rc = moe_add_rmsnorm_backward_workspace_size(m, h, &need);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (bad_rows(dout, ldd, h) || bad_rows(r, ldr, h) || !weight || !aligned(weight, 16) || !(eps >= 0.f) ||
+        !std::isfinite(eps) || (dresidual && bad_rows(dresidual, ldq, h)) || !dx || !aligned(dx, 16))
+        return MOE_ERR_INVALID_ARG;
+    if ((dx == dout && ldd != h) || (dx == dresidual && ldq != h) || dx == r) return MOE_ERR_INVALID_ARG;
+    if (dweight) {
+        if (!aligned(dweight, 4) || !workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    }
+    NormGradArgs a{};
+    a.dout = static_cast<const uint16_t*>(dout);
+    a.r = static_cast<const uint16_t*>(r);
+    a.dres = static_cast<const uint16_t*>(dresidual);
+    a.ldd = ldd;
+    a.ldr = ldr;
+    a.ldq = ldq;
+    a.w = weight;
+    a.eps = eps;
+    a.dx = static_cast<uint16_t*>(dx);
+    a.dw = dweight;
+    a.part = static_cast<float*>(workspace);
+    a.m = (int)m;
+    a.H = (int)h;
+    return status(launch_add_rmsnorm_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_balance_loss_workspace_size(int64_t m, int64_t seqs, size_t* bytes) {
+    if (m < 0 || seqs <= 0 || !bytes) return MOE_ERR_INVALID_ARG;
+    if (m > kMaxRows || seqs > 1 << 24) return MOE_ERR_UNSUPPORTED;
+    *bytes = align_up((size_t)seqs * 4) + align_up((size_t)balance_slots(m, seqs) * 8);
+    return MOE_OK;
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, int64_t m, int32_t e, int32_t k,
+                     const int32_t* seq_offsets, int64_t seqs, int scoring, float* balance, float* z, int32_t* counts,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    const int rc = check_router(m, e, k, seq_offsets, seqs, scoring);
+    if (rc != MOE_OK || m == 0) return rc;
+    if (bad_words(logits) || bad_words(topk_ids) || bad_words(balance) || bad_words(z) || bad_words(counts) || !workspace ||
+        !aligned(workspace, kAlign))
+        return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    moe_balance_loss_workspace_size(m, seqs, &need);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    RouterArgs a{};
+    a.logits = logits;
+    a.ids = topk_ids;
+    a.off = seq_offsets;
+    a.m = (int)m;
+    a.E = e;
+    a.k = k;
+    a.S = (int)seqs;
+    a.sigmoid = scoring == MOE_SCORING_SIGMOID;
+    a.counts = counts;
+    a.balance = balance;
+    a.z = z;
+    a.ticket = static_cast<int*>(workspace);
+    a.part = reinterpret_cast<float2*>(static_cast<char*>(workspace) + align_up((size_t)seqs * 4));
+    return status(launch_balance_loss(a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_route_backward(const float* logits, const int32_t* topk_ids, int64_t m, int32_t e, int32_t k, int scoring,
+                       int norm_topk_prob, float routed_scaling_factor, const float* dtopk_w,
+                       const int32_t* seq_offsets, int64_t seqs, const int32_t* counts, const float* dbalance,
+                       const float* dz, float* dlogits, void* stream) {
+    const int rc = check_router(m, e, k, seq_offsets, seqs, scoring);
+    if (rc != MOE_OK) return rc;
+    if (scoring == MOE_SCORING_SIGMOID && ((norm_topk_prob != 0 && norm_topk_prob != 1) || !(routed_scaling_factor > 0.f) ||
+                                           !std::isfinite(routed_scaling_factor)))
+        return MOE_ERR_INVALID_ARG;
+    if (m == 0) return MOE_OK;
+    if (bad_words(logits) || bad_words(topk_ids) || bad_words(dlogits) || dlogits == logits || !aligned(dtopk_w, 4) ||
+        !aligned(counts, 4) || !aligned(dbalance, 4) || !aligned(dz, 4) || (dbalance && !counts))
+        return MOE_ERR_INVALID_ARG;
+    RouterArgs a{};
+    a.logits = logits;
+    a.ids = topk_ids;
+    a.off = seq_offsets;
+    a.m = (int)m;
+    a.E = e;
+    a.k = k;
+    a.S = (int)seqs;
+    a.sigmoid = scoring == MOE_SCORING_SIGMOID;
+    a.counts = const_cast<int32_t*>(counts);  // only read
+    a.dtopk_w = dtopk_w;
+    a.dbalance = dbalance;
+    a.dz = dz;
+    a.norm = norm_topk_prob;
+    a.scale = a.sigmoid ? routed_scaling_factor : 1.f;
+    a.dlogits = dlogits;
+    return status(launch_route_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_lora_add_workspace_size(int64_t m, int64_t k, int64_t r, size_t* bytes) {
+    if (m < 0 || k <= 0 || k % 8 || r <= 0 || r % 8 || !bytes) return MOE_ERR_INVALID_ARG;
+    if (m > kMaxRows || k > 1 << 20 || r > kLoraMaxRank) return MOE_ERR_UNSUPPORTED;
+    *bytes = align_up(sizeof(WsHeader)) + align_up((size_t)lora_part_floats(m, r) * 4);
+    return MOE_OK;
+}
+
+int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y, int64_t ldy, int64_t d, const void* a,
+                 const void* b, int64_t n, int64_t r, const int32_t* ids, const float* scale, void* out, int64_t ldo,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    size_t need = 0;
+    const int rc = moe_lora_add_workspace_size(m, k, r, &need);
+    if (rc != MOE_OK) return rc;
+    if (d <= 0 || d % 8 || n <= 0) return MOE_ERR_INVALID_ARG;
+    if (d > 1 << 20 || n > (1 << 30) / r) return MOE_ERR_UNSUPPORTED;
+    if (m == 0) return MOE_OK;
+    if (bad_rows(x, ldx, k) || bad_rows(y, ldy, d) || bad_rows(out, ldo, d) || (out == y && ldo != ldy) || out == x || !a ||
+        !b || !aligned(a, 16) || !aligned(b, 16) || bad_words(ids) || !aligned(scale, 4) || !workspace ||
+        !aligned(workspace, kAlign))
+        return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+    LoraArgs p{};
+    p.x = static_cast<const uint16_t*>(x);
+    p.y = static_cast<const uint16_t*>(y);
+    p.a = static_cast<const uint16_t*>(a);
+    p.b = static_cast<const uint16_t*>(b);
+    p.out = static_cast<uint16_t*>(out);
+    p.scale = scale;
+    p.ids = ids;
+    p.ldx = ldx;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.m = (int)m;
+    p.K = (int)k;
+    p.N = (int)d;
+    p.r = (int)r;
+    p.n = (int)n;
+    p.hdr = static_cast<WsHeader*>(workspace);
+    p.wait_ns = kWaitNs;
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align_up(sizeof(WsHeader)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return status(p.m <= kLoraByToken ? launch_lora_tokens(p, st) : launch_lora_tiles(p, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,531 @@
+// Losses that keep a router's experts in use, and the gradient of its logits.
+//
+// For a sequence s of T tokens, c[s, e] the pairs (token, pick) of expert e, and
+// p[t, e] the token's normalised scores -- softmax(l), or sigma(l) over their sum
+// -- with k picks a token and E experts:
+//   balance[s] = E sum_e (c[s, e] / (k T)) (sum_t p[t, e] / T)
+//              = E / (k T^2) sum_t q[t],  q[t] = sum_e c[s, e] p[t, e]
+//   z[s] = 1 / T sum_t lse(l[t])^2,  lse the logarithm of the sum of exponentials
+// The second form of balance needs the counts first and then one number of each
+// token, so that no sums over tokens are kept per expert.  The counts come from the
+// ids alone, 4 k bytes a token; the logits are read once.
+// Gradients, with G[e] = dbalance[s] E / (k T^2) (c[s, e] - k T / E) -- the constant
+// changes nothing, the p of a token add up to one, and takes out of the difference
+// below what all experts have in common --
+//   softmax: p (G - sum p G)     sigmoid: p (1 - sigma) (G - sum p G)
+//   z: dz[s] / T 2 lse softmax(l)
+// and of the routing weights w[t, j] of the picks, given dw:
+//   softmax over the picks: w_j (dw_j - sum w dw)
+//   sigmoid, renormalised: with u = sigma_j / sum sigma, scale u_j (1 - sigma_j) (dw_j - sum u dw)
+//   sigmoid alone: scale sigma_j (1 - sigma_j) dw_j
+// Picks that name the same expert add up, in their order.  A token whose logits are
+// all -inf has p = 0 and no part in z.
+//
+// A token belongs to G lanes of a warp, which hold its E logits in registers.
+// Deterministic: integer counts, and sums in the order of the tokens of a chunk,
+// then of the chunks; whichever block finishes a sequence last adds its chunks up.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "ops.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxChunk = 128;   // tokens of a block
+constexpr int kMinChunk = 8;     // ... at least: what one round of 32-lane groups takes
+constexpr int kOffsShared = 512; // sequences whose offsets a block keeps in shared memory
+
+// The tokens of sequence s, within [0, m] whatever the offsets hold.
+__device__ __forceinline__ void span(const RouterArgs& a, int s, int& t0, int& t1) {
+    t0 = 0;
+    t1 = a.m;
+    if (a.off) {
+        t0 = min(max(a.off[s], 0), a.m);
+        t1 = min(max(a.off[s + 1], t0), a.m);
+    }
+}
+
+// Counts of a sequence's pairs: a cluster per sequence (or a block alone, where
+// sequences are many), a histogram in each block's shared memory, added up through
+// distributed shared memory.  Nothing has to be zeroed before and no atomics reach
+// global memory.  It also opens the losses' tickets.
+__global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a, int cluster) {
+    __shared__ int hist[kMaxExperts];
+    const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    int t0, t1;
+    span(a, s, t0, t1);
+    const int64_t end = (int64_t)t1 * a.k, step = (int64_t)cluster * kThreads;
+    int64_t p = (int64_t)t0 * a.k + rank * kThreads + threadIdx.x;
+    for (; p + 3 * step < end; p += 4 * step) {
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = a.ids[p + i * step];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((unsigned)id[i] < (unsigned)a.E) atomicAdd(&hist[id[i]], 1);
+    }
+    for (; p < end; p += step) {
+        const int id = a.ids[p];
+        if ((unsigned)id < (unsigned)a.E) atomicAdd(&hist[id], 1);
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        a.ticket[s] = 0;
+        if (t0 == t1) a.balance[s] = a.z[s] = 0.f;
+    }
+    __syncthreads();
+    if (cluster > 1) sm100::cluster_sync();
+    const uint32_t h = sm100::smem_u32(hist);
+    for (int e = rank * kThreads + threadIdx.x; e < a.E; e += cluster * kThreads) {
+        int n = 0;
+        if (cluster > 1) {
+            for (int c = 0; c < cluster; ++c) {
+                int v;
+                asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(sm100::mapa(h + 4 * e, c)) : "memory");
+                n += v;
+            }
+        } else {
+            n = hist[e];
+        }
+        a.counts[(size_t)s * a.E + e] = n;
+    }
+    if (cluster > 1) sm100::cluster_sync();  // the others may still read this block's histogram
+}
+
+// Sums and maxima over the G lanes of a token.
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// sigma(l) and 1 - sigma(l), neither by a difference.
+__device__ __forceinline__ void logistic(float l, float& s, float& rest) {
+    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e), small = e * big;
+    s = l >= 0.f ? big : small;
+    rest = l >= 0.f ? small : big;
+}
+// sigma(l) / exp(shift), shift = min(0, the largest l): sums of them do not underflow where all
+// l are far below zero.
+__device__ __forceinline__ float shifted_logistic(float l, float shift) {
+    const float e = expf(-fabsf(l));
+    return (l >= 0.f ? 1.f : shift == 0.f ? e : expf(l - shift)) / (1.0f + e);
+}
+
+// A token's values over its lanes: value n * VEC + j of lane i is that of expert
+// (i + G n) VEC + j.
+template <int G, int VEC, int NV>
+struct Row {
+    float v[NV * VEC];
+    __device__ __forceinline__ void load(const float* row, int i, int E, bool live, float none) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int e = (i + G * n) * VEC;
+            if (VEC == 4) {
+                const float4 q = live && e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(none, none, none, none);
+                v[n * VEC] = q.x;
+                v[n * VEC + VEC / 4] = q.y;
+                v[n * VEC + VEC / 2] = q.z;
+                v[n * VEC + VEC - 1] = q.w;
+            } else {
+                v[n * VEC] = live && e < E ? row[e] : none;
+            }
+        }
+    }
+    __device__ __forceinline__ void load_counts(const int32_t* row, int i, int E, bool live) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int e = (i + G * n) * VEC;
+            if (VEC == 4) {
+                const int4 q = live && e < E ? *reinterpret_cast<const int4*>(row + e) : make_int4(0, 0, 0, 0);
+                v[n * VEC] = (float)q.x;
+                v[n * VEC + VEC / 4] = (float)q.y;
+                v[n * VEC + VEC / 2] = (float)q.z;
+                v[n * VEC + VEC - 1] = (float)q.w;
+            } else {
+                v[n * VEC] = live && e < E ? (float)row[e] : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float* row, int i, int E) const {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int e = (i + G * n) * VEC;
+            if (e >= E) continue;
+            if (VEC == 4)
+                *reinterpret_cast<float4*>(row + e) =
+                    make_float4(v[n * VEC], v[n * VEC + VEC / 4], v[n * VEC + VEC / 2], v[n * VEC + VEC - 1]);
+            else
+                row[e] = v[n * VEC];
+        }
+    }
+};
+
+// The sequence of each token of the block's chunk, -1 outside of all.
+struct Chunk {
+    int seq[kMaxChunk];
+    int off[kOffsShared + 1];
+};
+__device__ __forceinline__ void find_sequences(const RouterArgs& a, int first, Chunk& ch) {
+    const bool kept = a.off && a.S <= kOffsShared;
+    if (kept)
+        for (int i = threadIdx.x; i <= a.S; i += kThreads) ch.off[i] = a.off[i];
+    __syncthreads();
+    if ((int)threadIdx.x < a.chunk) {
+        const int t = first + threadIdx.x;
+        int s = t < a.m ? 0 : -1;
+        if (a.off && t < a.m) {
+            const int* off = kept ? ch.off : a.off;
+            int lo = 0, hi = a.S;  // the first s whose end is past t, S: none
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (off[mid + 1] > t)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+            s = lo < a.S && off[lo] <= t ? lo : -1;
+        }
+        ch.seq[threadIdx.x] = s;
+    }
+    __syncthreads();
+}
+
+// The losses.  A block takes a chunk of tokens; then a warp for each sequence that
+// the chunk holds tokens of adds up theirs, and the warp that is the sequence's last
+// adds up the chunks.  Chunk c and sequence s meet at slot c + s, which no other
+// meeting has: along them c or s rises from one to the next and neither falls.
+template <int G, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
+    __shared__ Chunk ch;
+    __shared__ float2 each[kMaxChunk];
+    pdl_wait();
+    pdl_trigger();
+    const int first = blockIdx.x * a.chunk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    find_sequences(a, first, ch);
+    const int i = threadIdx.x % G, group = threadIdx.x / G;
+    constexpr int GROUPS = kThreads / G;
+    for (int r = 0; r < a.chunk; r += GROUPS) {  // warps stay together
+        const int j = r + group, s = j < a.chunk ? ch.seq[j] : -1;
+        Row<G, VEC, NV> l, c;
+        l.load(a.logits + (size_t)(first + j) * a.E, i, a.E, s >= 0, -INFINITY);
+        c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
+        top = group_max<G>(top);
+        const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+        float sum = 0.f, den = 0.f, q = 0.f;
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) {
+            const float e = expf(l.v[n] - at);
+            const float p = a.sigmoid ? shifted_logistic(l.v[n], shift) : e;
+            sum += e;
+            den += p;
+            q = fmaf(p, c.v[n], q);
+        }
+        sum = group_sum<G>(sum);
+        den = a.sigmoid ? group_sum<G>(den) : sum;
+        q = group_sum<G>(q);
+        const float lse = at + logf(sum);
+        if (i == 0 && j < a.chunk)
+            each[j] = s < 0 ? make_float2(0.f, 0.f) : make_float2(den == 0.f ? 0.f : q / den, sum == 0.f ? 0.f : lse * lse);
+    }
+    __syncthreads();
+    const int last = min(first + a.chunk, a.m);
+    // the sequences of the chunk's first and last tokens that are in any
+    int s0 = a.S, s1 = -1;
+    for (int j = lane; j < last - first; j += 32) {
+        const int s = ch.seq[j];
+        if (s >= 0) {
+            s0 = min(s0, s);
+            s1 = max(s1, s);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s0 = min(s0, __shfl_xor_sync(0xffffffffu, s0, o));
+        s1 = max(s1, __shfl_xor_sync(0xffffffffu, s1, o));
+    }
+    for (int s = s0 + warp; s <= s1; s += kThreads / 32) {
+        int t0, t1;
+        span(a, s, t0, t1);
+        const int from = max(t0, first), to = min(t1, last);
+        if (from >= to) continue;
+        float q = 0.f, z = 0.f;
+        for (int t = from + lane; t < to; t += 32) {
+            q += each[t - first].x;
+            z += each[t - first].y;
+        }
+        q = warp_sum(q);
+        z = warp_sum(z);
+        const int c0 = t0 / a.chunk, c1 = (t1 - 1) / a.chunk;
+        int done = 0;
+        if (lane == 0) {
+            a.part[blockIdx.x + s] = make_float2(q, z);
+            __threadfence();
+            done = atomicAdd(&a.ticket[s], 1) == c1 - c0;
+            __threadfence();
+        }
+        if (!__shfl_sync(0xffffffffu, done, 0)) continue;
+        __syncwarp();  // the other lanes' reads come after lane 0's
+        double qs = 0.0, zs = 0.0;
+        for (int c = c0 + lane; c <= c1; c += 32) {
+            const float2 v = __ldcg(&a.part[c + s]);
+            qs += (double)v.x;
+            zs += (double)v.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            qs += __shfl_xor_sync(0xffffffffu, qs, o);
+            zs += __shfl_xor_sync(0xffffffffu, zs, o);
+        }
+        if (lane == 0) {
+            const double T = (double)(t1 - t0);
+            a.balance[s] = (float)(qs * a.E / ((double)a.k * T * T));
+            a.z[s] = (float)(zs / T);
+        }
+    }
+}
+
+// The gradient of the logits: of the routing weights, and of the losses for tokens
+// of sequences.  Pick j of a token is lane j % G's, its number j / G there.
+template <int G, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
+    __shared__ Chunk ch;
+    pdl_wait();
+    pdl_trigger();
+    const int first = blockIdx.x * a.chunk;
+    const bool losses = a.dbalance || a.dz;
+    if (losses) find_sequences(a, first, ch);
+    const int i = threadIdx.x % G, group = threadIdx.x / G;
+    constexpr int GROUPS = kThreads / G;
+    constexpr int PICKS = G == 32 ? 1 : 4;  // k <= min(E, 32), and G < 32 only where E <= 4 G
+    for (int r = 0; r < a.chunk; r += GROUPS) {
+        const int j = r + group, t = first + j;
+        const bool live = j < a.chunk && t < a.m;
+        const int s = losses && live ? ch.seq[j] : -1;
+        const float* row = a.logits + (size_t)t * a.E;
+        Row<G, VEC, NV> l;
+        l.load(row, i, a.E, live, -INFINITY);
+        // the picks: their expert, their gradient
+        int id[PICKS];
+        float dk[PICKS];
+        if (a.dtopk_w) {
+            float lk[PICKS], top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                const int pick = n * G + i;
+                const bool in = live && pick < a.k;
+                const int e = in ? a.ids[(size_t)t * a.k + pick] : -1;
+                id[n] = (unsigned)e < (unsigned)a.E ? e : -1;
+                dk[n] = id[n] >= 0 ? a.dtopk_w[(size_t)t * a.k + pick] : 0.f;
+                lk[n] = id[n] >= 0 ? row[id[n]] : -INFINITY;
+                top = fmaxf(top, lk[n]);
+            }
+            top = group_max<G>(top);
+            const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+            float w[PICKS], sum = 0.f, mean = 0.f;
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                w[n] = a.sigmoid ? shifted_logistic(lk[n], shift) : expf(lk[n] - at);
+                sum += w[n];
+            }
+            sum = group_sum<G>(sum);
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                w[n] = sum == 0.f ? 0.f : w[n] / sum;
+                mean = fmaf(w[n], dk[n], mean);
+            }
+            mean = group_sum<G>(mean);
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                if (a.sigmoid) {
+                    float sg, rest;
+                    logistic(lk[n], sg, rest);
+                    dk[n] = a.scale * rest * (a.norm ? w[n] * (dk[n] - mean) : sg * dk[n]);
+                } else {
+                    dk[n] = w[n] * (dk[n] - mean);
+                }
+            }
+        }
+        Row<G, VEC, NV> d;
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
+        if (losses) {
+            int t0 = 0, t1 = 1;
+            if (s >= 0) span(a, s, t0, t1);
+            const float T = (float)max(t1 - t0, 1);
+            const float db = s >= 0 && a.dbalance ? a.dbalance[s] * (float)a.E / ((float)a.k * T) / T : 0.f;
+            const float dz = s >= 0 && a.dz ? a.dz[s] / T : 0.f;
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
+            top = group_max<G>(top);
+            const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+            float sum = 0.f;
+            Row<G, VEC, NV> p;
+#pragma unroll
+            for (int n = 0; n < NV * VEC; ++n) {
+                p.v[n] = expf(l.v[n] - at);
+                sum += p.v[n];
+            }
+            sum = group_sum<G>(sum);
+            const float soft = sum == 0.f ? 0.f : 1.0f / sum;
+            const float zc = a.dz ? dz * 2.f * (sum == 0.f ? 0.f : at + logf(sum)) * soft : 0.f;
+#pragma unroll
+            for (int n = 0; n < NV * VEC; ++n) d.v[n] = zc * p.v[n];
+            if (a.dbalance) {
+                float den = 0.f, inv = soft, mean = 0.f;
+                if (a.sigmoid) {
+#pragma unroll
+                    for (int n = 0; n < NV * VEC; ++n) {
+                        p.v[n] = shifted_logistic(l.v[n], shift);
+                        den += p.v[n];
+                    }
+                    den = group_sum<G>(den);
+                    inv = den == 0.f ? 0.f : 1.0f / den;
+                }
+                Row<G, VEC, NV> c;
+                c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
+                const float even = (float)a.k * T / (float)a.E;
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) {
+                    p.v[n] *= inv;
+                    c.v[n] -= even;
+                    mean = fmaf(p.v[n], c.v[n], mean);
+                }
+                mean = group_sum<G>(mean);
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) {
+                    float g = db * p.v[n] * (c.v[n] - mean);
+                    if (a.sigmoid) {
+                        float sg, rest;
+                        logistic(l.v[n], sg, rest);
+                        g *= rest;
+                    }
+                    d.v[n] += g;
+                }
+            }
+            if (s < 0) {  // padding, whatever its logits hold
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
+            }
+        }
+        if (a.dtopk_w) {
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                for (int q = 0; q < G && n * G + q < a.k; ++q) {
+                    const int e = __shfl_sync(0xffffffffu, id[n], q, G);
+                    const float g = __shfl_sync(0xffffffffu, dk[n], q, G);
+                    const int piece = e / VEC;
+                    const int pos = e >= 0 && piece % G == i ? piece / G * VEC + e % VEC : -1;
+#pragma unroll
+                    for (int v = 0; v < NV * VEC; ++v)
+                        if (v == pos) d.v[v] += g;
+                }
+            }
+        }
+        if (live) d.store(a.dlogits + (size_t)t * a.E, i, a.E);
+    }
+}
+
+int sms() {
+    static int n = device_sm_count();
+    return n;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// Lanes and registers by E: the fewest lanes (of 2 to 32) whose one piece of 4
+// experts each cover E, then more pieces a lane.  Rows that are not all 16-byte
+// aligned go by single values, a warp each (8 lanes up to 8 experts).
+template <class F>
+cudaError_t by_width(int E, bool wide, F&& f) {
+    if (wide) {
+        if (E <= 8) return f(Int<2>(), Int<4>(), Int<1>());
+        if (E <= 16) return f(Int<4>(), Int<4>(), Int<1>());
+        if (E <= 32) return f(Int<8>(), Int<4>(), Int<1>());
+        if (E <= 64) return f(Int<16>(), Int<4>(), Int<1>());
+        if (E <= 128) return f(Int<32>(), Int<4>(), Int<1>());
+        if (E <= 256) return f(Int<32>(), Int<4>(), Int<2>());
+        if (E <= 512) return f(Int<32>(), Int<4>(), Int<4>());
+        return f(Int<32>(), Int<4>(), Int<8>());
+    }
+    if (E <= 8) return f(Int<8>(), Int<1>(), Int<1>());
+    if (E <= 32) return f(Int<32>(), Int<1>(), Int<1>());
+    if (E <= 64) return f(Int<32>(), Int<1>(), Int<2>());
+    if (E <= 128) return f(Int<32>(), Int<1>(), Int<4>());
+    if (E <= 256) return f(Int<32>(), Int<1>(), Int<8>());
+    if (E <= 512) return f(Int<32>(), Int<1>(), Int<16>());
+    return f(Int<32>(), Int<1>(), Int<32>());
+}
+
+// Tokens of a block: what spreads them over the device four blocks to an SM, in
+// whole rounds of the block's groups.
+int chunk_for(int m, int groups) {
+    const int even = ceil_div(m, 4 * sms());
+    return std::min(kMaxChunk, std::max(kMinChunk, ceil_div(even, groups) * groups));
+}
+
+}  // namespace
+
+// Chunks of the losses and their meetings with sequences, at most.
+int64_t balance_slots(int64_t m, int64_t S) { return (m + kMinChunk - 1) / kMinChunk + S; }
+
+cudaError_t launch_balance_loss(RouterArgs a, cudaStream_t st) {
+    // a block counts 256 ids in a step; sequences that fill the device by themselves have one each
+    const int cluster = a.S >= sms() || (int64_t)a.m * a.k <= (int64_t)a.S * 4 * kThreads ? 1 : 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.S * cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, count_pairs, a, cluster);
+    if (e != cudaSuccess) return e;
+    return by_width(a.E, a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.counts), [&](auto g, auto vec, auto nv) {
+        a.chunk = chunk_for(a.m, kThreads / g);
+        return launch_pdl(balance_loss<g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), 0, st, (const RouterArgs)a);
+    });
+}
+
+cudaError_t launch_route_backward(RouterArgs a, cudaStream_t st) {
+    const bool wide = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits) && (!a.counts || aligned16(a.counts));
+    return by_width(a.E, wide, [&](auto g, auto vec, auto nv) {
+        a.chunk = chunk_for(a.m, kThreads / g);
+        return launch_pdl(route_backward<g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), 0, st, (const RouterArgs)a);
+    });
+}
+
+}  // namespace moe
