@@ -9,8 +9,9 @@
  * m == 0 launches nothing.  bf16 rows (and e4m3 codes) are 16-byte aligned with
  * strides in elements, multiples of 8 and at least the row; fp32 and int32
  * tensors are dense and aligned to their elements where nothing else is said.
- * Outputs share no memory with inputs but where it is said.  Up to 2^31 / 64
- * tokens.
+ * Outputs share no memory with inputs or with each other but where it is said
+ * (rows of one buffer whose columns do not meet share none); matrices that do are
+ * refused.  Up to 2^31 / 64 tokens.
  */
 #ifndef MOE_FFN_OPS_GB300_H
 #define MOE_FFN_OPS_GB300_H
@@ -107,6 +108,7 @@ MOE_API int moe_route_backward(const float* logits, const int32_t* topk_ids, int
  *   2^30.
  * workspace: moe_lora_add_workspace_size bytes, 256-byte aligned, its first 256
  * bytes (the header of moe_ffn.h) zero before its first use. */
+#define MOE_LORA_BY_TOKEN 64 /* up to so many tokens the header alone */
 MOE_API int moe_lora_add_workspace_size(int64_t m, int64_t k, int64_t r, size_t* bytes);
 MOE_API int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y, int64_t ldy, int64_t d,
                          const void* a, const void* b, int64_t n, int64_t r, const int32_t* ids, const float* scale,

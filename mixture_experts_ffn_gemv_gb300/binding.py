@@ -22,6 +22,7 @@ MOE_ACT_SILU, MOE_ACT_GELU_TANH = 0, 1
 ACTIVATIONS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU_TANH}
 MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
 MOE_ARM_AUTO, MOE_ARM_GEMV, MOE_ARM_GEMM = 0, 1, 2
+MOE_LORA_BY_TOKEN = 64  # up to so many tokens moe_lora_add needs no workspace but its header
 ARMS = {"auto": MOE_ARM_AUTO, "gemv": MOE_ARM_GEMV, "gemm": MOE_ARM_GEMM}
 
 EXPORTED = (
@@ -705,9 +706,10 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None, adapters=None, ada
         _need(codes.dim() == 2, "w: codes are [rows, n/2]")
         y = _empty((x.shape[0], codes.shape[0]), dtype=_BF16, device=x.device) if out is None else out
         _dense(y, _BF16, (x.shape[0], codes.shape[0]), "out")
-        add = _lora_call(y, x, a, b, adapter_ids, scale, None)  # all is checked before anything is launched
+        _lora_args(y, x, a, b, adapter_ids, scale, None, _device_of(x, "x"))  # refused before anything is launched
+        _need(x.data_ptr() != y.data_ptr(), "out: not x, where there are adapters")
         moe_mxfp4_linear(x, codes, scales, y)
-        return add()
+        return moe_lora_add(y, x, a, b, adapter_ids, scale)
     _need(adapter_ids is None, "adapter_ids without adapters")
     lib = _lib or load_library()
     n, k = _mx_matrix(codes, scales, "w")
@@ -907,29 +909,30 @@ class NormOut(NamedTuple):
     scales: torch.Tensor | None    # fp32 [m, ceil(h / 128)]
 
 
-def _share(a, b) -> bool:
-    """Whether two matrices of dense rows share memory: their spans meet and, where their rows are as
-    far apart, so do their columns."""
-    if a.numel() == 0 or b.numel() == 0:
-        return False
-    es, (m, n), (p, q) = a.element_size(), a.shape, b.shape
-    at, to = a.data_ptr(), b.data_ptr()
-    if at >= to + ((p - 1) * b.stride(0) + q) * es or to >= at + ((m - 1) * a.stride(0) + n) * es:
-        return False
-    pitch = a.stride(0) * es
-    if m == 1 or p == 1 or pitch != b.stride(0) * es:
-        return True
-    ahead = (to - at) % pitch  # of a's rows, b's columns begin
-    return ahead < n * es or ahead + q * es > pitch
+def _device_of(t, what: str) -> int:
+    """The device of a call by its first tensor: the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{what}: a device tensor")
+    if dev != _current_device():
+        _on(t)
+    return dev
 
 
-def _same(a, b) -> bool:
-    return a.data_ptr() == b.data_ptr() and a.shape == b.shape and (a.shape[0] <= 1 or a.stride() == b.stride())
+def _strided(t, n: int, rows: int, what: str) -> int:
+    """Checks a bf16 matrix [rows, n] on the current device as _rows does; returns its row stride.
+    Called where the common case, dense rows on that device, does not hold."""
+    ld = _rows(t, n, what)
+    _need(t.shape[0] == rows, f"{what}: {rows} rows, got {t.shape[0]}")
+    _on(t)
+    return ld
 
 
-def _vector(t, n: int, what: str):
-    _dense(t, _F32, (n,), what)
-    _need(t.data_ptr() % 16 == 0, f"{what}: 16-byte aligned")
+def _bad(t, dtype, shape, what: str):
+    """Words the refusal of a tensor that is not dense, of that type and shape and on the current device."""
+    _dense(t, dtype, shape, what)
+    _on(t)
+    raise ValueError(what)  # not reached: one of these refuses it
 
 
 def moe_add_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, out=None, bf16=True, fp8=False,
@@ -942,46 +945,46 @@ def moe_add_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, out=N
         with torch.cuda.stream(stream):
             return moe_add_rmsnorm(x, weight, eps, residual, residual_out, out, bf16, fp8)
     lib = _lib or load_library()
-    _need(x.dim() == 2, "x: [m, h]")
-    m, h = x.shape
-    ldx = _rows(x, h, "x")
-    _vector(weight, h, "weight")
-    _need(bf16 or fp8, "neither bf16 nor fp8 is asked for")
-    _need(out is None or bf16, "out: given, and bf16 not asked for")
-    st = _on(x, weight)
-    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x: [m, h]")
+    dev = _device_of(x, "x")
+    shape = m, h = x.shape
+    dense = x.is_contiguous() and x.dtype is _BF16 and x.get_device() == dev
+    ldx = h if dense else _strided(x, h, m, "x")
+    if not (weight.dtype is _F32 and weight.is_contiguous() and weight.shape == (h,) and weight.get_device() == dev):
+        _bad(weight, _F32, (h,), "weight")
     ldr = ldo = 0
+    res = res_out = to = codes_at = scales_at = codes = scales = None
     if residual is not None:
-        ldr = _rows(residual, h, "residual")
-        _need(residual.shape[0] == m, "x and residual differ in rows")
+        ldr = h
+        if not (residual.shape == shape and residual.is_contiguous() and residual.dtype is _BF16
+                and residual.get_device() == dev):
+            ldr = _strided(residual, h, m, "residual")
+        res = residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty((m, h), dtype=_BF16, device=dev)
+            residual_out = _empty_like(x, memory_format=_dense_rows)
             ldo = h
         else:
-            ldo = _rows(residual_out, h, "residual_out")
-            _need(residual_out.shape[0] == m, "x and residual_out differ in rows")
-            _need(not _share(residual_out, x) and (_same(residual_out, residual) or not _share(residual_out, residual)),
-                  "residual_out: residual itself, or memory of its own")
-        _on(residual, residual_out)
-    else:
-        _need(residual_out is None, "residual_out without a residual")
+            ldo = _strided(residual_out, h, m, "residual_out")
+        res_out = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
     if out is not None:
+        _need(bf16, "out: given, and bf16 not asked for")
         _dense(out, _BF16, (m, h), "out")
-        _need(out.data_ptr() % 16 == 0, "out: 16-byte aligned")
-        _need((_same(out, x) or not _share(out, x))
-              and not any(t is not None and _share(out, t) for t in (residual, residual_out)),
-              "out: x itself, or memory of its own")
         _on(out)
+        to = out.data_ptr()
     elif bf16:
-        out = _empty((m, h), dtype=_BF16, device=dev)
-    codes = scales = None
+        out = _empty_like(x, memory_format=_dense_rows)
+        to = out.data_ptr()
+    elif not fp8:
+        raise ValueError("neither bf16 nor fp8 is asked for")
     if fp8:
-        codes = _empty((m, h), dtype=_U8, device=dev)
-        scales = _empty((m, (h + 127) // 128), dtype=_F32, device=dev)
-    rc = lib.moe_add_rmsnorm(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, m, h,
-                             weight.data_ptr(), eps, None if residual is None else residual_out.data_ptr(), ldo,
-                             out.data_ptr() if bf16 else None, codes.data_ptr() if fp8 else None,
-                             scales.data_ptr() if fp8 else None, st)
+        codes = _empty((m, h), dtype=_U8, device=x.device)
+        scales = _empty((m, (h + 127) // 128), dtype=_F32, device=x.device)
+        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
+    rc = lib.moe_add_rmsnorm(x.data_ptr(), ldx, res, ldr, m, h, weight.data_ptr(), eps, res_out, ldo, to, codes_at,
+                             scales_at, _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_add_rmsnorm")
     return NormOut(out, residual_out, codes, scales)
@@ -995,52 +998,66 @@ def moe_add_rmsnorm_backward(dout, r, weight, eps=1e-6, dresidual=None, need_dw=
         with torch.cuda.stream(stream):
             return moe_add_rmsnorm_backward(dout, r, weight, eps, dresidual, need_dw)
     lib = _lib or load_library()
-    _need(r.dim() == 2, "r: [m, h]")
-    m, h = r.shape
-    ldd, ldr, ldq = _rows(dout, h, "dout"), _rows(r, h, "r"), 0
-    _need(dout.shape[0] == m, "dout and r differ in rows")
-    _vector(weight, h, "weight")
-    st = _on(dout, r, weight)
+    if r.dim() != 2:
+        raise ValueError("r: [m, h]")
+    dev = _device_of(r, "r")
+    shape = m, h = r.shape
+    ldr = h if r.is_contiguous() and r.dtype is _BF16 and r.get_device() == dev else _strided(r, h, m, "r")
+    ldd = h
+    if not (dout.shape == shape and dout.is_contiguous() and dout.dtype is _BF16 and dout.get_device() == dev):
+        ldd = _strided(dout, h, m, "dout")
+    if not (weight.dtype is _F32 and weight.is_contiguous() and weight.shape == (h,) and weight.get_device() == dev):
+        _bad(weight, _F32, (h,), "weight")
+    ldq, dres = 0, None
     if dresidual is not None:
-        ldq = _rows(dresidual, h, "dresidual")
-        _need(dresidual.shape[0] == m, "dresidual and r differ in rows")
-        _on(dresidual)
-    dx = _empty((m, h), dtype=_BF16, device=r.device)
-    dw = ws = None
+        ldq = h
+        if not (dresidual.shape == shape and dresidual.is_contiguous() and dresidual.dtype is _BF16
+                and dresidual.get_device() == dev):
+            ldq = _strided(dresidual, h, m, "dresidual")
+        dres = dresidual.data_ptr()
+    dx = _empty_like(r, memory_format=_dense_rows)
+    dw = to = ws = None
     need = 0
     if need_dw:
+        dw = _empty_like(weight) if m else torch.zeros_like(weight)
+        to = dw.data_ptr()
         size = ctypes.c_size_t()
-        _check(lib.moe_add_rmsnorm_backward_workspace_size(m, h, ctypes.byref(size)),
-               "moe_add_rmsnorm_backward_workspace_size")
+        rc = lib.moe_add_rmsnorm_backward_workspace_size(m, h, size)
+        if rc:
+            raise MoeError(rc, "moe_add_rmsnorm_backward")
         need = size.value
-        dw = (_empty if m else torch.zeros)((h,), dtype=_F32, device=r.device)
-        ws = _empty((need,), dtype=_U8, device=r.device)
-    rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps,
-                                      None if dresidual is None else dresidual.data_ptr(), ldq, dx.data_ptr(),
-                                      dw.data_ptr() if need_dw else None, ws.data_ptr() if need_dw else None, need, st)
+        space = _empty((need,), dtype=_U8, device=r.device)
+        ws = space.data_ptr()
+    rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps, dres, ldq,
+                                      dx.data_ptr(), to, ws, need, _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_add_rmsnorm_backward")
     return dx, dw
 
 
 SCORINGS = {"softmax": MOE_SCORING_SOFTMAX, "sigmoid": MOE_SCORING_SIGMOID}
+_I32 = torch.int32
 
 
-def _router_args(logits, topk_ids, seq_offsets, scoring):
-    """Checks what the router's operators share; returns (m, E, k, sequences, scoring, stream)."""
-    _need(logits.dim() == 2 and topk_ids.dim() == 2, "logits: [m, E], topk_ids: [m, k]")
-    (m, E), k = logits.shape, topk_ids.shape[1]
-    _dense(logits, _F32, (m, E), "logits")
-    _dense(topk_ids, torch.int32, (m, k), "topk_ids")
-    _need(scoring in SCORINGS, f"scoring: one of {sorted(SCORINGS)}")
-    seqs = 1
-    st = _on(logits, topk_ids)
-    if seq_offsets is not None:
+def _router_args(logits, topk_ids, seq_offsets, scoring, dev: int):
+    """Checks what the router's operators share; returns (m, E, k, sequences, their offsets' address, scoring)."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits: [m, E], topk_ids: [m, k]")
+    m, E = logits.shape
+    rows, k = topk_ids.shape
+    if not (logits.dtype is _F32 and logits.is_contiguous() and logits.get_device() == dev):
+        _bad(logits, _F32, (m, E), "logits")
+    if not (topk_ids.dtype is _I32 and topk_ids.is_contiguous() and rows == m and topk_ids.get_device() == dev):
+        _bad(topk_ids, _I32, (m, k), "topk_ids")
+    if scoring not in SCORINGS:
+        raise ValueError(f"scoring: one of {sorted(SCORINGS)}")
+    if seq_offsets is None:
+        return m, E, k, 1, None, SCORINGS[scoring]
+    if not (seq_offsets.dtype is _I32 and seq_offsets.dim() == 1 and seq_offsets.is_contiguous()
+            and seq_offsets.get_device() == dev and seq_offsets.shape[0] >= 2):
         _need(seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2, "seq_offsets: [sequences + 1], at least one sequence")
-        seqs = seq_offsets.shape[0] - 1
-        _dense(seq_offsets, torch.int32, (seqs + 1,), "seq_offsets")
-        _on(seq_offsets)
-    return m, E, k, seqs, SCORINGS[scoring], st
+        _bad(seq_offsets, _I32, tuple(seq_offsets.shape), "seq_offsets")
+    return m, E, k, seq_offsets.shape[0] - 1, seq_offsets.data_ptr(), SCORINGS[scoring]
 
 
 def moe_balance_loss(logits, topk_ids, seq_offsets=None, scoring="softmax", stream=None):
@@ -1052,20 +1069,20 @@ def moe_balance_loss(logits, topk_ids, seq_offsets=None, scoring="softmax", stre
         with torch.cuda.stream(stream):
             return moe_balance_loss(logits, topk_ids, seq_offsets, scoring)
     lib = _lib or load_library()
-    m, E, k, S, mode, st = _router_args(logits, topk_ids, seq_offsets, scoring)
-    dev = logits.device
+    dev = _device_of(logits, "logits")
+    m, E, k, S, off, mode = _router_args(logits, topk_ids, seq_offsets, scoring, dev)
+    on = logits.device
     new = _empty if m else torch.zeros
-    losses = new((2, S), dtype=_F32, device=dev)
-    counts = new((S, E), dtype=torch.int32, device=dev)
+    balance, z = new((2, S), dtype=_F32, device=on).unbind()
+    counts = new((S, E), dtype=_I32, device=on)
     # what moe_balance_loss_workspace_size returns
-    ws = _empty(((4 * S + 255) // 256 * 256 + (((m + 7) // 8 + S) * 8 + 255) // 256 * 256,), dtype=_U8, device=dev)
-    balance = losses.data_ptr()
-    rc = lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), m, E, k,
-                              None if seq_offsets is None else seq_offsets.data_ptr(), S, mode, balance, balance + 4 * S,
-                              counts.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    need = (4 * S + 255) // 256 * 256 + (((m + 7) // 8 + S) * 8 + 255) // 256 * 256
+    ws = _empty((need,), dtype=_U8, device=on)
+    rc = lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, off, S, mode, balance.data_ptr(),
+                              z.data_ptr(), counts.data_ptr(), ws.data_ptr(), need, _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_balance_loss")
-    return losses[0], losses[1], counts
+    return balance, z, counts
 
 
 def moe_route_backward(logits, topk_ids, dtopk_w=None, dbalance=None, dz=None, counts=None, seq_offsets=None,
@@ -1078,61 +1095,66 @@ def moe_route_backward(logits, topk_ids, dtopk_w=None, dbalance=None, dz=None, c
             return moe_route_backward(logits, topk_ids, dtopk_w, dbalance, dz, counts, seq_offsets, scoring,
                                       norm_topk_prob, routed_scaling)
     lib = _lib or load_library()
-    m, E, k, S, mode, st = _router_args(logits, topk_ids, seq_offsets, scoring)
-    for t, shape, dtype, what in ((dtopk_w, (m, k), _F32, "dtopk_w"), (dbalance, (S,), _F32, "dbalance"),
-                                  (dz, (S,), _F32, "dz"), (counts, (S, E), torch.int32, "counts")):
-        if t is not None:
-            _dense(t, dtype, shape, what)
-            _on(t)
-    _need(dbalance is None or counts is not None, "dbalance without counts")
-    d = _empty((m, E), dtype=_F32, device=logits.device)
-    ptr = [None if t is None else t.data_ptr() for t in (dtopk_w, seq_offsets, counts, dbalance, dz)]
-    rc = lib.moe_route_backward(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, mode, int(bool(norm_topk_prob)),
-                                routed_scaling, ptr[0], ptr[1], S, *ptr[2:], d.data_ptr(), st)
+    dev = _device_of(logits, "logits")
+    m, E, k, S, off, mode = _router_args(logits, topk_ids, seq_offsets, scoring, dev)
+    w = c = b = z = None
+    if dtopk_w is not None:
+        if not (dtopk_w.dtype is _F32 and dtopk_w.is_contiguous() and dtopk_w.shape == (m, k) and dtopk_w.get_device() == dev):
+            _bad(dtopk_w, _F32, (m, k), "dtopk_w")
+        w = dtopk_w.data_ptr()
+    if dbalance is not None:
+        if counts is None:
+            raise ValueError("dbalance without counts")
+        if not (dbalance.dtype is _F32 and dbalance.is_contiguous() and dbalance.shape == (S,) and dbalance.get_device() == dev):
+            _bad(dbalance, _F32, (S,), "dbalance")
+        b = dbalance.data_ptr()
+    if dz is not None:
+        if not (dz.dtype is _F32 and dz.is_contiguous() and dz.shape == (S,) and dz.get_device() == dev):
+            _bad(dz, _F32, (S,), "dz")
+        z = dz.data_ptr()
+    if counts is not None:
+        if not (counts.dtype is _I32 and counts.is_contiguous() and counts.shape == (S, E) and counts.get_device() == dev):
+            _bad(counts, _I32, (S, E), "counts")
+        c = counts.data_ptr()
+    d = _empty_like(logits, memory_format=_dense_rows)
+    rc = lib.moe_route_backward(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, mode, 1 if norm_topk_prob else 0,
+                                routed_scaling, w, off, S, c, b, z, d.data_ptr(), _raw_stream(dev))
     if rc:
         raise MoeError(rc, "moe_route_backward")
     return d
 
 
-def _lora_call(y, x, a, b, ids, scale, out):
-    """Checks a call of moe_lora_add; returns what makes it."""
-    lib = _lib or load_library()
-    _need(a.dim() == 3 and b.dim() == 3, "a: [n, r, k], b: [n, d, r]")
+def _lora_args(y, x, a, b, ids, scale, out, dev: int):
+    """Checks a call of moe_lora_add; returns its arguments up to out's stride, and out."""
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a: [n, r, k], b: [n, d, r]")
     n, r, k = a.shape
     d = b.shape[1]
-    _dense(a, _BF16, (n, r, k), "a")
-    _dense(b, _BF16, (n, d, r), "b")
-    ldx, ldy = _rows(x, k, "x"), _rows(y, d, "y")
-    m = x.shape[0]
-    _need(y.shape[0] == m, "x and y differ in rows")
-    _dense(ids, torch.int32, (m,), "ids")
-    st = _on(y, x, a, b, ids)
+    if not (a.dtype is _BF16 and a.is_contiguous() and a.get_device() == dev):
+        _bad(a, _BF16, (n, r, k), "a")
+    if not (b.dtype is _BF16 and b.is_contiguous() and b.shape == (n, d, r) and b.get_device() == dev):
+        _bad(b, _BF16, (n, d, r), "b")
+    m = x.shape[0] if x.dim() == 2 else -1
+    ldx = k if x.is_contiguous() and x.dtype is _BF16 and x.shape == (m, k) and x.get_device() == dev else \
+        _strided(x, k, m, "x")
+    ldy = d
+    if not (y.is_contiguous() and y.dtype is _BF16 and y.shape == (m, d) and y.get_device() == dev):
+        ldy = _strided(y, d, m, "y")
+    if not (ids.dtype is _I32 and ids.is_contiguous() and ids.shape == (m,) and ids.get_device() == dev):
+        _bad(ids, _I32, (m,), "ids")
+    s = None
     if scale is not None:
-        _dense(scale, _F32, (n,), "scale")
-        _on(scale)
+        if not (scale.dtype is _F32 and scale.is_contiguous() and scale.shape == (n,) and scale.get_device() == dev):
+            _bad(scale, _F32, (n,), "scale")
+        s = scale.data_ptr()
     if out is None:
         out, ldo = y, ldy
     else:
-        ldo = _rows(out, d, "out")
-        _need(out.shape[0] == m, "out and y differ in rows")
-        _need(_same(out, y) or not _share(out, y), "out: y itself, or memory of its own")
-        _on(out)
-    _need(not _share(out, x), "out shares memory with x")
-    size = ctypes.c_size_t()
-    rc = lib.moe_lora_add_workspace_size(m, k, r, ctypes.byref(size))
-    if rc:
-        raise MoeError(rc, "moe_lora_add")
-
-    def call():
-        with _spaces_lock:
-            ws = _space(x, st, size.value)
-            rc = lib.moe_lora_add(x.data_ptr(), ldx, m, k, y.data_ptr(), ldy, d, a.data_ptr(), b.data_ptr(), n, r,
-                                  ids.data_ptr(), None if scale is None else scale.data_ptr(), out.data_ptr(), ldo,
-                                  ws.data_ptr(), ws.numel(), st)
-        if rc:
-            raise MoeError(rc, "moe_lora_add")
-        return out
-    return call
+        ldo = d
+        if not (out.is_contiguous() and out.dtype is _BF16 and out.shape == (m, d) and out.get_device() == dev):
+            ldo = _strided(out, d, m, "out")
+    return out, (x.data_ptr(), ldx, m, k, y.data_ptr(), ldy, d, a.data_ptr(), b.data_ptr(), n, r, ids.data_ptr(), s,
+                 out.data_ptr(), ldo)
 
 
 def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
@@ -1143,4 +1165,20 @@ def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return moe_lora_add(y, x, a, b, ids, scale, out)
-    return _lora_call(y, x, a, b, ids, scale, out)()
+    lib = _lib or load_library()
+    dev = _device_of(x, "x")
+    out, args = _lora_args(y, x, a, b, ids, scale, out, dev)
+    need = 256
+    if args[2] > MOE_LORA_BY_TOKEN:
+        size = ctypes.c_size_t()
+        rc = lib.moe_lora_add_workspace_size(args[2], args[3], args[10], size)
+        if rc:
+            raise MoeError(rc, "moe_lora_add")
+        need = size.value
+    st = _raw_stream(dev)
+    with _spaces_lock:
+        ws = _space(x, st, need)
+        rc = lib.moe_lora_add(*args, ws.data_ptr(), ws.numel(), st)
+    if rc:
+        raise MoeError(rc, "moe_lora_add")
+    return out

@@ -244,26 +244,27 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
 constexpr int BN = 128;
 constexpr int EPI_WARPS = 8;
 constexpr int EXPAND_THREADS = 32 * (2 + EPI_WARPS);
-constexpr int Y_STAGES = 3, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
+constexpr int MAX_Y = 5, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
 constexpr int MAX_B = 4;
 
 __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
-    __shared__ uint64_t bars[2 * Y_STAGES + 2 * MAX_B + 6];
+    __shared__ uint64_t bars[2 * MAX_Y + 2 * MAX_B + 6];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nb = (p.r + BK - 1) / BK;  // boxes along r
+    const uint32_t YS = p.y_stages;
     // T's first parts, its second parts, y, B
-    const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + Y_STAGES * Y_BYTES;
-    const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * Y_STAGES, bfull0 = yempty0 + 8 * Y_STAGES,
+    const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + YS * Y_BYTES;
+    const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * MAX_Y, bfull0 = yempty0 + 8 * MAX_Y,
                    bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 16,
                    tready = dempty0 + 16, drain = tready + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Y_STAGES; ++s) {
+        for (int s = 0; s < p.y_stages; ++s) {
             mbar_init(yfull0 + 8 * s, 1);
             mbar_init(yempty0 + 8 * s, EPI_WARPS);
         }
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             }
             __syncwarp();
             ++yn;
-            if (++ys == Y_STAGES) {
+            if (++ys == YS) {
                 ys = 0;
                 yph ^= 1u;
             }
@@ -339,8 +340,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             abort_flag = 1;
         }
         const uint32_t S = p.stages;
-        for (uint32_t i = yn > Y_STAGES ? yn - Y_STAGES : 0; i < yn; ++i)
-            mbar_wait(yfull0 + 8 * (i % Y_STAGES), (i / Y_STAGES) & 1u, DRAIN_NS);
+        for (uint32_t i = yn > YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
         for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         uint32_t bs = 0, bph = 0, d = 0;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 if (before >= 0) mbar_arrive(yempty0 + 8 * before);
             }
             before = (int)ys;
-            if (++ys == Y_STAGES) {
+            if (++ys == YS) {
                 ys = 0;
                 yph ^= 1u;
             }
@@ -541,9 +541,11 @@ cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
     const int nb = ceil_div(p.r, BK);
     p.n_tiles = ceil_div(p.N, BN);
     p.n_ctas = std::max(1, std::min(p.n_tiles, sms() / tiles));
-    p.stages = std::min(MAX_B, (kSmem - 1024 - 2 * nb * X_BYTES - Y_STAGES * Y_BYTES) / X_BYTES);
+    const int room = kSmem - 1024 - 2 * nb * X_BYTES;
+    p.stages = 2;
+    p.y_stages = std::min(MAX_Y, (room - p.stages * X_BYTES) / Y_BYTES);
     return launch_pdl(lora_expand, dim3(tiles, p.n_ctas), dim3(EXPAND_THREADS),
-                      1024 + 2 * nb * X_BYTES + Y_STAGES * Y_BYTES + p.stages * X_BYTES, st, p);
+                      1024 + 2 * nb * X_BYTES + p.y_stages * Y_BYTES + p.stages * X_BYTES, st, p);
 }
 
 }  // namespace moe

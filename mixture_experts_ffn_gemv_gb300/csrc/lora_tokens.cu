@@ -13,6 +13,7 @@
 #include "launch.cuh"
 #include "ops.h"
 #include "sm100.cuh"
+#include "tmap.h"
 
 namespace moe {
 
@@ -20,7 +21,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kCluster = 8;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPieces = 4;  // pieces of 8 inputs that a lane holds of x at a time
 constexpr int kAhead = 4;   // rows of B that a lane has on their way at a time
@@ -31,7 +31,7 @@ __device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8]) {
 }
 
 // LPR lanes hold a row of B, 8 of its r values each (LPR the power of two from r / 8 on).
-template <int LPR>
+template <int LPR, int kCluster>
 __global__ void __launch_bounds__(kThreads) lora_tokens(const LoraArgs a) {
     __shared__ float part[kLoraMaxRank], low[kLoraMaxRank];
     pdl_wait();
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) lora_tokens(const LoraArgs a) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the others have read this block's
 }
 
-template <int LPR>
+template <int LPR, int kCluster>
 cudaError_t launch(const LoraArgs& a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.m * kCluster);
@@ -164,17 +164,23 @@ cudaError_t launch(const LoraArgs& a, cudaStream_t st) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, lora_tokens<LPR>, a);
+    return cudaLaunchKernelEx(&cfg, lora_tokens<LPR, kCluster>, a);
+}
+
+int sms() {
+    static int n = device_sm_count();
+    return n;
 }
 
 }  // namespace
 
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st) {
-    if (a.r <= 8) return launch<1>(a, st);
-    if (a.r <= 16) return launch<2>(a, st);
-    if (a.r <= 32) return launch<4>(a, st);
-    if (a.r <= 64) return launch<8>(a, st);
-    return launch<16>(a, st);
+    const bool eight = a.m * 8 <= 2 * sms();
+    if (a.r <= 8) return eight ? launch<1, 8>(a, st) : launch<1, 4>(a, st);
+    if (a.r <= 16) return eight ? launch<2, 8>(a, st) : launch<2, 4>(a, st);
+    if (a.r <= 32) return eight ? launch<4, 8>(a, st) : launch<4, 4>(a, st);
+    if (a.r <= 64) return eight ? launch<8, 8>(a, st) : launch<8, 4>(a, st);
+    return eight ? launch<16, 8>(a, st) : launch<16, 4>(a, st);
 }
 
 }  // namespace moe

@@ -148,138 +148,162 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) add_rmsnorm(const NormArgs 
     }
 }
 
+// Pairs of fp32 in one instruction.
+struct Pair {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(Pair p) { return __double_as_longlong(__hiloint2double(__float_as_int(p.y), __float_as_int(p.x))); }
+__device__ __forceinline__ Pair pair(uint64_t v) {
+    Pair p;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
+    return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+__device__ __forceinline__ Pair unpack2(uint32_t w) { return Pair{bf16lo(w), bf16hi(w)}; }
+__device__ __forceinline__ void load_w4(const float* p, Pair (&v)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p + 4));
+    v[0] = Pair{a.x, a.y}; v[1] = Pair{a.z, a.w}; v[2] = Pair{b.x, b.y}; v[3] = Pair{b.z, b.w};
+}
+// Waits for the T threads of group g of the block.
+__device__ __forceinline__ void group_sync(int g, int T) { asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(T) : "memory"); }
+
 // Backward: with g = dout w and n = r rstd, both of a row's sums (r^2 and g r)
 // in one pass,
 //   dx = rstd (g - n sum(g n) / H) + dres
 // and dw = sum over rows of dout n: a thread adds up its own columns over the
-// rows of its block, the blocks' sums [blocks, H] are added by column_sums in
-// their order.
-template <int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) add_rmsnorm_backward(const NormGradArgs a) {
-    __shared__ float buf[2][2][32];
-    extern __shared__ float wdw[];  // WARP: [kWarpRows, H]
+// rows of its group (T threads take a row, a block has several groups), the
+// groups of a block are added in shared memory and the blocks' sums [blocks, H]
+// by column_sums, each in its order.
+template <int V>
+__global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs a, int T) {
+    __shared__ float2 buf[2][32];
+    extern __shared__ float sum[];  // [H] where the block has more than one group
     pdl_wait();
     pdl_trigger();
-    const int n = WARP ? 32 : (int)blockDim.x, i = WARP ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-    const int pieces = a.H >> 3, warp = threadIdx.x >> 5;
-    float dw[V][8];
+    const int g = threadIdx.x / T, i = threadIdx.x % T, groups = blockDim.x / T;
+    const int pieces = a.H >> 3, warp = threadIdx.x >> 5, warps = T >> 5;
+    constexpr bool kEarly = V <= 2;  // registers for dres from the start
+    Pair dw[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[v][j] = 0.f;
-    const int step = (int)gridDim.x * (WARP ? kWarpRows : 1);
+        for (int j = 0; j < 4; ++j) dw[v][j] = Pair{0.f, 0.f};
     int turn = 0;
-    for (int t = WARP ? (int)blockIdx.x * kWarpRows + warp : (int)blockIdx.x; t < a.m; t += step, turn ^= 1) {
+    for (int t = blockIdx.x * groups + g; t < a.m; t += gridDim.x * groups, turn ^= 1) {
         const uint16_t *dout = a.dout + (size_t)t * a.ldd, *row = a.r + (size_t)t * a.ldr;
-        uint4 r[V], d[V];
+        const uint16_t* dres = a.dres ? a.dres + (size_t)t * a.ldq : nullptr;
+        uint4 r[V], d[V], q[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * n + i;
-            r[v] = c < pieces ? ld_once(row + 8 * c) : make_uint4(0, 0, 0, 0);
-            d[v] = c < pieces ? ld_once(dout + 8 * c) : make_uint4(0, 0, 0, 0);
+            const int c = v * T + i;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            r[v] = c < pieces ? ld_once(row + 8 * c) : none;
+            d[v] = c < pieces ? ld_once(dout + 8 * c) : none;
+            if (kEarly) q[v] = dres && c < pieces ? ld_once(dres + 8 * c) : none;
         }
-        float ss = 0.f, gr = 0.f;
+        Pair s2{0.f, 0.f}, g2{0.f, 0.f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * n + i;
+            const int c = v * T + i;
             if (c < pieces) {
-                float f[8], g[8], w[8];
-                unpack8(r[v], f);
-                unpack8(d[v], g);
-                load_w8(a.w + 8 * c, w);
+                const uint32_t rw[4] = {r[v].x, r[v].y, r[v].z, r[v].w}, ew[4] = {d[v].x, d[v].y, d[v].z, d[v].w};
+                Pair w[4];
+                load_w4(a.w + 8 * c, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    ss = fmaf(f[j], f[j], ss);
-                    gr = fmaf(g[j] * w[j], f[j], gr);
+                for (int j = 0; j < 4; ++j) {
+                    const Pair f = unpack2(rw[j]);
+                    s2 = fma2(f, f, s2);
+                    g2 = fma2(mul2(unpack2(ew[j]), w[j]), f, g2);
                 }
             }
         }
-        ss = warp_sum(ss);
-        gr = warp_sum(gr);
-        if (!WARP) {
-            if ((threadIdx.x & 31) == 0) {
-                buf[turn][0][warp] = ss;
-                buf[turn][1][warp] = gr;
-            }
-            __syncthreads();
+        float ss = warp_sum(s2.x + s2.y), gr = warp_sum(g2.x + g2.y);
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) buf[turn][warp] = make_float2(ss, gr);
+            group_sync(g, T);
             ss = gr = 0.f;
-            for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
-                ss += buf[turn][0][k];
-                gr += buf[turn][1][k];
+            for (int k = g * warps; k < (g + 1) * warps; ++k) {
+                const float2 b = buf[turn][k];
+                ss += b.x;
+                gr += b.y;
             }
         }
         const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
         const float mean = gr / (float)a.H * inv;  // of g n
+        const Pair inv2{inv, inv};
+        const Pair back{-mean * inv * inv, -mean * inv * inv};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = v * n + i;
+            const int c = v * T + i;
             if (c < pieces) {
-                float f[8], g[8], w[8], o[8];
-                unpack8(r[v], f);
-                unpack8(d[v], g);
-                load_w8(a.w + 8 * c, w);
+                if (!kEarly) q[v] = dres ? ld_once(dres + 8 * c) : make_uint4(0, 0, 0, 0);
+                const uint32_t rw[4] = {r[v].x, r[v].y, r[v].z, r[v].w}, ew[4] = {d[v].x, d[v].y, d[v].z, d[v].w},
+                               qw[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
+                Pair w[4];
+                load_w4(a.w + 8 * c, w);
+                uint32_t o[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float nj = f[j] * inv;
-                    dw[v][j] = fmaf(g[j], nj, dw[v][j]);
-                    o[j] = inv * fmaf(-nj, mean, g[j] * w[j]);
+                for (int j = 0; j < 4; ++j) {
+                    const Pair f = unpack2(rw[j]), e = unpack2(ew[j]);
+                    dw[v][j] = fma2(e, mul2(f, inv2), dw[v][j]);
+                    const Pair x = fma2(mul2(e, w[j]), inv2, fma2(f, back, unpack2(qw[j])));
+                    o[j] = pack_bf16x2(x.x, x.y);
                 }
-                if (a.dres) {
-                    float q[8];
-                    unpack8(ld_once(a.dres + (size_t)t * a.ldq + 8 * c), q);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] += q[j];
-                }
-                *reinterpret_cast<uint4*>(a.dx + (size_t)t * a.H + 8 * c) = pack8(o);
+                *reinterpret_cast<uint4*>(a.dx + (size_t)t * a.H + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
     }
     if (!a.dw) return;
     float* part = a.part + (size_t)blockIdx.x * a.H;
-    if (WARP) {
-        for (int v = 0; v < V; ++v) {
-            const int c = v * n + i;
-            if (c < pieces)
+    for (int k = 0; k < groups; ++k) {  // the last group's turn writes the block's sum out
+        if (k == g) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) wdw[warp * a.H + 8 * c + j] = dw[v][j];
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.H; c += 32 * kWarpRows) {
-            float s = 0.f;
+            for (int v = 0; v < V; ++v) {
+                const int c = v * T + i;
+                if (c < pieces)
 #pragma unroll
-            for (int k = 0; k < kWarpRows; ++k) s += wdw[k * a.H + c];
-            part[c] = s;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * n + i;
-            if (c < pieces) {
-                *reinterpret_cast<float4*>(part + 8 * c) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-                *reinterpret_cast<float4*>(part + 8 * c + 4) = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+                    for (int h = 0; h < 2; ++h) {
+                        float4 f = make_float4(dw[v][2 * h].x, dw[v][2 * h].y, dw[v][2 * h + 1].x, dw[v][2 * h + 1].y);
+                        float4* s4 = reinterpret_cast<float4*>(sum + 8 * c + 4 * h);
+                        if (k) {
+                            const float4 q = *s4;
+                            f = make_float4(f.x + q.x, f.y + q.y, f.z + q.z, f.w + q.w);
+                        }
+                        *(k == groups - 1 ? reinterpret_cast<float4*>(part + 8 * c + 4 * h) : s4) = f;
+                    }
             }
         }
+        __syncthreads();
     }
 }
 
 // out[c] = sum over p of part[p, c]: a block takes 32 columns, its warps every
-// eighth row, then the warps in order.
-__global__ void __launch_bounds__(256) column_sums(const float* __restrict__ part, int P, int H, float* __restrict__ out) {
-    __shared__ float s[8][32];
+// 16th row, then the warps in order.
+__global__ void __launch_bounds__(512) column_sums(const float* __restrict__ part, int P, int H, float* __restrict__ out) {
+    __shared__ float s[16][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < H) {
-#pragma unroll 8
-        for (int p = warp; p < P; p += 8) v += part[(size_t)p * H + c];
+#pragma unroll 10
+        for (int p = warp; p < P; p += 16) v += part[(size_t)p * H + c];
     }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < H) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t += s[k][lane];
+        for (int k = 0; k < 16; ++k) t += s[k][lane];
         out[c] = t;
     }
 }
@@ -311,7 +335,7 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st) {
             default: return launch_pdl(add_rmsnorm<4, true>, grid, block, 0, st, a);
         }
     }
-    const RowShape s = row_shape(a.H, a.m < 2 * sms() ? 1 : 2);
+    const RowShape s = row_shape(a.H, 2);
     const dim3 grid(a.m), block(s.threads);
     switch (s.v) {
         case 1: return launch_pdl(add_rmsnorm<1, false>, grid, block, 0, st, a);
@@ -320,31 +344,42 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st) {
     }
 }
 
+namespace {
+
+// Pieces of a thread, threads of a row, rows of a block at a time, blocks: 1024
+// threads to an SM, which the registers allow; few rows go to as many SMs.
+struct GradShape {
+    int v, T, most, groups, blocks;
+};
+GradShape grad_shape(int m, int H) {
+    GradShape s;
+    s.v = H <= 256 ? 1 : H <= 16384 ? 2 : 3;
+    s.T = ceil_div(ceil_div(H / 8, s.v), 32) * 32;
+    s.most = std::max(1, 512 / s.T);
+    s.groups = std::min(s.most, std::max(1, ceil_div(m, 2 * sms())));
+    s.blocks = std::min(ceil_div(m, s.groups), sms() * (1024 / (s.T * s.groups)));
+    return s;
+}
+}  // namespace
+
+// Blocks, at most, of m rows and of fewer: below s.most groups they are at most two an SM.
 int norm_grad_blocks(int m, int H) {
-    if (H <= kWarpMaxH) return std::min(ceil_div(m, kWarpRows), 4 * sms());
-    return std::min(m, sms() * std::max(1, 1024 / row_shape(H, 2).threads));
+    const GradShape s = grad_shape(m, H);
+    return std::min(m, sms() * std::max(2, 1024 / (s.T * s.most)));
 }
 
 cudaError_t launch_add_rmsnorm_backward(const NormGradArgs& a, cudaStream_t st) {
-    const int blocks = norm_grad_blocks(a.m, a.H);
+    const GradShape s = grad_shape(a.m, a.H);
+    const dim3 grid(s.blocks), block(s.T * s.groups);
+    const size_t smem = a.dw && s.groups > 1 ? (size_t)a.H * 4 : 0;  // at most 16 KB
     cudaError_t e;
-    if (a.H <= kWarpMaxH) {
-        const dim3 grid(blocks), block(32 * kWarpRows);
-        const size_t smem = a.dw ? (size_t)kWarpRows * a.H * 4 : 0;
-        switch (ceil_div(a.H, 256)) {
-            case 1: e = launch_pdl(add_rmsnorm_backward<1, true>, grid, block, smem, st, a); break;
-            case 2: e = launch_pdl(add_rmsnorm_backward<2, true>, grid, block, smem, st, a); break;
-            case 3: e = launch_pdl(add_rmsnorm_backward<3, true>, grid, block, smem, st, a); break;
-            default: e = launch_pdl(add_rmsnorm_backward<4, true>, grid, block, smem, st, a); break;
-        }
-    } else {
-        const RowShape s = row_shape(a.H, 2);
-        const dim3 grid(blocks), block(s.threads);
-        e = s.v == 2 ? launch_pdl(add_rmsnorm_backward<2, false>, grid, block, 0, st, a)
-                     : launch_pdl(add_rmsnorm_backward<3, false>, grid, block, 0, st, a);
+    switch (s.v) {
+        case 1: e = launch_pdl(add_rmsnorm_backward<1>, grid, block, smem, st, a, s.T); break;
+        case 2: e = launch_pdl(add_rmsnorm_backward<2>, grid, block, smem, st, a, s.T); break;
+        default: e = launch_pdl(add_rmsnorm_backward<3>, grid, block, smem, st, a, s.T); break;
     }
     if (e != cudaSuccess || !a.dw) return e;
-    return launch_pdl(column_sums, dim3(ceil_div(a.H, 32)), dim3(256), 0, st, (const float*)a.part, blocks, a.H, a.dw);
+    return launch_pdl(column_sums, dim3(ceil_div(a.H, 32)), dim3(512), 0, st, (const float*)a.part, s.blocks, a.H, a.dw);
 }
 
 }  // namespace moe

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "moe_ffn_ops.h"
+
 namespace moe {
 
 struct WsHeader;
@@ -78,11 +80,12 @@ struct LoraArgs {
     int splits, kblocks, split_blocks;
     int group;         // adapters whose products share a pass over x
     int a_bytes, stages;  // shrink: a stage's part for A; stages
-    int n_tiles, n_ctas;  // expand: tiles of N, blocks that share them
+    int n_tiles, n_ctas;  // expand: tiles of N, blocks that share them, stages of y (of B: stages)
+    int y_stages;
     CUtensorMap mx, ma, mb, my, mo;
 };
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraByToken = 64;  // up to so many tokens: a cluster each
+constexpr int kLoraByToken = MOE_LORA_BY_TOKEN;  // up to so many tokens: a cluster each
 int64_t lora_part_floats(int64_t m, int64_t r);  // never fewer for more tokens
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st);
 cudaError_t launch_lora_tiles(LoraArgs& a, cudaStream_t st);

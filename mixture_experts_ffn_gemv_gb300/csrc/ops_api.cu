@@ -24,6 +24,24 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 bool bad_rows(const void* p, int64_t ld, int64_t n) {
     return !p || !aligned(p, 16) || ld < n || ld % 8 || ld > (int64_t)1 << 38;
 }
+// m rows of n bytes, ld bytes apart
+struct Rows {
+    uintptr_t at;
+    int64_t ld, n;
+};
+Rows rows16(const void* p, int64_t ld, int64_t n) { return {reinterpret_cast<uintptr_t>(p), 2 * ld, 2 * n}; }
+// Whether two matrices of m rows share memory: their spans meet and, where their
+// rows are as far apart, so do their columns.
+bool share(const Rows& a, const Rows& b, int64_t m) {
+    if (!a.at || !b.at || a.at >= b.at + (m - 1) * b.ld + b.n || b.at >= a.at + (m - 1) * a.ld + a.n) return false;
+    if (m == 1 || a.ld != b.ld) return true;
+    const int64_t ahead = b.at >= a.at ? (int64_t)(b.at - a.at) % a.ld : (a.ld - (int64_t)(a.at - b.at) % a.ld) % a.ld;
+    return ahead < a.n || ahead + b.n > a.ld;
+}
+// ... where the two may be the same rows
+bool share_part(const Rows& a, const Rows& b, int64_t m) {
+    return !(a.at == b.at && a.n == b.n && (m == 1 || a.ld == b.ld)) && share(a, b, m);
+}
 bool bad_words(const void* p) { return !p || !aligned(p, 4); }
 int check_norm(int64_t m, int64_t h) {
     if (m < 0 || h <= 0 || h % 8) return MOE_ERR_INVALID_ARG;
@@ -48,12 +66,18 @@ int moe_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ld
     if (rc != MOE_OK || m == 0) return rc;
     if (bad_rows(x, ldx, h) || !weight || !aligned(weight, 16) || !(eps >= 0.f) || !std::isfinite(eps))
         return MOE_ERR_INVALID_ARG;
-    if (residual ? bad_rows(residual, ldr, h) || bad_rows(residual_out, ldo, h) || (residual_out == residual && ldo != ldr)
-                 : residual_out != nullptr)
+    if (residual ? bad_rows(residual, ldr, h) || bad_rows(residual_out, ldo, h) : residual_out != nullptr)
         return MOE_ERR_INVALID_ARG;
     if ((!out && !codes) || (codes != nullptr) != (scales != nullptr)) return MOE_ERR_INVALID_ARG;
-    if ((out && (!aligned(out, 16) || (out == x && ldx != h))) || (codes && (!aligned(codes, 16) || !aligned(scales, 4))))
+    if (!aligned(out, 16) || !aligned(codes, 16) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    const int64_t blocks = (h + 127) / 128;
+    const Rows rx = rows16(x, ldx, h), rr = rows16(residual, ldr, h), rn = rows16(residual_out, ldo, h), ro = rows16(out, h, h),
+               rc8{reinterpret_cast<uintptr_t>(codes), h, h}, rs{reinterpret_cast<uintptr_t>(scales), 4 * blocks, 4 * blocks};
+    if (share_part(rn, rr, m) || share(rn, rx, m) || share_part(ro, rx, m) || share(ro, rr, m) || share(ro, rn, m))
         return MOE_ERR_INVALID_ARG;
+    for (const Rows& q : {rx, rr, rn, ro})
+        if (share(rc8, q, m) || share(rs, q, m)) return MOE_ERR_INVALID_ARG;
+    if (share(rc8, rs, m)) return MOE_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = static_cast<const uint16_t*>(x);
     a.res = static_cast<const uint16_t*>(residual);
@@ -87,7 +111,9 @@ int moe_add_rmsnorm_backward(const void* dout, int64_t ldd, const void* r, int64
     if (bad_rows(dout, ldd, h) || bad_rows(r, ldr, h) || !weight || !aligned(weight, 16) || !(eps >= 0.f) ||
         !std::isfinite(eps) || (dresidual && bad_rows(dresidual, ldq, h)) || !dx || !aligned(dx, 16))
         return MOE_ERR_INVALID_ARG;
-    if ((dx == dout && ldd != h) || (dx == dresidual && ldq != h) || dx == r) return MOE_ERR_INVALID_ARG;
+    const Rows rx = rows16(dx, h, h);
+    if (share_part(rx, rows16(dout, ldd, h), m) || share_part(rx, rows16(dresidual, ldq, h), m) || share(rx, rows16(r, ldr, h), m))
+        return MOE_ERR_INVALID_ARG;
     if (dweight) {
         if (!aligned(dweight, 4) || !workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
         if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
@@ -192,7 +218,8 @@ int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y
     if (d <= 0 || d % 8 || n <= 0) return MOE_ERR_INVALID_ARG;
     if (d > 1 << 20 || n > (1 << 30) / r) return MOE_ERR_UNSUPPORTED;
     if (m == 0) return MOE_OK;
-    if (bad_rows(x, ldx, k) || bad_rows(y, ldy, d) || bad_rows(out, ldo, d) || (out == y && ldo != ldy) || out == x || !a ||
+    if (bad_rows(x, ldx, k) || bad_rows(y, ldy, d) || bad_rows(out, ldo, d) ||
+        share_part(rows16(out, ldo, d), rows16(y, ldy, d), m) || share(rows16(out, ldo, d), rows16(x, ldx, k), m) || !a ||
         !b || !aligned(a, 16) || !aligned(b, 16) || bad_words(ids) || !aligned(scale, 4) || !workspace ||
         !aligned(workspace, kAlign))
         return MOE_ERR_INVALID_ARG;

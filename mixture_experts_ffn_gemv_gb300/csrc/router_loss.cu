@@ -43,6 +43,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxChunk = 128;   // tokens of a block
 constexpr int kMinChunk = 8;     // ... at least: what one round of 32-lane groups takes
+constexpr int kIdsAhead = 16;    // ids that a counting thread has on their way
 constexpr int kOffsShared = 512; // sequences whose offsets a block keeps in shared memory
 
 // The tokens of sequence s, within [0, m] whatever the offsets hold.
@@ -59,7 +60,8 @@ __device__ __forceinline__ void span(const RouterArgs& a, int s, int& t0, int& t
 // sequences are many), a histogram in each block's shared memory, added up through
 // distributed shared memory.  Nothing has to be zeroed before and no atomics reach
 // global memory.  It also opens the losses' tickets.
-__global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a, int cluster) {
+template <int cluster>
+__global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a) {
     __shared__ int hist[kMaxExperts];
     const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
@@ -70,17 +72,13 @@ __global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a, int 
     span(a, s, t0, t1);
     const int64_t end = (int64_t)t1 * a.k, step = (int64_t)cluster * kThreads;
     int64_t p = (int64_t)t0 * a.k + rank * kThreads + threadIdx.x;
-    for (; p + 3 * step < end; p += 4 * step) {
-        int id[4];
+    for (; p < end; p += kIdsAhead * step) {
+        int id[kIdsAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = a.ids[p + i * step];
+        for (int i = 0; i < kIdsAhead; ++i) id[i] = p + i * step < end ? a.ids[p + i * step] : -1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kIdsAhead; ++i)
             if ((unsigned)id[i] < (unsigned)a.E) atomicAdd(&hist[id[i]], 1);
-    }
-    for (; p < end; p += step) {
-        const int id = a.ids[p];
-        if ((unsigned)id < (unsigned)a.E) atomicAdd(&hist[id], 1);
     }
     if (rank == 0 && threadIdx.x == 0) {
         a.ticket[s] = 0;
@@ -92,11 +90,12 @@ __global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a, int 
     for (int e = rank * kThreads + threadIdx.x; e < a.E; e += cluster * kThreads) {
         int n = 0;
         if (cluster > 1) {
-            for (int c = 0; c < cluster; ++c) {
-                int v;
-                asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(sm100::mapa(h + 4 * e, c)) : "memory");
-                n += v;
-            }
+            int v[cluster];
+#pragma unroll
+            for (int c = 0; c < cluster; ++c)
+                asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v[c]) : "r"(sm100::mapa(h + 4 * e, c)) : "memory");
+#pragma unroll
+            for (int c = 0; c < cluster; ++c) n += v[c];
         } else {
             n = hist[e];
         }
@@ -119,17 +118,33 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
+// exp(v) of v <= 0, as 2^(v log2 e): off by 2^-22 and by the product's rounding, |v| 2^-24,
+// of a number that counts for exp(v) (below 2^-126 for nothing).
+__device__ __forceinline__ float exp_neg(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    return r;
+}
+// 1 / v of 1 <= v <= 2, within 2^-23.
+__device__ __forceinline__ float inverse(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // sigma(l) and 1 - sigma(l), neither by a difference.
 __device__ __forceinline__ void logistic(float l, float& s, float& rest) {
-    const float e = expf(-fabsf(l)), big = 1.0f / (1.0f + e), small = e * big;
+    const float e = exp_neg(-fabsf(l)), big = inverse(1.0f + e), small = e * big;
     s = l >= 0.f ? big : small;
     rest = l >= 0.f ? small : big;
 }
-// sigma(l) / exp(shift), shift = min(0, the largest l): sums of them do not underflow where all
-// l are far below zero.
-__device__ __forceinline__ float shifted_logistic(float l, float shift) {
-    const float e = expf(-fabsf(l));
-    return (l >= 0.f ? 1.f : shift == 0.f ? e : expf(l - shift)) / (1.0f + e);
+// sigma(l) / exp(shift) and 1 - sigma(l), shift = min(0, the largest l): sums of the first do not
+// underflow where all l are far below zero.  low: shift < 0, for any lane of the warp.
+__device__ __forceinline__ float shifted_logistic(float l, float shift, bool low, float& rest) {
+    const float e = exp_neg(-fabsf(l)), big = inverse(1.0f + e);
+    rest = l >= 0.f ? e * big : big;
+    if (low) return (l >= 0.f ? 1.0f : exp_neg(l - shift)) * big;
+    return l >= 0.f ? big : e * big;
 }
 
 // A token's values over its lanes: value n * VEC + j of lane i is that of expert
@@ -215,37 +230,54 @@ __device__ __forceinline__ void find_sequences(const RouterArgs& a, int first, C
 // the chunk holds tokens of adds up theirs, and the warp that is the sequence's last
 // adds up the chunks.  Chunk c and sequence s meet at slot c + s, which no other
 // meeting has: along them c or s rises from one to the next and neither falls.
-template <int G, int VEC, int NV>
+template <bool SIGMOID, int G, int VEC, int NV>
 __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
     __shared__ Chunk ch;
     __shared__ float2 each[kMaxChunk];
-    pdl_wait();
-    pdl_trigger();
     const int first = blockIdx.x * a.chunk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    find_sequences(a, first, ch);
     const int i = threadIdx.x % G, group = threadIdx.x / G;
     constexpr int GROUPS = kThreads / G;
+    constexpr bool kAhead = NV * VEC <= 8;  // registers for the next token's logits
+    auto load = [&](int r) {
+        Row<G, VEC, NV> l;
+        const int j = r + group;
+        l.load(a.logits + (size_t)(first + j) * a.E, i, a.E, j < a.chunk && first + j < a.m, -INFINITY);
+        return l;
+    };
+    // logits and offsets are older than the counting kernel, whose counts alone are waited for
+    Row<G, VEC, NV> next;
+    if (kAhead) next = load(0);
+    find_sequences(a, first, ch);
+    pdl_wait();
+    pdl_trigger();
     for (int r = 0; r < a.chunk; r += GROUPS) {  // warps stay together
         const int j = r + group, s = j < a.chunk ? ch.seq[j] : -1;
         Row<G, VEC, NV> l, c;
-        l.load(a.logits + (size_t)(first + j) * a.E, i, a.E, s >= 0, -INFINITY);
+        if (kAhead) {
+            l = next;
+            next = load(r + GROUPS);
+        } else {
+            l = load(r);
+        }
         c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
         float top = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
         top = group_max<G>(top);
         const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+        const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
         float sum = 0.f, den = 0.f, q = 0.f;
 #pragma unroll
         for (int n = 0; n < NV * VEC; ++n) {
-            const float e = expf(l.v[n] - at);
-            const float p = a.sigmoid ? shifted_logistic(l.v[n], shift) : e;
+            const float e = exp_neg(l.v[n] - at);
+            float rest;
+            const float p = SIGMOID ? shifted_logistic(l.v[n], shift, low, rest) : e;
             sum += e;
             den += p;
             q = fmaf(p, c.v[n], q);
         }
         sum = group_sum<G>(sum);
-        den = a.sigmoid ? group_sum<G>(den) : sum;
+        den = SIGMOID ? group_sum<G>(den) : sum;
         q = group_sum<G>(q);
         const float lse = at + logf(sum);
         if (i == 0 && j < a.chunk)
@@ -310,16 +342,21 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
 
 // The gradient of the logits: of the routing weights, and of the losses for tokens
 // of sequences.  Pick j of a token is lane j % G's, its number j / G there.
-template <int G, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
+template <bool SIGMOID, int G, int VEC, int NV>
+__global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 1) route_backward(const RouterArgs a) {
     __shared__ Chunk ch;
+    extern __shared__ float4 row_mem[];  // [GROUPS, E], zero between tokens
+    float* row_of = reinterpret_cast<float*>(row_mem);
+    const int i = threadIdx.x % G, group = threadIdx.x / G;
+    constexpr int GROUPS = kThreads / G;
+    if (a.dtopk_w)
+        for (int e = i; e < a.E; e += G) row_of[group * a.E + e] = 0.f;
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
     const int first = blockIdx.x * a.chunk;
     const bool losses = a.dbalance || a.dz;
     if (losses) find_sequences(a, first, ch);
-    const int i = threadIdx.x % G, group = threadIdx.x / G;
-    constexpr int GROUPS = kThreads / G;
     constexpr int PICKS = G == 32 ? 1 : 4;  // k <= min(E, 32), and G < 32 only where E <= 4 G
     for (int r = 0; r < a.chunk; r += GROUPS) {
         const int j = r + group, t = first + j;
@@ -345,10 +382,12 @@ __global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
             }
             top = group_max<G>(top);
             const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+            const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
             float w[PICKS], sum = 0.f, mean = 0.f;
 #pragma unroll
             for (int n = 0; n < PICKS; ++n) {
-                w[n] = a.sigmoid ? shifted_logistic(lk[n], shift) : expf(lk[n] - at);
+                float rest;
+                w[n] = SIGMOID ? shifted_logistic(lk[n], shift, low, rest) : exp_neg(lk[n] - at);
                 sum += w[n];
             }
             sum = group_sum<G>(sum);
@@ -360,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
             mean = group_sum<G>(mean);
 #pragma unroll
             for (int n = 0; n < PICKS; ++n) {
-                if (a.sigmoid) {
+                if (SIGMOID) {
                     float sg, rest;
                     logistic(lk[n], sg, rest);
                     dk[n] = a.scale * rest * (a.norm ? w[n] * (dk[n] - mean) : sg * dk[n]);
@@ -383,24 +422,30 @@ __global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
             for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
             top = group_max<G>(top);
             const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
-            float sum = 0.f;
+            const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
             Row<G, VEC, NV> p;
+            float inv = 0.f;
+            if (a.dz || !SIGMOID) {
+                float sum = 0.f;
 #pragma unroll
-            for (int n = 0; n < NV * VEC; ++n) {
-                p.v[n] = expf(l.v[n] - at);
-                sum += p.v[n];
+                for (int n = 0; n < NV * VEC; ++n) {
+                    p.v[n] = exp_neg(l.v[n] - at);
+                    sum += p.v[n];
+                }
+                sum = group_sum<G>(sum);
+                inv = sum == 0.f ? 0.f : 1.0f / sum;
+                const float zc = a.dz ? dz * 2.f * (sum == 0.f ? 0.f : at + logf(sum)) * inv : 0.f;
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) d.v[n] = zc * p.v[n];
             }
-            sum = group_sum<G>(sum);
-            const float soft = sum == 0.f ? 0.f : 1.0f / sum;
-            const float zc = a.dz ? dz * 2.f * (sum == 0.f ? 0.f : at + logf(sum)) * soft : 0.f;
-#pragma unroll
-            for (int n = 0; n < NV * VEC; ++n) d.v[n] = zc * p.v[n];
             if (a.dbalance) {
-                float den = 0.f, inv = soft, mean = 0.f;
-                if (a.sigmoid) {
+                float mean = 0.f;
+                Row<G, VEC, NV> rest;
+                if (SIGMOID) {
+                    float den = 0.f;
 #pragma unroll
                     for (int n = 0; n < NV * VEC; ++n) {
-                        p.v[n] = shifted_logistic(l.v[n], shift);
+                        p.v[n] = shifted_logistic(l.v[n], shift, low, rest.v[n]);
                         den += p.v[n];
                     }
                     den = group_sum<G>(den);
@@ -418,13 +463,8 @@ __global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
                 mean = group_sum<G>(mean);
 #pragma unroll
                 for (int n = 0; n < NV * VEC; ++n) {
-                    float g = db * p.v[n] * (c.v[n] - mean);
-                    if (a.sigmoid) {
-                        float sg, rest;
-                        logistic(l.v[n], sg, rest);
-                        g *= rest;
-                    }
-                    d.v[n] += g;
+                    const float g = db * p.v[n] * (c.v[n] - mean);
+                    d.v[n] += SIGMOID ? g * rest.v[n] : g;
                 }
             }
             if (s < 0) {  // padding, whatever its logits hold
@@ -432,7 +472,35 @@ __global__ void __launch_bounds__(kThreads) route_backward(const RouterArgs a) {
                 for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
             }
         }
+        // The picks' gradients go to their experts' lanes through the group's row in shared memory,
+        // where each first leaves its number: one that is not found there shares its expert.
+        bool twice = false;
+        float* own = row_of + group * a.E;
         if (a.dtopk_w) {
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n)
+                if (id[n] >= 0) own[id[n]] = __int_as_float(n * G + i);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) twice |= id[n] >= 0 && __float_as_int(own[id[n]]) != n * G + i;
+            twice = __any_sync(0xffffffffu, twice);
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n)
+                if (id[n] >= 0) own[id[n]] = twice ? 0.f : dk[n];
+            __syncwarp();
+            if (!twice) {
+                Row<G, VEC, NV> k;
+                k.load(own, i, a.E, true, 0.f);
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) d.v[n] += k.v[n];
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < PICKS; ++n)
+                    if (id[n] >= 0) own[id[n]] = 0.f;
+            }
+            __syncwarp();
+        }
+        if (twice) {  // one after another, in their order
 #pragma unroll
             for (int n = 0; n < PICKS; ++n) {
                 for (int q = 0; q < G && n * G + q < a.k; ++q) {
@@ -484,10 +552,10 @@ cudaError_t by_width(int E, bool wide, F&& f) {
     return f(Int<32>(), Int<1>(), Int<32>());
 }
 
-// Tokens of a block: what spreads them over the device four blocks to an SM, in
+// Tokens of a block: what spreads them over the device so many blocks to an SM, in
 // whole rounds of the block's groups.
-int chunk_for(int m, int groups) {
-    const int even = ceil_div(m, 4 * sms());
+int chunk_for(int m, int groups, int per_sm) {
+    const int even = ceil_div(m, per_sm * sms());
     return std::min(kMaxChunk, std::max(kMinChunk, ceil_div(even, groups) * groups));
 }
 
@@ -512,19 +580,20 @@ cudaError_t launch_balance_loss(RouterArgs a, cudaStream_t st) {
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, count_pairs, a, cluster);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, cluster == 1 ? count_pairs<1> : count_pairs<8>, a);
     if (e != cudaSuccess) return e;
     return by_width(a.E, a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.counts), [&](auto g, auto vec, auto nv) {
-        a.chunk = chunk_for(a.m, kThreads / g);
-        return launch_pdl(balance_loss<g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), 0, st, (const RouterArgs)a);
+        a.chunk = chunk_for(a.m, kThreads / g, 6);
+        return launch_pdl(a.sigmoid ? balance_loss<true, g, vec, nv> : balance_loss<false, g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), 0, st, (const RouterArgs)a);
     });
 }
 
 cudaError_t launch_route_backward(RouterArgs a, cudaStream_t st) {
     const bool wide = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits) && (!a.counts || aligned16(a.counts));
     return by_width(a.E, wide, [&](auto g, auto vec, auto nv) {
-        a.chunk = chunk_for(a.m, kThreads / g);
-        return launch_pdl(route_backward<g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), 0, st, (const RouterArgs)a);
+        a.chunk = chunk_for(a.m, kThreads / g, 4);
+        const size_t smem = a.dtopk_w ? (size_t)(kThreads / g) * a.E * 4 : 0;  // at most 32 KB
+        return launch_pdl(a.sigmoid ? route_backward<true, g, vec, nv> : route_backward<false, g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), smem, st, (const RouterArgs)a);
     });
 }
 

@@ -137,9 +137,12 @@ def route_backward(logits, ids, off, sigmoid, norm, scale, dw, dbal, dz):
         if dbal is not None:
             c = (counts[s].double() - k * T / E).abs()
             pc = p[a:e]
-            b[a:e] += 4 * SMALL * dbal[s].double().abs() * E / (k * T * T) * pc * (c + (pc * c).sum(1, keepdim=True) + F32 * k * T)
+            # an exponential below 2^-126 may count for nothing: over a sum of at least 1, p is off by that
+            b[a:e] += dbal[s].double().abs() * E / (k * T * T) * (4 * SMALL * pc + 2.0 ** -126) * (
+                c + (pc * c).sum(1, keepdim=True) + F32 * k * T)
         if dz is not None:
-            b[a:e] += dz[s].double().abs() * 2 / T * soft[a:e] * (4 * SMALL * lse[a:e] + dl[a:e])[:, None]
+            b[a:e] += dz[s].double().abs() * 2 / T * (soft[a:e] * (4 * SMALL * lse[a:e] + dl[a:e])[:, None]
+                                                      + 2.0 ** -126 * lse[a:e, None])
     if dw is not None:
         ok = (ids >= 0) & (ids < E)
         w = route_weights(l, ids, sigmoid, norm, scale)

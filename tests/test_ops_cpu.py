@@ -24,6 +24,7 @@ def _call(fn, defaults, kw):
 
 NORM = dict(x=FAKE, ldx=64, res=FAKE + 4096, ldr=64, m=3, h=64, w=FAKE, eps=1e-6, res_out=FAKE + 8192, ldo=64, out=FAKE + 12288,
             codes=None, scales=None, st=None)
+CODES = dict(codes=FAKE + 16384, scales=FAKE + 20480)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -33,6 +34,9 @@ NORM = dict(x=FAKE, ldx=64, res=FAKE + 4096, ldr=64, m=3, h=64, w=FAKE, eps=1e-6
     (dict(res_out=None), 1), (dict(res=None), 1), (dict(ldr=56), 1), (dict(ldo=60), 1), (dict(res_out=FAKE + 4096, ldo=72), 1),
     (dict(out=None), 1), (dict(out=FAKE + 12290), 1), (dict(out=FAKE, ldx=72), 1),
     (dict(codes=FAKE), 1), (dict(scales=FAKE), 1), (dict(codes=FAKE + 8, scales=FAKE), 1), (dict(codes=FAKE, scales=FAKE + 2), 1),
+    (dict(out=FAKE + 16), 1), (dict(out=FAKE + 4096), 1), (dict(out=FAKE + 8192), 1), (dict(res_out=FAKE), 1),
+    (dict(res_out=FAKE + 4096 + 128), 1), (dict(CODES, codes=FAKE + 128), 1), (dict(CODES, scales=FAKE + 4096 + 256), 1),
+    (dict(CODES, scales=FAKE + 16384 + 188), 1), (dict(CODES, codes=FAKE + 12288 + 368), 1),
     (dict(m=0, x=None, w=None), 0),
 ])
 def test_norm_refuses(B, kw, want):
@@ -87,15 +91,15 @@ def test_route_backward_refuses(B, kw, want):
     assert _call(B.load_library().moe_route_backward, BACK, kw) == want
 
 
-LORA = dict(x=FAKE, ldx=64, m=200, k=64, y=FAKE + 4096, ldy=128, d=128, a=FAKE, b=FAKE, n=4, r=16, ids=FAKE, scale=FAKE,
-            out=FAKE + 8192, ldo=128, ws=FAKE, size=1 << 30, st=None)
+LORA = dict(x=FAKE, ldx=64, m=200, k=64, y=FAKE + (1 << 20), ldy=128, d=128, a=FAKE, b=FAKE, n=4, r=16, ids=FAKE, scale=FAKE,
+            out=FAKE + (2 << 20), ldo=128, ws=FAKE, size=1 << 30, st=None)
 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(m=-1), 1), (dict(k=60), 1), (dict(k=0), 1), (dict(d=12), 1), (dict(d=0), 1), (dict(r=0), 1), (dict(r=12), 1), (dict(n=0), 1),
     (dict(r=136), 2), (dict(m=1 << 30), 2), (dict(k=(1 << 20) + 8), 2), (dict(d=(1 << 20) + 8), 2), (dict(n=(1 << 26) + 1), 2),
     (dict(x=None), 1), (dict(x=FAKE + 2), 1), (dict(ldx=56), 1), (dict(ldy=120), 1), (dict(ldo=132), 1),
-    (dict(out=FAKE + 4096, ldo=136), 1), (dict(out=FAKE), 1), (dict(a=None), 1), (dict(b=FAKE + 8), 1), (dict(ids=None), 1),
+    (dict(out=FAKE + (1 << 20), ldo=136), 1), (dict(out=FAKE), 1), (dict(a=None), 1), (dict(b=FAKE + 8), 1), (dict(ids=None), 1),
     (dict(ids=FAKE + 2), 1), (dict(scale=FAKE + 2), 1), (dict(ws=None), 1), (dict(ws=FAKE + 64), 1), (dict(size=256), 3),
     (dict(m=0, x=None), 0),
 ])
@@ -114,25 +118,34 @@ def test_workspaces_never_shrink_with_tokens(B):
             last = n.value
 
 
-def test_what_shares_memory(B):
-    t = torch.zeros(10, 64, dtype=torch.bfloat16)
-    left, right = t[:, :24], t[:, 24:]
-    assert not B._share(left, right) and not B._share(right, left) and B._share(left, t) and B._share(t, right)
-    assert B._share(t[:, 8:32], t[:, 24:40]) and not B._share(t[:4], t[4:]) and B._share(t[:5], t[4:])
-    assert not B._share(t[2:4, :8], t[:, 8:16]) and B._share(t[2:4, :9], t[:, 8:16])
-    assert not B._share(t[:0], t) and B._share(t[3:4], t) and not B._share(t[3:4], t[4:])
-    assert B._share(t[:, 56:], t[1:, :]) and not B._share(t[:, 56:], t[1:, :8])
-    assert B._same(t, t.view(10, 64)) and not B._same(t, t[:5]) and not B._same(left, right)
+@pytest.mark.parametrize("kw,ok", [
+    (dict(), True),
+    (dict(y=FAKE + 128, out=FAKE + 128, ldx=192, ldy=192, ldo=192), True),          # side by side with x
+    (dict(y=FAKE + 112, out=FAKE + 112, ldx=192, ldy=192, ldo=192), False),         # ... and into its last columns
+    (dict(y=FAKE + 160, out=FAKE + 160, ldx=192, ldy=192, ldo=192), False),         # ... round to its next row's first
+    (dict(x=FAKE + 256, y=FAKE, out=FAKE, ldx=192, ldy=192, ldo=192), True),        # the other way about
+    (dict(out=FAKE + 4096 + 16, ldo=128), False),                                   # a part of y
+    (dict(out=FAKE + 4096, ldo=136), False),                                        # y's start, other rows
+    (dict(out=FAKE + 4096 + 200 * 256, ldo=128), True), (dict(out=FAKE + 4096 + 200 * 256 - 16, ldo=128), False),
+    (dict(m=1, out=FAKE + 4096, ldo=136), True), (dict(m=1, y=FAKE + 128, out=FAKE + 128), True),
+])
+def test_what_shares_memory(B, kw, ok):
+    """Calls refused for it fail there; the others come to the workspace that they lack."""
+    args = dict(LORA, x=FAKE, y=FAKE + 4096 + (1 << 20), out=FAKE + 8192 + (2 << 20), size=255) | kw
+    if "y" not in kw:
+        args["y"] = FAKE + 4096
+        args["x"] = FAKE + (1 << 24)
+    assert B.load_library().moe_lora_add(*args.values()) == (3 if ok else 1)
 
 
 @pytest.mark.parametrize("call,match", [
     (lambda B, t: B.moe_add_rmsnorm(t, t[0].float()), "x: "),
-    (lambda B, t: B.moe_add_rmsnorm_backward(t, t, t[0].float()), "dout: "),
+    (lambda B, t: B.moe_add_rmsnorm_backward(t, t, t[0].float()), "r: "),
     (lambda B, t: B.moe_balance_loss(t, t.int()), "logits: "),
     (lambda B, t: B.moe_balance_loss(t[0], t.int()), "logits: "),
     (lambda B, t: B.moe_route_backward(t.float(), t.int()), "logits: "),
-    (lambda B, t: B.moe_lora_add(t, t, t, t, t[0].int()), r"a: \[n, r, k\]"),
-    (lambda B, t: B.moe_lora_add(t, t, t[None], t[None], t[0].int()), "a: "),
+    (lambda B, t: B.moe_lora_add(t, t, t, t, t[0].int()), "x: "),
+    (lambda B, t: B.moe_lora_add(t, t, t[None], t[None], t[0].int()), "x: "),
     (lambda B, t: B.moe_mxfp4_linear(t, t, t, adapters=(t, t, None)), "adapter_ids"),
     (lambda B, t: B.moe_mxfp4_linear(t, t, t, adapter_ids=t), "adapters"),
 ])
