@@ -636,7 +636,7 @@ def moe_mxfp4_dequant(codes, scales, stream=None):
     return out
 
 
-_spaces = {}  # (device, stream) -> workspace of the MXFP4 products launched on that stream, _Workspaces
+_spaces = {}  # (device, stream) -> workspace of the operators without a handle launched on that stream, _Workspaces
 # Held from the choice of such a workspace to the last launch that uses it: a product may be two
 # launches, and other threads run during the library's calls.
 _spaces_lock = threading.RLock()
@@ -658,6 +658,16 @@ def _space(like, stream: int, need: int) -> torch.Tensor:
         past.called(ws)
         _spaces[key] = ws, past
     return ws
+
+
+def _scratch(like, stream: int, need: int):
+    """(address, what keeps it) of `need` bytes for a call on `stream` that keeps nothing in them: behind
+    the header of the stream's workspace, or a captured graph's own."""
+    if _capturing():
+        ws = _empty((need,), dtype=_U8, device=like.device)
+        return ws.data_ptr(), ws
+    ws = _space(like, stream, need + 256)
+    return ws.data_ptr() + 256, ws
 
 
 def mxfp4_device_status(stream=None) -> int:
@@ -1016,20 +1026,23 @@ def moe_add_rmsnorm_backward(dout, r, weight, eps=1e-6, dresidual=None, need_dw=
             ldq = _strided(dresidual, h, m, "dresidual")
         dres = dresidual.data_ptr()
     dx = _empty_like(r, memory_format=_dense_rows)
-    dw = to = ws = None
-    need = 0
-    if need_dw:
-        dw = _empty_like(weight) if m else torch.zeros_like(weight)
-        to = dw.data_ptr()
-        size = ctypes.c_size_t()
-        rc = lib.moe_add_rmsnorm_backward_workspace_size(m, h, size)
+    st = _raw_stream(dev)
+    if not need_dw:
+        rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps, dres,
+                                          ldq, dx.data_ptr(), None, None, 0, st)
         if rc:
             raise MoeError(rc, "moe_add_rmsnorm_backward")
-        need = size.value
-        space = _empty((need,), dtype=_U8, device=r.device)
-        ws = space.data_ptr()
-    rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps, dres, ldq,
-                                      dx.data_ptr(), to, ws, need, _raw_stream(dev))
+        return dx, None
+    dw = _empty_like(weight) if m else torch.zeros_like(weight)
+    size = ctypes.c_size_t()
+    rc = lib.moe_add_rmsnorm_backward_workspace_size(m, h, size)
+    if rc:
+        raise MoeError(rc, "moe_add_rmsnorm_backward")
+    need = size.value
+    with _spaces_lock:
+        ws, _kept = _scratch(r, st, need)
+        rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps, dres,
+                                          ldq, dx.data_ptr(), dw.data_ptr(), ws, need, st)
     if rc:
         raise MoeError(rc, "moe_add_rmsnorm_backward")
     return dx, dw
@@ -1077,9 +1090,11 @@ def moe_balance_loss(logits, topk_ids, seq_offsets=None, scoring="softmax", stre
     counts = new((S, E), dtype=_I32, device=on)
     # what moe_balance_loss_workspace_size returns
     need = (4 * S + 255) // 256 * 256 + (((m + 7) // 8 + S) * 8 + 255) // 256 * 256
-    ws = _empty((need,), dtype=_U8, device=on)
-    rc = lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, off, S, mode, balance.data_ptr(),
-                              z.data_ptr(), counts.data_ptr(), ws.data_ptr(), need, _raw_stream(dev))
+    st = _raw_stream(dev)
+    with _spaces_lock:
+        ws, _kept = _scratch(logits, st, need)
+        rc = lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), m, E, k, off, S, mode, balance.data_ptr(),
+                                  z.data_ptr(), counts.data_ptr(), ws, need, st)
     if rc:
         raise MoeError(rc, "moe_balance_loss")
     return balance, z, counts

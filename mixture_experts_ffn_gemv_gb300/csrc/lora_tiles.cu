@@ -36,7 +36,7 @@ using namespace sm100;
 constexpr int BM = 128, BK = 64;
 constexpr int X_BYTES = BM * BK * 2;  // a box of 128 rows x 64 columns, 128-byte swizzle
 constexpr uint64_t DRAIN_NS = 2000000000ull;
-constexpr int TMEM_COLS = 256;
+constexpr int SHRINK_COLS = 256;  // of tensor memory: two blocks on an SM
 
 // The adapters of a tile's tokens.
 struct Tile {
@@ -91,21 +91,22 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
 // ---------------------------------------------------------------- A x
 
 constexpr int SHRINK_THREADS = 192;
+constexpr int SHRINK_SMEM = 110 * 1024;  // two blocks on an SM
 
-__global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_constant__ LoraArgs p) {
+__global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
     __shared__ uint64_t bars[2 * 8 + 3];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t sbase = smem_u32(smem), stride = X_BYTES + p.a_bytes;
+    const uint32_t sbase = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + 8), tfull = smem_u32(bars + 16),
                    tempty = smem_u32(bars + 17), drain = smem_u32(bars + 18);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int z = blockIdx.y, m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
+        for (int s = 0; s < 8; ++s) {
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
@@ -120,13 +121,16 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
     list_adapters(p, m0, tl);
     if (tl.count == 0) return;  // the whole block: nothing is allocated yet
     if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+        tmem_alloc(smem_u32(&tmem_slot), SHRINK_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    // a stage holds a box of x and the rows of A of as many adapters as the tile has (or a pass takes)
+    const uint32_t stride = X_BYTES + (min(tl.count, p.group) * p.r + 15) / 16 * (16 * BK * 2);
+    const uint32_t stages = min(8u, (uint32_t)(SHRINK_SMEM - 1024) / stride);
     const int k0 = z * p.split_blocks, k1 = min(p.kblocks, k0 + p.split_blocks);
     const int passes = (tl.count + p.group - 1) / p.group;
 
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
                 }
                 __syncwarp();
                 ++n;
-                if (++s == (uint32_t)p.stages) {
+                if (++s == stages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
             set_error(p.hdr, DEV_ERR_TIMEOUT, 61);
             abort_flag = 1;
         }
-        const uint32_t S = p.stages;
+        const uint32_t S = stages;
         for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(full0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         uint32_t s = 0, ph = 0;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
                     if (kb == k1 - 1) mma_commit(tfull);
                 }
                 __syncwarp();
-                if (++s == (uint32_t)p.stages) {
+                if (++s == stages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -235,46 +239,49 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 1) lora_shrink(const __grid_co
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_dealloc(tmem, SHRINK_COLS);
     }
 }
 
 // ---------------------------------------------------------------- y + T B^T
 
 constexpr int BN = 128;
-constexpr int EPI_WARPS = 8;
+constexpr int TEAMS = 2, TEAM_WARPS = 8;  // epilogue warps: the teams take tiles in turn
+constexpr int EPI_WARPS = TEAMS * TEAM_WARPS;
 constexpr int EXPAND_THREADS = 32 * (2 + EPI_WARPS);
-constexpr int MAX_Y = 5, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
+// Accumulators and stages of y are each one team's own: a team waits for the phases of
+// a barrier one after another, which a parity alone tells apart.
+constexpr int ND = 2 * TEAMS, EXPAND_COLS = ND * BN;
+constexpr int YS = 2 * TEAMS, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
 constexpr int MAX_B = 4;
 
 __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
-    __shared__ uint64_t bars[2 * MAX_Y + 2 * MAX_B + 6];
+    __shared__ uint64_t bars[2 * YS + 2 * MAX_B + 2 * ND + 2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nb = (p.r + BK - 1) / BK;  // boxes along r
-    const uint32_t YS = p.y_stages;
     // T's first parts, its second parts, y, B
     const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + YS * Y_BYTES;
-    const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * MAX_Y, bfull0 = yempty0 + 8 * MAX_Y,
-                   bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 16,
-                   tready = dempty0 + 16, drain = tready + 8;
+    const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * YS, bfull0 = yempty0 + 8 * YS,
+                   bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 8 * ND,
+                   tready = dempty0 + 8 * ND, drain = tready + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.y_stages; ++s) {
+        for (int s = 0; s < YS; ++s) {
             mbar_init(yfull0 + 8 * s, 1);
-            mbar_init(yempty0 + 8 * s, EPI_WARPS);
+            mbar_init(yempty0 + 8 * s, TEAM_WARPS);
         }
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(bfull0 + 8 * s, 1);
             mbar_init(bempty0 + 8 * s, 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < ND; ++s) {
             mbar_init(dfull0 + 8 * s, 1);
-            mbar_init(dempty0 + 8 * s, EPI_WARPS);
+            mbar_init(dempty0 + 8 * s, TEAM_WARPS);
         }
         mbar_init(tready, EPI_WARPS);
         mbar_init(drain, 1);
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         return;
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+        tmem_alloc(smem_u32(&tmem_slot), EXPAND_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -340,15 +347,16 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             abort_flag = 1;
         }
         const uint32_t S = p.stages;
-        for (uint32_t i = yn > YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
+        for (uint32_t i = yn > (uint32_t)YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
         for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
     } else if (warp == 1) {
-        uint32_t bs = 0, bph = 0, d = 0;
+        uint32_t bs = 0, bph = 0, tile = 0;
         bool ok = tl.count == 0 || warp_wait(tready, 0, p.wait_ns);
         tc_fence_after();
-        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas)
-            for (int u = 0; u < tl.count && ok; ++u, ++d) {
-                if (warp_sees(&abort_flag) || !warp_wait(dempty0 + 8 * (d & 1), ((d >> 1) & 1u) ^ 1u, p.wait_ns)) {
+        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
+            for (int u = 0; u < tl.count && ok; ++u) {
+                const uint32_t turn = tile / TEAMS * tl.count + u, d = tile % TEAMS * 2 + (turn & 1);
+                if (warp_sees(&abort_flag) || !warp_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -363,11 +371,11 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                     const int steps = min(4, (p.r - kb * BK + 15) / 16);
                     if (elect_one()) {
                         for (int kk = 0; kk < steps; ++kk) {
-                            mma_bf16(tmem + (d & 1) * BN, hi + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), (kb | kk) != 0);
-                            mma_bf16(tmem + (d & 1) * BN, lo + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), 1);
+                            mma_bf16(tmem + d * BN, hi + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), (kb | kk) != 0);
+                            mma_bf16(tmem + d * BN, lo + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), 1);
                         }
                         mma_commit(bempty0 + 8 * bs);
-                        if (kb == nb - 1) mma_commit(dfull0 + 8 * (d & 1));
+                        if (kb == nb - 1) mma_commit(dfull0 + 8 * d);
                     }
                     __syncwarp();
                     if (++bs == (uint32_t)p.stages) {
@@ -384,23 +392,32 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         mbar_wait(drain, 0, DRAIN_NS);
         __syncwarp();
     } else {
-        const int q4 = warp & 3, half = (warp - 2) >> 2;  // lane quarter, which 64 columns
+        const int q4 = warp & 3, half = ((warp - 2) >> 2) & 1, team = (warp - 2) / TEAM_WARPS;  // lane quarter, which 64 columns
         const int row = q4 * 32 + lane, slot = tl.slot[row];
         pdl_wait();
         pdl_trigger();
         if (tl.count) {
-            // this row's T (its pieces of 8, every second one), then zeros up to a multiple of 16
+            // this row's T (its pieces of 8, every fourth one), then zeros up to a multiple of 16
             const int pieces = (p.r + 15) / 16 * 2;
             const float* src = p.part + (size_t)(m0 + row) * p.r;
             const float scale = slot >= 0 && p.scale ? p.scale[tl.id[row]] : 1.f;
-            for (int c = half; c < pieces; c += 2) {
+            for (int c = (warp - 2) >> 2; c < pieces; c += EPI_WARPS / 4) {
                 float v[8] = {};
                 if (slot >= 0 && 8 * c < p.r) {
-                    for (int z = 0; z < p.splits; ++z) {
-                        const float4* q = reinterpret_cast<const float4*>(src + (size_t)z * p.m * p.r + 8 * c);
-                        const float4 f = q[0], g = q[1];
-                        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
-                        v[4] += g.x; v[5] += g.y; v[6] += g.z; v[7] += g.w;
+                    for (int z0 = 0; z0 < p.splits; z0 += 4) {
+                        float4 f[4], g[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const bool in = z0 + z < p.splits;
+                            const float4* q = reinterpret_cast<const float4*>(src + (size_t)(z0 + z) * p.m * p.r + 8 * c);
+                            f[z] = in ? q[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+                            g[z] = in ? q[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            v[0] += f[z].x; v[1] += f[z].y; v[2] += f[z].z; v[3] += f[z].w;
+                            v[4] += g[z].x; v[5] += g[z].y; v[6] += g[z].z; v[7] += g[z].w;
+                        }
                     }
                 }
                 uint32_t hi[4], lo[4];
@@ -420,18 +437,20 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(tready);
         }
-        uint32_t ys = 0, yph = 0, d = 0;
         int before = -1;  // the stage whose stores are still being read
         bool ok = true;
-        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
-            if (warp_sees(&abort_flag) || !warp_wait(yfull0 + 8 * ys, yph, p.wait_ns)) {
+        uint32_t tile = team;
+        for (int nt = blockIdx.y + team * p.n_ctas; nt < p.n_tiles && ok; nt += TEAMS * p.n_ctas, tile += TEAMS) {
+            const uint32_t ys = tile % YS;
+            if (warp_sees(&abort_flag) || !warp_wait(yfull0 + 8 * ys, (tile / YS) & 1u, p.wait_ns)) {
                 ok = false;
                 break;
             }
             const int col = nt * BN + 64 * half;
             const uint32_t box = y_at + ys * Y_BYTES + half * X_BYTES, line = box + row * 128;
-            for (int u = 0; u < tl.count; ++u, ++d) {
-                if (!warp_wait(dfull0 + 8 * (d & 1), (d >> 1) & 1u, p.wait_ns)) {
+            for (int u = 0; u < tl.count; ++u) {
+                const uint32_t turn = tile / TEAMS * tl.count + u, d = team * 2 + (turn & 1);
+                if (!warp_wait(dfull0 + 8 * d, (turn >> 1) & 1u, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -439,14 +458,14 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 const bool own = slot == u, any = __any_sync(0xffffffffu, own);
                 uint32_t v[2][32];
                 if (any) {
-                    const uint32_t taddr = tmem + ((uint32_t)(q4 * 32) << 16) + (d & 1) * BN + 64 * half;
+                    const uint32_t taddr = tmem + ((uint32_t)(q4 * 32) << 16) + d * BN + 64 * half;
                     tmem_ld32(taddr, v[0]);
                     tmem_ld32(taddr + 32, v[1]);
                     tmem_wait_ld();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(dempty0 + 8 * (d & 1));
+                if (lane == 0) mbar_arrive(dempty0 + 8 * d);
                 if (own && col < p.N) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
@@ -476,10 +495,6 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 if (before >= 0) mbar_arrive(yempty0 + 8 * before);
             }
             before = (int)ys;
-            if (++ys == YS) {
-                ys = 0;
-                yph ^= 1u;
-            }
         }
         if (!ok && lane == 0) {
             set_error(p.hdr, DEV_ERR_TIMEOUT, 66);
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_dealloc(tmem, EXPAND_COLS);
     }
 }
 
@@ -503,19 +518,19 @@ int sms() {
 
 constexpr int kSmem = 225 * 1024;  // beside the static part (tile lists, barriers)
 
-// Slices of K: as many as fill the device, of at least 4 blocks of 64.
+// Slices of K: as many as fill the device twice over, of at least 4 blocks of 64.
 int split_blocks(int64_t m, int64_t K) {
     const int tiles = (int)std::min<int64_t>((m + BM - 1) / BM, 1 << 20), kblocks = (int)((K + BK - 1) / BK);
-    const int splits = std::max(1, std::min(sms() / tiles, kblocks / 4));
+    const int splits = std::max(1, std::min(2 * sms() / tiles, kblocks / 4));
     return ceil_div(kblocks, splits);
 }
 
 }  // namespace
 
-// Slices times tokens: tiles * splits is at most the SMs while there are splits.
+// Slices times tokens: tiles * splits is at most two an SM while there are splits.
 int64_t lora_part_floats(int64_t m, int64_t r) {
     if (m <= kLoraByToken) return 0;
-    return std::max<int64_t>(m, (int64_t)sms() * BM) * r;
+    return std::max<int64_t>(m, (int64_t)2 * sms() * BM) * r;
 }
 
 cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
@@ -524,7 +539,6 @@ cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
     p.split_blocks = split_blocks(p.m, p.K);
     p.splits = ceil_div(p.kblocks, p.split_blocks);
     p.group = std::min(std::min(256 / p.r, p.n), BM);
-    p.a_bytes = ceil_div(p.group * p.r, 16) * 16 * BK * 2;  // the MMA's N is a multiple of 16
     const uint64_t bdims[3] = {(uint64_t)p.r / 2, (uint64_t)p.N, (uint64_t)p.n};
     const uint64_t bstrides[2] = {(uint64_t)p.r * 2, (uint64_t)p.N * p.r * 2};
     const uint32_t bbox[3] = {BK / 2, BN, 1};
@@ -532,20 +546,18 @@ cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
         !tmap_encode_words(&p.mb, p.b, 3, bdims, bstrides, bbox) || !ffn_map(&p.my, p.y, p.m, p.N, p.ldy, BM) ||
         !ffn_map(&p.mo, p.out, p.m, p.N, p.ldo, 32))
         return cudaErrorUnknown;
-    cudaError_t e = allow_smem<lora_shrink>(kSmem);
+    cudaError_t e = allow_smem<lora_shrink>(SHRINK_SMEM);
     if (e == cudaSuccess) e = allow_smem<lora_expand>(kSmem);
     if (e != cudaSuccess) return e;
-    p.stages = std::min(8, (kSmem - 1024) / (X_BYTES + p.a_bytes));
-    e = launch_pdl(lora_shrink, dim3(tiles, p.splits), dim3(SHRINK_THREADS), 1024 + p.stages * (X_BYTES + p.a_bytes), st, p);
+    e = launch_pdl(lora_shrink, dim3(tiles, p.splits), dim3(SHRINK_THREADS), SHRINK_SMEM, st, p);
     if (e != cudaSuccess) return e;
     const int nb = ceil_div(p.r, BK);
     p.n_tiles = ceil_div(p.N, BN);
     p.n_ctas = std::max(1, std::min(p.n_tiles, sms() / tiles));
     const int room = kSmem - 1024 - 2 * nb * X_BYTES;
-    p.stages = 2;
-    p.y_stages = std::min(MAX_Y, (room - p.stages * X_BYTES) / Y_BYTES);
+    p.stages = std::min(MAX_B, (room - YS * Y_BYTES) / X_BYTES);
     return launch_pdl(lora_expand, dim3(tiles, p.n_ctas), dim3(EXPAND_THREADS),
-                      1024 + 2 * nb * X_BYTES + p.y_stages * Y_BYTES + p.stages * X_BYTES, st, p);
+                      1024 + 2 * nb * X_BYTES + YS * Y_BYTES + p.stages * X_BYTES, st, p);
 }
 
 }  // namespace moe

@@ -79,9 +79,8 @@ struct LoraArgs {
     float* part;       // [splits, m, r]: A x by slices of K
     int splits, kblocks, split_blocks;
     int group;         // adapters whose products share a pass over x
-    int a_bytes, stages;  // shrink: a stage's part for A; stages
-    int n_tiles, n_ctas;  // expand: tiles of N, blocks that share them, stages of y (of B: stages)
-    int y_stages;
+    int n_tiles, n_ctas;  // expand: tiles of N, blocks that share them
+    int stages;           // ... stages of B
     CUtensorMap mx, ma, mb, my, mo;
 };
 constexpr int kLoraMaxRank = 128;
