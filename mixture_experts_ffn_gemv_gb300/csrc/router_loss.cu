@@ -43,7 +43,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxChunk = 128;   // tokens of a block
 constexpr int kMinChunk = 8;     // ... at least: what one round of 32-lane groups takes
-constexpr int kIdsAhead = 16;    // ids that a counting thread has on their way
+// Threads of a counting block: what a block alone waits for is itself, and more of them take
+// longer to start (333 tokens 5.8 -> 6.8 us with 512); a cluster's long ranges want more.
+template <int cluster>
+constexpr int kCountThreads = cluster == 1 ? 256 : 512;
+constexpr int kIdsAhead = 8;     // ids that a counting thread has on their way
+constexpr int kPartsAhead = 8;   // chunks' sums that a lane has on their way
 constexpr int kOffsShared = 512; // sequences whose offsets a block keeps in shared memory
 
 // The tokens of sequence s, within [0, m] whatever the offsets hold.
@@ -61,17 +66,17 @@ __device__ __forceinline__ void span(const RouterArgs& a, int s, int& t0, int& t
 // distributed shared memory.  Nothing has to be zeroed before and no atomics reach
 // global memory.  It also opens the losses' tickets.
 template <int cluster>
-__global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a) {
+__global__ void __launch_bounds__(kCountThreads<cluster>) count_pairs(const RouterArgs a) {
     __shared__ int hist[kMaxExperts];
     const int s = blockIdx.x / cluster, rank = blockIdx.x % cluster;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += kCountThreads<cluster>) hist[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
     int t0, t1;
     span(a, s, t0, t1);
-    const int64_t end = (int64_t)t1 * a.k, step = (int64_t)cluster * kThreads;
-    int64_t p = (int64_t)t0 * a.k + rank * kThreads + threadIdx.x;
+    const int64_t end = (int64_t)t1 * a.k, step = (int64_t)cluster * kCountThreads<cluster>;
+    int64_t p = (int64_t)t0 * a.k + rank * kCountThreads<cluster> + threadIdx.x;
     for (; p < end; p += kIdsAhead * step) {
         int id[kIdsAhead];
 #pragma unroll
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a) {
     __syncthreads();
     if (cluster > 1) sm100::cluster_sync();
     const uint32_t h = sm100::smem_u32(hist);
-    for (int e = rank * kThreads + threadIdx.x; e < a.E; e += cluster * kThreads) {
+    for (int e = rank * kCountThreads<cluster> + threadIdx.x; e < a.E; e += cluster * kCountThreads<cluster>) {
         int n = 0;
         if (cluster > 1) {
             int v[cluster];
@@ -104,18 +109,20 @@ __global__ void __launch_bounds__(kThreads) count_pairs(const RouterArgs a) {
     if (cluster > 1) sm100::cluster_sync();  // the others may still read this block's histogram
 }
 
-// Sums and maxima over the G lanes of a token.
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+// Sums and maxima over the G lanes of a token, of several values at once.
+template <int G, int M>
+__device__ __forceinline__ void group_sum(float (&v)[M]) {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < M; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
+template <int G, int M>
+__device__ __forceinline__ void group_max(float (&v)[M]) {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < M; ++k) v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], o));
 }
 
 // exp(v) of v <= 0, as 2^(v log2 e): off by 2^-22 and by the product's rounding, |v| 2^-24,
@@ -125,23 +132,24 @@ __device__ __forceinline__ float exp_neg(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
     return r;
 }
-// 1 / v of 1 <= v <= 2, within 2^-23.
+// 1 / v of a normal v up to 2^126, within 2^-23; 0 of 0.
 __device__ __forceinline__ float inverse(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return v == 0.f ? 0.f : r;
+}
+
+// ... of a v that is not 0.
+__device__ __forceinline__ float inverse_of_some(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 
-// sigma(l) and 1 - sigma(l), neither by a difference.
-__device__ __forceinline__ void logistic(float l, float& s, float& rest) {
-    const float e = exp_neg(-fabsf(l)), big = inverse(1.0f + e), small = e * big;
-    s = l >= 0.f ? big : small;
-    rest = l >= 0.f ? small : big;
-}
-// sigma(l) / exp(shift) and 1 - sigma(l), shift = min(0, the largest l): sums of the first do not
+// sigma(l) / exp(shift) and 1 - sigma(l), neither by a difference, shift = min(0, the largest l): sums of the first do not
 // underflow where all l are far below zero.  low: shift < 0, for any lane of the warp.
 __device__ __forceinline__ float shifted_logistic(float l, float shift, bool low, float& rest) {
-    const float e = exp_neg(-fabsf(l)), big = inverse(1.0f + e);
+    const float e = exp_neg(-fabsf(l)), big = inverse_of_some(1.0f + e);
     rest = l >= 0.f ? e * big : big;
     if (low) return (l >= 0.f ? 1.0f : exp_neg(l - shift)) * big;
     return l >= 0.f ? big : e * big;
@@ -195,6 +203,19 @@ struct Row {
         }
     }
 };
+
+// The scores of a token's logits, and their complements.
+template <int G, int VEC, int NV>
+__device__ __forceinline__ void scores(const Row<G, VEC, NV>& l, float shift, bool low, Row<G, VEC, NV>& p,
+                                       Row<G, VEC, NV>& rest) {
+    if (low) {
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) p.v[n] = shifted_logistic(l.v[n], shift, true, rest.v[n]);
+    } else {
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) p.v[n] = shifted_logistic(l.v[n], shift, false, rest.v[n]);
+    }
+}
 
 // The sequence of each token of the block's chunk, -1 outside of all.
 struct Chunk {
@@ -250,38 +271,46 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
     find_sequences(a, first, ch);
     pdl_wait();
     pdl_trigger();
+    Row<G, VEC, NV> c;  // counts of sequence `of`
+    int of = -1;
     for (int r = 0; r < a.chunk; r += GROUPS) {  // warps stay together
         const int j = r + group, s = j < a.chunk ? ch.seq[j] : -1;
-        Row<G, VEC, NV> l, c;
+        Row<G, VEC, NV> l;
         if (kAhead) {
             l = next;
             next = load(r + GROUPS);
         } else {
             l = load(r);
         }
-        c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
-        float top = -INFINITY;
+        if (s != of || r == 0) {
+            c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
+            of = s;
+        }
+        float top[1] = {-INFINITY};
 #pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
-        top = group_max<G>(top);
-        const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
+        for (int n = 0; n < NV * VEC; ++n) top[0] = fmaxf(top[0], l.v[n]);
+        group_max<G>(top);
+        const float at = top[0] == -INFINITY ? 0.f : top[0], shift = fminf(at, 0.f);
         const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
-        float sum = 0.f, den = 0.f, q = 0.f;
+        float sum[3] = {};  // of exp(l - at), of the scores, of the scores times their counts
+        Row<G, VEC, NV> p, rest;
 #pragma unroll
         for (int n = 0; n < NV * VEC; ++n) {
-            const float e = exp_neg(l.v[n] - at);
-            float rest;
-            const float p = SIGMOID ? shifted_logistic(l.v[n], shift, low, rest) : e;
-            sum += e;
-            den += p;
-            q = fmaf(p, c.v[n], q);
+            p.v[n] = exp_neg(l.v[n] - at);
+            sum[0] += p.v[n];
         }
-        sum = group_sum<G>(sum);
-        den = SIGMOID ? group_sum<G>(den) : sum;
-        q = group_sum<G>(q);
-        const float lse = at + logf(sum);
+        if (SIGMOID) {
+            scores(l, shift, low, p, rest);
+#pragma unroll
+            for (int n = 0; n < NV * VEC; ++n) sum[1] += p.v[n];
+        }
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) sum[2] = fmaf(p.v[n], c.v[n], sum[2]);
+        group_sum<G>(sum);
+        const float lse = at + logf(sum[0]);
         if (i == 0 && j < a.chunk)
-            each[j] = s < 0 ? make_float2(0.f, 0.f) : make_float2(den == 0.f ? 0.f : q / den, sum == 0.f ? 0.f : lse * lse);
+            each[j] = s < 0 ? make_float2(0.f, 0.f)
+                            : make_float2(sum[2] * inverse(SIGMOID ? sum[1] : sum[0]), sum[0] == 0.f ? 0.f : lse * lse);
     }
     __syncthreads();
     const int last = min(first + a.chunk, a.m);
@@ -315,17 +344,23 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
         int done = 0;
         if (lane == 0) {
             a.part[blockIdx.x + s] = make_float2(q, z);
-            __threadfence();
-            done = atomicAdd(&a.ticket[s], 1) == c1 - c0;
-            __threadfence();
+            int before;  // after this block's sums, before the others' are read
+            asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.ticket + s) : "memory");
+            done = before == c1 - c0;
         }
         if (!__shfl_sync(0xffffffffu, done, 0)) continue;
         __syncwarp();  // the other lanes' reads come after lane 0's
         double qs = 0.0, zs = 0.0;
-        for (int c = c0 + lane; c <= c1; c += 32) {
-            const float2 v = __ldcg(&a.part[c + s]);
-            qs += (double)v.x;
-            zs += (double)v.y;
+        for (int c = c0 + lane; c <= c1; c += 32 * kPartsAhead) {
+            float2 v[kPartsAhead];
+#pragma unroll
+            for (int n = 0; n < kPartsAhead; ++n)
+                v[n] = c + 32 * n <= c1 ? __ldcg(&a.part[c + 32 * n + s]) : make_float2(0.f, 0.f);
+#pragma unroll
+            for (int n = 0; n < kPartsAhead; ++n) {
+                qs += (double)v[n].x;
+                zs += (double)v[n].y;
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -343,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
 // The gradient of the logits: of the routing weights, and of the losses for tokens
 // of sequences.  Pick j of a token is lane j % G's, its number j / G there.
 template <bool SIGMOID, int G, int VEC, int NV>
-__global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 1) route_backward(const RouterArgs a) {
+__global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 3 : 1) route_backward(const RouterArgs a) {
     __shared__ Chunk ch;
     extern __shared__ float4 row_mem[];  // [GROUPS, E], zero between tokens
     float* row_of = reinterpret_cast<float*>(row_mem);
@@ -358,118 +393,157 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 4 : 1) route_backwar
     const bool losses = a.dbalance || a.dz;
     if (losses) find_sequences(a, first, ch);
     constexpr int PICKS = G == 32 ? 1 : 4;  // k <= min(E, 32), and G < 32 only where E <= 4 G
+    constexpr bool kAhead = NV * VEC <= 8;  // registers for the next token's logits
+    struct Picks {
+        int id[PICKS];
+        float dk[PICKS];
+    };
+    auto load_picks = [&](int r) {
+        Picks x;
+        const int j = r + group, t = first + j;
+#pragma unroll
+        for (int n = 0; n < PICKS; ++n) {
+            const int pick = n * G + i;
+            const bool in = a.dtopk_w && j < a.chunk && t < a.m && pick < a.k;
+            x.id[n] = in ? a.ids[(size_t)t * a.k + pick] : -1;
+            x.dk[n] = in ? a.dtopk_w[(size_t)t * a.k + pick] : 0.f;
+        }
+        return x;
+    };
+    struct Token {
+        Row<G, VEC, NV> l;
+        int id[PICKS];
+        float dk[PICKS], lk[PICKS];
+    };
+    auto load = [&](int r, const Picks& picks) {
+        Token x;
+        const int j = r + group, t = first + j;
+        const float* row = a.logits + (size_t)t * a.E;
+        if (losses) x.l.load(row, i, a.E, j < a.chunk && t < a.m, -INFINITY);
+#pragma unroll
+        for (int n = 0; n < PICKS; ++n) {
+            x.id[n] = (unsigned)picks.id[n] < (unsigned)a.E ? picks.id[n] : -1;
+            x.dk[n] = picks.dk[n];
+            x.lk[n] = x.id[n] >= 0 ? row[x.id[n]] : -INFINITY;
+        }
+        return x;
+    };
+    // terms of sequence `of`: its counts less what an even share would be, factors of the two losses
+    Row<G, VEC, NV> c;
+    float db = 0.f, dz = 0.f;
+    int of = -2;
+    // the picks' logits are found through their ids: these are loaded a token earlier still
+    Picks later = load_picks(0);
+    Token next;
+    if (kAhead) {
+        next = load(0, later);
+        later = load_picks(GROUPS);
+    }
     for (int r = 0; r < a.chunk; r += GROUPS) {
         const int j = r + group, t = first + j;
         const bool live = j < a.chunk && t < a.m;
         const int s = losses && live ? ch.seq[j] : -1;
-        const float* row = a.logits + (size_t)t * a.E;
-        Row<G, VEC, NV> l;
-        l.load(row, i, a.E, live, -INFINITY);
-        // the picks: their expert, their gradient
-        int id[PICKS];
-        float dk[PICKS];
-        if (a.dtopk_w) {
-            float lk[PICKS], top = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < PICKS; ++n) {
-                const int pick = n * G + i;
-                const bool in = live && pick < a.k;
-                const int e = in ? a.ids[(size_t)t * a.k + pick] : -1;
-                id[n] = (unsigned)e < (unsigned)a.E ? e : -1;
-                dk[n] = id[n] >= 0 ? a.dtopk_w[(size_t)t * a.k + pick] : 0.f;
-                lk[n] = id[n] >= 0 ? row[id[n]] : -INFINITY;
-                top = fmaxf(top, lk[n]);
-            }
-            top = group_max<G>(top);
-            const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
-            const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
-            float w[PICKS], sum = 0.f, mean = 0.f;
-#pragma unroll
-            for (int n = 0; n < PICKS; ++n) {
-                float rest;
-                w[n] = SIGMOID ? shifted_logistic(lk[n], shift, low, rest) : exp_neg(lk[n] - at);
-                sum += w[n];
-            }
-            sum = group_sum<G>(sum);
-#pragma unroll
-            for (int n = 0; n < PICKS; ++n) {
-                w[n] = sum == 0.f ? 0.f : w[n] / sum;
-                mean = fmaf(w[n], dk[n], mean);
-            }
-            mean = group_sum<G>(mean);
-#pragma unroll
-            for (int n = 0; n < PICKS; ++n) {
-                if (SIGMOID) {
-                    float sg, rest;
-                    logistic(lk[n], sg, rest);
-                    dk[n] = a.scale * rest * (a.norm ? w[n] * (dk[n] - mean) : sg * dk[n]);
-                } else {
-                    dk[n] = w[n] * (dk[n] - mean);
-                }
-            }
+        Token x;
+        if (kAhead) {
+            x = next;
+            next = load(r + GROUPS, later);
+            later = load_picks(r + 2 * GROUPS);
+        } else {
+            x = load(r, later);
+            later = load_picks(r + GROUPS);
         }
-        Row<G, VEC, NV> d;
-#pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
-        if (losses) {
+        if (losses && s != of) {
             int t0 = 0, t1 = 1;
             if (s >= 0) span(a, s, t0, t1);
             const float T = (float)max(t1 - t0, 1);
-            const float db = s >= 0 && a.dbalance ? a.dbalance[s] * (float)a.E / ((float)a.k * T) / T : 0.f;
-            const float dz = s >= 0 && a.dz ? a.dz[s] / T : 0.f;
-            float top = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < NV * VEC; ++n) top = fmaxf(top, l.v[n]);
-            top = group_max<G>(top);
-            const float at = top == -INFINITY ? 0.f : top, shift = fminf(at, 0.f);
-            const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
-            Row<G, VEC, NV> p;
-            float inv = 0.f;
-            if (a.dz || !SIGMOID) {
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) {
-                    p.v[n] = exp_neg(l.v[n] - at);
-                    sum += p.v[n];
-                }
-                sum = group_sum<G>(sum);
-                inv = sum == 0.f ? 0.f : 1.0f / sum;
-                const float zc = a.dz ? dz * 2.f * (sum == 0.f ? 0.f : at + logf(sum)) * inv : 0.f;
-#pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) d.v[n] = zc * p.v[n];
-            }
+            dz = s >= 0 && a.dz ? a.dz[s] / T * 2.f : 0.f;
+            db = 0.f;
             if (a.dbalance) {
-                float mean = 0.f;
-                Row<G, VEC, NV> rest;
-                if (SIGMOID) {
-                    float den = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NV * VEC; ++n) {
-                        p.v[n] = shifted_logistic(l.v[n], shift, low, rest.v[n]);
-                        den += p.v[n];
-                    }
-                    den = group_sum<G>(den);
-                    inv = den == 0.f ? 0.f : 1.0f / den;
-                }
-                Row<G, VEC, NV> c;
+                if (s >= 0) db = a.dbalance[s] * (float)a.E / ((float)a.k * T) / T;
                 c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
                 const float even = (float)a.k * T / (float)a.E;
 #pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) {
-                    p.v[n] *= inv;
-                    c.v[n] -= even;
-                    mean = fmaf(p.v[n], c.v[n], mean);
-                }
-                mean = group_sum<G>(mean);
+                for (int n = 0; n < NV * VEC; ++n) c.v[n] -= even;
+            }
+            of = s;
+        }
+        float top[2] = {-INFINITY, -INFINITY};  // of the row, of the picks
+        if (losses) {
+#pragma unroll
+            for (int n = 0; n < NV * VEC; ++n) top[0] = fmaxf(top[0], x.l.v[n]);
+        }
+        if (a.dtopk_w) {
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) top[1] = fmaxf(top[1], x.lk[n]);
+        }
+        group_max<G>(top);
+        const float at = top[0] == -INFINITY ? 0.f : top[0], shift = fminf(at, 0.f);
+        const float pick_at = top[1] == -INFINITY ? 0.f : top[1], pick_shift = fminf(pick_at, 0.f);
+        const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f || pick_shift < 0.f);
+        // sums of: exp(l - at); the scores; the scores times c; the picks' scores; these times dw
+        float sum[5] = {};
+        Row<G, VEC, NV> e, p, rest;
+        float wk[PICKS], rest_k[PICKS];
+        if (losses) {
+            if (!SIGMOID || a.dz) {
 #pragma unroll
                 for (int n = 0; n < NV * VEC; ++n) {
-                    const float g = db * p.v[n] * (c.v[n] - mean);
+                    e.v[n] = exp_neg(x.l.v[n] - at);
+                    sum[0] += e.v[n];
+                }
+            }
+            if (a.dbalance) {
+                if (SIGMOID) {
+                    scores(x.l, shift, low, p, rest);
+#pragma unroll
+                    for (int n = 0; n < NV * VEC; ++n) sum[1] += p.v[n];
+                }
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) sum[2] = fmaf(SIGMOID ? p.v[n] : e.v[n], c.v[n], sum[2]);
+            }
+        }
+        if (a.dtopk_w) {
+#pragma unroll
+            for (int n = 0; n < PICKS; ++n) {
+                if (x.id[n] < 0) x.dk[n] = 0.f;
+                wk[n] = SIGMOID ? shifted_logistic(x.lk[n], pick_shift, low, rest_k[n]) : exp_neg(x.lk[n] - pick_at);
+                sum[3] += wk[n];
+                sum[4] = fmaf(wk[n], x.dk[n], sum[4]);
+            }
+        }
+        group_sum<G>(sum);
+        Row<G, VEC, NV> d;
+#pragma unroll
+        for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
+        if (losses && s >= 0) {  // padding gets nothing, whatever its logits hold
+            if (a.dz) {
+                const float f = sum[0] == 0.f ? 0.f : dz * (at + logf(sum[0])) * inverse_of_some(sum[0]);
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) d.v[n] = f * e.v[n];
+            }
+            if (a.dbalance) {
+                const float inv = inverse(SIGMOID ? sum[1] : sum[0]), mean = sum[2] * inv, f = db * inv;
+#pragma unroll
+                for (int n = 0; n < NV * VEC; ++n) {
+                    const float g = f * (SIGMOID ? p.v[n] : e.v[n]) * (c.v[n] - mean);
                     d.v[n] += SIGMOID ? g * rest.v[n] : g;
                 }
             }
-            if (s < 0) {  // padding, whatever its logits hold
+        }
+        int id[PICKS];
+        float dk[PICKS];
+        if (a.dtopk_w) {
+            const float inv = inverse(sum[3]), mean = sum[4] * inv;
 #pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) d.v[n] = 0.f;
+            for (int n = 0; n < PICKS; ++n) {
+                id[n] = x.id[n];
+                const float w = wk[n] * inv;
+                if (!SIGMOID)
+                    dk[n] = w * (x.dk[n] - mean);
+                else if (a.norm)
+                    dk[n] = a.scale * rest_k[n] * w * (x.dk[n] - mean);
+                else
+                    dk[n] = a.scale * rest_k[n] * (wk[n] * exp_neg(pick_shift)) * x.dk[n];
             }
         }
         // The picks' gradients go to their experts' lanes through the group's row in shared memory,
@@ -566,10 +640,10 @@ int64_t balance_slots(int64_t m, int64_t S) { return (m + kMinChunk - 1) / kMinC
 
 cudaError_t launch_balance_loss(RouterArgs a, cudaStream_t st) {
     // a block counts 256 ids in a step; sequences that fill the device by themselves have one each
-    const int cluster = a.S >= sms() || (int64_t)a.m * a.k <= (int64_t)a.S * 4 * kThreads ? 1 : 8;
+    const int cluster = a.S >= sms() || (int64_t)a.m * a.k <= (int64_t)a.S * 1024 ? 1 : 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.S * cluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(cluster == 1 ? kCountThreads<1> : kCountThreads<8>);
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -591,7 +665,7 @@ cudaError_t launch_balance_loss(RouterArgs a, cudaStream_t st) {
 cudaError_t launch_route_backward(RouterArgs a, cudaStream_t st) {
     const bool wide = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits) && (!a.counts || aligned16(a.counts));
     return by_width(a.E, wide, [&](auto g, auto vec, auto nv) {
-        a.chunk = chunk_for(a.m, kThreads / g, 4);
+        a.chunk = chunk_for(a.m, kThreads / g, 3);
         const size_t smem = a.dtopk_w ? (size_t)(kThreads / g) * a.E * 4 : 0;  // at most 32 KB
         return launch_pdl(a.sigmoid ? route_backward<true, g, vec, nv> : route_backward<false, g, vec, nv>, dim3(ceil_div(a.m, a.chunk)), dim3(kThreads), smem, st, (const RouterArgs)a);
     });
