@@ -306,24 +306,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
         bool ok = true;
         for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
-            if (warp_sees(&abort_flag) || !warp_wait(yempty0 + 8 * ys, yph, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            const bool two = nt * BN + 64 < p.N;
-            if (elect_one()) {
-                const uint32_t dst = y_at + ys * Y_BYTES, bar = yfull0 + 8 * ys;
-                mbar_arrive_expect_tx(bar, two ? Y_BYTES : X_BYTES);
-                tma_load_3d(dst, &p.my, nt * (BN / 2), m0, 0, bar);
-                if (two) tma_load_3d(dst + X_BYTES, &p.my, nt * (BN / 2) + 32, m0, 0, bar);
-            }
-            __syncwarp();
-            ++yn;
-            if (++ys == YS) {
-                ys = 0;
-                yph ^= 1u;
-            }
-            for (int u = 0; u < tl.count && ok; ++u)
+            const auto load_b = [&](int u) {
                 for (int kb = 0; kb < nb; ++kb) {
                     if (warp_sees(&abort_flag) || !warp_wait(bempty0 + 8 * bs, bph, p.wait_ns)) {
                         ok = false;
@@ -341,6 +324,28 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                         bph ^= 1u;
                     }
                 }
+            };
+            // the first adapter's B ahead of y: its product is to be there when y is.  No more of
+            // them: products beyond the accumulators wait for the first ones' addition to y.
+            if (tl.count) load_b(0);
+            if (!ok || warp_sees(&abort_flag) || !warp_wait(yempty0 + 8 * ys, yph, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            const bool two = nt * BN + 64 < p.N;
+            if (elect_one()) {
+                const uint32_t dst = y_at + ys * Y_BYTES, bar = yfull0 + 8 * ys;
+                mbar_arrive_expect_tx(bar, two ? Y_BYTES : X_BYTES);
+                tma_load_3d(dst, &p.my, nt * (BN / 2), m0, 0, bar);
+                if (two) tma_load_3d(dst + X_BYTES, &p.my, nt * (BN / 2) + 32, m0, 0, bar);
+            }
+            __syncwarp();
+            ++yn;
+            if (++ys == YS) {
+                ys = 0;
+                yph ^= 1u;
+            }
+            for (int u = 1; u < tl.count && ok; ++u) load_b(u);
         }
         if (!ok && lane == 0) {
             set_error(p.hdr, DEV_ERR_TIMEOUT, 64);
@@ -397,21 +402,25 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         pdl_wait();
         pdl_trigger();
         if (tl.count) {
-            // this row's T (its pieces of 8, every fourth one), then zeros up to a multiple of 16
+            // T, a thread a piece of 8 of a row (zeros up to a multiple of 16): neighbouring lanes read
+            // neighbouring pieces of the sums.  (With a row to a lane each load touched 32 lines, and
+            // this took 6.7 us of a block's 29 at r = 64.)
             const int pieces = (p.r + 15) / 16 * 2;
-            const float* src = p.part + (size_t)(m0 + row) * p.r;
-            const float scale = slot >= 0 && p.scale ? p.scale[tl.id[row]] : 1.f;
-            for (int c = (warp - 2) >> 2; c < pieces; c += EPI_WARPS / 4) {
+            for (int q = (int)threadIdx.x - 64; q < BM * pieces; q += 32 * EPI_WARPS) {
+                const int i = q / pieces, c = q % pieces;
+                const bool own = tl.slot[i] >= 0;
+                const float scale = own && p.scale ? p.scale[tl.id[i]] : 1.f;
+                const float* src = p.part + (size_t)(m0 + i) * p.r + 8 * c;
                 float v[8] = {};
-                if (slot >= 0 && 8 * c < p.r) {
+                if (own && 8 * c < p.r) {
                     for (int z0 = 0; z0 < p.splits; z0 += 4) {
                         float4 f[4], g[4];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const bool in = z0 + z < p.splits;
-                            const float4* q = reinterpret_cast<const float4*>(src + (size_t)(z0 + z) * p.m * p.r + 8 * c);
-                            f[z] = in ? q[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-                            g[z] = in ? q[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float4* at = reinterpret_cast<const float4*>(src + (size_t)(z0 + z) * p.m * p.r);
+                            f[z] = in ? at[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+                            g[z] = in ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
@@ -422,14 +431,14 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 }
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = v[2 * i] * scale, b = v[2 * i + 1] * scale;
-                    hi[i] = pack_bf16x2(a, b);
-                    const float ah = bf16lo(hi[i]), bh = bf16hi(hi[i]);
+                for (int e = 0; e < 4; ++e) {
+                    const float a = v[2 * e] * scale, b = v[2 * e + 1] * scale;
+                    hi[e] = pack_bf16x2(a, b);
+                    const float ah = bf16lo(hi[e]), bh = bf16hi(hi[e]);
                     // an infinite first part is all there is of it
-                    lo[i] = pack_bf16x2(isinf(ah) ? 0.f : a - ah, isinf(bh) ? 0.f : b - bh);
+                    lo[e] = pack_bf16x2(isinf(ah) ? 0.f : a - ah, isinf(bh) ? 0.f : b - bh);
                 }
-                const uint32_t at = t_at + (c >> 3) * X_BYTES + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+                const uint32_t at = t_at + (c >> 3) * X_BYTES + i * 128 + (((c & 7) ^ (i & 7)) << 4);
                 sts128(at, hi[0], hi[1], hi[2], hi[3]);
                 sts128(at + nb * X_BYTES, lo[0], lo[1], lo[2], lo[3]);
             }
@@ -437,7 +446,6 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(tready);
         }
-        int before = -1;  // the stage whose stores are still being read
         bool ok = true;
         uint32_t tile = team;
         for (int nt = blockIdx.y + team * p.n_ctas; nt < p.n_tiles && ok; nt += TEAMS * p.n_ctas, tile += TEAMS) {
@@ -487,14 +495,10 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             if (lane == 0) {
                 if (col < p.N && m0 + q4 * 32 < p.m) {
                     tma_store_3d(&p.mo, col / 2, m0 + q4 * 32, 0, box + q4 * 4096);
-                    tma_store_wait_read_but1();
-                } else {
                     tma_store_wait_read();
                 }
-                // this thread's store of the stage before, if there was one, has been read
-                if (before >= 0) mbar_arrive(yempty0 + 8 * before);
+                mbar_arrive(yempty0 + 8 * ys);
             }
-            before = (int)ys;
         }
         if (!ok && lane == 0) {
             set_error(p.hdr, DEV_ERR_TIMEOUT, 66);
