@@ -108,7 +108,7 @@ MOE_API int moe_route_backward(const float* logits, const int32_t* topk_ids, int
  *   2^30.
  * workspace: moe_lora_add_workspace_size bytes, 256-byte aligned, its first 256
  * bytes (the header of moe_ffn.h) zero before its first use. */
-#define MOE_LORA_BY_TOKEN 64 /* up to so many tokens the header alone */
+#define MOE_LORA_BY_TOKEN 64 /* up to so many tokens it is the header alone */
 MOE_API int moe_lora_add_workspace_size(int64_t m, int64_t k, int64_t r, size_t* bytes);
 MOE_API int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y, int64_t ldy, int64_t d,
                          const void* a, const void* b, int64_t n, int64_t r, const int32_t* ids, const float* scale,

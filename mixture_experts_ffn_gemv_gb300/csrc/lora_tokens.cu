@@ -1,13 +1,17 @@
 // Low-rank adapters for few tokens: out[t] = y[t] + scale B (A x[t]), the
 // adapter of each token its own.
 //
-// A token belongs to a cluster of 8 blocks and one launch does all of it: each
-// block takes an eighth of K of A x, the blocks add their r partial sums up
-// through distributed shared memory (in the order of the blocks), and each takes
-// an eighth of the rows of B.  The first rows of B are on their way before the
-// sums are done.  What it reads is the token's A and B, 2 r (K + N) bytes; tokens
-// that share an adapter read it from L2.
+// A token belongs to a cluster of 8, 4 or 2 blocks (as many as let all clusters run
+// at once, two blocks an SM) and one launch does all of it: each block takes its
+// share of K of A x, the blocks add their r partial sums up through distributed
+// shared memory (in the order of the blocks), and each takes its share of the rows
+// of B.  The first rows of B are on their way before the sums are done.
+// What it reads is the token's A and B, 2 r (K + N) bytes; tokens that share an
+// adapter read it from L2.  Bound by that for many tokens (128 of rank 16, 7168 ->
+// 7168: 59 MB in 12.5 us), by the chain of loads, sums and loads for one (4.8 us).
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "launch.cuh"
@@ -172,15 +176,30 @@ int sms() {
     return n;
 }
 
+template <int LPR>
+cudaError_t launch_by_tokens(const LoraArgs& a, cudaStream_t st) {
+    const int room = 2 * sms();
+    return a.m * 8 <= room ? launch<LPR, 8>(a, st) : a.m * 4 <= room ? launch<LPR, 4>(a, st) : launch<LPR, 2>(a, st);
+}
+
 }  // namespace
 
+// Clusters by token, or tiles of 128 tokens?  Tiles read a shared adapter once, but each
+// adapter that occurs costs a tile its products and an accumulator's way through the
+// epilogue; by token it makes no difference who shares what.  In us, by token / by tiles,
+// tokens of 32 adapters mixed and (one for all): 2048 -> 7168, r = 16: 64 tokens 6.7 / 32
+// (6.5 / 9.3), 256 tokens 15 / 36 (15 / 10); 7168 -> 2048, r = 64: 64 tokens 13 / 50 (13 / 15),
+// 128 tokens 24 / 63 (23 / 21); 4096 -> 4096, r = 128, 16 adapters: 64 tokens 20 / 55 (20 / 17),
+// 128 tokens 37 / 61 (37 / 24).  So few tokens, weighed by their rank, go by token where
+// there are adapters to mix.
+bool lora_by_token(int m, int n, int r) { return m <= kLoraByToken || (n >= 4 && m * std::max(r, 32) <= 8192); }
+
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st) {
-    const bool eight = a.m * 8 <= 2 * sms();
-    if (a.r <= 8) return eight ? launch<1, 8>(a, st) : launch<1, 4>(a, st);
-    if (a.r <= 16) return eight ? launch<2, 8>(a, st) : launch<2, 4>(a, st);
-    if (a.r <= 32) return eight ? launch<4, 8>(a, st) : launch<4, 4>(a, st);
-    if (a.r <= 64) return eight ? launch<8, 8>(a, st) : launch<8, 4>(a, st);
-    return eight ? launch<16, 8>(a, st) : launch<16, 4>(a, st);
+    if (a.r <= 8) return launch_by_tokens<1>(a, st);
+    if (a.r <= 16) return launch_by_tokens<2>(a, st);
+    if (a.r <= 32) return launch_by_tokens<4>(a, st);
+    if (a.r <= 64) return launch_by_tokens<8>(a, st);
+    return launch_by_tokens<16>(a, st);
 }
 
 }  // namespace moe

@@ -84,7 +84,8 @@ struct LoraArgs {
     CUtensorMap mx, ma, mb, my, mo;
 };
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraByToken = MOE_LORA_BY_TOKEN;  // up to so many tokens: a cluster each
+constexpr int kLoraByToken = MOE_LORA_BY_TOKEN;  // up to so many tokens always a cluster each
+bool lora_by_token(int m, int n, int r);  // which of the two kernels
 int64_t lora_part_floats(int64_t m, int64_t r);  // never fewer for more tokens
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st);
 cudaError_t launch_lora_tiles(LoraArgs& a, cudaStream_t st);

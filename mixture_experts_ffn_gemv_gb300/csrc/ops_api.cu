@@ -244,7 +244,7 @@ int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y
     p.wait_ns = kWaitNs;
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align_up(sizeof(WsHeader)));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return status(p.m <= kLoraByToken ? launch_lora_tokens(p, st) : launch_lora_tiles(p, st));
+    return status(lora_by_token(p.m, p.n, p.r) ? launch_lora_tokens(p, st) : launch_lora_tiles(p, st));
 }
 
 }  // extern "C"
