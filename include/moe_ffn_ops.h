@@ -31,8 +31,10 @@ extern "C" {
  *   out bf16 [m, h] or NULL; it may be x (ldx == h).
  *   codes uint8 [m, h] (e4m3) and scales fp32 [m, ceil(h / 128)], both or
  *   neither: out in 8 bits as moe_act_quant_fp8 makes them, s = amax / 448 per
- *   128 columns (the last block may be shorter), but of out before it is rounded
- *   to bf16.  One of out and codes is wanted at least.
+ *   128 columns (the last block may be shorter; s = 1 and codes 0 also where
+ *   amax / 448 is below fp32's numbers), but of out before it is rounded to
+ *   bf16.  A row that holds an infinity or a NaN has NaN codes, at the NaN of
+ *   out.  One of out and codes is wanted at least.
  *   h a multiple of 8, up to 24576.
  * The norm is taken of the rounded r, as moe_forward_residual_rmsnorm takes it.
  * Sums are fp32: a row whose squares pass its range (|r| from about 1e19 on)

@@ -717,7 +717,10 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None, adapters=None, ada
         y = _empty((x.shape[0], codes.shape[0]), dtype=_BF16, device=x.device) if out is None else out
         _dense(y, _BF16, (x.shape[0], codes.shape[0]), "out")
         _lora_args(y, x, a, b, adapter_ids, scale, None, _device_of(x, "x"))  # refused before anything is launched
-        _need(x.data_ptr() != y.data_ptr(), "out: not x, where there are adapters")
+        if out is not None and x.numel():
+            at, to = x.data_ptr(), out.data_ptr()
+            _need(to + 2 * out.numel() <= at or at + 2 * ((x.shape[0] - 1) * x.stride(0) + x.shape[1]) <= to,
+                  "out: no part of x, where there are adapters")
         moe_mxfp4_linear(x, codes, scales, y)
         return moe_lora_add(y, x, a, b, adapter_ids, scale)
     _need(adapter_ids is None, "adapter_ids without adapters")

@@ -136,10 +136,11 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) add_rmsnorm(const NormArgs 
             }
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float s = top > 0.f ? __fdiv_rn(top, 448.0f) : 1.0f;
+            // a block of zeros, or too small for a scale: 1, and codes 0 of either sign (NaN stays)
+            const float q = __fdiv_rn(top, 448.0f), s = q > 0.f ? q : 1.0f;
+            const uint32_t keep = q > 0.f ? 0xffffffffu : 0x7f7f7f7fu;
             const QuotientBracket b = quotient_bracket(s);
             if (in) {
-                const uint32_t keep = top > 0.f ? 0xffffffffu : 0x7f7f7f7fu;  // a block of zeros: codes 0, of either sign
                 *reinterpret_cast<uint2*>(a.codes + (size_t)t * a.H + 8 * c) =
                     make_uint2(e4m3x4_quotient(f, s, b) & keep, e4m3x4_quotient(f + 4, s, b) & keep);
                 if ((c & 15) == 0) a.scales[(size_t)t * blocks + (c >> 4)] = s;

@@ -33,7 +33,8 @@ Rows rows16(const void* p, int64_t ld, int64_t n) { return {reinterpret_cast<uin
 // Whether two matrices of m rows share memory: their spans meet and, where their
 // rows are as far apart, so do their columns.
 bool share(const Rows& a, const Rows& b, int64_t m) {
-    if (!a.at || !b.at || a.at >= b.at + (m - 1) * b.ld + b.n || b.at >= a.at + (m - 1) * a.ld + a.n) return false;
+    const auto end = [&](const Rows& q) { return (unsigned __int128)q.at + (unsigned __int128)(m - 1) * q.ld + q.n; };
+    if (!a.at || !b.at || a.at >= end(b) || b.at >= end(a)) return false;
     if (m == 1 || a.ld != b.ld) return true;
     const int64_t ahead = b.at >= a.at ? (int64_t)(b.at - a.at) % a.ld : (a.ld - (int64_t)(a.at - b.at) % a.ld) % a.ld;
     return ahead < a.n || ahead + b.n > a.ld;
@@ -180,7 +181,8 @@ int moe_route_backward(const float* logits, const int32_t* topk_ids, int64_t m, 
                                            !std::isfinite(routed_scaling_factor)))
         return MOE_ERR_INVALID_ARG;
     if (m == 0) return MOE_OK;
-    if (bad_words(logits) || bad_words(topk_ids) || bad_words(dlogits) || dlogits == logits || !aligned(dtopk_w, 4) ||
+    const Rows rl{reinterpret_cast<uintptr_t>(logits), 4 * (int64_t)e, 4 * (int64_t)e}, rd{reinterpret_cast<uintptr_t>(dlogits), rl.ld, rl.n};
+    if (bad_words(logits) || bad_words(topk_ids) || bad_words(dlogits) || share(rd, rl, m) || !aligned(dtopk_w, 4) ||
         !aligned(counts, 4) || !aligned(dbalance, 4) || !aligned(dz, 4) || (dbalance && !counts))
         return MOE_ERR_INVALID_ARG;
     RouterArgs a{};

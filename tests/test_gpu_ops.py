@@ -91,6 +91,21 @@ def test_norm_codes_are_the_quantisers(B):
     assert torch.equal(n.codes, codes) and torch.equal(n.scales, scales) and (scales[:, 1] == 1).all()
 
 
+def test_norm_codes_of_values_too_small_for_a_scale(B):
+    """Blocks whose largest value over 448 is below fp32's numbers: zero codes with a scale of 1, beside
+    zeros and blocks of ordinary values."""
+    x = torch.ones(3, 512, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(512, device="cuda")
+    w[:128] = 1e-43
+    w[5], w[128:256] = 0.0, 1e-40
+    n = B.moe_add_rmsnorm(x, w, 0.0, fp8=True)
+    assert (n.scales[:, 0] == 1).all() and not n.codes[:, :128].any()
+    v = P.e4m3(n.codes) * n.scales.double().repeat_interleave(128, 1)
+    # 1e-40 / 448 is 159 of fp32's smallest steps, off by half a one: 2^-8 of the value, and e4m3's 2^-4
+    assert ((v[:, 128:256] - 1e-40).abs() <= 1e-40 * (2.0 ** -4 + 2.0 ** -7)).all()
+    assert (n.codes[:, 256:] == 0x7E).all()  # 448
+
+
 def test_norm_eight_bits_alone_and_in_place(B):
     m, h = 37, 1160
     x, res, w = _n(1, m, h), _n(2, m, h), _n(3, h, dtype=torch.float32)
@@ -292,6 +307,19 @@ def test_router_masked_logits(B, E, sigmoid):
     _within(d[5:6], want[5:6], bound[5:6] + 2.0 ** -15 * want[5:6].abs(), "dlogits far below zero")
 
 
+@pytest.mark.parametrize("E", [4, 48, 256])
+def test_router_logits_of_any_alignment(B, E):
+    """Logits that begin 4 bytes past a multiple of 16 give what aligned ones give, within the bounds
+    of both (they are added up in another order)."""
+    logits, ids = _router_case(90, E, 3)
+    off = torch.tensor([0, 40, 90], dtype=torch.int32, device="cuda")
+    odd = torch.empty(90 * E + 1, device="cuda")[1:].view(90, E)
+    odd.copy_(logits)
+    assert odd.data_ptr() % 16 == 4 and odd.is_contiguous()
+    for sigmoid in (False, True):
+        _check_router(B, odd, ids, off, sigmoid)
+
+
 def test_router_bad_rows_spoil_no_other(B):
     logits, ids = _router_case(30, 64, 4)
     off = torch.tensor([0, 10, 20, 28], dtype=torch.int32, device="cuda")
@@ -358,7 +386,8 @@ def test_router_takes_what_the_layer_routes(B):
 LORA_SIZES = [(1, 7168, 2048, 16, 8), (1, 8, 8, 8, 1), (2, 72, 1032, 128, 3), (5, 8200, 264, 24, 4), (64, 2048, 712, 16, 40),
               (33, 136, 136, 72, 5), (64, 264, 8200, 64, 2), (65, 64, 64, 8, 1), (66, 264, 200, 8, 5), (128, 256, 128, 16, 3),
               (129, 520, 1032, 32, 2), (300, 1016, 680, 64, 4), (300, 72, 520, 128, 7), (200, 4104, 264, 24, 60),
-              (1777, 1016, 2728, 8, 6), (513, 2048, 72, 72, 9), (2500, 328, 264, 48, 130)]
+              (1777, 1016, 2728, 8, 6), (513, 2048, 72, 72, 9), (2500, 328, 264, 48, 130),
+              (130, 8, 8, 8, 3), (140, 264, 136, 16, 4), (90, 520, 264, 64, 5), (700, 64, 1032, 120, 20)]
 
 
 def _lora_case(m, k, d, r, n, seed=0):
@@ -483,6 +512,56 @@ def test_linear_with_adapters(B, m):
     assert B.moe_mxfp4_linear(x, *w, out=out, adapters=(a, b, scale), adapter_ids=ids) is out and torch.equal(out, want)
 
 
+def test_refusals(B):
+    """What a call refuses, it refuses before anything is launched: the buffers stay as they are."""
+    m, h = 10, 64
+    x, res, w = _n(1, m, h), _n(2, m, h), _n(3, h, dtype=torch.float32)
+    logits, ids = _router_case(m, 8, 2)
+    a, b, one = _n(4, 3, 8, h), _n(5, 3, h, 8), torch.ones(1, device="cuda")
+    which = torch.zeros(m, dtype=torch.int32, device="cuda")
+    pair = B.moe_mxfp4_quant(_n(6, h, h))
+    wide = torch.zeros(m, 2 * h, dtype=torch.bfloat16, device="cuda")
+    kept = x.clone()
+    value = [
+        lambda: B.moe_add_rmsnorm(x.float(), w), lambda: B.moe_add_rmsnorm(x.T, w), lambda: B.moe_add_rmsnorm(x[0], w),
+        lambda: B.moe_add_rmsnorm(x[:, 1:57], w[:56]), lambda: B.moe_add_rmsnorm(x, w.bfloat16()), lambda: B.moe_add_rmsnorm(x, w[:32]),
+        lambda: B.moe_add_rmsnorm(x, w, residual=res[:5]), lambda: B.moe_add_rmsnorm(x, w, residual_out=res),
+        lambda: B.moe_add_rmsnorm(x, w, bf16=False), lambda: B.moe_add_rmsnorm(x, w, out=wide[:, :h]),
+        lambda: B.moe_add_rmsnorm(x, w, residual=res.cpu()), lambda: B.moe_add_rmsnorm(x, w, bf16=False, fp8=True, out=res),
+        lambda: B.moe_add_rmsnorm_backward(x, res[:5], w), lambda: B.moe_add_rmsnorm_backward(x.float(), res, w),
+        lambda: B.moe_add_rmsnorm_backward(x, res, w, dresidual=x[:, :32]),
+        lambda: B.moe_balance_loss(logits.double(), ids), lambda: B.moe_balance_loss(logits, ids.long()),
+        lambda: B.moe_balance_loss(logits, ids[:5]), lambda: B.moe_balance_loss(logits, ids, which[:1]),
+        lambda: B.moe_balance_loss(logits, ids, which[:4].long()), lambda: B.moe_balance_loss(logits, ids, scoring="relu"),
+        lambda: B.moe_route_backward(logits, ids, dbalance=one), lambda: B.moe_route_backward(logits, ids, dz=one[:0]),
+        lambda: B.moe_route_backward(logits, ids, torch.ones(m, 3, device="cuda")),
+        lambda: B.moe_lora_add(res, x, a, b, which.long()), lambda: B.moe_lora_add(res, x, a, b, which[:5]),
+        lambda: B.moe_lora_add(res, x, a, b[:, :, :4], which), lambda: B.moe_lora_add(res, x, a.float(), b, which),
+        lambda: B.moe_lora_add(res, x[:5], a, b, which), lambda: B.moe_lora_add(res, x, a, b, which, one),
+        lambda: B.moe_mxfp4_linear(x, *pair, adapters=(a, b, None)), lambda: B.moe_mxfp4_linear(x, *pair, adapter_ids=which),
+        lambda: B.moe_mxfp4_linear(x, *pair, out=x, adapters=(a, b, None), adapter_ids=which),
+        lambda: B.moe_mxfp4_linear(x.float(), *pair, adapters=(a, b, None), adapter_ids=which),
+    ]
+    library = [
+        (lambda: B.moe_add_rmsnorm(x, w, eps=-1.0), 1), (lambda: B.moe_add_rmsnorm(x, w, residual=res, out=res), 1),
+        (lambda: B.moe_add_rmsnorm(x, w, residual=res, residual_out=x), 1),
+        (lambda: B.moe_add_rmsnorm(torch.zeros(1, 24584, dtype=torch.bfloat16, device="cuda"), torch.ones(24584, device="cuda")), 2),
+        (lambda: B.moe_route_backward(logits, ids, scoring="sigmoid", routed_scaling=0.0), 1),
+        (lambda: B.moe_balance_loss(torch.zeros(m, 1032, device="cuda"), ids), 2),
+        (lambda: B.moe_lora_add(x, x, a, b, which), 1), (lambda: B.moe_lora_add(res, x, a, b, which, out=x), 1),
+        (lambda: B.moe_lora_add(res, x, _n(4, 3, 136, h), _n(5, 3, h, 136), which), 2),
+        (lambda: B.moe_lora_add(res, x, _n(4, 3, 12, h), _n(5, 3, h, 12), which), 1),
+    ]
+    for call in value:
+        with pytest.raises(ValueError):
+            call()
+    for call, status in library:
+        with pytest.raises(B.MoeError) as e:
+            call()
+        assert e.value.status == status
+    assert torch.equal(x, kept)
+
+
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("m", [1, 7, 200])
 def test_experts_from_eight_bits(B, m, gate):
@@ -509,6 +588,45 @@ def test_experts_from_eight_bits(B, m, gate):
     # the two differ by x's rounding to bf16 ahead of its rounding to e4m3: at most one step of e4m3
     # in a code, 2^-3 of it, where it changes the code at all
     assert (a - b).norm() <= 2.0 ** -3 * b.norm() and layer.device_status() == 0
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_a_router_step_behind_the_norm(B, sigmoid):
+    """As a training step runs them: the norm, the layer's router and losses, the gradient of its logits,
+    of its weight and of its input, and through the norm, against 64 bits over all of it.
+    Roundings that the reference does not take: dlogits and the two products in fp32 (2^-18 of the sums of
+    magnitudes, far below the rest), the router's input gradient to bf16 ahead of the norm's backward pass
+    and that pass's result: 2^-9 of a value each on average at most, twice its own size through the norm
+    (it takes away the part along n) -- 2^-7 of the whole, in the 2-norm."""
+    from mixture_experts_ffn_gemv_gb300 import inputs as I
+    m, H, E, k = 200, 256, 16, 4
+    shape = I.LayerShape(hidden=H, num_experts=E, top_k=k, inter=128, scoring="sigmoid" if sigmoid else "softmax",
+                         routed_scaling=2.5 if sigmoid else 1.0)
+    ws = {n: _n(i, E, 128, H, std=0.05) for i, n in enumerate(("w1", "w3"))}
+    ws["w2"] = _n(3, E, H, 128, std=0.05)
+    layer = B.MoeLayer(shape, ws)
+    x, res, w, rw = _n(1, m, H), _n(2, m, H, std=2.0), 1 + _n(3, H, std=0.2, dtype=torch.float32), _n(4, E, H, std=0.1, dtype=torch.float32)
+    off = torch.tensor([0, 90, 190], dtype=torch.int32, device="cuda")
+    dw, db, dz = _n(5, m, k, dtype=torch.float32), torch.full((2,), 3.0, device="cuda"), torch.full((2,), 0.5, device="cuda")
+    n = B.moe_add_rmsnorm(x, w, residual=res)
+    ids, tw, logits = layer.moe_route(n.out, rw, logits=True)
+    assert torch.isfinite(layer.moe_experts(n.out, ids, tw)).all()
+    bal, z, counts = layer.moe_balance_loss(logits, ids, off)
+    d = layer.moe_route_backward(logits, ids, dw, db, dz, counts, off)
+    drw = d.T @ n.out.float()
+    dx, dweight = B.moe_add_rmsnorm_backward((d @ rw).to(torch.bfloat16), n.residual, w)
+
+    r64, w64, rw64 = (t.double().requires_grad_() for t in (n.residual, w, rw))
+    out = r64 / torch.sqrt(r64.square().mean(1, keepdim=True) + 1e-6) * w64
+    out = out + (n.out.double() - out).detach()  # as the router saw it
+    l = out @ rw64.T
+    b2, z2, c2 = P.router(l, ids, off, sigmoid)
+    total = (b2 * db.double()).sum() + (z2 * dz.double()).sum()
+    total = total + (P.route_weights(l, ids, sigmoid, True, 2.5 if sigmoid else 1.0) * dw.double()).sum()
+    want = torch.autograd.grad(total, (rw64, r64, w64))
+    assert torch.equal(counts, c2)
+    for got, ref, bound in zip((drw, dx, dweight), want, (2.0 ** -14, 2.0 ** -7, 2.0 ** -7)):
+        assert (got.double() - ref).norm() <= bound * ref.norm()
 
 
 # ---------------------------------------------------------------- calls together
