@@ -54,17 +54,15 @@ __device__ __forceinline__ void load_w8(const float* p, float (&v)[8]) {
 }
 
 // The sum of v over a row's threads, in a fixed order: a warp's butterfly, then
-// the block's warps one after another.  buf: a float per warp, two of them used
-// in turn by callers that loop.
+// every warp's over the block's warps.  buf: a float per warp.
 template <bool WARP>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
     v = warp_sum(v);
     if (WARP) return v;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    float t = 0.f;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) t += buf[i];
-    return t;
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < (int)(blockDim.x >> 5) ? buf[lane] : 0.f);
 }
 
 // Threads up to 512 for up to 4 pieces each; wider rows have 1024 threads.
@@ -231,12 +229,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs 
         if (warps > 1) {
             if ((threadIdx.x & 31) == 0) buf[turn][warp] = make_float2(ss, gr);
             group_sync(g, T);
-            ss = gr = 0.f;
-            for (int k = g * warps; k < (g + 1) * warps; ++k) {
-                const float2 b = buf[turn][k];
-                ss += b.x;
-                gr += b.y;
-            }
+            const float2 b = (int)(threadIdx.x & 31) < warps ? buf[turn][g * warps + (threadIdx.x & 31)] : make_float2(0.f, 0.f);
+            ss = warp_sum(b.x);
+            gr = warp_sum(b.y);
         }
         const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
         const float mean = gr / (float)a.H * inv;  // of g n
