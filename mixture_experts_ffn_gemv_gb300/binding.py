@@ -1003,6 +1003,9 @@ def moe_add_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, out=N
     return NormOut(out, residual_out, codes, scales)
 
 
+_grad_space = {}  # (m, h) -> moe_add_rmsnorm_backward_workspace_size
+
+
 def moe_add_rmsnorm_backward(dout, r, weight, eps=1e-6, dresidual=None, need_dw=True, stream=None):
     """Gradients (dx bf16 [m, h], dweight fp32 [h]) of moe_add_rmsnorm's out, given the r that it
     normalised (its residual, or x where there was none); dx is the gradient of x and of the residual
@@ -1037,11 +1040,15 @@ def moe_add_rmsnorm_backward(dout, r, weight, eps=1e-6, dresidual=None, need_dw=
             raise MoeError(rc, "moe_add_rmsnorm_backward")
         return dx, None
     dw = _empty_like(weight) if m else torch.zeros_like(weight)
-    size = ctypes.c_size_t()
-    rc = lib.moe_add_rmsnorm_backward_workspace_size(m, h, size)
-    if rc:
-        raise MoeError(rc, "moe_add_rmsnorm_backward")
-    need = size.value
+    need = _grad_space.get((m, h))
+    if need is None:
+        size = ctypes.c_size_t()
+        rc = lib.moe_add_rmsnorm_backward_workspace_size(m, h, size)
+        if rc:
+            raise MoeError(rc, "moe_add_rmsnorm_backward")
+        if len(_grad_space) >= 1024:
+            _grad_space.clear()
+        need = _grad_space[m, h] = size.value
     with _spaces_lock:
         ws, _kept = _scratch(r, st, need)
         rc = lib.moe_add_rmsnorm_backward(dout.data_ptr(), ldd, r.data_ptr(), ldr, m, h, weight.data_ptr(), eps, dres,
@@ -1089,7 +1096,8 @@ def moe_balance_loss(logits, topk_ids, seq_offsets=None, scoring="softmax", stre
     m, E, k, S, off, mode = _router_args(logits, topk_ids, seq_offsets, scoring, dev)
     on = logits.device
     new = _empty if m else torch.zeros
-    balance, z = new((2, S), dtype=_F32, device=on).unbind()
+    balance = new((S,), dtype=_F32, device=on)  # two tensors: rows of one cost more than its allocation
+    z = _empty_like(balance) if m else torch.zeros_like(balance)
     counts = new((S, E), dtype=_I32, device=on)
     # what moe_balance_loss_workspace_size returns
     need = (4 * S + 255) // 256 * 256 + (((m + 7) // 8 + S) * 8 + 255) // 256 * 256
