@@ -1,7 +1,8 @@
 """GB300-native MoE FFN layer forward (router, softmax top-k, permute, grouped
 SwiGLU experts, weighted unpermute-reduce, shared-expert add) behind a C-ABI
 CUDA library, with the dense gated feed-forward block (forward, backward, and
-served from MXFP4 weights) and the MXFP4 operators beside it.
+served from MXFP4 weights) and the MXFP4 operators beside it, and around both the
+norm, the router's losses with the gradient of its logits, and low-rank adapters.
 
 The compute lives in ``libmoe_ffn_gb300.so`` (hand-written sm_103a kernels);
 ``binding`` marshals torch tensors into its entry points.  The library is

@@ -16,6 +16,13 @@
 // own added to y in shared memory, rounded once, and out by TMA.  y and the first
 // B are loaded before the shrink kernel ends.
 // Each: warp 0 TMA producer, warp 1 MMA issuer, then the epilogue warps.
+//
+// 8192 tokens, 7168 -> 7168, r = 64, 4 requests: 68.6 us for 360 MB (52.9 at the copy
+// rate): shrink some 24 of them (17 at that rate), two launches' start and end and T's
+// way between them 10, expand 30.  In one kernel, clusters handing T over through
+// distributed shared memory, the same took 79 us: blocks wait for the slowest of their
+// cluster (5 us), and the exchange itself takes 4.  A tile of many adapters pays for each
+// about as much as for one: 256 tokens of 32 adapters, r = 16, 36 us, of one 10.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -8,7 +8,9 @@
 // with; out is rounded once, to bf16 and (from the same fp32 values) to e4m3.
 // Every element is read once and every result written once: a row stays in
 // registers, as the bf16 pairs it was rounded to, between its sum and its
-// scaling.  Bound by HBM for many rows, by one row's latency for few.
+// scaling.  Bound by HBM for many rows: 16384 x 7168 with residual and both outputs
+// (1061 MB) in 158 us, 6.7 TB/s; by one row's way through a block for few: 2.9 us for
+// one row of 7168.
 //
 // A row belongs to a warp (H up to 1024) or to a block; a thread holds V pieces
 // of 8 columns, piece v at v * threads + thread, so that 16 neighbouring lanes
@@ -182,6 +184,11 @@ __device__ __forceinline__ void group_sync(int g, int T) { asm volatile("bar.syn
 // rows of its group (T threads take a row, a block has several groups), the
 // groups of a block are added in shared memory and the blocks' sums [blocks, H]
 // by column_sums, each in its order.
+// 16384 x 2048 (268 MB) in 49.5 us, 5.4 TB/s, some 4 of it the sums of dw.  Registers
+// leave 1024 threads to an SM, whose loads, sums and stores hide each other only so
+// far: rows wider than 8192 columns, a block to an SM, reach 0.5 to 0.75 of the copy
+// rate.  (Copying the next row to shared memory meanwhile cost more than it hid:
+// 16384 x 2048 53 -> 59 us at the time, 4096 x 16384 126 -> 141.)
 template <int V>
 __global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs a, int T) {
     __shared__ float2 buf[2][32];
