@@ -67,7 +67,8 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
     return warp_sum(lane < (int)(blockDim.x >> 5) ? buf[lane] : 0.f);
 }
 
-// Threads up to 512 for up to 4 pieces each; wider rows have 1024 threads.
+// A block's rows have two pieces a thread (three above 16384 columns): with one, 16384 x
+// 7168 take 203 us instead of 161.
 template <int V, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) add_rmsnorm(const NormArgs a) {
     __shared__ float buf[32];
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs 
         const float inv = 1.0f / sqrtf(ss / (float)a.H + a.eps);
         const float mean = gr / (float)a.H * inv;  // of g n
         const Pair inv2{inv, inv};
-        const Pair back{-mean * inv * inv, -mean * inv * inv};
+        const Pair back{-mean * inv, -mean * inv};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = v * T + i;
@@ -257,8 +258,9 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const Pair f = unpack2(rw[j]), e = unpack2(ew[j]);
-                    dw[v][j] = fma2(e, mul2(f, inv2), dw[v][j]);
-                    const Pair x = fma2(mul2(e, w[j]), inv2, fma2(f, back, unpack2(qw[j])));
+                    const Pair nj = mul2(f, inv2);
+                    dw[v][j] = fma2(e, nj, dw[v][j]);
+                    const Pair x = fma2(mul2(e, w[j]), inv2, fma2(nj, back, unpack2(qw[j])));
                     o[j] = pack_bf16x2(x.x, x.y);
                 }
                 *reinterpret_cast<uint4*>(a.dx + (size_t)t * a.H + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(512) column_sums(const float* __restrict__ par
     float v = 0.f;
     if (c < H) {
 #pragma unroll 10
-        for (int p = warp; p < P; p += 16) v += part[(size_t)p * H + c];
+        for (int p = warp; p < P; p += 16) v += __ldcg(part + (size_t)p * H + c);
     }
     s[warp][lane] = v;
     __syncthreads();
@@ -316,16 +318,6 @@ int sms() {
     return n;
 }
 
-// Pieces a thread holds and threads of a block for rows of H columns.
-struct RowShape {
-    int v, threads;
-};
-RowShape row_shape(int H, int want_v) {
-    const int pieces = H / 8;
-    int v = std::max(want_v, ceil_div(pieces, 1024));
-    return {v, ceil_div(ceil_div(pieces, v), 32) * 32};
-}
-
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st) {
@@ -338,13 +330,9 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st) {
             default: return launch_pdl(add_rmsnorm<4, true>, grid, block, 0, st, a);
         }
     }
-    const RowShape s = row_shape(a.H, 2);
-    const dim3 grid(a.m), block(s.threads);
-    switch (s.v) {
-        case 1: return launch_pdl(add_rmsnorm<1, false>, grid, block, 0, st, a);
-        case 2: return launch_pdl(add_rmsnorm<2, false>, grid, block, 0, st, a);
-        default: return launch_pdl(add_rmsnorm<3, false>, grid, block, 0, st, a);
-    }
+    const int v = a.H <= 16384 ? 2 : 3;
+    const dim3 grid(a.m), block(ceil_div(ceil_div(a.H / 8, v), 32) * 32);
+    return v == 2 ? launch_pdl(add_rmsnorm<2, false>, grid, block, 0, st, a) : launch_pdl(add_rmsnorm<3, false>, grid, block, 0, st, a);
 }
 
 namespace {
@@ -363,6 +351,7 @@ GradShape grad_shape(int m, int H) {
     s.blocks = std::min(ceil_div(m, s.groups), sms() * (1024 / (s.T * s.groups)));
     return s;
 }
+
 }  // namespace
 
 // Blocks, at most, of m rows and of fewer: below s.most groups they are at most two an SM.

@@ -200,6 +200,20 @@ def test_norm_backward_against_differences(B):
         assert (dw[j].double() - diff).abs() <= bw[j] + 1e-9
 
 
+@pytest.mark.parametrize("h", [264, 2056])
+@pytest.mark.parametrize("size", [2.0 ** -55, 2.0 ** 55])
+def test_norm_of_very_small_and_large_rows(B, h, size):
+    """Rows whose squares are still fp32's, without eps: forward and backward as for rows of any size."""
+    r, dout, w = (_n(1, 5, h, dtype=torch.float32) * size).bfloat16(), _n(2, 5, h), _n(3, h, dtype=torch.float32)
+    n = B.moe_add_rmsnorm(r, w, 0.0, fp8=True)
+    _check_norm(B, n, r, None, w, 0.0, True)
+    dout = (dout.float() * size).bfloat16()  # dx is then of ordinary size
+    dx, dw = B.moe_add_rmsnorm_backward(dout, r, w, 0.0)
+    want, wdw, bx, bw = P.norm_backward(dout, r, w, 0.0, None)
+    _within(dx, want, bx, "dx")
+    _within(dw, wdw, bw, "dweight")
+
+
 def test_norm_backward_strided(B):
     m, h = 23, 1160
     r, dout, dres, w = _n(1, m, h), _n(2, m, h), _n(3, m, h), _n(4, h, dtype=torch.float32)
@@ -358,6 +372,36 @@ def test_router_against_differences(B):
             up[t, e] += 1e-4
             dn[t, e] -= 1e-4
             assert (d[t, e].double() - (loss(up) - loss(dn)) / 2e-4).abs() <= bound[t, e] + 1e-7
+
+
+def test_router_of_no_tokens(B):
+    logits, ids = torch.zeros(0, 8, device="cuda"), torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    bal, z, counts = B.moe_balance_loss(logits, ids, off)
+    assert not bal.any() and not z.any() and counts.shape == (3, 8) and not counts.any()
+    assert B.moe_route_backward(logits, ids, seq_offsets=off, dz=z).shape == (0, 8)
+
+
+def test_router_offsets_that_make_no_sense_touch_nothing_else(B):
+    """Falling offsets and such outside the tokens: values unspecified, nothing written around the
+    outputs and the right values in the calls after."""
+    logits, ids = _router_case(300, 16, 2)
+    good = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    want = B.moe_balance_loss(logits, ids, good)
+    one = torch.ones(2, device="cuda")
+    for bad in ([200, 100, 50], [-5, 1000, 40], [2 ** 31 - 1, -2 ** 31, 7], [-2 ** 31, 2 ** 31 - 1, -1]):
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        lib, p = B.load_library(), B._p
+        out = torch.full((4096,), 7.0, device="cuda")
+        counts = torch.full((4096,), 7, dtype=torch.int32, device="cuda")
+        ws = torch.full((1 << 16,), 0x5A, dtype=torch.uint8, device="cuda")
+        st = torch.cuda.current_stream().cuda_stream
+        assert lib.moe_balance_loss(p(logits), p(ids), 300, 16, 2, p(off), 2, 0, p(out[1024:]), p(out[2048:]), p(counts[1024:]), p(ws), 1024, st) == 0
+        d = B.moe_route_backward(logits, ids, dbalance=one, dz=one, counts=counts[1024:1056].view(2, 16), seq_offsets=off)
+        torch.cuda.synchronize()
+        assert (out[:1024] == 7).all() and (out[1026:2048] == 7).all() and (out[2050:] == 7).all()
+        assert (counts[:1024] == 7).all() and (counts[1056:] == 7).all() and (ws[1024:] == 0x5A).all() and d.shape == (300, 16)
+        assert all(torch.equal(a, b) for a, b in zip(B.moe_balance_loss(logits, ids, good), want))
 
 
 def test_router_takes_what_the_layer_routes(B):
