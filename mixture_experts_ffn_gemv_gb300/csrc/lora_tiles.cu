@@ -253,11 +253,14 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
 // ---------------------------------------------------------------- y + T B^T
 
 constexpr int BN = 128;
-constexpr int TEAMS = 2, TEAM_WARPS = 8;  // epilogue warps: the teams take tiles in turn
+// Epilogue warps.  The teams take tiles in turn or, where a tile has many adapters (from
+// MANY on), every second adapter of each tile.
+constexpr int TEAMS = 2, TEAM_WARPS = 8, MANY = 4;
 constexpr int EPI_WARPS = TEAMS * TEAM_WARPS;
 constexpr int EXPAND_THREADS = 32 * (2 + EPI_WARPS);
-// Accumulators and stages of y are each one team's own: a team waits for the phases of
-// a barrier one after another, which a parity alone tells apart.
+// Accumulators are each one team's own, and so are stages of y unless both teams take
+// every tile: whoever waits for the phases of a barrier waits for each of them, one after
+// another, which a parity alone tells apart.
 constexpr int ND = 2 * TEAMS, EXPAND_COLS = ND * BN;
 constexpr int YS = 2 * TEAMS, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
 constexpr int MAX_B = 4;
@@ -265,7 +268,7 @@ constexpr int MAX_B = 4;
 __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
-    __shared__ uint64_t bars[2 * YS + 2 * MAX_B + 2 * ND + 2];
+    __shared__ uint64_t bars[2 * YS + 2 * MAX_B + 2 * ND + 3];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
     const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + YS * Y_BYTES;
     const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * YS, bfull0 = yempty0 + 8 * YS,
                    bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 8 * ND,
-                   tready = dempty0 + 8 * ND, drain = tready + 8;
+                   tready = dempty0 + 8 * ND, drain = tready + 8, tdone = drain + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
@@ -292,6 +295,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         }
         mbar_init(tready, EPI_WARPS);
         mbar_init(drain, 1);
+        mbar_init(tdone, EPI_WARPS);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -308,6 +312,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    const bool both = tl.count >= MANY;  // teams take every tile, and every second adapter of it
 
     if (warp == 0) {
         uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
@@ -363,11 +368,13 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
     } else if (warp == 1) {
         uint32_t bs = 0, bph = 0, tile = 0;
+        uint32_t turns[TEAMS] = {};  // products of each team so far
         bool ok = tl.count == 0 || warp_wait(tready, 0, p.wait_ns);
         tc_fence_after();
         for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
             for (int u = 0; u < tl.count && ok; ++u) {
-                const uint32_t turn = tile / TEAMS * tl.count + u, d = tile % TEAMS * 2 + (turn & 1);
+                const uint32_t team = (both ? (uint32_t)u : tile) % TEAMS, turn = team ? turns[1]++ : turns[0]++;
+                const uint32_t d = team * 2 + (turn & 1);
                 if (warp_sees(&abort_flag) || !warp_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns)) {
                     ok = false;
                     break;
@@ -454,8 +461,10 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             if (lane == 0) mbar_arrive(tready);
         }
         bool ok = true;
-        uint32_t tile = team;
-        for (int nt = blockIdx.y + team * p.n_ctas; nt < p.n_tiles && ok; nt += TEAMS * p.n_ctas, tile += TEAMS) {
+        uint32_t turn = 0;
+        const int u0 = both ? team : 0, du = both ? TEAMS : 1, dt = both ? 1 : TEAMS;
+        uint32_t tile = both ? 0 : team;
+        for (int nt = blockIdx.y + tile * p.n_ctas; nt < p.n_tiles && ok; nt += dt * p.n_ctas, tile += dt) {
             const uint32_t ys = tile % YS;
             if (warp_sees(&abort_flag) || !warp_wait(yfull0 + 8 * ys, (tile / YS) & 1u, p.wait_ns)) {
                 ok = false;
@@ -463,8 +472,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             }
             const int col = nt * BN + 64 * half;
             const uint32_t box = y_at + ys * Y_BYTES + half * X_BYTES, line = box + row * 128;
-            for (int u = 0; u < tl.count; ++u) {
-                const uint32_t turn = tile / TEAMS * tl.count + u, d = team * 2 + (turn & 1);
+            for (int u = u0; u < tl.count; u += du, ++turn) {
+                const uint32_t d = team * 2 + (turn & 1);
                 if (!warp_wait(dfull0 + 8 * d, (turn >> 1) & 1u, p.wait_ns)) {
                     ok = false;
                     break;
@@ -499,6 +508,14 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             if (!ok) break;
             fence_async_smem();
             __syncwarp();
+            if (both) {  // until the other team's rows are done too; the first team stores them all
+                if (lane == 0) mbar_arrive(tdone);
+                if (!warp_wait(tdone, tile & 1u, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (team) continue;
+            }
             if (lane == 0) {
                 if (col < p.N && m0 + q4 * 32 < p.m) {
                     tma_store_3d(&p.mo, col / 2, m0 + q4 * 32, 0, box + q4 * 4096);
