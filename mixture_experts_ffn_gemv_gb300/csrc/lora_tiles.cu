@@ -22,7 +22,7 @@
 // way between them 10, expand 30.  In one kernel, clusters handing T over through
 // distributed shared memory, the same took 79 us: blocks wait for the slowest of their
 // cluster (5 us), and the exchange itself takes 4.  A tile of many adapters pays for each
-// about as much as for one: 256 tokens of 32 adapters, r = 16, 36 us, of one 10.
+// about as much as for one: 256 tokens of 32 adapters, 2048 -> 7168, r = 16, 33 us, of one 10.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -546,10 +546,13 @@ int sms() {
 
 constexpr int kSmem = 225 * 1024;  // beside the static part (tile lists, barriers)
 
-// Slices of K: as many as fill the device twice over, of at least 4 blocks of 64.
+// Slices of K: as many as fill the device twice over, of at least 4 blocks of 64, and 16 at
+// most: every expand block reads them all (1024 tokens, 7168 -> 7168, r = 64, one adapter: 25.7
+// us with up to 28, 19.9 with 16, 19.2 with 12; 512 tokens of 64 adapters, 4096 -> 4096, r = 16:
+// 53 with 16, 57 with 12).
 int split_blocks(int64_t m, int64_t K) {
     const int tiles = (int)std::min<int64_t>((m + BM - 1) / BM, 1 << 20), kblocks = (int)((K + BK - 1) / BK);
-    const int splits = std::max(1, std::min(2 * sms() / tiles, kblocks / 4));
+    const int splits = std::max(1, std::min({2 * sms() / tiles, kblocks / 4, 16}));
     return ceil_div(kblocks, splits);
 }
 

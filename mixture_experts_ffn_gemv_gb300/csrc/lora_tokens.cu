@@ -187,10 +187,10 @@ cudaError_t launch_by_tokens(const LoraArgs& a, cudaStream_t st) {
 // Clusters by token, or tiles of 128 tokens?  Tiles read a shared adapter once, but each
 // adapter that occurs costs a tile its products and an accumulator's way through the
 // epilogue; by token it makes no difference who shares what.  In us, by token / by tiles,
-// tokens of 32 adapters mixed and (one for all): 2048 -> 7168, r = 16: 64 tokens 6.7 / 32
-// (6.5 / 9.3), 256 tokens 15 / 36 (15 / 10); 7168 -> 2048, r = 64: 64 tokens 13 / 50 (13 / 15),
-// 128 tokens 24 / 63 (23 / 21); 4096 -> 4096, r = 128, 16 adapters: 64 tokens 20 / 55 (20 / 17),
-// 128 tokens 37 / 61 (37 / 24).  So few tokens, weighed by their rank, go by token where
+// tokens of 32 adapters mixed and (one for all): 2048 -> 7168, r = 16: 64 tokens 6.6 / 29
+// (6.5 / 9.7), 256 tokens 15 / 33 (15 / 10); 7168 -> 2048, r = 64: 64 tokens 14 / 52 (13 / 13),
+// 128 tokens 28 / 64 (23 / 17); 4096 -> 4096, r = 128, 16 adapters: 64 tokens 25 / 54 (20 / 17),
+// 128 tokens 38 / 60 (36 / 23).  So few tokens, weighed by their rank, go by token where
 // there are adapters to mix.
 bool lora_by_token(int m, int n, int r) { return m <= kLoraByToken || (n >= 4 && m * std::max(r, 32) <= 8192); }
 
