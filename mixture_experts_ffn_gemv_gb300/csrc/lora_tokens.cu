@@ -192,7 +192,9 @@ cudaError_t launch_by_tokens(const LoraArgs& a, cudaStream_t st) {
 // 128 tokens 28 / 64 (23 / 17); 4096 -> 4096, r = 128, 16 adapters: 64 tokens 25 / 54 (20 / 17),
 // 128 tokens 38 / 60 (36 / 23).  So few tokens, weighed by their rank, go by token where
 // there are adapters to mix.
-bool lora_by_token(int m, int n, int r) { return m <= kLoraByToken || (n >= 4 && m * std::max(r, 32) <= 8192); }
+bool lora_by_token(int m, int n, int r) {
+    return m <= kLoraByToken || (n >= 4 && (int64_t)m * std::max(r, 32) <= 8192);
+}
 
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st) {
     if (a.r <= 8) return launch_by_tokens<1>(a, st);

@@ -746,6 +746,25 @@ def test_graphs_and_other_streams(B):
     assert B.mxfp4_device_status() == 0 and B.mxfp4_device_status(st) == 0
 
 
+def test_two_streams_at_once(B):
+    """Calls of all operators on two streams, and products on tensor memory beside them: what runs at the
+    same time shares neither workspaces nor tensor memory."""
+    states = [_state(31, 300), _state(32, 1000)]
+    w = [B.moe_mxfp4_quant(_n(40 + i, 520, 544, std=0.05)) for i in range(2)]
+    xs = [_n(50 + i, 400, 544) for i in range(2)]
+    want = [(*_all(B, t), B.moe_mxfp4_linear(x, *q)) for t, x, q in zip(states, xs, w)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(25):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append((*_all(B, states[i]), B.moe_mxfp4_linear(xs[i], *w[i])))
+    torch.cuda.synchronize()
+    assert all(_equal(g, want[i]) for i in range(2) for g in got[i])
+    assert all(B.mxfp4_device_status(st) == 0 for st in streams)
+
+
 def test_threads_on_one_stream(B):
     import threading
     states = [_state(20 + i, 150 + 10 * i) for i in range(4)]
@@ -784,6 +803,22 @@ def test_offsets_past_32_bits(B):
     want, bound = P.lora(n.out[-3:], x[-3:], a, b, ids[-3:], None)
     got = B.moe_lora_add(x, n.out, a, b, ids)
     _within(got[-3:], want, bound)
+
+
+@pytest.mark.parametrize("m", [5, 200])
+def test_adapters_past_32_bits(B, m):
+    """Adapters that lie past 4 GB and rows of 2^20 columns: the last adapter, first and last columns."""
+    n, r, d = 40, 64, 1 << 20
+    b = torch.zeros(n, d, r, dtype=torch.bfloat16, device="cuda")
+    b[-1] = _n(1, d, r, std=0.1)
+    x, y, a = _n(2, m, 72), _n(3, m, d), _n(4, n, r, 72, std=0.1)
+    ids = torch.full((m,), n - 1, dtype=torch.int32, device="cuda")
+    ids[1] = 0
+    out = B.moe_lora_add(y, x, a, b, ids, out=torch.empty_like(y))
+    for cut in (slice(0, 1000), slice(d // 2, d // 2 + 1000), slice(d - 1000, d)):
+        want, bound = P.lora(x, y[:, cut], a, b[:, cut], ids, None)
+        _within(out[:, cut], want, bound)
+    assert torch.equal(out[1], y[1])
 
 
 def test_router_offsets_past_32_bits(B):
