@@ -673,6 +673,29 @@ def test_a_router_step_behind_the_norm(B, sigmoid):
         assert (got.double() - ref).norm() <= bound * ref.norm()
 
 
+def test_experts_from_eight_bits_refusals(B):
+    import dataclasses
+    from mixture_experts_ffn_gemv_gb300 import inputs as I
+    shape = I.LayerShape(hidden=512, num_experts=4, top_k=2, inter=512, shared_inter=512, fp8=True, shared_gate=True)
+    layer = B.MoeLayer(shape, I.make_layer(dataclasses.replace(I.WORKLOADS["tiny"], shape=shape), seed=0, device=torch.device("cuda", 0)))
+    x = _n(1, 6, 512)
+    codes, scales = B.moe_act_quant_fp8(x)
+    ids, w = torch.zeros(6, 2, dtype=torch.int32, device="cuda"), torch.ones(6, 2, device="cuda")
+    assert layer.moe_experts_fp8(codes[:0], scales[:0], ids[:0], w[:0], x=x[:0]).shape == (0, 512)
+    for bad in ((codes[:5], scales, ids, w, x), (codes, scales[:, :2], ids, w, x), (codes, scales, ids.long(), w, x),
+                (codes, scales, ids, w[:, :1], x), (codes, scales, ids, w, x.float()), (x, scales, ids, w, x), (codes.cpu(), scales, ids, w, x)):
+        with pytest.raises(ValueError):
+            layer.moe_experts_fp8(*bad[:4], x=bad[4])
+    with pytest.raises(B.MoeError) as e:  # its shared expert has a gate
+        layer.moe_experts_fp8(codes, scales, ids, w)
+    assert e.value.status == B.MOE_ERR_INVALID_ARG
+    plain = I.LayerShape(hidden=512, num_experts=4, top_k=2, inter=512)
+    t = {k: torch.zeros(4, 512, 512, dtype=torch.bfloat16, device="cuda") for k in ("w1", "w3", "w2")}
+    with pytest.raises(B.MoeError) as e:
+        B.MoeLayer(plain, t).moe_experts_fp8(codes, scales, ids, w)
+    assert e.value.status == B.MOE_ERR_UNSUPPORTED
+
+
 # ---------------------------------------------------------------- calls together
 
 def _all(B, t):

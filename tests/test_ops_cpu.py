@@ -107,6 +107,11 @@ def test_lora_refuses(B, kw, want):
     assert _call(B.load_library().moe_lora_add, LORA, kw) == want
 
 
+def test_experts_from_eight_bits_need_a_layer(B):
+    lib = B.load_library()
+    assert lib.moe_experts_fp8(None, FAKE, FAKE, None, 1, FAKE, FAKE, FAKE, 0, FAKE, 1 << 20, None) == 1
+
+
 def test_workspaces_never_shrink_with_tokens(B):
     lib = B.load_library()
     for fn, args in ((lib.moe_lora_add_workspace_size, (4096, 64)), (lib.moe_add_rmsnorm_backward_workspace_size, (1032,)),
