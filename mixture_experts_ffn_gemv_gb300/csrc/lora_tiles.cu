@@ -59,7 +59,7 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
     int id = -1;
     if (i < BM) {
         if (m0 + i < p.m) {
-            id = p.ids[m0 + i];
+            id = __ldcg(p.ids + m0 + i);  // past L1: lora_expand reads them before it waits
             if (id < -1 || id >= p.n) {
                 set_error(p.hdr, DEV_ERR_BAD_ID, m0 + i);
                 id = -1;
@@ -68,6 +68,15 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
         tl.id[i] = id;
     }
     __syncthreads();
+    if (__syncthreads_and(i >= BM || m0 + i >= p.m || id == tl.id[0])) {  // one request's, as most tiles are
+        if (i < BM) tl.slot[i] = id >= 0 ? 0 : -1;
+        if (i == 0) {
+            tl.list[0] = id;
+            tl.count = id >= 0;
+        }
+        __syncthreads();
+        return;
+    }
     int first = i;
     if (i < BM) {
         for (int j = BM - 4; j >= 0; j -= 4) {

@@ -163,18 +163,21 @@ __device__ __forceinline__ float shifted_logistic(float l, float shift, bool low
 template <int G, int VEC, int NV>
 struct Row {
     float v[NV * VEC];
+    // PAST_L1: global memory, read before this kernel waits for the one ahead of it
+    template <bool PAST_L1 = false>
     __device__ __forceinline__ void load(const float* row, int i, int E, bool live, float none) {
+        const auto get = [](const auto* p) { return PAST_L1 ? __ldcg(p) : *p; };
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const int e = (i + G * n) * VEC;
             if (VEC == 4) {
-                const float4 q = live && e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(none, none, none, none);
+                const float4 q = live && e < E ? get(reinterpret_cast<const float4*>(row + e)) : make_float4(none, none, none, none);
                 v[n * VEC] = q.x;
                 v[n * VEC + VEC / 4] = q.y;
                 v[n * VEC + VEC / 2] = q.z;
                 v[n * VEC + VEC - 1] = q.w;
             } else {
-                v[n * VEC] = live && e < E ? row[e] : none;
+                v[n * VEC] = live && e < E ? get(row + e) : none;
             }
         }
     }
@@ -228,22 +231,22 @@ struct Chunk {
 __device__ __forceinline__ void find_sequences(const RouterArgs& a, int first, Chunk& ch) {
     const bool kept = a.off && a.S <= kOffsShared;
     if (kept)
-        for (int i = threadIdx.x; i <= a.S; i += kThreads) ch.off[i] = a.off[i];
+        for (int i = threadIdx.x; i <= a.S; i += kThreads) ch.off[i] = __ldcg(a.off + i);
     __syncthreads();
     if ((int)threadIdx.x < a.chunk) {
         const int t = first + threadIdx.x;
         int s = t < a.m ? 0 : -1;
         if (a.off && t < a.m) {
-            const int* off = kept ? ch.off : a.off;
+            const auto off = [&](int i) { return kept ? ch.off[i] : __ldcg(a.off + i); };
             int lo = 0, hi = a.S;  // the first s whose end is past t, S: none
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (off[mid + 1] > t)
+                if (off(mid + 1) > t)
                     hi = mid;
                 else
                     lo = mid + 1;
             }
-            s = lo < a.S && off[lo] <= t ? lo : -1;
+            s = lo < a.S && off(lo) <= t ? lo : -1;
         }
         ch.seq[threadIdx.x] = s;
     }
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
     auto load = [&](int r) {
         Row<G, VEC, NV> l;
         const int j = r + group;
-        l.load(a.logits + (size_t)(first + j) * a.E, i, a.E, j < a.chunk && first + j < a.m, -INFINITY);
+        l.template load<true>(a.logits + (size_t)(first + j) * a.E, i, a.E, j < a.chunk && first + j < a.m, -INFINITY);
         return l;
     };
     // logits and offsets are older than the counting kernel, whose counts alone are waited for
