@@ -6,7 +6,8 @@
 // takes the result of its own.  That spends products, which the tensor core has to
 // spare (r is small and everything here is bound by x, y and out), and saves
 // sorting, gathering and scattering: x, y and out move as TMA boxes.  Requests that
-// lie together make one or two adapters a tile.
+// lie together make one or two adapters a tile.  Where there are few tiles and many
+// adapters, several blocks share a tile's adapters: each token is one block's own.
 //
 // lora_shrink: part[z, t, :] = A x[t] over slice z of K.  Up to 256 / r adapters
 // share a pass over x: their rows of A are the MMA's N.
@@ -22,7 +23,7 @@
 // way between them 10, expand 30.  In one kernel, clusters handing T over through
 // distributed shared memory, the same took 79 us: blocks wait for the slowest of their
 // cluster (5 us), and the exchange itself takes 4.  A tile of many adapters pays for each
-// about as much as for one: 256 tokens of 32 adapters, 2048 -> 7168, r = 16, 33 us, of one 10.
+// about as much as for one: 2048 tokens of 64 adapters, 4096 -> 4096, r = 16, 123 us, of one 15.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -45,16 +46,23 @@ constexpr int X_BYTES = BM * BK * 2;  // a box of 128 rows x 64 columns, 128-byt
 constexpr uint64_t DRAIN_NS = 2000000000ull;
 constexpr int SHRINK_COLS = 256;  // of tensor memory: two blocks on an SM
 
-// The adapters of a tile's tokens.
+// A role of one thread waits; what is there already costs no look at the others' flag.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int* abort_flag) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return !*abort_flag && mbar_wait(bar, parity, limit_ns);
+}
+
+// The adapters of a tile's tokens, or this block's share of them: every gridDim.z-th.
 struct Tile {
     int id[BM];    // of each token, -1: none
     int list[BM];  // those that occur
-    int slot[BM];  // a token's place in the list, -1: none
+    int slot[BM];  // a token's place in the list, -1: none, -2: in another block's list
     uint32_t firsts[4];
     int count;
 };
 // By all threads of the block (at least 128).
 __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& tl) {
+    const int share = blockIdx.z, shares = gridDim.z;
     const int i = threadIdx.x;
     int id = -1;
     if (i < BM) {
@@ -69,10 +77,10 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
     }
     __syncthreads();
     if (__syncthreads_and(i >= BM || m0 + i >= p.m || id == tl.id[0])) {  // one request's, as most tiles are
-        if (i < BM) tl.slot[i] = id >= 0 ? 0 : -1;
+        if (i < BM) tl.slot[i] = id < 0 ? -1 : share ? -2 : 0;
         if (i == 0) {
             tl.list[0] = id;
-            tl.count = id >= 0;
+            tl.count = id >= 0 && !share;
         }
         __syncthreads();
         return;
@@ -93,12 +101,13 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
     if (i < BM) {
         int place = __popc(tl.firsts[first >> 5] & ((1u << (first & 31)) - 1u));
         for (int w = 0; w < first >> 5; ++w) place += __popc(tl.firsts[w]);
-        tl.slot[i] = id >= 0 ? place : -1;
-        if (id >= 0 && first == i) tl.list[place] = id;
+        const bool mine = place % shares == share;
+        tl.slot[i] = id < 0 ? -1 : mine ? place / shares : -2;
+        if (id >= 0 && first == i && mine) tl.list[place / shares] = id;
         if (i == 0) {
             int n = 0;
             for (int w = 0; w < 4; ++w) n += __popc(tl.firsts[w]);
-            tl.count = n;
+            tl.count = (n + shares - 1 - share) / shares;
         }
     }
     __syncthreads();
@@ -274,6 +283,7 @@ constexpr int ND = 2 * TEAMS, EXPAND_COLS = ND * BN;
 constexpr int YS = 2 * TEAMS, Y_BYTES = 2 * X_BYTES;  // two boxes of 64 columns
 constexpr int MAX_B = 4;
 
+template <bool SHARED>
 __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
@@ -309,7 +319,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         fence_barrier_init();
     }
     list_adapters(p, m0, tl);  // ids, like y, are older than the shrink kernel, whose sums alone are waited for
-    if (tl.count == 0 && p.out == p.y && p.ldo == p.ldy) {
+    // nothing of this block's: what no adapter changes is the first share's
+    if (tl.count == 0 && ((SHARED && blockIdx.z) || (p.out == p.y && p.ldo == p.ldy))) {
         pdl_wait();
         return;
     }
@@ -376,48 +387,48 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         for (uint32_t i = yn > (uint32_t)YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
         for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
     } else if (warp == 1) {
-        uint32_t bs = 0, bph = 0, tile = 0;
-        uint32_t turns[TEAMS] = {};  // products of each team so far
-        bool ok = tl.count == 0 || warp_wait(tready, 0, p.wait_ns);
-        tc_fence_after();
-        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
-            for (int u = 0; u < tl.count && ok; ++u) {
-                const uint32_t team = (both ? (uint32_t)u : tile) % TEAMS, turn = team ? turns[1]++ : turns[0]++;
-                const uint32_t d = team * 2 + (turn & 1);
-                if (warp_sees(&abort_flag) || !warp_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                for (int kb = 0; kb < nb; ++kb) {
-                    if (!warp_wait(bfull0 + 8 * bs, bph, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t hi = desc_sw128(t_at + kb * X_BYTES), lo = desc_sw128(t_at + (nb + kb) * X_BYTES),
-                                   bd = desc_sw128(b_at + bs * X_BYTES);
-                    const int steps = min(4, (p.r - kb * BK + 15) / 16);
-                    if (elect_one()) {
-                        for (int kk = 0; kk < steps; ++kk) {
-                            mma_bf16(tmem + d * BN, hi + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), (kb | kk) != 0);
-                            mma_bf16(tmem + d * BN, lo + 2 * kk, bd + 2 * kk, idesc_bf16(BM, BN), 1);
+        // One thread from first to last.  With the warp's votes and joins at each wait an adapter's
+        // turn took 950 cycles at r = 16, now 770 (300 tokens of 64 adapters, 4096 -> 4096: 42.5 -> 37 us).
+        if (elect_one()) {
+            uint32_t bs = 0, bph = 0, tile = 0;
+            uint32_t turn0 = 0, turn1 = 0;  // products of each team so far
+            bool ok = tl.count == 0 || role_wait(tready, 0, p.wait_ns, &abort_flag);
+            tc_fence_after();
+            const int count = tl.count, last = p.r - (nb - 1) * BK;
+            const uint32_t idesc = idesc_bf16(BM, BN);
+            for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
+                for (int u = 0; u < count && ok; ++u) {
+                    const uint32_t team = (both ? (uint32_t)u : tile) % TEAMS, turn = team ? turn1++ : turn0++;
+                    const uint32_t d = team * 2 + (turn & 1);
+                    ok = role_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns, &abort_flag);
+                    for (int kb = 0; kb < nb && ok; ++kb) {
+                        ok = role_wait(bfull0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t hi = desc_sw128(t_at + kb * X_BYTES), lo = desc_sw128(t_at + (nb + kb) * X_BYTES),
+                                       bd = desc_sw128(b_at + bs * X_BYTES);
+                        const int steps = kb < nb - 1 ? 4 : (last + 15) / 16;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk >= steps) break;
+                            mma_bf16(tmem + d * BN, hi + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                            mma_bf16(tmem + d * BN, lo + 2 * kk, bd + 2 * kk, idesc, 1);
                         }
                         mma_commit(bempty0 + 8 * bs);
                         if (kb == nb - 1) mma_commit(dfull0 + 8 * d);
-                    }
-                    __syncwarp();
-                    if (++bs == (uint32_t)p.stages) {
-                        bs = 0;
-                        bph ^= 1u;
+                        if (++bs == (uint32_t)p.stages) {
+                            bs = 0;
+                            bph ^= 1u;
+                        }
                     }
                 }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 65);
+                abort_flag = 1;
             }
-        if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 65);
-            abort_flag = 1;
+            mma_commit(drain);
+            mbar_wait(drain, 0, DRAIN_NS);
         }
-        if (elect_one()) mma_commit(drain);
-        mbar_wait(drain, 0, DRAIN_NS);
         __syncwarp();
     } else {
         const int q4 = warp & 3, half = ((warp - 2) >> 2) & 1, team = (warp - 2) / TEAM_WARPS;  // lane quarter, which 64 columns
@@ -525,8 +536,17 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 }
                 if (team) continue;
             }
+            if (SHARED) {  // rows of its own among those of other blocks
+                for (int i = lane >> 3; i < 32; i += 4) {
+                    const int at = q4 * 32 + i, c = lane & 7, its = tl.slot[at];
+                    if ((its >= 0 || (its == -1 && blockIdx.z == 0)) && m0 + at < p.m && col + 8 * c < p.N)
+                        *reinterpret_cast<uint4*>(p.out + (size_t)(m0 + at) * p.ldo + col + 8 * c) =
+                            lds128(box + at * 128 + ((c ^ (at & 7)) << 4));
+                }
+                __syncwarp();
+            }
             if (lane == 0) {
-                if (col < p.N && m0 + q4 * 32 < p.m) {
+                if (!SHARED && col < p.N && m0 + q4 * 32 < p.m) {
                     tma_store_3d(&p.mo, col / 2, m0 + q4 * 32, 0, box + q4 * 4096);
                     tma_store_wait_read();
                 }
@@ -567,6 +587,15 @@ int split_blocks(int64_t m, int64_t K) {
 
 }  // namespace
 
+// Blocks among which a tile's adapters may be shared, where tiles, slices and outputs leave SMs
+// idle: one for each 128 columns that all adapters together have.  Tokens that use one adapter do
+// not lose by it (its block works, the others leave), many adapters gain: 256 tokens of 32, 7168 ->
+// 2048, r = 64, 67 -> 25.5 us.  With a block for each adapter small ranks lose: 1777 tokens of 6,
+// 1016 -> 2728, r = 8, 12.7 -> 13.3.
+int shares(int n, int r) {
+    return std::max(1, std::min(BM, ceil_div((int)std::min<int64_t>((int64_t)n * r, BM * 128), 128)));
+}
+
 // Slices times tokens: tiles * splits is at most two an SM while there are splits.
 int64_t lora_part_floats(int64_t m, int64_t r) {
     if (m <= kLoraByToken) return 0;
@@ -587,16 +616,19 @@ cudaError_t launch_lora_tiles(LoraArgs& p, cudaStream_t st) {
         !ffn_map(&p.mo, p.out, p.m, p.N, p.ldo, 32))
         return cudaErrorUnknown;
     cudaError_t e = allow_smem<lora_shrink>(SHRINK_SMEM);
-    if (e == cudaSuccess) e = allow_smem<lora_expand>(kSmem);
+    if (e == cudaSuccess) e = allow_smem<lora_expand<false>>(kSmem);
+    if (e == cudaSuccess) e = allow_smem<lora_expand<true>>(kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(lora_shrink, dim3(tiles, p.splits), dim3(SHRINK_THREADS), SHRINK_SMEM, st, p);
+    const int most = shares(p.n, p.r);
+    e = launch_pdl(lora_shrink, dim3(tiles, p.splits, std::clamp(2 * sms() / (tiles * p.splits), 1, most)), dim3(SHRINK_THREADS), SHRINK_SMEM, st, p);
     if (e != cudaSuccess) return e;
     const int nb = ceil_div(p.r, BK);
     p.n_tiles = ceil_div(p.N, BN);
     p.n_ctas = std::max(1, std::min(p.n_tiles, sms() / tiles));
     const int room = kSmem - 1024 - 2 * nb * X_BYTES;
     p.stages = std::min(MAX_B, (room - YS * Y_BYTES) / X_BYTES);
-    return launch_pdl(lora_expand, dim3(tiles, p.n_ctas), dim3(EXPAND_THREADS),
+    const int z = std::clamp(sms() / (tiles * p.n_ctas), 1, most);
+    return launch_pdl(z > 1 ? lora_expand<true> : lora_expand<false>, dim3(tiles, p.n_ctas, z), dim3(EXPAND_THREADS),
                       1024 + 2 * nb * X_BYTES + YS * Y_BYTES + p.stages * X_BYTES, st, p);
 }
 

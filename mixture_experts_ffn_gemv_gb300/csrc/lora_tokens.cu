@@ -187,13 +187,16 @@ cudaError_t launch_by_tokens(const LoraArgs& a, cudaStream_t st) {
 // Clusters by token, or tiles of 128 tokens?  Tiles read a shared adapter once, but each
 // adapter that occurs costs a tile its products and an accumulator's way through the
 // epilogue; by token it makes no difference who shares what.  In us, by token / by tiles,
-// tokens of 32 adapters mixed and (one for all): 2048 -> 7168, r = 16: 64 tokens 6.6 / 29
-// (6.5 / 9.7), 256 tokens 15 / 33 (15 / 10); 7168 -> 2048, r = 64: 64 tokens 14 / 52 (13 / 13),
-// 128 tokens 28 / 64 (23 / 17); 4096 -> 4096, r = 128, 16 adapters: 64 tokens 25 / 54 (20 / 17),
-// 128 tokens 38 / 60 (36 / 23).  So few tokens, weighed by their rank, go by token where
-// there are adapters to mix.
+// tokens of all adapters mixed and (one for all):
+//   2048 -> 7168, r = 16, 32 adapters: 128 tokens 8.6 / 18 (8.3 / 9.7), 256 tokens 15 / 26
+//     (15 / 9.5), 384 tokens 21 / 38 (21 / 10)
+//   7168 -> 2048, r = 32, 32 adapters: 128 tokens 14 / 17 (14 / 12), 192 tokens 24 / 21 (23 / 13)
+//   7168 -> 2048, r = 64, 32 adapters: 65 tokens 14 / 19 (14 / 14), 96 tokens 22 / 20 (23 / 15)
+//   4096 -> 4096, r = 16, 3 adapters: 128 tokens 7.9 / 13 (7.9 / 10), 192 tokens 13 / 13 (13 / 10)
+// So few tokens, weighed by their rank, go by token, and twice as many where there are
+// adapters to mix.
 bool lora_by_token(int m, int n, int r) {
-    return m <= kLoraByToken || (n >= 4 && (int64_t)m * std::max(r, 32) <= 8192);
+    return m <= kLoraByToken || (int64_t)m * std::max(r, 16) <= (n >= 4 ? 4096 : 2048);
 }
 
 cudaError_t launch_lora_tokens(const LoraArgs& a, cudaStream_t st) {

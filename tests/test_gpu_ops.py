@@ -463,6 +463,34 @@ def test_lora(B, m, k, d, r, n, mixed):
     assert B.mxfp4_device_status() == 0
 
 
+@pytest.mark.parametrize("m,k,d,r,n", [(129, 520, 136, 64, 5), (200, 4104, 264, 24, 60), (260, 1032, 1096, 128, 3), (384, 264, 2056, 16, 64),
+                                       (97, 7176, 72, 72, 128), (515, 2048, 200, 128, 130)])
+def test_lora_tokens_do_not_depend_on_the_others_adapters(B, m, k, d, r, n):
+    """Few tokens of many adapters, which several blocks share: each token's result is, bit for bit, what it is
+    where the others use none; in place, into strided rows, and beside adapters that hold NaN."""
+    x, y, a, b, scale = _lora_case(m, k, d, r, n)
+    ids = _ints(m + n, -1, n, m)
+    ids[m // 2] = -1
+    ids[0] = ids[m - 1] = 1
+    got = B.moe_lora_add(y, x, a, b, ids, scale, out=torch.empty_like(y))
+    want, bound = P.lora(x, y, a, b, ids, scale)
+    _within(got, want, bound)
+    for i in {-1, 0, 1, n - 1, int(ids[m // 3]), int(ids[m - 2])}:
+        mine = ids == i
+        alone = B.moe_lora_add(y, x, a, b, torch.where(mine, ids, -1).to(torch.int32), scale, out=torch.empty_like(y))
+        assert torch.equal(alone[mine], got[mine]) and torch.equal(alone[~mine], y[~mine]), i
+    place = y.clone()
+    assert torch.equal(B.moe_lora_add(place, x, a, b, ids, scale), got)
+    rows, wide = _strided(torch.zeros_like(y), 16, 8)
+    B.moe_lora_add(y, x, a, b, ids, scale, out=rows)
+    assert torch.equal(rows, got) and (wide[:, :8] == 77).all() and (wide[:, 8 + d:] == 77).all()
+    a[1], b[0] = NAN, INF
+    sound = (ids != 1) & (ids != 0)
+    spoilt = B.moe_lora_add(y, x, a, b, ids, scale, out=torch.empty_like(y))
+    assert torch.equal(spoilt[sound], got[sound]) and torch.isnan(spoilt[ids == 1]).all()
+    assert B.mxfp4_device_status() == 0
+
+
 @pytest.mark.parametrize("m", [3, 64, 65, 300])
 def test_lora_no_scale_no_adapters_no_tokens(B, m):
     x, y, a, b, _ = _lora_case(m, 264, 328, 16, 3)
