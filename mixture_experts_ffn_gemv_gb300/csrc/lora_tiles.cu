@@ -16,14 +16,17 @@
 // all of a block's tiles of 128 outputs; D = T B^T per adapter and tile, the row's
 // own added to y in shared memory, rounded once, and out by TMA.  y and the first
 // B are loaded before the shrink kernel ends.
-// Each: warp 0 TMA producer, warp 1 MMA issuer, then the epilogue warps.
+// Each: a thread of warp 0 loads by TMA, one of warp 1 issues the products, then the
+// epilogue warps.  (With whole warps, their votes and joins at each wait were most of an
+// adapter's turn: 950 cycles of the issuer at r = 16, now 770; 300 tokens of 64 adapters,
+// 4096 -> 4096, 42.5 -> 35 us.)
 //
-// 8192 tokens, 7168 -> 7168, r = 64, 4 requests: 68.6 us for 360 MB (52.9 at the copy
+// 8192 tokens, 7168 -> 7168, r = 64, 4 requests: 67 us for 360 MB (52.9 at the copy
 // rate): shrink some 24 of them (17 at that rate), two launches' start and end and T's
 // way between them 10, expand 30.  In one kernel, clusters handing T over through
 // distributed shared memory, the same took 79 us: blocks wait for the slowest of their
 // cluster (5 us), and the exchange itself takes 4.  A tile of many adapters pays for each
-// about as much as for one: 2048 tokens of 64 adapters, 4096 -> 4096, r = 16, 123 us, of one 15.
+// about as much as for one: 2048 tokens of 64 adapters, 4096 -> 4096, r = 16, 110 us, of one 14.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -160,73 +163,67 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
     const int passes = (tl.count + p.group - 1) / p.group;
 
     if (warp == 0) {
-        uint32_t s = 0, ph = 1, n = 0;
-        bool ok = true;
-        for (int g = 0; g < passes && ok; ++g) {
-            const int u0 = g * p.group, u1 = min(tl.count, u0 + p.group);
-            for (int kb = k0; kb < k1; ++kb) {
-                if (warp_sees(&abort_flag) || !warp_wait(empty0 + 8 * s, ph, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
+        if (elect_one()) {
+            uint32_t s = 0, ph = 1, n = 0;
+            const int count = tl.count;
+            bool ok = true;
+            for (int g = 0; g < passes && ok; ++g) {
+                const int u0 = g * p.group, u1 = min(count, u0 + p.group);
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = role_wait(empty0 + 8 * s, ph, p.wait_ns, &abort_flag);
+                    if (!ok) break;
                     const uint32_t sa = sbase + s * stride, bar = full0 + 8 * s;
                     mbar_arrive_expect_tx(bar, X_BYTES + (u1 - u0) * p.r * BK * 2);
                     tma_load_3d(sa, &p.mx, kb * (BK / 2), m0, 0, bar);
                     for (int u = u0; u < u1; ++u)
                         tma_load_3d(sa + X_BYTES + (u - u0) * p.r * BK * 2, &p.ma, kb * (BK / 2), tl.list[u] * p.r, 0, bar);
-                }
-                __syncwarp();
-                ++n;
-                if (++s == stages) {
-                    s = 0;
-                    ph ^= 1u;
+                    ++n;
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 61);
+                abort_flag = 1;
+            }
+            const uint32_t S = stages;
+            for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(full0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
         }
-        if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 61);
-            abort_flag = 1;
-        }
-        const uint32_t S = stages;
-        for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(full0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
+        __syncwarp();
     } else if (warp == 1) {
-        uint32_t s = 0, ph = 0;
-        bool ok = true;
-        for (int g = 0; g < passes && ok; ++g) {
-            const int u0 = g * p.group, u1 = min(tl.count, u0 + p.group);
-            const uint32_t idesc = idesc_bf16(BM, ((u1 - u0) * p.r + 15) / 16 * 16);
-            if (!warp_wait(tempty, (g & 1u) ^ 1u, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            for (int kb = k0; kb < k1; ++kb) {
-                if (warp_sees(&abort_flag) || !warp_wait(full0 + 8 * s, ph, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t sa = sbase + s * stride;
-                const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + X_BYTES);
-                if (elect_one()) {
+        if (elect_one()) {
+            uint32_t s = 0, ph = 0;
+            const int count = tl.count;
+            bool ok = true;
+            for (int g = 0; g < passes && ok; ++g) {
+                const int u0 = g * p.group, u1 = min(count, u0 + p.group);
+                const uint32_t idesc = idesc_bf16(BM, ((u1 - u0) * p.r + 15) / 16 * 16);
+                ok = role_wait(tempty, (g & 1u) ^ 1u, p.wait_ns, &abort_flag);
+                for (int kb = k0; kb < k1 && ok; ++kb) {
+                    ok = role_wait(full0 + 8 * s, ph, p.wait_ns, &abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = sbase + s * stride;
+                    const uint64_t ad = desc_sw128(sa), bd = desc_sw128(sa + X_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) mma_bf16(tmem, ad + 2 * kk, bd + 2 * kk, idesc, kb != k0 || kk != 0);
                     mma_commit(empty0 + 8 * s);
                     if (kb == k1 - 1) mma_commit(tfull);
-                }
-                __syncwarp();
-                if (++s == stages) {
-                    s = 0;
-                    ph ^= 1u;
+                    if (++s == stages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 62);
+                abort_flag = 1;
+            }
+            mma_commit(drain);
+            mbar_wait(drain, 0, DRAIN_NS);
         }
-        if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 62);
-            abort_flag = 1;
-        }
-        if (elect_one()) mma_commit(drain);
-        mbar_wait(drain, 0, DRAIN_NS);
         __syncwarp();
     } else {
         const int row = (warp & 3) * 32 + lane, slot = tl.slot[row];
@@ -335,60 +332,52 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
     const bool both = tl.count >= MANY;  // teams take every tile, and every second adapter of it
 
     if (warp == 0) {
-        uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
-        bool ok = true;
-        for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
-            const auto load_b = [&](int u) {
-                for (int kb = 0; kb < nb; ++kb) {
-                    if (warp_sees(&abort_flag) || !warp_wait(bempty0 + 8 * bs, bph, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
+        if (elect_one()) {
+            uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
+            const int count = tl.count;
+            bool ok = true;
+            for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
+                const auto load_b = [&](int u) {
+                    for (int kb = 0; kb < nb; ++kb) {
+                        ok = role_wait(bempty0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                        if (!ok) break;
                         const uint32_t bar = bfull0 + 8 * bs;
                         mbar_arrive_expect_tx(bar, X_BYTES);
                         tma_load_3d(b_at + bs * X_BYTES, &p.mb, kb * (BK / 2), nt * BN, tl.list[u], bar);
+                        ++bn;
+                        if (++bs == (uint32_t)p.stages) {
+                            bs = 0;
+                            bph ^= 1u;
+                        }
                     }
-                    __syncwarp();
-                    ++bn;
-                    if (++bs == (uint32_t)p.stages) {
-                        bs = 0;
-                        bph ^= 1u;
-                    }
-                }
-            };
-            // the first adapter's B ahead of y: its product is to be there when y is.  No more of
-            // them: products beyond the accumulators wait for the first ones' addition to y.
-            if (tl.count) load_b(0);
-            if (!ok || warp_sees(&abort_flag) || !warp_wait(yempty0 + 8 * ys, yph, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            const bool two = nt * BN + 64 < p.N;
-            if (elect_one()) {
+                };
+                // the first adapter's B ahead of y: its product is to be there when y is.  No more of
+                // them: products beyond the accumulators wait for the first ones' addition to y.
+                if (count) load_b(0);
+                ok = ok && role_wait(yempty0 + 8 * ys, yph, p.wait_ns, &abort_flag);
+                if (!ok) break;
+                const bool two = nt * BN + 64 < p.N;
                 const uint32_t dst = y_at + ys * Y_BYTES, bar = yfull0 + 8 * ys;
                 mbar_arrive_expect_tx(bar, two ? Y_BYTES : X_BYTES);
                 tma_load_3d(dst, &p.my, nt * (BN / 2), m0, 0, bar);
                 if (two) tma_load_3d(dst + X_BYTES, &p.my, nt * (BN / 2) + 32, m0, 0, bar);
+                ++yn;
+                if (++ys == YS) {
+                    ys = 0;
+                    yph ^= 1u;
+                }
+                for (int u = 1; u < count && ok; ++u) load_b(u);
             }
-            __syncwarp();
-            ++yn;
-            if (++ys == YS) {
-                ys = 0;
-                yph ^= 1u;
+            if (!ok) {
+                set_error(p.hdr, DEV_ERR_TIMEOUT, 64);
+                abort_flag = 1;
             }
-            for (int u = 1; u < tl.count && ok; ++u) load_b(u);
+            const uint32_t S = p.stages;
+            for (uint32_t i = yn > (uint32_t)YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
+            for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
         }
-        if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 64);
-            abort_flag = 1;
-        }
-        const uint32_t S = p.stages;
-        for (uint32_t i = yn > (uint32_t)YS ? yn - YS : 0; i < yn; ++i) mbar_wait(yfull0 + 8 * (i % YS), (i / YS) & 1u, DRAIN_NS);
-        for (uint32_t i = bn > S ? bn - S : 0; i < bn; ++i) mbar_wait(bfull0 + 8 * (i % S), (i / S) & 1u, DRAIN_NS);
+        __syncwarp();
     } else if (warp == 1) {
-        // One thread from first to last.  With the warp's votes and joins at each wait an adapter's
-        // turn took 950 cycles at r = 16, now 770 (300 tokens of 64 adapters, 4096 -> 4096: 42.5 -> 37 us).
         if (elect_one()) {
             uint32_t bs = 0, bph = 0, tile = 0;
             uint32_t turn0 = 0, turn1 = 0;  // products of each team so far
@@ -396,32 +385,67 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             tc_fence_after();
             const int count = tl.count, last = p.r - (nb - 1) * BK;
             const uint32_t idesc = idesc_bf16(BM, BN);
-            for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
-                for (int u = 0; u < count && ok; ++u) {
-                    const uint32_t team = (both ? (uint32_t)u : tile) % TEAMS, turn = team ? turn1++ : turn0++;
-                    const uint32_t d = team * 2 + (turn & 1);
-                    ok = role_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns, &abort_flag);
-                    for (int kb = 0; kb < nb && ok; ++kb) {
-                        ok = role_wait(bfull0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+            const auto products = [&](uint32_t d, int kb, uint32_t b) {
+                const uint64_t hi = desc_sw128(t_at + kb * X_BYTES), lo = desc_sw128(t_at + (nb + kb) * X_BYTES),
+                               bd = desc_sw128(b_at + b * X_BYTES);
+                const int steps = kb < nb - 1 ? 4 : (last + 15) / 16;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if (kk >= steps) break;
+                    mma_bf16(tmem + d * BN, hi + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                    mma_bf16(tmem + d * BN, lo + 2 * kk, bd + 2 * kk, idesc, 1);
+                }
+            };
+            const auto next_stage = [&]() {
+                if (++bs == (uint32_t)p.stages) {
+                    bs = 0;
+                    bph ^= 1u;
+                }
+            };
+            if (both && nb == 1) {  // two adapters at a time, one of each team: 512 tokens of 64, r = 64, 61 -> 57 us
+                for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas)
+                    for (int u = 0; u < count && ok; u += 2) {
+                        const bool two = u + 1 < count;
+                        const uint32_t d0 = turn0 & 1, d1 = 2 + (turn1 & 1), s0 = bs;
+                        ok = role_wait(dempty0 + 8 * d0, ((turn0 >> 1) & 1u) ^ 1u, p.wait_ns, &abort_flag) &&
+                             (!two || role_wait(dempty0 + 8 * d1, ((turn1 >> 1) & 1u) ^ 1u, p.wait_ns, &abort_flag)) &&
+                             role_wait(bfull0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                        next_stage();
+                        const uint32_t s1 = bs;
+                        if (two) {
+                            ok = ok && role_wait(bfull0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                            next_stage();
+                        }
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t hi = desc_sw128(t_at + kb * X_BYTES), lo = desc_sw128(t_at + (nb + kb) * X_BYTES),
-                                       bd = desc_sw128(b_at + bs * X_BYTES);
-                        const int steps = kb < nb - 1 ? 4 : (last + 15) / 16;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if (kk >= steps) break;
-                            mma_bf16(tmem + d * BN, hi + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
-                            mma_bf16(tmem + d * BN, lo + 2 * kk, bd + 2 * kk, idesc, 1);
-                        }
-                        mma_commit(bempty0 + 8 * bs);
-                        if (kb == nb - 1) mma_commit(dfull0 + 8 * d);
-                        if (++bs == (uint32_t)p.stages) {
-                            bs = 0;
-                            bph ^= 1u;
+                        products(d0, 0, s0);
+                        if (two) products(d1, 0, s1);
+                        mma_commit(bempty0 + 8 * s0);
+                        mma_commit(dfull0 + 8 * d0);
+                        ++turn0;
+                        if (two) {
+                            mma_commit(bempty0 + 8 * s1);
+                            mma_commit(dfull0 + 8 * d1);
+                            ++turn1;
                         }
                     }
-                }
+            } else {
+                for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas, ++tile)
+                    for (int u = 0; u < count && ok; ++u) {
+                        const uint32_t team = (both ? (uint32_t)u : tile) % TEAMS, turn = team ? turn1++ : turn0++;
+                        const uint32_t d = team * 2 + (turn & 1);
+                        ok = role_wait(dempty0 + 8 * d, ((turn >> 1) & 1u) ^ 1u, p.wait_ns, &abort_flag);
+                        for (int kb = 0; kb < nb && ok; ++kb) {
+                            ok = role_wait(bfull0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            products(d, kb, bs);
+                            mma_commit(bempty0 + 8 * bs);
+                            if (kb == nb - 1) mma_commit(dfull0 + 8 * d);
+                            next_stage();
+                        }
+                    }
+            }
             if (!ok) {
                 set_error(p.hdr, DEV_ERR_TIMEOUT, 65);
                 abort_flag = 1;
@@ -500,29 +524,37 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 }
                 tc_fence_after();
                 const bool own = slot == u, any = __any_sync(0xffffffffu, own);
-                uint32_t v[2][32];
-                if (any) {
-                    const uint32_t taddr = tmem + ((uint32_t)(q4 * 32) << 16) + d * BN + 64 * half;
-                    tmem_ld32(taddr, v[0]);
-                    tmem_ld32(taddr + 32, v[1]);
-                    tmem_wait_ld();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(dempty0 + 8 * d);
-                if (own && col < p.N) {
+                // half a row's 64 columns at a time (registers), loads of y on their way before its first
+                // store: 8192 tokens of 4 adapters mixed, 7168 -> 7168, r = 64, 122 -> 114 us
+                const uint32_t taddr = tmem + ((uint32_t)(q4 * 32) << 16) + d * BN + 64 * half;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t at = line + ((c ^ (row & 7)) << 4);
-                        const uint4 q = lds128(at);
-                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            o[i] = pack_bf16x2(bf16lo(w[i]) + __uint_as_float(v[c >> 2][(8 * c + 2 * i) & 31]),
-                                               bf16hi(w[i]) + __uint_as_float(v[c >> 2][(8 * c + 2 * i + 1) & 31]));
-                        sts128(at, o[0], o[1], o[2], o[3]);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[32];
+                    if (any) {
+                        tmem_ld32(taddr + 32 * h, v);
+                        tmem_wait_ld();
                     }
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(dempty0 + 8 * d);
+                    }
+                    if (own && col < p.N) {
+                        uint4 q[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) q[c] = lds128(line + (((4 * h + c) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+                            uint32_t o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                o[i] = pack_bf16x2(bf16lo(w[i]) + __uint_as_float(v[8 * c + 2 * i]),
+                                                   bf16hi(w[i]) + __uint_as_float(v[8 * c + 2 * i + 1]));
+                            sts128(line + (((4 * h + c) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             if (!ok) break;
