@@ -275,10 +275,12 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
     Row<G, VEC, NV> next;
     if (kAhead) next = load(0);
     find_sequences(a, first, ch);
-    pdl_wait();
-    pdl_trigger();
     Row<G, VEC, NV> c;  // counts of sequence `of`
     int of = -1;
+    const auto load_counts = [&](int s) {
+        c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
+        of = s;
+    };
     for (int r = 0; r < a.chunk; r += GROUPS) {  // warps stay together
         const int j = r + group, s = j < a.chunk ? ch.seq[j] : -1;
         Row<G, VEC, NV> l;
@@ -288,10 +290,7 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
         } else {
             l = load(r);
         }
-        if (s != of || r == 0) {
-            c.load_counts(a.counts + (size_t)max(s, 0) * a.E, i, a.E, s >= 0);
-            of = s;
-        }
+        if (s != of && r > 0) load_counts(s);
         float top[1] = {-INFINITY};
 #pragma unroll
         for (int n = 0; n < NV * VEC; ++n) top[0] = fmaxf(top[0], l.v[n]);
@@ -309,6 +308,11 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
             scores(l, shift, low, p, rest);
 #pragma unroll
             for (int n = 0; n < NV * VEC; ++n) sum[1] += p.v[n];
+        }
+        if (r == 0) {  // the first tokens' scores do without the counts
+            pdl_wait();
+            pdl_trigger();
+            load_counts(s);
         }
 #pragma unroll
         for (int n = 0; n < NV * VEC; ++n) sum[2] = fmaf(p.v[n], c.v[n], sum[2]);
