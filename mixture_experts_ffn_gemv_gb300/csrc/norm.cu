@@ -22,6 +22,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "ops.h"
+#include "pairs.cuh"
 #include "tmap.h"
 
 namespace moe {
@@ -150,26 +151,6 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) add_rmsnorm(const NormArgs 
     }
 }
 
-// Pairs of fp32 in one instruction.
-struct Pair {
-    float x, y;
-};
-__device__ __forceinline__ uint64_t bits(Pair p) { return __double_as_longlong(__hiloint2double(__float_as_int(p.y), __float_as_int(p.x))); }
-__device__ __forceinline__ Pair pair(uint64_t v) {
-    Pair p;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
-    return p;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-    return pair(r);
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return pair(r);
-}
 __device__ __forceinline__ Pair unpack2(uint32_t w) { return Pair{bf16lo(w), bf16hi(w)}; }
 __device__ __forceinline__ void load_w4(const float* p, Pair (&v)[4]) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p + 4));

@@ -25,9 +25,9 @@
 // Deterministic: integer counts, and sums in the order of the tokens of a chunk,
 // then of the chunks; whichever block finishes a sequence last adds its chunks up.
 //
-// 16384 tokens of 256 experts, 4 sequences, sigmoid: losses 15.7 us (counts some 5 of
-// it, the last sequence's sum 2), gradient 14.4 us for 34 MB, logits in L2.  Not the
-// memory but the instructions bound it (a token's lanes execute some 330 and 680), for
+// 16384 tokens of 256 experts, 4 sequences, sigmoid: losses 14.3 us (counts some 5 of
+// it, the last sequence's sum 2), gradient 13.5 us for 34 MB, logits in L2.  Not the
+// memory but the instructions bound it (a token's lanes execute some 280 and 600), for
 // fewer tokens the chain of loads, sums over lanes and, between two kernels, of counts:
 // 333 tokens of 8 experts 5.7 and 3.4 us.
 #include <cuda_runtime.h>
@@ -39,6 +39,7 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "ops.h"
+#include "pairs.cuh"
 #include "sm100.cuh"
 #include "tmap.h"
 
@@ -122,19 +123,26 @@ __device__ __forceinline__ void group_sum(float (&v)[M]) {
 }
 template <int G, int M>
 __device__ __forceinline__ void group_max(float (&v)[M]) {
+    if constexpr (G == 32) {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1)
+        for (int k = 0; k < M; ++k) asm volatile("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v[k]));
+    } else {
 #pragma unroll
-        for (int k = 0; k < M; ++k) v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], o));
+        for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < M; ++k) v[k] = fmaxf(v[k], __shfl_xor_sync(0xffffffffu, v[k], o));
+    }
 }
 
 // exp(v) of v <= 0, as 2^(v log2 e): off by 2^-22 and by the product's rounding, |v| 2^-24,
 // of a number that counts for exp(v) (below 2^-126 for nothing).
-__device__ __forceinline__ float exp_neg(float v) {
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_approx(float v) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float exp_neg(float v) { return exp2_approx(v * kLog2e); }
 // 1 / v of a normal v up to 2^126, within 2^-23; 0 of 0.
 __device__ __forceinline__ float inverse(float v) {
     float r;
@@ -142,11 +150,60 @@ __device__ __forceinline__ float inverse(float v) {
     return v == 0.f ? 0.f : r;
 }
 
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // ... of a v that is not 0.
 __device__ __forceinline__ float inverse_of_some(float v) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// Over the N values of a lane, two an instruction where there are two.
+template <int N>
+__device__ __forceinline__ Pair two(const float (&v)[N], int n) { return Pair{v[n], v[n + 1]}; }
+template <int N>
+__device__ __forceinline__ void put(float (&v)[N], int n, Pair p) {
+    v[n] = p.x;
+    v[n + 1] = p.y;
+}
+template <int N>
+__device__ __forceinline__ float dot(const float (&x)[N], const float (&y)[N]) {
+    if constexpr (N == 1) {
+        return x[0] * y[0];
+    } else {
+        Pair s{0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < N; n += 2) s = fma2(two(x, n), two(y, n), s);
+        return s.x + s.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ float total(const float (&x)[N]) {
+    if constexpr (N == 1) {
+        return x[0];
+    } else {
+        Pair s = two(x, 0);
+#pragma unroll
+        for (int n = 2; n < N; n += 2) s = add2(s, two(x, n));
+        return s.x + s.y;
+    }
+}
+// e = exp(l - at), l <= at; their sum
+template <int N>
+__device__ __forceinline__ float exps(const float (&l)[N], float at, float (&e)[N]) {
+    if constexpr (N == 1) e[0] = exp_neg(l[0] - at);
+#pragma unroll
+    for (int n = 0; n + 1 < N; n += 2) {
+        const Pair v = mul2(add2(two(l, n), Pair{-at, -at}), Pair{kLog2e, kLog2e});
+        e[n] = exp2_approx(v.x);
+        e[n + 1] = exp2_approx(v.y);
+    }
+    return total(e);
 }
 
 // sigma(l) / exp(shift) and 1 - sigma(l), neither by a difference, shift = min(0, the largest l): sums of the first do not
@@ -210,16 +267,23 @@ struct Row {
     }
 };
 
-// The scores of a token's logits, and their complements.
-template <int G, int VEC, int NV>
-__device__ __forceinline__ void scores(const Row<G, VEC, NV>& l, float shift, bool low, Row<G, VEC, NV>& p,
-                                       Row<G, VEC, NV>& rest) {
-    if (low) {
+// The scores of a token's logits, and their complements (of scores that are not 0; p times them is what is asked for).
+template <int N>
+__device__ __forceinline__ void scores(const float (&l)[N], float shift, bool low, float (&p)[N], float (&rest)[N]) {
+    if (low || N == 1) {
 #pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) p.v[n] = shifted_logistic(l.v[n], shift, true, rest.v[n]);
-    } else {
+        for (int n = 0; n < N; ++n) p[n] = shifted_logistic(l[n], shift, low, rest[n]);
+        return;
+    }
+    // 1 / (1 + e), e = exp(-l) up to 2^127.97: from 2^126 on, what counts for 0 (and -inf), the inverse is 0
 #pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) p.v[n] = shifted_logistic(l.v[n], shift, false, rest.v[n]);
+    for (int n = 0; n + 1 < N; n += 2) {
+        const Pair v = mul2(two(l, n), Pair{-kLog2e, -kLog2e});
+        const Pair e{exp2_approx(min_or_nan(v.x, 127.97f)), exp2_approx(min_or_nan(v.y, 127.97f))};
+        const Pair b = add2(e, Pair{1.0f, 1.0f});
+        const Pair s{inverse_of_some(b.x), inverse_of_some(b.y)};
+        put(p, n, s);
+        put(rest, n, mul2(e, s));
     }
 }
 
@@ -299,23 +363,17 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
         const bool low = SIGMOID && __any_sync(0xffffffffu, shift < 0.f);
         float sum[3] = {};  // of exp(l - at), of the scores, of the scores times their counts
         Row<G, VEC, NV> p, rest;
-#pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) {
-            p.v[n] = exp_neg(l.v[n] - at);
-            sum[0] += p.v[n];
-        }
+        sum[0] = exps(l.v, at, p.v);
         if (SIGMOID) {
-            scores(l, shift, low, p, rest);
-#pragma unroll
-            for (int n = 0; n < NV * VEC; ++n) sum[1] += p.v[n];
+            scores(l.v, shift, low, p.v, rest.v);
+            sum[1] = total(p.v);
         }
         if (r == 0) {  // the first tokens' scores do without the counts
             pdl_wait();
             pdl_trigger();
             load_counts(s);
         }
-#pragma unroll
-        for (int n = 0; n < NV * VEC; ++n) sum[2] = fmaf(p.v[n], c.v[n], sum[2]);
+        sum[2] = dot(p.v, c.v);
         group_sum<G>(sum);
         const float lse = at + logf(sum[0]);
         if (i == 0 && j < a.chunk)
@@ -389,6 +447,7 @@ __global__ void __launch_bounds__(kThreads) balance_loss(const RouterArgs a) {
 // of sequences.  Pick j of a token is lane j % G's, its number j / G there.
 template <bool SIGMOID, int G, int VEC, int NV>
 __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 3 : 1) route_backward(const RouterArgs a) {
+    constexpr int N = NV * VEC;
     __shared__ Chunk ch;
     extern __shared__ float4 row_mem[];  // [GROUPS, E], zero between tokens
     float* row_of = reinterpret_cast<float*>(row_mem);
@@ -495,21 +554,13 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 3 : 1) route_backwar
         Row<G, VEC, NV> e, p, rest;
         float wk[PICKS], rest_k[PICKS];
         if (losses) {
-            if (!SIGMOID || a.dz) {
-#pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) {
-                    e.v[n] = exp_neg(x.l.v[n] - at);
-                    sum[0] += e.v[n];
-                }
-            }
+            if (!SIGMOID || a.dz) sum[0] = exps(x.l.v, at, e.v);
             if (a.dbalance) {
                 if (SIGMOID) {
-                    scores(x.l, shift, low, p, rest);
-#pragma unroll
-                    for (int n = 0; n < NV * VEC; ++n) sum[1] += p.v[n];
+                    scores(x.l.v, shift, low, p.v, rest.v);
+                    sum[1] = total(p.v);
                 }
-#pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) sum[2] = fmaf(SIGMOID ? p.v[n] : e.v[n], c.v[n], sum[2]);
+                sum[2] = SIGMOID ? dot(p.v, c.v) : dot(e.v, c.v);
             }
         }
         if (a.dtopk_w) {
@@ -528,15 +579,21 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 3 : 1) route_backwar
         if (losses && s >= 0) {  // padding gets nothing, whatever its logits hold
             if (a.dz) {
                 const float f = sum[0] == 0.f ? 0.f : dz * (at + logf(sum[0])) * inverse_of_some(sum[0]);
+                if constexpr (N == 1) d.v[0] = f * e.v[0];
 #pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) d.v[n] = f * e.v[n];
+                for (int n = 0; n + 1 < N; n += 2) put(d.v, n, mul2(Pair{f, f}, two(e.v, n)));
             }
             if (a.dbalance) {
                 const float inv = inverse(SIGMOID ? sum[1] : sum[0]), mean = sum[2] * inv, f = db * inv;
+                if constexpr (N == 1) {
+                    const float g = f * (SIGMOID ? p.v[0] : e.v[0]);
+                    d.v[0] = fmaf(SIGMOID ? g * rest.v[0] : g, c.v[0] - mean, d.v[0]);
+                }
 #pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) {
-                    const float g = f * (SIGMOID ? p.v[n] : e.v[n]) * (c.v[n] - mean);
-                    d.v[n] += SIGMOID ? g * rest.v[n] : g;
+                for (int n = 0; n + 1 < N; n += 2) {
+                    Pair g = mul2(Pair{f, f}, SIGMOID ? two(p.v, n) : two(e.v, n));
+                    if (SIGMOID) g = mul2(g, two(rest.v, n));
+                    put(d.v, n, fma2(g, add2(two(c.v, n), Pair{-mean, -mean}), two(d.v, n)));
                 }
             }
         }
@@ -575,8 +632,9 @@ __global__ void __launch_bounds__(kThreads, NV * VEC <= 8 ? 3 : 1) route_backwar
             if (!twice) {
                 Row<G, VEC, NV> k;
                 k.load(own, i, a.E, true, 0.f);
+                if constexpr (N == 1) d.v[0] += k.v[0];
 #pragma unroll
-                for (int n = 0; n < NV * VEC; ++n) d.v[n] += k.v[n];
+                for (int n = 0; n + 1 < N; n += 2) put(d.v, n, add2(two(d.v, n), two(k.v, n)));
                 __syncwarp();
 #pragma unroll
                 for (int n = 0; n < PICKS; ++n)
