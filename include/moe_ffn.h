@@ -309,6 +309,18 @@ MOE_API int moe_act_quant_nvfp4_f32(const float* x, int64_t rows, int64_t n, uin
  * Returns MOE_OK, MOE_ERR_DEVICE when the word was set, or MOE_ERR_CUDA.    */
 MOE_API int moe_device_status(void* workspace, void* stream, int32_t* device_code);
 
+/* For calls without a handle that are captured into a CUDA graph on a workspace
+ * whose memory goes to others after them (one of the graph's own pool), so that
+ * nobody can read its error word later.  moe_captured_header zeroes such a
+ * workspace's header, in place of a memset and on `stream`, and has what uses the
+ * workspace note its errors in a word of the library's own, one per device (in the
+ * library's device memory, zero from the start, shared by all such graphs and
+ * streams).  moe_captured_status reads and clears that word of the current device
+ * as moe_device_status does a workspace's: it synchronises `stream`, on which the
+ * graphs were replayed or which waits for them. */
+MOE_API int moe_captured_header(void* workspace, void* stream);
+MOE_API int moe_captured_status(void* stream, int32_t* device_code);
+
 /* Router weight preparation (optional).  For m > 64 tokens (and E <= 256)
  * the router runs on the tensor cores over three bf16 planes whose sum
  * represents the fp32 router weight (hi, mid, lo); each call splits router_w

@@ -41,6 +41,7 @@ EXPORTED = (
     "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_size", "moe_add_rmsnorm_backward",
     "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
     "moe_lora_add_workspace_size", "moe_lora_add",
+    "moe_captured_header", "moe_captured_status",
 )
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
@@ -150,6 +151,8 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_lora_add_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
         lib.moe_lora_add.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
                                      sz, _vp]
+        lib.moe_captured_header.argtypes = [_vp, _vp]
+        lib.moe_captured_status.argtypes = [_vp, ctypes.POINTER(_i32)]
         _lib = lib
         return lib
 
@@ -640,19 +643,25 @@ _spaces = {}  # (device, stream) -> workspace of the operators without a handle 
 # Held from the choice of such a workspace to the last launch that uses it: a product may be two
 # launches, and other threads run during the library's calls.
 _spaces_lock = threading.RLock()
+_captured = set()  # devices on which a graph has captured calls of these operators
 
 
 def _space(like, stream: int, need: int) -> torch.Tensor:
     """A workspace of at least `need` bytes for calls on `stream`, the current one, its header
     zeroed before first use.  A call that is captured into a graph gets one from the graph's own
-    pool: the graph may be replayed beside eager calls, and after they have needed a larger one."""
+    pool: the graph may be replayed beside eager calls, and after they have needed a larger one.
+    The pool takes it back after the call, so that its errors go to the device's shared word."""
     key = (like.get_device(), stream)
     entry = _spaces.get(key)
     capturing = _capturing()
     if entry is not None and entry[0].numel() >= need and not capturing:
         return entry[0]
     ws = _empty((max(need, 1 << 16),), dtype=_U8, device=like.device)
-    ws[:256].zero_()
+    if capturing and ws.is_cuda:
+        _check((_lib or load_library()).moe_captured_header(_p(ws), stream), "moe_captured_header")
+        _captured.add(key[0])
+    else:
+        ws[:256].zero_()
     if not capturing:
         past = entry[1] if entry is not None else _Workspaces()
         past.called(ws)
@@ -671,12 +680,21 @@ def _scratch(like, stream: int, need: int):
 
 
 def mxfp4_device_status(stream=None) -> int:
-    """The first device error (0: none) of the MXFP4 products and adapters on `stream` since it was
-    last read (of eager calls: a captured one keeps its error word inside its graph)."""
+    """The first device error (0: none) of the MXFP4 products and adapters since it was last read: of
+    eager calls on `stream`, and of captured ones on its device, whichever stream replays them (of
+    other streams' replays, what has run by then)."""
     s = stream if stream is not None else torch.cuda.current_stream()
     with _spaces_lock:
         ws, past = _spaces.get((s.device.index, s.cuda_stream), (None, None))
-        return 0 if ws is None else past.status(s)
+        first = 0 if ws is None else past.status(s)
+        if s.device.index in _captured:
+            code = _i32()
+            with torch.cuda.device(s.device):
+                rc = load_library().moe_captured_status(s.cuda_stream, ctypes.byref(code))
+            if rc not in (MOE_OK, MOE_ERR_DEVICE):
+                raise MoeError(rc, "moe_captured_status")
+            first = first or code.value
+        return first
 
 
 def moe_mxfp4_gemm(a_codes, a_scales, b_codes, b_scales, out=None, stream=None):

@@ -15,7 +15,9 @@ struct WsHeader {
     int n_active;     // groups with at least one row
     int total_tiles;  // grouped GEMM: m-tiles over all active groups
     int group_done[32];  // fused decode routing: slices finished per group of 8 experts
-    int pad[27];
+    int pad0;
+    WsHeader* errors_at; // note_error: the header that errors go to; null: this one
+    int pad[24];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -41,6 +43,12 @@ enum : int {
 
 __device__ __forceinline__ void set_error(WsHeader* h, int code, int info) {
     if (atomicCAS(&h->err, 0, code) == 0) h->err_info = info;
+}
+// The same of kernels that calls without a handle launch: into the header that `h` names, if any.
+__device__ __forceinline__ void note_error(WsHeader* h, int code, int info) {
+    // past L1: kernels may come here before their wait for the one ahead
+    const unsigned long long at = __ldcg(reinterpret_cast<const unsigned long long*>(&h->errors_at));
+    set_error(at ? reinterpret_cast<WsHeader*>(at) : h, code, info);
 }
 
 // ---- bf16 / fp32

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             }
         }
         if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 41);
+            note_error(p.hdr, DEV_ERR_TIMEOUT, 41);
             *abort_flag = 1;
         }
         for (int j = max(0, i - p.stages); j < i; ++j)  // every issued copy has landed
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             }
         }
         if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 42);
+            note_error(p.hdr, DEV_ERR_TIMEOUT, 42);
             *abort_flag = 1;
         }
         if (elect_one()) mma_commit(done);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
             const Piece after = load(i + 2);
             if (warp_sees(abort_flag) || !warp_wait(empty0 + 8 * s, ph, p.wait_ns)) {
                 if (lane == 0) {
-                    set_error(p.hdr, DEV_ERR_TIMEOUT, 44);
+                    note_error(p.hdr, DEV_ERR_TIMEOUT, 44);
                     *abort_flag = 1;
                 }
                 break;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 2) ffn_narrow(const __grid_constant__
     }
     // the sums to shared memory, over the ring (its copies have landed and its
     // MMAs have read them): part[h][token][row], fp32
-    if (!mbar_wait(done, 0, DRAIN_NS) && threadIdx.x == 0) set_error(p.hdr, DEV_ERR_TIMEOUT, 43);
+    if (!mbar_wait(done, 0, DRAIN_NS) && threadIdx.x == 0) note_error(p.hdr, DEV_ERR_TIMEOUT, 43);
     __syncthreads();
     tc_fence_after();
     const int ntok = min(p.nt, p.T - tok0);

@@ -72,7 +72,7 @@ __device__ __forceinline__ void list_adapters(const LoraArgs& p, int m0, Tile& t
         if (m0 + i < p.m) {
             id = __ldcg(p.ids + m0 + i);  // past L1: lora_expand reads them before it waits
             if (id < -1 || id >= p.n) {
-                set_error(p.hdr, DEV_ERR_BAD_ID, m0 + i);
+                note_error(p.hdr, DEV_ERR_BAD_ID, m0 + i);
                 id = -1;
             }
         }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
                 }
             }
             if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 61);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 61);
                 abort_flag = 1;
             }
             const uint32_t S = stages;
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
                 }
             }
             if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 62);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 62);
                 abort_flag = 1;
             }
             mma_commit(drain);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
         for (int g = 0; g < passes; ++g) {
             if (!warp_wait(tfull, g & 1u, p.wait_ns) || warp_sees(&abort_flag)) {
                 if (lane == 0) {
-                    set_error(p.hdr, DEV_ERR_TIMEOUT, 63);
+                    note_error(p.hdr, DEV_ERR_TIMEOUT, 63);
                     abort_flag = 1;
                 }
                 break;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 for (int u = 1; u < count && ok; ++u) load_b(u);
             }
             if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 64);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 64);
                 abort_flag = 1;
             }
             const uint32_t S = p.stages;
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                     }
             }
             if (!ok) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 65);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 65);
                 abort_flag = 1;
             }
             mma_commit(drain);
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             }
         }
         if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 66);
+            note_error(p.hdr, DEV_ERR_TIMEOUT, 66);
             abort_flag = 1;
         }
         if (lane == 0) tma_store_wait();

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) lora_tokens(const LoraArgs a) {
     const int rows = (a.N + kCluster - 1) / kCluster, n0 = rank * rows, n1 = min(a.N, n0 + rows);
     const int id = a.ids[t];
     if (id < 0 || id >= a.n) {  // no adapter: the whole cluster leaves
-        if (id != -1 && rank == 0 && threadIdx.x == 0) set_error(a.hdr, DEV_ERR_BAD_ID, t);
+        if (id != -1 && rank == 0 && threadIdx.x == 0) note_error(a.hdr, DEV_ERR_BAD_ID, t);
         if (a.y != a.out)
             for (int j = n0 + threadIdx.x; j < n1; j += kThreads) out[j] = y[j];
         return;

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
             }
         }
         if (!ok && lane == 0) {
-            set_error(p.hdr, DEV_ERR_TIMEOUT, 31);
+            note_error(p.hdr, DEV_ERR_TIMEOUT, 31);
             *abort_flag = 1;
         }
         const uint32_t first = n > (uint32_t)STAGES ? n - STAGES : 0;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
                 }
             }
             if (!ok && lane == 0) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 32);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 32);
                 *abort_flag = 1;
             }
             if (elect_one()) mma_commit_pair(drain);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
         uint32_t s = 0, ph = 0;
         for (uint32_t it = 0; it < n; ++it) {
             if (warp_sees(abort_flag) || !warp_wait(sland0 + 8 * s, ph, p.wait_ns)) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 34);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 34);
                 *abort_flag = 1;
                 break;
             }
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(Shape<GATEUP>::THREADS, 1) mx_product(const __
             const int r = mt * 256 + (int)rank * BM + q4 * 32 + lane;
             const bool ok = r < p.M, any = r - lane < p.M;
             if (!warp_wait_cluster(tfull, tc & 1u, p.wait_ns)) {
-                set_error(p.hdr, DEV_ERR_TIMEOUT, 33);
+                note_error(p.hdr, DEV_ERR_TIMEOUT, 33);
                 *abort_flag = 1;
                 break;
             }

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 #include "moe_ffn_ops.h"
 #include "ops.h"
 
@@ -56,9 +57,32 @@ int check_router(int64_t m, int32_t e, int32_t k, const int32_t* off, int64_t se
 }
 int status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+__device__ WsHeader captured_errors;  // of workspaces that a graph's pool takes back
+
+__global__ void captured_header(WsHeader* h) {
+    pdl_wait();  // the workspace's memory may be in use until then
+    pdl_trigger();
+    reinterpret_cast<int4*>(h)[threadIdx.x] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    if (threadIdx.x == 0) h->errors_at = &captured_errors;
+}
+
 }  // namespace
 
 extern "C" {
+
+int moe_captured_header(void* workspace, void* stream) {
+    if (!workspace || !aligned(workspace, kAlign)) return MOE_ERR_INVALID_ARG;
+    return status(launch_pdl(captured_header, dim3(1), dim3(sizeof(WsHeader) / 16), 0, static_cast<cudaStream_t>(stream),
+                             static_cast<WsHeader*>(workspace)));
+}
+
+int moe_captured_status(void* stream, int32_t* device_code) {
+    if (!device_code) return MOE_ERR_INVALID_ARG;
+    void* at = nullptr;
+    if (cudaGetSymbolAddress(&at, captured_errors) != cudaSuccess) return MOE_ERR_CUDA;
+    return moe_device_status(at, stream, device_code);
+}
 
 int moe_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t m, int64_t h,
                     const float* weight, float eps, void* residual_out, int64_t ldo, void* out, uint8_t* codes,

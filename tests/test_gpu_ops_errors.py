@@ -1,0 +1,85 @@
+"""How the products and adapters without a handle report what went wrong: the error words of captured
+calls, refusals ahead of the first launch, and waits that run out."""
+import ctypes
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_ffn_gemv_gb300 import binding
+    binding.load_library()
+    return binding
+
+
+def _n(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+
+def _adapters(m, k=136, d=200, r=16, n=4):
+    """(y, x, a, b, ids): tokens of all adapters in turn, every fifth of none."""
+    ids = torch.arange(m, dtype=torch.int32, device="cuda") % 5 - 1
+    return _n(1, m, d), _n(2, m, k), _n(3, n, r, k, std=k ** -0.5), _n(4, n, d, r, std=r ** -0.5), ids
+
+
+@pytest.mark.parametrize("m", [40, 300])
+def test_errors_of_captured_calls_are_read(B, m):
+    """An id that names no adapter, in a replayed graph: the word is there on whichever stream it is asked
+    for, once, again after another replay, and not lost to a graph that is replayed in between without one."""
+    y, x, a, b, ids = _adapters(m)
+    good = ids.clone()
+    out, sound = torch.empty_like(y), torch.empty_like(y)
+    want = B.moe_lora_add(y, x, a, b, good, out=torch.empty_like(y))
+    torch.cuda.synchronize()
+    g, h = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_lora_add(y, x, a, b, ids, out=out)
+        later = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")  # the pool may place it where the workspace was
+    with torch.cuda.graph(h):
+        B.moe_lora_add(y, x, a, b, good, out=sound)
+    g.replay()
+    assert B.mxfp4_device_status() == 0 and torch.equal(out, want)
+    ids[3] = 4
+    g.replay()
+    h.replay()
+    assert B.mxfp4_device_status() == 1 and B.mxfp4_device_status() == 0
+    assert torch.equal(sound, want) and torch.equal(out[3], y[3]) and not later.any()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        g.replay()
+    assert B.mxfp4_device_status(st) == 1 and B.mxfp4_device_status() == 0
+    g.replay()
+    ids.copy_(good)
+    g.replay()  # without an error: the word of the replay before stays
+    assert B.mxfp4_device_status() == 1 and B.mxfp4_device_status() == 0 and torch.equal(out, want)
+
+
+def test_eager_errors_stay_their_streams_own(B):
+    """Captured calls beside them change nothing: an eager call's error is read on its stream alone."""
+    y, x, a, b, ids = _adapters(40)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_lora_add(y, x, a, b, ids, out=torch.empty_like(y))
+    g.replay()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        B.moe_lora_add(y, x, a, b, torch.full_like(ids, 9), out=torch.empty_like(y))
+    assert B.mxfp4_device_status() == 0 and B.mxfp4_device_status(st) == 1 and B.mxfp4_device_status(st) == 0
+
+
+def test_captured_headers(B):
+    """moe_captured_header leaves zeros but for where errors go, whatever was there, and nothing around it."""
+    lib, code = B.load_library(), ctypes.c_int32()
+    ws = torch.full((768,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert lib.moe_captured_header(ws.data_ptr() + 256, B._stream()) == 0
+    torch.cuda.synchronize()
+    words = ws[256:512].view(torch.int64)
+    assert int((words != 0).sum()) == 1 and (ws[:256] == 0x5A).all() and (ws[512:] == 0x5A).all()
+    assert lib.moe_captured_status(None, ctypes.byref(code)) == 0 and code.value == 0
+    assert lib.moe_device_status(ws.data_ptr() + 256, None, ctypes.byref(code)) == 0 and code.value == 0
