@@ -734,13 +734,20 @@ def moe_mxfp4_linear(x, codes, scales, out=None, stream=None, adapters=None, ada
         _need(codes.dim() == 2, "w: codes are [rows, n/2]")
         y = _empty((x.shape[0], codes.shape[0]), dtype=_BF16, device=x.device) if out is None else out
         _dense(y, _BF16, (x.shape[0], codes.shape[0]), "out")
-        _lora_args(y, x, a, b, adapter_ids, scale, None, _device_of(x, "x"))  # refused before anything is launched
+        dev = _device_of(x, "x")
+        _, args = _lora_args(y, x, a, b, adapter_ids, scale, None, dev)
         if out is not None and x.numel():
             at, to = x.data_ptr(), out.data_ptr()
             _need(to + 2 * out.numel() <= at or at + 2 * ((x.shape[0] - 1) * x.stride(0) + x.shape[1]) <= to,
                   "out: no part of x, where there are adapters")
+        # What the library refuses of the adapters is refused before the product writes out: a call
+        # without room for its workspace comes through all of its checks and launches nothing.
+        rc = (_lib or load_library()).moe_lora_add(*args, 256, 0, None)  # 256: an address nobody looks at
+        if rc not in (MOE_OK, MOE_ERR_WORKSPACE):
+            raise MoeError(rc, "moe_lora_add")
         moe_mxfp4_linear(x, codes, scales, y)
-        return moe_lora_add(y, x, a, b, adapter_ids, scale)
+        _lora_launch(x, args, dev)
+        return y
     _need(adapter_ids is None, "adapter_ids without adapters")
     lib = _lib or load_library()
     n, k = _mx_matrix(codes, scales, "w")
@@ -1201,17 +1208,9 @@ def _lora_args(y, x, a, b, ids, scale, out, dev: int):
                  out.data_ptr(), ldo)
 
 
-def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
-    """y (bf16 [m, d], a projection's output for x, bf16 [m, k]; rows may be strided) plus each token's
-    low-rank adapter: scale[i] b[i] (a[i] x[t]), i = ids[t] (int32 [m]; -1: none), a bf16 [n, r, k],
-    b bf16 [n, d, r], scale fp32 [n] (None: 1).  Into y unless out is given.  Ids outside [-1, n) count
-    as -1 and set the error word that mxfp4_device_status reads."""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return moe_lora_add(y, x, a, b, ids, scale, out)
+def _lora_launch(x, args, dev: int):
+    """Launches what _lora_args has checked, on the current stream."""
     lib = _lib or load_library()
-    dev = _device_of(x, "x")
-    out, args = _lora_args(y, x, a, b, ids, scale, out, dev)
     need = 256
     if args[2] > MOE_LORA_BY_TOKEN:
         size = ctypes.c_size_t()
@@ -1225,4 +1224,17 @@ def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
         rc = lib.moe_lora_add(*args, ws.data_ptr(), ws.numel(), st)
     if rc:
         raise MoeError(rc, "moe_lora_add")
+
+
+def moe_lora_add(y, x, a, b, ids, scale=None, out=None, stream=None):
+    """y (bf16 [m, d], a projection's output for x, bf16 [m, k]; rows may be strided) plus each token's
+    low-rank adapter: scale[i] b[i] (a[i] x[t]), i = ids[t] (int32 [m]; -1: none), a bf16 [n, r, k],
+    b bf16 [n, d, r], scale fp32 [n] (None: 1).  Into y unless out is given.  Ids outside [-1, n) count
+    as -1 and set the error word that mxfp4_device_status reads."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return moe_lora_add(y, x, a, b, ids, scale, out)
+    dev = _device_of(x, "x")
+    out, args = _lora_args(y, x, a, b, ids, scale, out, dev)
+    _lora_launch(x, args, dev)
     return out

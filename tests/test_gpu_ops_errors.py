@@ -83,3 +83,34 @@ def test_captured_headers(B):
     assert int((words != 0).sum()) == 1 and (ws[:256] == 0x5A).all() and (ws[512:] == 0x5A).all()
     assert lib.moe_captured_status(None, ctypes.byref(code)) == 0 and code.value == 0
     assert lib.moe_device_status(ws.data_ptr() + 256, None, ctypes.byref(code)) == 0 and code.value == 0
+
+
+def test_linear_with_adapters_refuses_before_it_writes(B):
+    """Whatever is refused of the adapters, out stays as it was, and so does y's memory where out is not given."""
+    m, k, d = 70, 128, 104
+    x, w, ids = _n(1, m, k), B.moe_mxfp4_quant(_n(2, d, k)), torch.zeros(m, dtype=torch.int32, device="cuda")
+
+    def pair(r, n=2):
+        return _n(3, n, r, k), _n(4, n, d, r), None
+    a, b, _ = pair(16)
+    askew = torch.zeros(a.numel() + 8, dtype=torch.bfloat16, device="cuda")
+    cases = [(pair(12), ids, B.MoeError, 1), (pair(136), ids, B.MoeError, 2), (pair(16, 0), ids, B.MoeError, 1),
+             ((askew[1:1 + a.numel()].view_as(a), b, None), ids, B.MoeError, 1),
+             ((a, askew[4:4 + b.numel()].view_as(b), None), ids, B.MoeError, 1),
+             ((a, b[:, :88], None), ids, ValueError, None), ((a, b, None), ids[:5], ValueError, None),
+             ((a, b, torch.ones(3, device="cuda")), ids, ValueError, None), ((a[:, :, :64], b, None), ids, ValueError, None)]
+    out = torch.full((m, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    for adapters, which, error, status in cases:
+        with pytest.raises(error) as e:
+            B.moe_mxfp4_linear(x, *w, out=out, adapters=adapters, adapter_ids=which)
+        assert status is None or e.value.status == status
+        with pytest.raises(error):
+            B.moe_mxfp4_linear(x, *w, adapters=adapters, adapter_ids=which)
+    for bad in (x.float(), x[:, :64], x[0], _n(5, m, k + 4)[:, 4:]):
+        with pytest.raises(ValueError):
+            B.moe_mxfp4_linear(bad, *w, out=out, adapters=(a, b, None), adapter_ids=ids)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    none = torch.empty(0, d, dtype=torch.bfloat16, device="cuda")
+    assert B.moe_mxfp4_linear(x[:0], *w, out=none, adapters=(a, b, None), adapter_ids=ids[:0]) is none
+    assert B.mxfp4_device_status() == 0
