@@ -116,6 +116,16 @@ MOE_API int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const
                          const void* a, const void* b, int64_t n, int64_t r, const int32_t* ids, const float* scale,
                          void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
+/* As moe_layer_set_wait_limit and moe_layer_stall_test, of every moe_lora_add of
+ * the process from then on, as adapters have no handle: the limit (ns; 0: 2 s) of
+ * each bounded wait in the kernels that take many tokens, and the test of their
+ * failure path, in which the tensor-core issuer of the first (1: A x) or second
+ * (2: B times it) first waits on a barrier that nothing completes (0: neither).  A
+ * wait that runs out leaves DEV_ERR_TIMEOUT (2) in the workspace's error word, and
+ * that call's out unspecified. */
+MOE_API int moe_lora_set_wait_limit(uint64_t ns);
+MOE_API int moe_lora_stall_test(int kernel);
+
 #ifdef __cplusplus
 }
 #endif

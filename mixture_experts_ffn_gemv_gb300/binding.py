@@ -40,7 +40,7 @@ EXPORTED = (
     "moe_mxfp4_linear_workspace_size", "moe_mxfp4_linear", "moe_mxfp4_linear_f32",
     "moe_add_rmsnorm", "moe_add_rmsnorm_backward_workspace_size", "moe_add_rmsnorm_backward",
     "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_route_backward",
-    "moe_lora_add_workspace_size", "moe_lora_add",
+    "moe_lora_add_workspace_size", "moe_lora_add", "moe_lora_set_wait_limit", "moe_lora_stall_test",
     "moe_captured_header", "moe_captured_status",
 )
 
@@ -151,6 +151,8 @@ def load_library(path: str | None = None, build: bool = True):
         lib.moe_lora_add_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(sz)]
         lib.moe_lora_add.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp,
                                      sz, _vp]
+        lib.moe_lora_set_wait_limit.argtypes = [ctypes.c_uint64]
+        lib.moe_lora_stall_test.argtypes = [ctypes.c_int]
         lib.moe_captured_header.argtypes = [_vp, _vp]
         lib.moe_captured_status.argtypes = [_vp, ctypes.POINTER(_i32)]
         _lib = lib

@@ -124,13 +124,14 @@ constexpr int SHRINK_SMEM = 110 * 1024;  // two blocks on an SM
 __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
-    __shared__ uint64_t bars[2 * 8 + 3];
+    __shared__ uint64_t bars[2 * 8 + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + 8), tfull = smem_u32(bars + 16),
-                   tempty = smem_u32(bars + 17), drain = smem_u32(bars + 18);
+                   tempty = smem_u32(bars + 17), drain = smem_u32(bars + 18),
+                   never = smem_u32(bars + 19);  // stall test: no thread ever arrives here
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int z = blockIdx.y, m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
         mbar_init(tfull, 1);
         mbar_init(tempty, 4);
         mbar_init(drain, 1);
+        mbar_init(never, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2) lora_shrink(const __grid_co
         if (elect_one()) {
             uint32_t s = 0, ph = 0;
             const int count = tl.count;
-            bool ok = true;
+            bool ok = p.stall != 1 || mbar_wait(never, 0, p.wait_ns);
             for (int g = 0; g < passes && ok; ++g) {
                 const int u0 = g * p.group, u1 = min(count, u0 + p.group);
                 const uint32_t idesc = idesc_bf16(BM, ((u1 - u0) * p.r + 15) / 16 * 16);
@@ -284,7 +286,7 @@ template <bool SHARED>
 __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_constant__ LoraArgs p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ alignas(16) Tile tl;
-    __shared__ uint64_t bars[2 * YS + 2 * MAX_B + 2 * ND + 3];
+    __shared__ uint64_t bars[2 * YS + 2 * MAX_B + 2 * ND + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
     const uint32_t t_at = smem_u32(smem), y_at = t_at + 2 * nb * X_BYTES, b_at = y_at + YS * Y_BYTES;
     const uint32_t yfull0 = smem_u32(bars), yempty0 = yfull0 + 8 * YS, bfull0 = yempty0 + 8 * YS,
                    bempty0 = bfull0 + 8 * MAX_B, dfull0 = bempty0 + 8 * MAX_B, dempty0 = dfull0 + 8 * ND,
-                   tready = dempty0 + 8 * ND, drain = tready + 8, tdone = drain + 8;
+                   tready = dempty0 + 8 * ND, drain = tready + 8, tdone = drain + 8,
+                   never = tdone + 8;  // stall test: no thread ever arrives here
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m0 = blockIdx.x * BM;
     if (threadIdx.x == 0) {
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         mbar_init(tready, EPI_WARPS);
         mbar_init(drain, 1);
         mbar_init(tdone, EPI_WARPS);
+        mbar_init(never, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
@@ -381,7 +385,8 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         if (elect_one()) {
             uint32_t bs = 0, bph = 0, tile = 0;
             uint32_t turn0 = 0, turn1 = 0;  // products of each team so far
-            bool ok = tl.count == 0 || role_wait(tready, 0, p.wait_ns, &abort_flag);
+            bool ok = tl.count == 0 || (role_wait(tready, 0, p.wait_ns, &abort_flag) &&
+                                        (p.stall != 2 || mbar_wait(never, 0, p.wait_ns)));
             tc_fence_after();
             const int count = tl.count, last = p.r - (nb - 1) * BK;
             const uint32_t idesc = idesc_bf16(BM, BN);

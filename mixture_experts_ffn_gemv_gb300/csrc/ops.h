@@ -75,6 +75,7 @@ struct LoraArgs {
     int m, K, N, r, n;
     WsHeader* hdr;
     uint64_t wait_ns;  // limit of every protocol wait
+    int stall;         // 1, 2: the issuer of lora_shrink, lora_expand first waits on a barrier nothing completes
     // tiles of tokens: set by launch_lora_tiles
     float* part;       // [splits, m, r]: A x by slices of K
     int splits, kblocks, split_blocks;

@@ -2,6 +2,7 @@
 // launches.  Declarations and contracts: include/moe_ffn_ops.h.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -17,6 +18,8 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: limit of every bounded mbarrier wait
+std::atomic<uint64_t> lora_wait_ns{kWaitNs};
+std::atomic<int> lora_stall{0};
 constexpr int64_t kMaxRows = INT32_MAX / 64;
 
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -267,10 +270,22 @@ int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y
     p.r = (int)r;
     p.n = (int)n;
     p.hdr = static_cast<WsHeader*>(workspace);
-    p.wait_ns = kWaitNs;
+    p.wait_ns = lora_wait_ns.load(std::memory_order_relaxed);
+    p.stall = lora_stall.load(std::memory_order_relaxed);
     p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align_up(sizeof(WsHeader)));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return status(lora_by_token(p.m, p.n, p.r) ? launch_lora_tokens(p, st) : launch_lora_tiles(p, st));
+}
+
+int moe_lora_set_wait_limit(uint64_t ns) {
+    lora_wait_ns = ns ? ns : kWaitNs;
+    return MOE_OK;
+}
+
+int moe_lora_stall_test(int kernel) {
+    if (kernel < 0 || kernel > 2) return MOE_ERR_INVALID_ARG;
+    lora_stall = kernel;
+    return MOE_OK;
 }
 
 }  // extern "C"

@@ -114,3 +114,46 @@ def test_linear_with_adapters_refuses_before_it_writes(B):
     none = torch.empty(0, d, dtype=torch.bfloat16, device="cuda")
     assert B.moe_mxfp4_linear(x[:0], *w, out=none, adapters=(a, b, None), adapter_ids=ids[:0]) is none
     assert B.mxfp4_device_status() == 0
+
+
+@pytest.fixture
+def stall(B):
+    """Sets the wait limit and what stalls; both are as they were afterwards."""
+    lib = B.load_library()
+
+    def set_to(kernel, ns=200_000):
+        assert lib.moe_lora_set_wait_limit(ns if kernel else 0) == 0 and lib.moe_lora_stall_test(kernel) == 0
+    yield set_to
+    set_to(0)
+
+
+# one adapter a tile; two; many, a box along r each; many, two boxes; many shared by several blocks, of one box and two
+STALLS = [(300, 1016, 1032, 16, 1), (400, 264, 2056, 64, 2), (300, 520, 264, 24, 30), (500, 264, 520, 128, 6), (2600, 136, 264, 8, 5),
+          (260, 520, 264, 16, 60), (140, 264, 136, 128, 20)]
+
+
+@pytest.mark.parametrize("kernel", [1, 2])
+@pytest.mark.parametrize("m,k,d,r,n", STALLS)
+def test_stalled_adapters_time_out_and_the_next_call_is_clean(B, stall, m, k, d, r, n, kernel):
+    """A wait that runs out ends its kernel with the error word set, twice in a row; what lies around out is
+    left alone; the call after it is right, also of a graph."""
+    y, x, a, b, _ = _adapters(m, k, d, r, n)
+    ids = torch.arange(m, dtype=torch.int32, device="cuda") % (n + 1) - 1
+    want = B.moe_lora_add(y, x, a, b, ids, out=torch.empty_like(y))
+    assert B.mxfp4_device_status() == 0
+    wide = torch.full((m, d + 24), 77.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, 8:8 + d]
+    stall(kernel)
+    for _ in range(2):
+        B.moe_lora_add(y, x, a, b, ids, out=out)
+        assert B.mxfp4_device_status() == 2
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.moe_lora_add(y, x, a, b, ids, out=out)
+    assert B.mxfp4_device_status() == 0
+    g.replay()
+    assert B.mxfp4_device_status() == 2
+    stall(0)
+    B.moe_lora_add(y, x, a, b, ids, out=out)
+    assert B.mxfp4_device_status() == 0 and torch.equal(out, want)
+    assert (wide[:, :8] == 77).all() and (wide[:, 8 + d:] == 77).all()

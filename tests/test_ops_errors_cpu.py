@@ -17,3 +17,9 @@ def test_captured_headers_refuse(B):
     lib = B.load_library()
     assert lib.moe_captured_header(None, None) == 1 and lib.moe_captured_header(FAKE + 64, None) == 1
     assert lib.moe_captured_status(None, None) == 1
+
+
+def test_stall_test_refuses(B):
+    lib = B.load_library()
+    assert lib.moe_lora_stall_test(3) == 1 and lib.moe_lora_stall_test(-1) == 1 and lib.moe_lora_stall_test(0) == 0
+    assert lib.moe_lora_set_wait_limit(0) == 0
