@@ -340,10 +340,18 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
             uint32_t ys = 0, yph = 1, yn = 0, bs = 0, bph = 1, bn = 0;
             const int count = tl.count;
             bool ok = true;
+            // Room comes free once the shrink kernel is done: the limit of a wait for it starts there.
+            bool shrunk = false;
+            const auto room = [&](uint32_t bar, uint32_t parity) {
+                if (mbar_try_wait(bar, parity)) return true;
+                if (!shrunk) pdl_wait();
+                shrunk = true;
+                return role_wait(bar, parity, p.wait_ns, &abort_flag);
+            };
             for (int nt = blockIdx.y; nt < p.n_tiles && ok; nt += p.n_ctas) {
                 const auto load_b = [&](int u) {
                     for (int kb = 0; kb < nb; ++kb) {
-                        ok = role_wait(bempty0 + 8 * bs, bph, p.wait_ns, &abort_flag);
+                        ok = room(bempty0 + 8 * bs, bph);
                         if (!ok) break;
                         const uint32_t bar = bfull0 + 8 * bs;
                         mbar_arrive_expect_tx(bar, X_BYTES);
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
                 // the first adapter's B ahead of y: its product is to be there when y is.  No more of
                 // them: products beyond the accumulators wait for the first ones' addition to y.
                 if (count) load_b(0);
-                ok = ok && role_wait(yempty0 + 8 * ys, yph, p.wait_ns, &abort_flag);
+                ok = ok && room(yempty0 + 8 * ys, yph);
                 if (!ok) break;
                 const bool two = nt * BN + 64 < p.N;
                 const uint32_t dst = y_at + ys * Y_BYTES, bar = yfull0 + 8 * ys;
@@ -385,6 +393,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS, 1) lora_expand(const __grid_co
         if (elect_one()) {
             uint32_t bs = 0, bph = 0, tile = 0;
             uint32_t turn0 = 0, turn1 = 0;  // products of each team so far
+            pdl_wait();  // T comes after it: the waits' limit starts here
             bool ok = tl.count == 0 || (role_wait(tready, 0, p.wait_ns, &abort_flag) &&
                                         (p.stall != 2 || mbar_wait(never, 0, p.wait_ns)));
             tc_fence_after();

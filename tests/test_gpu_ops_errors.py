@@ -157,3 +157,16 @@ def test_stalled_adapters_time_out_and_the_next_call_is_clean(B, stall, m, k, d,
     B.moe_lora_add(y, x, a, b, ids, out=out)
     assert B.mxfp4_device_status() == 0 and torch.equal(out, want)
     assert (wide[:, :8] == 77).all() and (wide[:, 8 + d:] == 77).all()
+
+
+@pytest.mark.parametrize("m,n", [(300, 2), (260, 60), (2600, 5)])
+def test_the_second_kernels_limit_starts_when_the_first_is_done(B, stall, m, n):
+    """Stalled until its limit, the first kernel leaves no time of the second's waits, if those started with
+    it: the second still completes, which rows without an adapter show, whose output needs no sums."""
+    y, x, a, b, _ = _adapters(m, 264, 1032, 16, n)
+    ids = torch.arange(m, dtype=torch.int32, device="cuda") % (n + 1) - 1
+    B.moe_lora_add(y, x, a, b, ids, out=torch.empty_like(y))
+    out = torch.full_like(y, 77.0)
+    stall(1, 2_000_000)
+    B.moe_lora_add(y, x, a, b, ids, out=out)
+    assert B.mxfp4_device_status() == 2 and torch.equal(out[ids < 0], y[ids < 0])
