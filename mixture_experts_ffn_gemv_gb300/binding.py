@@ -180,12 +180,21 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _new(stream, device, dtype, *shape):
+    """An empty tensor that belongs to the stream that writes it (None: the current one): its memory may
+    have been let go a moment ago with work of its old stream still to come, which only that one waits for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def moe_act_quant_fp8(x, stream=None):
     """x bf16 [rows, n] (device) -> (codes uint8 [rows, n], scales fp32 [rows, n/128])."""
     lib = load_library()
     rows, n = x.shape
-    codes = torch.empty(rows, n, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(rows, n // 128, dtype=torch.float32, device=x.device)
+    codes = _new(stream, x.device, torch.uint8, rows, n)
+    scales = _new(stream, x.device, torch.float32, rows, n // 128)
     _check(lib.moe_act_quant_fp8(_p(x), rows, n, _p(codes), _p(scales), _stream(stream)), "moe_act_quant_fp8")
     return codes, scales
 
@@ -195,9 +204,9 @@ def moe_act_quant_nvfp4(x, stream=None):
     e4m3 block-scale codes uint8 [rows, n/16], row scales fp32 [rows])."""
     lib = load_library()
     rows, n = x.shape
-    codes = torch.empty(rows, n // 2, dtype=torch.uint8, device=x.device)
-    sb = torch.empty(rows, n // 16, dtype=torch.uint8, device=x.device)
-    g = torch.empty(rows, dtype=torch.float32, device=x.device)
+    codes = _new(stream, x.device, torch.uint8, rows, n // 2)
+    sb = _new(stream, x.device, torch.uint8, rows, n // 16)
+    g = _new(stream, x.device, torch.float32, rows)
     if x.dtype == torch.float32:
         fn, name = lib.moe_act_quant_nvfp4_f32, "moe_act_quant_nvfp4_f32"
     else:
@@ -368,7 +377,7 @@ class MoeLayer:
             return
         n = ctypes.c_size_t()
         _check(self.lib.moe_router_planes_size(self.handle, ctypes.byref(n)), "moe_router_planes_size")
-        self._planes = torch.empty(max(n.value, 256), dtype=torch.uint8, device=router_w.device)
+        self._planes = _new(stream, router_w.device, torch.uint8, max(n.value, 256))
         _check(self.lib.moe_router_prepare(self.handle, _p(router_w), _p(self._planes), self._planes.numel(),
                                            _stream(stream)), "moe_router_prepare")
 
@@ -408,9 +417,9 @@ class MoeLayer:
     def moe_route(self, x, router_w, router_bias=None, logits=False, stream=None):
         m = x.shape[0]
         dev = x.device
-        ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
-        w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
-        lg = torch.empty(m, self.shape.num_experts, dtype=torch.float32, device=dev) if logits else None
+        ids = _new(stream, dev, torch.int32, m, self.shape.top_k)
+        w = _new(stream, dev, torch.float32, m, self.shape.top_k)
+        lg = _new(stream, dev, torch.float32, m, self.shape.num_experts) if logits else None
         ws = self._call_space(m, stream)
         _check(self.lib.moe_route(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(lg), _p(ids), _p(w),
                                   _p(ws), ws.numel(), _stream(stream)), "moe_route")
@@ -423,9 +432,9 @@ class MoeLayer:
         dev = topk_ids.device
         P = m * self.shape.top_k
         n_local = self.expert_range[1] - self.expert_range[0]  # this handle's experts
-        off = torch.empty(n_local + 1, dtype=torch.int32, device=dev)
-        sp = torch.empty(P, dtype=torch.int32, device=dev)
-        sl = torch.empty(P, dtype=torch.int32, device=dev)
+        off = _new(stream, dev, torch.int32, n_local + 1)
+        sp = _new(stream, dev, torch.int32, P)
+        sl = _new(stream, dev, torch.int32, P)
         ws = self._call_space(m, stream)
         _check(self.lib.moe_permute(self.handle, _p(topk_ids), m, _p(off), _p(sp), _p(sl), _p(ws), ws.numel(),
                                     _stream(stream)), "moe_permute")
@@ -436,7 +445,7 @@ class MoeLayer:
     def moe_experts(self, x, topk_ids, topk_w, arm="auto", out=None, stream=None):
         m = x.shape[0]
         if out is None:
-            out = torch.empty(m, self.shape.hidden, dtype=torch.bfloat16, device=x.device)
+            out = _new(stream, x.device, torch.bfloat16, m, self.shape.hidden)
         ws = self._call_space(m, stream)
         _check(self.lib.moe_experts(self.handle, _p(x), m, _p(topk_ids), _p(topk_w), _p(out), ARMS[arm], _p(ws),
                                     ws.numel(), _stream(stream)), "moe_experts")
@@ -459,7 +468,7 @@ class MoeLayer:
             _dense(x, _BF16, (m, H), "x")
             _on(x)
         if out is None:
-            out = torch.empty(m, H, dtype=torch.bfloat16, device=codes.device)
+            out = _new(stream, codes.device, torch.bfloat16, m, H)
         else:
             _dense(out, _BF16, (m, H), "out")
             _on(out)
@@ -496,11 +505,11 @@ class MoeLayer:
         m = x.shape[0]
         dev = x.device
         if out is None:
-            out = torch.empty(m, self.shape.hidden, dtype=torch.bfloat16, device=dev)
+            out = _new(stream, dev, torch.bfloat16, m, self.shape.hidden)
         ids = w = None
         if return_routing:
-            ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
-            w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
+            ids = _new(stream, dev, torch.int32, m, self.shape.top_k)
+            w = _new(stream, dev, torch.float32, m, self.shape.top_k)
         ws = self._call_space(m, stream)
         _check(self.lib.moe_forward(self.handle, _p(x), m, _p(router_w), _p(router_bias), _p(out), _p(ids), _p(w),
                                     ARMS[arm], _p(ws), ws.numel(), _stream(stream)), "moe_forward")
@@ -515,11 +524,11 @@ class MoeLayer:
         m = x.shape[0]
         dev = x.device
         if norm_out is None:
-            norm_out = torch.empty(m, self.shape.hidden, dtype=torch.bfloat16, device=dev)
+            norm_out = _new(stream, dev, torch.bfloat16, m, self.shape.hidden)
         ids = w = None
         if return_routing:
-            ids = torch.empty(m, self.shape.top_k, dtype=torch.int32, device=dev)
-            w = torch.empty(m, self.shape.top_k, dtype=torch.float32, device=dev)
+            ids = _new(stream, dev, torch.int32, m, self.shape.top_k)
+            w = _new(stream, dev, torch.float32, m, self.shape.top_k)
         ws = self._call_space(m, stream)
         _check(self.lib.moe_forward_residual_rmsnorm(self.handle, _p(x), m, _p(router_w), _p(router_bias),
                                                      _p(residual), _p(norm_w), float(eps), _p(norm_out), _p(ids),

@@ -170,3 +170,39 @@ def test_the_second_kernels_limit_starts_when_the_first_is_done(B, stall, m, n):
     stall(1, 2_000_000)
     B.moe_lora_add(y, x, a, b, ids, out=out)
     assert B.mxfp4_device_status() == 2 and torch.equal(out[ids < 0], y[ids < 0])
+
+
+def _owner(t):
+    """The stream whose memory holds t."""
+    at = t.data_ptr()
+    return next(s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"])
+
+
+def test_outputs_belong_to_the_stream_that_writes_them(B):
+    """The layer's calls and the quantisers, given a stream: every tensor they return is of its memory, so
+    that they write into none which the current stream has let go and still reads."""
+    import dataclasses
+    from mixture_experts_ffn_gemv_gb300 import inputs as I
+    shape = I.LayerShape(hidden=512, num_experts=8, top_k=2, inter=512, fp8=True)
+    t = I.make_layer(dataclasses.replace(I.WORKLOADS["tiny"], shape=shape), seed=0, device=torch.device("cuda", 0))
+    layer = B.MoeLayer(shape, t)
+    m = 70
+    x, res, w = _n(1, m, 512), _n(2, m, 512), torch.ones(512, device="cuda")
+    ids, tw = layer.moe_route(x, t["router_w"])
+    codes, scales = B.moe_act_quant_fp8(x)
+    calls = [lambda st: B.moe_act_quant_fp8(x, stream=st), lambda st: B.moe_act_quant_nvfp4(x, stream=st),
+             lambda st: layer.moe_route(x, t["router_w"], logits=True, stream=st), lambda st: layer.moe_permute(ids, stream=st),
+             lambda st: layer.moe_experts(x, ids, tw, stream=st), lambda st: layer.moe_experts_fp8(codes, scales, ids, tw, stream=st),
+             lambda st: layer.moe_forward(x, t["router_w"], return_routing=True, stream=st),
+             lambda st: layer.moe_forward_residual_rmsnorm(x, t["router_w"], res.clone(), w, return_routing=True, stream=st)]
+    st = torch.cuda.Stream()
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(st)
+        torch.cuda.synchronize()
+        want, got = ((v,) if isinstance(v, torch.Tensor) else v for v in (want, got))
+        for a, b in zip(want, got):
+            assert torch.equal(a, b) and _owner(b) == st.cuda_stream != _owner(a)
+    layer.prepare_router(t["router_w"], stream=st)
+    assert _owner(layer._planes) == st.cuda_stream
