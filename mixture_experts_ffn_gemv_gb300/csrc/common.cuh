@@ -16,8 +16,9 @@ struct WsHeader {
     int total_tiles;  // grouped GEMM: m-tiles over all active groups
     int group_done[32];  // fused decode routing: slices finished per group of 8 experts
     int pad0;
-    WsHeader* errors_at; // note_error: the header that errors go to; null: this one
-    int pad[24];
+    // note_error: the header that errors go to, and its address's complement; anything else: this one
+    unsigned long long errors_at, errors_at_not;
+    int pad[22];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -47,8 +48,8 @@ __device__ __forceinline__ void set_error(WsHeader* h, int code, int info) {
 // The same of kernels that calls without a handle launch: into the header that `h` names, if any.
 __device__ __forceinline__ void note_error(WsHeader* h, int code, int info) {
     // past L1: kernels may come here before their wait for the one ahead
-    const unsigned long long at = __ldcg(reinterpret_cast<const unsigned long long*>(&h->errors_at));
-    set_error(at ? reinterpret_cast<WsHeader*>(at) : h, code, info);
+    const unsigned long long at = __ldcg(&h->errors_at);
+    set_error(at == ~__ldcg(&h->errors_at_not) ? reinterpret_cast<WsHeader*>(at) : h, code, info);
 }
 
 // ---- bf16 / fp32

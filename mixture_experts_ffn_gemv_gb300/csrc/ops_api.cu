@@ -67,7 +67,10 @@ __global__ void captured_header(WsHeader* h) {
     pdl_trigger();
     reinterpret_cast<int4*>(h)[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    if (threadIdx.x == 0) h->errors_at = &captured_errors;
+    if (threadIdx.x == 0) {
+        h->errors_at = reinterpret_cast<unsigned long long>(&captured_errors);
+        h->errors_at_not = ~h->errors_at;
+    }
 }
 
 }  // namespace

@@ -80,7 +80,8 @@ def test_captured_headers(B):
     assert lib.moe_captured_header(ws.data_ptr() + 256, B._stream()) == 0
     torch.cuda.synchronize()
     words = ws[256:512].view(torch.int64)
-    assert int((words != 0).sum()) == 1 and (ws[:256] == 0x5A).all() and (ws[512:] == 0x5A).all()
+    where = words.nonzero()[:, 0].tolist()  # an address and its complement
+    assert len(where) == 2 and int(words[where[0]]) == ~int(words[where[1]]) and (ws[:256] == 0x5A).all() and (ws[512:] == 0x5A).all()
     assert lib.moe_captured_status(None, ctypes.byref(code)) == 0 and code.value == 0
     assert lib.moe_device_status(ws.data_ptr() + 256, None, ctypes.byref(code)) == 0 and code.value == 0
 
@@ -206,3 +207,15 @@ def test_outputs_belong_to_the_stream_that_writes_them(B):
             assert torch.equal(a, b) and _owner(b) == st.cuda_stream != _owner(a)
     layer.prepare_router(t["router_w"], stream=st)
     assert _owner(layer._planes) == st.cuda_stream
+
+
+def test_a_header_that_was_never_zeroed_is_no_address(B):
+    """Errors go where a header says only if moe_captured_header wrote it: one full of anything takes them itself."""
+    lib, code = B.load_library(), ctypes.c_int32()
+    y, x, a, b, ids = _adapters(40)
+    ids[3] = 4
+    ws = torch.full((256,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0
+    assert lib.moe_lora_add(x.data_ptr(), 136, 40, 136, y.data_ptr(), 200, 200, a.data_ptr(), b.data_ptr(), 4, 16, ids.data_ptr(),
+                            None, y.data_ptr(), 200, ws.data_ptr(), 256, None) == 0
+    assert lib.moe_device_status(ws.data_ptr(), None, ctypes.byref(code)) == 5 and code.value == 1
