@@ -10,8 +10,10 @@
  * strides in elements, multiples of 8 and at least the row; fp32 and int32
  * tensors are dense and aligned to their elements where nothing else is said.
  * Outputs share no memory with inputs or with each other but where it is said
- * (rows of one buffer whose columns do not meet share none); matrices that do are
- * refused.  Up to 2^31 / 64 tokens.
+ * (rows of one buffer whose columns do not meet share none).  Refused for it are
+ * the norm's rows, codes and scales, dx with dout, r and dresidual, dlogits with
+ * logits, and the adapters' out with x and y; other pointers (weights, ids, counts,
+ * losses, workspaces) are not compared.  Up to 2^31 / 64 tokens.
  */
 #ifndef MOE_FFN_OPS_GB300_H
 #define MOE_FFN_OPS_GB300_H
@@ -38,7 +40,9 @@ extern "C" {
  *   h a multiple of 8, up to 24576.
  * The norm is taken of the rounded r, as moe_forward_residual_rmsnorm takes it.
  * Sums are fp32: a row whose squares pass its range (|r| from about 1e19 on)
- * comes out as zeros. */
+ * comes out as zeros, and one whose squares fall below it counts as one of zeros,
+ * which only an eps of 0 shows (|r| below about 1e-19 loses bits, below 1e-23 out is
+ * infinite). */
 MOE_API int moe_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t m, int64_t h,
                             const float* weight, float eps, void* residual_out, int64_t ldo, void* out, uint8_t* codes,
                             float* scales, void* stream);
@@ -70,7 +74,9 @@ MOE_API int moe_add_rmsnorm_backward(const void* dout, int64_t ldd, const void* 
  *   balance[s]  = e / (k T^2) sum_i counts[s,i] sum_t p[t,i]
  *   z[s]        = 1 / T sum_t log(sum_i exp(logits[t,i]))^2
  * An empty sequence has zeros.  A token whose logits are all -inf has p = 0 and
- * no part in z.  counts int32 [seqs, e]; balance, z fp32 [seqs].  e in 1..1024,
+ * no part in z; one with a NaN makes its sequence's losses NaN, one with a +inf its
+ * z and, of softmax, its balance.
+ * counts int32 [seqs, e]; balance, z fp32 [seqs].  e in 1..1024,
  * k in 1..min(e, 32), seqs in 1..2^24.  Offsets that fall or leave [0, m] give
  * unspecified values, and touch nothing outside the tensors.
  * workspace: moe_balance_loss_workspace_size bytes, 256-byte aligned; it has no
@@ -99,9 +105,14 @@ MOE_API int moe_route_backward(const float* logits, const int32_t* topk_ids, int
 
 /* Low-rank adapters of many requests beside a projection they share:
  *   out[t,:] = y[t,:] + scale[i] B_i (A_i x[t,:]),  i = ids[t]
- * fp32 sums, rounded once.  ids int32 [m]; -1: no adapter (out[t,:] is y[t,:],
- * bit for bit); any other id outside [0, n) sets the device error word and
+ * in fp32 sums, out rounded once.  ids int32 [m]; -1: no adapter (out[t,:] is
+ * y[t,:], bit for bit); any other id outside [0, n) sets the device error word and
  * counts as -1.
+ * By tiles of 128 tokens (above MOE_LORA_BY_TOKEN tokens, sooner or later by r and
+ * n) scale[i] A_i x[t] goes into the second product as two bf16 parts, 16 bits of
+ * it, and infinities in b may then make NaN.  Which way and in which slices of k
+ * depends on m, k, n and r alone: for the same sizes a token's result does not
+ * depend on the others' adapters, bit for bit.
  *   x bf16 [m, k] (ldx); y bf16 [m, d] (ldy), the projection's output; out bf16
  *   [m, d] (ldo), which may be y (with the same stride); a bf16 [n, r, k], b
  *   bf16 [n, d, r]: the adapters stacked, smaller ranks padded with zeros; scale
@@ -109,7 +120,8 @@ MOE_API int moe_route_backward(const float* logits, const int32_t* topk_ids, int
  *   r a multiple of 8 up to 128; k and d multiples of 8 up to 2^20; n r up to
  *   2^30.
  * workspace: moe_lora_add_workspace_size bytes, 256-byte aligned, its first 256
- * bytes (the header of moe_ffn.h) zero before its first use. */
+ * bytes (the header of moe_ffn.h) zero before its first use.  Every wait of the
+ * kernels is bounded (moe_lora_set_wait_limit): moe_device_status. */
 #define MOE_LORA_BY_TOKEN 64 /* up to so many tokens it is the header alone */
 MOE_API int moe_lora_add_workspace_size(int64_t m, int64_t k, int64_t r, size_t* bytes);
 MOE_API int moe_lora_add(const void* x, int64_t ldx, int64_t m, int64_t k, const void* y, int64_t ldy, int64_t d,

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) lora_tokens(const LoraArgs a) {
         }
     };
 
-    // A x over this block's eighth of K
+    // A x over this block's share of K
     const int pieces = a.K / 8, each = (pieces + kCluster - 1) / kCluster;
     const int p1 = min(pieces, (rank + 1) * each);
     const uint16_t* x = a.x + (size_t)t * a.ldx;

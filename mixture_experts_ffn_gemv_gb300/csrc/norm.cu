@@ -166,11 +166,12 @@ __device__ __forceinline__ void group_sync(int g, int T) { asm volatile("bar.syn
 // rows of its group (T threads take a row, a block has several groups), the
 // groups of a block are added in shared memory and the blocks' sums [blocks, H]
 // by column_sums, each in its order.
-// 16384 x 2048 (268 MB) in 49.5 us, 5.4 TB/s, some 4 of it the sums of dw.  Registers
+// 16384 x 2048 (268 MB) in 49 us, 5.5 TB/s, some 5 of it the sums of dw.  Registers
 // leave 1024 threads to an SM, whose loads, sums and stores hide each other only so
 // far: rows wider than 8192 columns, a block to an SM, reach 0.5 to 0.75 of the copy
 // rate.  (Copying the next row to shared memory meanwhile cost more than it hid:
-// 16384 x 2048 53 -> 59 us at the time, 4096 x 16384 126 -> 141.)
+// 16384 x 2048 53 -> 59 us at the time, 4096 x 16384 126 -> 141.)  Three pieces a
+// thread (rows wider than 16384 columns) spill 92 bytes: 2048 x 24576 in 108 us.
 template <int V>
 __global__ void __launch_bounds__(1024) add_rmsnorm_backward(const NormGradArgs a, int T) {
     __shared__ float2 buf[2][32];

@@ -219,3 +219,35 @@ def test_a_header_that_was_never_zeroed_is_no_address(B):
     assert lib.moe_lora_add(x.data_ptr(), 136, 40, 136, y.data_ptr(), 200, 200, a.data_ptr(), b.data_ptr(), 4, 16, ids.data_ptr(),
                             None, y.data_ptr(), 200, ws.data_ptr(), 256, None) == 0
     assert lib.moe_device_status(ws.data_ptr(), None, ctypes.byref(code)) == 5 and code.value == 1
+
+
+@pytest.mark.parametrize("h", [264, 2056])
+def test_norm_past_the_range_of_its_sums(B, h):
+    """Squares past fp32's range make zeros; below it a row counts as one of zeros, infinite with an eps of 0
+    and, with an ordinary one, r / sqrt(eps) as the formula has it: two roundings of fp32 and bf16's half step."""
+    w = 1 + _n(1, h, std=0.1).float()
+    sign = torch.where(_n(2, 3, h) > 0, 1.0, -1.0)
+    x = (sign * 1e20).bfloat16()
+    assert not B.moe_add_rmsnorm(x, w).out.any()
+    x = (sign * 1e-24).bfloat16()
+    assert torch.isinf(B.moe_add_rmsnorm(x, w, 0.0).out).all()
+    want = x.double() / 1e-6 ** 0.5 * w.double()
+    assert ((B.moe_add_rmsnorm(x, w).out.double() - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E", [5, 64])
+def test_router_losses_of_bad_logits(B, E, sigmoid):
+    """A NaN makes its sequence's losses NaN, a +inf its z and, of softmax, its balance; other sequences are,
+    bit for bit, as without them."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(30, E, device="cuda", generator=g)
+    ids = torch.arange(60, dtype=torch.int32, device="cuda").view(30, 2) % E
+    off = torch.tensor([0, 7, 15, 30], dtype=torch.int32, device="cuda")
+    scoring = "sigmoid" if sigmoid else "softmax"
+    good = B.moe_balance_loss(logits, ids, off, scoring)
+    logits[3, 1], logits[9, 4] = float("nan"), float("inf")
+    balance, z, counts = B.moe_balance_loss(logits, ids, off, scoring)
+    assert torch.isnan(balance).tolist() == [True, not sigmoid, False] and torch.isnan(z).tolist() == [True, True, False]
+    assert torch.isfinite(balance[1]) == sigmoid
+    assert balance[2] == good[0][2] and z[2] == good[1][2] and torch.equal(counts, good[2])
